@@ -28,6 +28,7 @@ __all__ = [
     "cubic_moe_mlp_workspace_bytes", "cubic_moe_mlp", "EXPORTED_SYMBOLS", "cubic_moe_grouped_gemm_a8",
     "cubic_moe_mlp_a8_workspace_bytes", "cubic_moe_mlp_a8",
     "DTYPE_F32", "DTYPE_BF16", "DTYPE_F16",
+    "cubic_moe_topk", "cubic_moe_layer_workspace_bytes", "cubic_moe_layer", "SCORE_SOFTMAX", "SCORE_SIGMOID",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,8 +41,10 @@ EXPORTED_SYMBOLS = [
     "cubic_moe_mlp_workspace_bytes", "cubic_moe_mlp",
     "cubic_gemm_a16_ex", "act_quant_int8_per_token_ex", "cubic_gemm_a8_ex", "cubic_moe_grouped_gemm_ex",
     "cubic_moe_grouped_gemm_a8", "cubic_moe_mlp_a8_workspace_bytes", "cubic_moe_mlp_a8",
+    "cubic_moe_topk", "cubic_moe_layer_workspace_bytes", "cubic_moe_layer",
 ]
 MODE_A16, MODE_A8 = 0, 1          # cubic_linear_mode results
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 
 class CubicError(RuntimeError):
@@ -54,6 +57,12 @@ class _CWeight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("shapes", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("bits", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class _CRouter(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("logits_dtype", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("topk", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -74,6 +83,7 @@ def load_library():
     lib = ctypes.CDLL(path)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     wp = ctypes.POINTER(_CWeight)
+    rp = ctypes.POINTER(_CRouter)
     sigs = {
         "cubic_code_bytes": (sz, [i64, i64, i32]),
         "cubic_storage_bytes": (sz, [i64, i64, i32, i32]),
@@ -104,6 +114,9 @@ def load_library():
         "cubic_moe_mlp": (i32, [vp, i64, vp, vp, i32, wp, wp, i32, vp, vp, sz, vp]),
         "cubic_moe_mlp_a8_workspace_bytes": (sz, [i64, i32, i32, i64, i64]),
         "cubic_moe_mlp_a8": (i32, [vp, i64, vp, vp, i32, wp, wp, i32, vp, vp, sz, vp]),
+        "cubic_moe_topk": (i32, [rp, i64, vp, vp, vp]),
+        "cubic_moe_layer_workspace_bytes": (sz, [i64, i32, i32, i64, i64]),
+        "cubic_moe_layer": (i32, [vp, i64, rp, wp, wp, vp, i32, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -460,3 +473,104 @@ def cubic_moe_mlp_a8(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torc
                                            ctypes.byref(gu), ctypes.byref(dn), E, _ptr(out), _ptr(workspace),
                                            workspace.numel(), _stream(x)), "cubic_moe_mlp_a8")
     return out
+
+
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID, SCORE_SOFTMAX: SCORE_SOFTMAX,
+           SCORE_SIGMOID: SCORE_SIGMOID}
+_DT_LOGITS = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+
+
+def _call(device, f, *args):
+    """f(*args, the current stream of device) with that device current."""
+    if device.index == torch.cuda.current_device():
+        return f(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+    with torch.cuda.device(device):
+        return f(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+
+
+def _result(out, shape, dtype, device, name="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(out, dtype, name)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def _router(logits: torch.Tensor, topk: int, score, bias, renormalize: bool, scale: float) -> _CRouter:
+    if logits.dtype not in _DT_LOGITS:
+        raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
+    _need(logits, logits.dtype, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits: expected [T][E]")
+    if score not in _SCORES:
+        raise ValueError(f"score: expected 'softmax' or 'sigmoid', got {score!r}")
+    E = logits.shape[1]
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.numel() != E:
+            raise ValueError(f"bias: expected {E} values, got {bias.numel()}")
+    return _CRouter(logits.data_ptr(), bias.data_ptr() if bias is not None else None, _DT_LOGITS[logits.dtype], E,
+                    topk, _SCORES[score], 1 if renormalize else 0, scale)
+
+
+def cubic_moe_topk(logits: torch.Tensor, topk: int, score="softmax", bias: torch.Tensor | None = None,
+                   renormalize: bool = True, scale: float = 1.0, topk_ids: torch.Tensor | None = None,
+                   topk_weights: torch.Tensor | None = None):
+    """The router: logits [T][E] (fp32, bf16 or fp16) -> (ids int32 [T][topk], weights fp32 [T][topk]).
+    Experts are taken by score + bias (ties to the lowest index) and weighted by their scores,
+    renormalised over the taken ones and times scale; masked slots get id -1 and weight 0."""
+    r = _router(logits, topk, score, bias, renormalize, scale)
+    T, dev = logits.shape[0], logits.device
+    topk_ids = _result(topk_ids, (T, topk), torch.int32, dev, "topk_ids")
+    topk_weights = _result(topk_weights, (T, topk), torch.float32, dev, "topk_weights")
+    _on(dev, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights)
+    _check(_call(dev, load_library().cubic_moe_topk, ctypes.byref(r), T, _ptr(topk_ids), _ptr(topk_weights)),
+           "cubic_moe_topk")
+    return topk_ids, topk_weights
+
+
+def cubic_moe_layer_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> int:
+    return int(load_library().cubic_moe_layer_workspace_bytes(T, topk, E, H, I))
+
+
+def cubic_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate_up: CubicWeight, down: CubicWeight, E: int, topk: int,
+                    score="softmax", bias: torch.Tensor | None = None, renormalize: bool = True, scale: float = 1.0,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    out_dtype=torch.bfloat16):
+    """The whole routed-expert layer: x bf16 [T][H] and router logits [T][E] ->
+    (y [T][H] bf16 or fp32, ids int32 [T][topk], weights fp32 [T][topk]). Routing as in
+    cubic_moe_topk, experts as in cubic_moe_mlp."""
+    _need(x, torch.bfloat16, "x")
+    yd = _out_dtype(out_dtype)
+    r = _router(logits, topk, score, bias, renormalize, scale)
+    dev = x.device
+    if x.dim() != 2 or x.shape != (logits.shape[0], gate_up.K):
+        raise ValueError(f"x: expected [{logits.shape[0]}][{gate_up.K}], got {tuple(x.shape)}")
+    if r.E != E:
+        raise ValueError(f"logits: expected {E} experts, got {r.E}")
+    T, H = x.shape
+    gu, dn = gate_up.c_struct(), down.c_struct()
+    for name, w in (("gate_up", gate_up), ("down", down)):
+        groups = w.N * (w.K // w.group) if w.group > 0 else 0
+        if (w.codes.numel() < E * (w.N * w.K * w.bits // 8) or w.scales.numel() < E * groups
+                or w.shapes.numel() < 2 * E * groups):
+            raise ValueError(f"{name}: smaller than {E} experts of [{w.N}][{w.K}]")
+    out = _result(out, (T, H), out_dtype, dev)
+    ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    if workspace is None:
+        n = cubic_moe_layer_workspace_bytes(T, topk, E, gate_up.K, down.K)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    _on(dev, logits=logits, bias=bias, out=out, workspace=workspace, gate_up=gate_up.codes, down=down.codes)
+    _check(_call(dev, load_library().cubic_moe_layer, _ptr(x), T, ctypes.byref(r), ctypes.byref(gu), ctypes.byref(dn),
+                 _ptr(out), yd, _ptr(ids), _ptr(weights), _ptr(workspace), workspace.numel()), "cubic_moe_layer")
+    return out, ids, weights

@@ -86,6 +86,7 @@ CUBIC_API const char* cubic_status_string(int status) {
     case CUBIC_ERR_WORKSPACE: return "workspace missing or too small";
     case CUBIC_ERR_HIP: return "HIP runtime error";
     case CUBIC_ERR_DTYPE: return "unsupported activation or output dtype";
+    case CUBIC_ERR_OPTION: return "option outside its values";
     default: return "unknown status";
   }
 }
@@ -411,10 +412,11 @@ CUBIC_API size_t cubic_moe_mlp_workspace_bytes(int64_t T, int topk, int E, int64
   return mlp_layout(T, topk, E, H, I).total;
 }
 
-CUBIC_API int cubic_moe_mlp(const uint16_t* x_bf16, int64_t T, const int32_t* topk_ids,
-                            const float* topk_weights, int topk, const cubic_weight* gate_up0,
-                            const cubic_weight* down0, int E, float* y, void* workspace, size_t ws_bytes,
-                            cubic_stream_t stream) {
+namespace {
+// y: fp32, or bf16 when ybf16 is set.
+int moe_mlp_impl(const uint16_t* x_bf16, int64_t T, const int32_t* topk_ids, const float* topk_weights, int topk,
+                 const cubic_weight* gate_up0, const cubic_weight* down0, int E, float* y, bool ybf16,
+                 void* workspace, size_t ws_bytes, cubic_stream_t stream) {
   int st = check_weight(gate_up0);
   if (st != CUBIC_OK) return st;
   st = check_weight(down0);
@@ -453,8 +455,17 @@ CUBIC_API int cubic_moe_mlp(const uint16_t* x_bf16, int64_t T, const int32_t* to
       topk_ids, topk_weights, static_cast<int>(T), E, topk, params(gate_up0, x_bf16, y1), gate_up0->bits,
       params(down0, h, y2), down0->bits, reinterpret_cast<int32_t*>(ws + L.route.hdr),
       reinterpret_cast<int32_t*>(ws + L.route.erec), reinterpret_cast<int32_t*>(ws + L.route.sorted), h, y,
-      static_cast<hipStream_t>(stream));
+      ybf16, static_cast<hipStream_t>(stream));
   return hip_status(e);
+}
+}  // namespace
+
+CUBIC_API int cubic_moe_mlp(const uint16_t* x_bf16, int64_t T, const int32_t* topk_ids,
+                            const float* topk_weights, int topk, const cubic_weight* gate_up0,
+                            const cubic_weight* down0, int E, float* y, void* workspace, size_t ws_bytes,
+                            cubic_stream_t stream) {
+  return moe_mlp_impl(x_bf16, T, topk_ids, topk_weights, topk, gate_up0, down0, E, y, false, workspace, ws_bytes,
+                      stream);
 }
 
 namespace {
@@ -649,4 +660,111 @@ CUBIC_API int cubic_moe_grouped_gemm_static(const uint16_t* x_bf16, int64_t T, c
                                             cubic_stream_t stream) {
   return moe_grouped(x_bf16, false, T, topk_ids, topk, expert0, E, y, false, nullptr, moe_scratch_bytes(), true,
                      stream);
+}
+
+namespace {
+constexpr int kRouterMaxE = 2048;            // 32 experts per lane of the router's wave
+constexpr int kRouterTopk = 64;              // one lane per taken expert
+
+int check_router(const cubic_router* r, int64_t T) {
+  if (!r) return CUBIC_ERR_NULL;
+  if (T < 0 || r->E <= 0 || r->E > kRouterMaxE || r->topk <= 0 || r->topk > r->E || r->topk > kRouterTopk)
+    return CUBIC_ERR_SHAPE;
+  if (r->logits_dtype != CUBIC_DTYPE_F32 && r->logits_dtype != CUBIC_DTYPE_BF16 && r->logits_dtype != CUBIC_DTYPE_F16)
+    return CUBIC_ERR_DTYPE;
+  if (r->score != CUBIC_SCORE_SOFTMAX && r->score != CUBIC_SCORE_SIGMOID) return CUBIC_ERR_OPTION;
+  if (T > INT32_MAX / 2 / r->topk) return CUBIC_ERR_SHAPE;
+  if (T > 0) {
+    if (!r->logits) return CUBIC_ERR_NULL;
+    if (!aligned16(r->logits) || !aligned16(r->bias)) return CUBIC_ERR_ALIGN;
+  }
+  return CUBIC_OK;
+}
+
+MoeRouter moe_router(const cubic_router* r) {
+  return MoeRouter{r->logits, r->bias, r->logits_dtype, r->E, r->topk, r->score == CUBIC_SCORE_SIGMOID ? 1 : 0,
+                   r->renormalize ? 1 : 0, r->scale};
+}
+
+// The routing first, then the two-kernel path's intermediates or the MLP step's workspace.
+struct LayerLayout {
+  size_t ids, weights, rec, hq, hs, mlp, fused_total, total;
+};
+LayerLayout layer_layout(int64_t T, int topk, int E, int64_t H, int64_t I) {
+  LayerLayout L;
+  const size_t P = static_cast<size_t>(T) * topk;
+  size_t o = 0;
+  L.ids = o;      o += align256(P * 4);
+  L.weights = o;  o += align256(P * 4);
+  L.mlp = o;
+  L.rec = o;      o += align256((2 + 2 * P) * 4);
+  L.hq = o;       o += align256(P * 2 * static_cast<size_t>(I));
+  L.hs = o;       o += align256(P * 2 * static_cast<size_t>((I + 31) / 32));
+  L.fused_total = o;
+  const size_t mlp = L.mlp + mlp_layout(T, topk, E, H, I).total;
+  L.total = o > mlp ? o : mlp;
+  return L;
+}
+}  // namespace
+
+CUBIC_API int cubic_moe_topk(const cubic_router* router, int64_t T, int32_t* topk_ids, float* topk_weights,
+                             cubic_stream_t stream) {
+  const int st = check_router(router, T);
+  if (st != CUBIC_OK) return st;
+  if (T == 0) return CUBIC_OK;
+  if (!topk_ids || !topk_weights) return CUBIC_ERR_NULL;
+  if (!aligned16(topk_ids) || !aligned16(topk_weights)) return CUBIC_ERR_ALIGN;
+  return hip_status(launch_moe_topk(moe_router(router), T, topk_ids, topk_weights, static_cast<hipStream_t>(stream)));
+}
+
+CUBIC_API size_t cubic_moe_layer_workspace_bytes(int64_t T, int topk, int E, int64_t H, int64_t I) {
+  if (T < 0 || topk <= 0 || E <= 0 || H < 0 || I < 0) return 0;
+  return layer_layout(T, topk, E, H, I).total;
+}
+
+CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_router* router,
+                              const cubic_weight* gate_up0, const cubic_weight* down0, void* y, int y_dtype,
+                              int32_t* topk_ids, float* topk_weights, void* workspace, size_t ws_bytes,
+                              cubic_stream_t stream) {
+  int st = check_weight(gate_up0);
+  if (st != CUBIC_OK) return st;
+  st = check_weight(down0);
+  if (st != CUBIC_OK) return st;
+  st = check_router(router, T);
+  if (st != CUBIC_OK) return st;
+  if (!dtype_out_ok(y_dtype)) return CUBIC_ERR_DTYPE;
+  const int64_t H = gate_up0->K, I = down0->K;
+  const int E = router->E, topk = router->topk;
+  if (gate_up0->N != 2 * I || down0->N != H || H == 0 || I == 0) return CUBIC_ERR_SHAPE;
+  if (T == 0) return CUBIC_OK;
+  const bool fused = moe_layer_fused(T, topk, E, H, I, gate_up0->bits, gate_up0->group, down0->bits, down0->group);
+  if (!fused && ((st = moe_weight_fits(gate_up0)) != CUBIC_OK || (st = moe_weight_fits(down0)) != CUBIC_OK)) return st;
+  if (!x_bf16 || !y || !workspace) return CUBIC_ERR_NULL;
+  if (!aligned16(x_bf16) || !aligned16(y) || !aligned16(workspace) || !aligned16(topk_ids) || !aligned16(topk_weights))
+    return CUBIC_ERR_ALIGN;
+  const LayerLayout L = layer_layout(T, topk, E, H, I);
+  if (ws_bytes < (fused ? L.fused_total : L.total)) return CUBIC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  int32_t* ids = reinterpret_cast<int32_t*>(ws + L.ids);
+  float* weights = reinterpret_cast<float*>(ws + L.weights);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool ybf16 = y_dtype == CUBIC_DTYPE_BF16;
+  if (fused) {
+    auto weight = [](const cubic_weight* w) {
+      return MoeLayerWeight{w->codes, w->scales, w->shapes,
+                            static_cast<int64_t>(cubic_code_bytes(w->N, w->K, w->bits)), w->group};
+    };
+    const MoeLayerBuffers b{ids, weights, reinterpret_cast<int32_t*>(ws + L.rec),
+                            reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<uint8_t*>(ws + L.hs)};
+    return hip_status(launch_moe_layer(moe_router(router), x_bf16, static_cast<int>(T), weight(gate_up0), weight(down0),
+                                       static_cast<int>(H), static_cast<int>(I), b, topk_ids, topk_weights, y,
+                                       ybf16 ? 1 : 0, s));
+  }
+  // the caller's arrays hold the routing where given
+  if (topk_ids) ids = topk_ids;
+  if (topk_weights) weights = topk_weights;
+  const hipError_t e = launch_moe_topk(moe_router(router), T, ids, weights, s);
+  if (e != hipSuccess) return CUBIC_ERR_HIP;
+  return moe_mlp_impl(x_bf16, T, ids, weights, topk, gate_up0, down0, E, static_cast<float*>(y), ybf16, ws + L.mlp,
+                      ws_bytes - L.mlp, stream);
 }

@@ -136,7 +136,7 @@ hipError_t launch_moe_a8_product(const MoeA8Params& p, int P, int E, int T, int 
 // outputs y1 [P][2I], and the router-weighted sum of the pair outputs y2 [P][H].
 hipError_t launch_moe_act(const float* y1, int64_t P, int64_t I, uint16_t* h, hipStream_t st);
 hipError_t launch_moe_combine(const float* y2, const int32_t* ids, const float* topk_w, int64_t T, int topk,
-                              int E, int64_t H, float* out, hipStream_t st);
+                              int E, int64_t H, float* out, bool obf16, hipStream_t st);
 // The MLP step in the Dynamic A8 mode: the token rows (x bf16 [T][H]) and the
 // intermediate rows h are each quantised per row before their grouped product.
 struct MoeMlpA8Buffers {
@@ -157,7 +157,37 @@ hipError_t moe_scratch_address(void** out);
 // up.y: [T*topk][2I] fp32 scratch; dn.y: [T*topk][H] fp32 scratch; h: [T*topk][I] bf16 scratch.
 hipError_t launch_moe_mlp(const int32_t* ids, const float* topk_w, int T, int E, int topk,
                           const MoeGemvParams& up, int up_bits, const MoeGemvParams& dn, int dn_bits,
-                          int32_t* hdr, int32_t* erec, int32_t* sorted, uint16_t* h, float* out,
+                          int32_t* hdr, int32_t* erec, int32_t* sorted, uint16_t* h, float* out, bool obf16,
                           hipStream_t st);
+
+// The router (moe_layer.hip): logits [T][E] in fp32 (dtype 0), bf16 (1) or fp16
+// (2), the selection's bias [E] or NULL.
+struct MoeRouter {
+  const void* logits;
+  const float* bias;
+  int dtype, E, topk, sigmoid, renorm;
+  float scale;
+};
+hipError_t launch_moe_topk(const MoeRouter& r, int64_t T, int32_t* ids, float* weights, hipStream_t st);
+// The whole layer for a few tokens in two kernels (moe_layer.hip).
+struct MoeLayerWeight {
+  const uint8_t* codes;    // expert 0
+  const float* scales;
+  const uint16_t* shapes;
+  int64_t code_bytes;      // per expert
+  int group;
+};
+struct MoeLayerBuffers {
+  int32_t* ids;            // [T*topk]
+  float* weights;          // [T*topk]
+  int32_t* rec;            // [2 + 2 T*topk]: pairs with an expert, then (pair, expert) of each
+  uint8_t* hq;             // [T*topk][2][I]
+  uint8_t* hs;             // [T*topk][2][I / 32]
+};
+bool moe_layer_fused(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
+                     int dn_group);
+hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const MoeLayerWeight& up,
+                            const MoeLayerWeight& dn, int H, int I, const MoeLayerBuffers& b, int32_t* ids_user,
+                            float* weights_user, void* y, int ybf16, hipStream_t st);
 
 }  // namespace cubic

@@ -713,7 +713,7 @@ __global__ __launch_bounds__(256) void k_moe_act(const float* __restrict__ y1, i
 __global__ __launch_bounds__(256) void k_moe_combine(const float* __restrict__ y2,
                                                      const int32_t* __restrict__ ids,
                                                      const float* __restrict__ w, int64_t T, int topk,
-                                                     int E, int64_t H, float* __restrict__ out) {
+                                                     int E, int64_t H, float* __restrict__ out, int obf16) {
   const int64_t nvec = T * H / 4;
   for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < nvec;
        v += static_cast<int64_t>(gridDim.x) * 256) {
@@ -743,7 +743,8 @@ __global__ __launch_bounds__(256) void k_moe_combine(const float* __restrict__ y
         for (int e = 0; e < 4; ++e) acc[e] = fmaf(wj[u], r[u][e], acc[e]);
       }
     }
-    *reinterpret_cast<f32x4*>(out + t * H + n) = acc;
+    const float v4[4] = {acc[0], acc[1], acc[2], acc[3]};
+    store_out4(out, obf16 != 0, t * H + n, v4);
   }
 }
 
@@ -758,15 +759,15 @@ hipError_t launch_moe_act(const float* y1, int64_t P, int64_t I, uint16_t* h, hi
 }
 
 hipError_t launch_moe_combine(const float* y2, const int32_t* ids, const float* topk_w, int64_t T, int topk,
-                              int E, int64_t H, float* out, hipStream_t st) {
+                              int E, int64_t H, float* out, bool obf16, hipStream_t st) {
   hipLaunchKernelGGL(k_moe_combine, dim3(elementwise_grid(T * H / 4)), dim3(256), 0, st, y2, ids, topk_w, T,
-                     topk, E, H, out);
+                     topk, E, H, out, obf16 ? 1 : 0);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_mlp(const int32_t* ids, const float* topk_w, int T, int E, int topk,
                           const MoeGemvParams& up, int up_bits, const MoeGemvParams& dn, int dn_bits,
-                          int32_t* hdr, int32_t* erec, int32_t* sorted, uint16_t* h, float* out,
+                          int32_t* hdr, int32_t* erec, int32_t* sorted, uint16_t* h, float* out, bool obf16,
                           hipStream_t st) {
   const int P = T * topk;
   const int64_t I = dn.K, H = dn.N;
@@ -797,7 +798,7 @@ hipError_t launch_moe_mlp(const int32_t* ids, const float* topk_w, int T, int E,
   if (!dn_direct) { p.hdr = hdr; p.erec = erec; p.sorted = sorted; }
   err = launch_moe_product(p, P, E, T, dn_bits, false, st);
   if (err != hipSuccess) return err;
-  return launch_moe_combine(dn.y, ids, topk_w, T, topk, E, H, out, st);
+  return launch_moe_combine(dn.y, ids, topk_w, T, topk, E, H, out, obf16, st);
 }
 
 // ---------------------------------------------------------------------------

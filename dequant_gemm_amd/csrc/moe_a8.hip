@@ -718,7 +718,7 @@ hipError_t launch_moe_mlp_a8(const uint16_t* x, const int32_t* ids, const float*
     err = launch_moe_a8_product(pd, P, E, T, dn_bits, st);
   }
   if (err != hipSuccess) return err;
-  return launch_moe_combine(b.y2, ids, topk_w, T, topk, E, dn.N, out, st);
+  return launch_moe_combine(b.y2, ids, topk_w, T, topk, E, dn.N, out, false, st);
 }
 
 }  // namespace cubic

@@ -1,0 +1,908 @@
+// moe_layer.hip -- the router (cubic_moe_topk) and the whole routed-expert
+// layer for a few tokens (cubic_moe_layer) in two kernels.
+//
+//   ids, w  = the router of each token's logits (router.h)
+//   [g | u] = x_t * GU_e^T;  h = bf16(SiLU(g) * u);  y_t = sum_j w_tj * (h_tj * D_e^T)
+//
+// Every touched expert's codes are read once and each serves one to eight
+// rows, so the layer is bound by HBM as long as decoding a code costs little.
+// The 2-bit codes {00, 01, 11} = {0, +1, -1} are therefore turned into 4-bit
+// floats: field b1 b0 in the top half of a nibble is the e2m1 number {0, +2, -2}
+// (sign b1, exponent b0), so sixteen codes take one shift and two masks (the
+// field 10 reads as -0 and contributes nothing; where a wave sees one, a slow
+// pass adds its level's sum). The activations are split exactly into two
+// e4m3 halves: a bf16 number has eight significant bits, hi takes the upper
+// four rounded to nearest and lo the (signed) rest, with one power-of-two block
+// scale for 32 consecutive values. hi and lo (and the tokens) are rows of the
+// same 16 x 16 x 128 MFMA, which sums their products with the codes in fp32. Values
+// below 2^-14 of their block's largest are off by up to 2^-22 of it, and blocks
+// whose largest value is below 2^-116 by up to 2^-138.
+//
+// Kernel 1 (k_layer_up): every workgroup runs the router of all tokens (one wave
+// each), splits x into LDS, and then walks its share of the units (touched
+// expert, 16 gate rows and the 16 up rows beside them). Kernel 2 (k_layer_down):
+// every workgroup takes an equal share of the output rows and all pairs, one
+// (pair, K part) per wave at a time, so the router-weighted sum never leaves the
+// workgroup: no atomics, and the order of the sums does not depend on timing.
+//
+// Other code widths, more tokens and shapes beyond the kernels' LDS run as the
+// router kernel followed by the routed MLP step (moe.hip).
+#include <algorithm>
+
+#include "common.h"
+#include "launch.h"
+#include "router.h"
+
+namespace cubic {
+namespace {
+
+constexpr uint32_t kRsrc3 = 0x00020000u;       // raw buffer, 32-bit data format
+constexpr int kLayerWaves = 16;                // one workgroup of 1024 threads per compute unit
+constexpr int kLayerMaxT = 8;                  // hi and lo rows of eight tokens fill the MFMA's 16 rows
+constexpr int kLayerMaxE = 1024;               // experts of one router wave (16 per lane)
+constexpr int kLayerMaxPairs = kLayerMaxT * kRouterMaxTopk;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t layer_rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
+                                           static_cast<int>(kRsrc3));
+}
+
+// Barrier of the workgroup's LDS traffic alone: the code loads in flight stay
+// in flight (__syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// ---- the two e4m3 halves of bf16 values -----------------------------------
+// Block scale of a largest magnitude (finite; its fp32 bits): with ef the
+// (clamped) exponent field, v * 2^(134 - ef) lies below 256 and its largest
+// in [128, 256). Scale bytes (E8M0): ef - 7 for hi, ef - 11 for lo.
+__device__ __forceinline__ uint32_t block_exponent(float amax) {
+  const uint32_t ef = __float_as_uint(amax) >> 23;
+  return ef < 11u ? 11u : ef;
+}
+__device__ __forceinline__ float block_factor(uint32_t ef) { return __uint_as_float((261u - ef) << 23); }
+
+// Halves of two values: bytes 0 and 1 of hi and lo. Non-finite values become
+// NaN (0x7f) in hi, so their rows come out NaN.
+__device__ __forceinline__ void split2(float a, float b, float f, uint32_t& hi, uint32_t& lo) {
+  const bool fa = fabsf(a) < __builtin_inff(), fb = fabsf(b) < __builtin_inff();
+  const float va = fa ? a * f : 0.0f, vb = fb ? b * f : 0.0f;
+  hi = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(va, vb, 0, false)) & 0xffffu;
+  const float ra = (va - __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(hi), 0)) * 16.0f;
+  const float rb = (vb - __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(hi), 1)) * 16.0f;
+  lo = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(ra, rb, 0, false)) & 0xffffu;
+  hi = (fa ? hi : (hi & 0xff00u) | 0x7fu);
+  hi = (fb ? hi : (hi & 0x00ffu) | 0x7f00u);
+}
+
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a < __builtin_inff() ? a : 0.0f;
+}
+
+// Place of code c (0..31) of a 32-code chunk among the chunk's 32 operand slots:
+// dword d of the decoded chunk holds the even (d even) or odd codes of code
+// word d / 2.
+__device__ __forceinline__ int code_slot(int c) { return 16 * (c >> 4) + 8 * (c & 1) + ((c & 15) >> 1); }
+// Place of 32-chunk b of a row: with SPL = 2 a lane's 16-byte load holds two
+// chunks, which feed two MFMAs (a macro step of 256 codes, lane group kq takes
+// chunks 2 kq and 2 kq + 1, MFMA h the h-th of each).
+template <int SPL>
+__device__ __forceinline__ int chunk_place(int b) {
+  return SPL == 2 ? (b & ~7) + ((b & 1) << 2) + ((b & 7) >> 1) : b;
+}
+
+// ---- a wave's stream of code tiles ------------------------------------------
+// NT tiles of 16 weight rows, macro steps of SPL * 128 codes, PM steps in flight.
+template <int NT>
+struct CodeSrc {                               // a unit's code and scale buffers (wave-uniform)
+  __amdgpu_buffer_rsrc_t code[NT], scale[NT];
+};
+
+template <int SPL, int PM, int NT>
+struct CodeStream {
+  static constexpr int DW = 2 * SPL;           // code dwords per lane, tile and step
+  uint32_t cb[PM][NT][DW];
+  float sc[PM][NT];
+
+  using Src = CodeSrc<NT>;
+
+  // step t of src into slot u; spg: steps per group
+  template <int U>
+  __device__ __forceinline__ void issue(const Src& src, const uint32_t* vcode, const uint32_t* vscale, int t,
+                                        int spg_shift, uint32_t spg_mul) {
+    const int g = group_of(t, spg_shift, spg_mul);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if constexpr (SPL == 2) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.code[i], vcode[i], t * (4 * DW * 4), 0);
+        cb[U][i][0] = v.x; cb[U][i][1] = v.y; cb[U][i][2] = v.z; cb[U][i][3] = v.w;
+      } else {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.code[i], vcode[i], t * (4 * DW * 4), 0);
+        cb[U][i][0] = v.x; cb[U][i][1] = v.y;
+      }
+      sc[U][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src.scale[i], vscale[i], g * 4, 0));
+    }
+  }
+  // t / spg for t < 2^16: by a shift (powers of two) or a 32-bit reciprocal
+  static __device__ __forceinline__ int group_of(int t, int shift, uint32_t mul) {
+    return shift >= 0 ? t >> shift : static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * mul) >> 32);
+  }
+};
+
+typedef __attribute__((address_space(3))) const uint8_t lds_u8;
+
+// One macro step: A rows from LDS (xr: this lane's row, its bytes in operand
+// order; sr: its scale bytes), B from the code words of NT tiles. The step's sum
+// of hi + lo, times the group scale, goes to acc[tile][token 0 / 1 of the lane].
+// MODE 0: the codes 0, +1, -1; their unused field is collected in bad. MODE 1:
+// the unused field alone, as +1 (the slow pass).
+template <int SPL, int NT, int MODE>
+__device__ __forceinline__ void layer_step(const uint32_t (*w)[2 * SPL], const float* sc, const uint8_t* xr,
+                                           const uint8_t* sr, int t, int kq, float (*acc)[2], uint32_t& bad) {
+  uint32_t sx;
+  if constexpr (SPL == 2) {
+    sx = *reinterpret_cast<const uint16_t*>(sr + t * 8 + kq * 2);
+  } else {
+    sx = sr[t * 4 + kq];
+  }
+  f32x4 part[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) part[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < SPL; ++h) {
+    const u32x4 a0 = *reinterpret_cast<const u32x4*>(xr + (t * SPL + h) * 128 + 16 * kq);
+    const u32x4 a1 = *reinterpret_cast<const u32x4*>(xr + (t * SPL + h) * 128 + 64 + 16 * kq);
+    const i32x8 a = {static_cast<int>(a0.x), static_cast<int>(a0.y), static_cast<int>(a0.z), static_cast<int>(a0.w),
+                     static_cast<int>(a1.x), static_cast<int>(a1.y), static_cast<int>(a1.z), static_cast<int>(a1.w)};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      i32x8 b = {};
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const uint32_t v = w[i][2 * h + d];
+        if constexpr (MODE == 0) {
+          b[2 * d] = static_cast<int>((v << 2) & 0xCCCCCCCCu);
+          b[2 * d + 1] = static_cast<int>(v & 0xCCCCCCCCu);
+          bad |= v & ~(v << 1);
+        } else {
+          const uint32_t f = v & ~(v << 1) & 0xAAAAAAAAu;
+          b[2 * d] = static_cast<int>((f << 1) & 0x44444444u);
+          b[2 * d + 1] = static_cast<int>((f >> 1) & 0x44444444u);
+        }
+      }
+      // scale 2^-1 on the codes: the nibbles are +-2
+      if (h == 0) {
+        part[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part[i], 0, 4, 0, static_cast<int>(sx), 0, 126);
+      } else {
+        part[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part[i], 0, 4, 1, static_cast<int>(sx), 0, 126);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    acc[i][0] = fmaf(sc[i], part[i][0] + part[i][1], acc[i][0]);
+    acc[i][1] = fmaf(sc[i], part[i][2] + part[i][3], acc[i][1]);
+  }
+}
+
+// The slow pass: the level of the field 10 (code -2) is -q(2) s, q(2) = 2 a + 4 b +
+// 8 (1 - a - b); its codes' sums are added step by step.
+template <int SPL, int NT>
+__device__ __forceinline__ void layer_extra(const CodeSrc<NT>& src, const __amdgpu_buffer_rsrc_t* shp, const uint32_t* vcode,
+                                                      const uint32_t* vscale, int tb, int te, int spg_shift,
+                                                      uint32_t spg_mul, const uint8_t* xr, const uint8_t* sr, int kq,
+                                                      float (*acc)[2]) {
+#pragma unroll 1
+  for (int t = tb; t < te; ++t) {
+    CodeStream<SPL, 1, NT> st;
+    st.template issue<0>(src, vcode, vscale, t, spg_shift, spg_mul);
+    const int g = CodeStream<SPL, 1, NT>::group_of(t, spg_shift, spg_mul);
+    float lev[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint32_t ab = __builtin_amdgcn_raw_buffer_load_b32(shp[i], vscale[i], g * 4, 0);
+      const double a = f16_bits_to_f64(static_cast<uint16_t>(ab & 0xffffu));
+      const double b = f16_bits_to_f64(static_cast<uint16_t>(ab >> 16));
+      lev[i] = static_cast<float>(-static_cast<double>(st.sc[0][i]) * level_numerator(a, b, 2, 1));
+    }
+    uint32_t none = 0u;
+    layer_step<SPL, NT, 1>(st.cb[0], lev, xr, sr, t, kq, acc, none);
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// cubic_moe_topk: one wave per token.
+// ---------------------------------------------------------------------------
+template <int EPL>
+__global__ __launch_bounds__(256) void k_moe_topk(RouterParams p, int64_t T, int32_t* __restrict__ ids,
+                                                  float* __restrict__ weights) {
+  __shared__ uint32_t cand[4][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  if (t >= T) return;                          // no barrier in this kernel
+  int id;
+  float w;
+  wave_topk<EPL>(p, t, lane, cand[wave], &id, &w);
+  if (lane < p.topk) {
+    ids[t * p.topk + lane] = id;
+    weights[t * p.topk + lane] = w;
+  }
+}
+
+static RouterParams router_params(const MoeRouter& r) {
+  return RouterParams{r.logits, r.bias, r.dtype, r.E, r.topk, r.sigmoid, r.renorm, r.scale};
+}
+
+hipError_t launch_moe_topk(const MoeRouter& r, int64_t T, int32_t* ids, float* weights, hipStream_t st) {
+  const RouterParams p = router_params(r);
+  const dim3 grid(static_cast<unsigned>((T + 3) / 4)), block(256);
+  if (p.E <= 256) {
+    hipLaunchKernelGGL(k_moe_topk<4>, grid, block, 0, st, p, T, ids, weights);
+  } else if (p.E <= 1024) {
+    hipLaunchKernelGGL(k_moe_topk<16>, grid, block, 0, st, p, T, ids, weights);
+  } else {
+    hipLaunchKernelGGL(k_moe_topk<32>, grid, block, 0, st, p, T, ids, weights);
+  }
+  return hipGetLastError();
+}
+
+namespace {
+
+// Routing record that kernel 1 leaves for kernel 2: rec[0] = pairs with an
+// expert, then (pair, expert) of each, grouped by expert.
+struct LayerUpParams {
+  RouterParams r;
+  const uint16_t* x;       // bf16 [T][H]
+  int T;
+  int H, I;
+  const uint8_t* codes;    // gate_up, expert 0
+  const float* scales;
+  const uint16_t* shapes;
+  int64_t code_bytes;
+  int gpr;                 // groups per row
+  int spg_shift;           // steps per group as a shift, or -1
+  uint32_t spg_mul;
+  int ks;                  // waves per tile (each a part of K)
+  int down_spl;            // operand order of h
+  int32_t* ids;            // [T][topk] out
+  float* weights;
+  int32_t* ids_user;       // a second copy for the caller, or NULL
+  float* weights_user;
+  int32_t* rec;
+  uint8_t* hq;             // [T*topk][2][I] e4m3 halves of h in operand order
+  uint8_t* hs;             // [T*topk][2][I / 32] block scales
+};
+
+struct LayerUpLds {
+  int xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
+  int xq_stride, xs_stride;
+};
+__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H) {
+  LayerUpLds L;
+  const int P = T * topk;
+  auto up16 = [](int v) { return (v + 15) & ~15; };
+  L.xq_stride = H + 16;                        // 16 bytes of padding: the rows' reads hit other banks
+  L.xs_stride = up16(H / 32) + 16;
+  int o = 0;
+  L.xq = o;    o += 2 * T * L.xq_stride;
+  L.xs = o;    o += 2 * T * L.xs_stride;
+  // partial sums, two rounds: [2][waves][2 tiles][T][16]; the first-pair table of
+  // the experts uses the same bytes before the first round
+  const int red = 2 * kLayerWaves * 2 * T * 16 * 4;
+  L.red = o;   o += red > kLayerMaxE * 4 ? red : kLayerMaxE * 4;
+  L.first = L.red;
+  L.id = o;    o += up16(P * 4);
+  L.w = o;     o += up16(P * 4);
+  L.exp = o;   o += up16(P * 4);
+  L.slot = o;  o += up16(P * 8);
+  L.cand = o;  o += kLayerMaxT * 64 * 4;
+  L.misc = o;  o += 64;
+  L.total = o;
+  return L;
+}
+
+template <int SPL, int PM>
+__global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using Stream = CodeStream<SPL, PM, 2>;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nl = lane & 15, kq = lane >> 4;
+  const int T = p.T, topk = p.r.topk, P = T * topk;
+  const LayerUpLds L = layer_up_lds(T, topk, p.H);
+  int32_t* s_first = reinterpret_cast<int32_t*>(smem + L.first);
+  int32_t* s_id = reinterpret_cast<int32_t*>(smem + L.id);
+  float* s_w = reinterpret_cast<float*>(smem + L.w);
+  int32_t* s_exp = reinterpret_cast<int32_t*>(smem + L.exp);
+  uint8_t* s_slot = smem + L.slot;             // [touched][8]: the token's slot, 0xff: not routed here
+  int32_t* s_misc = reinterpret_cast<int32_t*>(smem + L.misc);
+
+  // ---- the tokens' routers (one wave each), and x split into its halves ----
+  if (wave < T) {
+    int id;
+    float w;
+    wave_topk<kLayerMaxE / 64>(p.r, wave, lane, reinterpret_cast<uint32_t*>(smem + L.cand) + 64 * wave, &id, &w);
+    if (lane < topk) {
+      s_id[wave * topk + lane] = id;
+      s_w[wave * topk + lane] = w;
+    }
+  }
+  for (int e = tid; e < p.r.E; e += 1024) s_first[e] = INT32_MAX;
+  for (int i = tid; i < 2 * P; i += 1024) reinterpret_cast<uint32_t*>(s_slot)[i] = 0xffffffffu;
+  {
+    // eight values a thread; four neighbouring threads share a 32-value block
+    const int per_row = p.H / 8, all = T * per_row;
+    for (int v0 = 0; v0 < all; v0 += 1024) {
+      const int v = v0 + tid;
+      const bool on = v < all;                 // whole blocks: all is a multiple of 16
+      const int t = on ? v / per_row : 0;
+      const int q = on ? v - t * per_row : 0;
+      const u32x4 raw = *reinterpret_cast<const u32x4*>(p.x + static_cast<int64_t>(t) * p.H + 8 * q);
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(raw[j] << 16);
+        f[2 * j + 1] = __uint_as_float(raw[j] & 0xffff0000u);
+      }
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(f[j]));
+      amax = fmaxf(amax, __shfl_xor(amax, 1));
+      amax = fmaxf(amax, __shfl_xor(amax, 2));
+      const uint32_t ef = block_exponent(amax);
+      const float fac = block_factor(ef);
+      // even codes, then odd codes, of the eight
+      uint32_t hi[4], lo[4];
+      split2(f[0], f[2], fac, hi[0], lo[0]);
+      split2(f[4], f[6], fac, hi[1], lo[1]);
+      split2(f[1], f[3], fac, hi[2], lo[2]);
+      split2(f[5], f[7], fac, hi[3], lo[3]);
+      if (on) {
+        const int b = q >> 2, qd = q & 3;      // block of the row, quarter of the block
+        const int at = 32 * chunk_place<SPL>(b) + 16 * (qd >> 1) + 4 * (qd & 1);
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc) {
+          unsigned char* dst = smem + L.xq + (2 * t + pc) * L.xq_stride + at;
+          const uint32_t* s = pc ? lo : hi;
+          *reinterpret_cast<uint32_t*>(dst) = s[0] | (s[1] << 16);
+          *reinterpret_cast<uint32_t*>(dst + 8) = s[2] | (s[3] << 16);
+          if (qd == 0) smem[L.xs + (2 * t + pc) * L.xs_stride + b] = static_cast<uint8_t>(ef - (pc ? 11u : 7u));
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // ---- touched experts in the order of their first pair ----
+  const int pe = tid < P ? s_id[tid] : -1;
+  if (pe >= 0) atomicMin(&s_first[pe], tid);
+  __syncthreads();
+  const bool lead = pe >= 0 && s_first[pe] == tid;
+  const uint64_t leads = __ballot(lead);
+  if (lane == 0 && wave < 8) s_misc[wave] = __popcll(leads);     // P <= 512 threads
+  __syncthreads();
+  int n = 0, before = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int c = s_misc[k];
+    before += k < wave ? c : 0;
+    n += c;
+  }
+  n = __builtin_amdgcn_readfirstlane(n);
+  if (lead) {
+    const int a = before + __popcll(leads & ((uint64_t{1} << lane) - 1u));
+    s_exp[a] = pe;
+    s_first[pe] = -1 - a;                      // from here on the expert's place
+  }
+  __syncthreads();
+  if (pe >= 0) {
+    const int t = tid / topk;
+    s_slot[8 * (-1 - s_first[pe]) + t] = static_cast<uint8_t>(tid - t * topk);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    // for kernel 2 and the caller: ids, weights and the pairs grouped by expert
+    if (tid < P) {
+      p.ids[tid] = pe;
+      p.weights[tid] = s_w[tid];
+      if (p.ids_user) p.ids_user[tid] = pe;
+      if (p.weights_user) p.weights_user[tid] = s_w[tid];
+    }
+    int pos = 0;
+    const int a0 = pe >= 0 ? -1 - s_first[pe] : 0;
+    if (pe >= 0) {
+      const int t = tid / topk;
+      for (int a = 0; a <= a0; ++a)
+#pragma unroll
+        for (int tt = 0; tt < kLayerMaxT; ++tt)
+          pos += (s_slot[8 * a + tt] != 0xffu && (a < a0 || tt < t)) ? 1 : 0;
+      p.rec[2 + 2 * pos] = tid;
+      p.rec[3 + 2 * pos] = pe;
+    }
+    const uint64_t on = __ballot(pe >= 0);
+    if (lane == 0 && wave < 8) s_misc[8 + wave] = __popcll(on);
+    __syncthreads();                           // (block-uniform branch)
+    if (tid == 0) {
+      int all = 0;
+      for (int k = 0; k < 8; ++k) all += s_misc[8 + k];
+      p.rec[0] = all;
+    }
+  }
+
+  // ---- units: round r, workgroup b, team m -> (r grid + b) teams + m ----
+  const int ks = p.ks, teams = kLayerWaves / ks;
+  const int team = wave / ks, part = wave - team * ks;
+  const int tiles = p.I / 16;
+  const int total = n * tiles;
+  const int nmacro = p.H / (SPL * 128);
+  const int tb = part * nmacro / ks, te = (part + 1) * nmacro / ks;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.H / 4);
+  const uint32_t vcode1 = nl * row_bytes + kq * (Stream::DW * 4);
+  const uint32_t vscale1 = static_cast<uint32_t>(nl * p.gpr * 4);
+  const uint32_t vcode[2] = {vcode1, vcode1}, vscale[2] = {vscale1, vscale1};
+  const int ml = nl < 2 * T ? nl : 0;          // rows past the tokens are not used
+  const uint8_t* xr = smem + L.xq + ml * L.xq_stride;
+  const uint8_t* sr = smem + L.xs + ml * L.xs_stride;
+
+  auto unit_row = [&](int u, int64_t& e, int& j) {
+    const int uu = u < total ? u : 0;
+    const int a = uu / tiles;
+    j = uu - a * tiles;
+    e = __builtin_amdgcn_readfirstlane(s_exp[a]);
+  };
+  auto source = [&](int u) {
+    typename Stream::Src s;
+    int64_t e;
+    int j;
+    unit_row(u, e, j);
+    const uint32_t live = u < total ? 1u : 0u;  // no unit: every load is out of range and reads nothing
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = static_cast<int64_t>(i) * p.I + 16 * j;
+      s.code[i] = layer_rsrc(p.codes + e * p.code_bytes + row * row_bytes, live * 16u * row_bytes);
+      s.scale[i] = layer_rsrc(p.scales + (e * 2 * p.I + row) * p.gpr, live * 64u * static_cast<uint32_t>(p.gpr));
+    }
+    return s;
+  };
+  if (n == 0) return;                          // no expert taken at all (block-uniform)
+  const int stride = static_cast<int>(gridDim.x) * teams;
+  int u = static_cast<int>(blockIdx.x) * teams + team;
+  const int rounds = (total - static_cast<int>(blockIdx.x) * teams + stride - 1) / stride;   // block-uniform
+  if (rounds <= 0) return;
+
+  Stream st;
+  typename Stream::Src cur = source(u);
+  [&]<int... U>(std::integer_sequence<int, U...>) {
+    (st.template issue<U>(cur, vcode, vscale, tb + U < te ? tb + U : (te > tb ? te - 1 : 0), p.spg_shift, p.spg_mul), ...);
+  }(std::make_integer_sequence<int, PM>{});
+
+  float* red = reinterpret_cast<float*>(smem + L.red);
+  const int red_wave = 2 * T * 16, red_buf = kLayerWaves * red_wave;
+  for (int r = 0; r < rounds; ++r) {
+    const typename Stream::Src nxt = source(u + stride);
+    float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    uint32_t bad = 0u;
+    for (int t0 = tb; t0 < te; t0 += PM) {
+      [&]<int... U>(std::integer_sequence<int, U...>) {
+        (([&] {
+           const int t = t0 + U;
+           if (t < te) {
+#pragma unroll
+             for (int i = 0; i < 2; ++i)
+#pragma unroll
+               for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
+             layer_step<SPL, 2, 0>(st.cb[U], st.sc[U], xr, sr, t, kq, acc, bad);
+           }
+           // slot U: this unit's step t + PM, or the next unit's step tb + U
+           const bool more = t + PM < te;
+           typename Stream::Src s;
+#pragma unroll
+           for (int i = 0; i < 2; ++i) {
+             s.code[i] = more ? cur.code[i] : nxt.code[i];
+             s.scale[i] = more ? cur.scale[i] : nxt.scale[i];
+           }
+           const int tn = more ? t + PM : (tb + U < te ? tb + U : te - 1);
+           st.template issue<U>(s, vcode, vscale, tn, p.spg_shift, p.spg_mul);
+           __builtin_amdgcn_sched_barrier(0);
+         }()),
+         ...);
+      }(std::make_integer_sequence<int, PM>{});
+    }
+    if (u < total && __any((bad & 0xAAAAAAAAu) != 0u)) {
+      int64_t e;
+      int j;
+      unit_row(u, e, j);
+      __amdgpu_buffer_rsrc_t shp[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        shp[i] = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + static_cast<int64_t>(i) * p.I + 16 * j) * p.gpr,
+                            64u * static_cast<uint32_t>(p.gpr));
+      layer_extra<SPL, 2>(cur, shp, vcode, vscale, tb, te, p.spg_shift, p.spg_mul, xr, sr, kq, acc);
+    }
+    // partial sums of the team's waves meet in LDS (two rounds' worth, so one
+    // barrier a round); lane group kq holds tokens 2 kq and 2 kq + 1
+    float* rb = red + (r & 1) * red_buf;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      if (2 * kq + m < T)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + 2 * kq + m) * 16 + nl] = acc[i][m];
+    lds_barrier();
+    // h of two neighbouring tiles: one scale block of 32 values per half wave
+    const int nsub = (teams / 2) * T;
+    const int ub = (r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) * teams;
+    for (int s0 = 0; s0 < nsub; s0 += 32) {
+      const int sub = s0 + (tid >> 5);
+      const int c = tid & 31;
+      const int pr = sub / T, t = sub - pr * T;
+      const int u0 = ub + 2 * pr;
+      const bool in = sub < nsub && u0 < total;
+      const int a = in ? u0 / tiles : 0;
+      const int j = in ? u0 - a * tiles : 0;
+      const int slot = in ? s_slot[8 * a + t] : 0xff;
+      float g = 0.0f, uu = 0.0f;
+      if (in) {
+        const int w0 = (2 * pr + (c >> 4)) * ks;
+        for (int k = 0; k < ks; ++k) {
+          g += rb[(w0 + k) * red_wave + t * 16 + (c & 15)];
+          uu += rb[(w0 + k) * red_wave + (T + t) * 16 + (c & 15)];
+        }
+      }
+      const float v = g / (1.0f + expf(-g)) * uu;
+      // rounded to bf16, as the down product's activations are (NaN stays NaN)
+      const float h = v != v ? v : __uint_as_float(bf16_rne_bits(v) << 16);
+      float amax = finite_abs(h);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+      const uint32_t ef = block_exponent(amax);
+      uint32_t hi, lo;
+      split2(h, h, block_factor(ef), hi, lo);
+      if (slot != 0xff) {
+        const int b = j / 2;
+        const int place = 32 * (p.down_spl == 2 ? chunk_place<2>(b) : b) + code_slot(c);
+        uint8_t* hq = p.hq + static_cast<int64_t>(t * topk + slot) * 2 * p.I + place;
+        hq[0] = static_cast<uint8_t>(hi);
+        hq[p.I] = static_cast<uint8_t>(lo);
+        if (c < 2) p.hs[(static_cast<int64_t>(t * topk + slot) * 2 + c) * (p.I / 32) + b] =
+            static_cast<uint8_t>(ef - (c ? 11u : 7u));
+      }
+    }
+    cur = nxt;
+    u += stride;
+  }
+}
+
+struct LayerDownParams {
+  const int32_t* rec;
+  const float* weights;    // [T][topk]
+  int T, topk;
+  const uint8_t* hq;       // [pair][2][I]
+  const uint8_t* hs;       // [pair][2][I / 32]
+  const uint8_t* codes;    // down, expert 0
+  const float* scales;
+  const uint16_t* shapes;
+  int64_t code_bytes;
+  int gpr, spg_shift;
+  uint32_t spg_mul;
+  int H, I;
+  int rows, rt;            // output rows per workgroup, and per tile
+  int ks;                  // K parts per pair
+  void* y;                 // [T][H]
+  int ybf16;
+};
+
+struct LayerDownLds {
+  int wave_bytes, hstride, sstride, sum, total;
+};
+__host__ __device__ inline LayerDownLds layer_down_lds(int T, int I, int spl, int ks) {
+  LayerDownLds L;
+  const int nmacro = I / (spl * 128);
+  const int kp = (nmacro + ks - 1) / ks * spl * 128;             // K values of a part
+  L.hstride = kp + 16;
+  L.sstride = ((kp / 32 + 15) & ~15) + 16;
+  L.wave_bytes = 2 * L.hstride + 2 * L.sstride;
+  L.sum = kLayerWaves * L.wave_bytes;
+  L.total = L.sum + kLayerWaves * T * 32 * 4;
+  return L;
+}
+
+template <int SPL, int PM, int NT>
+__global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using Stream = CodeStream<SPL, PM, NT>;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nl = lane & 15, kq = lane >> 4;
+  const LayerDownLds L = layer_down_lds(p.T, p.I, SPL, p.ks);
+  uint8_t* hreg = smem + wave * L.wave_bytes;
+  uint8_t* sreg = hreg + 2 * L.hstride;
+  float* sums = reinterpret_cast<float*>(smem + L.sum) + wave * p.T * 32;
+  for (int i = lane; i < p.T * 32; i += 64) sums[i] = 0.0f;
+  wave_lds_order();
+  const int n0 = static_cast<int>(blockIdx.x) * p.rows;
+  const int rows = min(p.rows, p.H - n0);
+  const int items = p.rec[0] * p.ks;
+  const int nmacro = p.I / (SPL * 128);
+  const uint32_t row_bytes = static_cast<uint32_t>(p.I / 4);
+  // this lane's row of each tile (past the workgroup's rows: its last one, whose
+  // sums are not used)
+  uint32_t vcode[NT], vscale[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int r = min(i * p.rt + min(nl, p.rt - 1), rows - 1);
+    vcode[i] = r * row_bytes + kq * (Stream::DW * 4);
+    vscale[i] = static_cast<uint32_t>(r * p.gpr * 4);
+  }
+  struct Item {
+    int pair, tb, te;
+    int64_t e;
+    uint32_t live;
+  };
+  auto item_of = [&](int it) {
+    Item q;
+    q.live = it < items ? 1u : 0u;
+    const int ii = it < items ? it : 0;
+    const int job = ii / p.ks, part = ii - job * p.ks;
+    q.pair = __builtin_amdgcn_readfirstlane(p.rec[2 + 2 * job]);
+    q.e = __builtin_amdgcn_readfirstlane(p.rec[3 + 2 * job]);
+    q.tb = part * nmacro / p.ks;
+    q.te = (part + 1) * nmacro / p.ks;
+    return q;
+  };
+  auto source = [&](const Item& q) {
+    typename Stream::Src s;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      s.code[i] = layer_rsrc(p.codes + q.e * p.code_bytes + static_cast<int64_t>(n0) * row_bytes,
+                             q.live * static_cast<uint32_t>(rows) * row_bytes);
+      s.scale[i] = layer_rsrc(p.scales + (q.e * p.H + n0) * p.gpr,
+                              q.live * static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
+    }
+    return s;
+  };
+  int it = wave;
+  if (it < items) {                            // wave-uniform; the barrier comes after
+    Stream st;
+    Item q = item_of(it);
+    typename Stream::Src cur = source(q);
+    [&]<int... U>(std::integer_sequence<int, U...>) {
+      (st.template issue<U>(cur, vcode, vscale, q.tb + U < q.te ? q.tb + U : q.te - 1, p.spg_shift, p.spg_mul), ...);
+    }(std::make_integer_sequence<int, PM>{});
+    const uint8_t* xr = hreg + (nl == 1 ? L.hstride : 0);        // row 0: hi, row 1: lo
+    const uint8_t* sr = sreg + (nl == 1 ? L.sstride : 0);
+    for (; it < items; it += kLayerWaves) {
+      // the part's h halves and scales into this wave's LDS
+      {
+        const int kp = (q.te - q.tb) * SPL * 128;
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc) {
+          const uint8_t* hsrc = p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128;
+          for (int i = lane * 16; i < kp; i += 64 * 16)
+            *reinterpret_cast<u32x4*>(hreg + pc * L.hstride + i) = *reinterpret_cast<const u32x4*>(hsrc + i);
+          const uint8_t* ssrc = p.hs + (static_cast<int64_t>(q.pair) * 2 + pc) * (p.I / 32) + q.tb * SPL * 4;
+          for (int i = lane * 4; i < kp / 32; i += 64 * 4)
+            *reinterpret_cast<uint32_t*>(sreg + pc * L.sstride + i) = *reinterpret_cast<const uint32_t*>(ssrc + i);
+        }
+        wave_lds_order();
+      }
+      const Item qn = item_of(it + kLayerWaves);
+      const typename Stream::Src nxt = source(qn);
+      const float w = p.weights[q.pair];
+      float acc[NT][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = 0.0f;
+      uint32_t bad = 0u;
+      for (int t0 = q.tb; t0 < q.te; t0 += PM) {
+        [&]<int... U>(std::integer_sequence<int, U...>) {
+          (([&] {
+             const int t = t0 + U;
+             if (t < q.te) {
+#pragma unroll
+               for (int i = 0; i < NT; ++i)
+#pragma unroll
+                 for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
+               layer_step<SPL, NT, 0>(st.cb[U], st.sc[U], xr, sr, t - q.tb, kq, acc, bad);
+             }
+             const bool more = t + PM < q.te;
+             typename Stream::Src s;
+#pragma unroll
+             for (int i = 0; i < NT; ++i) {
+               s.code[i] = more ? cur.code[i] : nxt.code[i];
+               s.scale[i] = more ? cur.scale[i] : nxt.scale[i];
+             }
+             const int tn = more ? t + PM : (qn.tb + U < qn.te ? qn.tb + U : qn.te - 1);
+             st.template issue<U>(s, vcode, vscale, tn, p.spg_shift, p.spg_mul);
+             __builtin_amdgcn_sched_barrier(0);
+           }()),
+           ...);
+        }(std::make_integer_sequence<int, PM>{});
+      }
+      if (__any((bad & 0xAAAAAAAAu) != 0u)) {
+        __amdgpu_buffer_rsrc_t shp[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          shp[i] = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
+                              static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
+        const int back = q.tb * SPL * 128;     // (steps count from the part's first in LDS)
+        layer_extra<SPL, NT>(cur, shp, vcode, vscale, q.tb, q.te, p.spg_shift, p.spg_mul, xr - back,
+                             sr - q.tb * SPL * 4, kq, acc);
+      }
+      if (kq == 0) {
+        const int t = q.pair / p.topk;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          if (nl < p.rt) sums[t * 32 + i * p.rt + nl] += w * acc[i][0];
+      }
+      wave_lds_order();
+      q = qn;
+      cur = nxt;
+    }
+  }
+  __syncthreads();
+  // the waves' sums in wave order
+  const float* all = reinterpret_cast<const float*>(smem + L.sum);
+  for (int i = tid; i < p.T * 32; i += 1024) {
+    const int t = i >> 5, r = i & 31;
+    if (r >= rows) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLayerWaves; ++k) v += all[k * p.T * 32 + i];
+    store_out(static_cast<float*>(p.y), p.ybf16 != 0, static_cast<int64_t>(t) * p.H + n0 + r, v);
+  }
+}
+
+// Steps per group as a shift, or a reciprocal for the others (t < 2^16).
+void group_steps(int group, int spl, int* shift, uint32_t* mul) {
+  const int spg = group / (128 * spl);
+  *shift = -1;
+  *mul = 0;
+  if ((spg & (spg - 1)) == 0) {
+    int s = 0;
+    while ((1 << s) < spg) ++s;
+    *shift = s;
+  } else {
+    *mul = static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint32_t>(spg) + 1);
+  }
+}
+
+int layer_spl(int group) { return group % 256 == 0 ? 2 : 1; }
+
+constexpr int kLayerLds = 160 * 1024;
+
+// K parts of kernel 1: the waves of a tile. At least two teams (a scale block of
+// h spans two tiles), and as few rounds of steps as possible for the expected
+// (largest) number of touched experts.
+int layer_up_parts(int T, int topk, int E, int I, int nmacro, int grid) {
+  const int64_t units = static_cast<int64_t>(std::min(E, T * topk)) * (I / 16);
+  int best = 8;
+  int64_t cost = INT64_MAX;
+  for (int ks = 1; ks <= 8; ks *= 2) {
+    if (ks > nmacro && ks > 1) break;
+    const int teams = kLayerWaves / ks;
+    const int64_t rounds = (units + static_cast<int64_t>(grid) * teams - 1) / (static_cast<int64_t>(grid) * teams);
+    const int64_t c = rounds * ((nmacro + ks - 1) / ks) * 8 + rounds;   // steps of a wave, and the rounds' joins
+    if (c < cost) { cost = c; best = ks; }
+  }
+  return best;
+}
+
+// K parts of kernel 2: enough items for every wave, and a part's h in LDS.
+int layer_down_parts(int T, int topk, int E, int I, int spl) {
+  const int nmacro = I / (spl * 128);
+  const int jobs = T * topk;
+  int ks = 1;
+  while (ks < nmacro && (jobs * ks < kLayerWaves || layer_down_lds(T, I, spl, ks).total > kLayerLds)) ks *= 2;
+  return std::min(ks, nmacro);
+}
+
+}  // namespace
+
+// The two-kernel path: 2-bit codes, up to eight tokens, and activations, lists
+// and partial sums in one compute unit's LDS.
+bool moe_layer_fused(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
+                     int dn_group) {
+  if (up_bits != 2 || dn_bits != 2) return false;
+  if (T < 1 || T > kLayerMaxT || E > kLayerMaxE || topk > kRouterMaxTopk) return false;
+  if (H > 65536 || I > 65536) return false;                       // 32-bit tile offsets, LDS
+  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H)).total > kLayerLds) return false;
+  const int spl = layer_spl(dn_group);
+  const int ks = layer_down_parts(static_cast<int>(T), topk, E, static_cast<int>(I), spl);
+  return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks).total <= kLayerLds;
+}
+
+namespace {
+
+template <class Kern, class Par>
+hipError_t launch_layer(Kern kern, unsigned grid, int lds, const Par& p, hipStream_t st) {
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(1024), static_cast<size_t>(lds), st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const MoeLayerWeight& up,
+                            const MoeLayerWeight& dn, int H, int I, const MoeLayerBuffers& b, int32_t* ids_user,
+                            float* weights_user, void* y, int ybf16, hipStream_t st) {
+  const int cu = device_cu_count();
+  const int cus = cu > 0 ? cu : 256;
+  LayerUpParams p{};
+  p.r = router_params(r);
+  p.x = x;
+  p.T = T;
+  p.H = H;
+  p.I = I;
+  p.codes = up.codes;
+  p.scales = up.scales;
+  p.shapes = up.shapes;
+  p.code_bytes = up.code_bytes;
+  p.gpr = H / up.group;
+  const int spl = layer_spl(up.group), dspl = layer_spl(dn.group);
+  group_steps(up.group, spl, &p.spg_shift, &p.spg_mul);
+  const int nmacro = H / (spl * 128);
+  p.ks = layer_up_parts(T, r.topk, r.E, I, nmacro, cus);
+  p.down_spl = dspl;
+  p.ids = b.ids;
+  p.weights = b.weights;
+  p.ids_user = ids_user;
+  p.weights_user = weights_user;
+  p.rec = b.rec;
+  p.hq = b.hq;
+  p.hs = b.hs;
+  const int teams = kLayerWaves / p.ks;
+  const int64_t units = static_cast<int64_t>(std::min(r.E, T * r.topk)) * (I / 16);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
+  const int lds = layer_up_lds(T, r.topk, H).total;
+  const int mpw = (nmacro + p.ks - 1) / p.ks;
+  hipError_t e;
+  if (spl == 2) {
+    // seven steps in flight, or four where a wave's part is short
+    e = mpw <= 4 ? launch_layer(k_layer_up<2, 4>, grid, lds, p, st) : launch_layer(k_layer_up<2, 7>, grid, lds, p, st);
+  } else {
+    e = launch_layer(k_layer_up<1, 8>, grid, lds, p, st);
+  }
+  if (e != hipSuccess) return e;
+
+  LayerDownParams d{};
+  d.rec = b.rec;
+  d.weights = b.weights;
+  d.T = T;
+  d.topk = r.topk;
+  d.hq = b.hq;
+  d.hs = b.hs;
+  d.codes = dn.codes;
+  d.scales = dn.scales;
+  d.shapes = dn.shapes;
+  d.code_bytes = dn.code_bytes;
+  d.gpr = I / dn.group;
+  group_steps(dn.group, dspl, &d.spg_shift, &d.spg_mul);
+  d.H = H;
+  d.I = I;
+  d.rows = std::min(32, std::max(4, (H + cus - 1) / cus));
+  const int nt = d.rows > 16 ? 2 : 1;
+  d.rt = (d.rows + nt - 1) / nt;
+  d.rows = d.rt * nt;
+  d.ks = layer_down_parts(T, r.topk, r.E, I, dspl);
+  d.y = y;
+  d.ybf16 = ybf16;
+  const unsigned dgrid = static_cast<unsigned>((H + d.rows - 1) / d.rows);
+  const int dlds = layer_down_lds(T, I, dspl, d.ks).total;
+  if (dspl == 2) {
+    return nt == 2 ? launch_layer(k_layer_down<2, 6, 2>, dgrid, dlds, d, st)
+                   : launch_layer(k_layer_down<2, 6, 1>, dgrid, dlds, d, st);
+  }
+  return nt == 2 ? launch_layer(k_layer_down<1, 8, 2>, dgrid, dlds, d, st)
+                 : launch_layer(k_layer_down<1, 8, 1>, dgrid, dlds, d, st);
+}
+
+}  // namespace cubic

@@ -61,7 +61,8 @@ enum {
   CUBIC_ERR_CODE_RANGE = -6,  /* cubic_pack found a code with |k| > Kmax       */
   CUBIC_ERR_WORKSPACE = -7,   /* workspace missing or smaller than required    */
   CUBIC_ERR_HIP = -8,         /* a HIP runtime call or a launch failed         */
-  CUBIC_ERR_DTYPE = -9        /* an activation or output dtype not supported   */
+  CUBIC_ERR_DTYPE = -9,       /* an activation or output dtype not supported   */
+  CUBIC_ERR_OPTION = -10      /* an option outside its values                  */
 };
 
 /* Element types of the _ex entry points' activations and outputs (CubicQuant
@@ -349,6 +350,56 @@ int cubic_moe_mlp_a8(const uint16_t* x_bf16, int64_t T, const int32_t* topk_ids,
                      const float* topk_weights, int topk, const cubic_weight* gate_up0,
                      const cubic_weight* down0, int E, float* y, void* workspace, size_t ws_bytes,
                      cubic_stream_t stream);
+
+/* The router of a routed-expert layer (Kimi K3 guide, model card: 896 experts,
+ * 16 active per token). For every token t, from its logits l = logits[t][0..E):
+ *   p    = softmax(l) (CUBIC_SCORE_SOFTMAX) or 1 / (1 + exp(-l)) (CUBIC_SCORE_SIGMOID)
+ *   key  = p + bias (bias enters the selection alone), or l when bias is NULL
+ *   topk_ids[t]     = the topk largest keys in descending order, ties to the lowest index
+ *   topk_weights[t] = p of those, divided by their sum when renormalize is set, times scale
+ * Logits of NaN or -inf mask an expert out: it is never taken and has no share of
+ * the softmax; +inf counts as the largest finite number. A bias of NaN or -inf
+ * keeps an expert from being taken. Slots left over get id -1 and weight 0, which
+ * the routed products skip. Taken scores that sum to zero give weights of zero.
+ * Keys are compared as exact real numbers would be up to fp64 rounding (ids do not
+ * depend on fp32 rounding of the scores); weights are rounded to fp32 once.
+ * logits: [T][E] in logits_dtype CUBIC_DTYPE_F32, _BF16 or _F16; bias fp32 [E] or
+ * NULL; topk_ids int32 and topk_weights fp32 [T][topk]. 1 <= topk <= min(E, 64) and
+ * E <= 2048 (CUBIC_ERR_SHAPE); CUBIC_ERR_OPTION for another score. T == 0 is a no-op. */
+enum { CUBIC_SCORE_SOFTMAX = 0, CUBIC_SCORE_SIGMOID = 1 };
+typedef struct cubic_router {
+  const void* logits;
+  const float* bias;
+  int32_t logits_dtype, E, topk;
+  int32_t score, renormalize;
+  float scale;
+} cubic_router;
+int cubic_moe_topk(const cubic_router* router, int64_t T, int32_t* topk_ids, float* topk_weights,
+                   cubic_stream_t stream);
+
+/* The whole routed-expert layer from router logits to the layer's output: the
+ * router above, then the MLP step of cubic_moe_mlp over the ids and weights it
+ * finds (gate_up0, down0: expert 0 of router->E experts back to back; h rounded to
+ * bf16 there as here):
+ *   y[t] = sum_j topk_weights[t][j] * (bf16(SiLU(g) * u) * D_e^T),  [g | u] = x_t * GU_e^T
+ * A token whose experts are all masked out gets a zero row. For 2-bit weights and
+ * up to eight tokens (E <= 1024, and activations that fit a compute unit's LDS)
+ * the layer runs in two kernels, which read each touched expert's codes from HBM
+ * once; otherwise the router kernel and the MLP step run one after the other, with
+ * the limits of cubic_moe_mlp. In the two kernels the activations are multiplied
+ * exactly unless they lie below 2^-14 of the largest of their 32 neighbours (then
+ * off by up to 2^-22 of that), and a token with a non-finite activation has NaN
+ * rows. The sums' order does not depend on timing.
+ * x_bf16 [T][H]; y [T][H] in y_dtype CUBIC_DTYPE_F32 or CUBIC_DTYPE_BF16 (rounded
+ * once); topk_ids and topk_weights [T][topk] receive the routing, or are NULL. The
+ * workspace (cubic_moe_layer_workspace_bytes) holds the routing and the
+ * intermediates; calls that overlap need one each. Errors as for cubic_moe_topk and
+ * cubic_moe_mlp. */
+size_t cubic_moe_layer_workspace_bytes(int64_t T, int topk, int E, int64_t H, int64_t I);
+int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_router* router,
+                    const cubic_weight* gate_up0, const cubic_weight* down0, void* y, int y_dtype,
+                    int32_t* topk_ids, float* topk_weights, void* workspace, size_t ws_bytes,
+                    cubic_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -62,6 +62,7 @@ __all__ = [
     "level_numerators", "levels", "dequant", "gemm_a16",
     "act_quant", "carrier_table", "carrier_codes", "gemm_a8", "moe_a16", "moe_a8",
     "format_levels", "dequant_f32", "encode", "bf16_rne", "silu_mul", "moe_mlp_hidden", "moe_mlp", "moe_mlp_a8",
+    "moe_topk", "moe_layer",
     "FIT_CLIP_STEPS", "fit_is_monotone", "fit_shape_candidates", "f64_to_f16_bits", "fit_group_sse", "fit",
 ]
 
@@ -730,3 +731,44 @@ def moe_mlp_a8(x_bf16: np.ndarray, topk_ids: np.ndarray, topk_w: np.ndarray, num
             v_all[t, j], h_all[t, j] = v, h
             y[t] += float(topk_w[t, j]) * o
     return y, v_all, h_all
+
+
+def moe_topk(logits: np.ndarray, topk: int, score: str, bias=None, renormalize: bool = True, scale: float = 1.0):
+    """The router: (ids int32 [T][topk], weights float64 [T][topk]). Scores are the softmax or the
+    sigmoid of the logits (values as float64); experts are taken by score + bias, without a bias by
+    the logit, in descending order, ties to the lowest index. NaN and -inf logits are masked out of
+    scores and selection, NaN and -inf biases out of the selection; +inf counts as the largest fp32."""
+    big = float(np.finfo(np.float32).max)
+    L = np.asarray(logits, dtype=np.float64)
+    T, E = L.shape
+    ids = np.full((T, topk), -1, dtype=np.int32)
+    weights = np.zeros((T, topk))
+    b = np.zeros(E) if bias is None else np.minimum(np.asarray(bias, dtype=np.float64), big)
+    for t in range(T):
+        l = np.minimum(L[t], big)
+        there = ~np.isnan(l) & (l > -np.inf)
+        p = np.zeros(E)
+        if there.any():
+            if score == "softmax":
+                e = np.exp(l[there] - l[there].max())
+                p[there] = e / e.sum()
+            else:
+                with np.errstate(over="ignore"):
+                    p[there] = 1.0 / (1.0 + np.exp(-l[there]))
+        key = (l if bias is None else p + b)
+        able = [e for e in range(E) if there[e] and not np.isnan(b[e]) and b[e] > -np.inf]
+        order = sorted(able, key=lambda e: (-key[e], e))[:topk]
+        ids[t, :len(order)] = order
+        weights[t, :len(order)] = p[order]
+        total = weights[t].sum()
+        if renormalize and total > 0:
+            weights[t] /= total
+    return ids, weights * scale
+
+
+def moe_layer(x_bf16: np.ndarray, logits: np.ndarray, topk: int, score: str, gate_up_weight, down_weight, bias=None,
+              renormalize: bool = True, scale: float = 1.0):
+    """The whole routed-expert layer: moe_topk, then moe_mlp over its ids and weights. Returns
+    (y float64 [T][H], ids, weights)."""
+    ids, weights = moe_topk(logits, topk, score, bias, renormalize, scale)
+    return moe_mlp(x_bf16, ids, weights, logits.shape[1], gate_up_weight, down_weight), ids, weights
