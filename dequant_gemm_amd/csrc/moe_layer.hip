@@ -96,44 +96,78 @@ __device__ __forceinline__ int chunk_place(int b) {
 }
 
 // ---- a wave's stream of code tiles ------------------------------------------
-// NT tiles of 16 weight rows, macro steps of SPL * 128 codes, PM steps in flight.
-template <int NT>
+// NT tiles of 16 weight rows, macro steps of SPL * 128 codes, in blocks of PM
+// steps that are in flight together. The MFMA wants row nl and K quarter kq in lane
+// 16 kq + nl, but the address unit takes four neighbouring lanes at a time: loads in
+// that order touch four rows a quad, and a load instruction takes four times as
+// long. So lane l loads quarter l % 4 of row l / 4 (64 contiguous bytes a quad, the
+// group scales of four steps likewise), and the lanes exchange the words through
+// the LDS crossbar when they are used (ds_bpermute, no LDS memory).
 struct CodeSrc {                               // a unit's code and scale buffers (wave-uniform)
-  __amdgpu_buffer_rsrc_t code[NT], scale[NT];
+  __amdgpu_buffer_rsrc_t code, scale;
+};
+
+struct Groups {                                // steps per group: as a shift, or (shift < 0) by a reciprocal
+  int shift;
+  uint32_t mul;
+  __device__ __forceinline__ int of(int t) const {   // t < 2^16
+    return shift >= 0 ? t >> shift : static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * mul) >> 32);
+  }
 };
 
 template <int SPL, int PM, int NT>
 struct CodeStream {
   static constexpr int DW = 2 * SPL;           // code dwords per lane, tile and step
+  static constexpr int SR = (PM + 3) / 4;      // scale registers per tile and block (four steps each)
   uint32_t cb[PM][NT][DW];
-  float sc[PM][NT];
+  float sc[NT][SR], scn[NT][SR];               // of the current block, and of the next
 
-  using Src = CodeSrc<NT>;
-
-  // step t of src into slot u; spg: steps per group
+  // step t into slot U; vcode: the lane's byte offset per tile
   template <int U>
-  __device__ __forceinline__ void issue(const Src& src, const uint32_t* vcode, const uint32_t* vscale, int t,
-                                        int spg_shift, uint32_t spg_mul) {
-    const int g = group_of(t, spg_shift, spg_mul);
+  __device__ __forceinline__ void issue(const CodeSrc& src, const uint32_t* vcode, int t) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       if constexpr (SPL == 2) {
-        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.code[i], vcode[i], t * (4 * DW * 4), 0);
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.code, vcode[i], t * (4 * DW * 4), 0);
         cb[U][i][0] = v.x; cb[U][i][1] = v.y; cb[U][i][2] = v.z; cb[U][i][3] = v.w;
       } else {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.code[i], vcode[i], t * (4 * DW * 4), 0);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.code, vcode[i], t * (4 * DW * 4), 0);
         cb[U][i][0] = v.x; cb[U][i][1] = v.y;
       }
-      sc[U][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src.scale[i], vscale[i], g * 4, 0));
     }
   }
-  // t / spg for t < 2^16: by a shift (powers of two) or a 32-bit reciprocal
-  static __device__ __forceinline__ int group_of(int t, int shift, uint32_t mul) {
-    return shift >= 0 ? t >> shift : static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * mul) >> 32);
+  // the group scales of a block into scn: lane l takes row l / 4 at the block's
+  // steps 4 r + l % 4; step(i) is the i-th step of the block
+  template <class Step>
+  __device__ __forceinline__ void issue_scales(const CodeSrc& src, const uint32_t* vscale, const Groups& gr, int lane,
+                                               Step step) {
+#pragma unroll
+    for (int r = 0; r < SR; ++r) {
+      const uint32_t g = 4u * static_cast<uint32_t>(gr.of(step(4 * r + (lane & 3))));
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        scn[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src.scale, vscale[i] + g, 0, 0));
+    }
+  }
+  __device__ __forceinline__ void take_scales() {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < SR; ++r) sc[i][r] = scn[i][r];
+  }
+  // slot U in operand order: w[tile][dword], s[tile]; xaddr = 4 (4 nl + kq)
+  template <int U>
+  __device__ __forceinline__ void take(int xaddr, int nl, uint32_t (*w)[DW], float* s) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int d = 0; d < DW; ++d)
+        w[i][d] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(xaddr, static_cast<int>(cb[U][i][d])));
+      s[i] = __uint_as_float(static_cast<uint32_t>(
+          __builtin_amdgcn_ds_bpermute(16 * nl + 4 * (U & 3), static_cast<int>(__float_as_uint(sc[i][U / 4])))));
+    }
   }
 };
-
-typedef __attribute__((address_space(3))) const uint8_t lds_u8;
 
 // One macro step: A rows from LDS (xr: this lane's row, its bytes in operand
 // order; sr: its scale bytes), B from the code words of NT tiles. The step's sum
@@ -190,24 +224,26 @@ __device__ __forceinline__ void layer_step(const uint32_t (*w)[2 * SPL], const f
 }
 
 // The slow pass: the level of the field 10 (code -2) is -q(2) s, q(2) = 2 a + 4 b +
-// 8 (1 - a - b); its codes' sums are added step by step.
+// 8 (1 - a - b); its codes' sums are added step by step. Loads in operand order:
+// vcode, vscale as in the stream, but of row nl and quarter kq.
 template <int SPL, int NT>
-__device__ __forceinline__ void layer_extra(const CodeSrc<NT>& src, const __amdgpu_buffer_rsrc_t* shp, const uint32_t* vcode,
-                                                      const uint32_t* vscale, int tb, int te, int spg_shift,
-                                                      uint32_t spg_mul, const uint8_t* xr, const uint8_t* sr, int kq,
-                                                      float (*acc)[2]) {
+__device__ __forceinline__ void layer_extra(const CodeSrc& src, const __amdgpu_buffer_rsrc_t& shp,
+                                            const uint32_t* vcode, const uint32_t* vscale, int tb, int te, int by,
+                                            const Groups& gr, const uint8_t* xr, const uint8_t* sr, int kq,
+                                            float (*acc)[2]) {
 #pragma unroll 1
-  for (int t = tb; t < te; ++t) {
+  for (int t = tb; t < te; t += by) {
     CodeStream<SPL, 1, NT> st;
-    st.template issue<0>(src, vcode, vscale, t, spg_shift, spg_mul);
-    const int g = CodeStream<SPL, 1, NT>::group_of(t, spg_shift, spg_mul);
+    st.template issue<0>(src, vcode, t);
+    const int g = gr.of(t);
     float lev[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const uint32_t ab = __builtin_amdgcn_raw_buffer_load_b32(shp[i], vscale[i], g * 4, 0);
+      const float s = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src.scale, vscale[i], g * 4, 0));
+      const uint32_t ab = __builtin_amdgcn_raw_buffer_load_b32(shp, vscale[i], g * 4, 0);
       const double a = f16_bits_to_f64(static_cast<uint16_t>(ab & 0xffffu));
       const double b = f16_bits_to_f64(static_cast<uint16_t>(ab >> 16));
-      lev[i] = static_cast<float>(-static_cast<double>(st.sc[0][i]) * level_numerator(a, b, 2, 1));
+      lev[i] = static_cast<float>(-static_cast<double>(s) * level_numerator(a, b, 2, 1));
     }
     uint32_t none = 0u;
     layer_step<SPL, NT, 1>(st.cb[0], lev, xr, sr, t, kq, acc, none);
@@ -227,13 +263,10 @@ __global__ __launch_bounds__(256) void k_moe_topk(RouterParams p, int64_t T, int
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (t >= T) return;                          // no barrier in this kernel
-  int id;
-  float w;
-  wave_topk<EPL>(p, t, lane, cand[wave], &id, &w);
-  if (lane < p.topk) {
-    ids[t * p.topk + lane] = id;
-    weights[t * p.topk + lane] = w;
-  }
+  wave_topk<EPL>(p, t, lane, cand[wave], [&](int slot, int id, float w) {
+    ids[t * p.topk + slot] = id;
+    weights[t * p.topk + slot] = w;
+  });
 }
 
 static RouterParams router_params(const MoeRouter& r) {
@@ -267,9 +300,9 @@ struct LayerUpParams {
   const uint16_t* shapes;
   int64_t code_bytes;
   int gpr;                 // groups per row
-  int spg_shift;           // steps per group as a shift, or -1
-  uint32_t spg_mul;
+  Groups groups;           // steps per group
   int ks;                  // waves per tile (each a part of K)
+  int batch;               // rounds between the joins of the waves' sums
   int down_spl;            // operand order of h
   int32_t* ids;            // [T][topk] out
   float* weights;
@@ -284,7 +317,7 @@ struct LayerUpLds {
   int xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
   int xq_stride, xs_stride;
 };
-__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H) {
+__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int batch) {
   LayerUpLds L;
   const int P = T * topk;
   auto up16 = [](int v) { return (v + 15) & ~15; };
@@ -293,9 +326,9 @@ __host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H) {
   int o = 0;
   L.xq = o;    o += 2 * T * L.xq_stride;
   L.xs = o;    o += 2 * T * L.xs_stride;
-  // partial sums, two rounds: [2][waves][2 tiles][T][16]; the first-pair table of
-  // the experts uses the same bytes before the first round
-  const int red = 2 * kLayerWaves * 2 * T * 16 * 4;
+  // partial sums, two batches of rounds: [2][batch][waves][2 tiles][T][16]; the
+  // first-pair table of the experts uses the same bytes before the first round
+  const int red = 2 * batch * kLayerWaves * 2 * T * 16 * 4;
   L.red = o;   o += red > kLayerMaxE * 4 ? red : kLayerMaxE * 4;
   L.first = L.red;
   L.id = o;    o += up16(P * 4);
@@ -316,7 +349,7 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
   const int T = p.T, topk = p.r.topk, P = T * topk;
-  const LayerUpLds L = layer_up_lds(T, topk, p.H);
+  const LayerUpLds L = layer_up_lds(T, topk, p.H, p.batch);
   int32_t* s_first = reinterpret_cast<int32_t*>(smem + L.first);
   int32_t* s_id = reinterpret_cast<int32_t*>(smem + L.id);
   float* s_w = reinterpret_cast<float*>(smem + L.w);
@@ -326,13 +359,11 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
 
   // ---- the tokens' routers (one wave each), and x split into its halves ----
   if (wave < T) {
-    int id;
-    float w;
-    wave_topk<kLayerMaxE / 64>(p.r, wave, lane, reinterpret_cast<uint32_t*>(smem + L.cand) + 64 * wave, &id, &w);
-    if (lane < topk) {
-      s_id[wave * topk + lane] = id;
-      s_w[wave * topk + lane] = w;
-    }
+    wave_topk<kLayerMaxE / 64>(p.r, wave, lane, reinterpret_cast<uint32_t*>(smem + L.cand) + 64 * wave,
+                               [&](int slot, int id, float w) {
+                                 s_id[wave * topk + slot] = id;
+                                 s_w[wave * topk + slot] = w;
+                               });
   }
   for (int e = tid; e < p.r.E; e += 1024) s_first[e] = INT32_MAX;
   for (int i = tid; i < 2 * P; i += 1024) reinterpret_cast<uint32_t*>(s_slot)[i] = 0xffffffffu;
@@ -384,8 +415,11 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   if (pe >= 0) atomicMin(&s_first[pe], tid);
   __syncthreads();
   const bool lead = pe >= 0 && s_first[pe] == tid;
-  const uint64_t leads = __ballot(lead);
-  if (lane == 0 && wave < 8) s_misc[wave] = __popcll(leads);     // P <= 512 threads
+  const uint64_t leads = __ballot(lead), routed = __ballot(pe >= 0);
+  if (lane == 0 && wave < 8) {                 // P <= 512 threads
+    s_misc[wave] = __popcll(leads);
+    s_misc[8 + wave] = __popcll(routed);
+  }
   __syncthreads();
   int n = 0, before = 0;
 #pragma unroll
@@ -401,33 +435,29 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
     s_first[pe] = -1 - a;                      // from here on the expert's place
   }
   __syncthreads();
-  if (pe >= 0) {
-    const int t = tid / topk;
-    s_slot[8 * (-1 - s_first[pe]) + t] = static_cast<uint8_t>(tid - t * topk);
-  }
+  const int pa = pe >= 0 ? -1 - s_first[pe] : 0;
+  const int pt = tid / topk;                   // the pair's token
+  if (pe >= 0) s_slot[8 * pa + pt] = static_cast<uint8_t>(tid - pt * topk);
   __syncthreads();
   if (blockIdx.x == 0) {
     // for kernel 2 and the caller: ids, weights and the pairs grouped by expert
     if (tid < P) {
+      const float w = s_w[tid];
       p.ids[tid] = pe;
-      p.weights[tid] = s_w[tid];
+      p.weights[tid] = w;
       if (p.ids_user) p.ids_user[tid] = pe;
-      if (p.weights_user) p.weights_user[tid] = s_w[tid];
+      if (p.weights_user) p.weights_user[tid] = w;
     }
-    int pos = 0;
-    const int a0 = pe >= 0 ? -1 - s_first[pe] : 0;
     if (pe >= 0) {
-      const int t = tid / topk;
-      for (int a = 0; a <= a0; ++a)
-#pragma unroll
-        for (int tt = 0; tt < kLayerMaxT; ++tt)
-          pos += (s_slot[8 * a + tt] != 0xffu && (a < a0 || tt < t)) ? 1 : 0;
+      // slots are below 64: the top bit of a byte is set where no token is
+      int pos = 0;
+      for (int a = 0; a < pa; ++a)
+        pos += 8 - __popcll(*reinterpret_cast<const uint64_t*>(s_slot + 8 * a) & 0x8080808080808080ull);
+      const uint64_t own = *reinterpret_cast<const uint64_t*>(s_slot + 8 * pa);
+      pos += pt - __popcll(own & 0x8080808080808080ull & ((uint64_t{1} << (8 * pt)) - 1u));
       p.rec[2 + 2 * pos] = tid;
       p.rec[3 + 2 * pos] = pe;
     }
-    const uint64_t on = __ballot(pe >= 0);
-    if (lane == 0 && wave < 8) s_misc[8 + wave] = __popcll(on);
-    __syncthreads();                           // (block-uniform branch)
     if (tid == 0) {
       int all = 0;
       for (int k = 0; k < 8; ++k) all += s_misc[8 + k];
@@ -441,11 +471,20 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   const int tiles = p.I / 16;
   const int total = n * tiles;
   const int nmacro = p.H / (SPL * 128);
-  const int tb = part * nmacro / ks, te = (part + 1) * nmacro / ks;
+  // this wave's steps: part, part + ks, ... (the team's waves read neighbouring
+  // pieces of a row at any time)
+  const int steps = (nmacro - part + ks - 1) / ks;
   const uint32_t row_bytes = static_cast<uint32_t>(p.H / 4);
-  const uint32_t vcode1 = nl * row_bytes + kq * (Stream::DW * 4);
-  const uint32_t vscale1 = static_cast<uint32_t>(nl * p.gpr * 4);
-  const uint32_t vcode[2] = {vcode1, vcode1}, vscale[2] = {vscale1, vscale1};
+  // a gate row of the tile, and the up row I rows below it
+  auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
+    vc[0] = row * row_bytes + quarter * (Stream::DW * 4);
+    vc[1] = vc[0] + static_cast<uint32_t>(p.I) * row_bytes;
+    vs[0] = static_cast<uint32_t>(row * p.gpr * 4);
+    vs[1] = vs[0] + static_cast<uint32_t>(p.I * p.gpr * 4);
+  };
+  uint32_t vcode[2], vscale[2];
+  lane_offsets(lane >> 2, lane & 3, vcode, vscale);
+  const int xaddr = 4 * (4 * nl + kq);
   const int ml = nl < 2 * T ? nl : 0;          // rows past the tokens are not used
   const uint8_t* xr = smem + L.xq + ml * L.xq_stride;
   const uint8_t* sr = smem + L.xs + ml * L.xs_stride;
@@ -457,17 +496,13 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
     e = __builtin_amdgcn_readfirstlane(s_exp[a]);
   };
   auto source = [&](int u) {
-    typename Stream::Src s;
+    CodeSrc s;
     int64_t e;
     int j;
     unit_row(u, e, j);
-    const uint32_t live = u < total ? 1u : 0u;  // no unit: every load is out of range and reads nothing
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t row = static_cast<int64_t>(i) * p.I + 16 * j;
-      s.code[i] = layer_rsrc(p.codes + e * p.code_bytes + row * row_bytes, live * 16u * row_bytes);
-      s.scale[i] = layer_rsrc(p.scales + (e * 2 * p.I + row) * p.gpr, live * 64u * static_cast<uint32_t>(p.gpr));
-    }
+    const uint32_t rows = u < total ? static_cast<uint32_t>(p.I + 16) : 0u;   // no unit: every load is out of range
+    s.code = layer_rsrc(p.codes + e * p.code_bytes + static_cast<int64_t>(16 * j) * row_bytes, rows * row_bytes);
+    s.scale = layer_rsrc(p.scales + (e * 2 * p.I + 16 * j) * p.gpr, rows * 4u * static_cast<uint32_t>(p.gpr));
     return s;
   };
   if (n == 0) return;                          // no expert taken at all (block-uniform)
@@ -477,38 +512,41 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   if (rounds <= 0) return;
 
   Stream st;
-  typename Stream::Src cur = source(u);
+  CodeSrc cur = source(u);
+  st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return min(i, steps - 1) * ks + part; });
   [&]<int... U>(std::integer_sequence<int, U...>) {
-    (st.template issue<U>(cur, vcode, vscale, tb + U < te ? tb + U : (te > tb ? te - 1 : 0), p.spg_shift, p.spg_mul), ...);
+    (st.template issue<U>(cur, vcode, min(U, steps - 1) * ks + part), ...);
   }(std::make_integer_sequence<int, PM>{});
 
   float* red = reinterpret_cast<float*>(smem + L.red);
-  const int red_wave = 2 * T * 16, red_buf = kLayerWaves * red_wave;
+  const int red_wave = 2 * T * 16, red_round = kLayerWaves * red_wave;
+  int slot_r = 0, half = 0, r0 = 0;            // round of the batch, its buffer, its first round
   for (int r = 0; r < rounds; ++r) {
-    const typename Stream::Src nxt = source(u + stride);
+    const CodeSrc nxt = source(u + stride);
     float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
     uint32_t bad = 0u;
-    for (int t0 = tb; t0 < te; t0 += PM) {
+    for (int t0 = 0; t0 < steps; t0 += PM) {
+      // the next block: this unit's next PM steps, or the next unit's first
+      st.take_scales();
+      const bool more = t0 + PM < steps;
+      CodeSrc src;
+      src.code = more ? cur.code : nxt.code;
+      src.scale = more ? cur.scale : nxt.scale;
+      const int tn = more ? t0 + PM : 0;
+      st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return min(tn + i, steps - 1) * ks + part; });
       [&]<int... U>(std::integer_sequence<int, U...>) {
         (([&] {
-           const int t = t0 + U;
-           if (t < te) {
+           if (t0 + U < steps) {
+             uint32_t w[2][Stream::DW];
+             float s[2];
 #pragma unroll
              for (int i = 0; i < 2; ++i)
 #pragma unroll
                for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
-             layer_step<SPL, 2, 0>(st.cb[U], st.sc[U], xr, sr, t, kq, acc, bad);
+             st.template take<U>(xaddr, nl, w, s);
+             layer_step<SPL, 2, 0>(w, s, xr, sr, (t0 + U) * ks + part, kq, acc, bad);
            }
-           // slot U: this unit's step t + PM, or the next unit's step tb + U
-           const bool more = t + PM < te;
-           typename Stream::Src s;
-#pragma unroll
-           for (int i = 0; i < 2; ++i) {
-             s.code[i] = more ? cur.code[i] : nxt.code[i];
-             s.scale[i] = more ? cur.scale[i] : nxt.scale[i];
-           }
-           const int tn = more ? t + PM : (tb + U < te ? tb + U : te - 1);
-           st.template issue<U>(s, vcode, vscale, tn, p.spg_shift, p.spg_mul);
+           st.template issue<U>(src, vcode, min(tn + U, steps - 1) * ks + part);
            __builtin_amdgcn_sched_barrier(0);
          }()),
          ...);
@@ -518,40 +556,47 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       int64_t e;
       int j;
       unit_row(u, e, j);
-      __amdgpu_buffer_rsrc_t shp[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        shp[i] = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + static_cast<int64_t>(i) * p.I + 16 * j) * p.gpr,
-                            64u * static_cast<uint32_t>(p.gpr));
-      layer_extra<SPL, 2>(cur, shp, vcode, vscale, tb, te, p.spg_shift, p.spg_mul, xr, sr, kq, acc);
+      const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + 16 * j) * p.gpr,
+                                                    static_cast<uint32_t>(p.I + 16) * 4u * static_cast<uint32_t>(p.gpr));
+      uint32_t vc[2], vs[2];
+      lane_offsets(nl, kq, vc, vs);
+      layer_extra<SPL, 2>(cur, shp, vc, vs, part, nmacro, ks, p.groups, xr, sr, kq, acc);
     }
-    // partial sums of the team's waves meet in LDS (two rounds' worth, so one
-    // barrier a round); lane group kq holds tokens 2 kq and 2 kq + 1
-    float* rb = red + (r & 1) * red_buf;
+    // partial sums of the team's waves meet in LDS; lane group kq holds tokens 2 kq
+    // and 2 kq + 1
+    float* rb = red + (half * p.batch + slot_r) * red_round;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
       if (2 * kq + m < T)
 #pragma unroll
         for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + 2 * kq + m) * 16 + nl] = acc[i][m];
+    cur = nxt;
+    u += stride;
+    ++slot_r;
+    if (slot_r < p.batch && r + 1 < rounds) continue;
+    // A join of the waves every `batch` rounds: in between they run apart, so that a
+    // wave whose loads come late holds nobody up. Two batches of sums: one barrier.
     lds_barrier();
     // h of two neighbouring tiles: one scale block of 32 values per half wave
-    const int nsub = (teams / 2) * T;
-    const int ub = (r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) * teams;
+    const int pairs = teams / 2;
+    const int nsub = slot_r * pairs * T;
+    const float* hb = red + half * p.batch * red_round;
     for (int s0 = 0; s0 < nsub; s0 += 32) {
       const int sub = s0 + (tid >> 5);
       const int c = tid & 31;
-      const int pr = sub / T, t = sub - pr * T;
-      const int u0 = ub + 2 * pr;
+      const int t = sub % T, rp = sub / T;
+      const int rr = rp / pairs, pr = rp - rr * pairs;
+      const int u0 = ((r0 + rr) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) * teams + 2 * pr;
       const bool in = sub < nsub && u0 < total;
       const int a = in ? u0 / tiles : 0;
       const int j = in ? u0 - a * tiles : 0;
       const int slot = in ? s_slot[8 * a + t] : 0xff;
       float g = 0.0f, uu = 0.0f;
       if (in) {
-        const int w0 = (2 * pr + (c >> 4)) * ks;
+        const float* src = hb + rr * red_round + (2 * pr + (c >> 4)) * ks * red_wave + t * 16 + (c & 15);
         for (int k = 0; k < ks; ++k) {
-          g += rb[(w0 + k) * red_wave + t * 16 + (c & 15)];
-          uu += rb[(w0 + k) * red_wave + (T + t) * 16 + (c & 15)];
+          g += src[k * red_wave];
+          uu += src[k * red_wave + T * 16];
         }
       }
       const float v = g / (1.0f + expf(-g)) * uu;
@@ -573,8 +618,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
             static_cast<uint8_t>(ef - (c ? 11u : 7u));
       }
     }
-    cur = nxt;
-    u += stride;
+    half ^= 1;
+    slot_r = 0;
+    r0 = r + 1;
   }
 }
 
@@ -588,8 +634,8 @@ struct LayerDownParams {
   const float* scales;
   const uint16_t* shapes;
   int64_t code_bytes;
-  int gpr, spg_shift;
-  uint32_t spg_mul;
+  int gpr;
+  Groups groups;
   int H, I;
   int rows, rt;            // output rows per workgroup, and per tile
   int ks;                  // K parts per pair
@@ -612,6 +658,59 @@ __host__ __device__ inline LayerDownLds layer_down_lds(int T, int I, int spl, in
   return L;
 }
 
+// One (pair, K part): the pair, its steps [tb, te), its expert; live 0: none.
+struct DownItem {
+  int pair, tb, te;
+  int64_t e;
+  uint32_t live;
+};
+
+// An item's h halves and block scales on their way into the wave's LDS: the first
+// 6 KB (a part of 3 K values) wait in registers, so that they are loaded before the
+// codes of their item; longer parts load the rest at the store.
+template <int SPL>
+struct DownActs {
+  static constexpr int R = 6;
+  u32x4 v[R];
+  uint32_t sv;
+  static __device__ __forceinline__ const uint8_t* row(const LayerDownParams& p, const DownItem& q, int pc) {
+    return p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128;
+  }
+  static __device__ __forceinline__ const uint8_t* scales(const LayerDownParams& p, const DownItem& q, int pc) {
+    return p.hs + (static_cast<int64_t>(q.pair) * 2 + pc) * (p.I / 32) + q.tb * SPL * 4;
+  }
+  // 16-byte chunk i of the part's two rows: row i / n, chunk i % n (n chunks a row)
+  __device__ __forceinline__ void load(const LayerDownParams& p, const DownItem& q, int lane) {
+    const int n = (q.te - q.tb) * SPL * 8;
+    const uint8_t* hi = row(p, q, 0);
+    const uint8_t* lo = row(p, q, 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = min(64 * r + lane, 2 * n - 1);
+      v[r] = *reinterpret_cast<const u32x4*>(i < n ? hi + 16 * i : lo + 16 * (i - n));
+    }
+    const int m = n / 8;                       // scale dwords a row
+    const int i = min(lane, 2 * m - 1);
+    sv = *reinterpret_cast<const uint32_t*>(i < m ? scales(p, q, 0) + 4 * i : scales(p, q, 1) + 4 * (i - m));
+  }
+  __device__ __forceinline__ void store(const LayerDownParams& p, const DownItem& q, uint8_t* hreg, uint8_t* sreg,
+                                        const LayerDownLds& L, int lane) const {
+    const int n = (q.te - q.tb) * SPL * 8, m = n / 8;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = 64 * r + lane;
+      if (i < 2 * n) *reinterpret_cast<u32x4*>(hreg + (i < n ? 16 * i : L.hstride + 16 * (i - n))) = v[r];
+    }
+    if (lane < 2 * m) *reinterpret_cast<uint32_t*>(sreg + (lane < m ? 4 * lane : L.sstride + 4 * (lane - m))) = sv;
+    for (int i = 64 * R + lane; i < 2 * n; i += 64)
+      *reinterpret_cast<u32x4*>(hreg + (i < n ? 16 * i : L.hstride + 16 * (i - n))) =
+          *reinterpret_cast<const u32x4*>(row(p, q, i < n ? 0 : 1) + 16 * (i < n ? i : i - n));
+    for (int i = 64 + lane; i < 2 * m; i += 64)
+      *reinterpret_cast<uint32_t*>(sreg + (i < m ? 4 * i : L.sstride + 4 * (i - m))) =
+          *reinterpret_cast<const uint32_t*>(scales(p, q, i < m ? 0 : 1) + 4 * (i < m ? i : i - m));
+  }
+};
+
 template <int SPL, int PM, int NT>
 __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -630,20 +729,19 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   const int items = p.rec[0] * p.ks;
   const int nmacro = p.I / (SPL * 128);
   const uint32_t row_bytes = static_cast<uint32_t>(p.I / 4);
-  // this lane's row of each tile (past the workgroup's rows: its last one, whose
-  // sums are not used)
-  uint32_t vcode[NT], vscale[NT];
+  // a row of each tile (past the workgroup's rows: its last one, whose sums are not used)
+  auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int r = min(i * p.rt + min(nl, p.rt - 1), rows - 1);
-    vcode[i] = r * row_bytes + kq * (Stream::DW * 4);
-    vscale[i] = static_cast<uint32_t>(r * p.gpr * 4);
-  }
-  struct Item {
-    int pair, tb, te;
-    int64_t e;
-    uint32_t live;
+    for (int i = 0; i < NT; ++i) {
+      const int r = min(i * p.rt + min(row, p.rt - 1), rows - 1);
+      vc[i] = r * row_bytes + quarter * (Stream::DW * 4);
+      vs[i] = static_cast<uint32_t>(r * p.gpr * 4);
+    }
   };
+  uint32_t vcode[NT], vscale[NT];
+  lane_offsets(lane >> 2, lane & 3, vcode, vscale);
+  const int xaddr = 4 * (4 * nl + kq);
+  using Item = DownItem;
   auto item_of = [&](int it) {
     Item q;
     q.live = it < items ? 1u : 0u;
@@ -656,82 +754,71 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
     return q;
   };
   auto source = [&](const Item& q) {
-    typename Stream::Src s;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      s.code[i] = layer_rsrc(p.codes + q.e * p.code_bytes + static_cast<int64_t>(n0) * row_bytes,
-                             q.live * static_cast<uint32_t>(rows) * row_bytes);
-      s.scale[i] = layer_rsrc(p.scales + (q.e * p.H + n0) * p.gpr,
-                              q.live * static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
-    }
+    CodeSrc s;
+    s.code = layer_rsrc(p.codes + q.e * p.code_bytes + static_cast<int64_t>(n0) * row_bytes,
+                        q.live * static_cast<uint32_t>(rows) * row_bytes);
+    s.scale = layer_rsrc(p.scales + (q.e * p.H + n0) * p.gpr,
+                         q.live * static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
     return s;
   };
   int it = wave;
   if (it < items) {                            // wave-uniform; the barrier comes after
     Stream st;
+    DownActs<SPL> hst;
     Item q = item_of(it);
-    typename Stream::Src cur = source(q);
+    CodeSrc cur = source(q);
+    hst.load(p, q, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return min(q.tb + i, q.te - 1); });
     [&]<int... U>(std::integer_sequence<int, U...>) {
-      (st.template issue<U>(cur, vcode, vscale, q.tb + U < q.te ? q.tb + U : q.te - 1, p.spg_shift, p.spg_mul), ...);
+      (st.template issue<U>(cur, vcode, min(q.tb + U, q.te - 1)), ...);
     }(std::make_integer_sequence<int, PM>{});
     const uint8_t* xr = hreg + (nl == 1 ? L.hstride : 0);        // row 0: hi, row 1: lo
     const uint8_t* sr = sreg + (nl == 1 ? L.sstride : 0);
     for (; it < items; it += kLayerWaves) {
-      // the part's h halves and scales into this wave's LDS
-      {
-        const int kp = (q.te - q.tb) * SPL * 128;
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-          const uint8_t* hsrc = p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128;
-          for (int i = lane * 16; i < kp; i += 64 * 16)
-            *reinterpret_cast<u32x4*>(hreg + pc * L.hstride + i) = *reinterpret_cast<const u32x4*>(hsrc + i);
-          const uint8_t* ssrc = p.hs + (static_cast<int64_t>(q.pair) * 2 + pc) * (p.I / 32) + q.tb * SPL * 4;
-          for (int i = lane * 4; i < kp / 32; i += 64 * 4)
-            *reinterpret_cast<uint32_t*>(sreg + pc * L.sstride + i) = *reinterpret_cast<const uint32_t*>(ssrc + i);
-        }
-        wave_lds_order();
-      }
+      hst.store(p, q, hreg, sreg, L, lane);    // the part's h into this wave's LDS
+      wave_lds_order();
       const Item qn = item_of(it + kLayerWaves);
-      const typename Stream::Src nxt = source(qn);
+      const CodeSrc nxt = source(qn);
       const float w = p.weights[q.pair];
+      hst.load(p, qn, lane);                   // ahead of the next item's codes
       float acc[NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = 0.0f;
       uint32_t bad = 0u;
       for (int t0 = q.tb; t0 < q.te; t0 += PM) {
+        st.take_scales();
+        const bool more = t0 + PM < q.te;
+        CodeSrc src;
+        src.code = more ? cur.code : nxt.code;
+        src.scale = more ? cur.scale : nxt.scale;
+        const int tn = more ? t0 + PM : qn.tb, last = (more ? q.te : qn.te) - 1;
+        st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return min(tn + i, last); });
         [&]<int... U>(std::integer_sequence<int, U...>) {
           (([&] {
-             const int t = t0 + U;
-             if (t < q.te) {
+             if (t0 + U < q.te) {
+               uint32_t w4[NT][Stream::DW];
+               float s[NT];
 #pragma unroll
                for (int i = 0; i < NT; ++i)
 #pragma unroll
                  for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
-               layer_step<SPL, NT, 0>(st.cb[U], st.sc[U], xr, sr, t - q.tb, kq, acc, bad);
+               st.template take<U>(xaddr, nl, w4, s);
+               layer_step<SPL, NT, 0>(w4, s, xr, sr, t0 + U - q.tb, kq, acc, bad);
              }
-             const bool more = t + PM < q.te;
-             typename Stream::Src s;
-#pragma unroll
-             for (int i = 0; i < NT; ++i) {
-               s.code[i] = more ? cur.code[i] : nxt.code[i];
-               s.scale[i] = more ? cur.scale[i] : nxt.scale[i];
-             }
-             const int tn = more ? t + PM : (qn.tb + U < qn.te ? qn.tb + U : qn.te - 1);
-             st.template issue<U>(s, vcode, vscale, tn, p.spg_shift, p.spg_mul);
+             st.template issue<U>(src, vcode, min(tn + U, last));
              __builtin_amdgcn_sched_barrier(0);
            }()),
            ...);
         }(std::make_integer_sequence<int, PM>{});
       }
       if (__any((bad & 0xAAAAAAAAu) != 0u)) {
-        __amdgpu_buffer_rsrc_t shp[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          shp[i] = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
-                              static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
+        const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
+                                                      static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
+        uint32_t vc[NT], vs[NT];
+        lane_offsets(nl, kq, vc, vs);
         const int back = q.tb * SPL * 128;     // (steps count from the part's first in LDS)
-        layer_extra<SPL, NT>(cur, shp, vcode, vscale, q.tb, q.te, p.spg_shift, p.spg_mul, xr - back,
-                             sr - q.tb * SPL * 4, kq, acc);
+        layer_extra<SPL, NT>(cur, shp, vc, vs, q.tb, q.te, 1, p.groups, xr - back, sr - q.tb * SPL * 4, kq, acc);
       }
       if (kq == 0) {
         const int t = q.pair / p.topk;
@@ -757,18 +844,12 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   }
 }
 
-// Steps per group as a shift, or a reciprocal for the others (t < 2^16).
-void group_steps(int group, int spl, int* shift, uint32_t* mul) {
+Groups group_steps(int group, int spl) {
   const int spg = group / (128 * spl);
-  *shift = -1;
-  *mul = 0;
-  if ((spg & (spg - 1)) == 0) {
-    int s = 0;
-    while ((1 << s) < spg) ++s;
-    *shift = s;
-  } else {
-    *mul = static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint32_t>(spg) + 1);
-  }
+  if ((spg & (spg - 1)) != 0) return Groups{-1, static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint32_t>(spg) + 1)};
+  int s = 0;
+  while ((1 << s) < spg) ++s;
+  return Groups{s, 0u};
 }
 
 int layer_spl(int group) { return group % 256 == 0 ? 2 : 1; }
@@ -809,8 +890,8 @@ bool moe_layer_fused(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bi
                      int dn_group) {
   if (up_bits != 2 || dn_bits != 2) return false;
   if (T < 1 || T > kLayerMaxT || E > kLayerMaxE || topk > kRouterMaxTopk) return false;
-  if (H > 65536 || I > 65536) return false;                       // 32-bit tile offsets, LDS
-  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H)).total > kLayerLds) return false;
+  if (H > 65536 || I > 65536 || (I + 16) * (H / 4) >= (int64_t{1} << 32)) return false;   // 32-bit tile offsets
+  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H), 1).total > kLayerLds) return false;
   const int spl = layer_spl(dn_group);
   const int ks = layer_down_parts(static_cast<int>(T), topk, E, static_cast<int>(I), spl);
   return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks).total <= kLayerLds;
@@ -848,7 +929,7 @@ hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const 
   p.code_bytes = up.code_bytes;
   p.gpr = H / up.group;
   const int spl = layer_spl(up.group), dspl = layer_spl(dn.group);
-  group_steps(up.group, spl, &p.spg_shift, &p.spg_mul);
+  p.groups = group_steps(up.group, spl);
   const int nmacro = H / (spl * 128);
   p.ks = layer_up_parts(T, r.topk, r.E, I, nmacro, cus);
   p.down_spl = dspl;
@@ -862,12 +943,12 @@ hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const 
   const int teams = kLayerWaves / p.ks;
   const int64_t units = static_cast<int64_t>(std::min(r.E, T * r.topk)) * (I / 16);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
-  const int lds = layer_up_lds(T, r.topk, H).total;
-  const int mpw = (nmacro + p.ks - 1) / p.ks;
+  p.batch = 4;
+  while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch).total > kLayerLds) --p.batch;
+  const int lds = layer_up_lds(T, r.topk, H, p.batch).total;
   hipError_t e;
   if (spl == 2) {
-    // seven steps in flight, or four where a wave's part is short
-    e = mpw <= 4 ? launch_layer(k_layer_up<2, 4>, grid, lds, p, st) : launch_layer(k_layer_up<2, 7>, grid, lds, p, st);
+    e = launch_layer(k_layer_up<2, 4>, grid, lds, p, st);
   } else {
     e = launch_layer(k_layer_up<1, 8>, grid, lds, p, st);
   }
@@ -885,7 +966,7 @@ hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const 
   d.shapes = dn.shapes;
   d.code_bytes = dn.code_bytes;
   d.gpr = I / dn.group;
-  group_steps(dn.group, dspl, &d.spg_shift, &d.spg_mul);
+  d.groups = group_steps(dn.group, dspl);
   d.H = H;
   d.I = I;
   d.rows = std::min(32, std::max(4, (H + cus - 1) / cus));
@@ -898,8 +979,8 @@ hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const 
   const unsigned dgrid = static_cast<unsigned>((H + d.rows - 1) / d.rows);
   const int dlds = layer_down_lds(T, I, dspl, d.ks).total;
   if (dspl == 2) {
-    return nt == 2 ? launch_layer(k_layer_down<2, 6, 2>, dgrid, dlds, d, st)
-                   : launch_layer(k_layer_down<2, 6, 1>, dgrid, dlds, d, st);
+    return nt == 2 ? launch_layer(k_layer_down<2, 4, 2>, dgrid, dlds, d, st)
+                   : launch_layer(k_layer_down<2, 4, 1>, dgrid, dlds, d, st);
   }
   return nt == 2 ? launch_layer(k_layer_down<1, 8, 2>, dgrid, dlds, d, st)
                  : launch_layer(k_layer_down<1, 8, 1>, dgrid, dlds, d, st);

@@ -10,12 +10,11 @@
 // rounded keys: logits compare exactly as fp32 numbers, and biased keys are
 // only narrowed down in fp32 (candidates whose fp32 key lies within its error
 // bound of the cut) and then compared in fp64. What bounds a single token is
-// the chain of dependent steps, so the cut is found by counting: a bisection
-// over the ordered key bits, one ballot and one scalar population count per
-// register and probe, that stops as soon as at least topk and at most
-// topk + 16 keys lie above the probe. The candidates then take one
-// lane each: their fp64 keys are evaluated side by side, and each lane counts
-// the candidates ahead of its own.
+// the chain of dependent steps, so the cut is found by counting (ballots and
+// scalar population counts in a bisection over the ordered key bits), the
+// candidates above it take one lane each, their fp64 keys are evaluated side by
+// side, and each lane counts the candidates ahead of its own. All loads are issued
+// before the first value is used.
 #pragma once
 #include "common.h"
 
@@ -42,24 +41,45 @@ __device__ __forceinline__ float order_value(uint32_t o) {
   return __uint_as_float((o >> 31) ? (o ^ 0x80000000u) : ~o);
 }
 
-__device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+// Reductions over the 64 lanes that end in every lane, in a fixed order: within
+// each row of 16 lanes by DPP (quad swaps, half-row mirror, row mirror), then the
+// four rows' results by readlane.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
 }
-template <class F>
-__device__ __forceinline__ F wave_sum_f(F v) {
+template <class T, class Op>
+__device__ __forceinline__ T wave_reduce(T v, Op op) {
+  auto each_dword = [](T x, auto f) {
+    if constexpr (sizeof(T) == 4) {
+      return __builtin_bit_cast(T, f(__builtin_bit_cast(uint32_t, x)));
+    } else {
+      const uint64_t b = __builtin_bit_cast(uint64_t, x);
+      const uint64_t lo = f(static_cast<uint32_t>(b)), hi = f(static_cast<uint32_t>(b >> 32));
+      return __builtin_bit_cast(T, lo | (hi << 32));
+    }
+  };
+  v = op(v, each_dword(v, [](uint32_t x) { return dpp_move<0xB1>(x); }));    // quad_perm [1, 0, 3, 2]
+  v = op(v, each_dword(v, [](uint32_t x) { return dpp_move<0x4E>(x); }));    // quad_perm [2, 3, 0, 1]
+  v = op(v, each_dword(v, [](uint32_t x) { return dpp_move<0x141>(x); }));   // row_half_mirror
+  v = op(v, each_dword(v, [](uint32_t x) { return dpp_move<0x140>(x); }));   // row_mirror
+  T r[4];
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  for (int k = 0; k < 4; ++k)
+    r[k] = each_dword(v, [k](uint32_t x) {
+      return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 16 * k));
+    });
+  return op(op(r[0], r[1]), op(r[2], r[3]));
 }
 
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
 
-// Expert lane * per + i of token t, as fp32; experts that are never taken
-// (NaN or -inf logits, NaN or -inf biases) come back as -inf, +inf as FLT_MAX.
-__device__ __forceinline__ float router_logit(const RouterParams& p, int64_t t, int e) {
-  const int64_t at = t * p.E + e;
+// A logit or bias as the router reads it: experts that are never taken (NaN,
+// -inf) as -inf, +inf as FLT_MAX, -0 as +0.
+__device__ __forceinline__ float router_value(float v) {
+  return v > -__builtin_inff() ? fminf(v, 3.4028234663852886e38f) + 0.0f : -__builtin_inff();
+}
+__device__ __forceinline__ float router_logit(const RouterParams& p, int64_t at) {
   float l;
   if (p.dtype == 0) {
     l = static_cast<const float*>(p.logits)[at];
@@ -67,64 +87,84 @@ __device__ __forceinline__ float router_logit(const RouterParams& p, int64_t t, 
     const uint16_t h = static_cast<const uint16_t*>(p.logits)[at];
     l = p.dtype == 1 ? bf16_to_f32(h) : static_cast<float>(__builtin_bit_cast(_Float16, h));
   }
-  if (!(l > -__builtin_inff())) return -__builtin_inff();         // NaN, -inf
-  return fminf(l, 3.4028234663852886e38f) + 0.0f;                 // -0 as +0
-}
-__device__ __forceinline__ float router_bias(const RouterParams& p, int e) {
-  const float b = p.bias[e];
-  return b > -__builtin_inff() ? fminf(b, 3.4028234663852886e38f) : -__builtin_inff();   // NaN as -inf
+  return router_value(l);
 }
 
-// The router of token t on one wave, EPL experts per lane (E <= 64 EPL; lane l
-// holds the consecutive experts l per .. l per + per - 1, per = ceil(E / 64), so
-// that lower lanes hold lower indices). cand: 64 dwords of LDS of this wave.
-// Lane j < topk returns slot j: id (-1: no expert left) and weight. Every lane
-// of the wave has to call it.
-template <int EPL>
-__device__ __forceinline__ void wave_topk(const RouterParams& p, int64_t t, int lane, uint32_t* cand, int* id_out,
-                                          float* w_out) {
-  const int per = (p.E + 63) >> 6;
-  const int e0 = lane * per;
-  const int k = p.topk;
-  float l[EPL];
-  uint32_t key[EPL];                           // ordered key; 0: not there or never taken
+// The router of token t on one wave, EPL experts per lane (E <= 64 EPL; lane l,
+// register i: expert 64 i + l). cand: 64 dwords of LDS of this wave. out(slot, id,
+// weight) is called once for every slot 0 .. topk - 1, each by some lane (id -1: no
+// expert left). Every lane of the wave has to call it.
+template <int EPL, class Out>
+__device__ __forceinline__ void wave_topk(const RouterParams& p, int64_t t, int lane, uint32_t* cand, Out&& out) {
+  const int k = p.topk, E = p.E;
+  const int64_t row = t * E;
+  float l[EPL], b[EPL];
+  // every load first, indices clamped
+  if (p.dtype == 0) {
+    const float* src = static_cast<const float*>(p.logits) + row;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) l[i] = i < per && e0 + i < p.E ? router_logit(p, t, e0 + i) : -__builtin_inff();
+    for (int i = 0; i < EPL; ++i) l[i] = src[min(64 * i + lane, E - 1)];
+  } else {
+    const uint16_t* src = static_cast<const uint16_t*>(p.logits) + row;
+    uint16_t h[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) h[i] = src[min(64 * i + lane, E - 1)];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      l[i] = p.dtype == 1 ? bf16_to_f32(h[i]) : static_cast<float>(__builtin_bit_cast(_Float16, h[i]));
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) b[i] = p.bias[min(64 * i + lane, E - 1)];
+  }
   float lmax = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) lmax = fmaxf(lmax, l[i]);
-  lmax = wave_max_f(lmax);
-  // softmax denominators: in fp64 where biased keys are compared, else in fp32
-  double total64 = 0.0;
-  float total = 0.0f;
-  if (!p.sigmoid && lmax > -__builtin_inff()) {
-    if (p.bias) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i < per && l[i] > -__builtin_inff()) total64 += exp(static_cast<double>(l[i]) - static_cast<double>(lmax));
-      total64 = wave_sum_f(total64);
-      total = static_cast<float>(total64);
-    } else if (!p.renorm) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) total += l[i] > -__builtin_inff() ? expf(l[i] - lmax) : 0.0f;
-      total = wave_sum_f(total);
-    }
-  }
-  uint32_t kmax = 0u;
-#pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    float f = l[i];
-    if (p.bias && i < per && f > -__builtin_inff()) {
-      const float b = router_bias(p, e0 + i);
-      const float pr = p.sigmoid ? 1.0f / (1.0f + expf(-f)) : expf(f - lmax) / total;
-      if (b > -__builtin_inff()) {
-        f = pr + b;
-      } else {
-        f = l[i] = -__builtin_inff();
+    l[i] = 64 * i + lane < E ? router_value(l[i]) : -__builtin_inff();
+    lmax = fmaxf(lmax, l[i]);
+  }
+  // softmax denominators: in fp64 where biased keys are compared, else in fp32
+  double total64 = 1.0;
+  float total = 1.0f;
+  if (!p.sigmoid) {
+    lmax = wave_reduce(lmax, [](float x, float y) { return fmaxf(x, y); });
+    if (lmax > -__builtin_inff()) {
+      if (p.bias) {
+        total64 = 0.0;
+#pragma unroll 1
+        for (int i = 0; 64 * i < E; ++i) {     // (rolled: fp64 exponentials are long; re-read, not indexed registers)
+          const int e = 64 * i + lane;
+          const float v = e < E ? router_logit(p, row + e) : -__builtin_inff();
+          if (v > -__builtin_inff()) total64 += exp(static_cast<double>(v) - static_cast<double>(lmax));
+        }
+        total64 = wave_reduce(total64, [](double x, double y) { return x + y; });
+        total = static_cast<float>(total64);
+      } else if (!p.renorm) {
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) total += expf(l[i] - lmax);
+        total = wave_reduce(total, [](float x, float y) { return x + y; });
       }
     }
-    key[i] = f > -__builtin_inff() ? order_bits(f) : 0u;
-    kmax = key[i] > kmax ? key[i] : kmax;
+  }
+  uint32_t key[EPL];                           // ordered key; 0: not there or never taken
+  uint32_t kmax = 0u;
+  if (p.bias) {
+    const float rt = 1.0f / total;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float bi = router_value(b[i]);
+      const float ex = __expf(p.sigmoid ? -l[i] : l[i] - lmax);
+      const float f = (p.sigmoid ? __builtin_amdgcn_rcpf(1.0f + ex) : ex * rt) + bi;
+      key[i] = l[i] > -__builtin_inff() && bi > -__builtin_inff() ? order_bits(f) : 0u;
+      kmax = max(kmax, key[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      key[i] = l[i] > -__builtin_inff() ? order_bits(l[i]) : 0u;
+      kmax = max(kmax, key[i]);
+    }
   }
   auto count_ge = [&](uint32_t thr) {          // wave-uniform
     int n = 0;
@@ -132,160 +172,151 @@ __device__ __forceinline__ void wave_topk(const RouterParams& p, int64_t t, int 
     for (int i = 0; i < EPL; ++i) n += __popcll(__ballot(key[i] >= thr));
     return n;
   };
-  // An fp32 biased key is off by less than 2^-20 (1 + |key|): the score by a few
-  // of its ulps (<= 2^-21), the sum by half an ulp. Keys of the definition's top k
+  // An fp32 biased key is off by less than 2^-20 (1 + |key|): the score (hardware
+  // exponential and reciprocal, the argument's rounding: below 2^-20 of a score
+  // that is at most 1) and half an ulp of the sum. Keys of the definition's top k
   // lie at most two such errors below a cut that k fp32 keys reach.
   auto lower = [&](uint32_t cut) {
-    if (!p.bias) return cut;
     const float v = order_value(cut);
     const float m = v - 0x1p-18f * (1.0f + fabsf(v));
     return m > -__builtin_inff() ? order_bits(m) : 1u;
   };
-  const int live = count_ge(1u);
+  // The cut: first the k-th largest of the lanes' largest keys, found by bisection
+  // on one register (k lanes reach it, so at least k keys do, and few more where
+  // large keys are spread over the lanes); only where more than 64 keys reach it,
+  // a bisection that counts all keys.
   uint32_t cut = 1u;                           // every live key
-  int n = live;
+  int n = count_ge(1u);
   bool many = false;
-  const int limit = k + 16 < 64 ? k + 16 : 64;   // a probe costs about as much as ranking a few candidates
-  if (live > limit) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-      const uint32_t u = __shfl_xor(kmax, o, 64);
-      kmax = u > kmax ? u : kmax;
+  const int limit = k + 8 < 64 ? k + 8 : 64;
+  if (n > limit) {
+    uint32_t lo = 1u;
+    const uint32_t top = wave_reduce(kmax, [](uint32_t x, uint32_t y) { return max(x, y); }) + 1u;
+    uint32_t hi = top;
+    if (__popcll(__ballot(kmax != 0u)) >= k) {
+      lo = wave_reduce(kmax, [](uint32_t x, uint32_t y) { return min(x, y); });
+      lo = lo ? lo : 1u;
+      while (hi - lo > 1u) {
+        const uint32_t mid = lo + ((hi - lo) >> 1);
+        const int c = __popcll(__ballot(kmax >= mid));
+        if (c >= k) {
+          lo = mid;
+          if (c == k) break;
+        } else {
+          hi = mid;
+        }
+      }
+      n = count_ge(lo);
     }
-    // count(lo) >= k > count(hi) throughout; stop once the candidates fit the lanes
-    uint32_t lo = 1u, hi = kmax + 1u;
-    while (n > limit && hi - lo > 1u) {
+    cut = p.bias ? lower(lo) : lo;
+    if (p.bias) n = count_ge(cut);
+    hi = top;
+    // count(lo) >= k > count(hi) throughout
+    while (n > 64 && hi - lo > 1u) {
       const uint32_t mid = lo + ((hi - lo) >> 1);
       const int c = count_ge(mid);
       if (c >= k) {
         lo = mid;
-        cut = lower(lo);
+        cut = p.bias ? lower(lo) : lo;
         n = p.bias ? count_ge(cut) : c;
       } else {
         hi = mid;
       }
     }
     many = n > 64;                             // ties (or near ties of biased keys) at the cut
-    if (many && !p.bias) {
-      // more than 64 keys reach lo, the k-th key itself: the fewer than k above it,
-      // and the lowest indices at it up to 64
-      cut = lo;
-    }
   }
   int ec = -1;                                 // this lane's candidate
-  if (!many || !p.bias) {
-    // candidates by ascending index; of more than 64 (unbiased ties) those above
-    // the cut first
+  if (!many) {
     int base = 0;
-    const int above = many ? count_ge(cut + 1u) : 0;
-    int tie_base = above;
-    // positions count lane by lane, register by register: a candidate's place is
-    // the number of candidates in lower lanes, then in lower registers of its own
-    int mine = 0, mine_tie = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const bool in = many ? key[i] > cut : key[i] >= cut;
-      mine += in;
-      mine_tie += many && key[i] == cut;
-    }
-    // exclusive prefix over lanes
-    int pre = mine, pre_tie = mine_tie;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(pre, o), v = __shfl_up(pre_tie, o);
-      if (lane >= o) { pre += u; pre_tie += v; }
-    }
-    base = pre - mine;
-    tie_base += pre_tie - mine_tie;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const bool in = many ? key[i] > cut : key[i] >= cut;
-      if (in && key[i] != 0u) {
-        if (base < 64) cand[base] = static_cast<uint32_t>(e0 + i);
-        ++base;
-      } else if (many && key[i] == cut) {
-        if (tie_base < 64) cand[tie_base] = static_cast<uint32_t>(e0 + i);
-        ++tie_base;
-      }
+      const bool in = key[i] >= cut;
+      const uint64_t m = __ballot(in);
+      const int at = base + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32),
+                                                      __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), 0));
+      if (in) cand[at] = static_cast<uint32_t>(64 * i + lane);
+      base += __popcll(m);
     }
     wave_lds_order();
-    if (many) n = 64;
     if (lane < n) ec = static_cast<int>(cand[lane]);
-    wave_lds_order();
   } else {
-    // More than 64 biased keys within the fp32 error of the cut: k rounds of a
-    // wave-wide maximum over fp64 keys (rare, and slow).
+    // More than 64 keys tie at the cut (or lie within the fp32 error of it): k rounds
+    // of a wave-wide maximum over exact keys (rare, and slow).
     uint32_t taken = 0u;
-    n = k;                                     // live > 64 >= k
+    n = k;
+#pragma unroll 1
     for (int j = 0; j < k; ++j) {
       double best = -__builtin_inf();
       int be = INT32_MAX;
 #pragma unroll 1
-      for (int i = 0; i < EPL; ++i) {
-        const int e = e0 + i;
-        if (i >= per || e >= p.E || ((taken >> i) & 1u)) continue;
-        const float f = router_logit(p, t, e);
-        const float b = router_bias(p, e);
-        if (!(f > -__builtin_inff()) || !(b > -__builtin_inff())) continue;
-        const double pr = p.sigmoid ? sigmoid64(f)
-                                    : exp(static_cast<double>(f) - static_cast<double>(lmax)) / total64;
-        const double v = pr + static_cast<double>(b);
+      for (int i = 0; 64 * i < E; ++i) {
+        const int e = 64 * i + lane;
+        if (e >= E || ((taken >> i) & 1u)) continue;
+        const float f = router_logit(p, row + e);
+        if (!(f > -__builtin_inff())) continue;
+        double v = static_cast<double>(f);
+        if (p.bias) {
+          const float bi = router_value(p.bias[e]);
+          if (!(bi > -__builtin_inff())) continue;
+          v = (p.sigmoid ? sigmoid64(f) : exp(v - static_cast<double>(lmax)) / total64) + static_cast<double>(bi);
+        }
         if (v > best || be == INT32_MAX) { best = v; be = e; }
       }
       double wb = best;
       int we = be;
-#pragma unroll
+#pragma unroll 1
       for (int o = 32; o >= 1; o >>= 1) {
         const double v = __shfl_xor(wb, o, 64);
         const int e = __shfl_xor(we, o, 64);
         if (e != INT32_MAX && (we == INT32_MAX || v > wb || (v == wb && e < we))) { wb = v; we = e; }
       }
-      if (we == be && be != INT32_MAX) taken |= 1u << (be - e0);
+      if (we == be && be != INT32_MAX) taken |= 1u << (be >> 6);
       if (lane == j) ec = we;
     }
   }
-  // one candidate per lane: its logit, score and key
-  const float lc = ec >= 0 ? router_logit(p, t, ec) : -__builtin_inff();
+  // one candidate per lane: its score and key in fp64
   double pc = 0.0, kc = -__builtin_inf();
   if (ec >= 0) {
+    const float lc = router_logit(p, row + ec);
     if (p.sigmoid) {
       pc = sigmoid64(lc);
     } else {
       pc = exp(static_cast<double>(lc) - static_cast<double>(lmax));
       if (p.bias) {
         pc /= total64;
-      } else if (!p.renorm) {
-        pc /= static_cast<double>(total);
+      } else {
+        pc /= static_cast<double>(total);      // (one with renormalisation)
       }
     }
-    kc = p.bias ? pc + static_cast<double>(router_bias(p, ec)) : static_cast<double>(lc);
+    kc = p.bias ? pc + static_cast<double>(router_value(p.bias[ec])) : static_cast<double>(lc);
   }
-  // rank: candidates with a larger key, or an equal one at a lower index
-  int rank = 0;
-  for (int j = 0; j < n; ++j) {
-    const uint64_t kb = __builtin_bit_cast(uint64_t, kc);
-    const uint32_t klo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(kb)), j);
-    const uint32_t khi = __builtin_amdgcn_readlane(static_cast<int>(kb >> 32), j);
-    const double kj = __builtin_bit_cast(double, (static_cast<uint64_t>(khi) << 32) | klo);
-    const int ej = __builtin_amdgcn_readlane(ec, j);
-    rank += (kj > kc || (kj == kc && ej < ec)) ? 1 : 0;
+  // Rank: candidates with a larger key, or an equal one at a lower index. The
+  // candidates lie in index order (the rare path has them in rank order already).
+  // Keys are compared as ordered integers; lanes past n hold the smallest one.
+  int rank = many ? lane : 0;
+  if (!many) {
+    const uint64_t kb = __builtin_bit_cast(uint64_t, kc + 0.0);
+    const uint64_t ok = ec >= 0 ? kb ^ ((kb >> 63) ? ~uint64_t{0} : uint64_t{1} << 63) : 0u;
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += 8) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int j = j0 + u;                  // n <= 64: j stays below 64
+        const uint32_t jlo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(ok)), j);
+        const uint32_t jhi = __builtin_amdgcn_readlane(static_cast<int>(ok >> 32), j);
+        const uint64_t oj = (static_cast<uint64_t>(jhi) << 32) | jlo;
+        rank += (oj > ok || (oj == ok && j < lane)) ? 1 : 0;
+      }
+    }
   }
   const bool win = ec >= 0 && rank < k;
   double sum = 1.0;
   if (p.renorm) {
-    sum = wave_sum_f(win ? pc : 0.0);
+    sum = wave_reduce(win ? pc : 0.0, [](double x, double y) { return x + y; });
     if (!(sum > 0.0)) sum = 1.0;               // every taken score is zero: weights zero
   }
-  const float wc = static_cast<float>(pc / sum * static_cast<double>(p.scale));
-  // slot rank -> lane rank
-  const int taken_n = n < k ? n : k;
-  if (win) cand[rank] = static_cast<uint32_t>(lane);
-  wave_lds_order();
-  const int src = lane < taken_n ? static_cast<int>(cand[lane]) : lane;
-  const int id = __shfl(ec, src, 64);
-  const float w = __shfl(wc, src, 64);
-  *id_out = lane < taken_n ? id : -1;
-  *w_out = lane < taken_n ? w : 0.0f;
+  if (win) out(rank, ec, static_cast<float>(pc / sum * static_cast<double>(p.scale)));
+  if (lane >= n && lane < k) out(lane, -1, 0.0f);
   wave_lds_order();
 }
 
