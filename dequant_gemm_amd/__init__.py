@@ -29,6 +29,7 @@ __all__ = [
     "cubic_moe_mlp_a8_workspace_bytes", "cubic_moe_mlp_a8",
     "DTYPE_F32", "DTYPE_BF16", "DTYPE_F16",
     "cubic_moe_topk", "cubic_moe_layer_workspace_bytes", "cubic_moe_layer", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "Int8Weight", "cubic_gemm_w8a8", "cubic_linear_w8a8_workspace_bytes", "cubic_linear_w8a8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +43,7 @@ EXPORTED_SYMBOLS = [
     "cubic_gemm_a16_ex", "act_quant_int8_per_token_ex", "cubic_gemm_a8_ex", "cubic_moe_grouped_gemm_ex",
     "cubic_moe_grouped_gemm_a8", "cubic_moe_mlp_a8_workspace_bytes", "cubic_moe_mlp_a8",
     "cubic_moe_topk", "cubic_moe_layer_workspace_bytes", "cubic_moe_layer",
+    "cubic_gemm_w8a8", "cubic_linear_w8a8_workspace_bytes", "cubic_linear_w8a8",
 ]
 MODE_A16, MODE_A8 = 0, 1          # cubic_linear_mode results
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
@@ -57,6 +59,11 @@ class _CWeight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("shapes", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("bits", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class _CWeightI8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64)]
 
 
 class _CRouter(ctypes.Structure):
@@ -84,6 +91,7 @@ def load_library():
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     wp = ctypes.POINTER(_CWeight)
     rp = ctypes.POINTER(_CRouter)
+    ip = ctypes.POINTER(_CWeightI8)
     sigs = {
         "cubic_code_bytes": (sz, [i64, i64, i32]),
         "cubic_storage_bytes": (sz, [i64, i64, i32, i32]),
@@ -117,6 +125,9 @@ def load_library():
         "cubic_moe_topk": (i32, [rp, i64, vp, vp, vp]),
         "cubic_moe_layer_workspace_bytes": (sz, [i64, i32, i32, i64, i64]),
         "cubic_moe_layer": (i32, [vp, i64, rp, wp, wp, vp, i32, vp, vp, vp, sz, vp]),
+        "cubic_gemm_w8a8": (i32, [vp, vp, i64, ip, vp, vp, i32, vp]),
+        "cubic_linear_w8a8_workspace_bytes": (sz, [i64, i64]),
+        "cubic_linear_w8a8": (i32, [vp, i32, i64, ip, vp, vp, i32, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -574,3 +585,69 @@ def cubic_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate_up: CubicWeight,
     _check(_call(dev, load_library().cubic_moe_layer, _ptr(x), T, ctypes.byref(r), ctypes.byref(gu), ctypes.byref(dn),
                  _ptr(out), yd, _ptr(ids), _ptr(weights), _ptr(workspace), workspace.numel()), "cubic_moe_layer")
     return out, ids, weights
+
+
+@dataclass
+class Int8Weight:
+    """A dense int8 weight with one scale per output channel (act_quant_int8_per_token of its rows)."""
+    codes: torch.Tensor     # int8 [N][K]
+    scales: torch.Tensor    # float32 [N]
+
+    def c_struct(self) -> _CWeightI8:
+        _need(self.codes, torch.int8, "codes")
+        _need(self.scales, torch.float32, "scales")
+        if self.codes.dim() != 2 or self.scales.shape != self.codes.shape[:1]:
+            raise ValueError("Int8Weight: expected codes [N][K] and scales [N]")
+        return _CWeightI8(self.codes.data_ptr(), self.scales.data_ptr(), *self.codes.shape)
+
+
+def _w8a8_args(x: torch.Tensor, w: Int8Weight, bias, out, out_dtype, name: str):
+    yd = _out_dtype(out_dtype)
+    cw = w.c_struct()
+    if x.dim() != 2 or x.shape[1] != cw.K:
+        raise ValueError(f"{name}: expected [M][{cw.K}], got {tuple(x.shape)}")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.numel() != cw.N:
+            raise ValueError(f"bias: expected {cw.N} values, got {bias.numel()}")
+    out = _result(out, (x.shape[0], cw.N), out_dtype, x.device)
+    _on(x.device, codes=w.codes, scales=w.scales, bias=bias, out=out)
+    return cw, yd, out
+
+
+def cubic_gemm_w8a8(xq: torch.Tensor, x_scale: torch.Tensor, w: Int8Weight, bias: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, out_dtype=torch.float32) -> torch.Tensor:
+    """y[M][N] = (xq int8 [M][K] times the int8 weight, exact in int32) * w.scales[n] * x_scale[m]
+    (+ bias[n]); y fp32 or bf16."""
+    _need(xq, torch.int8, "xq")
+    _need(x_scale, torch.float32, "x_scale")
+    cw, yd, out = _w8a8_args(xq, w, bias, out, out_dtype, "xq")
+    M = xq.shape[0]
+    if x_scale.numel() != M:
+        raise ValueError(f"x_scale: expected {M} values, got {x_scale.numel()}")
+    _on(xq.device, x_scale=x_scale)
+    _check(_call(xq.device, load_library().cubic_gemm_w8a8, _ptr(xq), _ptr(x_scale), M, ctypes.byref(cw), _ptr(bias),
+                 _ptr(out), yd), "cubic_gemm_w8a8")
+    return out
+
+
+def cubic_linear_w8a8_workspace_bytes(M: int, K: int) -> int:
+    return int(load_library().cubic_linear_w8a8_workspace_bytes(M, K))
+
+
+def cubic_linear_w8a8(x: torch.Tensor, w: Int8Weight, bias: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      out_dtype=torch.float32) -> torch.Tensor:
+    """cubic_gemm_w8a8 of bf16 or fp16 rows x [M][K], quantised per row on the way."""
+    xd = _in_dtype(x, "x")
+    cw, yd, out = _w8a8_args(x, w, bias, out, out_dtype, "x")
+    M = x.shape[0]
+    if workspace is None:
+        n = cubic_linear_w8a8_workspace_bytes(M, cw.K)
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    else:
+        _need(workspace, torch.uint8, "workspace")
+        _on(x.device, workspace=workspace)
+    _check(_call(x.device, load_library().cubic_linear_w8a8, _ptr(x), xd, M, ctypes.byref(cw), _ptr(bias), _ptr(out),
+                 yd, _ptr(workspace), workspace.numel() if workspace is not None else 0), "cubic_linear_w8a8")
+    return out

@@ -768,3 +768,75 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
   return moe_mlp_impl(x_bf16, T, ids, weights, topk, gate_up0, down0, E, static_cast<float*>(y), ybf16, ws + L.mlp,
                       ws_bytes - L.mlp, stream);
 }
+
+namespace {
+constexpr int64_t kW8MaxK = 131064;          // K * 128 * 128 below 2^31
+
+int check_weight_i8(const cubic_weight_i8* w, int64_t M) {
+  if (!w) return CUBIC_ERR_NULL;
+  if (M < 0 || w->N < 0 || w->K <= 0 || w->K % 8 != 0 || w->K > kW8MaxK) return CUBIC_ERR_SHAPE;
+  if (M > INT32_MAX / 2 || w->N > INT32_MAX / 2) return CUBIC_ERR_SHAPE;
+  if (M > 0 && w->N > 0) {
+    if (!w->codes || !w->scales) return CUBIC_ERR_NULL;
+    if (!aligned16(w->codes) || !aligned16(w->scales)) return CUBIC_ERR_ALIGN;
+  }
+  return CUBIC_OK;
+}
+
+W8Params w8_params(const cubic_weight_i8* w, int64_t M, const float* bias, void* y, int y_dtype) {
+  W8Params p{};
+  p.w = w->codes;
+  p.ws = w->scales;
+  p.bias = bias;
+  p.M = M;
+  p.N = w->N;
+  p.K = w->K;
+  p.y = y;
+  p.ybf16 = y_dtype == CUBIC_DTYPE_BF16 ? 1 : 0;
+  return p;
+}
+}  // namespace
+
+CUBIC_API int cubic_gemm_w8a8(const int8_t* xq, const float* x_scale, int64_t M, const cubic_weight_i8* w,
+                              const float* bias, void* y, int y_dtype, cubic_stream_t stream) {
+  const int st = check_weight_i8(w, M);
+  if (st != CUBIC_OK) return st;
+  if (!dtype_out_ok(y_dtype)) return CUBIC_ERR_DTYPE;
+  if (M == 0 || w->N == 0) return CUBIC_OK;
+  if (!xq || !x_scale || !y) return CUBIC_ERR_NULL;
+  if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(bias) || !aligned16(y)) return CUBIC_ERR_ALIGN;
+  W8Params p = w8_params(w, M, bias, y, y_dtype);
+  p.xq = xq;
+  p.xs = x_scale;
+  return hip_status(launch_w8a8(p, static_cast<hipStream_t>(stream)));
+}
+
+CUBIC_API size_t cubic_linear_w8a8_workspace_bytes(int64_t M, int64_t K) {
+  if (M <= 0 || K <= 0 || w8a8_quantises(M, K)) return 0;
+  return align256(static_cast<size_t>(M) * K) + align256(static_cast<size_t>(M) * 4);
+}
+
+CUBIC_API int cubic_linear_w8a8(const void* x, int x_dtype, int64_t M, const cubic_weight_i8* w, const float* bias,
+                                void* y, int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream) {
+  const int st = check_weight_i8(w, M);
+  if (st != CUBIC_OK) return st;
+  if (!dtype_in_ok(x_dtype) || !dtype_out_ok(y_dtype)) return CUBIC_ERR_DTYPE;
+  if (M == 0 || w->N == 0) return CUBIC_OK;
+  if (!x || !y) return CUBIC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(bias) || !aligned16(y)) return CUBIC_ERR_ALIGN;
+  W8Params p = w8_params(w, M, bias, y, y_dtype);
+  const size_t need = cubic_linear_w8a8_workspace_bytes(M, w->K);
+  if (need == 0) {
+    p.x = static_cast<const uint16_t*>(x);
+    return hip_status(launch_w8a8_linear(p, x_dtype == CUBIC_DTYPE_F16, static_cast<hipStream_t>(stream)));
+  }
+  if (!workspace || ws_bytes < need) return CUBIC_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return CUBIC_ERR_ALIGN;
+  int8_t* xq = static_cast<int8_t*>(workspace);
+  float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(M) * w->K));
+  const int q = act_quant_int8_per_token_ex(x, x_dtype, M, w->K, xq, xs, stream);
+  if (q != CUBIC_OK) return q;
+  p.xq = xq;
+  p.xs = xs;
+  return hip_status(launch_w8a8(p, static_cast<hipStream_t>(stream)));
+}

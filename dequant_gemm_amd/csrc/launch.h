@@ -190,4 +190,20 @@ hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const 
                             const MoeLayerWeight& dn, int H, int I, const MoeLayerBuffers& b, int32_t* ids_user,
                             float* weights_user, void* y, int ybf16, hipStream_t st);
 
+// The int8 product of per-token activations and per-channel weights (w8a8.hip).
+struct W8Params {
+  const int8_t* xq;        // [M][K]
+  const float* xs;         // [M]
+  const uint16_t* x;       // bf16 or fp16 [M][K] (launch_w8a8_linear, instead of xq and xs)
+  const int8_t* w;         // [N][K]
+  const float* ws;         // [N]
+  const float* bias;       // [N] or NULL
+  int64_t M, N, K;
+  void* y;                 // [M][N] fp32, or bf16 when ybf16
+  int ybf16;
+};
+bool w8a8_quantises(int64_t M, int64_t K);   // launch_w8a8_linear takes these rows
+hipError_t launch_w8a8_linear(const W8Params& p, bool xf16, hipStream_t st);
+hipError_t launch_w8a8(const W8Params& p, hipStream_t st);
+
 }  // namespace cubic

@@ -401,6 +401,35 @@ int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_router* route
                     int32_t* topk_ids, float* topk_weights, void* workspace, size_t ws_bytes,
                     cubic_stream_t stream);
 
+/* Dense int8 weights with one scale per output channel (msModelSlim article, W8A8
+ * scheme of the shared experts and projections, which stay beside the Cubic-coded
+ * routed experts): codes int8 [N][K], scales fp32 [N], weight [n][k] = codes * scales[n].
+ * act_quant_int8_per_token over a bf16 or fp16 weight's rows produces this form. K a
+ * positive multiple of 8, at most 131064 (so that K * 128 * 128 stays below 2^31). */
+typedef struct cubic_weight_i8 {
+  const int8_t* codes;
+  const float* scales;
+  int64_t N, K;
+} cubic_weight_i8;
+
+/* y[m][n] = fp32(I) * w->scales[n] * x_scale[m] (+ bias[n]), I = sum_k xq[m][k] *
+ * w->codes[n][k] exactly in int32 (values down to -128 included), for xq int8 [M][K]
+ * and x_scale fp32 [M] of act_quant_int8_per_token. Rounding: I to fp32, the product
+ * with the weight's scale, then the product with x_scale (one fused multiply-add where
+ * a bias is given); the bf16 output rounds that once more. The result does not depend
+ * on timing. bias fp32 [N] or NULL; y [M][N] in y_dtype CUBIC_DTYPE_F32 or _BF16.
+ * M == 0 or N == 0 is a no-op. */
+int cubic_gemm_w8a8(const int8_t* xq, const float* x_scale, int64_t M, const cubic_weight_i8* w,
+                    const float* bias, void* y, int y_dtype, cubic_stream_t stream);
+/* The same product of bf16 or fp16 activations x [M][K], quantised on the way:
+ * bit for bit act_quant_int8_per_token(_ex) followed by cubic_gemm_w8a8. Up to four
+ * rows of K <= 8192 are quantised inside the product's kernel and need no workspace;
+ * others pass through the workspace (cubic_linear_w8a8_workspace_bytes: xq, then
+ * x_scale, each rounded up to 256 bytes). */
+size_t cubic_linear_w8a8_workspace_bytes(int64_t M, int64_t K);
+int cubic_linear_w8a8(const void* x, int x_dtype, int64_t M, const cubic_weight_i8* w, const float* bias,
+                      void* y, int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -62,7 +62,7 @@ __all__ = [
     "level_numerators", "levels", "dequant", "gemm_a16",
     "act_quant", "carrier_table", "carrier_codes", "gemm_a8", "moe_a16", "moe_a8",
     "format_levels", "dequant_f32", "encode", "bf16_rne", "silu_mul", "moe_mlp_hidden", "moe_mlp", "moe_mlp_a8",
-    "moe_topk", "moe_layer",
+    "moe_topk", "moe_layer", "gemm_w8a8",
     "FIT_CLIP_STEPS", "fit_is_monotone", "fit_shape_candidates", "f64_to_f16_bits", "fit_group_sse", "fit",
 ]
 
@@ -772,3 +772,10 @@ def moe_layer(x_bf16: np.ndarray, logits: np.ndarray, topk: int, score: str, gat
     (y float64 [T][H], ids, weights)."""
     ids, weights = moe_topk(logits, topk, score, bias, renormalize, scale)
     return moe_mlp(x_bf16, ids, weights, logits.shape[1], gate_up_weight, down_weight), ids, weights
+
+
+def gemm_w8a8(xq: np.ndarray, sx: np.ndarray, wq: np.ndarray, sw: np.ndarray, bias=None) -> np.ndarray:
+    """float64 y[m][n] = (sum_k xq[m][k] wq[n][k]) * sw[n] * sx[m] (+ bias[n]); the sum in integers."""
+    I = np.asarray(xq, dtype=np.int64) @ np.asarray(wq, dtype=np.int64).T
+    y = I.astype(np.float64) * np.asarray(sw, dtype=np.float64)[None, :] * np.asarray(sx, dtype=np.float64)[:, None]
+    return y if bias is None else y + np.asarray(bias, dtype=np.float64)[None, :]
