@@ -491,44 +491,59 @@ _SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID, SCORE_SOFTMAX: SC
 _DT_LOGITS = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
-def _on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+# The calls below are short on the device (a few microseconds), so their checks are kept short too: one
+# pass over each tensor, integers for pointers, and the raw handle of the current stream.
 
 
-def _call(device, f, *args):
-    """f(*args, the current stream of device) with that device current."""
-    if device.index == torch.cuda.current_device():
-        return f(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
-    with torch.cuda.device(device):
-        return f(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+def _arg(t: torch.Tensor, dtype, index: int, name: str) -> int:
+    """Address of a contiguous tensor of this dtype on device `index`."""
+    if t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+        _need(t, dtype, name)
+        raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
+    return t.data_ptr()
 
 
-def _result(out, shape, dtype, device, name="out"):
+def _first(t: torch.Tensor, name: str) -> int:
+    """Device index of the argument that the others follow."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: must be a device tensor")
+    return index
+
+
+def _call(index: int, f, *args) -> int:
+    """f(*args, current stream of device `index`), with that device current."""
+    if index == torch.cuda.current_device():
+        return f(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return f(*args, torch._C._cuda_getCurrentRawStream(index))
+
+
+def _result(out, shape, dtype, index: int, name="out"):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(out, dtype, name)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+        return torch.empty(shape, dtype=dtype, device=index)
+    _arg(out, dtype, index, name)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(out.shape)}")
     return out
 
 
-def _router(logits: torch.Tensor, topk: int, score, bias, renormalize: bool, scale: float) -> _CRouter:
-    if logits.dtype not in _DT_LOGITS:
-        raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
-    _need(logits, logits.dtype, "logits")
+def _router(logits: torch.Tensor, index: int, topk: int, score, bias, renormalize: bool, scale: float) -> _CRouter:
+    dtype = logits.dtype
+    if dtype not in _DT_LOGITS:
+        raise TypeError(f"logits: expected float32, bfloat16 or float16, got {dtype}")
+    address = _arg(logits, dtype, index, "logits")
     if logits.dim() != 2:
         raise ValueError("logits: expected [T][E]")
     if score not in _SCORES:
         raise ValueError(f"score: expected 'softmax' or 'sigmoid', got {score!r}")
     E = logits.shape[1]
+    at = None
     if bias is not None:
-        _need(bias, torch.float32, "bias")
+        at = _arg(bias, torch.float32, index, "bias")
         if bias.numel() != E:
             raise ValueError(f"bias: expected {E} values, got {bias.numel()}")
-    return _CRouter(logits.data_ptr(), bias.data_ptr() if bias is not None else None, _DT_LOGITS[logits.dtype], E,
-                    topk, _SCORES[score], 1 if renormalize else 0, scale)
+    return _CRouter(address, at, _DT_LOGITS[dtype], E, topk, _SCORES[score], 1 if renormalize else 0, scale)
 
 
 def cubic_moe_topk(logits: torch.Tensor, topk: int, score="softmax", bias: torch.Tensor | None = None,
@@ -537,18 +552,31 @@ def cubic_moe_topk(logits: torch.Tensor, topk: int, score="softmax", bias: torch
     """The router: logits [T][E] (fp32, bf16 or fp16) -> (ids int32 [T][topk], weights fp32 [T][topk]).
     Experts are taken by score + bias (ties to the lowest index) and weighted by their scores,
     renormalised over the taken ones and times scale; masked slots get id -1 and weight 0."""
-    r = _router(logits, topk, score, bias, renormalize, scale)
-    T, dev = logits.shape[0], logits.device
-    topk_ids = _result(topk_ids, (T, topk), torch.int32, dev, "topk_ids")
-    topk_weights = _result(topk_weights, (T, topk), torch.float32, dev, "topk_weights")
-    _on(dev, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights)
-    _check(_call(dev, load_library().cubic_moe_topk, ctypes.byref(r), T, _ptr(topk_ids), _ptr(topk_weights)),
-           "cubic_moe_topk")
+    if logits.dtype not in _DT_LOGITS:
+        raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
+    index = _first(logits, "logits")
+    r = _router(logits, index, topk, score, bias, renormalize, scale)
+    T = logits.shape[0]
+    topk_ids = _result(topk_ids, (T, topk), torch.int32, index, "topk_ids")
+    topk_weights = _result(topk_weights, (T, topk), torch.float32, index, "topk_weights")
+    _check(_call(index, load_library().cubic_moe_topk, ctypes.byref(r), T, topk_ids.data_ptr(),
+                 topk_weights.data_ptr()), "cubic_moe_topk")
     return topk_ids, topk_weights
 
 
 def cubic_moe_layer_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> int:
     return int(load_library().cubic_moe_layer_workspace_bytes(T, topk, E, H, I))
+
+
+def _expert_args(w: CubicWeight, E: int, index: int, name: str) -> _CWeight:
+    """The descriptor of E back-to-back experts, every buffer of at least their size."""
+    groups = w.N * (w.K // w.group) if w.group > 0 else 0
+    c = _CWeight(_arg(w.codes, torch.uint8, index, name), _arg(w.scales, torch.float32, index, name),
+                 _arg(w.shapes, torch.int16, index, name), w.N, w.K, w.bits, w.group)
+    if (w.codes.numel() < E * (w.N * w.K * w.bits // 8) or w.scales.numel() < E * groups
+            or w.shapes.numel() < 2 * E * groups):
+        raise ValueError(f"{name}: smaller than {E} experts of [{w.N}][{w.K}]")
+    return c
 
 
 def cubic_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate_up: CubicWeight, down: CubicWeight, E: int, topk: int,
@@ -558,32 +586,25 @@ def cubic_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate_up: CubicWeight,
     """The whole routed-expert layer: x bf16 [T][H] and router logits [T][E] ->
     (y [T][H] bf16 or fp32, ids int32 [T][topk], weights fp32 [T][topk]). Routing as in
     cubic_moe_topk, experts as in cubic_moe_mlp."""
-    _need(x, torch.bfloat16, "x")
     yd = _out_dtype(out_dtype)
-    r = _router(logits, topk, score, bias, renormalize, scale)
-    dev = x.device
-    if x.dim() != 2 or x.shape != (logits.shape[0], gate_up.K):
-        raise ValueError(f"x: expected [{logits.shape[0]}][{gate_up.K}], got {tuple(x.shape)}")
+    index = _first(x, "x")
+    xa = _arg(x, torch.bfloat16, index, "x")
+    r = _router(logits, index, topk, score, bias, renormalize, scale)
+    T, H = logits.shape[0], gate_up.K
+    if tuple(x.shape) != (T, H):
+        raise ValueError(f"x: expected [{T}][{H}], got {tuple(x.shape)}")
     if r.E != E:
         raise ValueError(f"logits: expected {E} experts, got {r.E}")
-    T, H = x.shape
-    gu, dn = gate_up.c_struct(), down.c_struct()
-    for name, w in (("gate_up", gate_up), ("down", down)):
-        groups = w.N * (w.K // w.group) if w.group > 0 else 0
-        if (w.codes.numel() < E * (w.N * w.K * w.bits // 8) or w.scales.numel() < E * groups
-                or w.shapes.numel() < 2 * E * groups):
-            raise ValueError(f"{name}: smaller than {E} experts of [{w.N}][{w.K}]")
-    out = _result(out, (T, H), out_dtype, dev)
-    ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    gu, dn = _expert_args(gate_up, E, index, "gate_up"), _expert_args(down, E, index, "down")
+    out = _result(out, (T, H), out_dtype, index)
+    ids = torch.empty((T, topk), dtype=torch.int32, device=index)
+    weights = torch.empty((T, topk), dtype=torch.float32, device=index)
     if workspace is None:
-        n = cubic_moe_layer_workspace_bytes(T, topk, E, gate_up.K, down.K)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-    else:
-        _need(workspace, torch.uint8, "workspace")
-    _on(dev, logits=logits, bias=bias, out=out, workspace=workspace, gate_up=gate_up.codes, down=down.codes)
-    _check(_call(dev, load_library().cubic_moe_layer, _ptr(x), T, ctypes.byref(r), ctypes.byref(gu), ctypes.byref(dn),
-                 _ptr(out), yd, _ptr(ids), _ptr(weights), _ptr(workspace), workspace.numel()), "cubic_moe_layer")
+        n = cubic_moe_layer_workspace_bytes(T, topk, E, H, down.K)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=index)
+    wa = _arg(workspace, torch.uint8, index, "workspace")
+    _check(_call(index, load_library().cubic_moe_layer, xa, T, ctypes.byref(r), ctypes.byref(gu), ctypes.byref(dn),
+                 out.data_ptr(), yd, ids.data_ptr(), weights.data_ptr(), wa, workspace.numel()), "cubic_moe_layer")
     return out, ids, weights
 
 
@@ -593,41 +614,37 @@ class Int8Weight:
     codes: torch.Tensor     # int8 [N][K]
     scales: torch.Tensor    # float32 [N]
 
-    def c_struct(self) -> _CWeightI8:
-        _need(self.codes, torch.int8, "codes")
-        _need(self.scales, torch.float32, "scales")
-        if self.codes.dim() != 2 or self.scales.shape != self.codes.shape[:1]:
-            raise ValueError("Int8Weight: expected codes [N][K] and scales [N]")
-        return _CWeightI8(self.codes.data_ptr(), self.scales.data_ptr(), *self.codes.shape)
 
-
-def _w8a8_args(x: torch.Tensor, w: Int8Weight, bias, out, out_dtype, name: str):
+def _w8a8_args(x: torch.Tensor, w: Int8Weight, bias, out, out_dtype, index: int, name: str):
+    """(descriptor, bias address, output code, output) after the checks that both calls share."""
     yd = _out_dtype(out_dtype)
-    cw = w.c_struct()
-    if x.dim() != 2 or x.shape[1] != cw.K:
-        raise ValueError(f"{name}: expected [M][{cw.K}], got {tuple(x.shape)}")
+    codes, scales = w.codes, w.scales
+    if codes.dim() != 2 or scales.shape != codes.shape[:1]:
+        raise ValueError("Int8Weight: expected codes [N][K] and scales [N]")
+    N, K = codes.shape
+    cw = _CWeightI8(_arg(codes, torch.int8, index, "codes"), _arg(scales, torch.float32, index, "scales"), N, K)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"{name}: expected [M][{K}], got {tuple(x.shape)}")
+    ba = None
     if bias is not None:
-        _need(bias, torch.float32, "bias")
-        if bias.numel() != cw.N:
-            raise ValueError(f"bias: expected {cw.N} values, got {bias.numel()}")
-    out = _result(out, (x.shape[0], cw.N), out_dtype, x.device)
-    _on(x.device, codes=w.codes, scales=w.scales, bias=bias, out=out)
-    return cw, yd, out
+        ba = _arg(bias, torch.float32, index, "bias")
+        if bias.numel() != N:
+            raise ValueError(f"bias: expected {N} values, got {bias.numel()}")
+    return cw, ba, yd, _result(out, (x.shape[0], N), out_dtype, index)
 
 
 def cubic_gemm_w8a8(xq: torch.Tensor, x_scale: torch.Tensor, w: Int8Weight, bias: torch.Tensor | None = None,
                     out: torch.Tensor | None = None, out_dtype=torch.float32) -> torch.Tensor:
     """y[M][N] = (xq int8 [M][K] times the int8 weight, exact in int32) * w.scales[n] * x_scale[m]
     (+ bias[n]); y fp32 or bf16."""
-    _need(xq, torch.int8, "xq")
-    _need(x_scale, torch.float32, "x_scale")
-    cw, yd, out = _w8a8_args(xq, w, bias, out, out_dtype, "xq")
+    index = _first(xq, "xq")
+    xa, sa = _arg(xq, torch.int8, index, "xq"), _arg(x_scale, torch.float32, index, "x_scale")
+    cw, ba, yd, out = _w8a8_args(xq, w, bias, out, out_dtype, index, "xq")
     M = xq.shape[0]
     if x_scale.numel() != M:
         raise ValueError(f"x_scale: expected {M} values, got {x_scale.numel()}")
-    _on(xq.device, x_scale=x_scale)
-    _check(_call(xq.device, load_library().cubic_gemm_w8a8, _ptr(xq), _ptr(x_scale), M, ctypes.byref(cw), _ptr(bias),
-                 _ptr(out), yd), "cubic_gemm_w8a8")
+    _check(_call(index, load_library().cubic_gemm_w8a8, xa, sa, M, ctypes.byref(cw), ba, out.data_ptr(), yd),
+           "cubic_gemm_w8a8")
     return out
 
 
@@ -639,15 +656,17 @@ def cubic_linear_w8a8(x: torch.Tensor, w: Int8Weight, bias: torch.Tensor | None 
                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                       out_dtype=torch.float32) -> torch.Tensor:
     """cubic_gemm_w8a8 of bf16 or fp16 rows x [M][K], quantised per row on the way."""
-    xd = _in_dtype(x, "x")
-    cw, yd, out = _w8a8_args(x, w, bias, out, out_dtype, "x")
+    if x.dtype not in _DT_IN:
+        raise TypeError(f"x: expected bfloat16 or float16, got {x.dtype}")
+    index = _first(x, "x")
+    xa = _arg(x, x.dtype, index, "x")
+    cw, ba, yd, out = _w8a8_args(x, w, bias, out, out_dtype, index, "x")
     M = x.shape[0]
+    lib = load_library()
     if workspace is None:
-        n = cubic_linear_w8a8_workspace_bytes(M, cw.K)
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-    else:
-        _need(workspace, torch.uint8, "workspace")
-        _on(x.device, workspace=workspace)
-    _check(_call(x.device, load_library().cubic_linear_w8a8, _ptr(x), xd, M, ctypes.byref(cw), _ptr(bias), _ptr(out),
-                 yd, _ptr(workspace), workspace.numel() if workspace is not None else 0), "cubic_linear_w8a8")
+        n = lib.cubic_linear_w8a8_workspace_bytes(M, cw.K)
+        workspace = torch.empty(n, dtype=torch.uint8, device=index) if n else None
+    wa, n = (None, 0) if workspace is None else (_arg(workspace, torch.uint8, index, "workspace"), workspace.numel())
+    _check(_call(index, lib.cubic_linear_w8a8, xa, _DT_IN[x.dtype], M, ctypes.byref(cw), ba, out.data_ptr(), yd, wa, n),
+           "cubic_linear_w8a8")
     return out

@@ -413,9 +413,9 @@ CUBIC_API size_t cubic_moe_mlp_workspace_bytes(int64_t T, int topk, int E, int64
 }
 
 namespace {
-// y: fp32, or bf16 when ybf16 is set.
+// y: fp32, or bf16 when ybf16 is set; split: levels of wider codes in two bf16 halves.
 int moe_mlp_impl(const uint16_t* x_bf16, int64_t T, const int32_t* topk_ids, const float* topk_weights, int topk,
-                 const cubic_weight* gate_up0, const cubic_weight* down0, int E, float* y, bool ybf16,
+                 const cubic_weight* gate_up0, const cubic_weight* down0, int E, float* y, bool ybf16, bool split,
                  void* workspace, size_t ws_bytes, cubic_stream_t stream) {
   int st = check_weight(gate_up0);
   if (st != CUBIC_OK) return st;
@@ -455,7 +455,7 @@ int moe_mlp_impl(const uint16_t* x_bf16, int64_t T, const int32_t* topk_ids, con
       topk_ids, topk_weights, static_cast<int>(T), E, topk, params(gate_up0, x_bf16, y1), gate_up0->bits,
       params(down0, h, y2), down0->bits, reinterpret_cast<int32_t*>(ws + L.route.hdr),
       reinterpret_cast<int32_t*>(ws + L.route.erec), reinterpret_cast<int32_t*>(ws + L.route.sorted), h, y,
-      ybf16, static_cast<hipStream_t>(stream));
+      ybf16, split, static_cast<hipStream_t>(stream));
   return hip_status(e);
 }
 }  // namespace
@@ -464,8 +464,8 @@ CUBIC_API int cubic_moe_mlp(const uint16_t* x_bf16, int64_t T, const int32_t* to
                             const float* topk_weights, int topk, const cubic_weight* gate_up0,
                             const cubic_weight* down0, int E, float* y, void* workspace, size_t ws_bytes,
                             cubic_stream_t stream) {
-  return moe_mlp_impl(x_bf16, T, topk_ids, topk_weights, topk, gate_up0, down0, E, y, false, workspace, ws_bytes,
-                      stream);
+  return moe_mlp_impl(x_bf16, T, topk_ids, topk_weights, topk, gate_up0, down0, E, y, false, false, workspace,
+                      ws_bytes, stream);
 }
 
 namespace {
@@ -765,7 +765,7 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
   if (topk_weights) weights = topk_weights;
   const hipError_t e = launch_moe_topk(moe_router(router), T, ids, weights, s);
   if (e != hipSuccess) return CUBIC_ERR_HIP;
-  return moe_mlp_impl(x_bf16, T, ids, weights, topk, gate_up0, down0, E, static_cast<float*>(y), ybf16, ws + L.mlp,
+  return moe_mlp_impl(x_bf16, T, ids, weights, topk, gate_up0, down0, E, static_cast<float*>(y), ybf16, true, ws + L.mlp,
                       ws_bytes - L.mlp, stream);
 }
 

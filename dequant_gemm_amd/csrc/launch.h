@@ -119,7 +119,8 @@ hipError_t launch_prefill_a8(const TiledParams& p, int bits, hipStream_t st);
 // LDS the grouped kernel needs with one activation row per pass.
 size_t moe_lds_min_bytes(int64_t K, int bits, int group);
 hipError_t launch_moe(const int32_t* ids, int T, int E, int topk, const MoeGemvParams& base,
-                      int32_t* hdr, int32_t* erec, int32_t* sorted, int bits, bool xf16, hipStream_t st);
+                      int32_t* hdr, int32_t* erec, int32_t* sorted, int bits, bool xf16, hipStream_t st,
+                      bool split = false);
 // The routing kernel alone: pair ids grouped by expert into hdr / erec / sorted,
 // output rows of invalid pairs cleared.
 hipError_t launch_moe_route(const int32_t* ids, int P, int E, int64_t N, float* y, int ybf16, int32_t* hdr,
@@ -158,7 +159,7 @@ hipError_t moe_scratch_address(void** out);
 hipError_t launch_moe_mlp(const int32_t* ids, const float* topk_w, int T, int E, int topk,
                           const MoeGemvParams& up, int up_bits, const MoeGemvParams& dn, int dn_bits,
                           int32_t* hdr, int32_t* erec, int32_t* sorted, uint16_t* h, float* out, bool obf16,
-                          hipStream_t st);
+                          bool split, hipStream_t st);
 
 // The router (moe_layer.hip): logits [T][E] in fp32 (dtype 0), bf16 (1) or fp16
 // (2), the selection's bias [E] or NULL.

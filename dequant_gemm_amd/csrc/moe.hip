@@ -607,6 +607,7 @@ static hipError_t launch_moe_stream_t(const MoeGemvParams& p, int64_t blocks, in
 size_t moe_lds_min_bytes(int64_t K, int bits, int group) {
   const int spl = (bits == 2 && group % 256 == 0) ? 2 : 1;
   const GemvGeom geo = gemv_geom(K, group, spl);
+  // (the largest table: 2^8 fp16 levels a row; 2^6 levels in two halves are smaller)
   return bits == 2 ? moe_lds_bytes<DecodeW2>(geo, 1) : moe_lds_bytes<DecodeTable<8>>(geo, 1);
 }
 
@@ -635,14 +636,31 @@ static hipError_t launch_moe_product_t(const MoeGemvParams& p, int64_t blocks, i
   }
 }
 
+// bf16 activations against levels of 16 significant bits (two bf16 halves, two
+// MFMAs a fragment): the whole-layer call's products for codes of three bits and
+// more. With fp16 levels (2^-12) about a tenth of the h values round to another bf16
+// number than the exact ones would, which alone puts y off by 1e-3; with these, 2e-4.
+// XF16 = true makes the staging copy the rows as they are (16-bit values).
+static hipError_t launch_moe_product_split(const MoeGemvParams& p, int64_t blocks, int T, int bits, hipStream_t st) {
+  switch (bits) {
+    case 3: return launch_moe_gemv_t<DecodeTableSplit<3>, 1, 6, true>(p, blocks, T, st);
+    case 4: return launch_moe_gemv_t<DecodeTableSplit<4>, 1, 4, true>(p, blocks, T, st);
+    case 5: return launch_moe_gemv_t<DecodeTableSplit<5>, 1, 2, true>(p, blocks, T, st);
+    case 6: return launch_moe_gemv_t<DecodeTableSplit<6>, 1, 2, true>(p, blocks, T, st);
+    case 7: return launch_moe_gemv_t<DecodeDirect<7, true>, 1, 2, true>(p, blocks, T, st);
+    default: return launch_moe_gemv_t<DecodeDirect<8, true>, 1, 2, true>(p, blocks, T, st);
+  }
+}
+
 // The grouped product over a routing already in hdr / erec / sorted (p holds
 // them): P pairs, activation row of pair q = q / p.topk, output row q.
 static hipError_t launch_moe_product(const MoeGemvParams& p, int P, int E, int T, int bits,
-                                     bool xf16, hipStream_t st) {
+                                     bool xf16, hipStream_t st, bool split = false) {
   const int64_t tiles = (p.N + 15) / 16;
   const int64_t blocks = static_cast<int64_t>(min(E, P)) * tiles;
   if (blocks == 0) return hipSuccess;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (split && bits > 2) return launch_moe_product_split(p, blocks, T, bits, st);
   return xf16 ? launch_moe_product_t<true>(p, blocks, T, bits, st)
               : launch_moe_product_t<false>(p, blocks, T, bits, st);
 }
@@ -673,7 +691,7 @@ static bool moe_set_direct(MoeGemvParams& p, const int32_t* ids, int T, int P, i
 }
 
 hipError_t launch_moe(const int32_t* ids, int T, int E, int topk, const MoeGemvParams& base,
-                      int32_t* hdr, int32_t* erec, int32_t* sorted, int bits, bool xf16, hipStream_t st) {
+                      int32_t* hdr, int32_t* erec, int32_t* sorted, int bits, bool xf16, hipStream_t st, bool split) {
   const int P = T * topk;
   MoeGemvParams p = base;
   p.topk = topk;
@@ -683,7 +701,7 @@ hipError_t launch_moe(const int32_t* ids, int T, int E, int topk, const MoeGemvP
   const hipError_t err = launch_moe_route(ids, P, E, base.N, base.y, base.ybf16, hdr, erec, sorted, st);
   if (err != hipSuccess) return err;
   p.hdr = hdr; p.erec = erec; p.sorted = sorted;
-  return launch_moe_product(p, P, E, T, bits, xf16, st);
+  return launch_moe_product(p, P, E, T, bits, xf16, st, split);
 }
 
 // ---------------------------------------------------------------------------
@@ -768,7 +786,7 @@ hipError_t launch_moe_combine(const float* y2, const int32_t* ids, const float* 
 hipError_t launch_moe_mlp(const int32_t* ids, const float* topk_w, int T, int E, int topk,
                           const MoeGemvParams& up, int up_bits, const MoeGemvParams& dn, int dn_bits,
                           int32_t* hdr, int32_t* erec, int32_t* sorted, uint16_t* h, float* out, bool obf16,
-                          hipStream_t st) {
+                          bool split, hipStream_t st) {
   const int P = T * topk;
   const int64_t I = dn.K, H = dn.N;
   MoeGemvParams p = dn;
@@ -780,7 +798,7 @@ hipError_t launch_moe_mlp(const int32_t* ids, const float* topk_w, int T, int E,
   const bool dn_direct = moe_set_direct(p, ids, T, P, E, dn_bits, hdr);
   hipError_t err;
   if (dn_direct) {
-    err = launch_moe(ids, T, E, topk, up, hdr, erec, sorted, up_bits, false, st);
+    err = launch_moe(ids, T, E, topk, up, hdr, erec, sorted, up_bits, false, st, split);
   } else {
     // the gate_up product must be routed too, so that the routing exists for down
     err = launch_moe_route(ids, P, E, up.N, up.y, up.ybf16, hdr, erec, sorted, st);
@@ -789,14 +807,14 @@ hipError_t launch_moe_mlp(const int32_t* ids, const float* topk_w, int T, int E,
       u.topk = topk;
       u.direct = 0;
       u.hdr = hdr; u.erec = erec; u.sorted = sorted;
-      err = launch_moe_product(u, P, E, T, up_bits, false, st);
+      err = launch_moe_product(u, P, E, T, up_bits, false, st, split);
     }
   }
   if (err != hipSuccess) return err;
   err = launch_moe_act(up.y, P, I, h, st);
   if (err != hipSuccess) return err;
   if (!dn_direct) { p.hdr = hdr; p.erec = erec; p.sorted = sorted; }
-  err = launch_moe_product(p, P, E, T, dn_bits, false, st);
+  err = launch_moe_product(p, P, E, T, dn_bits, false, st, split);
   if (err != hipSuccess) return err;
   return launch_moe_combine(dn.y, ids, topk_w, T, topk, E, H, out, obf16, st);
 }
