@@ -252,6 +252,13 @@ __global__ __launch_bounds__(1024) void k_w8a8_rows(RowsParams p) {
 // ---------------------------------------------------------------------------
 constexpr int kTileStages = 4;
 constexpr int tile_stage_bytes(int MB, int NB) { return 64 * (MB + NB) * 64; }
+// Passes of the epilogue over the tile's rows: what fits in the ring's LDS beside the
+// channels' scales and biases.
+constexpr int tile_passes(int MB, int NB, int bytes) {
+  int np = 1;
+  while (64 * MB / np * (64 * NB * bytes + 16) + 8 * 64 * NB > kTileStages * tile_stage_bytes(MB, NB)) np *= 2;
+  return np;
+}
 
 // vmcnt(n) (n < 64: low bits in [3:0], high bits in [15:14]) and lgkmcnt(0).
 constexpr int w8_wait_vm(int n) { return (n & 15) | (7 << 4) | (((n >> 4) & 3) << 14); }
@@ -260,6 +267,7 @@ template <int MB, int NB>
 __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int TM = 64 * MB, TN = 64 * NB, NL = MB + NB;
+  constexpr int kLoads1 = (NL + 1) / 2;        // loads of a stage issued in the half step after its buffer is free
   constexpr int kStage = tile_stage_bytes(MB, NB), kBOff = TM * 64;
   static_assert(2 * NL < 64, "vmcnt");
   const int tid = threadIdx.x, lane = tid & 63;
@@ -343,23 +351,24 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
   w8_lds_barrier();
   if (ragged && S == 1) fix(0);
 #pragma unroll
-  for (int i = 0; i < NL; ++i) issue(3, i);
+  for (int i = 0; i < kLoads1; ++i) issue(3, i);
   i32x4 fa[2][MB], fb[2][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
 #pragma unroll
   for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
 
-  // One half step: the MFMAs of fragments f, with the reads of the other half's (and,
-  // LOADS, the stage's refill) spread between them.
-  auto half = [&](auto f_c, int s_read, int ks, auto loads_c, int s_load) {
-    constexpr int f = decltype(f_c)::value;
-    constexpr bool loads = decltype(loads_c)::value;
+  // One half step: the MFMAs of fragments f (weights times activations, so that a
+  // lane's results are consecutive channels of one row), with the reads of the other
+  // half's fragments and loads l0 .. l1 - 1 of stage s_load spread between them: the
+  // address unit takes longer over a load than an MFMA lasts.
+  auto half = [&](auto f_c, int s_read, int ks, int s_load, auto l0_c, auto l1_c) {
+    constexpr int f = decltype(f_c)::value, l0 = decltype(l0_c)::value, l1 = decltype(l1_c)::value;
     constexpr int Q = MB * NB;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
-      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[f][i], fb[f][j], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[f][j], fa[f][i], acc[i][j], 0, 0, 0);
 #pragma unroll
       for (int r = q * NL / Q; r < (q + 1) * NL / Q; ++r) {
         if (r < MB) {
@@ -367,42 +376,106 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
         } else {
           fb[1 - f][r - MB] = read_b(s_read, ks, r - MB);
         }
-        if (loads) issue(s_load, r);
       }
+#pragma unroll
+      for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) issue(s_load, r);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using IL = std::integral_constant<int, kLoads1>;
+  using IN = std::integral_constant<int, NL>;
   for (int s = 0; s < S; ++s) {
-    half(std::integral_constant<int, 0>{}, s, 1, std::false_type{}, 0);
+    half(I0{}, s, 1, s + 3, IL{}, IN{});       // the rest of the refill begun a half step ago
     // stage s + 1 has landed once only stages s + 2 and s + 3 are on their way; this
     // wave's reads of stage s are done, so after the barrier its buffer is free
     __builtin_amdgcn_s_waitcnt(w8_wait_vm(2 * NL));
     w8_lds_barrier();
     if (ragged && s + 1 == S - 1) fix(s + 1);
-    half(std::integral_constant<int, 1>{}, s + 1, 0, std::true_type{}, s + 4);
+    half(I1{}, s + 1, 0, s + 4, I0{}, IL{});
   }
   __builtin_amdgcn_s_waitcnt(0);               // (zero fills past K still target the ring)
   __syncthreads();
 
-  // ---- epilogue: D row m = 8 (e / 4) + 4 h + e % 4 of block (i, j), column c ----
-  float* sxs = reinterpret_cast<float*>(smem);
-  for (int i = tid; i < TM; i += 256) sxs[i] = m0 + i < p.M ? p.xs[m0 + i] : 0.0f;
+  // ---- epilogue: D row n = 8 (e / 4) + 4 h + e % 4 of block (i, j), column m = c;
+  // through LDS, so that rows leave in whole 16-byte pieces ----
+  float* s_ws = reinterpret_cast<float*>(smem);
+  float* s_bias = s_ws + TN;
+  unsigned char* tile = smem + 8 * TN;
+  for (int i = tid; i < TN; i += 256) {
+    const bool on = n0 + i < p.N;
+    s_ws[i] = on ? p.ws[n0 + i] : 0.0f;
+    s_bias[i] = on && p.bias ? p.bias[n0 + i] : 0.0f;
+  }
+  float xs[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    const int64_t m = m0 + wm * 32 * MB + 32 * i + c;
+    xs[i] = p.xs[m < p.M ? m : p.M - 1];
+  }
   __syncthreads();
+  auto write_out = [&](auto bytes_c) {
+    constexpr int kBytes = decltype(bytes_c)::value;             // of a result
+    constexpr int NP = tile_passes(MB, NB, kBytes);
+    constexpr int BP = MB / NP, kRows = 64 * BP, kStride = TN * kBytes + 16;
+    constexpr int kPer = 16 / kBytes;                            // results of a piece
+    const bool whole = p.N % kPer == 0;                          // rows start on 16 bytes
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int64_t n = n0 + wn * 32 * NB + 32 * j + c;
-    if (n >= p.N) continue;
-    const float ws = p.ws[n];
-    const float bias = p.bias ? p.bias[n] : 0.0f;
+    for (int ip = 0; ip < NP; ++ip) {
+      if (ip) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+      for (int ib = 0; ib < BP; ++ib) {
+        const int i = ip * BP + ib;
+        unsigned char* row = tile + (wm * 32 * BP + 32 * ib + c) * kStride;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int ml = wm * 32 * MB + 32 * i + 8 * (e >> 2) + 4 * h + (e & 3);
-        if (m0 + ml < p.M)
-          store_out(static_cast<float*>(p.y), p.ybf16 != 0, (m0 + ml) * p.N + n,
-                    w8_result(acc[i][j][e], ws, sxs[ml], p.bias != nullptr, bias));
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int nl = wn * 32 * NB + 32 * j + 8 * g + 4 * h;
+            const f32x4 ws = *reinterpret_cast<const f32x4*>(s_ws + nl);
+            const f32x4 bs = *reinterpret_cast<const f32x4*>(s_bias + nl);
+            float v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = w8_result(acc[i][j][4 * g + r], ws[r], xs[i], p.bias != nullptr, bs[r]);
+            store_out4(reinterpret_cast<float*>(row), kBytes == 2, nl, v);
+          }
       }
+      __syncthreads();
+      const int cols = static_cast<int>(min(static_cast<int64_t>(TN), p.N - n0));
+      auto global_row = [&](int r) {
+        const int w = r / (32 * BP);
+        return m0 + w * 32 * MB + ip * 32 * BP + (r - w * 32 * BP);
+      };
+      unsigned char* y = static_cast<unsigned char*>(p.y);
+      if (whole) {
+        constexpr int kPieces = TN / kPer;
+        for (int idx = tid; idx < kRows * kPieces; idx += 256) {
+          const int r = idx / kPieces, q = idx - r * kPieces;
+          const int64_t m = global_row(r);
+          if (m < p.M && q * kPer < cols)
+            *reinterpret_cast<u32x4*>(y + (m * p.N + n0 + q * kPer) * kBytes) =
+                *reinterpret_cast<const u32x4*>(tile + r * kStride + 16 * q);
+        }
+      } else {
+        for (int idx = tid; idx < kRows * TN; idx += 256) {
+          const int r = idx / TN, q = idx - r * TN;
+          const int64_t m = global_row(r);
+          if (m < p.M && q < cols) {
+            if constexpr (kBytes == 2) {
+              reinterpret_cast<uint16_t*>(y)[m * p.N + n0 + q] = reinterpret_cast<const uint16_t*>(tile + r * kStride)[q];
+            } else {
+              reinterpret_cast<float*>(y)[m * p.N + n0 + q] = reinterpret_cast<const float*>(tile + r * kStride)[q];
+            }
+          }
+        }
+      }
+    }
+  };
+  if (p.ybf16) {
+    write_out(std::integral_constant<int, 2>{});
+  } else {
+    write_out(std::integral_constant<int, 4>{});
   }
 }
 
