@@ -250,26 +250,34 @@ __global__ __launch_bounds__(1024) void k_w8a8_rows(RowsParams p) {
 }
 
 // ---------------------------------------------------------------------------
-constexpr int kTileStages = 4;
-constexpr int tile_stage_bytes(int MB, int NB) { return 64 * (MB + NB) * 64; }
-// Passes of the epilogue over the tile's rows: what fits in the ring's LDS beside the
-// channels' scales and biases.
-constexpr int tile_passes(int MB, int NB, int bytes) {
-  int np = 1;
-  while (64 * MB / np * (64 * NB * bytes + 16) + 8 * 64 * NB > kTileStages * tile_stage_bytes(MB, NB)) np *= 2;
-  return np;
-}
+// A tile's shape: WM x WN waves with MB x NB blocks of 32 x 32 each.
+template <int MB_, int NB_, int WM_, int WN_>
+struct Tile {
+  static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN;
+  static constexpr int TM = 32 * MB * WM, TN = 32 * NB * WN;
+  static constexpr int kStage = 64 * (TM + TN);                  // 64 codes of every row
+  // 16-row pieces of a stage per wave (the last ones may be past the tile)
+  static constexpr int LA = (TM / 16 + W - 1) / W, LB = (TN / 16 + W - 1) / W, NL = LA + LB;
+  // The epilogue takes the tile's rows in NP passes of what fits its share of LDS.
+  static constexpr int kLdsTarget = W == 8 ? 144 * 1024 : 40 * 1024;
+  static constexpr int out_bytes(int np, int bytes) { return TM / np * (TN * bytes + 16) + 8 * TN; }
+  static constexpr int passes(int bytes) {
+    int np = 1;
+    while (np < MB && out_bytes(np, bytes) > kLdsTarget) np *= 2;
+    return np;
+  }
+  static constexpr int max3(int x, int y, int z) { return x > y ? (x > z ? x : z) : (y > z ? y : z); }
+  static constexpr int kLds = max3(2 * kStage, out_bytes(passes(2), 2), out_bytes(passes(4), 4));
+  static_assert(kLds <= 160 * 1024, "one compute unit's LDS");
+};
 
-// vmcnt(n) (n < 64: low bits in [3:0], high bits in [15:14]) and lgkmcnt(0).
-constexpr int w8_wait_vm(int n) { return (n & 15) | (7 << 4) | (((n >> 4) & 3) << 14); }
-
-template <int MB, int NB>
-__global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
+template <class Shape>
+__global__ __launch_bounds__(64 * Shape::W) void k_w8a8_tile(W8Params p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int TM = 64 * MB, TN = 64 * NB, NL = MB + NB;
-  constexpr int kLoads1 = (NL + 1) / 2;        // loads of a stage issued in the half step after its buffer is free
-  constexpr int kStage = tile_stage_bytes(MB, NB), kBOff = TM * 64;
-  static_assert(2 * NL < 64, "vmcnt");
+  constexpr int MB = Shape::MB, NB = Shape::NB, WN = Shape::WN, W = Shape::W, kThreads = 64 * W;
+  constexpr int TM = Shape::TM, TN = Shape::TN, LA = Shape::LA, NL = Shape::NL;
+  constexpr int kLoads1 = (NL + 1) / 2;        // pieces of a stage that move in the half step after the barrier
+  constexpr int kStage = Shape::kStage, kBOff = TM * 64;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
@@ -289,50 +297,60 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
   const int64_t m0 = static_cast<int64_t>(4 * grp + in % gm) * TM;
   const int64_t n0 = static_cast<int64_t>(in / gm) * TN;
 
-  // ---- stage loads: wave w fills rows 16 (MB w + i) .. + 15 of A, then of B; lane l
-  // loads the 16-byte slot l % 4 of row l / 4, which holds piece slot ^ (row / 4 % 4)
-  // (any 16 rows read at one piece hit all banks) ----
+  // ---- stage loads: wave w takes rows 16 (W i + w) .. + 15 of A, then of B; lane l
+  // loads the 16-byte piece l % 4 of row l / 4 (64 contiguous bytes a lane quad) into
+  // registers and writes it to slot piece ^ (row / 4 % 4) of the row (any 16 rows read
+  // at one piece hit all banks). Direct global-to-LDS loads in place of the registers
+  // keep the address unit busy twice as long (32 against 64 bytes a cycle): 192 us
+  // against the 160 below for 4096 x 6144 x 7168. ----
   const uint32_t abytes = static_cast<uint32_t>(min(static_cast<int64_t>(TM), p.M - m0)) * static_cast<uint32_t>(K);
   const uint32_t bbytes = static_cast<uint32_t>(min(static_cast<int64_t>(TN), p.N - n0)) * static_cast<uint32_t>(K);
   const __amdgpu_buffer_rsrc_t ars = w8_rsrc(p.xq + m0 * K, abytes);
   const __amdgpu_buffer_rsrc_t brs = w8_rsrc(p.w + n0 * K, bbytes);
-  const int piece = (lane & 3) ^ ((lane >> 4) & 3);
-  const uint32_t abase = static_cast<uint32_t>(16 * MB * wave + (lane >> 2)) * static_cast<uint32_t>(K) + 16u * piece;
-  const uint32_t bbase = static_cast<uint32_t>(16 * NB * wave + (lane >> 2)) * static_cast<uint32_t>(K) + 16u * piece;
+  const uint32_t lane_k = 16u * (lane & 3);
+  const uint32_t abase = static_cast<uint32_t>(16 * wave + (lane >> 2)) * static_cast<uint32_t>(K) + lane_k;
+  const uint32_t bbase = static_cast<uint32_t>(16 * wave + (lane >> 2)) * static_cast<uint32_t>(K) + lane_k;
+  const uint32_t slot = 64u * (lane >> 2) + 16u * ((lane & 3) ^ ((lane >> 4) & 3));
   const int S = (K + 63) >> 6;
-  auto issue = [&](int s, int i) {             // load i of stage s; past K nothing is read: zeros
-    unsigned char* st = smem + (s & (kTileStages - 1)) * kStage;
+  u32x4 gr[2][NL];                             // pieces on their way: stages of either parity
+  auto load = [&](auto set_c, int s, int i) {  // piece i of stage s; past K nothing is read: zeros
+    constexpr int set = decltype(set_c)::value;
     const uint32_t k = 64u * static_cast<uint32_t>(s);
-    const bool on = k + 16u * piece < static_cast<uint32_t>(K);
-    if (i < MB) {
-      const uint32_t off = on ? abase + k + 16u * i * static_cast<uint32_t>(K) : abytes;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ars, st + (MB * wave + i) * 1024, 16, off, 0, 0, 0);
+    const bool on = k + lane_k < static_cast<uint32_t>(K);
+    const int g = i < LA ? i : i - LA;         // pieces past the tile read nothing
+    if (i < LA) {
+      const uint32_t off = on && 16 * (W * g + wave) < TM ? abase + k + 16u * W * g * static_cast<uint32_t>(K) : abytes;
+      gr[set][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ars, off, 0, 0));
     } else {
-      const uint32_t off = on ? bbase + k + 16u * (i - MB) * static_cast<uint32_t>(K) : bbytes;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(brs, st + kBOff + (NB * wave + i - MB) * 1024, 16, off, 0, 0, 0);
+      const uint32_t off = on && 16 * (W * g + wave) < TN ? bbase + k + 16u * W * g * static_cast<uint32_t>(K) : bbytes;
+      gr[set][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(brs, off, 0, 0));
     }
   };
-  // K a multiple of 8, not of 16: the last piece's upper half belongs to the next row
-  // (zeros in A make it count nothing)
-  const bool ragged = (K & 15) != 0;
-  auto fix = [&](int s) {
-    if (tid < TM) {
-      const int q = ((K & 63) >> 4) ^ ((tid >> 2) & 3);
-      *reinterpret_cast<uint2*>(smem + (s & (kTileStages - 1)) * kStage + tid * 64 + q * 16 + 8) = make_uint2(0u, 0u);
+  auto store = [&](auto set_c, int s, int i) { // piece i of stage s into LDS
+    constexpr int set = decltype(set_c)::value;
+    unsigned char* st = smem + (s & 1) * kStage;
+    u32x4 v = gr[set][i];
+    const int g = i < LA ? i : i - LA;
+    if (i < LA) {
+      // K a multiple of 8, not of 16: the last piece's upper half belongs to the next
+      // row (zeros in A make it count nothing)
+      if (64u * static_cast<uint32_t>(s) + lane_k + 8u >= static_cast<uint32_t>(K)) { v.z = 0u; v.w = 0u; }
+      if (16 * (W * g + wave) < TM) *reinterpret_cast<u32x4*>(st + (W * g + wave) * 1024 + slot) = v;
+    } else {
+      if (16 * (W * g + wave) < TN) *reinterpret_cast<u32x4*>(st + kBOff + (W * g + wave) * 1024 + slot) = v;
     }
-    w8_lds_barrier();
   };
 
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   const uint32_t swz = (c >> 2) & 3;
   auto frag = [&](const unsigned char* st, int row, int ks) {
     return *reinterpret_cast<const i32x4*>(st + row * 64 + (((2 * ks + h) ^ swz) << 4));
   };
   auto read_a = [&](int s, int ks, int i) {
-    return frag(smem + (s & (kTileStages - 1)) * kStage, wm * 32 * MB + 32 * i + c, ks);
+    return frag(smem + (s & 1) * kStage, wm * 32 * MB + 32 * i + c, ks);
   };
   auto read_b = [&](int s, int ks, int j) {
-    return frag(smem + (s & (kTileStages - 1)) * kStage + kBOff, wn * 32 * NB + 32 * j + c, ks);
+    return frag(smem + (s & 1) * kStage + kBOff, wn * 32 * NB + 32 * j + c, ks);
   };
 
   i32x16 acc[MB][NB];
@@ -343,15 +361,25 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using IL = std::integral_constant<int, kLoads1>;
+  using IN = std::integral_constant<int, NL>;
 #pragma unroll
-  for (int s = 0; s < 3; ++s)
+  for (int i = 0; i < NL; ++i) load(I0{}, 0, i);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) issue(s, i);
-  __builtin_amdgcn_s_waitcnt(w8_wait_vm(2 * NL));
+  for (int i = 0; i < NL; ++i) load(I1{}, 1, i);
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    store(I0{}, 0, i);
+    load(I0{}, 2, i);
+  }
   w8_lds_barrier();
-  if (ragged && S == 1) fix(0);
 #pragma unroll
-  for (int i = 0; i < kLoads1; ++i) issue(3, i);
+  for (int i = 0; i < kLoads1; ++i) {
+    store(I1{}, 1, i);
+    load(I1{}, 3, i);
+  }
   i32x4 fa[2][MB], fb[2][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
@@ -359,10 +387,10 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
   for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
 
   // One half step: the MFMAs of fragments f (weights times activations, so that a
-  // lane's results are consecutive channels of one row), with the reads of the other
-  // half's fragments and loads l0 .. l1 - 1 of stage s_load spread between them: the
-  // address unit takes longer over a load than an MFMA lasts.
-  auto half = [&](auto f_c, int s_read, int ks, int s_load, auto l0_c, auto l1_c) {
+  // lane's results are consecutive channels of one row). Spread between them: the
+  // reads of the other half's fragments, and for pieces l0 .. l1 - 1 of stage s_st the
+  // write to LDS and the load of the piece two stages later into its registers.
+  auto half = [&](auto f_c, int s_read, int ks, auto set_c, int s_st, auto l0_c, auto l1_c) {
     constexpr int f = decltype(f_c)::value, l0 = decltype(l0_c)::value, l1 = decltype(l1_c)::value;
     constexpr int Q = MB * NB;
 #pragma unroll
@@ -370,7 +398,7 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
       const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
       acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[f][j], fa[f][i], acc[i][j], 0, 0, 0);
 #pragma unroll
-      for (int r = q * NL / Q; r < (q + 1) * NL / Q; ++r) {
+      for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
         if (r < MB) {
           fa[1 - f][r] = read_a(s_read, ks, r);
         } else {
@@ -378,24 +406,28 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
         }
       }
 #pragma unroll
-      for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) issue(s_load, r);
+      for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) {
+        store(set_c, s_st, r);
+        load(set_c, s_st + 2, r);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using IL = std::integral_constant<int, kLoads1>;
-  using IN = std::integral_constant<int, NL>;
-  for (int s = 0; s < S; ++s) {
-    half(I0{}, s, 1, s + 3, IL{}, IN{});       // the rest of the refill begun a half step ago
-    // stage s + 1 has landed once only stages s + 2 and s + 3 are on their way; this
-    // wave's reads of stage s are done, so after the barrier its buffer is free
-    __builtin_amdgcn_s_waitcnt(w8_wait_vm(2 * NL));
+  // Stage s: its second half's fragments are read beside the first half's MFMAs; then
+  // stage s + 1 is whole in LDS (its last pieces were written there) and every wave is
+  // done with stage s, so that after the barrier stage s + 1 is read and stage s + 2
+  // takes the place of s.
+  auto stage = [&](int s, auto next_c, auto after_c) {
+    half(I0{}, s, 1, next_c, s + 1, IL{}, IN{});
     w8_lds_barrier();
-    if (ragged && s + 1 == S - 1) fix(s + 1);
-    half(I1{}, s + 1, 0, s + 4, I0{}, IL{});
+    half(I1{}, s + 1, 0, after_c, s + 2, I0{}, IL{});
+  };
+  int s = 0;
+  for (; s + 1 < S; s += 2) {
+    stage(s, I1{}, I0{});
+    stage(s + 1, I0{}, I1{});
   }
-  __builtin_amdgcn_s_waitcnt(0);               // (zero fills past K still target the ring)
+  if (s < S) stage(s, I1{}, I0{});
   __syncthreads();
 
   // ---- epilogue: D row n = 8 (e / 4) + 4 h + e % 4 of block (i, j), column m = c;
@@ -403,7 +435,7 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
   float* s_ws = reinterpret_cast<float*>(smem);
   float* s_bias = s_ws + TN;
   unsigned char* tile = smem + 8 * TN;
-  for (int i = tid; i < TN; i += 256) {
+  for (int i = tid; i < TN; i += kThreads) {
     const bool on = n0 + i < p.N;
     s_ws[i] = on ? p.ws[n0 + i] : 0.0f;
     s_bias[i] = on && p.bias ? p.bias[n0 + i] : 0.0f;
@@ -417,8 +449,8 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
   __syncthreads();
   auto write_out = [&](auto bytes_c) {
     constexpr int kBytes = decltype(bytes_c)::value;             // of a result
-    constexpr int NP = tile_passes(MB, NB, kBytes);
-    constexpr int BP = MB / NP, kRows = 64 * BP, kStride = TN * kBytes + 16;
+    constexpr int NP = Shape::passes(kBytes);
+    constexpr int BP = MB / NP, kRows = TM / NP, kStride = TN * kBytes + 16;
     constexpr int kPer = 16 / kBytes;                            // results of a piece
     const bool whole = p.N % kPer == 0;                          // rows start on 16 bytes
 #pragma unroll
@@ -450,7 +482,7 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
       unsigned char* y = static_cast<unsigned char*>(p.y);
       if (whole) {
         constexpr int kPieces = TN / kPer;
-        for (int idx = tid; idx < kRows * kPieces; idx += 256) {
+        for (int idx = tid; idx < kRows * kPieces; idx += kThreads) {
           const int r = idx / kPieces, q = idx - r * kPieces;
           const int64_t m = global_row(r);
           if (m < p.M && q * kPer < cols)
@@ -458,7 +490,7 @@ __global__ __launch_bounds__(256) void k_w8a8_tile(W8Params p) {
                 *reinterpret_cast<const u32x4*>(tile + r * kStride + 16 * q);
         }
       } else {
-        for (int idx = tid; idx < kRows * TN; idx += 256) {
+        for (int idx = tid; idx < kRows * TN; idx += kThreads) {
           const int r = idx / TN, q = idx - r * TN;
           const int64_t m = global_row(r);
           if (m < p.M && q < cols) {
@@ -515,17 +547,15 @@ hipError_t launch_rows(const W8Params& q, hipStream_t st) {
   }
 }
 
-template <int MB, int NB>
+template <class Shape>
 hipError_t launch_tile(const W8Params& p, hipStream_t st) {
-  auto kern = k_w8a8_tile<MB, NB>;
-  constexpr int lds = kTileStages * tile_stage_bytes(MB, NB);
-  static_assert(lds <= 160 * 1024, "one compute unit's LDS");
+  auto kern = k_w8a8_tile<Shape>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, Shape::kLds);
   if (e != hipSuccess) return e;
-  const int64_t tiles = ((p.M + 64 * MB - 1) / (64 * MB)) * ((p.N + 64 * NB - 1) / (64 * NB));
+  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + Shape::TN - 1) / Shape::TN);
   if (tiles > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(256), lds, st, p);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(64 * Shape::W), Shape::kLds, st, p);
   return hipGetLastError();
 }
 
@@ -545,25 +575,25 @@ hipError_t launch_w8a8(const W8Params& p, hipStream_t st) {
   // The tile with the least time by a simple model: waves of workgroups over the
   // compute units times the larger of a stage's MFMA and LDS-fill cycles.
   const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256;
-  static constexpr int kTiles[][2] = {{4, 4}, {4, 3}, {4, 2}, {2, 4}, {2, 2}, {2, 1}, {1, 2}, {1, 1}};
+  static constexpr int kTiles[][2] = {{256, 256}, {256, 192}, {256, 128}, {128, 256}, {128, 128}, {128, 64}, {64, 128}, {64, 64}};
   int best = 0;
   int64_t cost = INT64_MAX;
   for (int k = 0; k < 8; ++k) {
-    const int mb = kTiles[k][0], nb = kTiles[k][1];
-    const int64_t tiles = ((p.M + 64 * mb - 1) / (64 * mb)) * ((p.N + 64 * nb - 1) / (64 * nb));
-    const int64_t per = std::max(64 * mb * nb, 64 * (mb + nb)) + 64;   // a stage of 64 codes, and its barrier
+    const int tm = kTiles[k][0], tn = kTiles[k][1];
+    const int64_t tiles = ((p.M + tm - 1) / tm) * ((p.N + tn - 1) / tn);
+    const int64_t per = std::max(tm * tn / 64, tm + tn) + 64;   // a stage of 64 codes, and its barrier
     const int64_t c = (tiles + cu - 1) / cu * per;
     if (c < cost) { cost = c; best = k; }
   }
   switch (best) {
-    case 0: return launch_tile<4, 4>(p, st);
-    case 1: return launch_tile<4, 3>(p, st);
-    case 2: return launch_tile<4, 2>(p, st);
-    case 3: return launch_tile<2, 4>(p, st);
-    case 4: return launch_tile<2, 2>(p, st);
-    case 5: return launch_tile<2, 1>(p, st);
-    case 6: return launch_tile<1, 2>(p, st);
-    default: return launch_tile<1, 1>(p, st);
+    case 0: return launch_tile<Tile<2, 4, 4, 2>>(p, st);
+    case 1: return launch_tile<Tile<2, 3, 4, 2>>(p, st);
+    case 2: return launch_tile<Tile<2, 2, 4, 2>>(p, st);
+    case 3: return launch_tile<Tile<2, 2, 2, 4>>(p, st);
+    case 4: return launch_tile<Tile<2, 2, 2, 2>>(p, st);
+    case 5: return launch_tile<Tile<2, 1, 2, 2>>(p, st);
+    case 6: return launch_tile<Tile<1, 2, 2, 2>>(p, st);
+    default: return launch_tile<Tile<1, 1, 2, 2>>(p, st);
   }
 }
 
