@@ -18,6 +18,8 @@
 // split bf16 levels (hi + lo, two MFMAs per fragment; DecodeTableSplit), again
 // one kernel. 5 <= M <= 16, 2-bit codes: k_xprep reorders x once into the
 // decoder's slot order.
+#include <mutex>
+
 #include "gemv_core.h"
 #include "launch.h"
 
@@ -233,6 +235,32 @@ static hipError_t launch_gemv_t(const GemvParams& p, hipStream_t st) {
   const unsigned grid = static_cast<unsigned>((p.N + q.rows - 1) / q.rows);
   hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * W), lds, st, q);
   return hipGetLastError();
+}
+
+hipError_t allow_lds(const void* kernel, int bytes) {
+  struct Entry {
+    const void* kernel;
+    int dev, bytes;
+  };
+  static std::mutex mutex;
+  static Entry table[128];                     // more kernels than that: the runtime is asked every time
+  static int used = 0;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  Entry* have = nullptr;
+  for (int i = 0; i < used && !have; ++i)
+    if (table[i].kernel == kernel && table[i].dev == dev) have = &table[i];
+  if (have && bytes <= have->bytes) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  if (!have && used < 128) {
+    table[used] = Entry{kernel, dev, 0};
+    have = &table[used++];
+  }
+  if (have) have->bytes = bytes;
+  return hipSuccess;
 }
 
 int device_cu_count() {

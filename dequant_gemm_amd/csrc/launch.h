@@ -84,6 +84,10 @@ struct MoeA8Params {
 };
 
 int device_cu_count();   // compute units of the current device (0 if unknown)
+// Lets a kernel use `bytes` of dynamic LDS on the current device. The runtime keeps the
+// setting, so a kernel's largest one so far is remembered per device and the runtime is
+// asked only for more.
+hipError_t allow_lds(const void* kernel, int bytes);
 hipError_t launch_pack(const int8_t* codes, uint8_t* packed, int64_t N, int64_t K, int bits,
                        hipStream_t st, unsigned int* range_error);
 hipError_t launch_unpack(const uint8_t* packed, int8_t* codes, int64_t N, int64_t K, int bits,

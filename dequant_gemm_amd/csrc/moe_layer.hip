@@ -39,7 +39,7 @@ namespace {
 constexpr uint32_t kRsrc3 = 0x00020000u;       // raw buffer, 32-bit data format
 constexpr int kLayerWaves = 16;                // one workgroup of 1024 threads per compute unit
 constexpr int kLayerMaxT = 8;                  // hi and lo rows of eight tokens fill the MFMA's 16 rows
-constexpr int kLayerMaxE = 1024;               // experts of one router wave (16 per lane)
+constexpr int kLayerMaxE = 1024;               // experts of one router wave (4 or 16 per lane)
 constexpr int kLayerMaxPairs = kLayerMaxT * kRouterMaxTopk;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t layer_rsrc(const void* p, uint32_t bytes) {
@@ -341,7 +341,7 @@ __host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int b
   return L;
 }
 
-template <int SPL, int PM>
+template <int SPL, int PM, int EPL>
 __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   using Stream = CodeStream<SPL, PM, 2>;
@@ -359,11 +359,14 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
 
   // ---- the tokens' routers (one wave each), and x split into its halves ----
   if (wave < T) {
-    wave_topk<kLayerMaxE / 64>(p.r, wave, lane, reinterpret_cast<uint32_t*>(smem + L.cand) + 64 * wave,
+    // everything after waits for these waves
+    __builtin_amdgcn_s_setprio(3);
+    wave_topk<EPL>(p.r, wave, lane, reinterpret_cast<uint32_t*>(smem + L.cand) + 64 * wave,
                                [&](int slot, int id, float w) {
                                  s_id[wave * topk + slot] = id;
                                  s_w[wave * topk + slot] = w;
                                });
+    __builtin_amdgcn_s_setprio(0);
   }
   for (int e = tid; e < p.r.E; e += 1024) s_first[e] = INT32_MAX;
   for (int i = tid; i < 2 * P; i += 1024) reinterpret_cast<uint32_t*>(s_slot)[i] = 0xffffffffu;
@@ -902,8 +905,7 @@ namespace {
 template <class Kern, class Par>
 hipError_t launch_layer(Kern kern, unsigned grid, int lds, const Par& p, hipStream_t st) {
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), lds);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(kern, dim3(grid), dim3(1024), static_cast<size_t>(lds), st, p);
@@ -947,10 +949,11 @@ hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const 
   while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch).total > kLayerLds) --p.batch;
   const int lds = layer_up_lds(T, r.topk, H, p.batch).total;
   hipError_t e;
+  const bool few = r.E <= 256;                 // a router wave with 4 experts a lane, or 16
   if (spl == 2) {
-    e = launch_layer(k_layer_up<2, 4>, grid, lds, p, st);
+    e = few ? launch_layer(k_layer_up<2, 4, 4>, grid, lds, p, st) : launch_layer(k_layer_up<2, 4, 16>, grid, lds, p, st);
   } else {
-    e = launch_layer(k_layer_up<1, 8>, grid, lds, p, st);
+    e = few ? launch_layer(k_layer_up<1, 8, 4>, grid, lds, p, st) : launch_layer(k_layer_up<1, 8, 16>, grid, lds, p, st);
   }
   if (e != hipSuccess) return e;
 

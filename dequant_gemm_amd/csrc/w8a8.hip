@@ -518,8 +518,7 @@ hipError_t launch_rows_k(const RowsParams& p, unsigned grid, hipStream_t st) {
   const int red = kRowsWaves * NT * 16 * MT * 16 * 4;
   const int x = QUANT ? nsteps * 256 : 131072;
   const int lds = std::max(red, x);
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(grid), dim3(1024), lds, st, p);
   return hipGetLastError();
@@ -550,8 +549,7 @@ hipError_t launch_rows(const W8Params& q, hipStream_t st) {
 template <class Shape>
 hipError_t launch_tile(const W8Params& p, hipStream_t st) {
   auto kern = k_w8a8_tile<Shape>;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, Shape::kLds);
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
   if (e != hipSuccess) return e;
   const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + Shape::TN - 1) / Shape::TN);
   if (tiles > 0x7fffffff) return hipErrorInvalidValue;
