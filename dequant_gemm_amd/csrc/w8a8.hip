@@ -216,7 +216,8 @@ __global__ __launch_bounds__(1024) void k_w8a8_rows(RowsParams p) {
     }(std::make_integer_sequence<int, PM>{});
   }
 
-  // ---- the waves' sums meet in LDS: [wave][tile][16 MT rows][16] ----
+  // ---- the waves' sums meet in LDS: [wave][tile][MT][register][lane], the order in
+  // which a wave writes 64 neighbouring words ----
   w8_lds_barrier();                            // the activations are read
   int* red = reinterpret_cast<int*>(smem);
   constexpr int kTile = 16 * MT * 16;
@@ -227,16 +228,17 @@ __global__ __launch_bounds__(1024) void k_w8a8_rows(RowsParams p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int m = 16 * a + 4 * kq + r;
-        if (m < M) red[(wave * NT + t) * kTile + m * 16 + nl] = acc[a][t][r];
+        if (m < M) red[(wave * NT + t) * kTile + 256 * a + 64 * r + lane] = acc[a][t][r];
       }
   w8_lds_barrier();
   for (int idx = tid; idx < M * 32; idx += 1024) {
     const int m = idx >> 5, j = idx & 31;
     const int t = NT == 1 ? 0 : (j >= p.rt ? 1 : 0), col = j - t * p.rt;
     if (j >= rows || col >= p.rt) continue;
+    const int at = 256 * (m >> 4) + 64 * (m & 3) + 16 * ((m >> 2) & 3) + col;
     int sum = 0;
 #pragma unroll
-    for (int k = 0; k < kRowsWaves; ++k) sum += red[(k * NT + t) * kTile + m * 16 + col];
+    for (int k = 0; k < kRowsWaves; ++k) sum += red[(k * NT + t) * kTile + at];
     const int64_t n = n0 + j;
     float xs;
     if constexpr (QUANT) {
