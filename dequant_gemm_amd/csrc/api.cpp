@@ -737,7 +737,9 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
   const int E = router->E, topk = router->topk;
   if (gate_up0->N != 2 * I || down0->N != H || H == 0 || I == 0) return CUBIC_ERR_SHAPE;
   if (T == 0) return CUBIC_OK;
-  const bool fused = moe_layer_fused(T, topk, E, H, I, gate_up0->bits, gate_up0->group, down0->bits, down0->group);
+  const int64_t run =
+      moe_layer_tokens(T, topk, E, H, I, gate_up0->bits, gate_up0->group, down0->bits, down0->group);
+  const bool fused = run > 0;
   if (!fused && ((st = moe_weight_fits(gate_up0)) != CUBIC_OK || (st = moe_weight_fits(down0)) != CUBIC_OK)) return st;
   if (!x_bf16 || !y || !workspace) return CUBIC_ERR_NULL;
   if (!aligned16(x_bf16) || !aligned16(y) || !aligned16(workspace) || !aligned16(topk_ids) || !aligned16(topk_weights))
@@ -756,8 +758,8 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
     };
     const MoeLayerBuffers b{ids, weights, reinterpret_cast<int32_t*>(ws + L.rec),
                             reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<uint8_t*>(ws + L.hs)};
-    return hip_status(launch_moe_layer(moe_router(router), x_bf16, static_cast<int>(T), weight(gate_up0), weight(down0),
-                                       static_cast<int>(H), static_cast<int>(I), b, topk_ids, topk_weights, y,
+    return hip_status(launch_moe_layer(moe_router(router), x_bf16, static_cast<int>(T), static_cast<int>(run), weight(gate_up0),
+                                       weight(down0), static_cast<int>(H), static_cast<int>(I), b, topk_ids, topk_weights, y,
                                        ybf16 ? 1 : 0, s));
   }
   // the caller's arrays hold the routing where given

@@ -189,9 +189,10 @@ struct MoeLayerBuffers {
   uint8_t* hq;             // [T*topk][2][I]
   uint8_t* hs;             // [T*topk][2][I / 32]
 };
-bool moe_layer_fused(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
-                     int dn_group);
-hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, const MoeLayerWeight& up,
+// Tokens that one run of the two kernels takes (0: not on this path).
+int64_t moe_layer_tokens(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
+                         int dn_group);
+hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, int run, const MoeLayerWeight& up,
                             const MoeLayerWeight& dn, int H, int I, const MoeLayerBuffers& b, int32_t* ids_user,
                             float* weights_user, void* y, int ybf16, hipStream_t st);
 

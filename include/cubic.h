@@ -385,7 +385,8 @@ int cubic_moe_topk(const cubic_router* router, int64_t T, int32_t* topk_ids, flo
  * A token whose experts are all masked out gets a zero row. For 2-bit weights and
  * up to eight tokens (E <= 1024, and activations that fit a compute unit's LDS)
  * the layer runs in two kernels, which read each touched expert's codes from HBM
- * once; otherwise the router kernel and the MLP step run one after the other, with
+ * once, and for up to 32 tokens (weights of 4 MB and more) in such runs of up to
+ * eight; otherwise the router kernel and the MLP step run one after the other, with
  * the limits of cubic_moe_mlp. In the two kernels the activations are multiplied
  * exactly unless they lie below 2^-14 of the largest of their 32 neighbours (then
  * off by up to 2^-22 of that), and a token with a non-finite activation has NaN
