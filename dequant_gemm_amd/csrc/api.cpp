@@ -754,7 +754,7 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
   if (fused) {
     auto weight = [](const cubic_weight* w) {
       return MoeLayerWeight{w->codes, w->scales, w->shapes,
-                            static_cast<int64_t>(cubic_code_bytes(w->N, w->K, w->bits)), w->group};
+                            static_cast<int64_t>(cubic_code_bytes(w->N, w->K, w->bits)), w->bits, w->group};
     };
     const MoeLayerBuffers b{ids, weights, reinterpret_cast<int32_t*>(ws + L.rec),
                             reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<uint8_t*>(ws + L.hs)};

@@ -180,7 +180,7 @@ struct MoeLayerWeight {
   const float* scales;
   const uint16_t* shapes;
   int64_t code_bytes;      // per expert
-  int group;
+  int bits, group;
 };
 struct MoeLayerBuffers {
   int32_t* ids;            // [T*topk]

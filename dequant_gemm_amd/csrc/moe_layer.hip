@@ -25,11 +25,12 @@
 // (pair, K part) per wave at a time, so the router-weighted sum never leaves the
 // workgroup: no atomics, and the order of the sums does not depend on timing.
 //
-// Other code widths, more tokens and shapes beyond the kernels' LDS run as the
-// router kernel followed by the routed MLP step (moe.hip).
+// 3- and 4-bit codes run on the same two kernels with table levels (CodesWide); wider
+// codes, more tokens and shapes beyond the kernels' LDS run as the router kernel
+// followed by the routed MLP step (moe.hip).
 #include <algorithm>
 
-#include "common.h"
+#include "gemv_core.h"
 #include "launch.h"
 #include "router.h"
 
@@ -95,6 +96,27 @@ __device__ __forceinline__ int chunk_place(int b) {
   return SPL == 2 ? (b & ~7) + ((b & 1) << 2) + ((b & 7) >> 1) : b;
 }
 
+// ---- the two kinds of codes ---------------------------------------------------
+// 2-bit codes: e2m1 nibbles against the activations' e4m3 halves (rows 2 t and 2 t + 1
+// of the MFMA's activations for token t).
+template <int SPL_>
+struct Codes2 {
+  static constexpr bool kWide = false;
+  static constexpr int kBits = 2, SPL = SPL_, DW = 2 * SPL_, kTable = 0;
+  static constexpr int kTokens = 2;            // tokens whose sums a lane holds
+};
+// 3- and 4-bit codes: levels as two bf16 halves (16 significant bits) from a table of
+// the row's 2^B levels in LDS (decode.h), against the bf16 activations as they are (row
+// t for token t); two bf16 MFMAs a fragment. A wave builds a tile's table when a step
+// enters another group.
+template <int B>
+struct CodesWide {
+  static constexpr bool kWide = true;
+  static constexpr int kBits = B, SPL = 1, DW = B, kTable = 16 * (1 << B) * 4;   // table bytes of a tile
+  static constexpr int kTokens = 4;
+  using Dec = DecodeTableSplit<B>;
+};
+
 // ---- a wave's stream of code tiles ------------------------------------------
 // NT tiles of 16 weight rows, macro steps of SPL * 128 codes, in blocks of PM
 // steps that are in flight together. The MFMA wants row nl and K quarter kq in lane
@@ -104,7 +126,7 @@ __device__ __forceinline__ int chunk_place(int b) {
 // group scales of four steps likewise), and the lanes exchange the words through
 // the LDS crossbar when they are used (ds_bpermute, no LDS memory).
 struct CodeSrc {                               // a unit's code and scale buffers (wave-uniform)
-  __amdgpu_buffer_rsrc_t code, scale;
+  __amdgpu_buffer_rsrc_t code, scale, shape;   // (shape: of table levels only)
 };
 
 struct Groups {                                // steps per group: as a shift, or (shift < 0) by a reciprocal
@@ -115,21 +137,26 @@ struct Groups {                                // steps per group: as a shift, o
   }
 };
 
-template <int SPL, int PM, int NT>
+template <class F, int PM, int NT>
 struct CodeStream {
-  static constexpr int DW = 2 * SPL;           // code dwords per lane, tile and step
+  static constexpr int DW = F::DW;             // code dwords per lane, tile and step
   static constexpr int SR = (PM + 3) / 4;      // scale registers per tile and block (four steps each)
   uint32_t cb[PM][NT][DW];
   float sc[NT][SR], scn[NT][SR];               // of the current block, and of the next
+  uint32_t ab[NT][F::kWide ? SR : 1], abn[NT][F::kWide ? SR : 1];   // shape parameters likewise (table levels)
 
   // step t into slot U; vcode: the lane's byte offset per tile
   template <int U>
   __device__ __forceinline__ void issue(const CodeSrc& src, const uint32_t* vcode, int t) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if constexpr (SPL == 2) {
+      if constexpr (DW == 4) {
         const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.code, vcode[i], t * (4 * DW * 4), 0);
         cb[U][i][0] = v.x; cb[U][i][1] = v.y; cb[U][i][2] = v.z; cb[U][i][3] = v.w;
+      } else if constexpr (DW == 3) {
+        typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
+        const u32x3 v = __builtin_amdgcn_raw_buffer_load_b96(src.code, vcode[i], t * (4 * DW * 4), 0);
+        cb[U][i][0] = v.x; cb[U][i][1] = v.y; cb[U][i][2] = v.z;
       } else {
         const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.code, vcode[i], t * (4 * DW * 4), 0);
         cb[U][i][0] = v.x; cb[U][i][1] = v.y;
@@ -145,19 +172,25 @@ struct CodeStream {
     for (int r = 0; r < SR; ++r) {
       const uint32_t g = 4u * static_cast<uint32_t>(gr.of(step(4 * r + (lane & 3))));
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < NT; ++i) {
         scn[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(src.scale, vscale[i] + g, 0, 0));
+        if constexpr (F::kWide) abn[i][r] = __builtin_amdgcn_raw_buffer_load_b32(src.shape, vscale[i] + g, 0, 0);
+      }
     }
   }
   __device__ __forceinline__ void take_scales() {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int r = 0; r < SR; ++r) sc[i][r] = scn[i][r];
+      for (int r = 0; r < SR; ++r) {
+        sc[i][r] = scn[i][r];
+        if constexpr (F::kWide) ab[i][r] = abn[i][r];
+      }
   }
-  // slot U in operand order: w[tile][dword], s[tile]; xaddr = 4 (4 nl + kq)
+  // slot U in operand order: w[tile][dword], s[tile] and (wide codes) a | b in sh[tile];
+  // xaddr = 4 (4 nl + kq)
   template <int U>
-  __device__ __forceinline__ void take(int xaddr, int nl, uint32_t (*w)[DW], float* s) {
+  __device__ __forceinline__ void take(int xaddr, int nl, uint32_t (*w)[DW], float* s, uint32_t* sh) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -165,6 +198,8 @@ struct CodeStream {
         w[i][d] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(xaddr, static_cast<int>(cb[U][i][d])));
       s[i] = __uint_as_float(static_cast<uint32_t>(
           __builtin_amdgcn_ds_bpermute(16 * nl + 4 * (U & 3), static_cast<int>(__float_as_uint(sc[i][U / 4])))));
+      if constexpr (F::kWide)
+        sh[i] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(16 * nl + 4 * (U & 3), static_cast<int>(ab[i][U / 4])));
     }
   }
 };
@@ -223,6 +258,38 @@ __device__ __forceinline__ void layer_step(const uint32_t (*w)[2 * SPL], const f
   }
 }
 
+// The same for wide codes: activation rows xr of bf16 values, the tiles' tables tab (of
+// group gtab; rebuilt when the step's group g is another), sums of tokens 4 kq + r.
+template <class F, int NT>
+__device__ __forceinline__ void wide_step(const uint32_t (*w)[F::DW], const float* sc, const uint32_t* sh,
+                                          const uint8_t* xr, int t, int g, int& gtab, uint16_t* tab, int nl, int kq,
+                                          float (*acc)[4]) {
+  using Dec = typename F::Dec;
+  if (g != gtab) {                             // wave-uniform
+    gtab = g;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) build_table<Dec>(tab + i * (F::kTable / 2), nl, kq, sh[i]);
+    wave_lds_order();
+  }
+  u32x4 a[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const u32x4*>(xr + (t * 128 + kq * 32 + 8 * j) * 2);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    uint32_t hi[16], lo[16];
+    Dec::decode(w[i], reinterpret_cast<const uint32_t*>(tab + i * (F::kTable / 2)) + nl * (1 << F::kBits),
+                Dec::swizzle(nl), hi, lo);
+    f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      part = mfma16<true>(a[j], u32x4{hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]}, part);
+      part = mfma16<true>(a[j], u32x4{lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]}, part);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(sc[i], part[r], acc[i][r]);
+  }
+}
+
 // The slow pass: the level of the field 10 (code -2) is -q(2) s, q(2) = 2 a + 4 b +
 // 8 (1 - a - b); its codes' sums are added step by step. Loads in operand order:
 // vcode, vscale as in the stream, but of row nl and quarter kq.
@@ -233,7 +300,7 @@ __device__ __forceinline__ void layer_extra(const CodeSrc& src, const __amdgpu_b
                                             float (*acc)[2]) {
 #pragma unroll 1
   for (int t = tb; t < te; t += by) {
-    CodeStream<SPL, 1, NT> st;
+    CodeStream<Codes2<SPL>, 1, NT> st;
     st.template issue<0>(src, vcode, t);
     const int g = gr.of(t);
     float lev[NT];
@@ -303,29 +370,32 @@ struct LayerUpParams {
   Groups groups;           // steps per group
   int ks;                  // waves per tile (each a part of K)
   int batch;               // rounds between the joins of the waves' sums
-  int down_spl;            // operand order of h
+  int down_spl;            // operand order of h: chunks per lane and step of 2-bit down codes; 0: bf16 rows
   int32_t* ids;            // [T][topk] out
   float* weights;
   int32_t* ids_user;       // a second copy for the caller, or NULL
   float* weights_user;
   int32_t* rec;
-  uint8_t* hq;             // [T*topk][2][I] e4m3 halves of h in operand order
+  uint8_t* hq;             // [T*topk][2][I] e4m3 halves of h in operand order, or [T*topk][I] bf16
   uint8_t* hs;             // [T*topk][2][I / 32] block scales
 };
 
 struct LayerUpLds {
-  int xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
+  int tab, xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
   int xq_stride, xs_stride;
 };
-__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int batch) {
+__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int batch, int table) {
   LayerUpLds L;
   const int P = T * topk;
   auto up16 = [](int v) { return (v + 15) & ~15; };
-  L.xq_stride = H + 16;                        // 16 bytes of padding: the rows' reads hit other banks
+  // Rows of the MFMA: two halves a token, or (table > 0) one bf16 row; 16 bytes of
+  // padding each: the rows' reads hit other banks.
+  L.xq_stride = (table ? 2 * H : H) + 16;
   L.xs_stride = up16(H / 32) + 16;
   int o = 0;
-  L.xq = o;    o += 2 * T * L.xq_stride;
-  L.xs = o;    o += 2 * T * L.xs_stride;
+  L.tab = o;   o += kLayerWaves * 2 * table;   // (tables start at multiples of their size)
+  L.xq = o;    o += (table ? T : 2 * T) * L.xq_stride;
+  L.xs = o;    o += table ? 0 : 2 * T * L.xs_stride;
   // partial sums, two batches of rounds: [2][batch][waves][2 tiles][T][16]; the
   // first-pair table of the experts uses the same bytes before the first round
   const int red = 2 * batch * kLayerWaves * 2 * T * 16 * 4;
@@ -341,15 +411,16 @@ __host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int b
   return L;
 }
 
-template <int SPL, int PM, int EPL>
+template <class F, int PM, int EPL>
 __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  using Stream = CodeStream<SPL, PM, 2>;
+  extern __shared__ __align__(1024) unsigned char smem[];        // (table rows rely on this alignment)
+  constexpr int SPL = F::SPL;
+  using Stream = CodeStream<F, PM, 2>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
   const int T = p.T, topk = p.r.topk, P = T * topk;
-  const LayerUpLds L = layer_up_lds(T, topk, p.H, p.batch);
+  const LayerUpLds L = layer_up_lds(T, topk, p.H, p.batch, F::kTable);
   int32_t* s_first = reinterpret_cast<int32_t*>(smem + L.first);
   int32_t* s_id = reinterpret_cast<int32_t*>(smem + L.id);
   float* s_w = reinterpret_cast<float*>(smem + L.w);
@@ -379,6 +450,10 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       const int t = on ? v / per_row : 0;
       const int q = on ? v - t * per_row : 0;
       const u32x4 raw = *reinterpret_cast<const u32x4*>(p.x + static_cast<int64_t>(t) * p.H + 8 * q);
+      if constexpr (F::kWide) {
+        if (on) *reinterpret_cast<u32x4*>(smem + L.xq + t * L.xq_stride + 16 * q) = raw;
+        continue;
+      }
       float f[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -475,9 +550,11 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   const int total = n * tiles;
   const int nmacro = p.H / (SPL * 128);
   // this wave's steps: part, part + ks, ... (the team's waves read neighbouring
-  // pieces of a row at any time)
-  const int steps = (nmacro - part + ks - 1) / ks;
-  const uint32_t row_bytes = static_cast<uint32_t>(p.H / 4);
+  // pieces of a row at any time); wide codes: a run of steps, so that a table serves
+  // several
+  const int first = F::kWide ? part * nmacro / ks : part, by = F::kWide ? 1 : ks;
+  const int steps = F::kWide ? (part + 1) * nmacro / ks - first : (nmacro - part + ks - 1) / ks;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.H * F::kBits / 8);
   // a gate row of the tile, and the up row I rows below it
   auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
     vc[0] = row * row_bytes + quarter * (Stream::DW * 4);
@@ -488,9 +565,10 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   uint32_t vcode[2], vscale[2];
   lane_offsets(lane >> 2, lane & 3, vcode, vscale);
   const int xaddr = 4 * (4 * nl + kq);
-  const int ml = nl < 2 * T ? nl : 0;          // rows past the tokens are not used
+  const int ml = nl < (F::kWide ? T : 2 * T) ? nl : 0;           // rows past the tokens are not used
   const uint8_t* xr = smem + L.xq + ml * L.xq_stride;
   const uint8_t* sr = smem + L.xs + ml * L.xs_stride;
+  uint16_t* tab = reinterpret_cast<uint16_t*>(smem + L.tab + wave * 2 * F::kTable);
 
   auto unit_row = [&](int u, int64_t& e, int& j) {
     const int uu = u < total ? u : 0;
@@ -506,6 +584,7 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
     const uint32_t rows = u < total ? static_cast<uint32_t>(p.I + 16) : 0u;   // no unit: every load is out of range
     s.code = layer_rsrc(p.codes + e * p.code_bytes + static_cast<int64_t>(16 * j) * row_bytes, rows * row_bytes);
     s.scale = layer_rsrc(p.scales + (e * 2 * p.I + 16 * j) * p.gpr, rows * 4u * static_cast<uint32_t>(p.gpr));
+    s.shape = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + 16 * j) * p.gpr, rows * 4u * static_cast<uint32_t>(p.gpr));
     return s;
   };
   if (n == 0) return;                          // no expert taken at all (block-uniform)
@@ -516,9 +595,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
 
   Stream st;
   CodeSrc cur = source(u);
-  st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return min(i, steps - 1) * ks + part; });
+  st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return first + min(i, steps - 1) * by; });
   [&]<int... U>(std::integer_sequence<int, U...>) {
-    (st.template issue<U>(cur, vcode, min(U, steps - 1) * ks + part), ...);
+    (st.template issue<U>(cur, vcode, first + min(U, steps - 1) * by), ...);
   }(std::make_integer_sequence<int, PM>{});
 
   float* red = reinterpret_cast<float*>(smem + L.red);
@@ -526,8 +605,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   int slot_r = 0, half = 0, r0 = 0;            // round of the batch, its buffer, its first round
   for (int r = 0; r < rounds; ++r) {
     const CodeSrc nxt = source(u + stride);
-    float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    float acc[2][F::kTokens] = {};
     uint32_t bad = 0u;
+    int gtab = -1;
     for (int t0 = 0; t0 < steps; t0 += PM) {
       // the next block: this unit's next PM steps, or the next unit's first
       st.take_scales();
@@ -535,8 +615,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       CodeSrc src;
       src.code = more ? cur.code : nxt.code;
       src.scale = more ? cur.scale : nxt.scale;
+      if constexpr (F::kWide) src.shape = more ? cur.shape : nxt.shape;
       const int tn = more ? t0 + PM : 0;
-      st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return min(tn + i, steps - 1) * ks + part; });
+      st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return first + min(tn + i, steps - 1) * by; });
       [&]<int... U>(std::integer_sequence<int, U...>) {
         (([&] {
            if (t0 + U < steps) {
@@ -546,33 +627,41 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
              for (int i = 0; i < 2; ++i)
 #pragma unroll
                for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
-             st.template take<U>(xaddr, nl, w, s);
-             layer_step<SPL, 2, 0>(w, s, xr, sr, (t0 + U) * ks + part, kq, acc, bad);
+             uint32_t sh[2];
+             st.template take<U>(xaddr, nl, w, s, sh);
+             const int t = first + (t0 + U) * by;
+             if constexpr (F::kWide) {
+               wide_step<F, 2>(w, s, sh, xr, t, p.groups.of(t), gtab, tab, nl, kq, acc);
+             } else {
+               layer_step<SPL, 2, 0>(w, s, xr, sr, t, kq, acc, bad);
+             }
            }
-           st.template issue<U>(src, vcode, min(tn + U, steps - 1) * ks + part);
+           st.template issue<U>(src, vcode, first + min(tn + U, steps - 1) * by);
            __builtin_amdgcn_sched_barrier(0);
          }()),
          ...);
       }(std::make_integer_sequence<int, PM>{});
     }
-    if (u < total && __any((bad & 0xAAAAAAAAu) != 0u)) {
-      int64_t e;
-      int j;
-      unit_row(u, e, j);
-      const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + 16 * j) * p.gpr,
-                                                    static_cast<uint32_t>(p.I + 16) * 4u * static_cast<uint32_t>(p.gpr));
-      uint32_t vc[2], vs[2];
-      lane_offsets(nl, kq, vc, vs);
-      layer_extra<SPL, 2>(cur, shp, vc, vs, part, nmacro, ks, p.groups, xr, sr, kq, acc);
+    if constexpr (!F::kWide) {
+      if (u < total && __any((bad & 0xAAAAAAAAu) != 0u)) {
+        int64_t e;
+        int j;
+        unit_row(u, e, j);
+        const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + 16 * j) * p.gpr,
+                                                      static_cast<uint32_t>(p.I + 16) * 4u * static_cast<uint32_t>(p.gpr));
+        uint32_t vc[2], vs[2];
+        lane_offsets(nl, kq, vc, vs);
+        layer_extra<SPL, 2>(cur, shp, vc, vs, part, nmacro, ks, p.groups, xr, sr, kq, acc);
+      }
     }
     // partial sums of the team's waves meet in LDS; lane group kq holds tokens 2 kq
-    // and 2 kq + 1
+    // and 2 kq + 1 (wide codes: 4 kq .. 4 kq + 3)
     float* rb = red + (half * p.batch + slot_r) * red_round;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-      if (2 * kq + m < T)
+    for (int m = 0; m < F::kTokens; ++m)
+      if (F::kTokens * kq + m < T)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + 2 * kq + m) * 16 + nl] = acc[i][m];
+        for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + F::kTokens * kq + m) * 16 + nl] = acc[i][m];
     cur = nxt;
     u += stride;
     ++slot_r;
@@ -611,7 +700,10 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       const uint32_t ef = block_exponent(amax);
       uint32_t hi, lo;
       split2(h, h, block_factor(ef), hi, lo);
-      if (slot != 0xff) {
+      if (slot != 0xff && p.down_spl == 0) {
+        const uint16_t hb = static_cast<uint16_t>(v != v ? (__float_as_uint(v) >> 16) | 0x40u : __float_as_uint(h) >> 16);
+        reinterpret_cast<uint16_t*>(p.hq)[static_cast<int64_t>(t * topk + slot) * p.I + 16 * j + c] = hb;
+      } else if (slot != 0xff) {
         const int b = j / 2;
         const int place = 32 * (p.down_spl == 2 ? chunk_place<2>(b) : b) + code_slot(c);
         uint8_t* hq = p.hq + static_cast<int64_t>(t * topk + slot) * 2 * p.I + place;
@@ -631,7 +723,7 @@ struct LayerDownParams {
   const int32_t* rec;
   const float* weights;    // [T][topk]
   int T, topk;
-  const uint8_t* hq;       // [pair][2][I]
+  const uint8_t* hq;       // [pair][2][I], or [pair][I] bf16 (wide codes)
   const uint8_t* hs;       // [pair][2][I / 32]
   const uint8_t* codes;    // down, expert 0
   const float* scales;
@@ -647,16 +739,18 @@ struct LayerDownParams {
 };
 
 struct LayerDownLds {
-  int wave_bytes, hstride, sstride, sum, total;
+  int wave_bytes, hstride, sstride, wave0, sum, total;
 };
-__host__ __device__ inline LayerDownLds layer_down_lds(int T, int I, int spl, int ks) {
+// table: table bytes of a tile (wide codes), two tiles a wave
+__host__ __device__ inline LayerDownLds layer_down_lds(int T, int I, int spl, int ks, int table) {
   LayerDownLds L;
   const int nmacro = I / (spl * 128);
   const int kp = (nmacro + ks - 1) / ks * spl * 128;             // K values of a part
   L.hstride = kp + 16;
   L.sstride = ((kp / 32 + 15) & ~15) + 16;
-  L.wave_bytes = 2 * L.hstride + 2 * L.sstride;
-  L.sum = kLayerWaves * L.wave_bytes;
+  L.wave_bytes = 2 * L.hstride + (table ? 0 : 2 * L.sstride);
+  L.wave0 = kLayerWaves * 2 * table;
+  L.sum = L.wave0 + kLayerWaves * L.wave_bytes;
   L.total = L.sum + kLayerWaves * T * 32 * 4;
   return L;
 }
@@ -671,58 +765,63 @@ struct DownItem {
 // An item's h halves and block scales on their way into the wave's LDS: the first
 // 6 KB (a part of 3 K values) wait in registers, so that they are loaded before the
 // codes of their item; longer parts load the rest at the store.
-template <int SPL>
+template <class F>
 struct DownActs {
-  static constexpr int R = 6;
+  static constexpr int R = F::kWide ? 1 : 6, SPL = F::SPL;       // (the tables need the registers)
   u32x4 v[R];
   uint32_t sv;
-  static __device__ __forceinline__ const uint8_t* row(const LayerDownParams& p, const DownItem& q, int pc) {
-    return p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128;
+  // 16-byte chunk i of the part: of its two half rows (n chunks each), or of its bf16
+  // row of 2 n chunks
+  static __device__ __forceinline__ const uint8_t* chunk(const LayerDownParams& p, const DownItem& q, int i, int n) {
+    if constexpr (F::kWide) {
+      return p.hq + (static_cast<int64_t>(q.pair) * p.I + q.tb * 128) * 2 + 16 * i;
+    } else {
+      const int pc = i < n ? 0 : 1;
+      return p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128 + 16 * (i - pc * n);
+    }
   }
-  static __device__ __forceinline__ const uint8_t* scales(const LayerDownParams& p, const DownItem& q, int pc) {
-    return p.hs + (static_cast<int64_t>(q.pair) * 2 + pc) * (p.I / 32) + q.tb * SPL * 4;
+  static __device__ __forceinline__ int place(const LayerDownLds& L, int i, int n) {
+    return F::kWide || i < n ? 16 * i : L.hstride + 16 * (i - n);
   }
-  // 16-byte chunk i of the part's two rows: row i / n, chunk i % n (n chunks a row)
+  // dword i of the part's scales (m a row)
+  static __device__ __forceinline__ const uint8_t* scale(const LayerDownParams& p, const DownItem& q, int i, int m) {
+    const int pc = i < m ? 0 : 1;
+    return p.hs + (static_cast<int64_t>(q.pair) * 2 + pc) * (p.I / 32) + q.tb * SPL * 4 + 4 * (i - pc * m);
+  }
   __device__ __forceinline__ void load(const LayerDownParams& p, const DownItem& q, int lane) {
     const int n = (q.te - q.tb) * SPL * 8;
-    const uint8_t* hi = row(p, q, 0);
-    const uint8_t* lo = row(p, q, 1);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = min(64 * r + lane, 2 * n - 1);
-      v[r] = *reinterpret_cast<const u32x4*>(i < n ? hi + 16 * i : lo + 16 * (i - n));
-    }
-    const int m = n / 8;                       // scale dwords a row
-    const int i = min(lane, 2 * m - 1);
-    sv = *reinterpret_cast<const uint32_t*>(i < m ? scales(p, q, 0) + 4 * i : scales(p, q, 1) + 4 * (i - m));
+    for (int r = 0; r < R; ++r) v[r] = *reinterpret_cast<const u32x4*>(chunk(p, q, min(64 * r + lane, 2 * n - 1), n));
+    if constexpr (!F::kWide) sv = *reinterpret_cast<const uint32_t*>(scale(p, q, min(lane, n / 4 - 1), n / 8));
   }
   __device__ __forceinline__ void store(const LayerDownParams& p, const DownItem& q, uint8_t* hreg, uint8_t* sreg,
                                         const LayerDownLds& L, int lane) const {
     const int n = (q.te - q.tb) * SPL * 8, m = n / 8;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = 64 * r + lane;
-      if (i < 2 * n) *reinterpret_cast<u32x4*>(hreg + (i < n ? 16 * i : L.hstride + 16 * (i - n))) = v[r];
-    }
-    if (lane < 2 * m) *reinterpret_cast<uint32_t*>(sreg + (lane < m ? 4 * lane : L.sstride + 4 * (lane - m))) = sv;
+    for (int r = 0; r < R; ++r)
+      if (64 * r + lane < 2 * n) *reinterpret_cast<u32x4*>(hreg + place(L, 64 * r + lane, n)) = v[r];
     for (int i = 64 * R + lane; i < 2 * n; i += 64)
-      *reinterpret_cast<u32x4*>(hreg + (i < n ? 16 * i : L.hstride + 16 * (i - n))) =
-          *reinterpret_cast<const u32x4*>(row(p, q, i < n ? 0 : 1) + 16 * (i < n ? i : i - n));
-    for (int i = 64 + lane; i < 2 * m; i += 64)
-      *reinterpret_cast<uint32_t*>(sreg + (i < m ? 4 * i : L.sstride + 4 * (i - m))) =
-          *reinterpret_cast<const uint32_t*>(scales(p, q, i < m ? 0 : 1) + 4 * (i < m ? i : i - m));
+      *reinterpret_cast<u32x4*>(hreg + place(L, i, n)) = *reinterpret_cast<const u32x4*>(chunk(p, q, i, n));
+    if constexpr (!F::kWide) {
+      if (lane < 2 * m) *reinterpret_cast<uint32_t*>(sreg + (lane < m ? 4 * lane : L.sstride + 4 * (lane - m))) = sv;
+      for (int i = 64 + lane; i < 2 * m; i += 64)
+        *reinterpret_cast<uint32_t*>(sreg + (i < m ? 4 * i : L.sstride + 4 * (i - m))) =
+            *reinterpret_cast<const uint32_t*>(scale(p, q, i, m));
+    }
   }
 };
 
-template <int SPL, int PM, int NT>
+template <class F, int PM, int NT>
 __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  using Stream = CodeStream<SPL, PM, NT>;
+  extern __shared__ __align__(1024) unsigned char smem[];        // (table rows rely on this alignment)
+  constexpr int SPL = F::SPL;
+  using Stream = CodeStream<F, PM, NT>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
-  const LayerDownLds L = layer_down_lds(p.T, p.I, SPL, p.ks);
-  uint8_t* hreg = smem + wave * L.wave_bytes;
+  const LayerDownLds L = layer_down_lds(p.T, p.I, SPL, p.ks, F::kTable);
+  uint16_t* tab = reinterpret_cast<uint16_t*>(smem + wave * 2 * F::kTable);
+  uint8_t* hreg = smem + L.wave0 + wave * L.wave_bytes;
   uint8_t* sreg = hreg + 2 * L.hstride;
   float* sums = reinterpret_cast<float*>(smem + L.sum) + wave * p.T * 32;
   for (int i = lane; i < p.T * 32; i += 64) sums[i] = 0.0f;
@@ -731,7 +830,7 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   const int rows = min(p.rows, p.H - n0);
   const int items = p.rec[0] * p.ks;
   const int nmacro = p.I / (SPL * 128);
-  const uint32_t row_bytes = static_cast<uint32_t>(p.I / 4);
+  const uint32_t row_bytes = static_cast<uint32_t>(p.I * F::kBits / 8);
   // a row of each tile (past the workgroup's rows: its last one, whose sums are not used)
   auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
 #pragma unroll
@@ -762,12 +861,14 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
                         q.live * static_cast<uint32_t>(rows) * row_bytes);
     s.scale = layer_rsrc(p.scales + (q.e * p.H + n0) * p.gpr,
                          q.live * static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
+    s.shape = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
+                         q.live * static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
     return s;
   };
   int it = wave;
   if (it < items) {                            // wave-uniform; the barrier comes after
     Stream st;
-    DownActs<SPL> hst;
+    DownActs<F> hst;
     Item q = item_of(it);
     CodeSrc cur = source(q);
     hst.load(p, q, lane);
@@ -776,7 +877,7 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
     [&]<int... U>(std::integer_sequence<int, U...>) {
       (st.template issue<U>(cur, vcode, min(q.tb + U, q.te - 1)), ...);
     }(std::make_integer_sequence<int, PM>{});
-    const uint8_t* xr = hreg + (nl == 1 ? L.hstride : 0);        // row 0: hi, row 1: lo
+    const uint8_t* xr = hreg + (!F::kWide && nl == 1 ? L.hstride : 0);   // row 0: hi, row 1: lo; or one bf16 row
     const uint8_t* sr = sreg + (nl == 1 ? L.sstride : 0);
     for (; it < items; it += kLayerWaves) {
       hst.store(p, q, hreg, sreg, L, lane);    // the part's h into this wave's LDS
@@ -785,16 +886,16 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
       const CodeSrc nxt = source(qn);
       const float w = p.weights[q.pair];
       hst.load(p, qn, lane);                   // ahead of the next item's codes
-      float acc[NT][2];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = 0.0f;
+      float acc[NT][F::kTokens] = {};
       uint32_t bad = 0u;
+      int gtab = -1;
       for (int t0 = q.tb; t0 < q.te; t0 += PM) {
         st.take_scales();
         const bool more = t0 + PM < q.te;
         CodeSrc src;
         src.code = more ? cur.code : nxt.code;
         src.scale = more ? cur.scale : nxt.scale;
+        if constexpr (F::kWide) src.shape = more ? cur.shape : nxt.shape;
         const int tn = more ? t0 + PM : qn.tb, last = (more ? q.te : qn.te) - 1;
         st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return min(tn + i, last); });
         [&]<int... U>(std::integer_sequence<int, U...>) {
@@ -806,8 +907,13 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
                for (int i = 0; i < NT; ++i)
 #pragma unroll
                  for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
-               st.template take<U>(xaddr, nl, w4, s);
-               layer_step<SPL, NT, 0>(w4, s, xr, sr, t0 + U - q.tb, kq, acc, bad);
+               uint32_t sh[NT];
+               st.template take<U>(xaddr, nl, w4, s, sh);
+               if constexpr (F::kWide) {
+                 wide_step<F, NT>(w4, s, sh, xr, t0 + U - q.tb, p.groups.of(t0 + U), gtab, tab, nl, kq, acc);
+               } else {
+                 layer_step<SPL, NT, 0>(w4, s, xr, sr, t0 + U - q.tb, kq, acc, bad);
+               }
              }
              st.template issue<U>(src, vcode, min(tn + U, last));
              __builtin_amdgcn_sched_barrier(0);
@@ -815,13 +921,15 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
            ...);
         }(std::make_integer_sequence<int, PM>{});
       }
-      if (__any((bad & 0xAAAAAAAAu) != 0u)) {
-        const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
-                                                      static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
-        uint32_t vc[NT], vs[NT];
-        lane_offsets(nl, kq, vc, vs);
-        const int back = q.tb * SPL * 128;     // (steps count from the part's first in LDS)
-        layer_extra<SPL, NT>(cur, shp, vc, vs, q.tb, q.te, 1, p.groups, xr - back, sr - q.tb * SPL * 4, kq, acc);
+      if constexpr (!F::kWide) {
+        if (__any((bad & 0xAAAAAAAAu) != 0u)) {
+          const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
+                                                        static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
+          uint32_t vc[NT], vs[NT];
+          lane_offsets(nl, kq, vc, vs);
+          const int back = q.tb * SPL * 128;     // (steps count from the part's first in LDS)
+          layer_extra<SPL, NT>(cur, shp, vc, vs, q.tb, q.te, 1, p.groups, xr - back, sr - q.tb * SPL * 4, kq, acc);
+        }
       }
       if (kq == 0) {
         const int t = q.pair / p.topk;
@@ -855,7 +963,8 @@ Groups group_steps(int group, int spl) {
   return Groups{s, 0u};
 }
 
-int layer_spl(int group) { return group % 256 == 0 ? 2 : 1; }
+int layer_spl(int bits, int group) { return bits == 2 && group % 256 == 0 ? 2 : 1; }
+int layer_table(int bits) { return bits == 2 ? 0 : 16 * (1 << bits) * 4; }
 
 constexpr int kLayerLds = 160 * 1024;
 
@@ -877,41 +986,44 @@ int layer_up_parts(int T, int topk, int E, int I, int nmacro, int grid) {
 }
 
 // K parts of kernel 2: enough items for every wave, and a part's h in LDS.
-int layer_down_parts(int T, int topk, int E, int I, int spl) {
+int layer_down_parts(int T, int topk, int I, int spl, int table) {
   const int nmacro = I / (spl * 128);
   const int jobs = T * topk;
   int ks = 1;
-  while (ks < nmacro && (jobs * ks < kLayerWaves || layer_down_lds(T, I, spl, ks).total > kLayerLds)) ks *= 2;
+  while (ks < nmacro && (jobs * ks < kLayerWaves || layer_down_lds(T, I, spl, ks, table).total > kLayerLds)) ks *= 2;
   return std::min(ks, nmacro);
 }
 
 }  // namespace
 
-// One run of the two kernels: 2-bit codes, up to eight tokens, and activations, lists
-// and partial sums in one compute unit's LDS.
+// One run of the two kernels: 2- to 4-bit codes, up to eight tokens, and activations,
+// tables, lists and partial sums in one compute unit's LDS.
 static bool layer_fits(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
                        int dn_group) {
-  if (up_bits != 2 || dn_bits != 2) return false;
+  if (up_bits < 2 || up_bits > 4 || dn_bits < 2 || dn_bits > 4) return false;
   if (T < 1 || T > kLayerMaxT || E > kLayerMaxE || topk > kRouterMaxTopk) return false;
-  if (H > 65536 || I > 65536 || (I + 16) * (H / 4) >= (int64_t{1} << 32)) return false;   // 32-bit tile offsets
-  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H), 1).total > kLayerLds) return false;
-  const int spl = layer_spl(dn_group);
-  const int ks = layer_down_parts(static_cast<int>(T), topk, E, static_cast<int>(I), spl);
-  return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks).total <= kLayerLds;
+  if (H > 65536 || I > 65536 || (I + 16) * (H * up_bits / 8) >= (int64_t{1} << 32)) return false;   // 32-bit tile offsets
+  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H), 1, layer_table(up_bits)).total > kLayerLds)
+    return false;
+  const int spl = layer_spl(dn_bits, dn_group);
+  const int ks = layer_down_parts(static_cast<int>(T), topk, static_cast<int>(I), spl, layer_table(dn_bits));
+  return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks, layer_table(dn_bits)).total <= kLayerLds;
 }
 
 // Tokens of one run of the two kernels; 0: the composed path. Nine to 32 tokens take
 // runs of up to eight: an expert that tokens of several runs share is read again, but
-// at twice the composed path's rate (2048 x 1024, 16 tokens, top-8 of 128: 80 against
-// 158 us; 7168 x 3 K, 32 tokens, top-16 of 128: 1.24 against 1.46 ms). With weights
-// below 4 MB the launches count, not the rate (16 tokens, 512 x 256, top-2 of 8: 40
-// against 33 us).
+// at twice the composed path's rate (2-bit codes, 2048 x 1024, 16 tokens, top-8 of 128:
+// 80 against 158 us; 7168 x 3 K, 32 tokens, top-16 of 128: 1.24 against 1.46 ms). Wider
+// codes take two runs at most (4 bits, 2048 x 1024, top-4 of 32: 16 tokens 151 against
+// 158 us, 24 tokens 222 against 210). With weights below 4 MB the launches count, not
+// the rate (16 tokens, 512 x 256, top-2 of 8: 40 against 33 us).
 int64_t moe_layer_tokens(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
                          int dn_group) {
-  if (T < 1 || T > 4 * kLayerMaxT) return 0;
+  const int64_t most = up_bits == 2 && dn_bits == 2 ? 4 : 2;
+  if (T < 1 || T > most * kLayerMaxT) return 0;
   const int64_t runs = (T + kLayerMaxT - 1) / kLayerMaxT, n = (T + runs - 1) / runs;
   if (!layer_fits(n, topk, E, H, I, up_bits, up_group, dn_bits, dn_group)) return 0;
-  if (runs > 1 && 3 * H * I / 4 * std::min<int64_t>(E, T * topk) < (int64_t{4} << 20)) return 0;
+  if (runs > 1 && 3 * H * I * up_bits / 8 * std::min<int64_t>(E, T * topk) < (int64_t{4} << 20)) return 0;
   return n;
 }
 
@@ -945,11 +1057,12 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   p.shapes = up.shapes;
   p.code_bytes = up.code_bytes;
   p.gpr = H / up.group;
-  const int spl = layer_spl(up.group), dspl = layer_spl(dn.group);
+  const int spl = layer_spl(up.bits, up.group), dspl = layer_spl(dn.bits, dn.group);
+  const int table = layer_table(up.bits), dtable = layer_table(dn.bits);
   p.groups = group_steps(up.group, spl);
   const int nmacro = H / (spl * 128);
   p.ks = layer_up_parts(T, r.topk, r.E, I, nmacro, cus);
-  p.down_spl = dspl;
+  p.down_spl = dtable ? 0 : dspl;
   p.ids = b.ids;
   p.weights = b.weights;
   p.ids_user = ids_user;
@@ -961,14 +1074,22 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   const int64_t units = static_cast<int64_t>(std::min(r.E, T * r.topk)) * (I / 16);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
   p.batch = 4;
-  while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch).total > kLayerLds) --p.batch;
-  const int lds = layer_up_lds(T, r.topk, H, p.batch).total;
+  while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch, table).total > kLayerLds) --p.batch;
+  const int lds = layer_up_lds(T, r.topk, H, p.batch, table).total;
   hipError_t e;
   const bool few = r.E <= 256;                 // a router wave with 4 experts a lane, or 16
-  if (spl == 2) {
-    e = few ? launch_layer(k_layer_up<2, 4, 4>, grid, lds, p, st) : launch_layer(k_layer_up<2, 4, 16>, grid, lds, p, st);
+  auto up_kernel = [&](auto f_c, auto pm_c) {
+    using F = decltype(f_c);
+    constexpr int PM = decltype(pm_c)::value;
+    return few ? launch_layer(k_layer_up<F, PM, 4>, grid, lds, p, st) : launch_layer(k_layer_up<F, PM, 16>, grid, lds, p, st);
+  };
+  using I2 = std::integral_constant<int, 2>;   // (more spill)
+  using I4 = std::integral_constant<int, 4>;
+  using I8 = std::integral_constant<int, 8>;
+  if (up.bits == 2) {
+    e = spl == 2 ? up_kernel(Codes2<2>{}, I4{}) : up_kernel(Codes2<1>{}, I8{});
   } else {
-    e = few ? launch_layer(k_layer_up<1, 8, 4>, grid, lds, p, st) : launch_layer(k_layer_up<1, 8, 16>, grid, lds, p, st);
+    e = up.bits == 3 ? up_kernel(CodesWide<3>{}, I2{}) : up_kernel(CodesWide<4>{}, I2{});
   }
   if (e != hipSuccess) return e;
 
@@ -991,17 +1112,19 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   const int nt = d.rows > 16 ? 2 : 1;
   d.rt = (d.rows + nt - 1) / nt;
   d.rows = d.rt * nt;
-  d.ks = layer_down_parts(T, r.topk, r.E, I, dspl);
+  d.ks = layer_down_parts(T, r.topk, I, dspl, dtable);
   d.y = y;
   d.ybf16 = ybf16;
   const unsigned dgrid = static_cast<unsigned>((H + d.rows - 1) / d.rows);
-  const int dlds = layer_down_lds(T, I, dspl, d.ks).total;
-  if (dspl == 2) {
-    return nt == 2 ? launch_layer(k_layer_down<2, 4, 2>, dgrid, dlds, d, st)
-                   : launch_layer(k_layer_down<2, 4, 1>, dgrid, dlds, d, st);
-  }
-  return nt == 2 ? launch_layer(k_layer_down<1, 8, 2>, dgrid, dlds, d, st)
-                 : launch_layer(k_layer_down<1, 8, 1>, dgrid, dlds, d, st);
+  const int dlds = layer_down_lds(T, I, dspl, d.ks, dtable).total;
+  auto down_kernel = [&](auto f_c, auto pm_c) {
+    using F = decltype(f_c);
+    constexpr int PM = decltype(pm_c)::value;
+    return nt == 2 ? launch_layer(k_layer_down<F, PM, 2>, dgrid, dlds, d, st)
+                   : launch_layer(k_layer_down<F, PM, 1>, dgrid, dlds, d, st);
+  };
+  if (dn.bits == 2) return dspl == 2 ? down_kernel(Codes2<2>{}, I4{}) : down_kernel(Codes2<1>{}, I8{});
+  return dn.bits == 3 ? down_kernel(CodesWide<3>{}, I2{}) : down_kernel(CodesWide<4>{}, I2{});
 }
 
 hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, int run, const MoeLayerWeight& up,

@@ -382,15 +382,16 @@ int cubic_moe_topk(const cubic_router* router, int64_t T, int32_t* topk_ids, flo
  * finds (gate_up0, down0: expert 0 of router->E experts back to back; h rounded to
  * bf16 there as here):
  *   y[t] = sum_j topk_weights[t][j] * (bf16(SiLU(g) * u) * D_e^T),  [g | u] = x_t * GU_e^T
- * A token whose experts are all masked out gets a zero row. For 2-bit weights and
- * up to eight tokens (E <= 1024, and activations that fit a compute unit's LDS)
+ * A token whose experts are all masked out gets a zero row. For 2- to 4-bit weights
+ * and up to eight tokens (E <= 1024, and activations that fit a compute unit's LDS)
  * the layer runs in two kernels, which read each touched expert's codes from HBM
- * once, and for up to 32 tokens (weights of 4 MB and more) in such runs of up to
- * eight; otherwise the router kernel and the MLP step run one after the other, with
- * the limits of cubic_moe_mlp. In the two kernels the activations are multiplied
- * exactly unless they lie below 2^-14 of the largest of their 32 neighbours (then
- * off by up to 2^-22 of that), and a token with a non-finite activation has NaN
- * rows. The sums' order does not depend on timing.
+ * once, and with weights of 4 MB and more for up to 32 tokens (3 and 4 bits: 16) in
+ * such runs of up to eight; otherwise the router kernel and the MLP step run one after
+ * the other, with the limits of cubic_moe_mlp. 2-bit weights multiply the activations
+ * exactly, in the two kernels unless they lie below 2^-14 of the largest of their 32
+ * neighbours (then off by up to 2^-22 of that); wider codes' levels have 16 significant
+ * bits. A non-finite activation makes its token's row non-finite and no other. The sums'
+ * order does not depend on timing.
  * x_bf16 [T][H]; y [T][H] in y_dtype CUBIC_DTYPE_F32 or CUBIC_DTYPE_BF16 (rounded
  * once); topk_ids and topk_weights [T][topk] receive the routing, or are NULL. The
  * workspace (cubic_moe_layer_workspace_bytes) holds the routing and the

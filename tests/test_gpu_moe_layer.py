@@ -216,6 +216,88 @@ def test_layer_wide_codes(bits, ug, dg):
         assert np.array_equal(yb, torch.from_numpy(y).to(torch.bfloat16).float().numpy())
 
 
+@pytest.mark.parametrize("bits", [3, 4])
+@pytest.mark.parametrize("H,I,ug,dg", [(256, 128, 128, 128), (768, 640, 384, 640), (1152, 256, 128, 256),
+                                       (2048, 512, 512, 128)])
+def test_layer_wide_codes_in_two_kernels(bits, H, I, ug, dg):
+    """3- and 4-bit codes, the field value -2^(B-1) among them, one to eight tokens: levels of 16
+    significant bits put the sums off by some 2^-17, so that of the h values a few in a hundred round to
+    a neighbour (2-norm error sqrt(0.03) * 2^-8 = 7e-4); the bar is 2e-3."""
+    for T, E, topk in ((1, 5, 5), (3, 9, 2), (8, 6, 4)):
+        say(f"layer bits={bits} H={H} I={I} groups {ug}/{dg} T={T}")
+        gu, dn = Experts(bits + T, E, 2 * I, H, bits, ug, 0.01), Experts(T, E, H, I, bits, dg, 0.01)
+        x, logits = _x(T, T, H), _logits(T, T, E)
+        if T == 3:
+            logits[1] = -float("inf")
+        y, ids, w = _run(x, logits, gu, dn, topk, score="sigmoid")
+        ref, rids, _ = _reference(x, logits, gu, dn, topk, score="sigmoid")
+        assert np.array_equal(ids, rids) and _norm_err(y, ref) <= 2e-3
+        again, _, _ = _run(x, logits, gu, dn, topk, score="sigmoid")
+        assert np.array_equal(y, again)
+
+
+@pytest.mark.parametrize("ub,db", [(2, 4), (4, 2), (3, 2), (2, 3), (4, 3), (2, 6)])
+def test_layer_mixed_widths(ub, db):
+    say(f"layer bits {ub}/{db}")
+    gu, dn = Experts(ub, 6, 512, 512, ub, 256), Experts(db, 6, 512, 256, db, 128)
+    for T in (1, 5):
+        x, logits = _x(T, T, 512), _logits(T, T, 6)
+        y, ids, _ = _run(x, logits, gu, dn, 3)
+        ref, rids, _ = _reference(x, logits, gu, dn, 3)
+        assert np.array_equal(ids, rids) and _norm_err(y, ref) <= 2e-3
+
+
+@pytest.mark.parametrize("bits,T", [(2, 9), (2, 21), (2, 32), (2, 33), (4, 9), (4, 16), (4, 17)])
+def test_layer_runs_of_tokens(bits, T):
+    """More than eight tokens, with weights above 4 MB: runs of up to eight on the same buffers, then the
+    composed path."""
+    say(f"layer runs bits={bits} T={T}")
+    H, I, E, topk = 1024, 512, 12, 3
+    gu, dn = Experts(T, E, 2 * I, H, bits, 256), Experts(T + 1, E, H, I, bits, 256)
+    x, logits = _x(T, T, H), _logits(T, T, E)
+    logits[T // 2] = -float("inf")
+    for dtype in (torch.float32, torch.bfloat16):
+        y, ids, w = _run(x, logits.to(dtype), gu, dn, topk, score="sigmoid", scale=2.5)
+        ref, rids, rw = _reference(x, logits.to(dtype), gu, dn, topk, score="sigmoid", scale=2.5)
+        assert np.array_equal(ids, rids) and np.allclose(w, rw, rtol=2.0 ** -23, atol=0)
+        assert _norm_err(y, ref) <= 2e-3
+
+
+@pytest.mark.parametrize("T,E,topk", [(8, 70, 64), (2, 300, 20), (1, 1024, 16), (1, 1025, 16)])
+def test_layer_many_experts(T, E, topk):
+    """Routers of 4 and 16 experts a lane, 512 pairs, and more experts than the two kernels take."""
+    say(f"layer E={E} topk={topk} T={T}")
+    H, I = 256, 128
+    gu, dn = Experts(1, E, 2 * I, H, 2, 256), Experts(2, E, H, I, 2, 128)
+    x, logits = _x(T, T, H), _logits(T, T, E)
+    y, ids, _ = _run(x, logits, gu, dn, topk)
+    ref, rids, _ = _reference(x, logits, gu, dn, topk)
+    assert np.array_equal(ids, rids) and _norm_err(y, ref) <= 1e-3
+
+
+@pytest.mark.parametrize("H,T", [(9216, 8), (10240, 8), (16384, 1), (20480, 4)])
+def test_layer_long_rows(H, T):
+    """Rows around and beyond what the two kernels hold in LDS; output rows in more than 256 blocks."""
+    say(f"layer H={H} T={T}")
+    I, E, topk = 256, 3, 2
+    gu, dn = Experts(1, E, 2 * I, H, 2, 512), Experts(2, E, H, I, 2, 256)
+    x, logits = _x(T, T, H), _logits(T, T, E)
+    y, ids, _ = _run(x, logits, gu, dn, topk)
+    ref, rids, _ = _reference(x, logits, gu, dn, topk)
+    assert np.array_equal(ids, rids) and _norm_err(y, ref) <= 1e-3
+
+
+def test_layer_long_intermediate():
+    """h rows longer than a wave's share of LDS: K parts in kernel 2."""
+    for bits, I, T in ((2, 8192, 1), (2, 12800, 2), (4, 6144, 1)):
+        say(f"layer bits={bits} I={I} T={T}")
+        gu, dn = Experts(1, 2, 2 * I, 256, bits, 128), Experts(2, 2, 256, I, bits, 256)
+        x, logits = _x(T, T, 256), _logits(T, T, 2)
+        y, _, _ = _run(x, logits, gu, dn, 2)
+        ref, _, _ = _reference(x, logits, gu, dn, 2)
+        assert _norm_err(y, ref) <= 2e-3
+
+
 def test_layer_mixed_widths_and_more_tokens():
     say("layer W3 gate_up, W2 down; then W2 with 9 and 40 tokens")
     gu, dn = Experts(1, 6, 512, 512, 3, 256), Experts(2, 6, 512, 256, 2, 256)
