@@ -655,7 +655,8 @@ def cubic_linear_w8a8_workspace_bytes(M: int, K: int) -> int:
 def cubic_linear_w8a8(x: torch.Tensor, w: Int8Weight, bias: torch.Tensor | None = None,
                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                       out_dtype=torch.float32) -> torch.Tensor:
-    """cubic_gemm_w8a8 of bf16 or fp16 rows x [M][K], quantised per row on the way."""
+    """cubic_gemm_w8a8 of bf16 or fp16 rows x [M][K], quantised per row on the way (scale
+    amax * fp32(1 / 127), as torch's x.abs().amax(-1) / 127 on the device)."""
     if x.dtype not in _DT_IN:
         raise TypeError(f"x: expected bfloat16 or float16, got {x.dtype}")
     index = _first(x, "x")

@@ -20,6 +20,13 @@ namespace cubic {
 // rows, where the bound or the reciprocal fails), take the IEEE division.
 constexpr float kRneMagic = 12582912.0f;        // 1.5 * 2^23
 
+// A row's scale: fp32(amax / 127) (act_quant_int8_per_token), or with RECIP
+// fp32(amax * fp32(1 / 127)) (cubic_linear_w8a8).
+template <bool RECIP>
+__device__ __forceinline__ float scale_of(float amax) {
+  return RECIP ? amax * (1.0f / 127.0f) : __fdiv_rn(amax, 127.0f);
+}
+
 // Eight bf16 values (one 16-byte vector) to eight int8 codes.
 // Eight bf16 (or, with XF16, fp16) values of one 16-byte vector as fp32 (exact).
 template <bool XF16>

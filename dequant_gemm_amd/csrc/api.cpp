@@ -836,8 +836,9 @@ CUBIC_API int cubic_linear_w8a8(const void* x, int x_dtype, int64_t M, const cub
   if (!aligned16(workspace)) return CUBIC_ERR_ALIGN;
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(M) * w->K));
-  const int q = act_quant_int8_per_token_ex(x, x_dtype, M, w->K, xq, xs, stream);
-  if (q != CUBIC_OK) return q;
+  const hipError_t q = launch_act_quant(static_cast<const uint16_t*>(x), x_dtype == CUBIC_DTYPE_F16, M, w->K, xq, xs,
+                                        static_cast<hipStream_t>(stream), true);
+  if (q != hipSuccess) return CUBIC_ERR_HIP;
   p.xq = xq;
   p.xs = xs;
   return hip_status(launch_w8a8(p, static_cast<hipStream_t>(stream)));

@@ -105,12 +105,13 @@ __global__ __launch_bounds__(256) void k_dequant(const uint32_t* __restrict__ st
 }
 
 // Row maximum over the block's 256 threads; returns sx, written by thread 0.
+template <bool RECIP>
 __device__ __forceinline__ float row_scale(float amax, float* red, float* xs_m) {
   amax = wave_max(amax);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
   __syncthreads();
   amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float sx = __fdiv_rn(amax, 127.0f);
+  const float sx = scale_of<RECIP>(amax);
   if (threadIdx.x == 0) *xs_m = sx;
   return sx;
 }
@@ -118,7 +119,7 @@ __device__ __forceinline__ float row_scale(float amax, float* red, float* xs_m) 
 // One 256-thread block per row. V > 0: the row (at most 256 * V vectors of 8)
 // is read once into registers, all of its loads in flight together. V == 0:
 // rows of any length, two passes (the second hits L2).
-template <int V, bool XF16>
+template <int V, bool XF16, bool RECIP>
 __global__ __launch_bounds__(256) void k_act_quant(const uint16_t* __restrict__ x, int64_t K,
                                                    int8_t* __restrict__ xq,
                                                    float* __restrict__ xs) {
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(256) void k_act_quant(const uint16_t* __restrict__ 
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) amax = absmax8<XF16>(v[j], amax);
-    const float sx = row_scale(amax, red, xs + m);
+    const float sx = row_scale<RECIP>(amax, red, xs + m);
     const bool fast = sx >= 0x1p-100f && sx <= 0x1p100f;
     const float rcp = __builtin_amdgcn_rcpf(sx);
 #pragma unroll
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(256) void k_act_quant(const uint16_t* __restrict__ 
     }
   } else {
     for (int64_t i = tid; i < nvec; i += 256) amax = absmax8<XF16>(rv[i], amax);
-    const float sx = row_scale(amax, red, xs + m);
+    const float sx = row_scale<RECIP>(amax, red, xs + m);
     const bool fast = sx >= 0x1p-100f && sx <= 0x1p100f;
     const float rcp = __builtin_amdgcn_rcpf(sx);
     for (int64_t i = tid; i < nvec; i += 256) qv[i] = quant8<XF16>(rv[i], sx, rcp, fast);
@@ -325,17 +326,18 @@ hipError_t launch_dequant(const uint8_t* stream, const float* scales, const uint
   return hipGetLastError();
 }
 
-template <bool XF16>
+template <bool XF16, bool RECIP>
 static auto act_quant_kernel(int64_t K) {
   // registers per thread: the row's vectors over 256 threads, in steps of powers of two
   const int64_t per = (K / 8 + 255) / 256;
-  return per <= 1 ? k_act_quant<1, XF16> : per <= 2 ? k_act_quant<2, XF16> : per <= 4 ? k_act_quant<4, XF16>
-                  : per <= 8 ? k_act_quant<8, XF16> : k_act_quant<0, XF16>;
+  return per <= 1 ? k_act_quant<1, XF16, RECIP> : per <= 2 ? k_act_quant<2, XF16, RECIP>
+         : per <= 4 ? k_act_quant<4, XF16, RECIP> : per <= 8 ? k_act_quant<8, XF16, RECIP> : k_act_quant<0, XF16, RECIP>;
 }
 
 hipError_t launch_act_quant(const uint16_t* x, bool xf16, int64_t M, int64_t K, int8_t* xq, float* xs,
-                            hipStream_t st) {
-  auto kern = xf16 ? act_quant_kernel<true>(K) : act_quant_kernel<false>(K);
+                            hipStream_t st, bool recip) {
+  auto kern = xf16 ? (recip ? act_quant_kernel<true, true>(K) : act_quant_kernel<true, false>(K))
+                   : (recip ? act_quant_kernel<false, true>(K) : act_quant_kernel<false, false>(K));
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(M)), dim3(256), 0, st, x, K, xq, xs);
   return hipGetLastError();
 }

@@ -100,8 +100,9 @@ hipError_t launch_encode(const float* w, int64_t N, int64_t K, int bits, int gro
 int fit_max_group();
 hipError_t launch_fit(const float* w, int64_t N, int64_t K, int bits, int group, int8_t* codes,
                       float* scales, uint16_t* shapes, float* loss, hipStream_t st);
+// recip: the row scale is amax * fp32(1 / 127) instead of fp32(amax / 127)
 hipError_t launch_act_quant(const uint16_t* x, bool xf16, int64_t M, int64_t K, int8_t* xq, float* xs,
-                            hipStream_t st);
+                            hipStream_t st, bool recip = false);
 // xf16: the activations are fp16 (x, or xp with xback NULL on the multi-row path)
 hipError_t launch_gemv(const GemvParams& p, int bits, bool ink, bool xf16, hipStream_t st);
 // One activation row of 2-bit codes with groups of 256 or 512 and at most 16

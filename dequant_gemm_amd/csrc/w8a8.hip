@@ -151,7 +151,7 @@ __global__ __launch_bounds__(1024) void k_w8a8_rows(RowsParams p) {
         float a = 0.0f;
 #pragma unroll
         for (int k = 0; k < kRowsWaves; ++k) a = fmaxf(a, s_red[m * kRowsWaves + k]);
-        const float sx = __fdiv_rn(a, 127.0f);
+        const float sx = scale_of<true>(a);
         qscale[m] = sx;
         const bool fast = sx >= 0x1p-100f && sx <= 0x1p100f;
         const uint2 c = quant8<XF16>(v[m], sx, __builtin_amdgcn_rcpf(sx), fast);

@@ -423,11 +423,16 @@ typedef struct cubic_weight_i8 {
  * M == 0 or N == 0 is a no-op. */
 int cubic_gemm_w8a8(const int8_t* xq, const float* x_scale, int64_t M, const cubic_weight_i8* w,
                     const float* bias, void* y, int y_dtype, cubic_stream_t stream);
-/* The same product of bf16 or fp16 activations x [M][K], quantised on the way:
- * bit for bit act_quant_int8_per_token(_ex) followed by cubic_gemm_w8a8. Up to four
- * rows of K <= 8192 are quantised inside the product's kernel and need no workspace;
- * others pass through the workspace (cubic_linear_w8a8_workspace_bytes: xq, then
- * x_scale, each rounded up to 256 bytes). */
+/* The same product of bf16 or fp16 activations x [M][K], quantised per row on the way:
+ * amax = max |x[m][:]|, x_scale[m] = fp32(amax * fp32(1 / 127)), xq = clamp(rint(fp32(x /
+ * x_scale[m])), -127, 127), ties to even; a zero row gives scale 0 and codes 0. This is
+ * the rule that a torch program's x.abs().amax(-1) / 127 follows on the device, where a
+ * division by a constant is a product with its reciprocal; act_quant_int8_per_token
+ * divides, so its scale may differ in the last bit, and a code where x / x_scale then
+ * falls on the other side of a half. The result equals cubic_gemm_w8a8 of these xq and
+ * x_scale bit for bit. Up to four rows of K <= 8192 are quantised inside the product's
+ * kernel and need no workspace; others pass through the workspace
+ * (cubic_linear_w8a8_workspace_bytes: xq, then x_scale, each rounded up to 256 bytes). */
 size_t cubic_linear_w8a8_workspace_bytes(int64_t M, int64_t K);
 int cubic_linear_w8a8(const void* x, int x_dtype, int64_t M, const cubic_weight_i8* w, const float* bias,
                       void* y, int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream);

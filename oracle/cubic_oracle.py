@@ -62,7 +62,7 @@ __all__ = [
     "level_numerators", "levels", "dequant", "gemm_a16",
     "act_quant", "carrier_table", "carrier_codes", "gemm_a8", "moe_a16", "moe_a8",
     "format_levels", "dequant_f32", "encode", "bf16_rne", "silu_mul", "moe_mlp_hidden", "moe_mlp", "moe_mlp_a8",
-    "moe_topk", "moe_layer", "gemm_w8a8",
+    "moe_topk", "moe_layer", "gemm_w8a8", "quant_w8a8",
     "FIT_CLIP_STEPS", "fit_is_monotone", "fit_shape_candidates", "f64_to_f16_bits", "fit_group_sse", "fit",
 ]
 
@@ -779,3 +779,12 @@ def gemm_w8a8(xq: np.ndarray, sx: np.ndarray, wq: np.ndarray, sw: np.ndarray, bi
     I = np.asarray(xq, dtype=np.int64) @ np.asarray(wq, dtype=np.int64).T
     y = I.astype(np.float64) * np.asarray(sw, dtype=np.float64)[None, :] * np.asarray(sx, dtype=np.float64)[:, None]
     return y if bias is None else y + np.asarray(bias, dtype=np.float64)[None, :]
+
+
+def quant_w8a8(x: np.ndarray):
+    """Rows of float32 values (exact bf16 or fp16 numbers) -> (int8 codes, float32 scales) by the int8
+    product's own rule: scale fp32(amax * fp32(1 / 127)), code rint(fp32(x / scale)), ties to even."""
+    x = np.asarray(x, dtype=np.float32)
+    s = np.abs(x).max(axis=1) * np.float32(1.0 / 127.0)
+    q = np.rint(x / np.where(s > 0, s, np.float32(1.0))[:, None])
+    return np.clip(q, -127, 127).astype(np.int8), s

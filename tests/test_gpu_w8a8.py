@@ -85,13 +85,33 @@ def test_linear_equals_quantiser_then_product(M, N, K, dtype):
         x[2] *= 1e-38 if dtype == torch.bfloat16 else 1e-6
     x = x.to(dtype)
     _, _, w, b = _data(K, M, N, K, True)
-    xq, sx = cq.act_quant_int8_per_token(x)
+    xq, sx = (torch.from_numpy(v).to(DEV) for v in oracle.quant_w8a8(x.float().cpu().numpy()))
+    near = cq.act_quant_int8_per_token(x)[1]          # divides instead: the last bit may differ
+    assert bool(((near - sx).abs() <= 2.0 ** -23 * sx).all())
     for bias in (b, None):
         for od in (torch.float32, torch.bfloat16):
             want = cq.cubic_gemm_w8a8(xq, sx, w, bias=bias, out_dtype=od)
             got = cq.cubic_linear_w8a8(x, w, bias=bias, out_dtype=od)
             assert torch.equal(got.view(torch.int16), want.view(torch.int16))
     _check(xq, sx, w, b)
+
+
+@pytest.mark.parametrize("M", [3, 700])
+def test_linear_codes_at_halves(M):
+    """Rows whose values lie at exact halves of the scale's steps (x = amax (2 n + 1) / 254): the codes
+    follow the reciprocal rule and equal those of torch's quotients on the device."""
+    say(f"w8a8 linear at halves M={M}")
+    g = torch.Generator(device=DEV).manual_seed(M)
+    K, N = 264, 40
+    amax = (torch.randint(128, 256, (M, 1), generator=g, device=DEV) * 2.0 ** torch.randint(-9, 9, (M, 1), generator=g, device=DEV))
+    x = (amax * (2 * torch.randint(-64, 64, (M, K), generator=g, device=DEV) + 1) / 254).to(torch.bfloat16)
+    x[:, 0] = amax[:, 0].to(torch.bfloat16)
+    x[:, 1] = (amax[:, 0] / 2).to(torch.bfloat16)
+    xq, sx = (torch.from_numpy(v).to(DEV) for v in oracle.quant_w8a8(x.float().cpu().numpy()))
+    ts = x.float().abs().amax(dim=1) / 127.0
+    assert torch.equal(ts, sx) and torch.equal(torch.round(x.float() / ts[:, None]).to(torch.int8), xq)
+    _, _, w, b = _data(M, M, N, K, True)
+    assert torch.equal(cq.cubic_linear_w8a8(x, w, bias=b), cq.cubic_gemm_w8a8(xq, sx, w, bias=b))
 
 
 def test_large_shapes_sampled():
@@ -155,7 +175,7 @@ def test_weight_quantised_by_the_same_rule_and_shared_expert():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
     # against float64 on the quantised weights
-    xq, sx = cq.act_quant_int8_per_token(xs[0])
+    xq, sx = (torch.from_numpy(v).to(DEV) for v in oracle.quant_w8a8(xs[0].float().cpu().numpy()))
     gu = oracle.gemm_w8a8(*_np(xq, sx, up.codes, up.scales))
     h = gu[:, :I] / (1 + np.exp(-gu[:, :I])) * gu[:, I:]
     dense = down.codes.cpu().numpy().astype(np.float64) * down.scales.cpu().numpy().astype(np.float64)[:, None]

@@ -29,6 +29,26 @@ def test_oracle_against_rationals():
             assert abs(Fraction(float(y[m, n])) - ref) <= abs(ref) * Fraction(1, 2 ** 50) + Fraction(1, 2 ** 60)
 
 
+def test_oracle_quantiser():
+    """The rule by rationals: one rounding for the scale, one for each quotient, ties to even."""
+    rn32 = lambda v: np.float32(float(v))                    # exact products of two fp32 numbers fit a double
+    inv = np.float32(1.0 / 127.0)
+    assert inv == np.float32(float(Fraction(1, 127)))
+    rng = np.random.default_rng(2)
+    x = (rng.integers(-255, 256, (20, 24)) * 2.0 ** rng.integers(-6, 6, (20, 1))).astype(np.float32)
+    x[3] = 0
+    q, s = oracle.quant_w8a8(x)
+    for m in range(20):
+        amax = max(Fraction(float(abs(v))) for v in x[m])
+        assert s[m] == rn32(amax * Fraction(float(inv)))
+        for k in range(24):
+            if s[m] == 0:
+                assert q[m, k] == 0
+                continue
+            quot = np.float32(float(x[m, k]) / float(s[m]))  # 53 bits hold enough of the quotient to round once more
+            assert q[m, k] == max(-127, min(127, round(Fraction(float(quot)))))
+
+
 def test_refusals():
     lib = cq.load_library()
     call = lambda w=_w(), M=4, xq=P16, xs=P16, b=None, y=P16, yd=0: lib.cubic_gemm_w8a8(
