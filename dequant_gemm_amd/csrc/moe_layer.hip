@@ -25,6 +25,14 @@
 // (pair, K part) per wave at a time, so the router-weighted sum never leaves the
 // workgroup: no atomics, and the order of the sums does not depend on timing.
 //
+// Measured (hidden 7168, intermediate 3 K, G512, on one card whose large copy runs at
+// 5.1 TB/s): one token through 16 of 64 experts, 281 MB: kernel 1 42 us (8 us until the
+// first load is issued: router, splitting, lists; then 5.7 TB/s), kernel 2 21 us
+// (5.9 TB/s while streaming), 56-64 us together; four tokens through about 52 of 128
+// experts, 930 MB: 132 + 63 us. HBM traffic is 1.00 of the codes and scales. Against
+// loads in operand order, a barrier a round and seven steps in flight, the first version,
+// kernel 1 took 62 us and kernel 2 26.
+//
 // 3- and 4-bit codes run on the same two kernels with table levels (CodesWide); wider
 // codes, more tokens and shapes beyond the kernels' LDS run as the router kernel
 // followed by the routed MLP step (moe.hip).

@@ -16,9 +16,21 @@
 // are quantised by every workgroup itself, beside its first weight loads, which saves a
 // launch.
 //
-// k_w8a8_tile (more rows; bound by the int8 MFMA): tiles of 64 MB x 64 NB, four waves
-// with 32 MB x 32 NB each, both operands from a ring of four LDS stages of 64 codes
-// filled by direct global-to-LDS loads.
+// Measured: 6144 x 7168, one bf16 row: 44.1 MB in 9.8-10.2 us (4.4 TB/s; a large copy
+// runs at 5.1); 7168 x 2048, 64 rows: 9.7 us, where the launch, the chunks' round trips
+// and the join of sixteen waves' sums count, not the 3 us of the weight's bytes.
+//
+// k_w8a8_tile (more rows; bound by the int8 MFMA, at the clock that its power allows):
+// eight waves a tile of 256 rows (four a smaller one), both operands in two LDS stages of
+// 64 codes, filled through registers two stages ahead, so that a stage costs one barrier;
+// the result leaves through LDS in 16-byte pieces. Measured: 4096 x 6144 x 7168 in
+// 181-220 us by box and clock (1.64-2.0 POP/s; the library's int8 product 168-184 us on
+// the same boxes), 151 us on zeros (less power, a higher clock; library 141). MFMA busy
+// 54 % of the cycles. Not faster: four waves with direct global-to-LDS stages (192-225)
+// or through registers (196-230), 256 x 256 tiles (209; a second, half-empty round of
+// tiles), 128 x 192 tiles two to a compute unit (227), fragment reads moved ahead, wave
+// priorities and workgroups at rotated K offsets (all within 2 us). Faster than 2-byte
+// stores from the MFMA layout: 30 us.
 #include <algorithm>
 #include <utility>
 
@@ -302,9 +314,7 @@ __global__ __launch_bounds__(64 * Shape::W) void k_w8a8_tile(W8Params p) {
   // ---- stage loads: wave w takes rows 16 (W i + w) .. + 15 of A, then of B; lane l
   // loads the 16-byte piece l % 4 of row l / 4 (64 contiguous bytes a lane quad) into
   // registers and writes it to slot piece ^ (row / 4 % 4) of the row (any 16 rows read
-  // at one piece hit all banks). Direct global-to-LDS loads in place of the registers
-  // keep the address unit busy twice as long (32 against 64 bytes a cycle): 192 us
-  // against the 160 below for 4096 x 6144 x 7168. ----
+  // at one piece hit all banks) ----
   const uint32_t abytes = static_cast<uint32_t>(min(static_cast<int64_t>(TM), p.M - m0)) * static_cast<uint32_t>(K);
   const uint32_t bbytes = static_cast<uint32_t>(min(static_cast<int64_t>(TN), p.N - n0)) * static_cast<uint32_t>(K);
   const __amdgpu_buffer_rsrc_t ars = w8_rsrc(p.xq + m0 * K, abytes);
