@@ -275,6 +275,7 @@ __device__ __forceinline__ void wide_step(const uint32_t (*w)[F::DW], const floa
   using Dec = typename F::Dec;
   if (g != gtab) {                             // wave-uniform
     gtab = g;
+    wave_lds_order();                          // the old table is read
 #pragma unroll
     for (int i = 0; i < NT; ++i) build_table<Dec>(tab + i * (F::kTable / 2), nl, kq, sh[i]);
     wave_lds_order();

@@ -17,8 +17,9 @@
 // before the first value is used.
 //
 // Measured: one token, 896 experts, biased sigmoids: 4.9 us as a kernel of its own (an
-// empty launch takes 1.7; with the loads issued one after another it took 16); 4096 tokens 11.5 us (15 MB: 3 us at the copy rate; the fp32 keys and counts of
-// 16 experts a lane bound it, 32 us in the first version).
+// empty launch takes 1.7; with the loads issued one after another it took 16); 4096
+// tokens 11.5 us (15 MB: 3 us at the copy rate; the fp32 keys and counts of 16 experts a
+// lane bound it, 32 us in the first version).
 #pragma once
 #include "common.h"
 
