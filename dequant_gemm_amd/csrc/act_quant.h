@@ -27,7 +27,17 @@ __device__ __forceinline__ float scale_of(float amax) {
   return RECIP ? amax * (1.0f / 127.0f) : __fdiv_rn(amax, 127.0f);
 }
 
-// Eight bf16 values (one 16-byte vector) to eight int8 codes.
+// The larger of two magnitudes. RECIP: of their bits, so that a NaN is the largest and
+// reaches the row's scale; else a NaN is passed over.
+template <bool RECIP>
+__device__ __forceinline__ float larger(float a, float b) {
+  if constexpr (RECIP) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+  } else {
+    return fmaxf(a, b);
+  }
+}
+
 // Eight bf16 (or, with XF16, fp16) values of one 16-byte vector as fp32 (exact).
 template <bool XF16>
 __device__ __forceinline__ void unpack8(const u32x4& v, float* xv) {
@@ -44,6 +54,7 @@ __device__ __forceinline__ void unpack8(const u32x4& v, float* xv) {
   }
 }
 
+// Their eight int8 codes.
 template <bool XF16>
 __device__ __forceinline__ uint2 quant8(const u32x4& v, float sx, float rcp, bool fast) {
   float xv[8];
@@ -77,13 +88,21 @@ __device__ __forceinline__ uint2 quant8(const u32x4& v, float sx, float rcp, boo
   return make_uint2(lo, hi);
 }
 
-template <bool XF16>
+template <bool XF16, bool RECIP>
 __device__ __forceinline__ float absmax8(const u32x4& v, float a) {
   float xv[8];
   unpack8<XF16>(v, xv);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(xv[e]));
+  for (int e = 0; e < 8; ++e) a = larger<RECIP>(a, fabsf(xv[e]));
   return a;
+}
+
+// The largest of the wave's magnitudes, in every lane.
+template <bool RECIP>
+__device__ __forceinline__ float wave_larger(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = larger<RECIP>(v, __shfl_xor(v, o, 64));
+  return v;
 }
 
 }  // namespace cubic

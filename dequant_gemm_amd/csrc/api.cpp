@@ -665,6 +665,7 @@ CUBIC_API int cubic_moe_grouped_gemm_static(const uint16_t* x_bf16, int64_t T, c
 namespace {
 constexpr int kRouterMaxE = 2048;            // 32 experts per lane of the router's wave
 constexpr int kRouterTopk = 64;              // one lane per taken expert
+constexpr int64_t kRouterMaxT = 1 << 25;     // one wave per token: a launch takes below 2^32 threads
 
 int check_router(const cubic_router* r, int64_t T) {
   if (!r) return CUBIC_ERR_NULL;
@@ -673,7 +674,7 @@ int check_router(const cubic_router* r, int64_t T) {
   if (r->logits_dtype != CUBIC_DTYPE_F32 && r->logits_dtype != CUBIC_DTYPE_BF16 && r->logits_dtype != CUBIC_DTYPE_F16)
     return CUBIC_ERR_DTYPE;
   if (r->score != CUBIC_SCORE_SOFTMAX && r->score != CUBIC_SCORE_SIGMOID) return CUBIC_ERR_OPTION;
-  if (T > INT32_MAX / 2 / r->topk) return CUBIC_ERR_SHAPE;
+  if (T > kRouterMaxT || T > INT32_MAX / 2 / r->topk) return CUBIC_ERR_SHAPE;
   if (T > 0) {
     if (!r->logits) return CUBIC_ERR_NULL;
     if (!aligned16(r->logits) || !aligned16(r->bias)) return CUBIC_ERR_ALIGN;
@@ -773,11 +774,12 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
 
 namespace {
 constexpr int64_t kW8MaxK = 131064;          // K * 128 * 128 below 2^31
+constexpr int64_t kW8MaxRows = (1 << 24) - 1;   // 256 threads a row of x: a launch takes below 2^32
 
 int check_weight_i8(const cubic_weight_i8* w, int64_t M) {
   if (!w) return CUBIC_ERR_NULL;
   if (M < 0 || w->N < 0 || w->K <= 0 || w->K % 8 != 0 || w->K > kW8MaxK) return CUBIC_ERR_SHAPE;
-  if (M > INT32_MAX / 2 || w->N > INT32_MAX / 2) return CUBIC_ERR_SHAPE;
+  if (M > kW8MaxRows || w->N > kW8MaxRows) return CUBIC_ERR_SHAPE;
   if (M > 0 && w->N > 0) {
     if (!w->codes || !w->scales) return CUBIC_ERR_NULL;
     if (!aligned16(w->codes) || !aligned16(w->scales)) return CUBIC_ERR_ALIGN;

@@ -107,10 +107,10 @@ __global__ __launch_bounds__(256) void k_dequant(const uint32_t* __restrict__ st
 // Row maximum over the block's 256 threads; returns sx, written by thread 0.
 template <bool RECIP>
 __device__ __forceinline__ float row_scale(float amax, float* red, float* xs_m) {
-  amax = wave_max(amax);
+  amax = wave_larger<RECIP>(amax);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
   __syncthreads();
-  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  amax = larger<RECIP>(larger<RECIP>(red[0], red[1]), larger<RECIP>(red[2], red[3]));
   const float sx = scale_of<RECIP>(amax);
   if (threadIdx.x == 0) *xs_m = sx;
   return sx;
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(256) void k_act_quant(const uint16_t* __restrict__ 
       v[j] = i < nvec ? rv[i] : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) amax = absmax8<XF16>(v[j], amax);
+    for (int j = 0; j < V; ++j) amax = absmax8<XF16, RECIP>(v[j], amax);
     const float sx = row_scale<RECIP>(amax, red, xs + m);
     const bool fast = sx >= 0x1p-100f && sx <= 0x1p100f;
     const float rcp = __builtin_amdgcn_rcpf(sx);
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256) void k_act_quant(const uint16_t* __restrict__ 
       if (i < nvec) qv[i] = quant8<XF16>(v[j], sx, rcp, fast);
     }
   } else {
-    for (int64_t i = tid; i < nvec; i += 256) amax = absmax8<XF16>(rv[i], amax);
+    for (int64_t i = tid; i < nvec; i += 256) amax = absmax8<XF16, RECIP>(rv[i], amax);
     const float sx = row_scale<RECIP>(amax, red, xs + m);
     const bool fast = sx >= 0x1p-100f && sx <= 0x1p100f;
     const float rcp = __builtin_amdgcn_rcpf(sx);

@@ -151,7 +151,7 @@ __global__ __launch_bounds__(1024) void k_w8a8_rows(RowsParams p) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       if (m < M) {
-        const float a = wave_max(absmax8<XF16>(v[m], 0.0f));
+        const float a = wave_larger<true>(absmax8<XF16, true>(v[m], 0.0f));
         if (lane == 0) s_red[m * kRowsWaves + wave] = a;
       }
     }
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(1024) void k_w8a8_rows(RowsParams p) {
       if (m < M) {
         float a = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kRowsWaves; ++k) a = fmaxf(a, s_red[m * kRowsWaves + k]);
+        for (int k = 0; k < kRowsWaves; ++k) a = larger<true>(a, s_red[m * kRowsWaves + k]);
         const float sx = scale_of<true>(a);
         qscale[m] = sx;
         const bool fast = sx >= 0x1p-100f && sx <= 0x1p100f;

@@ -365,7 +365,8 @@ int cubic_moe_mlp_a8(const uint16_t* x_bf16, int64_t T, const int32_t* topk_ids,
  * depend on fp32 rounding of the scores); weights are rounded to fp32 once.
  * logits: [T][E] in logits_dtype CUBIC_DTYPE_F32, _BF16 or _F16; bias fp32 [E] or
  * NULL; topk_ids int32 and topk_weights fp32 [T][topk]. 1 <= topk <= min(E, 64) and
- * E <= 2048 (CUBIC_ERR_SHAPE); CUBIC_ERR_OPTION for another score. T == 0 is a no-op. */
+ * E <= 2048, T <= 2^25 and T * topk < 2^30 (CUBIC_ERR_SHAPE); CUBIC_ERR_OPTION for another
+ * score. T == 0 is a no-op. */
 enum { CUBIC_SCORE_SOFTMAX = 0, CUBIC_SCORE_SIGMOID = 1 };
 typedef struct cubic_router {
   const void* logits;
@@ -420,12 +421,13 @@ typedef struct cubic_weight_i8 {
  * with the weight's scale, then the product with x_scale (one fused multiply-add where
  * a bias is given); the bf16 output rounds that once more. The result does not depend
  * on timing. bias fp32 [N] or NULL; y [M][N] in y_dtype CUBIC_DTYPE_F32 or _BF16.
- * M == 0 or N == 0 is a no-op. */
+ * M and N below 2^24; M == 0 or N == 0 is a no-op. */
 int cubic_gemm_w8a8(const int8_t* xq, const float* x_scale, int64_t M, const cubic_weight_i8* w,
                     const float* bias, void* y, int y_dtype, cubic_stream_t stream);
 /* The same product of bf16 or fp16 activations x [M][K], quantised per row on the way:
  * amax = max |x[m][:]|, x_scale[m] = fp32(amax * fp32(1 / 127)), xq = clamp(rint(fp32(x /
- * x_scale[m])), -127, 127), ties to even; a zero row gives scale 0 and codes 0. This is
+ * x_scale[m])), -127, 127), ties to even; a zero row gives scale 0 and codes 0, and a
+ * non-finite value makes its row of y non-finite. This is
  * the rule that a torch program's x.abs().amax(-1) / 127 follows on the device, where a
  * division by a constant is a product with its reciprocal; act_quant_int8_per_token
  * divides, so its scale may differ in the last bit, and a code where x / x_scale then

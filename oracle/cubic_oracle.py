@@ -783,7 +783,7 @@ def gemm_w8a8(xq: np.ndarray, sx: np.ndarray, wq: np.ndarray, sw: np.ndarray, bi
 
 def quant_w8a8(x: np.ndarray):
     """Rows of float32 values (exact bf16 or fp16 numbers) -> (int8 codes, float32 scales) by the int8
-    product's own rule: scale fp32(amax * fp32(1 / 127)), code rint(fp32(x / scale)), ties to even."""
+    product's own rule: scale fp32(amax * fp32(1 / 127)), code rint(fp32(x / scale)), ties to even. Finite rows."""
     x = np.asarray(x, dtype=np.float32)
     s = np.abs(x).max(axis=1) * np.float32(1.0 / 127.0)
     q = np.rint(x / np.where(s > 0, s, np.float32(1.0))[:, None])

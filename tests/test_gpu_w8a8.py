@@ -53,7 +53,8 @@ def test_rows_kernel(M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(65, 1, 8), (65, 64, 64), (128, 129, 72), (100, 4097, 136), (257, 300, 1000),
                                    (192, 1003, 1928), (513, 1030, 264), (1000, 2050, 48), (300, 6000, 200),
-                                   (2049, 513, 328), (4096, 1537, 64), (1025, 3073, 24)])
+                                   (2049, 513, 328), (4096, 1537, 64), (1025, 3073, 24), (389, 28670, 136),
+                                   (517, 12285, 72), (515, 14330, 200)])
 def test_tile_kernel(M, N, K):
     say(f"w8a8 tiles M={M} N={N} K={K}")
     _check(*_data(M + N, M, N, K, bias=bool(N & 1)))
@@ -112,6 +113,29 @@ def test_linear_codes_at_halves(M):
     assert torch.equal(ts, sx) and torch.equal(torch.round(x.float() / ts[:, None]).to(torch.int8), xq)
     _, _, w, b = _data(M, M, N, K, True)
     assert torch.equal(cq.cubic_linear_w8a8(x, w, bias=b), cq.cubic_gemm_w8a8(xq, sx, w, bias=b))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("M,K", [(1, 64), (4, 4104), (6, 1928), (70, 136), (3, 8200), (5, 20000)])
+def test_linear_non_finite_rows(M, K, bad):
+    """A non-finite value makes its row non-finite, and no other row changes."""
+    say(f"w8a8 linear non-finite M={M} K={K} {bad}")
+    g = torch.Generator(device=DEV).manual_seed(K)
+    _, _, w, b = _data(K, M, 50, K, True)
+    x = torch.randn((M, K), generator=g, device=DEV).to(torch.bfloat16)
+    want = cq.cubic_linear_w8a8(x, w, bias=b)
+    for dtype in (torch.bfloat16, torch.float16):
+        for row, col in ((0, 0), (M - 1, K - 1), (M // 2, K // 2 + 3)):
+            z = x.clone()
+            z[row, col] = bad
+            for od in (torch.float32, torch.bfloat16):
+                y = cq.cubic_linear_w8a8(z.to(dtype), w, bias=b, out_dtype=od)
+                assert not bool(y[row].isfinite().any())
+                others = [m for m in range(M) if m != row]
+                if dtype == torch.bfloat16 and od == torch.float32:
+                    assert torch.equal(y[others], want[others])
+                else:
+                    assert bool(y[others].isfinite().all())
 
 
 def test_large_shapes_sampled():

@@ -76,6 +76,7 @@ def test_topk_refusals():
     assert call(_router(E=128, topk=65)) == ERR_SHAPE
     assert call(_router(), T=-1) == ERR_SHAPE
     assert call(_router(), T=1 << 40) == ERR_SHAPE
+    assert call(_router(), T=(1 << 25) + 1) == ERR_SHAPE
     assert call(_router(dtype=3)) == ERR_DTYPE
     assert call(_router(score=2)) == ERR_OPTION
     assert call(_router(logits=0)) == ERR_NULL

@@ -57,6 +57,7 @@ def test_refusals():
     for K in (0, -8, 12, 131072):
         assert call(_w(K=K)) == ERR_SHAPE
     assert call(_w(N=-1)) == ERR_SHAPE and call(M=-1) == ERR_SHAPE and call(M=1 << 31) == ERR_SHAPE
+    assert call(M=1 << 24) == ERR_SHAPE and call(_w(N=1 << 24)) == ERR_SHAPE
     assert call(yd=2) == ERR_DTYPE
     assert call(M=0) == OK and call(_w(N=0, codes=0)) == OK             # no-ops
     assert call(_w(codes=0)) == ERR_NULL and call(xq=None) == ERR_NULL and call(xs=None) == ERR_NULL
