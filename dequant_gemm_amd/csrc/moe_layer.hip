@@ -92,10 +92,12 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a < __builtin_inff() ? a : 0.0f;
 }
 
-// Place of code c (0..31) of a 32-code chunk among the chunk's 32 operand slots:
-// dword d of the decoded chunk holds the even (d even) or odd codes of code
-// word d / 2.
-__device__ __forceinline__ int code_slot(int c) { return 16 * (c >> 4) + 8 * (c & 1) + ((c & 15) >> 1); }
+// Place of code c (0..31) of a 32-code chunk among the chunk's 32 operand bytes. 2-bit
+// codes: dword d of the decoded chunk holds the even (d even) or odd codes of code word
+// d / 2; wider codes: the even or odd ones of codes 8 (d / 2) .. + 7.
+__device__ __forceinline__ int code_slot(int c, bool wide) {
+  return 16 * (c >> 4) + (wide ? 8 * ((c & 15) >> 3) + 4 * (c & 1) + ((c & 7) >> 1) : 8 * (c & 1) + ((c & 15) >> 1));
+}
 // Place of 32-chunk b of a row: with SPL = 2 a lane's 16-byte load holds two
 // chunks, which feed two MFMAs (a macro step of 256 codes, lane group kq takes
 // chunks 2 kq and 2 kq + 1, MFMA h the h-th of each).
@@ -105,25 +107,103 @@ __device__ __forceinline__ int chunk_place(int b) {
 }
 
 // ---- the two kinds of codes ---------------------------------------------------
-// 2-bit codes: e2m1 nibbles against the activations' e4m3 halves (rows 2 t and 2 t + 1
-// of the MFMA's activations for token t).
+// Both multiply the activations' e4m3 halves (rows 2 t and 2 t + 1 of the MFMA for token
+// t). 2-bit codes are e2m1 nibbles; a lane's operand is one or two 32-code chunks.
 template <int SPL_>
 struct Codes2 {
   static constexpr bool kWide = false;
-  static constexpr int kBits = 2, SPL = SPL_, DW = 2 * SPL_, kTable = 0;
-  static constexpr int kTokens = 2;            // tokens whose sums a lane holds
+  static constexpr int kBits = 2, SPL = SPL_;
+  static constexpr int DW = 2 * SPL_, W = DW;  // dwords of a lane's loads, and of its operand codes
+  static constexpr int kPiece = 4 * DW;        // bytes between the loads of neighbouring lanes
 };
-// 3- and 4-bit codes: levels as two bf16 halves (16 significant bits) from a table of
-// the row's 2^B levels in LDS (decode.h), against the bf16 activations as they are (row
-// t for token t); two bf16 MFMAs a fragment. A wave builds a tile's table when a step
-// enters another group.
+// 3- and 4-bit codes j = -M .. K (M = 2^(B-1), K = M - 1): with n = |j| and c = 1 - a - b
+// their level s (a t + b t |t| + c t^3), t = j / K, is a sum of three fixed odd functions
+//   p1 = j,  p2 = +-n (M - n),  p3 = +-n (M - n) (n - M / 2):
+//   level = s ((a / K + M b / K^2 + M^2 c / K^3) p1 - (b / K^2 + 1.5 M c / K^3) p2 - c / K^3 p3)
+// whose products with the activations' halves MFMAs sum exactly: the values are e4m3
+// numbers (four significant bits), looked up four at a time by byte permutes in registers,
+// and the coefficients of a group enter with its scale. A table of a group's levels costs
+// its building and an LDS read a code.
+// 4 bits: a code is -8 sign + l. The low bits l of j and of -j add up to 8, where p2 is
+// even and p3 odd, so both need only l, and p2 the sign. p3 + l has four significant bits
+// (p3 has not); l and the unsigned code u = 8 sign + l are e4m3 numbers as they stand (the
+// bytes 0 .. 15 mean 2^-9 of that), and p1 = 2 l - u: twelve operations for eight codes and
+// four MFMAs. (Whole 16-entry look-ups of three functions took 26 and three; 4 bits, 7168 x
+// 2 K, 8 tokens: 419 us.) 3 bits: three look-ups in eight entries.
+// The MFMA wants codes 16 kq .. + 15 and 64 + 16 kq .. + 15 of a step in lane group kq.
+// 4 bits: loaded as 8-byte pieces of either half; 3 bits: as 12-byte chunks of 32 codes,
+// of which two lane groups take a half each.
 template <int B>
 struct CodesWide {
   static constexpr bool kWide = true;
-  static constexpr int kBits = B, SPL = 1, DW = B, kTable = 16 * (1 << B) * 4;   // table bytes of a tile
-  static constexpr int kTokens = 4;
-  using Dec = DecodeTableSplit<B>;
+  static constexpr int kBits = B, SPL = 1;
+  static constexpr int DW = B, W = 4;
+  static constexpr int kPiece = B == 4 ? 8 : 12;
+  static constexpr int M = 1 << (B - 1), K = M - 1;
+  static constexpr int kSums = B == 4 ? 4 : 3; // MFMAs a step
 };
+
+// An integer of at most four significant bits as an e4m3 number.
+constexpr uint32_t e4m3_int(int v) {
+  uint32_t m = static_cast<uint32_t>(v < 0 ? -v : v), e = 0;
+  if (m == 0) return 0u;
+  while (m >= 16u) { m >>= 1; ++e; }           // (exact: the bits shifted out are zero)
+  while (m < 8u) { m <<= 1; --e; }
+  return ((e + 10u) << 3 | (m & 7u)) | (v < 0 ? 0x80u : 0u);   // m 2^e = m/8 2^(e+3), bias 7
+}
+// Four bytes of f(j0) .. f(j0 + 3).
+template <class Fn>
+constexpr uint32_t e4m3_bytes(Fn f, int j0) {
+  uint32_t v = 0;
+  for (int i = 0; i < 4; ++i) v |= e4m3_int(f(j0 + i)) << (8 * i);
+  return v;
+}
+// The lane's 32 operand codes (w: 16 and 16; the even and odd ones of eight in turn) as
+// bytes. 4 bits: b = l, u, p2, p3 + l; 3 bits: p1, p2, p3.
+template <int B>
+__device__ __forceinline__ void poly_decode(const uint32_t* w, i32x8* b) {
+  if constexpr (B == 4) {
+    constexpr auto p2 = [](int l) { return l * (8 - l); };
+    constexpr auto p3l = [](int l) { return l * (8 - l) * (l - 4) + l; };
+    constexpr uint32_t a0 = e4m3_bytes(p2, 0), a4 = e4m3_bytes(p2, 4), c0 = e4m3_bytes(p3l, 0), c4 = e4m3_bytes(p3l, 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {              // eight codes
+      const uint32_t v = w[u], vs = v >> 4;
+      const uint32_t le = v & 0x07070707u, lo = vs & 0x07070707u;
+      b[0][2 * u] = static_cast<int>(le);
+      b[0][2 * u + 1] = static_cast<int>(lo);
+      b[1][2 * u] = static_cast<int>(v & 0x0F0F0F0Fu);
+      b[1][2 * u + 1] = static_cast<int>(vs & 0x0F0F0F0Fu);
+      b[2][2 * u] = static_cast<int>(((v << 4) & 0x80808080u) | __builtin_amdgcn_perm(a4, a0, le));
+      b[2][2 * u + 1] = static_cast<int>((v & 0x80808080u) | __builtin_amdgcn_perm(a4, a0, lo));
+      b[3][2 * u] = static_cast<int>(__builtin_amdgcn_perm(c4, c0, le));
+      b[3][2 * u + 1] = static_cast<int>(__builtin_amdgcn_perm(c4, c0, lo));
+    }
+  } else {
+    // codes 0 .. 3 are their values, 4 .. 7 those less 8
+    constexpr auto sign = [](int j) { return j < 0 ? -1 : 1; };
+    constexpr auto p1 = [](int j) { return j; };
+    constexpr auto p2 = [sign](int j) { return j * (4 - sign(j) * j); };
+    constexpr auto p3 = [sign](int j) { return j * (4 - sign(j) * j) * (sign(j) * j - 2); };
+    constexpr uint32_t t[3][2] = {{e4m3_bytes(p1, 0), e4m3_bytes(p1, -4)},
+                                  {e4m3_bytes(p2, 0), e4m3_bytes(p2, -4)},
+                                  {e4m3_bytes(p3, 0), e4m3_bytes(p3, -4)}};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t* q = w + 2 * (u >> 1);    // 48 bits
+      const uint32_t v = (u & 1) ? __builtin_amdgcn_alignbit(q[1], q[0], 24) : q[0];
+      // fields of three bits at 0, 3, 6, 9 and 16, 19, 22, 25; then those of even and odd codes in bytes
+      const uint32_t y = (v & 0xFFFu) | ((v & 0xFFF000u) << 4);
+      const uint32_t se = (y & 0x00070007u) | ((y & 0x01C001C0u) << 2);
+      const uint32_t so = ((y >> 3) & 0x00070007u) | ((y & 0x0E000E00u) >> 1);
+#pragma unroll
+      for (int f = 0; f < 3; ++f) {
+        b[f][2 * u] = static_cast<int>(__builtin_amdgcn_perm(t[f][1], t[f][0], se));
+        b[f][2 * u + 1] = static_cast<int>(__builtin_amdgcn_perm(t[f][1], t[f][0], so));
+      }
+    }
+  }
+}
 
 // ---- a wave's stream of code tiles ------------------------------------------
 // NT tiles of 16 weight rows, macro steps of SPL * 128 codes, in blocks of PM
@@ -158,7 +238,11 @@ struct CodeStream {
   __device__ __forceinline__ void issue(const CodeSrc& src, const uint32_t* vcode, int t) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if constexpr (DW == 4) {
+      if constexpr (F::kBits == 4) {
+        const u32x2 v0 = __builtin_amdgcn_raw_buffer_load_b64(src.code, vcode[i], t * 64, 0);
+        const u32x2 v1 = __builtin_amdgcn_raw_buffer_load_b64(src.code, vcode[i], t * 64 + 32, 0);
+        cb[U][i][0] = v0.x; cb[U][i][1] = v0.y; cb[U][i][2] = v1.x; cb[U][i][3] = v1.y;
+      } else if constexpr (DW == 4) {
         const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.code, vcode[i], t * (4 * DW * 4), 0);
         cb[U][i][0] = v.x; cb[U][i][1] = v.y; cb[U][i][2] = v.z; cb[U][i][3] = v.w;
       } else if constexpr (DW == 3) {
@@ -195,19 +279,28 @@ struct CodeStream {
         if constexpr (F::kWide) ab[i][r] = abn[i][r];
       }
   }
-  // slot U in operand order: w[tile][dword], s[tile] and (wide codes) a | b in sh[tile];
-  // xaddr = 4 (4 nl + kq)
+  // slot U in operand order: w[tile][dword], s[tile] and (wide codes) a | b in sh[tile]
   template <int U>
-  __device__ __forceinline__ void take(int xaddr, int nl, uint32_t (*w)[DW], float* s, uint32_t* sh) {
+  __device__ __forceinline__ void take(int nl, int kq, uint32_t (*w)[F::W], float* s, uint32_t* sh) {
+    auto from = [](int lane, uint32_t v) {
+      return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(4 * lane, static_cast<int>(v)));
+    };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
+      if constexpr (F::kBits == 3) {
 #pragma unroll
-      for (int d = 0; d < DW; ++d)
-        w[i][d] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(xaddr, static_cast<int>(cb[U][i][d])));
-      s[i] = __uint_as_float(static_cast<uint32_t>(
-          __builtin_amdgcn_ds_bpermute(16 * nl + 4 * (U & 3), static_cast<int>(__float_as_uint(sc[i][U / 4])))));
-      if constexpr (F::kWide)
-        sh[i] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(16 * nl + 4 * (U & 3), static_cast<int>(ab[i][U / 4])));
+        for (int h = 0; h < 2; ++h) {          // chunk 2 h + kq / 2; its upper half for odd kq
+          const int l = 4 * nl + 2 * h + (kq >> 1);
+          const uint32_t d0 = from(l, cb[U][i][0]), d1 = from(l, cb[U][i][1]), d2 = from(l, cb[U][i][2]);
+          w[i][2 * h] = (kq & 1) ? __builtin_amdgcn_alignbit(d2, d1, 16) : d0;
+          w[i][2 * h + 1] = (kq & 1) ? d2 >> 16 : d1;
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < DW; ++d) w[i][d] = from(4 * nl + kq, cb[U][i][d]);
+      }
+      s[i] = __uint_as_float(from(4 * nl + (U & 3), __float_as_uint(sc[i][U / 4])));
+      if constexpr (F::kWide) sh[i] = from(4 * nl + (U & 3), ab[i][U / 4]);
     }
   }
 };
@@ -266,36 +359,52 @@ __device__ __forceinline__ void layer_step(const uint32_t (*w)[2 * SPL], const f
   }
 }
 
-// The same for wide codes: activation rows xr of bf16 values, the tiles' tables tab (of
-// group gtab; rebuilt when the step's group g is another), sums of tokens 4 kq + r.
-template <class F, int NT>
-__device__ __forceinline__ void wide_step(const uint32_t (*w)[F::DW], const float* sc, const uint32_t* sh,
-                                          const uint8_t* xr, int t, int g, int& gtab, uint16_t* tab, int nl, int kq,
-                                          float (*acc)[4]) {
-  using Dec = typename F::Dec;
-  if (g != gtab) {                             // wave-uniform
-    gtab = g;
-    wave_lds_order();                          // the old table is read
-#pragma unroll
-    for (int i = 0; i < NT; ++i) build_table<Dec>(tab + i * (F::kTable / 2), nl, kq, sh[i]);
-    wave_lds_order();
-  }
-  u32x4 a[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const u32x4*>(xr + (t * 128 + kq * 32 + 8 * j) * 2);
+// The same for wide codes, sh: the tiles' shapes a | b.
+template <int B, int NT>
+__device__ __forceinline__ void wide_step(const uint32_t (*w)[4], const float* sc, const uint32_t* sh, const uint8_t* xr,
+                                          const uint8_t* sr, int t, int kq, float (*acc)[2]) {
+  constexpr float K = CodesWide<B>::K, M = CodesWide<B>::M;
+  constexpr int NS = CodesWide<B>::kSums;
+  const int sx = sr[t * 4 + kq];
+  const u32x4 a0 = *reinterpret_cast<const u32x4*>(xr + t * 128 + 16 * kq);
+  const u32x4 a1 = *reinterpret_cast<const u32x4*>(xr + t * 128 + 64 + 16 * kq);
+  const i32x8 a = {static_cast<int>(a0.x), static_cast<int>(a0.y), static_cast<int>(a0.z), static_cast<int>(a0.w),
+                   static_cast<int>(a1.x), static_cast<int>(a1.y), static_cast<int>(a1.z), static_cast<int>(a1.w)};
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    uint32_t hi[16], lo[16];
-    Dec::decode(w[i], reinterpret_cast<const uint32_t*>(tab + i * (F::kTable / 2)) + nl * (1 << F::kBits),
-                Dec::swizzle(nl), hi, lo);
-    f32x4 part = {0.f, 0.f, 0.f, 0.f};
+    i32x8 b[NS];
+    poly_decode<B>(w[i], b);
+    f32x4 part[NS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      part = mfma16<true>(a[j], u32x4{hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]}, part);
-      part = mfma16<true>(a[j], u32x4{lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]}, part);
+    for (int f = 0; f < NS; ++f) {
+      constexpr f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      if (B == 4 && f < 2) {                   // (bytes of 2^-9)
+        part[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[f], zero, 0, 0, 0, sx, 0, 136);
+      } else {
+        part[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[f], zero, 0, 0, 0, sx, 0, 127);
+      }
     }
+    const float sa = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sh[i] & 0xffffu)));
+    const float sb = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sh[i] >> 16)));
+    const float c = (1.0f - sa - sb) * (1.0f / (K * K * K));
+    const float k1 = sc[i] * fmaf(M * M, c, fmaf(sb, M / (K * K), sa * (1.0f / K)));
+    const float k2 = sc[i] * -fmaf(1.5f * M, c, sb * (1.0f / (K * K)));
+    const float k3 = sc[i] * -c;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(sc[i], part[r], acc[i][r]);
+    for (int m = 0; m < 2; ++m) {
+      float p[NS];
+#pragma unroll
+      for (int f = 0; f < NS; ++f) p[f] = part[f][2 * m] + part[f][2 * m + 1];
+      if constexpr (B == 4) {
+        acc[i][m] = fmaf(k1, fmaf(2.0f, p[0], -p[1]), acc[i][m]);
+        acc[i][m] = fmaf(k2, p[2], acc[i][m]);
+        acc[i][m] = fmaf(k3, p[3] - p[0], acc[i][m]);
+      } else {
+        acc[i][m] = fmaf(k1, p[0], acc[i][m]);
+        acc[i][m] = fmaf(k2, p[1], acc[i][m]);
+        acc[i][m] = fmaf(k3, p[2], acc[i][m]);
+      }
+    }
   }
 }
 
@@ -379,32 +488,31 @@ struct LayerUpParams {
   Groups groups;           // steps per group
   int ks;                  // waves per tile (each a part of K)
   int batch;               // rounds between the joins of the waves' sums
-  int down_spl;            // operand order of h: chunks per lane and step of 2-bit down codes; 0: bf16 rows
+  int down_spl;            // operand order of h: chunks per lane and step of 2-bit down codes; 0: wider codes
   int32_t* ids;            // [T][topk] out
   float* weights;
   int32_t* ids_user;       // a second copy for the caller, or NULL
   float* weights_user;
   int32_t* rec;
-  uint8_t* hq;             // [T*topk][2][I] e4m3 halves of h in operand order, or [T*topk][I] bf16
+  uint8_t* hq;             // [T*topk][2][I] e4m3 halves of h in operand order
   uint8_t* hs;             // [T*topk][2][I / 32] block scales
 };
 
 struct LayerUpLds {
-  int tab, xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
+  int xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
   int xq_stride, xs_stride;
 };
-__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int batch, int table) {
+__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int batch) {
   LayerUpLds L;
   const int P = T * topk;
   auto up16 = [](int v) { return (v + 15) & ~15; };
-  // Rows of the MFMA: two halves a token, or (table > 0) one bf16 row; 16 bytes of
-  // padding each: the rows' reads hit other banks.
-  L.xq_stride = (table ? 2 * H : H) + 16;
+  // Rows of the MFMA: two halves a token; 16 bytes of padding each: the rows' reads hit
+  // other banks.
+  L.xq_stride = H + 16;
   L.xs_stride = up16(H / 32) + 16;
   int o = 0;
-  L.tab = o;   o += kLayerWaves * 2 * table;   // (tables start at multiples of their size)
-  L.xq = o;    o += (table ? T : 2 * T) * L.xq_stride;
-  L.xs = o;    o += table ? 0 : 2 * T * L.xs_stride;
+  L.xq = o;    o += 2 * T * L.xq_stride;
+  L.xs = o;    o += 2 * T * L.xs_stride;
   // partial sums, two batches of rounds: [2][batch][waves][2 tiles][T][16]; the
   // first-pair table of the experts uses the same bytes before the first round
   const int red = 2 * batch * kLayerWaves * 2 * T * 16 * 4;
@@ -422,14 +530,14 @@ __host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int b
 
 template <class F, int PM, int EPL>
 __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
-  extern __shared__ __align__(1024) unsigned char smem[];        // (table rows rely on this alignment)
+  extern __shared__ __align__(16) unsigned char smem[];
   constexpr int SPL = F::SPL;
   using Stream = CodeStream<F, PM, 2>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
   const int T = p.T, topk = p.r.topk, P = T * topk;
-  const LayerUpLds L = layer_up_lds(T, topk, p.H, p.batch, F::kTable);
+  const LayerUpLds L = layer_up_lds(T, topk, p.H, p.batch);
   int32_t* s_first = reinterpret_cast<int32_t*>(smem + L.first);
   int32_t* s_id = reinterpret_cast<int32_t*>(smem + L.id);
   float* s_w = reinterpret_cast<float*>(smem + L.w);
@@ -459,10 +567,6 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       const int t = on ? v / per_row : 0;
       const int q = on ? v - t * per_row : 0;
       const u32x4 raw = *reinterpret_cast<const u32x4*>(p.x + static_cast<int64_t>(t) * p.H + 8 * q);
-      if constexpr (F::kWide) {
-        if (on) *reinterpret_cast<u32x4*>(smem + L.xq + t * L.xq_stride + 16 * q) = raw;
-        continue;
-      }
       float f[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -484,13 +588,13 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       split2(f[5], f[7], fac, hi[3], lo[3]);
       if (on) {
         const int b = q >> 2, qd = q & 3;      // block of the row, quarter of the block
-        const int at = 32 * chunk_place<SPL>(b) + 16 * (qd >> 1) + 4 * (qd & 1);
+        const int at = 32 * chunk_place<SPL>(b) + code_slot(8 * qd, F::kWide);
 #pragma unroll
         for (int pc = 0; pc < 2; ++pc) {
           unsigned char* dst = smem + L.xq + (2 * t + pc) * L.xq_stride + at;
           const uint32_t* s = pc ? lo : hi;
           *reinterpret_cast<uint32_t*>(dst) = s[0] | (s[1] << 16);
-          *reinterpret_cast<uint32_t*>(dst + 8) = s[2] | (s[3] << 16);
+          *reinterpret_cast<uint32_t*>(dst + (F::kWide ? 4 : 8)) = s[2] | (s[3] << 16);
           if (qd == 0) smem[L.xs + (2 * t + pc) * L.xs_stride + b] = static_cast<uint8_t>(ef - (pc ? 11u : 7u));
         }
       }
@@ -559,25 +663,21 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   const int total = n * tiles;
   const int nmacro = p.H / (SPL * 128);
   // this wave's steps: part, part + ks, ... (the team's waves read neighbouring
-  // pieces of a row at any time); wide codes: a run of steps, so that a table serves
-  // several
-  const int first = F::kWide ? part * nmacro / ks : part, by = F::kWide ? 1 : ks;
-  const int steps = F::kWide ? (part + 1) * nmacro / ks - first : (nmacro - part + ks - 1) / ks;
+  // pieces of a row at any time)
+  const int steps = (nmacro - part + ks - 1) / ks;
   const uint32_t row_bytes = static_cast<uint32_t>(p.H * F::kBits / 8);
   // a gate row of the tile, and the up row I rows below it
-  auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
-    vc[0] = row * row_bytes + quarter * (Stream::DW * 4);
+  auto lane_offsets = [&](int row, int quarter, int piece, uint32_t* vc, uint32_t* vs) {
+    vc[0] = row * row_bytes + quarter * piece;
     vc[1] = vc[0] + static_cast<uint32_t>(p.I) * row_bytes;
     vs[0] = static_cast<uint32_t>(row * p.gpr * 4);
     vs[1] = vs[0] + static_cast<uint32_t>(p.I * p.gpr * 4);
   };
   uint32_t vcode[2], vscale[2];
-  lane_offsets(lane >> 2, lane & 3, vcode, vscale);
-  const int xaddr = 4 * (4 * nl + kq);
-  const int ml = nl < (F::kWide ? T : 2 * T) ? nl : 0;           // rows past the tokens are not used
+  lane_offsets(lane >> 2, lane & 3, F::kPiece, vcode, vscale);
+  const int ml = nl < 2 * T ? nl : 0;           // rows past the tokens are not used
   const uint8_t* xr = smem + L.xq + ml * L.xq_stride;
   const uint8_t* sr = smem + L.xs + ml * L.xs_stride;
-  uint16_t* tab = reinterpret_cast<uint16_t*>(smem + L.tab + wave * 2 * F::kTable);
 
   auto unit_row = [&](int u, int64_t& e, int& j) {
     const int uu = u < total ? u : 0;
@@ -604,9 +704,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
 
   Stream st;
   CodeSrc cur = source(u);
-  st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return first + min(i, steps - 1) * by; });
+  st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return part + min(i, steps - 1) * ks; });
   [&]<int... U>(std::integer_sequence<int, U...>) {
-    (st.template issue<U>(cur, vcode, first + min(U, steps - 1) * by), ...);
+    (st.template issue<U>(cur, vcode, part + min(U, steps - 1) * ks), ...);
   }(std::make_integer_sequence<int, PM>{});
 
   float* red = reinterpret_cast<float*>(smem + L.red);
@@ -614,9 +714,8 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   int slot_r = 0, half = 0, r0 = 0;            // round of the batch, its buffer, its first round
   for (int r = 0; r < rounds; ++r) {
     const CodeSrc nxt = source(u + stride);
-    float acc[2][F::kTokens] = {};
+    float acc[2][2] = {};
     uint32_t bad = 0u;
-    int gtab = -1;
     for (int t0 = 0; t0 < steps; t0 += PM) {
       // the next block: this unit's next PM steps, or the next unit's first
       st.take_scales();
@@ -626,26 +725,26 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       src.scale = more ? cur.scale : nxt.scale;
       if constexpr (F::kWide) src.shape = more ? cur.shape : nxt.shape;
       const int tn = more ? t0 + PM : 0;
-      st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return first + min(tn + i, steps - 1) * by; });
+      st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return part + min(tn + i, steps - 1) * ks; });
       [&]<int... U>(std::integer_sequence<int, U...>) {
         (([&] {
            if (t0 + U < steps) {
-             uint32_t w[2][Stream::DW];
+             uint32_t w[2][F::W];
              float s[2];
 #pragma unroll
              for (int i = 0; i < 2; ++i)
 #pragma unroll
                for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
              uint32_t sh[2];
-             st.template take<U>(xaddr, nl, w, s, sh);
-             const int t = first + (t0 + U) * by;
+             st.template take<U>(nl, kq, w, s, sh);
+             const int t = part + (t0 + U) * ks;
              if constexpr (F::kWide) {
-               wide_step<F, 2>(w, s, sh, xr, t, p.groups.of(t), gtab, tab, nl, kq, acc);
+               wide_step<F::kBits, 2>(w, s, sh, xr, sr, t, kq, acc);
              } else {
                layer_step<SPL, 2, 0>(w, s, xr, sr, t, kq, acc, bad);
              }
            }
-           st.template issue<U>(src, vcode, first + min(tn + U, steps - 1) * by);
+           st.template issue<U>(src, vcode, part + min(tn + U, steps - 1) * ks);
            __builtin_amdgcn_sched_barrier(0);
          }()),
          ...);
@@ -659,18 +758,18 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
         const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + 16 * j) * p.gpr,
                                                       static_cast<uint32_t>(p.I + 16) * 4u * static_cast<uint32_t>(p.gpr));
         uint32_t vc[2], vs[2];
-        lane_offsets(nl, kq, vc, vs);
+        lane_offsets(nl, kq, F::kPiece, vc, vs);
         layer_extra<SPL, 2>(cur, shp, vc, vs, part, nmacro, ks, p.groups, xr, sr, kq, acc);
       }
     }
     // partial sums of the team's waves meet in LDS; lane group kq holds tokens 2 kq
-    // and 2 kq + 1 (wide codes: 4 kq .. 4 kq + 3)
+    // and 2 kq + 1
     float* rb = red + (half * p.batch + slot_r) * red_round;
 #pragma unroll
-    for (int m = 0; m < F::kTokens; ++m)
-      if (F::kTokens * kq + m < T)
+    for (int m = 0; m < 2; ++m)
+      if (2 * kq + m < T)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + F::kTokens * kq + m) * 16 + nl] = acc[i][m];
+        for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + 2 * kq + m) * 16 + nl] = acc[i][m];
     cur = nxt;
     u += stride;
     ++slot_r;
@@ -709,12 +808,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       const uint32_t ef = block_exponent(amax);
       uint32_t hi, lo;
       split2(h, h, block_factor(ef), hi, lo);
-      if (slot != 0xff && p.down_spl == 0) {
-        const uint16_t hb = static_cast<uint16_t>(v != v ? (__float_as_uint(v) >> 16) | 0x40u : __float_as_uint(h) >> 16);
-        reinterpret_cast<uint16_t*>(p.hq)[static_cast<int64_t>(t * topk + slot) * p.I + 16 * j + c] = hb;
-      } else if (slot != 0xff) {
+      if (slot != 0xff) {
         const int b = j / 2;
-        const int place = 32 * (p.down_spl == 2 ? chunk_place<2>(b) : b) + code_slot(c);
+        const int place = 32 * (p.down_spl == 2 ? chunk_place<2>(b) : b) + code_slot(c, p.down_spl == 0);
         uint8_t* hq = p.hq + static_cast<int64_t>(t * topk + slot) * 2 * p.I + place;
         hq[0] = static_cast<uint8_t>(hi);
         hq[p.I] = static_cast<uint8_t>(lo);
@@ -732,7 +828,7 @@ struct LayerDownParams {
   const int32_t* rec;
   const float* weights;    // [T][topk]
   int T, topk;
-  const uint8_t* hq;       // [pair][2][I], or [pair][I] bf16 (wide codes)
+  const uint8_t* hq;       // [pair][2][I]
   const uint8_t* hs;       // [pair][2][I / 32]
   const uint8_t* codes;    // down, expert 0
   const float* scales;
@@ -748,18 +844,16 @@ struct LayerDownParams {
 };
 
 struct LayerDownLds {
-  int wave_bytes, hstride, sstride, wave0, sum, total;
+  int wave_bytes, hstride, sstride, sum, total;
 };
-// table: table bytes of a tile (wide codes), two tiles a wave
-__host__ __device__ inline LayerDownLds layer_down_lds(int T, int I, int spl, int ks, int table) {
+__host__ __device__ inline LayerDownLds layer_down_lds(int T, int I, int spl, int ks) {
   LayerDownLds L;
   const int nmacro = I / (spl * 128);
   const int kp = (nmacro + ks - 1) / ks * spl * 128;             // K values of a part
   L.hstride = kp + 16;
   L.sstride = ((kp / 32 + 15) & ~15) + 16;
-  L.wave_bytes = 2 * L.hstride + (table ? 0 : 2 * L.sstride);
-  L.wave0 = kLayerWaves * 2 * table;
-  L.sum = L.wave0 + kLayerWaves * L.wave_bytes;
+  L.wave_bytes = 2 * L.hstride + 2 * L.sstride;
+  L.sum = kLayerWaves * L.wave_bytes;
   L.total = L.sum + kLayerWaves * T * 32 * 4;
   return L;
 }
@@ -774,23 +868,18 @@ struct DownItem {
 // An item's h halves and block scales on their way into the wave's LDS: the first
 // 6 KB (a part of 3 K values) wait in registers, so that they are loaded before the
 // codes of their item; longer parts load the rest at the store.
-template <class F>
+template <int SPL>
 struct DownActs {
-  static constexpr int R = F::kWide ? 1 : 6, SPL = F::SPL;       // (the tables need the registers)
+  static constexpr int R = 6;
   u32x4 v[R];
   uint32_t sv;
-  // 16-byte chunk i of the part: of its two half rows (n chunks each), or of its bf16
-  // row of 2 n chunks
+  // 16-byte chunk i of the part's two half rows (n chunks each)
   static __device__ __forceinline__ const uint8_t* chunk(const LayerDownParams& p, const DownItem& q, int i, int n) {
-    if constexpr (F::kWide) {
-      return p.hq + (static_cast<int64_t>(q.pair) * p.I + q.tb * 128) * 2 + 16 * i;
-    } else {
-      const int pc = i < n ? 0 : 1;
-      return p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128 + 16 * (i - pc * n);
-    }
+    const int pc = i < n ? 0 : 1;
+    return p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128 + 16 * (i - pc * n);
   }
   static __device__ __forceinline__ int place(const LayerDownLds& L, int i, int n) {
-    return F::kWide || i < n ? 16 * i : L.hstride + 16 * (i - n);
+    return i < n ? 16 * i : L.hstride + 16 * (i - n);
   }
   // dword i of the part's scales (m a row)
   static __device__ __forceinline__ const uint8_t* scale(const LayerDownParams& p, const DownItem& q, int i, int m) {
@@ -801,7 +890,7 @@ struct DownActs {
     const int n = (q.te - q.tb) * SPL * 8;
 #pragma unroll
     for (int r = 0; r < R; ++r) v[r] = *reinterpret_cast<const u32x4*>(chunk(p, q, min(64 * r + lane, 2 * n - 1), n));
-    if constexpr (!F::kWide) sv = *reinterpret_cast<const uint32_t*>(scale(p, q, min(lane, n / 4 - 1), n / 8));
+    sv = *reinterpret_cast<const uint32_t*>(scale(p, q, min(lane, n / 4 - 1), n / 8));
   }
   __device__ __forceinline__ void store(const LayerDownParams& p, const DownItem& q, uint8_t* hreg, uint8_t* sreg,
                                         const LayerDownLds& L, int lane) const {
@@ -811,26 +900,23 @@ struct DownActs {
       if (64 * r + lane < 2 * n) *reinterpret_cast<u32x4*>(hreg + place(L, 64 * r + lane, n)) = v[r];
     for (int i = 64 * R + lane; i < 2 * n; i += 64)
       *reinterpret_cast<u32x4*>(hreg + place(L, i, n)) = *reinterpret_cast<const u32x4*>(chunk(p, q, i, n));
-    if constexpr (!F::kWide) {
-      if (lane < 2 * m) *reinterpret_cast<uint32_t*>(sreg + (lane < m ? 4 * lane : L.sstride + 4 * (lane - m))) = sv;
-      for (int i = 64 + lane; i < 2 * m; i += 64)
-        *reinterpret_cast<uint32_t*>(sreg + (i < m ? 4 * i : L.sstride + 4 * (i - m))) =
-            *reinterpret_cast<const uint32_t*>(scale(p, q, i, m));
-    }
+    if (lane < 2 * m) *reinterpret_cast<uint32_t*>(sreg + (lane < m ? 4 * lane : L.sstride + 4 * (lane - m))) = sv;
+    for (int i = 64 + lane; i < 2 * m; i += 64)
+      *reinterpret_cast<uint32_t*>(sreg + (i < m ? 4 * i : L.sstride + 4 * (i - m))) =
+          *reinterpret_cast<const uint32_t*>(scale(p, q, i, m));
   }
 };
 
 template <class F, int PM, int NT>
 __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
-  extern __shared__ __align__(1024) unsigned char smem[];        // (table rows rely on this alignment)
+  extern __shared__ __align__(16) unsigned char smem[];
   constexpr int SPL = F::SPL;
   using Stream = CodeStream<F, PM, NT>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
-  const LayerDownLds L = layer_down_lds(p.T, p.I, SPL, p.ks, F::kTable);
-  uint16_t* tab = reinterpret_cast<uint16_t*>(smem + wave * 2 * F::kTable);
-  uint8_t* hreg = smem + L.wave0 + wave * L.wave_bytes;
+  const LayerDownLds L = layer_down_lds(p.T, p.I, SPL, p.ks);
+  uint8_t* hreg = smem + wave * L.wave_bytes;
   uint8_t* sreg = hreg + 2 * L.hstride;
   float* sums = reinterpret_cast<float*>(smem + L.sum) + wave * p.T * 32;
   for (int i = lane; i < p.T * 32; i += 64) sums[i] = 0.0f;
@@ -841,17 +927,16 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   const int nmacro = p.I / (SPL * 128);
   const uint32_t row_bytes = static_cast<uint32_t>(p.I * F::kBits / 8);
   // a row of each tile (past the workgroup's rows: its last one, whose sums are not used)
-  auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
+  auto lane_offsets = [&](int row, int quarter, int piece, uint32_t* vc, uint32_t* vs) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int r = min(i * p.rt + min(row, p.rt - 1), rows - 1);
-      vc[i] = r * row_bytes + quarter * (Stream::DW * 4);
+      vc[i] = r * row_bytes + quarter * piece;
       vs[i] = static_cast<uint32_t>(r * p.gpr * 4);
     }
   };
   uint32_t vcode[NT], vscale[NT];
-  lane_offsets(lane >> 2, lane & 3, vcode, vscale);
-  const int xaddr = 4 * (4 * nl + kq);
+  lane_offsets(lane >> 2, lane & 3, F::kPiece, vcode, vscale);
   using Item = DownItem;
   auto item_of = [&](int it) {
     Item q;
@@ -877,7 +962,7 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   int it = wave;
   if (it < items) {                            // wave-uniform; the barrier comes after
     Stream st;
-    DownActs<F> hst;
+    DownActs<SPL> hst;
     Item q = item_of(it);
     CodeSrc cur = source(q);
     hst.load(p, q, lane);
@@ -886,7 +971,7 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
     [&]<int... U>(std::integer_sequence<int, U...>) {
       (st.template issue<U>(cur, vcode, min(q.tb + U, q.te - 1)), ...);
     }(std::make_integer_sequence<int, PM>{});
-    const uint8_t* xr = hreg + (!F::kWide && nl == 1 ? L.hstride : 0);   // row 0: hi, row 1: lo; or one bf16 row
+    const uint8_t* xr = hreg + (nl == 1 ? L.hstride : 0);   // row 0: hi, row 1: lo
     const uint8_t* sr = sreg + (nl == 1 ? L.sstride : 0);
     for (; it < items; it += kLayerWaves) {
       hst.store(p, q, hreg, sreg, L, lane);    // the part's h into this wave's LDS
@@ -895,9 +980,8 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
       const CodeSrc nxt = source(qn);
       const float w = p.weights[q.pair];
       hst.load(p, qn, lane);                   // ahead of the next item's codes
-      float acc[NT][F::kTokens] = {};
+      float acc[NT][2] = {};
       uint32_t bad = 0u;
-      int gtab = -1;
       for (int t0 = q.tb; t0 < q.te; t0 += PM) {
         st.take_scales();
         const bool more = t0 + PM < q.te;
@@ -910,16 +994,16 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
         [&]<int... U>(std::integer_sequence<int, U...>) {
           (([&] {
              if (t0 + U < q.te) {
-               uint32_t w4[NT][Stream::DW];
+               uint32_t w4[NT][F::W];
                float s[NT];
 #pragma unroll
                for (int i = 0; i < NT; ++i)
 #pragma unroll
                  for (int d = 0; d < Stream::DW; ++d) asm volatile("" : "+v"(st.cb[U][i][d]));
                uint32_t sh[NT];
-               st.template take<U>(xaddr, nl, w4, s, sh);
+               st.template take<U>(nl, kq, w4, s, sh);
                if constexpr (F::kWide) {
-                 wide_step<F, NT>(w4, s, sh, xr, t0 + U - q.tb, p.groups.of(t0 + U), gtab, tab, nl, kq, acc);
+                 wide_step<F::kBits, NT>(w4, s, sh, xr, sr, t0 + U - q.tb, kq, acc);
                } else {
                  layer_step<SPL, NT, 0>(w4, s, xr, sr, t0 + U - q.tb, kq, acc, bad);
                }
@@ -935,7 +1019,7 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
           const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
                                                         static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
           uint32_t vc[NT], vs[NT];
-          lane_offsets(nl, kq, vc, vs);
+          lane_offsets(nl, kq, F::kPiece, vc, vs);
           const int back = q.tb * SPL * 128;     // (steps count from the part's first in LDS)
           layer_extra<SPL, NT>(cur, shp, vc, vs, q.tb, q.te, 1, p.groups, xr - back, sr - q.tb * SPL * 4, kq, acc);
         }
@@ -973,7 +1057,6 @@ Groups group_steps(int group, int spl) {
 }
 
 int layer_spl(int bits, int group) { return bits == 2 && group % 256 == 0 ? 2 : 1; }
-int layer_table(int bits) { return bits == 2 ? 0 : 16 * (1 << bits) * 4; }
 
 constexpr int kLayerLds = 160 * 1024;
 
@@ -995,28 +1078,27 @@ int layer_up_parts(int T, int topk, int E, int I, int nmacro, int grid) {
 }
 
 // K parts of kernel 2: enough items for every wave, and a part's h in LDS.
-int layer_down_parts(int T, int topk, int I, int spl, int table) {
+int layer_down_parts(int T, int topk, int I, int spl) {
   const int nmacro = I / (spl * 128);
   const int jobs = T * topk;
   int ks = 1;
-  while (ks < nmacro && (jobs * ks < kLayerWaves || layer_down_lds(T, I, spl, ks, table).total > kLayerLds)) ks *= 2;
+  while (ks < nmacro && (jobs * ks < kLayerWaves || layer_down_lds(T, I, spl, ks).total > kLayerLds)) ks *= 2;
   return std::min(ks, nmacro);
 }
 
 }  // namespace
 
 // One run of the two kernels: 2- to 4-bit codes, up to eight tokens, and activations,
-// tables, lists and partial sums in one compute unit's LDS.
+// lists and partial sums in one compute unit's LDS.
 static bool layer_fits(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
                        int dn_group) {
   if (up_bits < 2 || up_bits > 4 || dn_bits < 2 || dn_bits > 4) return false;
   if (T < 1 || T > kLayerMaxT || E > kLayerMaxE || topk > kRouterMaxTopk) return false;
   if (H > 65536 || I > 65536 || (I + 16) * (H * up_bits / 8) >= (int64_t{1} << 32)) return false;   // 32-bit tile offsets
-  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H), 1, layer_table(up_bits)).total > kLayerLds)
-    return false;
+  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H), 1).total > kLayerLds) return false;
   const int spl = layer_spl(dn_bits, dn_group);
-  const int ks = layer_down_parts(static_cast<int>(T), topk, static_cast<int>(I), spl, layer_table(dn_bits));
-  return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks, layer_table(dn_bits)).total <= kLayerLds;
+  const int ks = layer_down_parts(static_cast<int>(T), topk, static_cast<int>(I), spl);
+  return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks).total <= kLayerLds;
 }
 
 // Tokens of one run of the two kernels; 0: the composed path. Nine to 32 tokens take
@@ -1067,11 +1149,10 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   p.code_bytes = up.code_bytes;
   p.gpr = H / up.group;
   const int spl = layer_spl(up.bits, up.group), dspl = layer_spl(dn.bits, dn.group);
-  const int table = layer_table(up.bits), dtable = layer_table(dn.bits);
   p.groups = group_steps(up.group, spl);
   const int nmacro = H / (spl * 128);
   p.ks = layer_up_parts(T, r.topk, r.E, I, nmacro, cus);
-  p.down_spl = dtable ? 0 : dspl;
+  p.down_spl = dn.bits == 2 ? dspl : 0;
   p.ids = b.ids;
   p.weights = b.weights;
   p.ids_user = ids_user;
@@ -1083,8 +1164,8 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   const int64_t units = static_cast<int64_t>(std::min(r.E, T * r.topk)) * (I / 16);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
   p.batch = 4;
-  while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch, table).total > kLayerLds) --p.batch;
-  const int lds = layer_up_lds(T, r.topk, H, p.batch, table).total;
+  while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch).total > kLayerLds) --p.batch;
+  const int lds = layer_up_lds(T, r.topk, H, p.batch).total;
   hipError_t e;
   const bool few = r.E <= 256;                 // a router wave with 4 experts a lane, or 16
   auto up_kernel = [&](auto f_c, auto pm_c) {
@@ -1121,11 +1202,11 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   const int nt = d.rows > 16 ? 2 : 1;
   d.rt = (d.rows + nt - 1) / nt;
   d.rows = d.rt * nt;
-  d.ks = layer_down_parts(T, r.topk, I, dspl, dtable);
+  d.ks = layer_down_parts(T, r.topk, I, dspl);
   d.y = y;
   d.ybf16 = ybf16;
   const unsigned dgrid = static_cast<unsigned>((H + d.rows - 1) / d.rows);
-  const int dlds = layer_down_lds(T, I, dspl, d.ks, dtable).total;
+  const int dlds = layer_down_lds(T, I, dspl, d.ks).total;
   auto down_kernel = [&](auto f_c, auto pm_c) {
     using F = decltype(f_c);
     constexpr int PM = decltype(pm_c)::value;
