@@ -486,7 +486,6 @@ struct LayerUpParams {
   int64_t code_bytes;
   int gpr;                 // groups per row
   Groups groups;           // steps per group
-  int ks;                  // waves per tile (each a part of K)
   int batch;               // rounds between the joins of the waves' sums
   int down_spl;            // operand order of h: chunks per lane and step of 2-bit down codes; 0: wider codes
   int32_t* ids;            // [T][topk] out
@@ -497,6 +496,28 @@ struct LayerUpParams {
   uint8_t* hq;             // [T*topk][2][I] e4m3 halves of h in operand order
   uint8_t* hs;             // [T*topk][2][I / 32] block scales
 };
+
+// K parts of kernel 1: the waves of a tile, so many that the slowest workgroup has the
+// least to do (units: touched experts' tiles; kRoundCost: eighths of a step that a round
+// costs beside its steps). At least two teams: a scale block of h spans two tiles. The
+// number of touched experts is known on the device alone: taken for the largest possible
+// one (64 for 8 tokens of top-8, where 41 are usual), the last of two rounds was a third
+// full, and 4 bits, 7168 x 2 K took 250 us.
+constexpr int kRoundCost = 4;
+__host__ __device__ inline int layer_up_max_parts(int nmacro) { return nmacro >= 8 ? 8 : nmacro >= 4 ? 4 : nmacro >= 2 ? 2 : 1; }
+__device__ __forceinline__ int layer_up_parts(uint32_t units, int nmacro, uint32_t grid) {
+  int best = 1;
+  uint32_t cost = 0xffffffffu;
+  const int most = layer_up_max_parts(nmacro);
+#pragma unroll
+  for (int ks = 1; ks <= 8; ks *= 2) {
+    if (ks > most) break;
+    const uint32_t round = grid * (kLayerWaves / ks);
+    const uint32_t c = (units + round - 1) / round * ((nmacro + ks - 1) / ks * 8 + kRoundCost);
+    if (c < cost) { cost = c; best = ks; }
+  }
+  return best;
+}
 
 struct LayerUpLds {
   int xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
@@ -657,11 +678,12 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   }
 
   // ---- units: round r, workgroup b, team m -> (r grid + b) teams + m ----
-  const int ks = p.ks, teams = kLayerWaves / ks;
-  const int team = wave / ks, part = wave - team * ks;
   const int tiles = p.I / 16;
   const int total = n * tiles;
   const int nmacro = p.H / (SPL * 128);
+  const int ks = __builtin_amdgcn_readfirstlane(layer_up_parts(static_cast<uint32_t>(total), nmacro, gridDim.x));
+  const int teams = kLayerWaves / ks;
+  const int team = wave / ks, part = wave - team * ks;
   // this wave's steps: part, part + ks, ... (the team's waves read neighbouring
   // pieces of a row at any time)
   const int steps = (nmacro - part + ks - 1) / ks;
@@ -1060,23 +1082,6 @@ int layer_spl(int bits, int group) { return bits == 2 && group % 256 == 0 ? 2 : 
 
 constexpr int kLayerLds = 160 * 1024;
 
-// K parts of kernel 1: the waves of a tile. At least two teams (a scale block of
-// h spans two tiles), and as few rounds of steps as possible for the expected
-// (largest) number of touched experts.
-int layer_up_parts(int T, int topk, int E, int I, int nmacro, int grid) {
-  const int64_t units = static_cast<int64_t>(std::min(E, T * topk)) * (I / 16);
-  int best = 8;
-  int64_t cost = INT64_MAX;
-  for (int ks = 1; ks <= 8; ks *= 2) {
-    if (ks > nmacro && ks > 1) break;
-    const int teams = kLayerWaves / ks;
-    const int64_t rounds = (units + static_cast<int64_t>(grid) * teams - 1) / (static_cast<int64_t>(grid) * teams);
-    const int64_t c = rounds * ((nmacro + ks - 1) / ks) * 8 + rounds;   // steps of a wave, and the rounds' joins
-    if (c < cost) { cost = c; best = ks; }
-  }
-  return best;
-}
-
 // K parts of kernel 2: enough items for every wave, and a part's h in LDS.
 int layer_down_parts(int T, int topk, int I, int spl) {
   const int nmacro = I / (spl * 128);
@@ -1151,7 +1156,6 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   const int spl = layer_spl(up.bits, up.group), dspl = layer_spl(dn.bits, dn.group);
   p.groups = group_steps(up.group, spl);
   const int nmacro = H / (spl * 128);
-  p.ks = layer_up_parts(T, r.topk, r.E, I, nmacro, cus);
   p.down_spl = dn.bits == 2 ? dspl : 0;
   p.ids = b.ids;
   p.weights = b.weights;
@@ -1160,7 +1164,7 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   p.rec = b.rec;
   p.hq = b.hq;
   p.hs = b.hs;
-  const int teams = kLayerWaves / p.ks;
+  const int teams = kLayerWaves / layer_up_max_parts(nmacro);    // at least
   const int64_t units = static_cast<int64_t>(std::min(r.E, T * r.topk)) * (I / 16);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
   p.batch = 4;
