@@ -14,9 +14,15 @@
 // e4m3 halves: a bf16 number has eight significant bits, hi takes the upper
 // four rounded to nearest and lo the (signed) rest, with one power-of-two block
 // scale for 32 consecutive values. hi and lo (and the tokens) are rows of the
-// same 16 x 16 x 128 MFMA, which sums their products with the codes in fp32. Values
-// below 2^-14 of their block's largest are off by up to 2^-22 of it, and blocks
-// whose largest value is below 2^-116 by up to 2^-138.
+// same 16 x 16 x 128 MFMA. Values below 2^-14 of their block's largest are off by up to
+// 2^-22 of it, and blocks whose largest value is below 2^-116 by up to 2^-138. The MFMA
+// aligns the products of its 128 codes to the largest and drops what lies about 2^-14
+// below it: measured, its sums of normal values are off by 2^-18 to 2^-19 (rms; exact
+// where the products span less), by 2^-16 where outliers of 40 times the rest are among
+// them, and at worst by 2^-11 of the largest product. Steps are added up in fp32. The
+// result is 2^-16 off where an fp32 sum would be 2^-24, which moves about one h in a
+// hundred to the neighbouring bf16 number; exact sums would need a third row a token, and
+// hold five tokens.
 //
 // Kernel 1 (k_layer_up): every workgroup runs the router of all tokens (one wave
 // each), splits x into LDS, and then walks its share of the units (touched
@@ -33,8 +39,8 @@
 // loads in operand order, a barrier a round and seven steps in flight, the first version,
 // kernel 1 took 62 us and kernel 2 26.
 //
-// 3- and 4-bit codes run on the same two kernels with table levels (CodesWide); wider
-// codes, more tokens and shapes beyond the kernels' LDS run as the router kernel
+// 3- and 4-bit codes run on the same two kernels as sums of fixed functions of the code
+// (CodesWide); wider codes, more tokens and shapes beyond the kernels' LDS run as the router kernel
 // followed by the routed MLP step (moe.hip).
 #include <algorithm>
 
@@ -125,11 +131,12 @@ struct Codes2 {
 // and the coefficients of a group enter with its scale. A table of a group's levels costs
 // its building and an LDS read a code.
 // 4 bits: a code is -8 sign + l. The low bits l of j and of -j add up to 8, where p2 is
-// even and p3 odd, so both need only l, and p2 the sign. p3 + l has four significant bits
-// (p3 has not); l and the unsigned code u = 8 sign + l are e4m3 numbers as they stand (the
-// bytes 0 .. 15 mean 2^-9 of that), and p1 = 2 l - u: twelve operations for eight codes and
-// four MFMAs. (Whole 16-entry look-ups of three functions took 26 and three; 4 bits, 7168 x
-// 2 K, 8 tokens: 419 us.) 3 bits: three look-ups in eight entries.
+// even and p3 odd, so both need only l, and p2 the sign; p1 = (l - 4) +- 4, and p3 + l - 4
+// has four significant bits (p3 has not): fourteen operations for eight codes and four
+// MFMAs. Whole 16-entry look-ups of three functions took 26 and three (7168 x 2 K, 8
+// tokens: 419 us against 291 to 310); l and the unsigned code as they stand (small e4m3
+// numbers) take twelve, but their sums' cancellation costs two bits (2^-14.5). 3 bits:
+// three look-ups in eight entries.
 // The MFMA wants codes 16 kq .. + 15 and 64 + 16 kq .. + 15 of a step in lane group kq.
 // 4 bits: loaded as 8-byte pieces of either half; 3 bits: as 12-byte chunks of 32 codes,
 // of which two lane groups take a half each.
@@ -159,21 +166,23 @@ constexpr uint32_t e4m3_bytes(Fn f, int j0) {
   return v;
 }
 // The lane's 32 operand codes (w: 16 and 16; the even and odd ones of eight in turn) as
-// bytes. 4 bits: b = l, u, p2, p3 + l; 3 bits: p1, p2, p3.
+// bytes. 4 bits: b = l - 4, +-4, p2, p3 + l - 4; 3 bits: p1, p2, p3.
 template <int B>
 __device__ __forceinline__ void poly_decode(const uint32_t* w, i32x8* b) {
   if constexpr (B == 4) {
     constexpr auto p2 = [](int l) { return l * (8 - l); };
-    constexpr auto p3l = [](int l) { return l * (8 - l) * (l - 4) + l; };
-    constexpr uint32_t a0 = e4m3_bytes(p2, 0), a4 = e4m3_bytes(p2, 4), c0 = e4m3_bytes(p3l, 0), c4 = e4m3_bytes(p3l, 4);
+    constexpr auto p3l4 = [](int l) { return l * (8 - l) * (l - 4) + l - 4; };
+    constexpr auto l4 = [](int l) { return l - 4; };
+    constexpr uint32_t four = e4m3_int(4) * 0x01010101u, d0 = e4m3_bytes(l4, 0), d4 = e4m3_bytes(l4, 4);
+    constexpr uint32_t a0 = e4m3_bytes(p2, 0), a4 = e4m3_bytes(p2, 4), c0 = e4m3_bytes(p3l4, 0), c4 = e4m3_bytes(p3l4, 4);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {              // eight codes
       const uint32_t v = w[u], vs = v >> 4;
       const uint32_t le = v & 0x07070707u, lo = vs & 0x07070707u;
-      b[0][2 * u] = static_cast<int>(le);
-      b[0][2 * u + 1] = static_cast<int>(lo);
-      b[1][2 * u] = static_cast<int>(v & 0x0F0F0F0Fu);
-      b[1][2 * u + 1] = static_cast<int>(vs & 0x0F0F0F0Fu);
+      b[0][2 * u] = static_cast<int>(__builtin_amdgcn_perm(d4, d0, le));
+      b[0][2 * u + 1] = static_cast<int>(__builtin_amdgcn_perm(d4, d0, lo));
+      b[1][2 * u] = static_cast<int>(((v << 4) & 0x80808080u) | four);
+      b[1][2 * u + 1] = static_cast<int>((v & 0x80808080u) | four);
       b[2][2 * u] = static_cast<int>(((v << 4) & 0x80808080u) | __builtin_amdgcn_perm(a4, a0, le));
       b[2][2 * u + 1] = static_cast<int>((v & 0x80808080u) | __builtin_amdgcn_perm(a4, a0, lo));
       b[3][2 * u] = static_cast<int>(__builtin_amdgcn_perm(c4, c0, le));
@@ -214,7 +223,7 @@ __device__ __forceinline__ void poly_decode(const uint32_t* w, i32x8* b) {
 // group scales of four steps likewise), and the lanes exchange the words through
 // the LDS crossbar when they are used (ds_bpermute, no LDS memory).
 struct CodeSrc {                               // a unit's code and scale buffers (wave-uniform)
-  __amdgpu_buffer_rsrc_t code, scale, shape;   // (shape: of table levels only)
+  __amdgpu_buffer_rsrc_t code, scale, shape;   // (shape: of wide codes only)
 };
 
 struct Groups {                                // steps per group: as a shift, or (shift < 0) by a reciprocal
@@ -231,7 +240,7 @@ struct CodeStream {
   static constexpr int SR = (PM + 3) / 4;      // scale registers per tile and block (four steps each)
   uint32_t cb[PM][NT][DW];
   float sc[NT][SR], scn[NT][SR];               // of the current block, and of the next
-  uint32_t ab[NT][F::kWide ? SR : 1], abn[NT][F::kWide ? SR : 1];   // shape parameters likewise (table levels)
+  uint32_t ab[NT][F::kWide ? SR : 1], abn[NT][F::kWide ? SR : 1];   // shape parameters likewise (wide codes)
 
   // step t into slot U; vcode: the lane's byte offset per tile
   template <int U>
@@ -378,11 +387,7 @@ __device__ __forceinline__ void wide_step(const uint32_t (*w)[4], const float* s
 #pragma unroll
     for (int f = 0; f < NS; ++f) {
       constexpr f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-      if (B == 4 && f < 2) {                   // (bytes of 2^-9)
-        part[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[f], zero, 0, 0, 0, sx, 0, 136);
-      } else {
-        part[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[f], zero, 0, 0, 0, sx, 0, 127);
-      }
+      part[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[f], zero, 0, 0, 0, sx, 0, 127);
     }
     const float sa = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sh[i] & 0xffffu)));
     const float sb = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sh[i] >> 16)));
@@ -396,7 +401,7 @@ __device__ __forceinline__ void wide_step(const uint32_t (*w)[4], const float* s
 #pragma unroll
       for (int f = 0; f < NS; ++f) p[f] = part[f][2 * m] + part[f][2 * m + 1];
       if constexpr (B == 4) {
-        acc[i][m] = fmaf(k1, fmaf(2.0f, p[0], -p[1]), acc[i][m]);
+        acc[i][m] = fmaf(k1, p[0] + p[1], acc[i][m]);
         acc[i][m] = fmaf(k2, p[2], acc[i][m]);
         acc[i][m] = fmaf(k3, p[3] - p[0], acc[i][m]);
       } else {
@@ -1106,19 +1111,21 @@ static bool layer_fits(int64_t T, int topk, int E, int64_t H, int64_t I, int up_
   return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks).total <= kLayerLds;
 }
 
-// Tokens of one run of the two kernels; 0: the composed path. Nine to 32 tokens take
-// runs of up to eight: an expert that tokens of several runs share is read again, but
-// at twice the composed path's rate (2-bit codes, 2048 x 1024, 16 tokens, top-8 of 128:
-// 80 against 158 us; 7168 x 3 K, 32 tokens, top-16 of 128: 1.24 against 1.46 ms). Wider
-// codes take two runs at most (4 bits, 2048 x 1024, top-4 of 32: 16 tokens 151 against
-// 158 us, 24 tokens 222 against 210). With weights below 4 MB the launches count, not
-// the rate (16 tokens, 512 x 256, top-2 of 8: 40 against 33 us).
+// Tokens of one run of the two kernels; 0: the composed path. Nine to 64 tokens take
+// runs of up to eight: an expert that tokens of several runs share is read again, but at
+// twice the composed path's rate or more (2-bit codes, 2048 x 1024, top-8 of 128, 16
+// tokens: 80 against 158 us, 64: 302 against 433; 7168 x 3 K, top-16 of 128, 64 tokens:
+// 2.28 against 2.61 ms; 4 bits, 2048 x 1024, top-4 of 32, 64 tokens: 325 against 506).
+// The composed path is ahead where many pairs of 2-bit codes share an expert (2048 x 1024,
+// top-4 of 16: 40 tokens 128 against 128 us, 64 tokens 200 against 191), and with weights
+// below 4 MB, where the launches count, not the rate (16 tokens, 512 x 256, top-2 of 8: 40
+// against 33 us).
 int64_t moe_layer_tokens(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
                          int dn_group) {
-  const int64_t most = up_bits == 2 && dn_bits == 2 ? 4 : 2;
-  if (T < 1 || T > most * kLayerMaxT) return 0;
+  if (T < 1 || T > 8 * kLayerMaxT) return 0;
   const int64_t runs = (T + kLayerMaxT - 1) / kLayerMaxT, n = (T + runs - 1) / runs;
   if (!layer_fits(n, topk, E, H, I, up_bits, up_group, dn_bits, dn_group)) return 0;
+  if (up_bits == 2 && runs > 4 && T * topk > 10 * static_cast<int64_t>(E)) return 0;
   if (runs > 1 && 3 * H * I * up_bits / 8 * std::min<int64_t>(E, T * topk) < (int64_t{4} << 20)) return 0;
   return n;
 }

@@ -386,12 +386,13 @@ int cubic_moe_topk(const cubic_router* router, int64_t T, int32_t* topk_ids, flo
  * A token whose experts are all masked out gets a zero row. For 2- to 4-bit weights
  * and up to eight tokens (E <= 1024, and activations that fit a compute unit's LDS)
  * the layer runs in two kernels, which read each touched expert's codes from HBM
- * once, and with weights of 4 MB and more for up to 32 tokens (3 and 4 bits: 16) in
- * such runs of up to eight; otherwise the router kernel and the MLP step run one after
- * the other, with the limits of cubic_moe_mlp. 2-bit weights multiply the activations
- * exactly, in the two kernels unless they lie below 2^-14 of the largest of their 32
- * neighbours (then off by up to 2^-22 of that); wider codes' levels have 16 significant
- * bits. A non-finite activation makes its token's row non-finite and no other. The sums'
+ * once, and with weights of 4 MB and more for up to 64 tokens (2 bits and more than 32
+ * tokens: while at most ten pairs share an expert on average) in such runs of up to
+ * eight; otherwise the router kernel and the MLP step run one after the other, with the
+ * limits of cubic_moe_mlp. Products are as good as 16 significant bits: the two kernels'
+ * sums of 128 codes are off by about 2^-16 of the sum (at worst 2^-11 of its largest
+ * product), and in the MLP step the levels of wider codes are rounded to 16 bits; sums
+ * are fp32 beyond. About one h in a hundred rounds to a neighbour for it. A non-finite activation makes its token's row non-finite and no other. The sums'
  * order does not depend on timing.
  * x_bf16 [T][H]; y [T][H] in y_dtype CUBIC_DTYPE_F32 or CUBIC_DTYPE_BF16 (rounded
  * once); topk_ids and topk_weights [T][topk] receive the routing, or are NULL. The
