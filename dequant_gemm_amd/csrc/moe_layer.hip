@@ -491,6 +491,7 @@ struct LayerUpParams {
   int64_t code_bytes;
   int gpr;                 // groups per row
   Groups groups;           // steps per group
+  float share;             // 1 / (workgroups * waves)
   int batch;               // rounds between the joins of the waves' sums
   int down_spl;            // operand order of h: chunks per lane and step of 2-bit down codes; 0: wider codes
   int32_t* ids;            // [T][topk] out
@@ -510,16 +511,19 @@ struct LayerUpParams {
 // full, and 4 bits, 7168 x 2 K took 250 us.
 constexpr int kRoundCost = 4;
 __host__ __device__ inline int layer_up_max_parts(int nmacro) { return nmacro >= 8 ? 8 : nmacro >= 4 ? 4 : nmacro >= 2 ? 2 : 1; }
-__device__ __forceinline__ int layer_up_parts(uint32_t units, int nmacro, uint32_t grid) {
+// share: 1 / (workgroups * waves). (Every workgroup computes the same; integer divisions
+// take 0.5 us.)
+__device__ __forceinline__ int layer_up_parts(int units, int nmacro, float share) {
   int best = 1;
-  uint32_t cost = 0xffffffffu;
+  float cost = __builtin_inff();
   const int most = layer_up_max_parts(nmacro);
+  const float whole = static_cast<float>(units) * share;
 #pragma unroll
-  for (int ks = 1; ks <= 8; ks *= 2) {
-    if (ks > most) break;
-    const uint32_t round = grid * (kLayerWaves / ks);
-    const uint32_t c = (units + round - 1) / round * ((nmacro + ks - 1) / ks * 8 + kRoundCost);
-    if (c < cost) { cost = c; best = ks; }
+  for (int sh = 0; sh <= 3; ++sh) {
+    const int ks = 1 << sh;
+    const float rounds = ceilf(whole * static_cast<float>(ks) - 1e-3f);
+    const float c = rounds * static_cast<float>(((nmacro + ks - 1) >> sh) * 8 + kRoundCost);
+    if (ks <= most && c < cost) { cost = c; best = ks; }
   }
   return best;
 }
@@ -686,7 +690,7 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   const int tiles = p.I / 16;
   const int total = n * tiles;
   const int nmacro = p.H / (SPL * 128);
-  const int ks = __builtin_amdgcn_readfirstlane(layer_up_parts(static_cast<uint32_t>(total), nmacro, gridDim.x));
+  const int ks = __builtin_amdgcn_readfirstlane(layer_up_parts(total, nmacro, p.share));
   const int teams = kLayerWaves / ks;
   const int team = wave / ks, part = wave - team * ks;
   // this wave's steps: part, part + ks, ... (the team's waves read neighbouring
@@ -1174,6 +1178,7 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   const int teams = kLayerWaves / layer_up_max_parts(nmacro);    // at least
   const int64_t units = static_cast<int64_t>(std::min(r.E, T * r.topk)) * (I / 16);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
+  p.share = 1.0f / (static_cast<float>(grid) * kLayerWaves);
   p.batch = 4;
   while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch).total > kLayerLds) --p.batch;
   const int lds = layer_up_lds(T, r.topk, H, p.batch).total;
