@@ -35,7 +35,8 @@
 // 5.1 TB/s): one token through 16 of 64 experts, 281 MB: kernel 1 42 us (8 us until the
 // first load is issued: router, splitting, lists; then 5.7 TB/s), kernel 2 21 us
 // (5.9 TB/s while streaming), 56-64 us together; four tokens through about 52 of 128
-// experts, 930 MB: 132 + 63 us. HBM traffic is 1.00 of the codes and scales. Against
+// experts, 930 MB: 112 + 64 us; 4 bits, G128, 2048 x 1024, two tokens of top-4 of 32: 12.7
+// + 8.6 us. HBM traffic is 1.00 of the codes and scales. Against
 // loads in operand order, a barrier a round and seven steps in flight, the first version,
 // kernel 1 took 62 us and kernel 2 26.
 //
@@ -129,7 +130,8 @@ struct Codes2 {
 // whose products with the activations' halves MFMAs sum exactly: the values are e4m3
 // numbers (four significant bits), looked up four at a time by byte permutes in registers,
 // and the coefficients of a group enter with its scale. A table of a group's levels costs
-// its building and an LDS read a code.
+// its building and an LDS read a code (2048 x 1024, W4 G128, two tokens: 17.5 + 11.2 us
+// with tables).
 // 4 bits: a code is -8 sign + l. The low bits l of j and of -j add up to 8, where p2 is
 // even and p3 odd, so both need only l, and p2 the sign; p1 = (l - 4) +- 4, and p3 + l - 4
 // has four significant bits (p3 has not): fourteen operations for eight codes and four
@@ -1119,7 +1121,7 @@ static bool layer_fits(int64_t T, int topk, int E, int64_t H, int64_t I, int up_
 // runs of up to eight: an expert that tokens of several runs share is read again, but at
 // twice the composed path's rate or more (2-bit codes, 2048 x 1024, top-8 of 128, 16
 // tokens: 80 against 158 us, 64: 302 against 433; 7168 x 3 K, top-16 of 128, 64 tokens:
-// 2.28 against 2.61 ms; 4 bits, 2048 x 1024, top-4 of 32, 64 tokens: 325 against 506).
+// 2.28 against 2.61 ms; 4 bits, 2048 x 1024, top-4 of 32, 64 tokens: 347 against 506).
 // The composed path is ahead where many pairs of 2-bit codes share an expert (2048 x 1024,
 // top-4 of 16: 40 tokens 128 against 128 us, 64 tokens 200 against 191), and with weights
 // below 4 MB, where the launches count, not the rate (16 tokens, 512 x 256, top-2 of 8: 40
