@@ -14,7 +14,8 @@
 // are used. The activations pass through LDS in chunks of 64 KB, two buffers, one
 // barrier a chunk that leaves the weight loads in flight. Up to four bf16 or fp16 rows
 // are quantised by every workgroup itself, beside its first weight loads, which saves a
-// launch.
+// launch; with more rows the quantiser is a launch of its own (every workgroup quantising
+// 37 rows of 1928, chunk by chunk: 43 us instead of 10).
 //
 // Measured: 6144 x 7168, one bf16 row: 44.1 MB in 9.8-10.2 us (4.4 TB/s; a large copy
 // runs at 5.1); 7168 x 2048, 64 rows: 9.7 us, where the launch, the chunks' round trips
