@@ -689,7 +689,7 @@ MoeRouter moe_router(const cubic_router* r) {
 
 // The routing first, then the two-kernel path's intermediates or the MLP step's workspace.
 struct LayerLayout {
-  size_t ids, weights, rec, hq, hs, mlp, fused_total, total;
+  size_t ids, weights, rec, h, partial, mlp, fused_total, total;
 };
 LayerLayout layer_layout(int64_t T, int topk, int E, int64_t H, int64_t I) {
   LayerLayout L;
@@ -699,8 +699,8 @@ LayerLayout layer_layout(int64_t T, int topk, int E, int64_t H, int64_t I) {
   L.weights = o;  o += align256(P * 4);
   L.mlp = o;
   L.rec = o;      o += align256((2 + 2 * P) * 4);
-  L.hq = o;       o += align256(P * 2 * static_cast<size_t>(I));
-  L.hs = o;       o += align256(P * 2 * static_cast<size_t>((I + 31) / 32));
+  L.h = o;        o += align256(P * 2 * static_cast<size_t>(I));
+  L.partial = o;  o += align256(P * 8 * static_cast<size_t>(I));
   L.fused_total = o;
   const size_t mlp = L.mlp + mlp_layout(T, topk, E, H, I).total;
   L.total = o > mlp ? o : mlp;
@@ -738,8 +738,7 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
   const int E = router->E, topk = router->topk;
   if (gate_up0->N != 2 * I || down0->N != H || H == 0 || I == 0) return CUBIC_ERR_SHAPE;
   if (T == 0) return CUBIC_OK;
-  const int64_t run =
-      moe_layer_tokens(T, topk, E, H, I, gate_up0->bits, gate_up0->group, down0->bits, down0->group);
+  const int64_t run = moe_layer_tokens(T, topk, E, H, I, gate_up0->bits, gate_up0->group, down0->bits);
   const bool fused = run > 0;
   if (!fused && ((st = moe_weight_fits(gate_up0)) != CUBIC_OK || (st = moe_weight_fits(down0)) != CUBIC_OK)) return st;
   if (!x_bf16 || !y || !workspace) return CUBIC_ERR_NULL;
@@ -758,7 +757,7 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
                             static_cast<int64_t>(cubic_code_bytes(w->N, w->K, w->bits)), w->bits, w->group};
     };
     const MoeLayerBuffers b{ids, weights, reinterpret_cast<int32_t*>(ws + L.rec),
-                            reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<uint8_t*>(ws + L.hs)};
+                            reinterpret_cast<uint16_t*>(ws + L.h), reinterpret_cast<float*>(ws + L.partial)};
     return hip_status(launch_moe_layer(moe_router(router), x_bf16, static_cast<int>(T), static_cast<int>(run), weight(gate_up0),
                                        weight(down0), static_cast<int>(H), static_cast<int>(I), b, topk_ids, topk_weights, y,
                                        ybf16 ? 1 : 0, s));

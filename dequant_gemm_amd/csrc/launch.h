@@ -187,12 +187,11 @@ struct MoeLayerBuffers {
   int32_t* ids;            // [T*topk]
   float* weights;          // [T*topk]
   int32_t* rec;            // [2 + 2 T*topk]: pairs with an expert, then (pair, expert) of each
-  uint8_t* hq;             // [T*topk][2][I]
-  uint8_t* hs;             // [T*topk][2][I / 32]
+  uint16_t* h;             // bf16 [T*topk][I]
+  float* partial;          // [T*topk][2I]
 };
 // Tokens that one run of the two kernels takes (0: not on this path).
-int64_t moe_layer_tokens(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
-                         int dn_group);
+int64_t moe_layer_tokens(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits);
 hipError_t launch_moe_layer(const MoeRouter& r, const uint16_t* x, int T, int run, const MoeLayerWeight& up,
                             const MoeLayerWeight& dn, int H, int I, const MoeLayerBuffers& b, int32_t* ids_user,
                             float* weights_user, void* y, int ybf16, hipStream_t st);

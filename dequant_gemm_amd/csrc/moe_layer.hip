@@ -4,44 +4,42 @@
 //   ids, w  = the router of each token's logits (router.h)
 //   [g | u] = x_t * GU_e^T;  h = bf16(SiLU(g) * u);  y_t = sum_j w_tj * (h_tj * D_e^T)
 //
-// Every touched expert's codes are read once and each serves one to eight
-// rows, so the layer is bound by HBM as long as decoding a code costs little.
-// The 2-bit codes {00, 01, 11} = {0, +1, -1} are therefore turned into 4-bit
-// floats: field b1 b0 in the top half of a nibble is the e2m1 number {0, +2, -2}
-// (sign b1, exponent b0), so sixteen codes take one shift and two masks (the
-// field 10 reads as -0 and contributes nothing; where a wave sees one, a slow
-// pass adds its level's sum). The activations are split exactly into two
-// e4m3 halves: a bf16 number has eight significant bits, hi takes the upper
-// four rounded to nearest and lo the (signed) rest, with one power-of-two block
-// scale for 32 consecutive values. hi and lo (and the tokens) are rows of the
-// same 16 x 16 x 128 MFMA. Values below 2^-14 of their block's largest are off by up to
-// 2^-22 of it, and blocks whose largest value is below 2^-116 by up to 2^-138. The MFMA
-// aligns the products of its 128 codes to the largest and drops what lies about 2^-14
-// below it: measured, its sums of normal values are off by 2^-18 to 2^-19 (rms; exact
-// where the products span less), by 2^-16 where outliers of 40 times the rest are among
-// them, and at worst by 2^-11 of the largest product. Steps are added up in fp32. The
-// result is 2^-16 off where an fp32 sum would be 2^-24, which moves about one h in a
-// hundred to the neighbouring bf16 number; exact sums would need a third row a token, and
-// hold five tokens.
+// The layer is bound by HBM as long as decoding a code costs little and codes are read once
+// for all rows that share them. Both products run on the int8 MFMA, whose sums are exact: the
+// activations are fixed-point numbers of 30 bits under a power of two for each block of 128
+// or 256 (a macro step), in four planes of signed base-256 digits, which are four rows of
+// one 16 x 16 x 64 tile; four tokens fill its rows. A bf16 number has eight significant bits,
+// so a value is exact down to 2^-22 of its block's largest and below that off by at most 2^-30
+// of it; blocks whose largest value is below 2^-90 are multiples of 2^-120. A step's sum is
+// rounded to fp32 where it leaves the integers, and steps are added up in fp32. (Two e4m3
+// halves on the scaled 16 x 16 x 128 MFMA are as many rows for eight tokens, and 2-bit codes
+// e2m1 nibbles, but that MFMA aligns 128 products to the largest and drops what lies about
+// 2^-14 below it: sums off by 2^-16, and by 2^-11 of the largest product where large products
+// cancel. Against it the layer takes 2 % longer with one and with four tokens of 7168 / 3 K,
+// 20 % with eight.)
+// 2-bit codes {00, 01, 11} = {0, +1, -1}: a field in the top bits of a byte is the signed byte
+// 64 code, so sixteen codes take three shifts and four masks. The field 10 counts as -2 there;
+// where a wave sees one, a slow pass adds what its level lacks.
 //
 // Kernel 1 (k_layer_up): every workgroup runs the router of all tokens (one wave
 // each), splits x into LDS, and then walks its share of the units (touched
-// expert, 16 gate rows and the 16 up rows beside them). Kernel 2 (k_layer_down):
-// every workgroup takes an equal share of the output rows and all pairs, one
-// (pair, K part) per wave at a time, so the router-weighted sum never leaves the
-// workgroup: no atomics, and the order of the sums does not depend on timing.
+// expert, 16 gate rows and the 16 up rows beside them); a unit's codes serve all tokens. Rows
+// of x that do not fit in LDS are taken in several launches, whose sums go through the
+// workspace. Kernel 2 (k_layer_down): every workgroup takes an equal share of the output rows
+// and all pairs, one (pair, K part) per wave at a time, so the router-weighted sum never
+// leaves the workgroup: no atomics, and the order of the sums does not depend on timing. Pairs
+// of one expert read its codes again, one soon after the other (from L2), and decode them again.
 //
 // Measured (hidden 7168, intermediate 3 K, G512, on one card whose large copy runs at
-// 5.1 TB/s): one token through 16 of 64 experts, 281 MB: kernel 1 42 us (8 us until the
-// first load is issued: router, splitting, lists; then 5.7 TB/s), kernel 2 21 us
-// (5.9 TB/s while streaming), 56-64 us together; four tokens through about 52 of 128
-// experts, 930 MB: 112 + 64 us; 4 bits, G128, 2048 x 1024, two tokens of top-4 of 32: 12.7
-// + 8.6 us. HBM traffic is 1.00 of the codes and scales. Against
+// 5.1 TB/s): one token through 16 of 64 experts, 281 MB: kernel 1 43 us (8 us until the
+// first load is issued: router, splitting, lists; then 5.7 TB/s), kernel 2 24 us, 67-70 us
+// together; four tokens through about 52 of 128 experts, 930 MB: 109 + 74 us; 4 bits, G128,
+// 2048 x 1024, two tokens of top-4 of 32: 13.5 + 8.8 us. Against
 // loads in operand order, a barrier a round and seven steps in flight, the first version,
 // kernel 1 took 62 us and kernel 2 26.
 //
 // 3- and 4-bit codes run on the same two kernels as sums of fixed functions of the code
-// (CodesWide); wider codes, more tokens and shapes beyond the kernels' LDS run as the router kernel
+// (CodesWide); wider codes, more tokens and shapes beyond the kernels' limits run as the router kernel
 // followed by the routed MLP step (moe.hip).
 #include <algorithm>
 
@@ -54,7 +52,7 @@ namespace {
 
 constexpr uint32_t kRsrc3 = 0x00020000u;       // raw buffer, 32-bit data format
 constexpr int kLayerWaves = 16;                // one workgroup of 1024 threads per compute unit
-constexpr int kLayerMaxT = 8;                  // hi and lo rows of eight tokens fill the MFMA's 16 rows
+constexpr int kLayerMaxT = 8;                  // two tiles of four tokens' planes
 constexpr int kLayerMaxE = 1024;               // experts of one router wave (4 or 16 per lane)
 constexpr int kLayerMaxPairs = kLayerMaxT * kRouterMaxTopk;
 
@@ -71,124 +69,141 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// ---- the two e4m3 halves of bf16 values -----------------------------------
-// Block scale of a largest magnitude (finite; its fp32 bits): with ef the
-// (clamped) exponent field, v * 2^(134 - ef) lies below 256 and its largest
-// in [128, 256). Scale bytes (E8M0): ef - 7 for hi, ef - 11 for lo.
-__device__ __forceinline__ uint32_t block_exponent(float amax) {
-  const uint32_t ef = __float_as_uint(amax) >> 23;
-  return ef < 11u ? 11u : ef;
-}
-__device__ __forceinline__ float block_factor(uint32_t ef) { return __uint_as_float((261u - ef) << 23); }
+// ---- activations in fixed point --------------------------------------------
+// A block of activations (the codes of a macro step) shares an exponent: with ef the
+// (clamped) exponent field of its largest magnitude, X = rint(v 2^(156 - ef)) lies in
+// -2^30 .. 2^30 and is four signed bytes in base 256. The block's factor 2^(ef - 162) takes
+// the 64 of a code's unit with it; it has to be a normal number, so blocks whose largest
+// magnitude is below 2^-90 are multiples of 2^-120.
+constexpr int kPlanes = 4;
+__device__ __forceinline__ float fixed_factor(uint32_t ef) { return __uint_as_float((283u - ef) << 23); }
+__device__ __forceinline__ float block_factor(uint32_t ef) { return __uint_as_float((ef - 35u) << 23); }
 
-// Halves of two values: bytes 0 and 1 of hi and lo. Non-finite values become
-// NaN (0x7f) in hi, so their rows come out NaN.
-__device__ __forceinline__ void split2(float a, float b, float f, uint32_t& hi, uint32_t& lo) {
-  const bool fa = fabsf(a) < __builtin_inff(), fb = fabsf(b) < __builtin_inff();
-  const float va = fa ? a * f : 0.0f, vb = fb ? b * f : 0.0f;
-  hi = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(va, vb, 0, false)) & 0xffffu;
-  const float ra = (va - __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(hi), 0)) * 16.0f;
-  const float rb = (vb - __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(hi), 1)) * 16.0f;
-  lo = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(ra, rb, 0, false)) & 0xffffu;
-  hi = (fa ? hi : (hi & 0xff00u) | 0x7fu);
-  hi = (fb ? hi : (hi & 0x00ffu) | 0x7f00u);
+// X as four signed base-256 digits, the lowest in byte 0. (The limits are for values that are
+// not finite, whose block's factor is NaN.)
+__device__ __forceinline__ uint32_t digits(float v, float f) {
+  const int x = __float2int_rn(__builtin_amdgcn_fmed3f(v * f, -0x1p30f, 0x1p30f));
+  return (static_cast<uint32_t>(x) + 0x00808080u) ^ 0x00808080u;
 }
-
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a < __builtin_inff() ? a : 0.0f;
+// The largest of G (8 or 16) neighbouring lanes' values, in each of them.
+template <int G>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+  v = max(v, dpp_move<0xB1>(v));               // quad_perm [1, 0, 3, 2]
+  v = max(v, dpp_move<0x4E>(v));               // quad_perm [2, 3, 0, 1]
+  v = max(v, dpp_move<0x141>(v));              // row_half_mirror
+  if constexpr (G == 16) v = max(v, dpp_move<0x140>(v));   // row_mirror
+  return v;
 }
 
-// Place of code c (0..31) of a 32-code chunk among the chunk's 32 operand bytes. 2-bit
-// codes: dword d of the decoded chunk holds the even (d even) or odd codes of code word
-// d / 2; wider codes: the even or odd ones of codes 8 (d / 2) .. + 7.
-__device__ __forceinline__ int code_slot(int c, bool wide) {
-  return 16 * (c >> 4) + (wide ? 8 * ((c & 15) >> 3) + 4 * (c & 1) + ((c & 7) >> 1) : 8 * (c & 1) + ((c & 15) >> 1));
+// One operand: sixteen consecutive bf16 values (raw, two 16-byte pieces) of a block of
+// 16 G values, whose operands lie in G neighbouring lanes. Returns the block's factor; plane
+// r (weight 256^r) gets sixteen digits in the order in which the codes are decoded: dword q
+// of 2-bit codes holds codes q, q + 4, q + 8, q + 12; of wider codes the even (q even) or odd
+// ones of codes 8 (q / 2) .. + 7.
+template <bool WIDE, int G>
+__device__ __forceinline__ float split16(const u32x4& r0, const u32x4& r1, u32x4* plane) {
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t w = j < 4 ? r0[j & 3] : r1[j & 3];
+    v[2 * j] = __uint_as_float(w << 16);
+    v[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
+  }
+  uint32_t top = 0u;                           // magnitudes order as their bits, what is not finite last
+#pragma unroll
+  for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  top = block_max<G>(top);
+  const bool finite = top < 0x7f800000u;
+  const uint32_t ef = finite ? max(top >> 23, 36u) : 36u;
+  const float f = fixed_factor(ef);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = digits(v[WIDE ? 8 * (q >> 1) + (q & 1) + 2 * i : q + 4 * i], f);
+    const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u), b = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
+    const uint32_t c = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u), e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+    plane[0][q] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+    plane[1][q] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    plane[2][q] = __builtin_amdgcn_perm(e, c, 0x05040100u);
+    plane[3][q] = __builtin_amdgcn_perm(e, c, 0x07060302u);
+  }
+  return finite ? block_factor(ef) : __builtin_nanf("");
 }
-// Place of 32-chunk b of a row: with SPL = 2 a lane's 16-byte load holds two
-// chunks, which feed two MFMAs (a macro step of 256 codes, lane group kq takes
-// chunks 2 kq and 2 kq + 1, MFMA h the h-th of each).
+
+// Place of operand o (codes 16 o .. + 15 of a row) in a plane's bytes. Lane group kq of a
+// macro step owns 32 SPL consecutive codes, 2 SPL operands; the MFMA of operand d takes the
+// d-th of each group.
 template <int SPL>
-__device__ __forceinline__ int chunk_place(int b) {
-  return SPL == 2 ? (b & ~7) + ((b & 1) << 2) + ((b & 7) >> 1) : b;
+__device__ __forceinline__ int operand_place(int o) {
+  constexpr int kOps = 2 * SPL;
+  return 128 * SPL * (o / (4 * kOps)) + 64 * (o % kOps) + 16 * (o / kOps % 4);
+}
+
+// The four planes' sums of one token (rows 4 t .. 4 t + 3 of the MFMA are registers of one
+// lane) as one number: both halves are exact integers, rounded to fp32 once each.
+__device__ __forceinline__ float plane_sum(const i32x4& s) {
+  return fmaf(static_cast<float>(s[3] * 256 + s[2]), 65536.0f, static_cast<float>(s[1] * 256 + s[0]));
 }
 
 // ---- the two kinds of codes ---------------------------------------------------
-// Both multiply the activations' e4m3 halves (rows 2 t and 2 t + 1 of the MFMA for token
-// t). 2-bit codes are e2m1 nibbles; a lane's operand is one or two 32-code chunks.
+// Both multiply the activations' planes (rows 4 t .. + 3 of the MFMA for token t).
 template <int SPL_>
 struct Codes2 {
   static constexpr bool kWide = false;
   static constexpr int kBits = 2, SPL = SPL_;
-  static constexpr int DW = 2 * SPL_, W = DW;  // dwords of a lane's loads, and of its operand codes
-  static constexpr int kPiece = 4 * DW;        // bytes between the loads of neighbouring lanes
+  static constexpr int DW = 2 * SPL_;          // dwords of a lane's loads: one an operand
 };
 // 3- and 4-bit codes j = -M .. K (M = 2^(B-1), K = M - 1): with n = |j| and c = 1 - a - b
 // their level s (a t + b t |t| + c t^3), t = j / K, is a sum of three fixed odd functions
 //   p1 = j,  p2 = +-n (M - n),  p3 = +-n (M - n) (n - M / 2):
 //   level = s ((a / K + M b / K^2 + M^2 c / K^3) p1 - (b / K^2 + 1.5 M c / K^3) p2 - c / K^3 p3)
-// whose products with the activations' halves MFMAs sum exactly: the values are e4m3
-// numbers (four significant bits), looked up four at a time by byte permutes in registers,
-// and the coefficients of a group enter with its scale. A table of a group's levels costs
-// its building and an LDS read a code (2048 x 1024, W4 G128, two tokens: 17.5 + 11.2 us
-// with tables).
-// 4 bits: a code is -8 sign + l. The low bits l of j and of -j add up to 8, where p2 is
-// even and p3 odd, so both need only l, and p2 the sign; p1 = (l - 4) +- 4, and p3 + l - 4
-// has four significant bits (p3 has not): fourteen operations for eight codes and four
-// MFMAs. Whole 16-entry look-ups of three functions took 26 and three (7168 x 2 K, 8
-// tokens: 419 us against 291 to 310); l and the unsigned code as they stand (small e4m3
-// numbers) take twelve, but their sums' cancellation costs two bits (2^-14.5). 3 bits:
-// three look-ups in eight entries.
-// The MFMA wants codes 16 kq .. + 15 and 64 + 16 kq .. + 15 of a step in lane group kq.
-// 4 bits: loaded as 8-byte pieces of either half; 3 bits: as 12-byte chunks of 32 codes,
-// of which two lane groups take a half each.
+// whose values are small integers, looked up four at a time by byte permutes in registers and
+// summed exactly against the planes; the coefficients of a group enter with its scale. A table
+// of a group's levels costs its building and an LDS read a code (2048 x 1024, W4 G128, two
+// tokens: 17.5 + 11.2 us with tables).
+// 4 bits: a code is -8 sign + l. 16 p1 is the nibble in a byte's upper half; the low bits l of
+// j and of -j add up to 8, where l (8 - l) is even and p3 odd, so p3 needs only l, and p2 the
+// sign, spread over its byte by a permute.
+// 3 bits: three look-ups in eight entries.
 template <int B>
 struct CodesWide {
   static constexpr bool kWide = true;
   static constexpr int kBits = B, SPL = 1;
-  static constexpr int DW = B, W = 4;
-  static constexpr int kPiece = B == 4 ? 8 : 12;
+  static constexpr int DW = B;
   static constexpr int M = 1 << (B - 1), K = M - 1;
-  static constexpr int kSums = B == 4 ? 4 : 3; // MFMAs a step
+  static constexpr int kP1 = B == 4 ? 16 : 1;  // p1's factor
 };
 
-// An integer of at most four significant bits as an e4m3 number.
-constexpr uint32_t e4m3_int(int v) {
-  uint32_t m = static_cast<uint32_t>(v < 0 ? -v : v), e = 0;
-  if (m == 0) return 0u;
-  while (m >= 16u) { m >>= 1; ++e; }           // (exact: the bits shifted out are zero)
-  while (m < 8u) { m <<= 1; --e; }
-  return ((e + 10u) << 3 | (m & 7u)) | (v < 0 ? 0x80u : 0u);   // m 2^e = m/8 2^(e+3), bias 7
-}
 // Four bytes of f(j0) .. f(j0 + 3).
 template <class Fn>
-constexpr uint32_t e4m3_bytes(Fn f, int j0) {
+constexpr uint32_t i8_bytes(Fn f, int j0) {
   uint32_t v = 0;
-  for (int i = 0; i < 4; ++i) v |= e4m3_int(f(j0 + i)) << (8 * i);
+  for (int i = 0; i < 4; ++i) v |= (static_cast<uint32_t>(f(j0 + i)) & 0xffu) << (8 * i);
   return v;
 }
-// The lane's 32 operand codes (w: 16 and 16; the even and odd ones of eight in turn) as
-// bytes. 4 bits: b = l - 4, +-4, p2, p3 + l - 4; 3 bits: p1, p2, p3.
+// Operand d (16 codes) of the lane's 32: b[0] = kP1 p1, b[1] = p2, b[2] = p3.
 template <int B>
-__device__ __forceinline__ void poly_decode(const uint32_t* w, i32x8* b) {
+__device__ __forceinline__ void poly_decode(const uint32_t* w, int d, i32x4* b) {
   if constexpr (B == 4) {
     constexpr auto p2 = [](int l) { return l * (8 - l); };
-    constexpr auto p3l4 = [](int l) { return l * (8 - l) * (l - 4) + l - 4; };
-    constexpr auto l4 = [](int l) { return l - 4; };
-    constexpr uint32_t four = e4m3_int(4) * 0x01010101u, d0 = e4m3_bytes(l4, 0), d4 = e4m3_bytes(l4, 4);
-    constexpr uint32_t a0 = e4m3_bytes(p2, 0), a4 = e4m3_bytes(p2, 4), c0 = e4m3_bytes(p3l4, 0), c4 = e4m3_bytes(p3l4, 4);
+    constexpr auto m2 = [](int l) { return -l * (8 - l); };
+    constexpr auto p3 = [](int l) { return l * (8 - l) * (l - 4); };
+    constexpr uint32_t a0 = i8_bytes(p2, 0), a4 = i8_bytes(p2, 4), n0 = i8_bytes(m2, 0), n4 = i8_bytes(m2, 4);
+    constexpr uint32_t c0 = i8_bytes(p3, 0), c4 = i8_bytes(p3, 4);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {              // eight codes
-      const uint32_t v = w[u], vs = v >> 4;
-      const uint32_t le = v & 0x07070707u, lo = vs & 0x07070707u;
-      b[0][2 * u] = static_cast<int>(__builtin_amdgcn_perm(d4, d0, le));
-      b[0][2 * u + 1] = static_cast<int>(__builtin_amdgcn_perm(d4, d0, lo));
-      b[1][2 * u] = static_cast<int>(((v << 4) & 0x80808080u) | four);
-      b[1][2 * u + 1] = static_cast<int>((v & 0x80808080u) | four);
-      b[2][2 * u] = static_cast<int>(((v << 4) & 0x80808080u) | __builtin_amdgcn_perm(a4, a0, le));
-      b[2][2 * u + 1] = static_cast<int>((v & 0x80808080u) | __builtin_amdgcn_perm(a4, a0, lo));
-      b[3][2 * u] = static_cast<int>(__builtin_amdgcn_perm(c4, c0, le));
-      b[3][2 * u + 1] = static_cast<int>(__builtin_amdgcn_perm(c4, c0, lo));
+    for (int u = 0; u < 2; ++u) {              // eight codes: the even ones, then the odd ones
+      const uint32_t v = w[2 * d + u], vl = v << 4;
+      const uint32_t le = v & 0x07070707u, lo = (v >> 4) & 0x07070707u;
+      // the sign bits of four bytes as byte masks (selectors 8 .. 11: bytes 1, 3 of either source)
+      const uint32_t se = __builtin_amdgcn_perm(vl, vl << 8, 0x0b090a08u);
+      const uint32_t so = __builtin_amdgcn_perm(v, v << 8, 0x0b090a08u);
+      b[0][2 * u] = static_cast<int>(vl & 0xF0F0F0F0u);
+      b[0][2 * u + 1] = static_cast<int>(v & 0xF0F0F0F0u);
+      b[1][2 * u] = static_cast<int>((__builtin_amdgcn_perm(n4, n0, le) & se) | (__builtin_amdgcn_perm(a4, a0, le) & ~se));
+      b[1][2 * u + 1] = static_cast<int>((__builtin_amdgcn_perm(n4, n0, lo) & so) | (__builtin_amdgcn_perm(a4, a0, lo) & ~so));
+      b[2][2 * u] = static_cast<int>(__builtin_amdgcn_perm(c4, c0, le));
+      b[2][2 * u + 1] = static_cast<int>(__builtin_amdgcn_perm(c4, c0, lo));
     }
   } else {
     // codes 0 .. 3 are their values, 4 .. 7 those less 8
@@ -196,13 +211,14 @@ __device__ __forceinline__ void poly_decode(const uint32_t* w, i32x8* b) {
     constexpr auto p1 = [](int j) { return j; };
     constexpr auto p2 = [sign](int j) { return j * (4 - sign(j) * j); };
     constexpr auto p3 = [sign](int j) { return j * (4 - sign(j) * j) * (sign(j) * j - 2); };
-    constexpr uint32_t t[3][2] = {{e4m3_bytes(p1, 0), e4m3_bytes(p1, -4)},
-                                  {e4m3_bytes(p2, 0), e4m3_bytes(p2, -4)},
-                                  {e4m3_bytes(p3, 0), e4m3_bytes(p3, -4)}};
+    constexpr uint32_t t[3][2] = {{i8_bytes(p1, 0), i8_bytes(p1, -4)},
+                                  {i8_bytes(p2, 0), i8_bytes(p2, -4)},
+                                  {i8_bytes(p3, 0), i8_bytes(p3, -4)}};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t* q = w + 2 * (u >> 1);    // 48 bits
-      const uint32_t v = (u & 1) ? __builtin_amdgcn_alignbit(q[1], q[0], 24) : q[0];
+    for (int u = 0; u < 2; ++u) {              // 24 bits: eight codes
+      const int g = 2 * d + u;
+      const uint32_t v = g == 0 ? w[0] : g == 1 ? __builtin_amdgcn_alignbit(w[1], w[0], 24)
+                                     : g == 2 ? __builtin_amdgcn_alignbit(w[2], w[1], 16) : w[2] >> 8;
       // fields of three bits at 0, 3, 6, 9 and 16, 19, 22, 25; then those of even and odd codes in bytes
       const uint32_t y = (v & 0xFFFu) | ((v & 0xFFF000u) << 4);
       const uint32_t se = (y & 0x00070007u) | ((y & 0x01C001C0u) << 2);
@@ -249,11 +265,7 @@ struct CodeStream {
   __device__ __forceinline__ void issue(const CodeSrc& src, const uint32_t* vcode, int t) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if constexpr (F::kBits == 4) {
-        const u32x2 v0 = __builtin_amdgcn_raw_buffer_load_b64(src.code, vcode[i], t * 64, 0);
-        const u32x2 v1 = __builtin_amdgcn_raw_buffer_load_b64(src.code, vcode[i], t * 64 + 32, 0);
-        cb[U][i][0] = v0.x; cb[U][i][1] = v0.y; cb[U][i][2] = v1.x; cb[U][i][3] = v1.y;
-      } else if constexpr (DW == 4) {
+      if constexpr (DW == 4) {
         const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.code, vcode[i], t * (4 * DW * 4), 0);
         cb[U][i][0] = v.x; cb[U][i][1] = v.y; cb[U][i][2] = v.z; cb[U][i][3] = v.w;
       } else if constexpr (DW == 3) {
@@ -292,137 +304,118 @@ struct CodeStream {
   }
   // slot U in operand order: w[tile][dword], s[tile] and (wide codes) a | b in sh[tile]
   template <int U>
-  __device__ __forceinline__ void take(int nl, int kq, uint32_t (*w)[F::W], float* s, uint32_t* sh) {
+  __device__ __forceinline__ void take(int nl, int kq, uint32_t (*w)[DW], float* s, uint32_t* sh) {
     auto from = [](int lane, uint32_t v) {
       return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(4 * lane, static_cast<int>(v)));
     };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if constexpr (F::kBits == 3) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {          // chunk 2 h + kq / 2; its upper half for odd kq
-          const int l = 4 * nl + 2 * h + (kq >> 1);
-          const uint32_t d0 = from(l, cb[U][i][0]), d1 = from(l, cb[U][i][1]), d2 = from(l, cb[U][i][2]);
-          w[i][2 * h] = (kq & 1) ? __builtin_amdgcn_alignbit(d2, d1, 16) : d0;
-          w[i][2 * h + 1] = (kq & 1) ? d2 >> 16 : d1;
-        }
-      } else {
-#pragma unroll
-        for (int d = 0; d < DW; ++d) w[i][d] = from(4 * nl + kq, cb[U][i][d]);
-      }
+      for (int d = 0; d < DW; ++d) w[i][d] = from(4 * nl + kq, cb[U][i][d]);
       s[i] = __uint_as_float(from(4 * nl + (U & 3), __float_as_uint(sc[i][U / 4])));
       if constexpr (F::kWide) sh[i] = from(4 * nl + (U & 3), ab[i][U / 4]);
     }
   }
 };
 
-// One macro step: A rows from LDS (xr: this lane's row, its bytes in operand
-// order; sr: its scale bytes), B from the code words of NT tiles. The step's sum
-// of hi + lo, times the group scale, goes to acc[tile][token 0 / 1 of the lane].
-// MODE 0: the codes 0, +1, -1; their unused field is collected in bad. MODE 1:
-// the unused field alone, as +1 (the slow pass).
-template <int SPL, int NT, int MODE>
-__device__ __forceinline__ void layer_step(const uint32_t (*w)[2 * SPL], const float* sc, const uint8_t* xr,
-                                           const uint8_t* sr, int t, int kq, float (*acc)[2], uint32_t& bad) {
-  uint32_t sx;
-  if constexpr (SPL == 2) {
-    sx = *reinterpret_cast<const uint16_t*>(sr + t * 8 + kq * 2);
-  } else {
-    sx = sr[t * 4 + kq];
-  }
-  f32x4 part[NT];
+// The activations of a lane: its row (a token's plane) and its token's block factors in
+// LDS, per tile of sixteen rows (four tokens).
+template <int MT>
+struct Acts {
+  const uint8_t* row[MT];
+  const float* factor[MT];
+};
+
+// One macro step of 2-bit codes: the step's sums, times block factor and group scale, go to
+// acc[tile][tokens' tile]. A field in a byte's top bits is the signed byte 64 code.
+// MODE 0: the field 10 counts as -2 and is collected in bad. MODE 1: the field 10 alone, as +1
+// (the slow pass).
+template <int SPL, int NT, int MT, int MODE>
+__device__ __forceinline__ void layer_step(const uint32_t (*w)[2 * SPL], const float* sc, const Acts<MT>& x, int t, int kq,
+                                           float (*acc)[MT], uint32_t& bad) {
+  i32x4 part[NT][MT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) part[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-  for (int h = 0; h < SPL; ++h) {
-    const u32x4 a0 = *reinterpret_cast<const u32x4*>(xr + (t * SPL + h) * 128 + 16 * kq);
-    const u32x4 a1 = *reinterpret_cast<const u32x4*>(xr + (t * SPL + h) * 128 + 64 + 16 * kq);
-    const i32x8 a = {static_cast<int>(a0.x), static_cast<int>(a0.y), static_cast<int>(a0.z), static_cast<int>(a0.w),
-                     static_cast<int>(a1.x), static_cast<int>(a1.y), static_cast<int>(a1.z), static_cast<int>(a1.w)};
+    for (int m = 0; m < MT; ++m) part[i][m] = i32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int d = 0; d < 2 * SPL; ++d) {
+    i32x4 a[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) a[m] = *reinterpret_cast<const i32x4*>(x.row[m] + t * (128 * SPL) + 64 * d + 16 * kq);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      i32x8 b = {};
+      const uint32_t v = w[i][d];
+      i32x4 b;
+      if constexpr (MODE == 0) {
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const uint32_t v = w[i][2 * h + d];
-        if constexpr (MODE == 0) {
-          b[2 * d] = static_cast<int>((v << 2) & 0xCCCCCCCCu);
-          b[2 * d + 1] = static_cast<int>(v & 0xCCCCCCCCu);
-          bad |= v & ~(v << 1);
-        } else {
-          const uint32_t f = v & ~(v << 1) & 0xAAAAAAAAu;
-          b[2 * d] = static_cast<int>((f << 1) & 0x44444444u);
-          b[2 * d + 1] = static_cast<int>((f >> 1) & 0x44444444u);
-        }
-      }
-      // scale 2^-1 on the codes: the nibbles are +-2
-      if (h == 0) {
-        part[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part[i], 0, 4, 0, static_cast<int>(sx), 0, 126);
+        for (int q = 0; q < 4; ++q) b[q] = static_cast<int>((v << (6 - 2 * q)) & 0xC0C0C0C0u);
+        bad |= v & ~(v << 1);
       } else {
-        part[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part[i], 0, 4, 1, static_cast<int>(sx), 0, 126);
+        const uint32_t f = (v & ~(v << 1) & 0xAAAAAAAAu) >> 1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) b[q] = static_cast<int>((f << (6 - 2 * q)) & 0x40404040u);
       }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) part[i][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[m], b, part[i][m], 0, 0, 0);
     }
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    acc[i][0] = fmaf(sc[i], part[i][0] + part[i][1], acc[i][0]);
-    acc[i][1] = fmaf(sc[i], part[i][2] + part[i][3], acc[i][1]);
+  for (int m = 0; m < MT; ++m) {
+    const float f = x.factor[m][t];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][m] = fmaf(f, sc[i] * plane_sum(part[i][m]), acc[i][m]);
   }
 }
 
 // The same for wide codes, sh: the tiles' shapes a | b.
-template <int B, int NT>
-__device__ __forceinline__ void wide_step(const uint32_t (*w)[4], const float* sc, const uint32_t* sh, const uint8_t* xr,
-                                          const uint8_t* sr, int t, int kq, float (*acc)[2]) {
+template <int B, int NT, int MT>
+__device__ __forceinline__ void wide_step(const uint32_t (*w)[B], const float* sc, const uint32_t* sh, const Acts<MT>& x,
+                                          int t, int kq, float (*acc)[MT]) {
   constexpr float K = CodesWide<B>::K, M = CodesWide<B>::M;
-  constexpr int NS = CodesWide<B>::kSums;
-  const int sx = sr[t * 4 + kq];
-  const u32x4 a0 = *reinterpret_cast<const u32x4*>(xr + t * 128 + 16 * kq);
-  const u32x4 a1 = *reinterpret_cast<const u32x4*>(xr + t * 128 + 64 + 16 * kq);
-  const i32x8 a = {static_cast<int>(a0.x), static_cast<int>(a0.y), static_cast<int>(a0.z), static_cast<int>(a0.w),
-                   static_cast<int>(a1.x), static_cast<int>(a1.y), static_cast<int>(a1.z), static_cast<int>(a1.w)};
+  i32x4 a[2][MT];
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) a[d][m] = *reinterpret_cast<const i32x4*>(x.row[m] + t * 128 + 64 * d + 16 * kq);
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    i32x8 b[NS];
-    poly_decode<B>(w[i], b);
-    f32x4 part[NS];
+    i32x4 part[3][MT];
 #pragma unroll
-    for (int f = 0; f < NS; ++f) {
-      constexpr f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-      part[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[f], zero, 0, 0, 0, sx, 0, 127);
+    for (int d = 0; d < 2; ++d) {
+      i32x4 b[3];
+      poly_decode<B>(w[i], d, b);
+#pragma unroll
+      for (int f = 0; f < 3; ++f)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          constexpr i32x4 zero = {0, 0, 0, 0};
+          part[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[d][m], b[f], d ? part[f][m] : zero, 0, 0, 0);
+        }
     }
+    // (64: a code's unit in the block factor)
     const float sa = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sh[i] & 0xffffu)));
     const float sb = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sh[i] >> 16)));
-    const float c = (1.0f - sa - sb) * (1.0f / (K * K * K));
-    const float k1 = sc[i] * fmaf(M * M, c, fmaf(sb, M / (K * K), sa * (1.0f / K)));
-    const float k2 = sc[i] * -fmaf(1.5f * M, c, sb * (1.0f / (K * K)));
+    const float c = (1.0f - sa - sb) * (64.0f / (K * K * K));
+    constexpr float p1 = 1.0f / CodesWide<B>::kP1;
+    const float k1 = sc[i] * fmaf(M * M * p1, c, fmaf(sb, 64.0f * M * p1 / (K * K), sa * (64.0f * p1 / K)));
+    const float k2 = sc[i] * -fmaf(1.5f * M, c, sb * (64.0f / (K * K)));
     const float k3 = sc[i] * -c;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      float p[NS];
-#pragma unroll
-      for (int f = 0; f < NS; ++f) p[f] = part[f][2 * m] + part[f][2 * m + 1];
-      if constexpr (B == 4) {
-        acc[i][m] = fmaf(k1, p[0] + p[1], acc[i][m]);
-        acc[i][m] = fmaf(k2, p[2], acc[i][m]);
-        acc[i][m] = fmaf(k3, p[3] - p[0], acc[i][m]);
-      } else {
-        acc[i][m] = fmaf(k1, p[0], acc[i][m]);
-        acc[i][m] = fmaf(k2, p[1], acc[i][m]);
-        acc[i][m] = fmaf(k3, p[2], acc[i][m]);
-      }
+    for (int m = 0; m < MT; ++m) {
+      const float v = fmaf(k3, plane_sum(part[2][m]), fmaf(k2, plane_sum(part[1][m]), k1 * plane_sum(part[0][m])));
+      acc[i][m] = fmaf(x.factor[m][t], v, acc[i][m]);
     }
   }
 }
 
 // The slow pass: the level of the field 10 (code -2) is -q(2) s, q(2) = 2 a + 4 b +
-// 8 (1 - a - b); its codes' sums are added step by step. Loads in operand order:
-// vcode, vscale as in the stream, but of row nl and quarter kq.
-template <int SPL, int NT>
+// 8 (1 - a - b), of which the sums above hold -2 s; the rest is added step by step. Loads in
+// operand order: vcode, vscale as in the stream, but of row nl and quarter kq.
+template <int SPL, int NT, int MT>
 __device__ __forceinline__ void layer_extra(const CodeSrc& src, const __amdgpu_buffer_rsrc_t& shp,
                                             const uint32_t* vcode, const uint32_t* vscale, int tb, int te, int by,
-                                            const Groups& gr, const uint8_t* xr, const uint8_t* sr, int kq,
-                                            float (*acc)[2]) {
+                                            const Groups& gr, const Acts<MT>& x, int t0, int kq, float (*acc)[MT]) {
 #pragma unroll 1
   for (int t = tb; t < te; t += by) {
     CodeStream<Codes2<SPL>, 1, NT> st;
@@ -435,10 +428,10 @@ __device__ __forceinline__ void layer_extra(const CodeSrc& src, const __amdgpu_b
       const uint32_t ab = __builtin_amdgcn_raw_buffer_load_b32(shp, vscale[i], g * 4, 0);
       const double a = f16_bits_to_f64(static_cast<uint16_t>(ab & 0xffffu));
       const double b = f16_bits_to_f64(static_cast<uint16_t>(ab >> 16));
-      lev[i] = static_cast<float>(-static_cast<double>(s) * level_numerator(a, b, 2, 1));
+      lev[i] = static_cast<float>(-static_cast<double>(s) * (level_numerator(a, b, 2, 1) - 2.0));
     }
     uint32_t none = 0u;
-    layer_step<SPL, NT, 1>(st.cb[0], lev, xr, sr, t, kq, acc, none);
+    layer_step<SPL, NT, MT, 1>(st.cb[0], lev, x, t - t0, kq, acc, none);
   }
 }
 
@@ -495,19 +488,20 @@ struct LayerUpParams {
   Groups groups;           // steps per group
   float share;             // 1 / (workgroups * waves)
   int batch;               // rounds between the joins of the waves' sums
-  int down_spl;            // operand order of h: chunks per lane and step of 2-bit down codes; 0: wider codes
+  int k0, steps;           // macro steps of this launch: k0 .. k0 + steps - 1
+  int add, last;           // the sums start from `partial`; they are whole (else they go there)
+  float* partial;          // [T*topk][2I]
   int32_t* ids;            // [T][topk] out
   float* weights;
   int32_t* ids_user;       // a second copy for the caller, or NULL
   float* weights_user;
   int32_t* rec;
-  uint8_t* hq;             // [T*topk][2][I] e4m3 halves of h in operand order
-  uint8_t* hs;             // [T*topk][2][I / 32] block scales
+  uint16_t* h;             // bf16 [T*topk][I]
 };
 
 // K parts of kernel 1: the waves of a tile, so many that the slowest workgroup has the
 // least to do (units: touched experts' tiles; kRoundCost: eighths of a step that a round
-// costs beside its steps). At least two teams: a scale block of h spans two tiles. The
+// costs beside its steps). At least two teams: h leaves in pieces of two tiles. The
 // number of touched experts is known on the device alone: taken for the largest possible
 // one (64 for 8 tokens of top-8, where 41 are usual), the last of two rounds was a third
 // full, and 4 bits, 7168 x 2 K took 250 us.
@@ -531,20 +525,21 @@ __device__ __forceinline__ int layer_up_parts(int units, int nmacro, float share
 }
 
 struct LayerUpLds {
-  int xq, xs, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
-  int xq_stride, xs_stride;
+  int xq, xf, red, first, id, w, exp, slot, cand, misc, total;   // byte offsets
+  int xq_stride, xf_stride;
 };
-__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int batch) {
+// K: the activations of a token that a launch takes.
+__host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int K, int batch) {
   LayerUpLds L;
   const int P = T * topk;
   auto up16 = [](int v) { return (v + 15) & ~15; };
-  // Rows of the MFMA: two halves a token; 16 bytes of padding each: the rows' reads hit
-  // other banks.
-  L.xq_stride = H + 16;
-  L.xs_stride = up16(H / 32) + 16;
+  // Rows of the MFMA: four planes a token; 16 bytes of padding each: the rows' reads hit
+  // other banks. Block factors: at most one per 128 values.
+  L.xq_stride = K + 16;
+  L.xf_stride = K / 128;
   int o = 0;
-  L.xq = o;    o += 2 * T * L.xq_stride;
-  L.xs = o;    o += 2 * T * L.xs_stride;
+  L.xq = o;    o += kPlanes * T * L.xq_stride;
+  L.xf = o;    o += up16(T * L.xf_stride * 4);
   // partial sums, two batches of rounds: [2][batch][waves][2 tiles][T][16]; the
   // first-pair table of the experts uses the same bytes before the first round
   const int red = 2 * batch * kLayerWaves * 2 * T * 16 * 4;
@@ -560,7 +555,7 @@ __host__ __device__ inline LayerUpLds layer_up_lds(int T, int topk, int H, int b
   return L;
 }
 
-template <class F, int PM, int EPL>
+template <class F, int PM, int EPL, int MT>
 __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int SPL = F::SPL;
@@ -569,7 +564,8 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
   const int T = p.T, topk = p.r.topk, P = T * topk;
-  const LayerUpLds L = layer_up_lds(T, topk, p.H, p.batch);
+  const int K = p.steps * SPL * 128;
+  const LayerUpLds L = layer_up_lds(T, topk, K, p.batch);
   int32_t* s_first = reinterpret_cast<int32_t*>(smem + L.first);
   int32_t* s_id = reinterpret_cast<int32_t*>(smem + L.id);
   float* s_w = reinterpret_cast<float*>(smem + L.w);
@@ -591,44 +587,22 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   for (int e = tid; e < p.r.E; e += 1024) s_first[e] = INT32_MAX;
   for (int i = tid; i < 2 * P; i += 1024) reinterpret_cast<uint32_t*>(s_slot)[i] = 0xffffffffu;
   {
-    // eight values a thread; four neighbouring threads share a 32-value block
-    const int per_row = p.H / 8, all = T * per_row;
+    // one operand of sixteen values a thread; the operands of a block lie in neighbouring lanes
+    constexpr int G = 8 * SPL;
+    const int per_row = K / 16, all = T * per_row;
     for (int v0 = 0; v0 < all; v0 += 1024) {
       const int v = v0 + tid;
-      const bool on = v < all;                 // whole blocks: all is a multiple of 16
+      const bool on = v < all;                 // whole blocks: all is a multiple of G
       const int t = on ? v / per_row : 0;
-      const int q = on ? v - t * per_row : 0;
-      const u32x4 raw = *reinterpret_cast<const u32x4*>(p.x + static_cast<int64_t>(t) * p.H + 8 * q);
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(raw[j] << 16);
-        f[2 * j + 1] = __uint_as_float(raw[j] & 0xffff0000u);
-      }
-      float amax = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(f[j]));
-      amax = fmaxf(amax, __shfl_xor(amax, 1));
-      amax = fmaxf(amax, __shfl_xor(amax, 2));
-      const uint32_t ef = block_exponent(amax);
-      const float fac = block_factor(ef);
-      // even codes, then odd codes, of the eight
-      uint32_t hi[4], lo[4];
-      split2(f[0], f[2], fac, hi[0], lo[0]);
-      split2(f[4], f[6], fac, hi[1], lo[1]);
-      split2(f[1], f[3], fac, hi[2], lo[2]);
-      split2(f[5], f[7], fac, hi[3], lo[3]);
+      const int o = on ? v - t * per_row : 0;
+      const u32x4* src = reinterpret_cast<const u32x4*>(p.x + static_cast<int64_t>(t) * p.H + p.k0 * (SPL * 128) + 16 * o);
+      u32x4 plane[kPlanes];
+      const float f = split16<F::kWide, G>(src[0], src[1], plane);
       if (on) {
-        const int b = q >> 2, qd = q & 3;      // block of the row, quarter of the block
-        const int at = 32 * chunk_place<SPL>(b) + code_slot(8 * qd, F::kWide);
+        unsigned char* dst = smem + L.xq + kPlanes * t * L.xq_stride + operand_place<SPL>(o);
 #pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-          unsigned char* dst = smem + L.xq + (2 * t + pc) * L.xq_stride + at;
-          const uint32_t* s = pc ? lo : hi;
-          *reinterpret_cast<uint32_t*>(dst) = s[0] | (s[1] << 16);
-          *reinterpret_cast<uint32_t*>(dst + (F::kWide ? 4 : 8)) = s[2] | (s[3] << 16);
-          if (qd == 0) smem[L.xs + (2 * t + pc) * L.xs_stride + b] = static_cast<uint8_t>(ef - (pc ? 11u : 7u));
-        }
+        for (int r = 0; r < kPlanes; ++r) *reinterpret_cast<u32x4*>(dst + r * L.xq_stride) = plane[r];
+        if (o % G == 0) reinterpret_cast<float*>(smem + L.xf)[t * L.xf_stride + o / G] = f;
       }
     }
   }
@@ -691,7 +665,7 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   // ---- units: round r, workgroup b, team m -> (r grid + b) teams + m ----
   const int tiles = p.I / 16;
   const int total = n * tiles;
-  const int nmacro = p.H / (SPL * 128);
+  const int nmacro = p.steps, k0 = p.k0;
   const int ks = __builtin_amdgcn_readfirstlane(layer_up_parts(total, nmacro, p.share));
   const int teams = kLayerWaves / ks;
   const int team = wave / ks, part = wave - team * ks;
@@ -700,17 +674,21 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   const int steps = (nmacro - part + ks - 1) / ks;
   const uint32_t row_bytes = static_cast<uint32_t>(p.H * F::kBits / 8);
   // a gate row of the tile, and the up row I rows below it
-  auto lane_offsets = [&](int row, int quarter, int piece, uint32_t* vc, uint32_t* vs) {
-    vc[0] = row * row_bytes + quarter * piece;
+  auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
+    vc[0] = row * row_bytes + quarter * (4 * F::DW);
     vc[1] = vc[0] + static_cast<uint32_t>(p.I) * row_bytes;
     vs[0] = static_cast<uint32_t>(row * p.gpr * 4);
     vs[1] = vs[0] + static_cast<uint32_t>(p.I * p.gpr * 4);
   };
   uint32_t vcode[2], vscale[2];
-  lane_offsets(lane >> 2, lane & 3, F::kPiece, vcode, vscale);
-  const int ml = nl < 2 * T ? nl : 0;           // rows past the tokens are not used
-  const uint8_t* xr = smem + L.xq + ml * L.xq_stride;
-  const uint8_t* sr = smem + L.xs + ml * L.xs_stride;
+  lane_offsets(lane >> 2, lane & 3, vcode, vscale);
+  Acts<MT> acts;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {               // rows past the tokens are not used
+    const int t = 4 * m + (nl >> 2), u = 4 * m + kq;
+    acts.row[m] = smem + L.xq + (t < T ? 4 * t + (nl & 3) : 0) * L.xq_stride;
+    acts.factor[m] = reinterpret_cast<const float*>(smem + L.xf) + (u < T ? u : 0) * L.xf_stride;
+  }
 
   auto unit_row = [&](int u, int64_t& e, int& j) {
     const int uu = u < total ? u : 0;
@@ -737,9 +715,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
 
   Stream st;
   CodeSrc cur = source(u);
-  st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return part + min(i, steps - 1) * ks; });
+  st.issue_scales(cur, vscale, p.groups, lane, [&](int i) { return k0 + part + min(i, steps - 1) * ks; });
   [&]<int... U>(std::integer_sequence<int, U...>) {
-    (st.template issue<U>(cur, vcode, part + min(U, steps - 1) * ks), ...);
+    (st.template issue<U>(cur, vcode, k0 + part + min(U, steps - 1) * ks), ...);
   }(std::make_integer_sequence<int, PM>{});
 
   float* red = reinterpret_cast<float*>(smem + L.red);
@@ -747,7 +725,7 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   int slot_r = 0, half = 0, r0 = 0;            // round of the batch, its buffer, its first round
   for (int r = 0; r < rounds; ++r) {
     const CodeSrc nxt = source(u + stride);
-    float acc[2][2] = {};
+    float acc[2][MT] = {};
     uint32_t bad = 0u;
     for (int t0 = 0; t0 < steps; t0 += PM) {
       // the next block: this unit's next PM steps, or the next unit's first
@@ -758,11 +736,11 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
       src.scale = more ? cur.scale : nxt.scale;
       if constexpr (F::kWide) src.shape = more ? cur.shape : nxt.shape;
       const int tn = more ? t0 + PM : 0;
-      st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return part + min(tn + i, steps - 1) * ks; });
+      st.issue_scales(src, vscale, p.groups, lane, [&](int i) { return k0 + part + min(tn + i, steps - 1) * ks; });
       [&]<int... U>(std::integer_sequence<int, U...>) {
         (([&] {
            if (t0 + U < steps) {
-             uint32_t w[2][F::W];
+             uint32_t w[2][F::DW];
              float s[2];
 #pragma unroll
              for (int i = 0; i < 2; ++i)
@@ -772,12 +750,12 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
              st.template take<U>(nl, kq, w, s, sh);
              const int t = part + (t0 + U) * ks;
              if constexpr (F::kWide) {
-               wide_step<F::kBits, 2>(w, s, sh, xr, sr, t, kq, acc);
+               wide_step<F::kBits, 2, MT>(w, s, sh, acts, t, kq, acc);
              } else {
-               layer_step<SPL, 2, 0>(w, s, xr, sr, t, kq, acc, bad);
+               layer_step<SPL, 2, MT, 0>(w, s, acts, t, kq, acc, bad);
              }
            }
-           st.template issue<U>(src, vcode, part + min(tn + U, steps - 1) * ks);
+           st.template issue<U>(src, vcode, k0 + part + min(tn + U, steps - 1) * ks);
            __builtin_amdgcn_sched_barrier(0);
          }()),
          ...);
@@ -791,18 +769,17 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
         const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (e * 2 * p.I + 16 * j) * p.gpr,
                                                       static_cast<uint32_t>(p.I + 16) * 4u * static_cast<uint32_t>(p.gpr));
         uint32_t vc[2], vs[2];
-        lane_offsets(nl, kq, F::kPiece, vc, vs);
-        layer_extra<SPL, 2>(cur, shp, vc, vs, part, nmacro, ks, p.groups, xr, sr, kq, acc);
+        lane_offsets(nl, kq, vc, vs);
+        layer_extra<SPL, 2, MT>(cur, shp, vc, vs, k0 + part, k0 + nmacro, ks, p.groups, acts, k0, kq, acc);
       }
     }
-    // partial sums of the team's waves meet in LDS; lane group kq holds tokens 2 kq
-    // and 2 kq + 1
+    // partial sums of the team's waves meet in LDS; lane group kq holds tokens kq and 4 + kq
     float* rb = red + (half * p.batch + slot_r) * red_round;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-      if (2 * kq + m < T)
+    for (int m = 0; m < MT; ++m)
+      if (4 * m + kq < T)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + 2 * kq + m) * 16 + nl] = acc[i][m];
+        for (int i = 0; i < 2; ++i) rb[wave * red_wave + (i * T + 4 * m + kq) * 16 + nl] = acc[i][m];
     cur = nxt;
     u += stride;
     ++slot_r;
@@ -810,7 +787,7 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
     // A join of the waves every `batch` rounds: in between they run apart, so that a
     // wave whose loads come late holds nobody up. Two batches of sums: one barrier.
     lds_barrier();
-    // h of two neighbouring tiles: one scale block of 32 values per half wave
+    // h of two neighbouring tiles: 32 values per half wave
     const int pairs = teams / 2;
     const int nsub = slot_r * pairs * T;
     const float* hb = red + half * p.batch * red_round;
@@ -832,23 +809,20 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
           uu += src[k * red_wave + T * 16];
         }
       }
-      const float v = g / (1.0f + expf(-g)) * uu;
-      // rounded to bf16, as the down product's activations are (NaN stays NaN)
-      const float h = v != v ? v : __uint_as_float(bf16_rne_bits(v) << 16);
-      float amax = finite_abs(h);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-      const uint32_t ef = block_exponent(amax);
-      uint32_t hi, lo;
-      split2(h, h, block_factor(ef), hi, lo);
-      if (slot != 0xff) {
-        const int b = j / 2;
-        const int place = 32 * (p.down_spl == 2 ? chunk_place<2>(b) : b) + code_slot(c, p.down_spl == 0);
-        uint8_t* hq = p.hq + static_cast<int64_t>(t * topk + slot) * 2 * p.I + place;
-        hq[0] = static_cast<uint8_t>(hi);
-        hq[p.I] = static_cast<uint8_t>(lo);
-        if (c < 2) p.hs[(static_cast<int64_t>(t * topk + slot) * 2 + c) * (p.I / 32) + b] =
-            static_cast<uint8_t>(ef - (c ? 11u : 7u));
+      if (slot == 0xff) continue;
+      const int64_t pair = t * topk + slot;
+      float* sums = p.partial + pair * 2 * p.I + 16 * j + c;
+      if (p.add) {
+        g += sums[0];
+        uu += sums[p.I];
+      }
+      if (p.last) {
+        const float v = g / (1.0f + expf(-g)) * uu;
+        // rounded to bf16, as the down product's activations are (NaN stays NaN)
+        p.h[pair * p.I + 16 * j + c] = v != v ? uint16_t{0x7fc0u} : static_cast<uint16_t>(bf16_rne_bits(v));
+      } else {
+        sums[0] = g;
+        sums[p.I] = uu;
       }
     }
     half ^= 1;
@@ -861,8 +835,7 @@ struct LayerDownParams {
   const int32_t* rec;
   const float* weights;    // [T][topk]
   int T, topk;
-  const uint8_t* hq;       // [pair][2][I]
-  const uint8_t* hs;       // [pair][2][I / 32]
+  const uint16_t* h;       // bf16 [pair][I]
   const uint8_t* codes;    // down, expert 0
   const float* scales;
   const uint16_t* shapes;
@@ -877,15 +850,15 @@ struct LayerDownParams {
 };
 
 struct LayerDownLds {
-  int wave_bytes, hstride, sstride, sum, total;
+  int wave_bytes, hstride, factor, sum, total;
 };
 __host__ __device__ inline LayerDownLds layer_down_lds(int T, int I, int spl, int ks) {
   LayerDownLds L;
   const int nmacro = I / (spl * 128);
-  const int kp = (nmacro + ks - 1) / ks * spl * 128;             // K values of a part
-  L.hstride = kp + 16;
-  L.sstride = ((kp / 32 + 15) & ~15) + 16;
-  L.wave_bytes = 2 * L.hstride + 2 * L.sstride;
+  const int steps = (nmacro + ks - 1) / ks;    // of a part
+  L.hstride = steps * spl * 128 + 16;
+  L.factor = kPlanes * L.hstride;
+  L.wave_bytes = L.factor + ((steps * 4 + 15) & ~15);
   L.sum = kLayerWaves * L.wave_bytes;
   L.total = L.sum + kLayerWaves * T * 32 * 4;
   return L;
@@ -898,45 +871,28 @@ struct DownItem {
   uint32_t live;
 };
 
-// An item's h halves and block scales on their way into the wave's LDS: the first
-// 6 KB (a part of 3 K values) wait in registers, so that they are loaded before the
-// codes of their item; longer parts load the rest at the store.
-template <int SPL>
+// An item's h on its way into the planes of the wave's LDS, one operand a lane: it waits in
+// registers, so that it is loaded before the codes of its item. (Split here and not by kernel
+// 1: a block's values come from several of its workgroups.)
+template <class F>
 struct DownActs {
-  static constexpr int R = 6;
-  u32x4 v[R];
-  uint32_t sv;
-  // 16-byte chunk i of the part's two half rows (n chunks each)
-  static __device__ __forceinline__ const uint8_t* chunk(const LayerDownParams& p, const DownItem& q, int i, int n) {
-    const int pc = i < n ? 0 : 1;
-    return p.hq + (static_cast<int64_t>(q.pair) * 2 + pc) * p.I + q.tb * SPL * 128 + 16 * (i - pc * n);
-  }
-  static __device__ __forceinline__ int place(const LayerDownLds& L, int i, int n) {
-    return i < n ? 16 * i : L.hstride + 16 * (i - n);
-  }
-  // dword i of the part's scales (m a row)
-  static __device__ __forceinline__ const uint8_t* scale(const LayerDownParams& p, const DownItem& q, int i, int m) {
-    const int pc = i < m ? 0 : 1;
-    return p.hs + (static_cast<int64_t>(q.pair) * 2 + pc) * (p.I / 32) + q.tb * SPL * 4 + 4 * (i - pc * m);
-  }
+  static constexpr int G = 8 * F::SPL;
+  u32x4 v[2];
   __device__ __forceinline__ void load(const LayerDownParams& p, const DownItem& q, int lane) {
-    const int n = (q.te - q.tb) * SPL * 8;
-#pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = *reinterpret_cast<const u32x4*>(chunk(p, q, min(64 * r + lane, 2 * n - 1), n));
-    sv = *reinterpret_cast<const uint32_t*>(scale(p, q, min(lane, n / 4 - 1), n / 8));
+    const int o = min(lane, (q.te - q.tb) * G - 1);
+    const u32x4* src = reinterpret_cast<const u32x4*>(p.h + static_cast<int64_t>(q.pair) * p.I + q.tb * (16 * G) + 16 * o);
+    v[0] = src[0];
+    v[1] = src[1];
   }
-  __device__ __forceinline__ void store(const LayerDownParams& p, const DownItem& q, uint8_t* hreg, uint8_t* sreg,
-                                        const LayerDownLds& L, int lane) const {
-    const int n = (q.te - q.tb) * SPL * 8, m = n / 8;
+  __device__ __forceinline__ void store(const DownItem& q, uint8_t* hreg, const LayerDownLds& L, int lane) const {
+    u32x4 plane[kPlanes];
+    const float f = split16<F::kWide, G>(v[0], v[1], plane);
+    if (lane < (q.te - q.tb) * G) {            // whole blocks
+      uint8_t* dst = hreg + operand_place<F::SPL>(lane);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (64 * r + lane < 2 * n) *reinterpret_cast<u32x4*>(hreg + place(L, 64 * r + lane, n)) = v[r];
-    for (int i = 64 * R + lane; i < 2 * n; i += 64)
-      *reinterpret_cast<u32x4*>(hreg + place(L, i, n)) = *reinterpret_cast<const u32x4*>(chunk(p, q, i, n));
-    if (lane < 2 * m) *reinterpret_cast<uint32_t*>(sreg + (lane < m ? 4 * lane : L.sstride + 4 * (lane - m))) = sv;
-    for (int i = 64 + lane; i < 2 * m; i += 64)
-      *reinterpret_cast<uint32_t*>(sreg + (i < m ? 4 * i : L.sstride + 4 * (i - m))) =
-          *reinterpret_cast<const uint32_t*>(scale(p, q, i, m));
+      for (int r = 0; r < kPlanes; ++r) *reinterpret_cast<u32x4*>(dst + r * L.hstride) = plane[r];
+      if (lane % G == 0) reinterpret_cast<float*>(hreg + L.factor)[lane / G] = f;
+    }
   }
 };
 
@@ -950,7 +906,6 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   const int nl = lane & 15, kq = lane >> 4;
   const LayerDownLds L = layer_down_lds(p.T, p.I, SPL, p.ks);
   uint8_t* hreg = smem + wave * L.wave_bytes;
-  uint8_t* sreg = hreg + 2 * L.hstride;
   float* sums = reinterpret_cast<float*>(smem + L.sum) + wave * p.T * 32;
   for (int i = lane; i < p.T * 32; i += 64) sums[i] = 0.0f;
   wave_lds_order();
@@ -960,16 +915,16 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   const int nmacro = p.I / (SPL * 128);
   const uint32_t row_bytes = static_cast<uint32_t>(p.I * F::kBits / 8);
   // a row of each tile (past the workgroup's rows: its last one, whose sums are not used)
-  auto lane_offsets = [&](int row, int quarter, int piece, uint32_t* vc, uint32_t* vs) {
+  auto lane_offsets = [&](int row, int quarter, uint32_t* vc, uint32_t* vs) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int r = min(i * p.rt + min(row, p.rt - 1), rows - 1);
-      vc[i] = r * row_bytes + quarter * piece;
+      vc[i] = r * row_bytes + quarter * (4 * F::DW);
       vs[i] = static_cast<uint32_t>(r * p.gpr * 4);
     }
   };
   uint32_t vcode[NT], vscale[NT];
-  lane_offsets(lane >> 2, lane & 3, F::kPiece, vcode, vscale);
+  lane_offsets(lane >> 2, lane & 3, vcode, vscale);
   using Item = DownItem;
   auto item_of = [&](int it) {
     Item q;
@@ -995,7 +950,7 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
   int it = wave;
   if (it < items) {                            // wave-uniform; the barrier comes after
     Stream st;
-    DownActs<SPL> hst;
+    DownActs<F> hst;
     Item q = item_of(it);
     CodeSrc cur = source(q);
     hst.load(p, q, lane);
@@ -1004,16 +959,16 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
     [&]<int... U>(std::integer_sequence<int, U...>) {
       (st.template issue<U>(cur, vcode, min(q.tb + U, q.te - 1)), ...);
     }(std::make_integer_sequence<int, PM>{});
-    const uint8_t* xr = hreg + (nl == 1 ? L.hstride : 0);   // row 0: hi, row 1: lo
-    const uint8_t* sr = sreg + (nl == 1 ? L.sstride : 0);
+    // rows 0 .. 3: the pair's planes (the others repeat them)
+    const Acts<1> acts{{hreg + (nl & 3) * L.hstride}, {reinterpret_cast<const float*>(hreg + L.factor)}};
     for (; it < items; it += kLayerWaves) {
-      hst.store(p, q, hreg, sreg, L, lane);    // the part's h into this wave's LDS
+      hst.store(q, hreg, L, lane);             // the part's h into this wave's LDS
       wave_lds_order();
       const Item qn = item_of(it + kLayerWaves);
       const CodeSrc nxt = source(qn);
       const float w = p.weights[q.pair];
       hst.load(p, qn, lane);                   // ahead of the next item's codes
-      float acc[NT][2] = {};
+      float acc[NT][1] = {};
       uint32_t bad = 0u;
       for (int t0 = q.tb; t0 < q.te; t0 += PM) {
         st.take_scales();
@@ -1027,7 +982,7 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
         [&]<int... U>(std::integer_sequence<int, U...>) {
           (([&] {
              if (t0 + U < q.te) {
-               uint32_t w4[NT][F::W];
+               uint32_t w4[NT][F::DW];
                float s[NT];
 #pragma unroll
                for (int i = 0; i < NT; ++i)
@@ -1036,9 +991,9 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
                uint32_t sh[NT];
                st.template take<U>(nl, kq, w4, s, sh);
                if constexpr (F::kWide) {
-                 wide_step<F::kBits, NT>(w4, s, sh, xr, sr, t0 + U - q.tb, kq, acc);
+                 wide_step<F::kBits, NT, 1>(w4, s, sh, acts, t0 + U - q.tb, kq, acc);
                } else {
-                 layer_step<SPL, NT, 0>(w4, s, xr, sr, t0 + U - q.tb, kq, acc, bad);
+                 layer_step<SPL, NT, 1, 0>(w4, s, acts, t0 + U - q.tb, kq, acc, bad);
                }
              }
              st.template issue<U>(src, vcode, min(tn + U, last));
@@ -1052,9 +1007,8 @@ __global__ __launch_bounds__(1024) void k_layer_down(LayerDownParams p) {
           const __amdgpu_buffer_rsrc_t shp = layer_rsrc(p.shapes + 2 * (q.e * p.H + n0) * p.gpr,
                                                         static_cast<uint32_t>(rows) * 4u * static_cast<uint32_t>(p.gpr));
           uint32_t vc[NT], vs[NT];
-          lane_offsets(nl, kq, F::kPiece, vc, vs);
-          const int back = q.tb * SPL * 128;     // (steps count from the part's first in LDS)
-          layer_extra<SPL, NT>(cur, shp, vc, vs, q.tb, q.te, 1, p.groups, xr - back, sr - q.tb * SPL * 4, kq, acc);
+          lane_offsets(nl, kq, vc, vs);
+          layer_extra<SPL, NT, 1>(cur, shp, vc, vs, q.tb, q.te, 1, p.groups, acts, q.tb, kq, acc);
         }
       }
       if (kq == 0) {
@@ -1093,46 +1047,59 @@ int layer_spl(int bits, int group) { return bits == 2 && group % 256 == 0 ? 2 : 
 
 constexpr int kLayerLds = 160 * 1024;
 
-// K parts of kernel 2: enough items for every wave, and a part's h in LDS.
+// Launches of kernel 1: the fewest whose shares of the row fit in LDS (four bytes a value).
+// Each routes again and passes its sums on through the workspace, some 8 us, where shorter
+// runs of tokens would read the shared experts' codes again (7168 / 3 K, top-16 of 128, eight
+// tokens: 100 + 106 us in two launches; two runs of four 218).
+int layer_up_launches(int T, int topk, int H, int spl) {
+  const int nmacro = H / (spl * 128);
+  int n = 1;
+  while (n < nmacro && layer_up_lds(T, topk, (nmacro + n - 1) / n * spl * 128, 1).total > kLayerLds) ++n;
+  return n;
+}
+
+// K parts of kernel 2: of at most 1024 values, one operand a lane (7168 / 3 K, top-16 of 128,
+// four tokens: 73 us against 81 with parts of 1536), and enough items for every wave.
+constexpr int kDownPart = 1024;
 int layer_down_parts(int T, int topk, int I, int spl) {
   const int nmacro = I / (spl * 128);
   const int jobs = T * topk;
-  int ks = 1;
-  while (ks < nmacro && (jobs * ks < kLayerWaves || layer_down_lds(T, I, spl, ks).total > kLayerLds)) ks *= 2;
+  int ks = (I + kDownPart - 1) / kDownPart;
+  while (ks < nmacro && jobs * ks < kLayerWaves) ks *= 2;
   return std::min(ks, nmacro);
 }
 
 }  // namespace
 
-// One run of the two kernels: 2- to 4-bit codes, up to eight tokens, and activations,
-// lists and partial sums in one compute unit's LDS.
-static bool layer_fits(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
-                       int dn_group) {
+// One run of the two kernels: 2- to 4-bit codes, up to eight tokens.
+static bool layer_fits(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int dn_bits) {
   if (up_bits < 2 || up_bits > 4 || dn_bits < 2 || dn_bits > 4) return false;
   if (T < 1 || T > kLayerMaxT || E > kLayerMaxE || topk > kRouterMaxTopk) return false;
   if (H > 65536 || I > 65536 || (I + 16) * (H * up_bits / 8) >= (int64_t{1} << 32)) return false;   // 32-bit tile offsets
-  if (layer_up_lds(static_cast<int>(T), topk, static_cast<int>(H), 1).total > kLayerLds) return false;
-  const int spl = layer_spl(dn_bits, dn_group);
-  const int ks = layer_down_parts(static_cast<int>(T), topk, static_cast<int>(I), spl);
-  return layer_down_lds(static_cast<int>(T), static_cast<int>(I), spl, ks).total <= kLayerLds;
+  return true;
 }
 
 // Tokens of one run of the two kernels; 0: the composed path. Nine to 64 tokens take
-// runs of up to eight: an expert that tokens of several runs share is read again, but at
-// twice the composed path's rate or more (2-bit codes, 2048 x 1024, top-8 of 128, 16
-// tokens: 80 against 158 us, 64: 302 against 433; 7168 x 3 K, top-16 of 128, 64 tokens:
-// 2.28 against 2.61 ms; 4 bits, 2048 x 1024, top-4 of 32, 64 tokens: 347 against 506).
-// The composed path is ahead where many pairs of 2-bit codes share an expert (2048 x 1024,
-// top-4 of 16: 40 tokens 128 against 128 us, 64 tokens 200 against 191), and with weights
-// below 4 MB, where the launches count, not the rate (16 tokens, 512 x 256, top-2 of 8: 40
-// against 33 us).
-int64_t moe_layer_tokens(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits,
-                         int dn_group) {
+// runs of up to eight: an expert that tokens of several runs share is read again, yet that is
+// ahead of the composed path (us, runs against composed; 2048 x 1024, 2 bits, top-8 of 128: 16
+// tokens 81 / 161, 64: 319 / 424; top-4 of 16, 64 tokens: 187 / 214; 4 bits, top-4 of 32: 16
+// tokens 95 / 140, 64: 367 / 487; 7168 x 2 K, 4 bits, top-8 of 64: 64 tokens 2578 / 4644) but
+// - where launches count, not rates: 2 bits, top-2 of 8, 512 x 256 (0.8 MB): 16 tokens 33 / 29;
+//   top-4 of 16, 1024 x 512 (6 MB): 16 tokens 43 / 47, 32: 84 / 67. Wider codes are ahead with
+//   a third of the bytes (4 bits, 1.6 MB: 16 tokens 37 / 47, 64: 144 / 114; 3 bits, 9 MB: 32
+//   tokens 109 / 122, 64: 217 / 214);
+// - with 2-bit codes and rows that take several launches of kernel 1 (7168 / 3 K, top-16 of
+//   128: 16 tokens 719 / 832, 24: 1080 / 1104, 32: 1434 / 1399, 64: 2863 / 2686).
+int64_t moe_layer_tokens(int64_t T, int topk, int E, int64_t H, int64_t I, int up_bits, int up_group, int dn_bits) {
   if (T < 1 || T > 8 * kLayerMaxT) return 0;
   const int64_t runs = (T + kLayerMaxT - 1) / kLayerMaxT, n = (T + runs - 1) / runs;
-  if (!layer_fits(n, topk, E, H, I, up_bits, up_group, dn_bits, dn_group)) return 0;
-  if (up_bits == 2 && runs > 4 && T * topk > 10 * static_cast<int64_t>(E)) return 0;
-  if (runs > 1 && 3 * H * I * up_bits / 8 * std::min<int64_t>(E, T * topk) < (int64_t{4} << 20)) return 0;
+  if (!layer_fits(n, topk, E, H, I, up_bits, dn_bits)) return 0;
+  if (runs == 1) return n;
+  const bool two = up_bits == 2 && dn_bits == 2;
+  const int64_t bytes = H * I * (2 * up_bits + dn_bits) / 8 * std::min<int64_t>(E, T * topk);
+  if ((two ? 1 : 3) * bytes < runs * (int64_t{2} << 20)) return 0;
+  const int launches = layer_up_launches(static_cast<int>(n), topk, static_cast<int>(H), layer_spl(up_bits, up_group));
+  if (two && launches > 1 && runs > 3) return 0;
   return n;
 }
 
@@ -1168,36 +1135,49 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   p.gpr = H / up.group;
   const int spl = layer_spl(up.bits, up.group), dspl = layer_spl(dn.bits, dn.group);
   p.groups = group_steps(up.group, spl);
-  const int nmacro = H / (spl * 128);
-  p.down_spl = dn.bits == 2 ? dspl : 0;
+  p.partial = b.partial;
   p.ids = b.ids;
   p.weights = b.weights;
   p.ids_user = ids_user;
   p.weights_user = weights_user;
   p.rec = b.rec;
-  p.hq = b.hq;
-  p.hs = b.hs;
-  const int teams = kLayerWaves / layer_up_max_parts(nmacro);    // at least
+  p.h = b.h;
+  const int nmacro = H / (spl * 128), launches = layer_up_launches(T, r.topk, H, spl);
   const int64_t units = static_cast<int64_t>(std::min(r.E, T * r.topk)) * (I / 16);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
-  p.share = 1.0f / (static_cast<float>(grid) * kLayerWaves);
-  p.batch = 4;
-  while (p.batch > 1 && layer_up_lds(T, r.topk, H, p.batch).total > kLayerLds) --p.batch;
-  const int lds = layer_up_lds(T, r.topk, H, p.batch).total;
   hipError_t e;
   const bool few = r.E <= 256;                 // a router wave with 4 experts a lane, or 16
-  auto up_kernel = [&](auto f_c, auto pm_c) {
+  // steps in flight: up to four tokens, and more (whose second tile takes registers: more spill)
+  auto up_kernel = [&](auto f_c, auto pm_c, auto pm2_c) {
     using F = decltype(f_c);
-    constexpr int PM = decltype(pm_c)::value;
-    return few ? launch_layer(k_layer_up<F, PM, 4>, grid, lds, p, st) : launch_layer(k_layer_up<F, PM, 16>, grid, lds, p, st);
+    constexpr int PM = decltype(pm_c)::value, PM2 = decltype(pm2_c)::value;
+    hipError_t err = hipSuccess;
+    for (int c = 0; c < launches && err == hipSuccess; ++c) {
+      p.k0 = c * nmacro / launches;
+      p.steps = (c + 1) * nmacro / launches - p.k0;
+      p.add = c > 0;
+      p.last = c == launches - 1;
+      const int teams = kLayerWaves / layer_up_max_parts(p.steps);   // at least
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cus, (units + teams - 1) / teams));
+      p.share = 1.0f / (static_cast<float>(grid) * kLayerWaves);
+      const int K = p.steps * spl * 128;
+      p.batch = 4;
+      while (p.batch > 1 && layer_up_lds(T, r.topk, K, p.batch).total > kLayerLds) --p.batch;
+      const int lds = layer_up_lds(T, r.topk, K, p.batch).total;
+      if (T > 4) {
+        err = few ? launch_layer(k_layer_up<F, PM2, 4, 2>, grid, lds, p, st) : launch_layer(k_layer_up<F, PM2, 16, 2>, grid, lds, p, st);
+      } else {
+        err = few ? launch_layer(k_layer_up<F, PM, 4, 1>, grid, lds, p, st) : launch_layer(k_layer_up<F, PM, 16, 1>, grid, lds, p, st);
+      }
+    }
+    return err;
   };
-  using I2 = std::integral_constant<int, 2>;   // (more spill)
+  using I2 = std::integral_constant<int, 2>;
   using I4 = std::integral_constant<int, 4>;
   using I8 = std::integral_constant<int, 8>;
   if (up.bits == 2) {
-    e = spl == 2 ? up_kernel(Codes2<2>{}, I4{}) : up_kernel(Codes2<1>{}, I8{});
+    e = spl == 2 ? up_kernel(Codes2<2>{}, I4{}, I2{}) : up_kernel(Codes2<1>{}, I8{}, I4{});
   } else {
-    e = up.bits == 3 ? up_kernel(CodesWide<3>{}, I2{}) : up_kernel(CodesWide<4>{}, I2{});
+    e = up.bits == 3 ? up_kernel(CodesWide<3>{}, I2{}, I2{}) : up_kernel(CodesWide<4>{}, I2{}, I2{});
   }
   if (e != hipSuccess) return e;
 
@@ -1206,8 +1186,7 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   d.weights = b.weights;
   d.T = T;
   d.topk = r.topk;
-  d.hq = b.hq;
-  d.hs = b.hs;
+  d.h = b.h;
   d.codes = dn.codes;
   d.scales = dn.scales;
   d.shapes = dn.shapes;

@@ -384,16 +384,19 @@ int cubic_moe_topk(const cubic_router* router, int64_t T, int32_t* topk_ids, flo
  * bf16 there as here):
  *   y[t] = sum_j topk_weights[t][j] * (bf16(SiLU(g) * u) * D_e^T),  [g | u] = x_t * GU_e^T
  * A token whose experts are all masked out gets a zero row. For 2- to 4-bit weights
- * and up to eight tokens (E <= 1024, and activations that fit a compute unit's LDS)
- * the layer runs in two kernels, which read each touched expert's codes from HBM
- * once, and with weights of 4 MB and more for up to 64 tokens (2 bits and more than 32
- * tokens: while at most ten pairs share an expert on average) in such runs of up to
- * eight; otherwise the router kernel and the MLP step run one after the other, with the
- * limits of cubic_moe_mlp. Products are as good as 16 significant bits: the two kernels'
- * sums of 128 codes are off by about 2^-16 of the sum (at worst 2^-11 of its largest
- * product), and in the MLP step the levels of wider codes are rounded to 16 bits; sums
- * are fp32 beyond. About one h in a hundred rounds to a neighbour for it. A non-finite activation makes its token's row non-finite and no other. The sums'
- * order does not depend on timing.
+ * and up to eight tokens (E <= 1024, H and I <= 65536) the layer runs in two kernels
+ * (the first one in several launches where rows do not fit a compute unit's LDS), which
+ * read each touched expert's codes from HBM once; up to 64 tokens go in such runs of up
+ * to eight where that is the faster way, by the sizes; otherwise the router kernel and
+ * the MLP step run one after the other, with the limits of cubic_moe_mlp.
+ * The two kernels' sums of 128 or 256 codes are exact and added up in fp32, of
+ * activations held as multiples of 2^-29 of their block's largest power of two (the
+ * blocks are the sums'; a value is exact down to 2^-22 of the block's largest, and below
+ * off by at most 2^-30 of it; 2^-120 is the finest multiple). In the MLP step sums are
+ * fp32, and the levels of wider codes two bf16 halves (16 significant bits). A
+ * non-finite activation makes its token's row non-finite and no other. The sums' order
+ * does not depend on timing, but on the whole call: a token's last bits may differ
+ * with the number of tokens and the experts they touch.
  * x_bf16 [T][H]; y [T][H] in y_dtype CUBIC_DTYPE_F32 or CUBIC_DTYPE_BF16 (rounded
  * once); topk_ids and topk_weights [T][topk] receive the routing, or are NULL. The
  * workspace (cubic_moe_layer_workspace_bytes) holds the routing and the
