@@ -128,34 +128,30 @@ __device__ __forceinline__ void wave_topk(const RouterParams& p, int64_t t, int 
     l[i] = 64 * i + lane < E ? router_value(l[i]) : -__builtin_inff();
     lmax = fmaxf(lmax, l[i]);
   }
-  // softmax denominators: in fp64 where biased keys are compared, else in fp32
-  double total64 = 1.0;
-  float total = 1.0f;
+  // The softmax's denominator, where a key or a weight needs it.
+  double total = 1.0;
   if (!p.sigmoid) {
     lmax = wave_reduce(lmax, [](float x, float y) { return fmaxf(x, y); });
-    if (lmax > -__builtin_inff()) {
-      if (p.bias) {
-        total64 = 0.0;
-#pragma unroll 1
-        for (int i = 0; 64 * i < E; ++i) {     // (rolled: fp64 exponentials are long; re-read, not indexed registers)
-          const int e = 64 * i + lane;
-          const float v = e < E ? router_logit(p, row + e) : -__builtin_inff();
-          if (v > -__builtin_inff()) total64 += exp(static_cast<double>(v) - static_cast<double>(lmax));
-        }
-        total64 = wave_reduce(total64, [](double x, double y) { return x + y; });
-        total = static_cast<float>(total64);
-      } else if (!p.renorm) {
-        total = 0.0f;
+    if (lmax > -__builtin_inff() && (p.bias || !p.renorm)) {
+      total = 0.0;
+      // four exponentials side by side: one by one they follow each other (one token of 896
+      // experts: 7.9 us; this way 5.8, and 5.3 with a sum in fp32)
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) total += expf(l[i] - lmax);
-        total = wave_reduce(total, [](float x, float y) { return x + y; });
+      for (int i0 = 0; i0 < EPL; i0 += 4) {
+        if (64 * i0 < E) {
+          double e4[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) e4[u] = exp(static_cast<double>(l[i0 + u]) - static_cast<double>(lmax));
+          total += (e4[0] + e4[1]) + (e4[2] + e4[3]);
+        }
       }
+      total = wave_reduce(total, [](double x, double y) { return x + y; });
     }
   }
   uint32_t key[EPL];                           // ordered key; 0: not there or never taken
   uint32_t kmax = 0u;
   if (p.bias) {
-    const float rt = 1.0f / total;
+    const float rt = 1.0f / static_cast<float>(total);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const float bi = router_value(b[i]);
@@ -263,7 +259,7 @@ __device__ __forceinline__ void wave_topk(const RouterParams& p, int64_t t, int 
         if (p.bias) {
           const float bi = router_value(p.bias[e]);
           if (!(bi > -__builtin_inff())) continue;
-          v = (p.sigmoid ? sigmoid64(f) : exp(v - static_cast<double>(lmax)) / total64) + static_cast<double>(bi);
+          v = (p.sigmoid ? sigmoid64(f) : exp(v - static_cast<double>(lmax)) / total) + static_cast<double>(bi);
         }
         if (v > best || be == INT32_MAX) { best = v; be = e; }
       }
@@ -286,12 +282,7 @@ __device__ __forceinline__ void wave_topk(const RouterParams& p, int64_t t, int 
     if (p.sigmoid) {
       pc = sigmoid64(lc);
     } else {
-      pc = exp(static_cast<double>(lc) - static_cast<double>(lmax));
-      if (p.bias) {
-        pc /= total64;
-      } else {
-        pc /= static_cast<double>(total);      // (one with renormalisation)
-      }
+      pc = exp(static_cast<double>(lc) - static_cast<double>(lmax)) / total;
     }
     kc = p.bias ? pc + static_cast<double>(router_value(p.bias[ec])) : static_cast<double>(lc);
   }
