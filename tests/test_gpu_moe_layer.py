@@ -3,13 +3,14 @@
 
 Tolerances, from the arithmetic:
 * ids are equal.
-* weights: scores, sums and quotients in fp64, rounded to fp32 once: 2^-24 relative. The softmax
-  without a bias and without renormalisation has its denominator in fp32: at most 38 additions in a
-  row (2^-24 each), expf within an ulp and its argument's rounding (below 2^-23): 42 * 2^-24.
-* y in fp32, as a 2-norm: fp32 sums move g and u by some 1e-6, so about 2e-6 / 2^-8 = 5e-4 of the h
-  values round to the neighbouring bf16 number, 2^-8 away: sqrt(5e-4) * 2^-8 = 9e-5; the bar is 1e-3.
-  Wider codes keep their levels in fp16 (2^-12): products' bar 2e-3 and its effect on h, 1e-2 per row.
-  A bf16 output adds half a step, 2^-8.
+* weights: scores, sums and quotients in fp64, rounded to fp32 once: 2^-24 relative. (The softmax
+  without a bias and without renormalisation is given 42 * 2^-24 here, as if its denominator were a
+  sum in fp32; test_gpu_router_precision.py holds it to one rounding.)
+* y in fp32, as a 2-norm: bars of 1e-3 to 5e-3, and 1e-2 per row for some wide codes. They are wide: they
+  allow for sums off by 2^-16 and more, of which 2^-7 of the h values would round to a neighbour, and for
+  levels in fp16. The two kernels' sums are exact and added up in fp32, and the levels of the composed
+  path two bf16 halves; test_gpu_moe_layer_precision.py and test_gpu_moe_layer_composed.py hold them to
+  the bounds that follow from that. A bf16 output adds half a step, 2^-8.
 """
 import numpy as np
 import pytest
