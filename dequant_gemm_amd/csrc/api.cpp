@@ -756,7 +756,7 @@ CUBIC_API int cubic_moe_layer(const uint16_t* x_bf16, int64_t T, const cubic_rou
       return MoeLayerWeight{w->codes, w->scales, w->shapes,
                             static_cast<int64_t>(cubic_code_bytes(w->N, w->K, w->bits)), w->bits, w->group};
     };
-    const MoeLayerBuffers b{ids, weights, reinterpret_cast<int32_t*>(ws + L.rec),
+    const MoeLayerBuffers b{weights, reinterpret_cast<int32_t*>(ws + L.rec),
                             reinterpret_cast<uint16_t*>(ws + L.h), reinterpret_cast<float*>(ws + L.partial)};
     return hip_status(launch_moe_layer(moe_router(router), x_bf16, static_cast<int>(T), static_cast<int>(run), weight(gate_up0),
                                        weight(down0), static_cast<int>(H), static_cast<int>(I), b, topk_ids, topk_weights, y,

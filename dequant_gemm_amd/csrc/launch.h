@@ -184,7 +184,6 @@ struct MoeLayerWeight {
   int bits, group;
 };
 struct MoeLayerBuffers {
-  int32_t* ids;            // [T*topk]
   float* weights;          // [T*topk]
   int32_t* rec;            // [2 + 2 T*topk]: pairs with an expert, then (pair, expert) of each
   uint16_t* h;             // bf16 [T*topk][I]

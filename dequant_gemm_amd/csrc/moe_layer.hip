@@ -54,7 +54,6 @@ constexpr uint32_t kRsrc3 = 0x00020000u;       // raw buffer, 32-bit data format
 constexpr int kLayerWaves = 16;                // one workgroup of 1024 threads per compute unit
 constexpr int kLayerMaxT = 8;                  // two tiles of four tokens' planes
 constexpr int kLayerMaxE = 1024;               // experts of one router wave (4 or 16 per lane)
-constexpr int kLayerMaxPairs = kLayerMaxT * kRouterMaxTopk;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t layer_rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
@@ -491,9 +490,8 @@ struct LayerUpParams {
   int k0, steps;           // macro steps of this launch: k0 .. k0 + steps - 1
   int add, last;           // the sums start from `partial`; they are whole (else they go there)
   float* partial;          // [T*topk][2I]
-  int32_t* ids;            // [T][topk] out
-  float* weights;
-  int32_t* ids_user;       // a second copy for the caller, or NULL
+  float* weights;          // [T][topk] out, for kernel 2
+  int32_t* ids_user;       // [T][topk] out for the caller, or NULL
   float* weights_user;
   int32_t* rec;
   uint16_t* h;             // bf16 [T*topk][I]
@@ -637,10 +635,9 @@ __global__ __launch_bounds__(1024) void k_layer_up(LayerUpParams p) {
   if (pe >= 0) s_slot[8 * pa + pt] = static_cast<uint8_t>(tid - pt * topk);
   __syncthreads();
   if (blockIdx.x == 0) {
-    // for kernel 2 and the caller: ids, weights and the pairs grouped by expert
+    // for kernel 2 and the caller: weights, ids and the pairs grouped by expert
     if (tid < P) {
       const float w = s_w[tid];
-      p.ids[tid] = pe;
       p.weights[tid] = w;
       if (p.ids_user) p.ids_user[tid] = pe;
       if (p.weights_user) p.weights_user[tid] = w;
@@ -1136,7 +1133,6 @@ static hipError_t launch_layer_run(const MoeRouter& r, const uint16_t* x, int T,
   const int spl = layer_spl(up.bits, up.group), dspl = layer_spl(dn.bits, dn.group);
   p.groups = group_steps(up.group, spl);
   p.partial = b.partial;
-  p.ids = b.ids;
   p.weights = b.weights;
   p.ids_user = ids_user;
   p.weights_user = weights_user;
