@@ -30,6 +30,11 @@ __all__ = [
     "DTYPE_F32", "DTYPE_BF16", "DTYPE_F16",
     "cubic_moe_topk", "cubic_moe_layer_workspace_bytes", "cubic_moe_layer", "SCORE_SOFTMAX", "SCORE_SIGMOID",
     "Int8Weight", "cubic_gemm_w8a8", "cubic_linear_w8a8_workspace_bytes", "cubic_linear_w8a8",
+    "Fp8Weight", "cubic_quant_fp8", "cubic_gemm_fp8_workspace_bytes", "cubic_gemm_fp8",
+    "cubic_linear_fp8_workspace_bytes", "cubic_linear_fp8",
+    "ACT_SILU", "ACT_GELU_TANH", "cubic_gated_ff_workspace_bytes", "cubic_gated_ff",
+    "cubic_gated_ff_backward_workspace_bytes", "cubic_gated_ff_backward",
+    "cubic_gated_ff_fp8_workspace_bytes", "cubic_gated_ff_fp8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -44,9 +49,15 @@ EXPORTED_SYMBOLS = [
     "cubic_moe_grouped_gemm_a8", "cubic_moe_mlp_a8_workspace_bytes", "cubic_moe_mlp_a8",
     "cubic_moe_topk", "cubic_moe_layer_workspace_bytes", "cubic_moe_layer",
     "cubic_gemm_w8a8", "cubic_linear_w8a8_workspace_bytes", "cubic_linear_w8a8",
+    "cubic_quant_fp8", "cubic_gemm_fp8_workspace_bytes", "cubic_gemm_fp8",
+    "cubic_linear_fp8_workspace_bytes", "cubic_linear_fp8",
+    "cubic_gated_ff_workspace_bytes", "cubic_gated_ff",
+    "cubic_gated_ff_backward_workspace_bytes", "cubic_gated_ff_backward",
+    "cubic_gated_ff_fp8_workspace_bytes", "cubic_gated_ff_fp8",
 ]
 MODE_A16, MODE_A8 = 0, 1          # cubic_linear_mode results
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1
 
 
 class CubicError(RuntimeError):
@@ -62,6 +73,11 @@ class _CWeight(ctypes.Structure):
 
 
 class _CWeightI8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64)]
+
+
+class _CWeightFp8(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64)]
 
@@ -92,6 +108,7 @@ def load_library():
     wp = ctypes.POINTER(_CWeight)
     rp = ctypes.POINTER(_CRouter)
     ip = ctypes.POINTER(_CWeightI8)
+    fp = ctypes.POINTER(_CWeightFp8)
     sigs = {
         "cubic_code_bytes": (sz, [i64, i64, i32]),
         "cubic_storage_bytes": (sz, [i64, i64, i32, i32]),
@@ -128,6 +145,17 @@ def load_library():
         "cubic_gemm_w8a8": (i32, [vp, vp, i64, ip, vp, vp, i32, vp]),
         "cubic_linear_w8a8_workspace_bytes": (sz, [i64, i64]),
         "cubic_linear_w8a8": (i32, [vp, i32, i64, ip, vp, vp, i32, vp, sz, vp]),
+        "cubic_quant_fp8": (i32, [vp, i32, i64, i64, i32, vp, vp, vp]),
+        "cubic_gemm_fp8_workspace_bytes": (sz, [i64, i64, i64]),
+        "cubic_gemm_fp8": (i32, [vp, vp, i64, fp, vp, vp, i32, vp, sz, vp]),
+        "cubic_linear_fp8_workspace_bytes": (sz, [i64, i64, i64]),
+        "cubic_linear_fp8": (i32, [vp, i32, i64, fp, vp, vp, i32, vp, sz, vp]),
+        "cubic_gated_ff_workspace_bytes": (sz, [i64, i64, i64]),
+        "cubic_gated_ff": (i32, [vp, vp, i32, i64, i64, i64, i32, vp, vp, vp, sz, vp]),
+        "cubic_gated_ff_backward_workspace_bytes": (sz, [i64, i64, i64]),
+        "cubic_gated_ff_backward": (i32, [vp, vp, vp, vp, i32, i64, i64, i64, i32, vp, vp, vp, sz, vp]),
+        "cubic_gated_ff_fp8_workspace_bytes": (sz, [i64, i64, i64]),
+        "cubic_gated_ff_fp8": (i32, [vp, i32, i64, fp, i32, vp, i32, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -670,4 +698,189 @@ def cubic_linear_w8a8(x: torch.Tensor, w: Int8Weight, bias: torch.Tensor | None 
     wa, n = (None, 0) if workspace is None else (_arg(workspace, torch.uint8, index, "workspace"), workspace.numel())
     _check(_call(index, lib.cubic_linear_w8a8, xa, _DT_IN[x.dtype], M, ctypes.byref(cw), ba, out.data_ptr(), yd, wa, n),
            "cubic_linear_w8a8")
+    return out
+
+
+@dataclass
+class Fp8Weight:
+    """A dense e4m3 weight with one scale per block of 128 x 128 (cubic_quant_fp8 with block_rows=128)."""
+    codes: torch.Tensor     # float8_e4m3fn [N][K]
+    scales: torch.Tensor    # float32 [ceil(N / 128)][ceil(K / 128)]
+
+
+_DT_DENSE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, ACT_SILU: ACT_SILU, ACT_GELU_TANH: ACT_GELU_TANH}
+
+
+def _dense_dtype(dtype, name: str, floats: dict) -> int:
+    if dtype not in floats:
+        raise TypeError(f"{name}: expected one of {', '.join(str(d) for d in floats)}, got {dtype}")
+    return floats[dtype]
+
+
+def _act(act) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act: expected 'silu' or 'gelu_tanh', got {act!r}")
+    return _ACTS[act]
+
+
+def _scratch(workspace, need: int, index: int):
+    """(tensor to keep, address, bytes) of the caller's workspace or a new one."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=index)
+    return workspace, _arg(workspace, torch.uint8, index, "workspace"), workspace.numel()
+
+
+def _fp8_weight(w: Fp8Weight, index: int) -> _CWeightFp8:
+    if w.codes.dim() != 2 or tuple(w.scales.shape) != (-(-w.codes.shape[0] // 128), -(-w.codes.shape[1] // 128)):
+        raise ValueError("Fp8Weight: expected codes [N][K] and scales [ceil(N / 128)][ceil(K / 128)]")
+    return _CWeightFp8(_arg(w.codes, torch.float8_e4m3fn, index, "codes"), _arg(w.scales, torch.float32, index, "scales"),
+                       *w.codes.shape)
+
+
+def _fp8_args(x: torch.Tensor, w: Fp8Weight, bias, out, out_dtype, index: int, name: str):
+    """(descriptor, bias address, output code, output) after the checks that both calls share."""
+    yd = _dense_dtype(out_dtype, "out_dtype", _DT_DENSE)
+    cw = _fp8_weight(w, index)
+    if x.dim() != 2 or x.shape[1] != cw.K:
+        raise ValueError(f"{name}: expected [M][{cw.K}], got {tuple(x.shape)}")
+    ba = None
+    if bias is not None:
+        ba = _arg(bias, torch.float32, index, "bias")
+        if bias.numel() != cw.N:
+            raise ValueError(f"bias: expected {cw.N} values, got {bias.numel()}")
+    return cw, ba, yd, _result(out, (x.shape[0], cw.N), out_dtype, index)
+
+
+def cubic_quant_fp8(x: torch.Tensor, block_rows: int = 1, xq: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None):
+    """x bf16 or fp16 [M][K] -> (e4m3 codes [M][K], fp32 scales [ceil(M / block_rows)][ceil(K / 128)]),
+    block_rows 1 (activations) or 128 (weights)."""
+    if x.dim() != 2 or block_rows <= 0:
+        raise ValueError(f"x: expected [M][K] and a positive block_rows, got {tuple(x.shape)} and {block_rows}")
+    xd = _dense_dtype(x.dtype, "x", _DT_IN)
+    index = _first(x, "x")
+    xa = _arg(x, x.dtype, index, "x")
+    M, K = x.shape
+    xq = _result(xq, (M, K), torch.float8_e4m3fn, index, "xq")
+    scales = _result(scales, (-(-M // block_rows), -(-K // 128)), torch.float32, index, "scales")
+    _check(_call(index, load_library().cubic_quant_fp8, xa, xd, M, K, block_rows, xq.data_ptr(), scales.data_ptr()),
+           "cubic_quant_fp8")
+    return xq, scales
+
+
+def cubic_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().cubic_gemm_fp8_workspace_bytes(M, N, K))
+
+
+def cubic_gemm_fp8(xq: torch.Tensor, x_scale: torch.Tensor, w: Fp8Weight, bias: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   out_dtype=torch.float32) -> torch.Tensor:
+    """y[M][N] of e4m3 rows xq [M][K] with scales [M][ceil(K / 128)] and the block-scaled weight (+ bias[n]);
+    y fp32, bf16 or fp16."""
+    index = _first(xq, "xq")
+    xa, sa = _arg(xq, torch.float8_e4m3fn, index, "xq"), _arg(x_scale, torch.float32, index, "x_scale")
+    cw, ba, yd, out = _fp8_args(xq, w, bias, out, out_dtype, index, "xq")
+    M = xq.shape[0]
+    if tuple(x_scale.shape) != (M, -(-cw.K // 128)):
+        raise ValueError(f"x_scale: expected [{M}][{-(-cw.K // 128)}], got {tuple(x_scale.shape)}")
+    lib = load_library()
+    workspace, wa, n = _scratch(workspace, lib.cubic_gemm_fp8_workspace_bytes(M, cw.N, cw.K), index)
+    _check(_call(index, lib.cubic_gemm_fp8, xa, sa, M, ctypes.byref(cw), ba, out.data_ptr(), yd, wa, n), "cubic_gemm_fp8")
+    return out
+
+
+def cubic_linear_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().cubic_linear_fp8_workspace_bytes(M, N, K))
+
+
+def cubic_linear_fp8(x: torch.Tensor, w: Fp8Weight, bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, out_dtype=torch.float32) -> torch.Tensor:
+    """cubic_gemm_fp8 of bf16 or fp16 rows x [M][K], quantised per 128 channels on the way (cubic_quant_fp8)."""
+    xd = _dense_dtype(x.dtype, "x", _DT_IN)
+    index = _first(x, "x")
+    xa = _arg(x, x.dtype, index, "x")
+    cw, ba, yd, out = _fp8_args(x, w, bias, out, out_dtype, index, "x")
+    M = x.shape[0]
+    lib = load_library()
+    workspace, wa, n = _scratch(workspace, lib.cubic_linear_fp8_workspace_bytes(M, cw.N, cw.K), index)
+    _check(_call(index, lib.cubic_linear_fp8, xa, xd, M, ctypes.byref(cw), ba, out.data_ptr(), yd, wa, n), "cubic_linear_fp8")
+    return out
+
+
+def _ff_args(x: torch.Tensor, w: torch.Tensor, index: int):
+    """(x, w addresses, dtype code, M, H, I) of a block over 16-bit weights [2 I][H]."""
+    xd = _dense_dtype(x.dtype, "x", _DT_IN)
+    if x.dim() != 2 or w.dim() != 2 or w.shape[0] % 2 != 0 or w.shape[1] != x.shape[1]:
+        raise ValueError(f"expected x [M][H] and w [2 I][H], got {tuple(x.shape)} and {tuple(w.shape)}")
+    return _arg(x, x.dtype, index, "x"), _arg(w, x.dtype, index, "w"), xd, x.shape[0], x.shape[1], w.shape[0] // 2
+
+
+def cubic_gated_ff_workspace_bytes(M: int, H: int, I: int) -> int:
+    return int(load_library().cubic_gated_ff_workspace_bytes(M, H, I))
+
+
+def cubic_gated_ff(x: torch.Tensor, w: torch.Tensor, act="silu", save_pre: bool = False, out: torch.Tensor | None = None,
+                   pre: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """h [M][I] = act(x Wg^T) * (x Wu^T) for x [M][H] and w [2 I][H] (gate rows, then up rows), bf16 or fp16.
+    With save_pre or a tensor for it, (h, pre): pre fp32 [M][2 I] is what the backward pass takes."""
+    index = _first(x, "x")
+    xa, wa, xd, M, H, I = _ff_args(x, w, index)
+    kind = _act(act)
+    out = _result(out, (M, I), x.dtype, index)
+    if save_pre or pre is not None:
+        pre = _result(pre, (M, 2 * I), torch.float32, index, "pre")
+    lib = load_library()
+    workspace, sa, n = _scratch(workspace, lib.cubic_gated_ff_workspace_bytes(M, H, I), index)
+    _check(_call(index, lib.cubic_gated_ff, xa, wa, xd, M, H, I, kind, out.data_ptr(), None if pre is None else pre.data_ptr(),
+                 sa, n), "cubic_gated_ff")
+    return out if pre is None else (out, pre)
+
+
+def cubic_gated_ff_backward_workspace_bytes(M: int, H: int, I: int) -> int:
+    return int(load_library().cubic_gated_ff_backward_workspace_bytes(M, H, I))
+
+
+def cubic_gated_ff_backward(dh: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre: torch.Tensor, act="silu",
+                            need_dx: bool = True, need_dw: bool = True, dx: torch.Tensor | None = None,
+                            dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """(dx [M][H], dw [2 I][H]) of cubic_gated_ff from dh [M][I] and the forward's pre; None for what is not needed."""
+    index = _first(x, "x")
+    xa, wa, xd, M, H, I = _ff_args(x, w, index)
+    kind = _act(act)
+    da, pa = _arg(dh, x.dtype, index, "dh"), _arg(pre, torch.float32, index, "pre")
+    if tuple(dh.shape) != (M, I) or tuple(pre.shape) != (M, 2 * I):
+        raise ValueError(f"expected dh [{M}][{I}] and pre [{M}][{2 * I}], got {tuple(dh.shape)} and {tuple(pre.shape)}")
+    dx = _result(dx, (M, H), x.dtype, index, "dx") if need_dx else None
+    dw = _result(dw, (2 * I, H), x.dtype, index, "dw") if need_dw else None
+    lib = load_library()
+    workspace, sa, n = _scratch(workspace, lib.cubic_gated_ff_backward_workspace_bytes(M, H, I), index)
+    _check(_call(index, lib.cubic_gated_ff_backward, da, xa, wa, pa, xd, M, H, I, kind, None if dx is None else dx.data_ptr(),
+                 None if dw is None else dw.data_ptr(), sa, n), "cubic_gated_ff_backward")
+    return dx, dw
+
+
+def cubic_gated_ff_fp8_workspace_bytes(M: int, H: int, I: int) -> int:
+    return int(load_library().cubic_gated_ff_fp8_workspace_bytes(M, H, I))
+
+
+def cubic_gated_ff_fp8(x: torch.Tensor, w: Fp8Weight, act="silu", out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, out_dtype=torch.bfloat16) -> torch.Tensor:
+    """cubic_gated_ff over a block-scaled e4m3 weight [2 I][H] (I a multiple of 128), the activations quantised
+    on the way; h bf16 or fp16."""
+    xd, hd = _dense_dtype(x.dtype, "x", _DT_IN), _dense_dtype(out_dtype, "out_dtype", _DT_IN)
+    index = _first(x, "x")
+    xa = _arg(x, x.dtype, index, "x")
+    cw = _fp8_weight(w, index)
+    if x.dim() != 2 or x.shape[1] != cw.K or cw.N % 2 != 0:
+        raise ValueError(f"expected x [M][H] and a weight [2 I][H], got {tuple(x.shape)} and [{cw.N}][{cw.K}]")
+    kind = _act(act)
+    M, I = x.shape[0], cw.N // 2
+    out = _result(out, (M, I), out_dtype, index)
+    lib = load_library()
+    workspace, sa, n = _scratch(workspace, lib.cubic_gated_ff_fp8_workspace_bytes(M, cw.K, I), index)
+    _check(_call(index, lib.cubic_gated_ff_fp8, xa, xd, M, ctypes.byref(cw), kind, out.data_ptr(), hd, sa, n),
+           "cubic_gated_ff_fp8")
     return out

@@ -844,3 +844,203 @@ CUBIC_API int cubic_linear_w8a8(const void* x, int x_dtype, int64_t M, const cub
   p.xs = xs;
   return hip_status(launch_w8a8(p, static_cast<hipStream_t>(stream)));
 }
+
+namespace {
+constexpr int64_t kDenseMaxK = 1 << 20;      // a tile's rows stay within 32-bit byte offsets
+constexpr int64_t kDenseMaxRows = (1 << 24) - 1;
+
+bool dtype_dense_out_ok(int d) { return d == CUBIC_DTYPE_F32 || d == CUBIC_DTYPE_BF16 || d == CUBIC_DTYPE_F16; }
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+int check_weight_fp8(const cubic_weight_fp8* w, int64_t M) {
+  if (!w) return CUBIC_ERR_NULL;
+  if (M < 0 || w->N < 0 || w->K <= 0 || w->K % 16 != 0 || w->K > kDenseMaxK) return CUBIC_ERR_SHAPE;
+  if (M > kDenseMaxRows || w->N > kDenseMaxRows) return CUBIC_ERR_SHAPE;
+  if (M > 0 && w->N > 0) {
+    if (!w->codes || !w->scales) return CUBIC_ERR_NULL;
+    if (!aligned16(w->codes) || !aligned16(w->scales)) return CUBIC_ERR_ALIGN;
+  }
+  return CUBIC_OK;
+}
+
+size_t fp8_codes_bytes(int64_t M, int64_t K) { return align256(static_cast<size_t>(M) * K); }
+size_t fp8_staging_bytes(int64_t M, int64_t K) {
+  return fp8_codes_bytes(M, K) + align256(static_cast<size_t>(M) * blocks128(K) * 4);
+}
+
+Fp8Params fp8_params(const cubic_weight_fp8* w, int64_t M, const float* bias, void* y, int y_dtype) {
+  Fp8Params p{};
+  p.w = w->codes;
+  p.ws = w->scales;
+  p.bias = bias;
+  p.M = M;
+  p.N = w->N;
+  p.K = w->K;
+  p.y = y;
+  p.ydt = y_dtype;
+  return p;
+}
+
+// x quantised into the workspace's first part; p's activations are that.
+hipError_t fp8_stage(Fp8Params* p, const void* x, int x_dtype, char* ws, hipStream_t s) {
+  uint8_t* xq = reinterpret_cast<uint8_t*>(ws);
+  float* xs = reinterpret_cast<float*>(ws + fp8_codes_bytes(p->M, p->K));
+  p->xq = xq;
+  p->xs = xs;
+  return launch_quant_fp8(static_cast<const uint16_t*>(x), x_dtype == CUBIC_DTYPE_F16, p->M, p->K, false, xq, xs, s);
+}
+}  // namespace
+
+CUBIC_API int cubic_quant_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int block_rows, uint8_t* xq, float* scales,
+                              cubic_stream_t stream) {
+  if (!dtype_in_ok(x_dtype)) return CUBIC_ERR_DTYPE;
+  if (block_rows != 1 && block_rows != 128) return CUBIC_ERR_OPTION;
+  if (M < 0 || M > kDenseMaxRows || K <= 0 || K % 16 != 0 || K > kDenseMaxK) return CUBIC_ERR_SHAPE;
+  if (M == 0) return CUBIC_OK;
+  if (!x || !xq || !scales) return CUBIC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(xq) || !aligned16(scales)) return CUBIC_ERR_ALIGN;
+  return hip_status(launch_quant_fp8(static_cast<const uint16_t*>(x), x_dtype == CUBIC_DTYPE_F16, M, K, block_rows == 128, xq,
+                                     scales, static_cast<hipStream_t>(stream)));
+}
+
+CUBIC_API size_t cubic_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  (void)M, (void)N, (void)K;
+  return 0;
+}
+
+CUBIC_API int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, const cubic_weight_fp8* w, const float* bias,
+                             void* y, int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream) {
+  const int st = check_weight_fp8(w, M);
+  if (st != CUBIC_OK) return st;
+  if (!dtype_dense_out_ok(y_dtype)) return CUBIC_ERR_DTYPE;
+  if (M == 0 || w->N == 0) return CUBIC_OK;
+  if (!xq || !x_scale || !y) return CUBIC_ERR_NULL;
+  if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(bias) || !aligned16(y) || !aligned16(workspace)) return CUBIC_ERR_ALIGN;
+  const size_t need = cubic_gemm_fp8_workspace_bytes(M, w->N, w->K);
+  if (need > 0 && (!workspace || ws_bytes < need)) return CUBIC_ERR_WORKSPACE;
+  Fp8Params p = fp8_params(w, M, bias, y, y_dtype);
+  p.xq = xq;
+  p.xs = x_scale;
+  return hip_status(launch_fp8(p, static_cast<hipStream_t>(stream)));
+}
+
+CUBIC_API size_t cubic_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return fp8_staging_bytes(M, K) + cubic_gemm_fp8_workspace_bytes(M, N, K);
+}
+
+CUBIC_API int cubic_linear_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* w, const float* bias, void* y,
+                               int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream) {
+  const int st = check_weight_fp8(w, M);
+  if (st != CUBIC_OK) return st;
+  if (!dtype_in_ok(x_dtype) || !dtype_dense_out_ok(y_dtype)) return CUBIC_ERR_DTYPE;
+  if (M == 0 || w->N == 0) return CUBIC_OK;
+  if (!x || !y) return CUBIC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(bias) || !aligned16(y) || !aligned16(workspace)) return CUBIC_ERR_ALIGN;
+  const size_t need = cubic_linear_fp8_workspace_bytes(M, w->N, w->K);
+  if (need > 0 && (!workspace || ws_bytes < need)) return CUBIC_ERR_WORKSPACE;
+  Fp8Params p = fp8_params(w, M, bias, y, y_dtype);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = fp8_stage(&p, x, x_dtype, static_cast<char*>(workspace), s);
+  return hip_status(e != hipSuccess ? e : launch_fp8(p, s));
+}
+
+namespace {
+int check_ff(int64_t M, int64_t H, int64_t I, int dtype, int act) {
+  if (M < 0 || M > kDenseMaxRows || H <= 0 || I <= 0 || H % 8 != 0 || I % 8 != 0) return CUBIC_ERR_SHAPE;
+  if (H > kDenseMaxK || I > kDenseMaxK) return CUBIC_ERR_SHAPE;
+  if (!dtype_in_ok(dtype)) return CUBIC_ERR_DTYPE;
+  if (act != CUBIC_ACT_SILU && act != CUBIC_ACT_GELU_TANH) return CUBIC_ERR_OPTION;
+  return CUBIC_OK;
+}
+size_t pre_bytes(int64_t M, int64_t I) { return align256(static_cast<size_t>(M) * I * 8); }
+}  // namespace
+
+CUBIC_API size_t cubic_gated_ff_workspace_bytes(int64_t M, int64_t H, int64_t I) {
+  if (M <= 0 || H <= 0 || I <= 0) return 0;
+  return pre_bytes(M, I);
+}
+
+CUBIC_API int cubic_gated_ff(const void* x, const void* w, int dtype, int64_t M, int64_t H, int64_t I, int act, void* h, float* pre,
+                             void* workspace, size_t ws_bytes, cubic_stream_t stream) {
+  const int st = check_ff(M, H, I, dtype, act);
+  if (st != CUBIC_OK) return st;
+  if (M == 0) return CUBIC_OK;
+  if (!x || !w || !h) return CUBIC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(h) || !aligned16(pre) || !aligned16(workspace)) return CUBIC_ERR_ALIGN;
+  const size_t need = cubic_gated_ff_workspace_bytes(M, H, I);
+  if (need > 0 && (!workspace || ws_bytes < need)) return CUBIC_ERR_WORKSPACE;
+  FfParams p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.w = static_cast<const uint16_t*>(w);
+  p.M = M;
+  p.H = H;
+  p.I = I;
+  p.f16 = dtype == CUBIC_DTYPE_F16 ? 1 : 0;
+  p.gelu = act == CUBIC_ACT_GELU_TANH ? 1 : 0;
+  p.h = static_cast<uint16_t*>(h);
+  p.pre = pre ? pre : static_cast<float*>(workspace);
+  return hip_status(launch_gated_ff(p, static_cast<hipStream_t>(stream)));
+}
+
+CUBIC_API size_t cubic_gated_ff_backward_workspace_bytes(int64_t M, int64_t H, int64_t I) {
+  if (M <= 0 || H <= 0 || I <= 0) return 0;
+  return align256(static_cast<size_t>(M) * I * 4);
+}
+
+CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void* w, const float* pre, int dtype, int64_t M, int64_t H,
+                                      int64_t I, int act, void* dx, void* dw, void* workspace, size_t ws_bytes,
+                                      cubic_stream_t stream) {
+  const int st = check_ff(M, H, I, dtype, act);
+  if (st != CUBIC_OK) return st;
+  if (!aligned16(dx) || !aligned16(dw)) return CUBIC_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (M == 0)                                // no rows: no dx, and a weight gradient of zeros
+    return dw ? hip_status(launch_fill_zero(static_cast<float*>(dw), 2 * I * H, true, s)) : CUBIC_OK;
+  if (!dx && !dw) return CUBIC_OK;
+  if (!dh || !pre || (dx && !w) || (dw && !x)) return CUBIC_ERR_NULL;
+  if (!aligned16(dh) || !aligned16(x) || !aligned16(w) || !aligned16(pre) || !aligned16(workspace)) return CUBIC_ERR_ALIGN;
+  const size_t need = cubic_gated_ff_backward_workspace_bytes(M, H, I);
+  if (!workspace || ws_bytes < need) return CUBIC_ERR_WORKSPACE;
+  FfParams p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.w = static_cast<const uint16_t*>(w);
+  p.M = M;
+  p.H = H;
+  p.I = I;
+  p.f16 = dtype == CUBIC_DTYPE_F16 ? 1 : 0;
+  p.gelu = act == CUBIC_ACT_GELU_TANH ? 1 : 0;
+  p.pre = const_cast<float*>(pre);
+  p.dh = static_cast<const uint16_t*>(dh);
+  p.dpre = static_cast<uint16_t*>(workspace);
+  p.dx = static_cast<uint16_t*>(dx);
+  p.dw = static_cast<uint16_t*>(dw);
+  return hip_status(launch_gated_ff_backward(p, s));
+}
+
+CUBIC_API size_t cubic_gated_ff_fp8_workspace_bytes(int64_t M, int64_t H, int64_t I) {
+  if (M <= 0 || H <= 0 || I <= 0) return 0;
+  return fp8_staging_bytes(M, H) + pre_bytes(M, I);
+}
+
+CUBIC_API int cubic_gated_ff_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* gate_up, int act, void* h, int h_dtype,
+                                 void* workspace, size_t ws_bytes, cubic_stream_t stream) {
+  const int st = check_weight_fp8(gate_up, M);
+  if (st != CUBIC_OK) return st;
+  if (gate_up->N % 256 != 0) return CUBIC_ERR_SHAPE;
+  if (!dtype_in_ok(x_dtype) || !dtype_in_ok(h_dtype)) return CUBIC_ERR_DTYPE;
+  if (act != CUBIC_ACT_SILU && act != CUBIC_ACT_GELU_TANH) return CUBIC_ERR_OPTION;
+  if (M == 0 || gate_up->N == 0) return CUBIC_OK;
+  if (!x || !h) return CUBIC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(h) || !aligned16(workspace)) return CUBIC_ERR_ALIGN;
+  const int64_t I = gate_up->N / 2, H = gate_up->K;
+  if (!workspace || ws_bytes < cubic_gated_ff_fp8_workspace_bytes(M, H, I)) return CUBIC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  float* pre = reinterpret_cast<float*>(ws + fp8_staging_bytes(M, H));
+  Fp8Params p = fp8_params(gate_up, M, nullptr, pre, CUBIC_DTYPE_F32);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = fp8_stage(&p, x, x_dtype, ws, s);
+  if (e == hipSuccess) e = launch_fp8(p, s);
+  if (e == hipSuccess) e = launch_ff_act(pre, M, I, act == CUBIC_ACT_GELU_TANH ? 1 : 0, h, h_dtype, s);
+  return hip_status(e);
+}

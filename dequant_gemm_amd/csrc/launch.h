@@ -211,4 +211,39 @@ bool w8a8_quantises(int64_t M, int64_t K);   // launch_w8a8_linear takes these r
 hipError_t launch_w8a8_linear(const W8Params& p, bool xf16, hipStream_t st);
 hipError_t launch_w8a8(const W8Params& p, hipStream_t st);
 
+// The e4m3 product with fp32 scales per block of 128 (fp8.hip). Outputs of these dense
+// products are fp32 (0), bf16 (1) or fp16 (2).
+struct Fp8Params {
+  const uint8_t* xq;       // e4m3 [M][K]
+  const float* xs;         // [M][ceil(K / 128)]
+  const uint8_t* w;        // e4m3 [N][K]
+  const float* ws;         // [ceil(N / 128)][ceil(K / 128)]
+  const float* bias;       // [N] or NULL
+  int64_t M, N, K;
+  void* y;                 // [M][N]
+  int ydt;
+};
+// One scale per 128 channels of a row, or (blocks) per 128 x 128 values.
+hipError_t launch_quant_fp8(const uint16_t* x, bool xf16, int64_t M, int64_t K, bool blocks, uint8_t* xq, float* xs,
+                            hipStream_t st);
+hipError_t launch_fp8(const Fp8Params& p, hipStream_t st);
+
+// The gated feed-forward block over 16-bit weights (gated_ff.hip).
+struct FfParams {
+  const uint16_t* x;       // [M][H]
+  const uint16_t* w;       // [2 I][H]: gate rows, then up rows
+  int64_t M, H, I;
+  int f16, gelu;
+  uint16_t* h;             // [M][I]
+  float* pre;              // [M][2 I]: gate, up before the activation
+  const uint16_t* dh;      // [M][I]
+  uint16_t* dpre;          // [M][2 I]: their gradients
+  uint16_t* dx;            // [M][H] or NULL
+  uint16_t* dw;            // [2 I][H] or NULL
+};
+hipError_t launch_gated_ff(const FfParams& p, hipStream_t st);
+hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st);
+// h [M][I] in hdt = act(gate) * up of pre [M][2 I]
+hipError_t launch_ff_act(const float* pre, int64_t M, int64_t I, int gelu, void* h, int hdt, hipStream_t st);
+
 }  // namespace cubic

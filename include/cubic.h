@@ -443,6 +443,82 @@ size_t cubic_linear_w8a8_workspace_bytes(int64_t M, int64_t K);
 int cubic_linear_w8a8(const void* x, int x_dtype, int64_t M, const cubic_weight_i8* w, const float* bias,
                       void* y, int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream);
 
+/* Block-scaled 8-bit floating point, beside the int8 form above for the dense parts (shared
+ * experts, projections, dense first layers) that stay beside the Cubic-coded routed experts
+ * (CubicQuant article, section "Kimi-K3-Cubic-2.5Bit 是怎样得到 2.4986 bit 的？": they keep the
+ * source's precision). Codes are e4m3 (no infinities, largest 448); every block of 128
+ * channels has an fp32 scale: of one row for activations, of 128 rows for weights.
+ *
+ * cubic_quant_fp8: x bf16 or fp16 [M][K] -> xq e4m3 [M][K] and scales fp32
+ * [ceil(M / block_rows)][ceil(K / 128)], block_rows 1 (activations) or 128 (weights);
+ * blocks at the edges are cut. amax = max |x| of the block, scale = fp32(amax / 448) (IEEE
+ * division), xq = e4m3(fp32(x / scale)) to nearest, ties to even, at most 448 in magnitude.
+ * A scale of zero gives codes of zero; a non-finite value makes its block's scale non-finite
+ * and some of its codes NaN. Bit-exact. K a positive multiple of 16 up to 2^20, M below 2^24
+ * (CUBIC_ERR_SHAPE); CUBIC_ERR_OPTION for another block_rows. M == 0 is a no-op. */
+int cubic_quant_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int block_rows,
+                    uint8_t* xq, float* scales, cubic_stream_t stream);
+
+/* A dense e4m3 weight: codes [N][K], scales fp32 [ceil(N / 128)][ceil(K / 128)]; weight
+ * [n][k] = codes * scales[n / 128][k / 128]. */
+typedef struct cubic_weight_fp8 {
+  const uint8_t* codes;
+  const float* scales;
+  int64_t N, K;
+} cubic_weight_fp8;
+
+/* y[m][n] = sum over blocks kb of x_scale[m][kb] * w->scales[n / 128][kb] * (sum of xq[m][k] *
+ * w->codes[n][k] in the block) (+ bias[n]), for xq e4m3 [M][K] and x_scale fp32
+ * [M][ceil(K / 128)] of cubic_quant_fp8. A block's products are exact and its sum and the sum
+ * over blocks are fp32; the product of the two scales is rounded to fp32 first. y [M][N] in
+ * CUBIC_DTYPE_F32, _BF16 or _F16, rounded once; bias fp32 [N] or NULL. The result does not
+ * depend on timing. Codes of NaN and non-finite scales make what they enter non-finite. K a
+ * positive multiple of 16 up to 2^20, M and N below 2^24; M == 0 or N == 0 is a no-op.
+ * `workspace` may be NULL where the size query gives 0; calls that overlap need one each. */
+size_t cubic_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, const cubic_weight_fp8* w,
+                   const float* bias, void* y, int y_dtype, void* workspace, size_t ws_bytes,
+                   cubic_stream_t stream);
+/* The same product of bf16 or fp16 activations x [M][K], quantised on the way by the rule of
+ * cubic_quant_fp8 with block_rows 1: the result of that call followed by cubic_gemm_fp8. */
+size_t cubic_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int cubic_linear_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* w, const float* bias,
+                     void* y, int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream);
+
+/* The gated feed-forward block of a shared expert or a dense layer (Kimi K3 guide, model card:
+ * fused gate_up projections; the routed experts' form of it is cubic_moe_mlp's):
+ *   [g | u] = x W^T      W [2I][H]: gate rows 0 .. I-1, up rows I .. 2I-1
+ *   h       = act(g) * u
+ * act: CUBIC_ACT_SILU, g / (1 + exp(-g)), or CUBIC_ACT_GELU_TANH, 0.5 g (1 + tanh(sqrt(2/pi)
+ * (g + 0.044715 g^3))). x [M][H], w and h [M][I] in one dtype, CUBIC_DTYPE_BF16 or _F16; sums,
+ * activation and product in fp32, h rounded once. pre fp32 [M][2I] receives g and u for the
+ * backward pass, or is NULL (fp32, since g and u rounded to 16 bits would add as much error to
+ * the gradients as the gradients' own rounding). H and I multiples of 8 up to 2^20, M below
+ * 2^24 (CUBIC_ERR_SHAPE); CUBIC_ERR_OPTION for another act. M == 0 is a no-op. `workspace` may
+ * be NULL where the size query gives 0; calls that overlap need one each. */
+enum { CUBIC_ACT_SILU = 0, CUBIC_ACT_GELU_TANH = 1 };
+size_t cubic_gated_ff_workspace_bytes(int64_t M, int64_t H, int64_t I);
+int cubic_gated_ff(const void* x, const void* w, int dtype, int64_t M, int64_t H, int64_t I, int act,
+                   void* h, float* pre, void* workspace, size_t ws_bytes, cubic_stream_t stream);
+/* Its backward pass: from dh [M][I], x, w and the forward's pre,
+ *   dg = dh * u * act'(g),  du = dh * act(g)     fp32, rounded to dtype
+ *   dx = dg Wg + du Wu      [M][H]
+ *   dw = [dg | du]^T x      [2I][H]
+ * with fp32 sums, dx and dw rounded to dtype once. The products take 16-bit operands, which is
+ * why dg and du are rounded: one rounding of each term, of the size of the results' own. dx or
+ * dw may be NULL and is then not computed (w is read for dx alone, x for dw alone, and may be
+ * NULL too). M == 0 writes zeros to dw. dw is overwritten, not added to. */
+size_t cubic_gated_ff_backward_workspace_bytes(int64_t M, int64_t H, int64_t I);
+int cubic_gated_ff_backward(const void* dh, const void* x, const void* w, const float* pre, int dtype,
+                            int64_t M, int64_t H, int64_t I, int act, void* dx, void* dw,
+                            void* workspace, size_t ws_bytes, cubic_stream_t stream);
+/* The block over e4m3 weights (gate_up: N = 2I rows, gate rows first; I a multiple of 128, so
+ * that no block of scales holds rows of both) and activations quantised on the way as in
+ * cubic_linear_fp8: h = act(g) * u in h_dtype CUBIC_DTYPE_BF16 or _F16, from fp32 g and u. */
+size_t cubic_gated_ff_fp8_workspace_bytes(int64_t M, int64_t H, int64_t I);
+int cubic_gated_ff_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* gate_up, int act,
+                       void* h, int h_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

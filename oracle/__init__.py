@@ -5,3 +5,4 @@ TEST INFRASTRUCTURE ONLY. Only ``tests/``, ``__graft_entry__.smoke()`` and the
 HIP library never links, imports or calls it, and shares no code with it.
 """
 from .cubic_oracle import *  # noqa: F401,F403
+from .dense_oracle import *  # noqa: F401,F403
