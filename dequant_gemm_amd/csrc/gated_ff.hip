@@ -2,85 +2,312 @@
 //
 //   [g | u] = x W^T,  h = act(g) * u;   dg = dh * u * act'(g),  du = dh * act(g)
 //   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
 #include "dense.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace cubic {
 namespace {
 
-// C[m][n] = sum_k A(m, k) B(n, k) for 64 x 64 outputs a workgroup, 32 k a step. A(m, k) is
-// a[m * lda + k], or with AT a[k * lda + m]; B likewise.
-template <bool F16, bool AT, bool BT>
-__global__ __launch_bounds__(256) void k_simple16(const uint16_t* __restrict__ a, int64_t lda, const uint16_t* __restrict__ b,
-                                                  int64_t ldb, int64_t M, int64_t N, int64_t K, void* __restrict__ c, int cdt) {
-  constexpr int kStride = 40;
-  __shared__ __align__(16) uint16_t sa[64 * kStride], sb[64 * kStride];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = lane & 15, q = lane >> 4;
-  const int64_t tn = (N + 63) / 64, tile = blockIdx.x;
-  const int64_t m0 = tile / tn * 64, n0 = tile % tn * 64;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  auto stage = [&](auto t_c, const uint16_t* p, int64_t ld, int64_t row0, int64_t rows, int64_t k0, uint16_t* s) {
-    constexpr bool T = decltype(t_c)::value;
+// ---------------------------------------------------------------------------
+// C[m][n] = sum_k A(m, k) B(n, k) in 16-bit operands and fp32 sums. A(m, k) is a[m * lda + k],
+// or with AT a[k * lda + m] (the contraction runs down the rows); B likewise.
+struct TileParams {
+  const uint16_t *a, *b;
+  int64_t lda, ldb;
+  int64_t M, N, K;
+  void* y;                 // [M][ldy], 16 bits, or fp32 when ydt is 0
+  int64_t ldy;
+  int ydt;
+  // gated form: b holds N gate rows and N up rows behind them; y gets act(gate) * up and,
+  // where it is given, pre [M][2 N] both
+  float* pre;
+  int gelu;
+};
+
+// A tile's shape: WM x WN waves with MB x NB blocks of 32 x 32 each.
+template <int MB_, int NB_, int WM_, int WN_>
+struct Tile16 {
+  static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN;
+  static constexpr int TM = 32 * MB * WM, TN = 32 * NB * WN;
+  static constexpr int kStage = 64 * (TM + TN);                  // 32 k of every row
+  // 1024-byte pieces of a stage per wave (the last ones may be past the tile)
+  static constexpr int LA = (TM / 16 + W - 1) / W, LB = (TN / 16 + W - 1) / W, NL = LA + LB;
+  static constexpr int kLds = W == 8 ? 148 * 1024 : (2 * kStage > 64 * 1024 ? 2 * kStage : 64 * 1024);
+  static_assert(2 * kStage <= kLds && kLds <= 160 * 1024, "one compute unit's LDS");
+};
+
+// One operand's stages: rows of 64 bytes (32 k), or with T 32 rows (one k each) of 2 ROWS bytes.
+template <bool T, int ROWS, int W>
+struct Operand {
+  static constexpr int kPieces = ROWS / 8;     // T: 16-byte pieces of a k row
+  static constexpr int kPer = 64 / kPieces;    // T: k rows of a wave's load
+  const uint16_t* p;                           // first row, or with T first column
+  int64_t ld;
+  uint32_t bytes;                              // that the resource covers
+  uint32_t lane_off, step, lane_k, slot;
+  int K, wave;
+  bool on_col;
+
+  __device__ __forceinline__ void init(const uint16_t* base, int64_t ld_, int64_t row0, int64_t rows, int64_t K_, int wave_) {
+    const int lane = threadIdx.x & 63;
+    ld = ld_;
+    K = static_cast<int>(K_);
+    wave = wave_;
     if constexpr (T) {
-      const int k = tid >> 3, row = 8 * (tid & 7);
-      const bool on = k0 + k < K && row0 + row < rows;   // rows a multiple of 8
-      const u32x4 v = on ? *reinterpret_cast<const u32x4*>(p + (k0 + k) * ld + row0 + row) : u32x4{0u, 0u, 0u, 0u};
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[(row + i) * kStride + k] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+      p = base + row0;
+      const int kk = kPer * wave + lane / kPieces, piece = lane % kPieces;
+      lane_k = static_cast<uint32_t>(kk);
+      lane_off = static_cast<uint32_t>(kk) * static_cast<uint32_t>(2 * ld) + 16u * piece;
+      step = static_cast<uint32_t>(kPer * W) * static_cast<uint32_t>(2 * ld);
+      on_col = 8 * piece < rows - row0;        // rows a multiple of 8
+      bytes = 32u * static_cast<uint32_t>(2 * ld);
+      slot = static_cast<uint32_t>(kk) * (2 * ROWS) + (((piece >> 2) ^ swizzle(kk)) << 6) + 16 * (piece & 3);
     } else {
-      const int row = tid >> 2, k = 8 * (tid & 3);
-      const bool on = row0 + row < rows && k0 + k < K;   // K a multiple of 8
-      *reinterpret_cast<u32x4*>(s + row * kStride + k) =
-          on ? *reinterpret_cast<const u32x4*>(p + (row0 + row) * ld + k0 + k) : u32x4{0u, 0u, 0u, 0u};
+      p = base + row0 * ld;
+      lane_k = 16u * (lane & 3);
+      lane_off = static_cast<uint32_t>(16 * wave + (lane >> 2)) * static_cast<uint32_t>(2 * ld) + lane_k;
+      step = 16u * W * static_cast<uint32_t>(2 * ld);
+      on_col = true;
+      bytes = static_cast<uint32_t>(min(static_cast<int64_t>(ROWS), rows - row0)) * static_cast<uint32_t>(2 * ld);
+      slot = 1024u * wave + 64u * (lane >> 2) + 16u * ((lane & 3) ^ ((lane >> 4) & 3));
     }
-  };
-  f32x4 acc[2][2] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += 32) {
-    stage(std::bool_constant<AT>{}, a, lda, m0, M, k0, sa);
-    stage(std::bool_constant<BT>{}, b, ldb, n0, N, k0, sb);
-    __syncthreads();
-    u32x4 fa[2], fb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      fa[i] = *reinterpret_cast<const u32x4*>(sa + (wm + 16 * i + r) * kStride + 8 * q);
-      fb[i] = *reinterpret_cast<const u32x4*>(sb + (wn + 16 * i + r) * kStride + 8 * q);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if constexpr (F16) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, fb[j]), __builtin_bit_cast(f16x8, fa[i]), acc[i][j], 0, 0, 0);
-        } else {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[j]), __builtin_bit_cast(bf16x8, fa[i]), acc[i][j], 0, 0, 0);
-        }
-      }
-    __syncthreads();
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t m = m0 + wm + 16 * i + r, n = n0 + wn + 16 * j + 4 * q + e;
-        if (m < M && n < N) store_as(c, cdt, m * N + n, acc[i][j][e]);
-      }
+  // T: the 64-byte segment of a k row is XORed with this, so that four k rows read at one
+  // segment hit all banks
+  static __device__ __forceinline__ int swizzle(int kk) {
+    constexpr int nseg = ROWS / 32;            // segments of a row
+    return nseg >= 4 ? (kk & 3) : nseg == 2 ? ((kk >> 1) & 1) : 0;
+  }
+  static constexpr bool inside(int g, int wave) { return 16 * (W * g + wave) < ROWS; }
+  // piece g of stage s; past K and past the tile zeros
+  __device__ __forceinline__ u32x4 load(int s, int g) const {
+    if constexpr (T) {
+      const bool on = on_col && inside(g, wave) && 32 * s + static_cast<int>(lane_k) + kPer * W * g < K;
+      return tile_load(tile_rsrc(p + static_cast<int64_t>(s) * 32 * ld, bytes), on ? lane_off + step * g : kPast);
+    } else {
+      const bool on = inside(g, wave) && 64u * static_cast<uint32_t>(s) + lane_k < 2u * static_cast<uint32_t>(K);
+      return tile_load(tile_rsrc(p, bytes), on ? lane_off + 64u * s + step * g : kPast);
+    }
+  }
+  __device__ __forceinline__ void store(unsigned char* st, int g, const u32x4& v) const {
+    if (inside(g, wave)) *reinterpret_cast<u32x4*>(st + slot + 1024 * W * g) = v;
+  }
+};
+
+// Fragments of block `blk` (32 rows) for k 16 ks .. + 15 of a stage: lane l has row l % 32 and
+// eight k from 8 (l / 32) on.
+template <bool T, int ROWS>
+__device__ __forceinline__ s16x8 fragment(const unsigned char* st, int blk, int ks) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (T) {
+    // four k rows of 16 columns at a time come transposed out of LDS
+    typedef __attribute__((address_space(3))) s16x4* LdsPtr;
+    const int grp = lane >> 4, kr = (lane & 15) >> 2;
+    const int kk = 16 * ks + 8 * (grp >> 1) + kr;
+    const unsigned char* at = st + kk * (2 * ROWS) + ((blk ^ Operand<true, ROWS, 1>::swizzle(kr)) << 6) + 32 * (grp & 1) + 8 * (lane & 3);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + 4 * (2 * ROWS)));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  } else {
+    const int c = lane & 31, h = lane >> 5;
+    return *reinterpret_cast<const s16x8*>(st + (32 * blk + c) * 64 + (((2 * ks + h) ^ ((c >> 2) & 3)) << 4));
+  }
 }
 
-template <bool F16, bool AT, bool BT>
-hipError_t simple16(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K, void* c, int cdt,
-                    hipStream_t st) {
-  const int64_t tiles = ((N + 63) / 64) * ((M + 63) / 64);
-  if (tiles >= 1 << 24) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_simple16<F16, AT, BT>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0, st, static_cast<const uint16_t*>(a), lda,
-                     static_cast<const uint16_t*>(b), ldb, M, N, K, c, cdt);
+template <bool F16>
+__device__ __forceinline__ f32x16 mma(const s16x8& a, const s16x8& b, const f32x16& c) {
+  if constexpr (F16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+}
+
+template <class Shape, bool F16, bool AT, bool BT, bool GATED>
+__global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
+  constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL;
+  constexpr int kLoads1 = (NL + 1) / 2;        // pieces of a stage that move in the half step after the barrier
+  constexpr int kStage = Shape::kStage, kBOff = TM * 64;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  int im, in;
+  tile_place(static_cast<int>(blockIdx.x), static_cast<int>((p.M + TM - 1) / TM), static_cast<int>((p.N + TC - 1) / TC), &im, &in);
+  const int64_t m0 = static_cast<int64_t>(im) * TM, n0 = static_cast<int64_t>(in) * TC;
+
+  Operand<AT, TM, W> A;
+  A.init(p.a, p.lda, m0, p.M, p.K, wave);
+  Operand<BT, TN, W> B;
+  // gated: blocks of 32 rows are gate and up in turn, so that a wave holds both of a column
+  uint32_t gated_off[GATED ? LB : 1];
+  __amdgpu_buffer_rsrc_t gated_rs[GATED ? LB : 1];
+  B.init(p.b, p.ldb, n0, p.N, p.K, wave);
+  if constexpr (GATED) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(TC), p.N - n0)) * static_cast<uint32_t>(2 * p.ldb);
+#pragma unroll
+    for (int g = 0; g < LB; ++g) {
+      const int piece = W * g + wave, blk = piece >> 1;
+      gated_rs[g] = tile_rsrc(p.b + ((blk & 1) * p.N + n0) * p.ldb, bytes);
+      gated_off[g] = static_cast<uint32_t>(32 * (blk >> 1) + 16 * (piece & 1) + (lane >> 2)) * static_cast<uint32_t>(2 * p.ldb) + B.lane_k;
+    }
+  }
+  const int S = static_cast<int>((p.K + 31) >> 5);
+  u32x4 gr[2][NL];                             // pieces on their way: stages of either parity
+  auto load = [&](auto set_c, int s, int i) {
+    constexpr int set = decltype(set_c)::value;
+    if (i < LA) {
+      gr[set][i] = A.load(s, i);
+    } else if constexpr (GATED) {
+      const bool on = B.inside(i - LA, wave) && 64u * static_cast<uint32_t>(s) + B.lane_k < 2u * static_cast<uint32_t>(B.K);
+      gr[set][i] = tile_load(gated_rs[i - LA], on ? gated_off[i - LA] + 64u * s : kPast);
+    } else {
+      gr[set][i] = B.load(s, i - LA);
+    }
+  };
+  auto store = [&](auto set_c, int s, int i) {
+    constexpr int set = decltype(set_c)::value;
+    unsigned char* st = smem + (s & 1) * kStage;
+    if (i < LA) {
+      A.store(st, i, gr[set][i]);
+    } else {
+      B.store(st + kBOff, i - LA, gr[set][i]);
+    }
+  };
+  const int wm = wave / WN, wn = wave % WN;
+  auto read_a = [&](int s, int ks, int i) { return fragment<AT, TM>(smem + (s & 1) * kStage, wm * MB + i, ks); };
+  auto read_b = [&](int s, int ks, int j) { return fragment<BT, TN>(smem + (s & 1) * kStage + kBOff, wn * NB + j, ks); };
+
+  f32x16 acc[MB][NB] = {};
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using IL = std::integral_constant<int, kLoads1>;
+  using IN = std::integral_constant<int, NL>;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) load(I0{}, 0, i);
+#pragma unroll
+  for (int i = 0; i < NL; ++i) load(I1{}, 1, i);
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    store(I0{}, 0, i);
+    load(I0{}, 2, i);
+  }
+  tile_barrier();
+#pragma unroll
+  for (int i = 0; i < kLoads1; ++i) {
+    store(I1{}, 1, i);
+    load(I1{}, 3, i);
+  }
+  s16x8 fa[2][MB], fb[2][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
+
+  // One half step: the MFMAs of fragments f (B times A, so that a lane's results are
+  // neighbouring columns of one row). Spread between them: the reads of the other half's
+  // fragments, and for pieces l0 .. l1 - 1 of stage s_st the write to LDS and the load of
+  // the piece two stages later into its registers.
+  auto half = [&](auto f_c, int s_read, int ks, auto set_c, int s_st, auto l0_c, auto l1_c) {
+    constexpr int f = decltype(f_c)::value, l0 = decltype(l0_c)::value, l1 = decltype(l1_c)::value;
+    constexpr int Q = MB * NB;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
+      acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
+#pragma unroll
+      for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
+        if (r < MB) {
+          fa[1 - f][r] = read_a(s_read, ks, r);
+        } else {
+          fb[1 - f][r - MB] = read_b(s_read, ks, r - MB);
+        }
+      }
+#pragma unroll
+      for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) {
+        store(set_c, s_st, r);
+        load(set_c, s_st + 2, r);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Stage s: its second half's fragments are read beside the first half's MFMAs; then
+  // stage s + 1 is whole in LDS (its last pieces were written there) and every wave is
+  // done with stage s, so that after the barrier stage s + 1 is read and stage s + 2
+  // takes the place of s.
+  auto stage = [&](int s, auto next_c, auto after_c) {
+    half(I0{}, s, 1, next_c, s + 1, IL{}, IN{});
+    tile_barrier();
+    half(I1{}, s + 1, 0, after_c, s + 2, I0{}, IL{});
+  };
+  int s = 0;
+  for (; s + 1 < S; s += 2) {
+    stage(s, I1{}, I0{});
+    stage(s + 1, I0{}, I1{});
+  }
+  if (s < S) stage(s, I1{}, I0{});
+
+  if constexpr (GATED) {
+    auto quad = [&](int i, int j, int g) { return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]}; };
+    if (p.pre) {
+      tile_write<MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j, g); });
+      tile_write<MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre + p.N, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j + 1, g); });
+    }
+    tile_write<MB, NB / 2, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
+      const f32x4 a = quad(i, 2 * j, g), u = quad(i, 2 * j + 1, g);
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = act_of(a[e], p.gelu).value * u[e];
+      return v;
+    });
+  } else {
+    tile_write<MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
+      return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    });
+  }
+}
+
+template <class Shape, bool F16, bool AT, bool BT, bool GATED>
+hipError_t launch_shape(const TileParams& p, hipStream_t st) {
+  auto kern = k_tile16<Shape, F16, AT, BT, GATED>;
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
+  if (e != hipSuccess) return e;
+  constexpr int TC = GATED ? Shape::TN / 2 : Shape::TN;
+  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + TC - 1) / TC);
+  if (tiles * 64 * Shape::W >= int64_t{1} << 32) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(64 * Shape::W), Shape::kLds, st, p);
   return hipGetLastError();
+}
+
+template <bool AT, bool BT, bool GATED>
+hipError_t launch_tile16(const TileParams& p, bool f16, hipStream_t st) {
+  const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256;
+  static constexpr int kTiles[][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 128}, {64, 64}};
+  int best = 0;
+  int64_t cost = INT64_MAX;
+  for (int k = 0; k < 5; ++k) {
+    const int tm = kTiles[k][0], tn = kTiles[k][1], tc = GATED ? tn / 2 : tn;
+    const int64_t tiles = ((p.M + tm - 1) / tm) * ((p.N + tc - 1) / tc);
+    const int64_t per = std::max(tm * tn / 64, tm + tn) + 64;   // a stage's MFMA or LDS-fill cycles, and its barrier
+    const int64_t c = (tiles + cu - 1) / cu * per;
+    if (c < cost) { cost = c; best = k; }
+  }
+  auto go = [&](auto shape) {
+    using Shape = decltype(shape);
+    return f16 ? launch_shape<Shape, true, AT, BT, GATED>(p, st) : launch_shape<Shape, false, AT, BT, GATED>(p, st);
+  };
+  switch (best) {
+    case 0: return go(Tile16<2, 4, 4, 2>{});
+    case 1: return go(Tile16<2, 2, 4, 2>{});
+    case 2: return go(Tile16<2, 2, 2, 2>{});
+    case 3: return go(Tile16<1, 2, 2, 2>{});
+    default: return go(Tile16<1, 2, 2, 1>{});
+  }
 }
 
 // h = act(g) * u from pre [M][2 I], four values a thread (I a multiple of 8).
@@ -132,9 +359,8 @@ hipError_t launch_ff_act(const float* pre, int64_t M, int64_t I, int gelu, void*
 }
 
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
-  const hipError_t e = p.f16 ? simple16<true, false, false>(p.x, p.H, p.w, p.H, p.M, 2 * p.I, p.H, p.pre, 0, st)
-                             : simple16<false, false, false>(p.x, p.H, p.w, p.H, p.M, 2 * p.I, p.H, p.pre, 0, st);
-  return e != hipSuccess ? e : launch_ff_act(p.pre, p.M, p.I, p.gelu, p.h, p.f16 ? 2 : 1, st);
+  const int dt = p.f16 ? 2 : 1;
+  return launch_tile16<false, false, true>({p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, p.I, dt, p.pre, p.gelu}, p.f16, st);
 }
 
 hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
@@ -148,14 +374,10 @@ hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   const int dt = p.f16 ? 2 : 1;
   if (p.dx) {
-    e = p.f16 ? simple16<true, false, true>(p.dpre, 2 * p.I, p.w, p.H, p.M, p.H, 2 * p.I, p.dx, dt, st)
-              : simple16<false, false, true>(p.dpre, 2 * p.I, p.w, p.H, p.M, p.H, 2 * p.I, p.dx, dt, st);
+    e = launch_tile16<false, true, false>({p.dpre, p.w, 2 * p.I, p.H, p.M, p.H, 2 * p.I, p.dx, p.H, dt, nullptr, 0}, p.f16, st);
     if (e != hipSuccess) return e;
   }
-  if (p.dw) {
-    e = p.f16 ? simple16<true, true, true>(p.dpre, 2 * p.I, p.x, p.H, 2 * p.I, p.H, p.M, p.dw, dt, st)
-              : simple16<false, true, true>(p.dpre, 2 * p.I, p.x, p.H, 2 * p.I, p.H, p.M, p.dw, dt, st);
-  }
+  if (p.dw) e = launch_tile16<true, true, false>({p.dpre, p.x, 2 * p.I, p.H, 2 * p.I, p.H, p.M, p.dw, p.H, dt, nullptr, 0}, p.f16, st);
   return e;
 }
 

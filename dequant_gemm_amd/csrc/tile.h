@@ -1,0 +1,116 @@
+// tile.h -- what the dense tile kernels (gated_ff.hip, fp8.hip) share: buffer loads, the
+// order of tiles over the compute units, and the way of a tile's results through LDS.
+#pragma once
+#include "common.h"
+#include "dense.h"
+
+namespace cubic {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr uint32_t kPast = 0xffffffffu;        // an offset behind every buffer: the load gives zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
+                                           static_cast<int>(0x00020000u));
+}
+__device__ __forceinline__ u32x4 tile_load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0));
+}
+// A barrier that leaves global loads in flight.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tile `t` of tm x tn to (row, column): neighbouring workgroup ids go to different XCDs, so
+// each XCD takes a run of tiles, in groups of four tile rows (a run's tiles share operand
+// rows in its L2).
+__device__ __forceinline__ void tile_place(int t, int tm, int tn, int* im, int* in) {
+  const int nt = tm * tn, base = nt >> 3, rem = nt & 7, x = t & 7;
+  t = x * base + min(x, rem) + (t >> 3);
+  const int per = 4 * tn, grp = t / per, r = t - grp * per;
+  const int gm = min(4, tm - 4 * grp);
+  *im = 4 * grp + r % gm;
+  *in = r / gm;
+}
+
+// Writes a tile's results to y[m][n] (row stride ld) through LDS, so that rows leave in whole
+// 16-byte pieces. The tile has WM x WN waves with MB x CB blocks of 32 x 32 each, a lane
+// holding row c and four neighbouring columns for every g: value(i, j, g) gives them as four
+// floats. Rows go in NP passes of what fits in kSpace bytes. Starts and ends with a barrier.
+template <int MB, int CB, int WM, int WN, int kBytes, int kSpace, class Value>
+__device__ __forceinline__ void tile_write(unsigned char* smem, void* y, int ydt, int64_t ld, int64_t m0, int64_t M, int64_t n0,
+                                           int64_t N, Value value) {
+  constexpr int TC = 32 * CB * WN, kThreads = 64 * WM * WN, kStride = TC * kBytes + 16, kPer = 16 / kBytes;
+  constexpr auto passes = [] {
+    int np = 1;
+    while (np < MB && 32 * MB * WM / np * kStride > kSpace) np *= 2;
+    return np;
+  };
+  constexpr int NP = passes(), BP = MB / NP, kRows = 32 * BP * WM;
+  static_assert(kRows * kStride <= 160 * 1024 && BP * NP == MB, "passes of whole blocks that fit");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c = lane & 31, h = lane >> 5, wm = wave / WN, wn = wave % WN;
+  const int cols = static_cast<int>(min(static_cast<int64_t>(TC), N - n0));
+  const bool whole = ld % kPer == 0 && cols % kPer == 0;       // rows start on 16 bytes
+#pragma unroll
+  for (int ip = 0; ip < NP; ++ip) {
+    __syncthreads();
+#pragma unroll
+    for (int ib = 0; ib < BP; ++ib) {
+      const int i = ip * BP + ib;
+      unsigned char* row = smem + (wm * 32 * BP + 32 * ib + c) * kStride;
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int n = wn * 32 * CB + 32 * j + 8 * g + 4 * h;
+          const f32x4 v = value(i, j, g);
+          if constexpr (kBytes == 4) {
+            *reinterpret_cast<f32x4*>(row + 4 * n) = v;
+          } else {
+            uint2 w;
+            if (ydt == 2) {
+              w = make_uint2(bits16<true>(v[0]) | bits16<true>(v[1]) << 16, bits16<true>(v[2]) | bits16<true>(v[3]) << 16);
+            } else {
+              w = make_uint2(bits16<false>(v[0]) | bits16<false>(v[1]) << 16, bits16<false>(v[2]) | bits16<false>(v[3]) << 16);
+            }
+            *reinterpret_cast<uint2*>(row + 2 * n) = w;
+          }
+        }
+    }
+    __syncthreads();
+    auto global_row = [&](int r) {
+      const int w = r / (32 * BP);
+      return m0 + w * 32 * MB + ip * 32 * BP + (r - w * 32 * BP);
+    };
+    unsigned char* out = static_cast<unsigned char*>(y);
+    if (whole) {
+      constexpr int kPieces = TC / kPer;
+      for (int idx = tid; idx < kRows * kPieces; idx += kThreads) {
+        const int r = idx / kPieces, q = idx - r * kPieces;
+        const int64_t m = global_row(r);
+        if (m < M && q * kPer < cols)
+          *reinterpret_cast<u32x4*>(out + (m * ld + n0 + q * kPer) * kBytes) = *reinterpret_cast<const u32x4*>(smem + r * kStride + 16 * q);
+      }
+    } else {
+      for (int idx = tid; idx < kRows * TC; idx += kThreads) {
+        const int r = idx / TC, q = idx - r * TC;
+        const int64_t m = global_row(r);
+        if (m < M && q < cols) {
+          if constexpr (kBytes == 2) {
+            reinterpret_cast<uint16_t*>(out)[m * ld + n0 + q] = reinterpret_cast<const uint16_t*>(smem + r * kStride)[q];
+          } else {
+            reinterpret_cast<float*>(out)[m * ld + n0 + q] = reinterpret_cast<const float*>(smem + r * kStride)[q];
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+}
+
+}  // namespace cubic
