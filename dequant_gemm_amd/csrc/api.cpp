@@ -953,7 +953,6 @@ int check_ff(int64_t M, int64_t H, int64_t I, int dtype, int act) {
   if (act != CUBIC_ACT_SILU && act != CUBIC_ACT_GELU_TANH) return CUBIC_ERR_OPTION;
   return CUBIC_OK;
 }
-size_t pre_bytes(int64_t M, int64_t I) { return align256(static_cast<size_t>(M) * I * 8); }
 }  // namespace
 
 CUBIC_API size_t cubic_gated_ff_workspace_bytes(int64_t M, int64_t H, int64_t I) {
@@ -1020,7 +1019,7 @@ CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void*
 
 CUBIC_API size_t cubic_gated_ff_fp8_workspace_bytes(int64_t M, int64_t H, int64_t I) {
   if (M <= 0 || H <= 0 || I <= 0) return 0;
-  return fp8_staging_bytes(M, H) + pre_bytes(M, I);
+  return fp8_staging_bytes(M, H);
 }
 
 CUBIC_API int cubic_gated_ff_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* gate_up, int act, void* h, int h_dtype,
@@ -1035,12 +1034,9 @@ CUBIC_API int cubic_gated_ff_fp8(const void* x, int x_dtype, int64_t M, const cu
   if (!aligned16(x) || !aligned16(h) || !aligned16(workspace)) return CUBIC_ERR_ALIGN;
   const int64_t I = gate_up->N / 2, H = gate_up->K;
   if (!workspace || ws_bytes < cubic_gated_ff_fp8_workspace_bytes(M, H, I)) return CUBIC_ERR_WORKSPACE;
-  char* ws = static_cast<char*>(workspace);
-  float* pre = reinterpret_cast<float*>(ws + fp8_staging_bytes(M, H));
-  Fp8Params p = fp8_params(gate_up, M, nullptr, pre, CUBIC_DTYPE_F32);
+  Fp8Params p = fp8_params(gate_up, M, nullptr, h, h_dtype);
+  p.gelu = act == CUBIC_ACT_GELU_TANH ? 1 : 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = fp8_stage(&p, x, x_dtype, ws, s);
-  if (e == hipSuccess) e = launch_fp8(p, s);
-  if (e == hipSuccess) e = launch_ff_act(pre, M, I, act == CUBIC_ACT_GELU_TANH ? 1 : 0, h, h_dtype, s);
-  return hip_status(e);
+  const hipError_t e = fp8_stage(&p, x, x_dtype, static_cast<char*>(workspace), s);
+  return hip_status(e != hipSuccess ? e : launch_fp8_gated(p, s));
 }

@@ -11,6 +11,7 @@
 #include "common.h"
 #include "dense.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace cubic {
 namespace {
@@ -73,66 +74,248 @@ __global__ __launch_bounds__(256) void k_quant_fp8_blocks(const uint16_t* __rest
   }
 }
 
-// 64 x 64 outputs a workgroup, one block of 128 codes a step.
-__global__ __launch_bounds__(256) void k_fp8_simple(Fp8Params p) {
-  constexpr int kStride = 128 + 16;
-  __shared__ __align__(16) unsigned char sa[64 * kStride], sb[64 * kStride];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = lane & 15, q = lane >> 4;
-  const int64_t tn = (p.N + 63) / 64, tile = blockIdx.x;
-  const int64_t m0 = tile / tn * 64, n0 = tile % tn * 64;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  const int64_t kb = (p.K + 127) / 128;
-  f32x4 acc[2][2] = {};
-  for (int64_t b = 0; b < kb; ++b) {
+// ---------------------------------------------------------------------------
+// A tile's shape: WM x WN waves with MB x NB blocks of 16 x 16 each.
+template <int MB_, int NB_, int WM_, int WN_>
+struct Tile8 {
+  static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN;
+  static constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN;
+  static constexpr int kStage = 128 * (TM + TN) + 4 * TM;        // 128 codes of every row, the rows' scales
+  // 1024-byte pieces of a stage per wave (eight rows each)
+  static constexpr int LA = TM / 8 / W, LB = TN / 8 / W, NL = LA + LB;
+  static_assert(LA * 8 * W == TM && LB * 8 * W == TN && TM <= 64 * W && 16 * NB <= 128 && 128 % (16 * NB) == 0, "whole pieces; a wave's rows in one block");
+  static constexpr int kLds = W == 8 ? 148 * 1024 : (2 * kStage > 64 * 1024 ? 2 * kStage : 64 * 1024);
+  static_assert(2 * kStage <= kLds && kLds <= 160 * 1024, "one compute unit's LDS");
+};
+
+// One 16 x 16 block of results over the 128 codes of a stage. EXACT: on the bf16 MFMA, whose
+// products and sums of such codes are those of fp32; else on the 8-bit one, twice as fast,
+// which drops what lies below about 2^-14 of the largest of the products that it adds
+// (2-norm of the sums off by 1.3e-5 to 2.2e-5: far below a 16-bit result's own rounding).
+template <bool EXACT>
+__device__ __forceinline__ f32x4 fp8_dot(const i32x8& a, const i32x8& b) {
+  f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (EXACT) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int idx = tid + 256 * i, row = idx >> 3, piece = idx & 7;
-      const int64_t k = b * 128 + 16 * piece;
-      const u32x4 zero{0u, 0u, 0u, 0u};
-      *reinterpret_cast<u32x4*>(sa + row * kStride + 16 * piece) =
-          m0 + row < p.M && k < p.K ? *reinterpret_cast<const u32x4*>(p.xq + (m0 + row) * p.K + k) : zero;
-      *reinterpret_cast<u32x4*>(sb + row * kStride + 16 * piece) =
-          n0 + row < p.N && k < p.K ? *reinterpret_cast<const u32x4*>(p.w + (n0 + row) * p.K + k) : zero;
-    }
-    __syncthreads();
-    f32x4 part[2][2] = {};
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      bf16x8 fa[2], fb[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fa[i] = e4m3x8_to_bf16(*reinterpret_cast<const u32x2*>(sa + (wm + 16 * i + r) * kStride + 32 * s + 8 * q));
-        fb[i] = e4m3x8_to_bf16(*reinterpret_cast<const u32x2*>(sb + (wn + 16 * i + r) * kStride + 32 * s + 8 * q));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], part[i][j], 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t m = m0 + wm + 16 * i + r;
-      const float xs = m < p.M ? p.xs[m * kb + b] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t n = n0 + wn + 16 * j;
-        const float s = xs * (n < p.N ? p.ws[(n >> 7) * kb + b] : 0.0f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(part[i][j][e], s, acc[i][j][e]);
-      }
-    }
-    __syncthreads();
+    for (int s = 0; s < 4; ++s)
+      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(a[2 * s]), static_cast<uint32_t>(a[2 * s + 1])}),
+          e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(b[2 * s]), static_cast<uint32_t>(b[2 * s + 1])}), part, 0, 0, 0);
+  } else {
+    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part, 0, 0, 0, 127, 0, 127);   // scales 2^0
   }
+  return part;
+}
+
+template <class Shape, bool EXACT, bool GATED>
+__global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
+  constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL;
+  constexpr int kStage = Shape::kStage, kBOff = TM * 128, kSOff = kBOff + TN * 128;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t N = GATED ? p.N / 2 : p.N;     // columns of results
+  int im, in;
+  tile_place(static_cast<int>(blockIdx.x), static_cast<int>((p.M + TM - 1) / TM), static_cast<int>((N + TC - 1) / TC), &im, &in);
+  const int64_t m0 = static_cast<int64_t>(im) * TM, n0 = static_cast<int64_t>(in) * TC;
+  const uint32_t K = static_cast<uint32_t>(p.K);
+  const int64_t kb = (p.K + 127) >> 7;
+  const int S = static_cast<int>(kb);
+
+  // ---- stage loads: wave w takes rows 8 (W i + w) .. + 7 of A, then of B; lane l loads the
+  // 16-byte piece l % 8 of row l / 8 into registers and writes it to slot piece ^ (row / 2 %
+  // 8) of the row (any 16 rows read at one piece hit all banks) ----
+  const uint32_t lane_k = 16u * (lane & 7);
+  const uint32_t base = static_cast<uint32_t>(8 * wave + (lane >> 3)) * K + lane_k;
+  const uint32_t slot = 1024u * wave + 128u * (lane >> 3) + 16u * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+  const __amdgpu_buffer_rsrc_t ars = tile_rsrc(p.xq + m0 * p.K, static_cast<uint32_t>(min(static_cast<int64_t>(TM), p.M - m0)) * K);
+  __amdgpu_buffer_rsrc_t brs[LB];
+  uint32_t boff[LB];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int g = 0; g < LB; ++g) {
+    const uint32_t rows = static_cast<uint32_t>(min(static_cast<int64_t>(TC), N - n0));
+    if constexpr (GATED) {                     // blocks of 16 rows are gate and up in turn
+      const int row = 8 * (W * g + wave), blk = row >> 4;
+      brs[g] = tile_rsrc(p.w + ((blk & 1) * N + n0) * p.K, rows * K);
+      boff[g] = static_cast<uint32_t>(16 * (blk >> 1) + (row & 15) + (lane >> 3)) * K + lane_k;
+    } else {
+      brs[g] = tile_rsrc(p.w + n0 * p.K, rows * K);
+      boff[g] = base + 8u * W * g * K;
+    }
+  }
+  const float* xs = p.xs + m0 * kb;
+  const __amdgpu_buffer_rsrc_t srs = tile_rsrc(xs, static_cast<uint32_t>(min(static_cast<int64_t>(TM), p.M - m0) * kb * 4));
+  u32x4 gr[NL];
+  float sr = 0.0f;
+  auto load = [&](int s, int i) {              // piece i of stage s; past K and past the rows zeros
+    const uint32_t k = 128u * static_cast<uint32_t>(s);
+    const bool on = k + lane_k < K;
+    if (i < LA) {
+      gr[i] = tile_load(ars, on ? base + k + 8u * W * i * K : kPast);
+    } else {
+      gr[i] = tile_load(brs[i - LA], on ? boff[i - LA] + k : kPast);
+    }
+  };
+  auto load_scale = [&](int s) {
+    const bool on = tid < TM && s < S;
+    sr = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(srs, on ? static_cast<int>(4u * (static_cast<uint32_t>(tid) * static_cast<uint32_t>(kb) + static_cast<uint32_t>(s))) : -1, 0, 0));
+  };
+  auto store = [&](int s, int i) {
+    unsigned char* st = smem + (s & 1) * kStage;
+    *reinterpret_cast<u32x4*>(st + (i < LA ? 1024 * W * i : kBOff + 1024 * W * (i - LA)) + slot) = gr[i];
+  };
+  auto store_scale = [&](int s) {
+    if (tid < TM) *reinterpret_cast<float*>(smem + (s & 1) * kStage + kSOff + 4 * tid) = sr;
+  };
+
+  const int wm = wave / WN, wn = wave % WN;
+  const int c = lane & 15, q = lane >> 4;
+  const uint32_t f0 = 128u * c + 16u * (q ^ (c >> 1)), f1 = 128u * c + 16u * ((q + 4) ^ (c >> 1));
+  auto frag = [&](const unsigned char* at) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(at + f0), hi = *reinterpret_cast<const i32x4*>(at + f1);
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  auto read_a = [&](int s, int i) { return frag(smem + (s & 1) * kStage + (wm * MB + i) * 2048); };
+  auto read_b = [&](int s, int j) { return frag(smem + (s & 1) * kStage + kBOff + (wn * NB + j) * 2048); };
+  auto read_scale = [&](int s, int i) { return *reinterpret_cast<const float*>(smem + (s & 1) * kStage + kSOff + 4 * ((wm * MB + i) * 16 + c)); };
+  // the wave's weight rows lie in one block of scales (gated: gate and up in one each)
+  const int64_t nb = GATED ? n0 + 8 * NB * wn : n0 + 16 * NB * wn;
+  const float* ws0 = p.ws + (min(nb, N - 1) >> 7) * kb;
+  const float* ws1 = GATED ? p.ws + ((N + min(nb, N - 1)) >> 7) * kb : ws0;
+
+  f32x4 acc[MB][NB] = {};
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+  for (int i = 0; i < NL; ++i) load(0, i);
+  load_scale(0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t m = m0 + wm + 16 * i + r, n = n0 + wn + 16 * j + 4 * q + e;
-        if (m < p.M && n < p.N) store_as(p.y, p.ydt, m * p.N + n, acc[i][j][e] + (p.bias ? p.bias[n] : 0.0f));
+  for (int i = 0; i < NL; ++i) {
+    store(0, i);
+    load(1, i);
+  }
+  store_scale(0);
+  load_scale(1);
+  tile_barrier();
+  i32x8 fa[MB], fb[2];
+  float sx[MB], sc0[MB], sc1[GATED ? MB : 1];
+  fb[0] = read_b(0, 0);
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    fa[i] = read_a(0, i);
+    sx[i] = read_scale(0, i);
+  }
+  float w0 = ws0[0], w1 = ws1[0];
+  constexpr int Q = MB * NB, kLag = 2;         // results are added this many MFMAs later
+  static_assert(NB % 2 == 0, "fb[0] holds a stage's first block again");
+  for (int s = 0; s < S; ++s) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      sc0[i] = sx[i] * w0;
+      if constexpr (GATED) sc1[i] = sx[i] * w1;
+    }
+    w0 = ws0[min(s + 1, S - 1)];
+    if constexpr (GATED) w1 = ws1[min(s + 1, S - 1)];
+    f32x4 part[kLag + 1];
+    auto add = [&](int t) {
+      const int i = t % MB, j = t / MB;
+      const float f = GATED && (j & 1) ? sc1[GATED ? i : 0] : sc0[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(part[t % (kLag + 1)][e], f, acc[i][j][e]);
+    };
+#pragma unroll
+    for (int t = 0; t < Q; ++t) {
+      const int i = t % MB, j = t / MB;
+      if (i == 0 && j == NB - 1) {
+        // every wave has this stage's last fragments in registers and the next stage in
+        // LDS: the next stage is read from here on
+        tile_barrier();
+        fb[(j + 1) & 1] = read_b(s + 1, 0);
+      } else if (i == 0) {
+        fb[(j + 1) & 1] = read_b(s, j + 1);
       }
+      part[t % (kLag + 1)] = fp8_dot<EXACT>(fb[j & 1], fa[i]);
+      if (j == NB - 1) {
+        fa[i] = read_a(s + 1, i);
+        sx[i] = read_scale(s + 1, i);
+      }
+      if (t >= kLag) add(t - kLag);
+      // the next stage into LDS and the one after it into its registers, in the first
+      // NB - 1 of NB parts
+      constexpr int kOver = MB * (NB - 1);
+#pragma unroll
+      for (int r = t * NL / kOver; r < (t + 1) * NL / kOver && r < NL; ++r) {
+        store(s + 1, r);
+        load(s + 2, r);
+      }
+      if (t == 0) {
+        store_scale(s + 1);
+        load_scale(s + 2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int t = Q - kLag; t < Q; ++t) add(t);
+  }
+
+  if constexpr (GATED) {
+    tile_write<16, MB, NB / 2, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, N, m0, p.M, n0, N, [&](int i, int j, int) {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = act_of(acc[i][2 * j][e], p.gelu).value * acc[i][2 * j + 1][e];
+      return v;
+    });
+  } else {
+    auto value = [&](int i, int j, int) {
+      f32x4 v = acc[i][j];
+      if (p.bias) {
+        const int64_t n = n0 + 16 * (wn * NB + j) + 4 * q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += n + e < N ? p.bias[n + e] : 0.0f;
+      }
+      return v;
+    };
+    if constexpr (EXACT) {
+      tile_write<16, MB, NB, WM, WN, 4, Shape::kLds>(smem, p.y, 0, N, m0, p.M, n0, N, value);
+    } else {
+      tile_write<16, MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, N, m0, p.M, n0, N, value);
+    }
+  }
+}
+
+template <class Shape, bool EXACT, bool GATED>
+hipError_t launch_tile8(const Fp8Params& p, hipStream_t st) {
+  auto kern = k_fp8_tile<Shape, EXACT, GATED>;
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
+  if (e != hipSuccess) return e;
+  const int64_t N = GATED ? p.N / 2 : p.N, TC = GATED ? Shape::TN / 2 : Shape::TN;
+  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((N + TC - 1) / TC);
+  if (tiles * 64 * Shape::W >= int64_t{1} << 32) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(64 * Shape::W), Shape::kLds, st, p);
+  return hipGetLastError();
+}
+
+template <bool GATED>
+hipError_t launch_fp8_tiles(const Fp8Params& p, hipStream_t st) {
+  // fp32 results: a smaller tile, since the converted operands take registers
+  if (!GATED && p.ydt == 0) return launch_tile8<Tile8<4, 4, 2, 2>, true, false>(p, st);
+  const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256, N = GATED ? p.N / 2 : p.N;
+  static constexpr int kTiles[][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 128}, {64, 64}};
+  int best = 0;
+  int64_t cost = INT64_MAX;
+  for (int k = 0; k < 5; ++k) {
+    const int tm = kTiles[k][0], tn = kTiles[k][1], tc = GATED ? tn / 2 : tn;
+    const int64_t tiles = ((p.M + tm - 1) / tm) * ((N + tc - 1) / tc);
+    const int64_t per = std::max(tm * tn / 64, tm + tn) + 64;   // a stage's MFMA or LDS-fill cycles, and its barrier
+    const int64_t c = (tiles + cu - 1) / cu * per;
+    if (c < cost) { cost = c; best = k; }
+  }
+  switch (best) {
+    case 0: return launch_tile8<Tile8<4, 8, 4, 2>, false, GATED>(p, st);
+    case 1: return launch_tile8<Tile8<4, 4, 4, 2>, false, GATED>(p, st);
+    case 2: return launch_tile8<Tile8<4, 4, 2, 2>, false, GATED>(p, st);
+    case 3: return launch_tile8<Tile8<2, 4, 2, 2>, false, GATED>(p, st);
+    default: return launch_tile8<Tile8<2, 2, 2, 2>, false, GATED>(p, st);
+  }
 }
 
 }  // namespace
@@ -152,11 +335,8 @@ hipError_t launch_quant_fp8(const uint16_t* x, bool xf16, int64_t M, int64_t K, 
   return hipGetLastError();
 }
 
-hipError_t launch_fp8(const Fp8Params& p, hipStream_t st) {
-  const int64_t tiles = ((p.N + 63) / 64) * ((p.M + 63) / 64);
-  if (tiles > kMaxGrid) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(k_fp8_simple, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, st, p);
-  return hipGetLastError();
-}
+hipError_t launch_fp8(const Fp8Params& p, hipStream_t st) { return launch_fp8_tiles<false>(p, st); }
+
+hipError_t launch_fp8_gated(const Fp8Params& p, hipStream_t st) { return launch_fp8_tiles<true>(p, st); }
 
 }  // namespace cubic

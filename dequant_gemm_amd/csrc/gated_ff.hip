@@ -255,10 +255,10 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   if constexpr (GATED) {
     auto quad = [&](int i, int j, int g) { return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]}; };
     if (p.pre) {
-      tile_write<MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j, g); });
-      tile_write<MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre + p.N, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j + 1, g); });
+      tile_write<32, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j, g); });
+      tile_write<32, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre + p.N, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j + 1, g); });
     }
-    tile_write<MB, NB / 2, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
+    tile_write<32, MB, NB / 2, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
       const f32x4 a = quad(i, 2 * j, g), u = quad(i, 2 * j + 1, g);
       f32x4 v;
 #pragma unroll
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
       return v;
     });
   } else {
-    tile_write<MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
+    tile_write<32, MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
       return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
     });
   }
@@ -310,18 +310,6 @@ hipError_t launch_tile16(const TileParams& p, bool f16, hipStream_t st) {
   }
 }
 
-// h = act(g) * u from pre [M][2 I], four values a thread (I a multiple of 8).
-__global__ __launch_bounds__(256) void k_ff_act(const float* __restrict__ pre, int64_t M, int64_t I, int gelu, void* __restrict__ h,
-                                                int hdt) {
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256, quads = M * (I >> 2);
-  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < quads; v += step) {
-    const int64_t m = v / (I >> 2), i = 4 * (v - m * (I >> 2));
-    const f32x4 g = *reinterpret_cast<const f32x4*>(pre + m * 2 * I + i), u = *reinterpret_cast<const f32x4*>(pre + m * 2 * I + I + i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) store_as(h, hdt, m * I + i + e, act_of(g[e], gelu).value * u[e]);
-  }
-}
-
 // [dg | du] from pre and dh, in the operands' type: the products that follow take 16-bit
 // operands, and their results are 16-bit values of the same type.
 template <bool F16>
@@ -352,11 +340,6 @@ unsigned quad_grid(int64_t M, int64_t I) {
 }
 
 }  // namespace
-
-hipError_t launch_ff_act(const float* pre, int64_t M, int64_t I, int gelu, void* h, int hdt, hipStream_t st) {
-  hipLaunchKernelGGL(k_ff_act, dim3(quad_grid(M, I)), dim3(256), 0, st, pre, M, I, gelu, h, hdt);
-  return hipGetLastError();
-}
 
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
   const int dt = p.f16 ? 2 : 1;

@@ -222,11 +222,14 @@ struct Fp8Params {
   int64_t M, N, K;
   void* y;                 // [M][N]
   int ydt;
+  int gelu;                // launch_fp8_gated
 };
 // One scale per 128 channels of a row, or (blocks) per 128 x 128 values.
 hipError_t launch_quant_fp8(const uint16_t* x, bool xf16, int64_t M, int64_t K, bool blocks, uint8_t* xq, float* xs,
                             hipStream_t st);
 hipError_t launch_fp8(const Fp8Params& p, hipStream_t st);
+// N = 2 I rows of w, gate rows first (I a multiple of 128): y [M][I] = act(gate) * up in bf16 or fp16
+hipError_t launch_fp8_gated(const Fp8Params& p, hipStream_t st);
 
 // The gated feed-forward block over 16-bit weights (gated_ff.hip).
 struct FfParams {
@@ -243,7 +246,5 @@ struct FfParams {
 };
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st);
 hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st);
-// h [M][I] in hdt = act(gate) * up of pre [M][2 I]
-hipError_t launch_ff_act(const float* pre, int64_t M, int64_t I, int gelu, void* h, int hdt, hipStream_t st);
 
 }  // namespace cubic

@@ -38,22 +38,23 @@ __device__ __forceinline__ void tile_place(int t, int tm, int tn, int* im, int* 
 }
 
 // Writes a tile's results to y[m][n] (row stride ld) through LDS, so that rows leave in whole
-// 16-byte pieces. The tile has WM x WN waves with MB x CB blocks of 32 x 32 each, a lane
-// holding row c and four neighbouring columns for every g: value(i, j, g) gives them as four
-// floats. Rows go in NP passes of what fits in kSpace bytes. Starts and ends with a barrier.
-template <int MB, int CB, int WM, int WN, int kBytes, int kSpace, class Value>
+// 16-byte pieces. The tile has WM x WN waves with MB x CB blocks of BLK x BLK (32 or 16) each, a
+// lane holding row c and four neighbouring columns, 8 g + 4 h on in the block: value(i, j, g)
+// gives them as four floats. Rows go in NP passes of what fits in kSpace bytes. Starts and
+// ends with a barrier.
+template <int BLK, int MB, int CB, int WM, int WN, int kBytes, int kSpace, class Value>
 __device__ __forceinline__ void tile_write(unsigned char* smem, void* y, int ydt, int64_t ld, int64_t m0, int64_t M, int64_t n0,
                                            int64_t N, Value value) {
-  constexpr int TC = 32 * CB * WN, kThreads = 64 * WM * WN, kStride = TC * kBytes + 16, kPer = 16 / kBytes;
+  constexpr int TC = BLK * CB * WN, kThreads = 64 * WM * WN, kStride = TC * kBytes + 16, kPer = 16 / kBytes;
   constexpr auto passes = [] {
     int np = 1;
-    while (np < MB && 32 * MB * WM / np * kStride > kSpace) np *= 2;
+    while (np < MB && BLK * MB * WM / np * kStride > kSpace) np *= 2;
     return np;
   };
-  constexpr int NP = passes(), BP = MB / NP, kRows = 32 * BP * WM;
+  constexpr int NP = passes(), BP = MB / NP, kRows = BLK * BP * WM;
   static_assert(kRows * kStride <= 160 * 1024 && BP * NP == MB, "passes of whole blocks that fit");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int c = lane & 31, h = lane >> 5, wm = wave / WN, wn = wave % WN;
+  const int c = lane & (BLK - 1), h = lane / BLK, wm = wave / WN, wn = wave % WN;
   const int cols = static_cast<int>(min(static_cast<int64_t>(TC), N - n0));
   const bool whole = ld % kPer == 0 && cols % kPer == 0;       // rows start on 16 bytes
 #pragma unroll
@@ -62,12 +63,12 @@ __device__ __forceinline__ void tile_write(unsigned char* smem, void* y, int ydt
 #pragma unroll
     for (int ib = 0; ib < BP; ++ib) {
       const int i = ip * BP + ib;
-      unsigned char* row = smem + (wm * 32 * BP + 32 * ib + c) * kStride;
+      unsigned char* row = smem + (wm * BLK * BP + BLK * ib + c) * kStride;
 #pragma unroll
       for (int j = 0; j < CB; ++j)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int n = wn * 32 * CB + 32 * j + 8 * g + 4 * h;
+        for (int g = 0; g < BLK / 8 * BLK / 32; ++g) {
+          const int n = wn * BLK * CB + BLK * j + 8 * g + 4 * h;
           const f32x4 v = value(i, j, g);
           if constexpr (kBytes == 4) {
             *reinterpret_cast<f32x4*>(row + 4 * n) = v;
@@ -84,8 +85,8 @@ __device__ __forceinline__ void tile_write(unsigned char* smem, void* y, int ydt
     }
     __syncthreads();
     auto global_row = [&](int r) {
-      const int w = r / (32 * BP);
-      return m0 + w * 32 * MB + ip * 32 * BP + (r - w * 32 * BP);
+      const int w = r / (BLK * BP);
+      return m0 + w * BLK * MB + ip * BLK * BP + (r - w * BLK * BP);
     };
     unsigned char* out = static_cast<unsigned char*>(y);
     if (whole) {
