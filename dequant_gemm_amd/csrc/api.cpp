@@ -864,7 +864,9 @@ int check_weight_fp8(const cubic_weight_fp8* w, int64_t M) {
 }
 
 size_t fp8_codes_bytes(int64_t M, int64_t K) { return align256(static_cast<size_t>(M) * K); }
+// The activations' codes and scales, where the product does not quantise them itself.
 size_t fp8_staging_bytes(int64_t M, int64_t K) {
+  if (fp8_quantises(M, K)) return 0;
   return fp8_codes_bytes(M, K) + align256(static_cast<size_t>(M) * blocks128(K) * 4);
 }
 
@@ -881,8 +883,12 @@ Fp8Params fp8_params(const cubic_weight_fp8* w, int64_t M, const float* bias, vo
   return p;
 }
 
-// x quantised into the workspace's first part; p's activations are that.
+// x quantised into the workspace's first part, or for the product to quantise.
 hipError_t fp8_stage(Fp8Params* p, const void* x, int x_dtype, char* ws, hipStream_t s) {
+  if (fp8_quantises(p->M, p->K)) {
+    p->x = static_cast<const uint16_t*>(x);
+    return hipSuccess;
+  }
   uint8_t* xq = reinterpret_cast<uint8_t*>(ws);
   float* xs = reinterpret_cast<float*>(ws + fp8_codes_bytes(p->M, p->K));
   p->xq = xq;
@@ -921,7 +927,7 @@ CUBIC_API int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M,
   Fp8Params p = fp8_params(w, M, bias, y, y_dtype);
   p.xq = xq;
   p.xs = x_scale;
-  return hip_status(launch_fp8(p, static_cast<hipStream_t>(stream)));
+  return hip_status(launch_fp8(p, false, static_cast<hipStream_t>(stream)));
 }
 
 CUBIC_API size_t cubic_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -942,7 +948,7 @@ CUBIC_API int cubic_linear_fp8(const void* x, int x_dtype, int64_t M, const cubi
   Fp8Params p = fp8_params(w, M, bias, y, y_dtype);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = fp8_stage(&p, x, x_dtype, static_cast<char*>(workspace), s);
-  return hip_status(e != hipSuccess ? e : launch_fp8(p, s));
+  return hip_status(e != hipSuccess ? e : launch_fp8(p, x_dtype == CUBIC_DTYPE_F16, s));
 }
 
 namespace {
@@ -1033,10 +1039,11 @@ CUBIC_API int cubic_gated_ff_fp8(const void* x, int x_dtype, int64_t M, const cu
   if (!x || !h) return CUBIC_ERR_NULL;
   if (!aligned16(x) || !aligned16(h) || !aligned16(workspace)) return CUBIC_ERR_ALIGN;
   const int64_t I = gate_up->N / 2, H = gate_up->K;
-  if (!workspace || ws_bytes < cubic_gated_ff_fp8_workspace_bytes(M, H, I)) return CUBIC_ERR_WORKSPACE;
+  const size_t need = cubic_gated_ff_fp8_workspace_bytes(M, H, I);
+  if (need > 0 && (!workspace || ws_bytes < need)) return CUBIC_ERR_WORKSPACE;
   Fp8Params p = fp8_params(gate_up, M, nullptr, h, h_dtype);
   p.gelu = act == CUBIC_ACT_GELU_TANH ? 1 : 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = fp8_stage(&p, x, x_dtype, static_cast<char*>(workspace), s);
-  return hip_status(e != hipSuccess ? e : launch_fp8_gated(p, s));
+  return hip_status(e != hipSuccess ? e : launch_fp8_gated(p, x_dtype == CUBIC_DTYPE_F16, s));
 }

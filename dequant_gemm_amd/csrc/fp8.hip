@@ -10,6 +10,7 @@
 #include "act_quant.h"
 #include "common.h"
 #include "dense.h"
+#include "few_rows.h"
 #include "launch.h"
 #include "tile.h"
 
@@ -335,8 +336,36 @@ hipError_t launch_quant_fp8(const uint16_t* x, bool xf16, int64_t M, int64_t K, 
   return hipGetLastError();
 }
 
-hipError_t launch_fp8(const Fp8Params& p, hipStream_t st) { return launch_fp8_tiles<false>(p, st); }
+namespace {
+FewParams few_params(const Fp8Params& p, bool gated) {
+  FewParams f{};
+  f.x = p.x ? static_cast<const void*>(p.x) : p.xq;
+  f.xs = p.xs;
+  f.w = p.w;
+  f.ws = p.ws;
+  f.bias = p.bias;
+  f.N = gated ? p.N / 2 : p.N;
+  f.K = p.K;
+  f.M = static_cast<int>(p.M);
+  f.y = p.y;
+  f.ydt = p.ydt;
+  f.gelu = p.gelu;
+  return f;
+}
+}  // namespace
 
-hipError_t launch_fp8_gated(const Fp8Params& p, hipStream_t st) { return launch_fp8_tiles<true>(p, st); }
+bool fp8_quantises(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
+
+hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st) {
+  if (p.M > kFewMaxM) return launch_fp8_tiles<false>(p, st);
+  const FewParams f = few_params(p, false);
+  return p.ydt == 0 ? launch_few<kFewFp8Exact, false>(f, p.x != nullptr, xf16, st)
+                    : launch_few<kFewFp8, false>(f, p.x != nullptr, xf16, st);
+}
+
+hipError_t launch_fp8_gated(const Fp8Params& p, bool xf16, hipStream_t st) {
+  if (p.M > kFewMaxM) return launch_fp8_tiles<true>(p, st);
+  return launch_few<kFewFp8, true>(few_params(p, true), p.x != nullptr, xf16, st);
+}
 
 }  // namespace cubic

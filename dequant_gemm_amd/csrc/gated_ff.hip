@@ -7,6 +7,7 @@
 
 #include "common.h"
 #include "dense.h"
+#include "few_rows.h"
 #include "launch.h"
 #include "tile.h"
 
@@ -343,6 +344,20 @@ unsigned quad_grid(int64_t M, int64_t I) {
 
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
   const int dt = p.f16 ? 2 : 1;
+  if (p.M <= kFewMaxM) {
+    FewParams f{};
+    f.x = p.x;
+    f.w = p.w;
+    f.N = p.I;
+    f.K = p.H;
+    f.M = static_cast<int>(p.M);
+    f.y = p.h;
+    f.ydt = dt;
+    f.gelu = p.gelu;
+    f.pre = p.pre;
+    const bool whole = p.M <= kFewWholeM && 2 * p.H <= kFewWholeBytes;
+    return p.f16 ? launch_few<kFewF16, true>(f, whole, false, st) : launch_few<kFewBf16, true>(f, whole, false, st);
+  }
   return launch_tile16<false, false, true>({p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, p.I, dt, p.pre, p.gelu}, p.f16, st);
 }
 

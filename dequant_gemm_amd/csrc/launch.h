@@ -216,6 +216,7 @@ hipError_t launch_w8a8(const W8Params& p, hipStream_t st);
 struct Fp8Params {
   const uint8_t* xq;       // e4m3 [M][K]
   const float* xs;         // [M][ceil(K / 128)]
+  const uint16_t* x;       // instead of both, where fp8_quantises: bf16 or fp16 [M][K]
   const uint8_t* w;        // e4m3 [N][K]
   const float* ws;         // [ceil(N / 128)][ceil(K / 128)]
   const float* bias;       // [N] or NULL
@@ -227,9 +228,10 @@ struct Fp8Params {
 // One scale per 128 channels of a row, or (blocks) per 128 x 128 values.
 hipError_t launch_quant_fp8(const uint16_t* x, bool xf16, int64_t M, int64_t K, bool blocks, uint8_t* xq, float* xs,
                             hipStream_t st);
-hipError_t launch_fp8(const Fp8Params& p, hipStream_t st);
+bool fp8_quantises(int64_t M, int64_t K);   // the product takes x itself
+hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st);
 // N = 2 I rows of w, gate rows first (I a multiple of 128): y [M][I] = act(gate) * up in bf16 or fp16
-hipError_t launch_fp8_gated(const Fp8Params& p, hipStream_t st);
+hipError_t launch_fp8_gated(const Fp8Params& p, bool xf16, hipStream_t st);
 
 // The gated feed-forward block over 16-bit weights (gated_ff.hip).
 struct FfParams {
