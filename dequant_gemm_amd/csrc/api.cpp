@@ -889,6 +889,7 @@ hipError_t fp8_stage(Fp8Params* p, const void* x, int x_dtype, char* ws, hipStre
     p->x = static_cast<const uint16_t*>(x);
     return hipSuccess;
   }
+  p->part = reinterpret_cast<float*>(ws + fp8_staging_bytes(p->M, p->K));
   uint8_t* xq = reinterpret_cast<uint8_t*>(ws);
   float* xs = reinterpret_cast<float*>(ws + fp8_codes_bytes(p->M, p->K));
   p->xq = xq;
@@ -910,8 +911,7 @@ CUBIC_API int cubic_quant_fp8(const void* x, int x_dtype, int64_t M, int64_t K, 
 }
 
 CUBIC_API size_t cubic_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M, (void)N, (void)K;
-  return 0;
+  return M <= 0 || N <= 0 || K <= 0 ? 0 : fp8_part_bytes(M, N, K);
 }
 
 CUBIC_API int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, const cubic_weight_fp8* w, const float* bias,
@@ -927,6 +927,7 @@ CUBIC_API int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M,
   Fp8Params p = fp8_params(w, M, bias, y, y_dtype);
   p.xq = xq;
   p.xs = x_scale;
+  p.part = static_cast<float*>(workspace);
   return hip_status(launch_fp8(p, false, static_cast<hipStream_t>(stream)));
 }
 
@@ -962,8 +963,7 @@ int check_ff(int64_t M, int64_t H, int64_t I, int dtype, int act) {
 }  // namespace
 
 CUBIC_API size_t cubic_gated_ff_workspace_bytes(int64_t M, int64_t H, int64_t I) {
-  (void)M, (void)H, (void)I;
-  return 0;
+  return M <= 0 || H <= 0 || I <= 0 ? 0 : gated_ff_part_bytes(M, H, I);
 }
 
 CUBIC_API int cubic_gated_ff(const void* x, const void* w, int dtype, int64_t M, int64_t H, int64_t I, int act, void* h, float* pre,
@@ -985,12 +985,13 @@ CUBIC_API int cubic_gated_ff(const void* x, const void* w, int dtype, int64_t M,
   p.gelu = act == CUBIC_ACT_GELU_TANH ? 1 : 0;
   p.h = static_cast<uint16_t*>(h);
   p.pre = pre;
+  p.part = static_cast<float*>(workspace);
   return hip_status(launch_gated_ff(p, static_cast<hipStream_t>(stream)));
 }
 
 CUBIC_API size_t cubic_gated_ff_backward_workspace_bytes(int64_t M, int64_t H, int64_t I) {
   if (M <= 0 || H <= 0 || I <= 0) return 0;
-  return align256(static_cast<size_t>(M) * I * 4);
+  return align256(static_cast<size_t>(M) * I * 4) + gated_ff_backward_part_bytes(M, H, I);
 }
 
 CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void* w, const float* pre, int dtype, int64_t M, int64_t H,
@@ -1018,6 +1019,7 @@ CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void*
   p.pre = const_cast<float*>(pre);
   p.dh = static_cast<const uint16_t*>(dh);
   p.dpre = static_cast<uint16_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(M) * I * 4));
   p.dx = static_cast<uint16_t*>(dx);
   p.dw = static_cast<uint16_t*>(dw);
   return hip_status(launch_gated_ff_backward(p, s));
@@ -1025,7 +1027,7 @@ CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void*
 
 CUBIC_API size_t cubic_gated_ff_fp8_workspace_bytes(int64_t M, int64_t H, int64_t I) {
   if (M <= 0 || H <= 0 || I <= 0) return 0;
-  return fp8_staging_bytes(M, H);
+  return fp8_staging_bytes(M, H) + cubic_gemm_fp8_workspace_bytes(M, 2 * I, H);
 }
 
 CUBIC_API int cubic_gated_ff_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* gate_up, int act, void* h, int h_dtype,

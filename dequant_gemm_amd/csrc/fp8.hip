@@ -118,11 +118,14 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t N = GATED ? p.N / 2 : p.N;     // columns of results
   int im, in;
-  tile_place(static_cast<int>(blockIdx.x), static_cast<int>((p.M + TM - 1) / TM), static_cast<int>((N + TC - 1) / TC), &im, &in);
+  const int tm = static_cast<int>((p.M + TM - 1) / TM), tn = static_cast<int>((N + TC - 1) / TC);
+  const int slice = static_cast<int>(blockIdx.x) / (tm * tn);
+  tile_place(static_cast<int>(blockIdx.x) - slice * tm * tn, tm, tn, &im, &in);
   const int64_t m0 = static_cast<int64_t>(im) * TM, n0 = static_cast<int64_t>(in) * TC;
   const uint32_t K = static_cast<uint32_t>(p.K);
   const int64_t kb = (p.K + 127) >> 7;
-  const int S = static_cast<int>(kb);
+  const int len = (static_cast<int>(kb) + p.slices - 1) / p.slices;
+  const int s0 = slice * len, S = min(static_cast<int>(kb) - s0, len);   // stages s0 .. s0 + S - 1
 
   // ---- stage loads: wave w takes rows 8 (W i + w) .. + 7 of A, then of B; lane l loads the
   // 16-byte piece l % 8 of row l / 8 into registers and writes it to slot piece ^ (row / 2 %
@@ -150,7 +153,7 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
   u32x4 gr[NL];
   float sr = 0.0f;
   auto load = [&](int s, int i) {              // piece i of stage s; past K and past the rows zeros
-    const uint32_t k = 128u * static_cast<uint32_t>(s);
+    const uint32_t k = 128u * static_cast<uint32_t>(s0 + s);
     const bool on = k + lane_k < K;
     if (i < LA) {
       gr[i] = tile_load(ars, on ? base + k + 8u * W * i * K : kPast);
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
   };
   auto load_scale = [&](int s) {
     const bool on = tid < TM && s < S;
-    sr = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(srs, on ? static_cast<int>(4u * (static_cast<uint32_t>(tid) * static_cast<uint32_t>(kb) + static_cast<uint32_t>(s))) : -1, 0, 0));
+    sr = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(srs, on ? static_cast<int>(4u * (static_cast<uint32_t>(tid) * static_cast<uint32_t>(kb) + static_cast<uint32_t>(s0 + s))) : -1, 0, 0));
   };
   auto store = [&](int s, int i) {
     unsigned char* st = smem + (s & 1) * kStage;
@@ -182,8 +185,8 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
   auto read_scale = [&](int s, int i) { return *reinterpret_cast<const float*>(smem + (s & 1) * kStage + kSOff + 4 * ((wm * MB + i) * 16 + c)); };
   // the wave's weight rows lie in one block of scales (gated: gate and up in one each)
   const int64_t nb = GATED ? n0 + 8 * NB * wn : n0 + 16 * NB * wn;
-  const float* ws0 = p.ws + (min(nb, N - 1) >> 7) * kb;
-  const float* ws1 = GATED ? p.ws + ((N + min(nb, N - 1)) >> 7) * kb : ws0;
+  const float* ws0 = p.ws + (min(nb, N - 1) >> 7) * kb + s0;
+  const float* ws1 = GATED ? p.ws + ((N + min(nb, N - 1)) >> 7) * kb + s0 : ws0;
 
   f32x4 acc[MB][NB] = {};
 #pragma unroll
@@ -259,6 +262,12 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
   }
 
   if constexpr (GATED) {
+    if (p.slices > 1) {
+      float* part = p.part + static_cast<int64_t>(slice) * p.M * p.N;
+      tile_write<16, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, part, 0, p.N, m0, p.M, n0, N, [&](int i, int j, int) { return acc[i][2 * j]; });
+      tile_write<16, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, part + N, 0, p.N, m0, p.M, n0, N, [&](int i, int j, int) { return acc[i][2 * j + 1]; });
+      return;
+    }
     tile_write<16, MB, NB / 2, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, N, m0, p.M, n0, N, [&](int i, int j, int) {
       f32x4 v;
 #pragma unroll
@@ -266,6 +275,11 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
       return v;
     });
   } else {
+    if (p.slices > 1) {
+      tile_write<16, MB, NB, WM, WN, 4, Shape::kLds>(smem, p.part + static_cast<int64_t>(slice) * p.M * N, 0, N, m0, p.M, n0, N,
+                                                     [&](int i, int j, int) { return acc[i][j]; });
+      return;
+    }
     auto value = [&](int i, int j, int) {
       f32x4 v = acc[i][j];
       if (p.bias) {
@@ -289,34 +303,38 @@ hipError_t launch_tile8(const Fp8Params& p, hipStream_t st) {
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
   if (e != hipSuccess) return e;
   const int64_t N = GATED ? p.N / 2 : p.N, TC = GATED ? Shape::TN / 2 : Shape::TN;
-  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((N + TC - 1) / TC);
+  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((N + TC - 1) / TC) * p.slices;
   if (tiles * 64 * Shape::W >= int64_t{1} << 32) return hipErrorInvalidValue;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(64 * Shape::W), Shape::kLds, st, p);
   return hipGetLastError();
 }
 
+// Slices are whole blocks of 128 codes.
+TilePlan plan8(int64_t M, int64_t N, int64_t K) { return plan_tiles(M, N, (K + 127) / 128, 2); }
+
 template <bool GATED>
-hipError_t launch_fp8_tiles(const Fp8Params& p, hipStream_t st) {
-  // fp32 results: a smaller tile, since the converted operands take registers
-  if (!GATED && p.ydt == 0) return launch_tile8<Tile8<4, 4, 2, 2>, true, false>(p, st);
-  const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256, N = GATED ? p.N / 2 : p.N;
-  static constexpr int kTiles[][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 128}, {64, 64}};
-  int best = 0;
-  int64_t cost = INT64_MAX;
-  for (int k = 0; k < 5; ++k) {
-    const int tm = kTiles[k][0], tn = kTiles[k][1], tc = GATED ? tn / 2 : tn;
-    const int64_t tiles = ((p.M + tm - 1) / tm) * ((N + tc - 1) / tc);
-    const int64_t per = std::max(tm * tn / 64, tm + tn) + 64;   // a stage's MFMA or LDS-fill cycles, and its barrier
-    const int64_t c = (tiles + cu - 1) / cu * per;
-    if (c < cost) { cost = c; best = k; }
+hipError_t launch_fp8_tiles(Fp8Params p, hipStream_t st) {
+  const TilePlan plan = plan8(p.M, p.N, p.K);
+  p.slices = plan.slices;
+  hipError_t e;
+  if (!GATED && p.ydt == 0) {
+    // fp32 results: smaller tiles for the largest shapes, since the converted operands take registers
+    switch (plan.shape) {
+      case 0: case 1: case 2: e = launch_tile8<Tile8<4, 4, 2, 2>, true, false>(p, st); break;
+      case 3: e = launch_tile8<Tile8<2, 4, 2, 2>, true, false>(p, st); break;
+      default: e = launch_tile8<Tile8<2, 2, 2, 2>, true, false>(p, st); break;
+    }
+  } else {
+    switch (plan.shape) {
+      case 0: e = launch_tile8<Tile8<4, 8, 4, 2>, false, GATED>(p, st); break;
+      case 1: e = launch_tile8<Tile8<4, 4, 4, 2>, false, GATED>(p, st); break;
+      case 2: e = launch_tile8<Tile8<4, 4, 2, 2>, false, GATED>(p, st); break;
+      case 3: e = launch_tile8<Tile8<2, 4, 2, 2>, false, GATED>(p, st); break;
+      default: e = launch_tile8<Tile8<2, 2, 2, 2>, false, GATED>(p, st); break;
+    }
   }
-  switch (best) {
-    case 0: return launch_tile8<Tile8<4, 8, 4, 2>, false, GATED>(p, st);
-    case 1: return launch_tile8<Tile8<4, 4, 4, 2>, false, GATED>(p, st);
-    case 2: return launch_tile8<Tile8<4, 4, 2, 2>, false, GATED>(p, st);
-    case 3: return launch_tile8<Tile8<2, 4, 2, 2>, false, GATED>(p, st);
-    default: return launch_tile8<Tile8<2, 2, 2, 2>, false, GATED>(p, st);
-  }
+  if (e != hipSuccess || plan.slices == 1) return e;
+  return launch_tile_join<GATED>({p.part, plan.slices, p.M, GATED ? p.N / 2 : p.N, p.N, p.bias, p.y, p.ydt, p.gelu, nullptr}, st);
 }
 
 }  // namespace
@@ -353,6 +371,8 @@ FewParams few_params(const Fp8Params& p, bool gated) {
   return f;
 }
 }  // namespace
+
+size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewMaxM ? 0 : plan_bytes(plan8(M, N, K), M, N); }
 
 bool fp8_quantises(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
 

@@ -21,13 +21,16 @@ struct TileParams {
   const uint16_t *a, *b;
   int64_t lda, ldb;
   int64_t M, N, K;
-  void* y;                 // [M][ldy], 16 bits, or fp32 when ydt is 0
-  int64_t ldy;
+  void* y;                 // [M][N] in bf16 (ydt 1) or fp16 (2)
   int ydt;
   // gated form: b holds N gate rows and N up rows behind them; y gets act(gate) * up and,
   // where it is given, pre [M][2 N] both
   float* pre;
   int gelu;
+  // slices of the contraction, and where their sums go if there are several: fp32
+  // [slices][M][N], gated [slices][M][2 N]
+  int slices;
+  float* part;
 };
 
 // A tile's shape: WM x WN waves with MB x NB blocks of 32 x 32 each.
@@ -138,7 +141,9 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   constexpr int kStage = Shape::kStage, kBOff = TM * 64;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   int im, in;
-  tile_place(static_cast<int>(blockIdx.x), static_cast<int>((p.M + TM - 1) / TM), static_cast<int>((p.N + TC - 1) / TC), &im, &in);
+  const int tm = static_cast<int>((p.M + TM - 1) / TM), tn = static_cast<int>((p.N + TC - 1) / TC);
+  const int slice = static_cast<int>(blockIdx.x) / (tm * tn);
+  tile_place(static_cast<int>(blockIdx.x) - slice * tm * tn, tm, tn, &im, &in);
   const int64_t m0 = static_cast<int64_t>(im) * TM, n0 = static_cast<int64_t>(in) * TC;
 
   Operand<AT, TM, W> A;
@@ -158,17 +163,19 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
       gated_off[g] = static_cast<uint32_t>(32 * (blk >> 1) + 16 * (piece & 1) + (lane >> 2)) * static_cast<uint32_t>(2 * p.ldb) + B.lane_k;
     }
   }
-  const int S = static_cast<int>((p.K + 31) >> 5);
+  const int all = static_cast<int>((p.K + 31) >> 5), len = (all + p.slices - 1) / p.slices;
+  const int s0 = slice * len, S = min(all - s0, len);   // stages s0 .. s0 + S - 1
   u32x4 gr[2][NL];                             // pieces on their way: stages of either parity
   auto load = [&](auto set_c, int s, int i) {
     constexpr int set = decltype(set_c)::value;
     if (i < LA) {
-      gr[set][i] = A.load(s, i);
+      gr[set][i] = A.load(s0 + s, i);
     } else if constexpr (GATED) {
-      const bool on = B.inside(i - LA, wave) && 64u * static_cast<uint32_t>(s) + B.lane_k < 2u * static_cast<uint32_t>(B.K);
-      gr[set][i] = tile_load(gated_rs[i - LA], on ? gated_off[i - LA] + 64u * s : kPast);
+      const uint32_t k = 64u * static_cast<uint32_t>(s0 + s);
+      const bool on = B.inside(i - LA, wave) && k + B.lane_k < 2u * static_cast<uint32_t>(B.K);
+      gr[set][i] = tile_load(gated_rs[i - LA], on ? gated_off[i - LA] + k : kPast);
     } else {
-      gr[set][i] = B.load(s, i - LA);
+      gr[set][i] = B.load(s0 + s, i - LA);
     }
   };
   auto store = [&](auto set_c, int s, int i) {
@@ -253,23 +260,25 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   }
   if (s < S) stage(s, I1{}, I0{});
 
+  auto quad = [&](int i, int j, int g) { return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]}; };
   if constexpr (GATED) {
-    auto quad = [&](int i, int j, int g) { return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]}; };
-    if (p.pre) {
-      tile_write<32, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j, g); });
-      tile_write<32, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, p.pre + p.N, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j + 1, g); });
+    float* pre = p.slices > 1 ? p.part + static_cast<int64_t>(slice) * p.M * 2 * p.N : p.pre;
+    if (pre) {
+      tile_write<32, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, pre, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j, g); });
+      tile_write<32, MB, NB / 2, WM, WN, 4, Shape::kLds>(smem, pre + p.N, 0, 2 * p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) { return quad(i, 2 * j + 1, g); });
     }
-    tile_write<32, MB, NB / 2, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
+    if (p.slices > 1) return;
+    tile_write<32, MB, NB / 2, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.N, m0, p.M, n0, p.N, [&](int i, int j, int g) {
       const f32x4 a = quad(i, 2 * j, g), u = quad(i, 2 * j + 1, g);
       f32x4 v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = act_of(a[e], p.gelu).value * u[e];
       return v;
     });
+  } else if (p.slices > 1) {
+    tile_write<32, MB, NB, WM, WN, 4, Shape::kLds>(smem, p.part + static_cast<int64_t>(slice) * p.M * p.N, 0, p.N, m0, p.M, n0, p.N, quad);
   } else {
-    tile_write<32, MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.ldy, m0, p.M, n0, p.N, [&](int i, int j, int g) {
-      return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-    });
+    tile_write<32, MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.N, m0, p.M, n0, p.N, quad);
   }
 }
 
@@ -279,36 +288,35 @@ hipError_t launch_shape(const TileParams& p, hipStream_t st) {
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
   if (e != hipSuccess) return e;
   constexpr int TC = GATED ? Shape::TN / 2 : Shape::TN;
-  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + TC - 1) / TC);
+  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + TC - 1) / TC) * p.slices;
   if (tiles * 64 * Shape::W >= int64_t{1} << 32) return hipErrorInvalidValue;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(64 * Shape::W), Shape::kLds, st, p);
   return hipGetLastError();
 }
 
+TilePlan plan16(int64_t M, int64_t width, int64_t K) { return plan_tiles(M, width, (K + 31) / 32, 1); }
+
+// part: scratch of plan_bytes (several slices)
 template <bool AT, bool BT, bool GATED>
-hipError_t launch_tile16(const TileParams& p, bool f16, hipStream_t st) {
-  const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256;
-  static constexpr int kTiles[][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 128}, {64, 64}};
-  int best = 0;
-  int64_t cost = INT64_MAX;
-  for (int k = 0; k < 5; ++k) {
-    const int tm = kTiles[k][0], tn = kTiles[k][1], tc = GATED ? tn / 2 : tn;
-    const int64_t tiles = ((p.M + tm - 1) / tm) * ((p.N + tc - 1) / tc);
-    const int64_t per = std::max(tm * tn / 64, tm + tn) + 64;   // a stage's MFMA or LDS-fill cycles, and its barrier
-    const int64_t c = (tiles + cu - 1) / cu * per;
-    if (c < cost) { cost = c; best = k; }
-  }
+hipError_t launch_tile16(TileParams p, bool f16, float* part, hipStream_t st) {
+  const int64_t width = GATED ? 2 * p.N : p.N;
+  const TilePlan plan = plan16(p.M, width, p.K);
+  p.slices = plan.slices;
+  p.part = part;
   auto go = [&](auto shape) {
     using Shape = decltype(shape);
     return f16 ? launch_shape<Shape, true, AT, BT, GATED>(p, st) : launch_shape<Shape, false, AT, BT, GATED>(p, st);
   };
-  switch (best) {
-    case 0: return go(Tile16<2, 4, 4, 2>{});
-    case 1: return go(Tile16<2, 2, 4, 2>{});
-    case 2: return go(Tile16<2, 2, 2, 2>{});
-    case 3: return go(Tile16<1, 2, 2, 2>{});
-    default: return go(Tile16<1, 2, 2, 1>{});
+  hipError_t e;
+  switch (plan.shape) {
+    case 0: e = go(Tile16<2, 4, 4, 2>{}); break;
+    case 1: e = go(Tile16<2, 2, 4, 2>{}); break;
+    case 2: e = go(Tile16<2, 2, 2, 2>{}); break;
+    case 3: e = go(Tile16<1, 2, 2, 2>{}); break;
+    default: e = go(Tile16<1, 2, 2, 1>{}); break;
   }
+  if (e != hipSuccess || plan.slices == 1) return e;
+  return launch_tile_join<GATED>({part, plan.slices, p.M, p.N, width, nullptr, p.y, p.ydt, p.gelu, p.pre}, st);
 }
 
 // [dg | du] from pre and dh, in the operands' type: the products that follow take 16-bit
@@ -342,6 +350,15 @@ unsigned quad_grid(int64_t M, int64_t I) {
 
 }  // namespace
 
+size_t gated_ff_part_bytes(int64_t M, int64_t H, int64_t I) {
+  return M <= kFewMaxM ? 0 : plan_bytes(plan16(M, 2 * I, H), M, 2 * I);
+}
+
+// dx and dw run one after the other and share the scratch
+size_t gated_ff_backward_part_bytes(int64_t M, int64_t H, int64_t I) {
+  return std::max(plan_bytes(plan16(M, H, 2 * I), M, H), plan_bytes(plan16(2 * I, H, M), 2 * I, H));
+}
+
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
   const int dt = p.f16 ? 2 : 1;
   if (p.M <= kFewMaxM) {
@@ -358,7 +375,7 @@ hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
     const bool whole = p.M <= kFewWholeM && 2 * p.H <= kFewWholeBytes;
     return p.f16 ? launch_few<kFewF16, true>(f, whole, false, st) : launch_few<kFewBf16, true>(f, whole, false, st);
   }
-  return launch_tile16<false, false, true>({p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, p.I, dt, p.pre, p.gelu}, p.f16, st);
+  return launch_tile16<false, false, true>({p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, dt, p.pre, p.gelu, 1, nullptr}, p.f16, p.part, st);
 }
 
 hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
@@ -372,10 +389,10 @@ hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   const int dt = p.f16 ? 2 : 1;
   if (p.dx) {
-    e = launch_tile16<false, true, false>({p.dpre, p.w, 2 * p.I, p.H, p.M, p.H, 2 * p.I, p.dx, p.H, dt, nullptr, 0}, p.f16, st);
+    e = launch_tile16<false, true, false>({p.dpre, p.w, 2 * p.I, p.H, p.M, p.H, 2 * p.I, p.dx, dt, nullptr, 0, 1, nullptr}, p.f16, p.part, st);
     if (e != hipSuccess) return e;
   }
-  if (p.dw) e = launch_tile16<true, true, false>({p.dpre, p.x, 2 * p.I, p.H, 2 * p.I, p.H, p.M, p.dw, p.H, dt, nullptr, 0}, p.f16, st);
+  if (p.dw) e = launch_tile16<true, true, false>({p.dpre, p.x, 2 * p.I, p.H, 2 * p.I, p.H, p.M, p.dw, dt, nullptr, 0, 1, nullptr}, p.f16, p.part, st);
   return e;
 }
 

@@ -224,7 +224,10 @@ struct Fp8Params {
   void* y;                 // [M][N]
   int ydt;
   int gelu;                // launch_fp8_gated
+  float* part;             // scratch of fp8_part_bytes
+  int slices;              // (the launcher sets it)
 };
+size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K);
 // One scale per 128 channels of a row, or (blocks) per 128 x 128 values.
 hipError_t launch_quant_fp8(const uint16_t* x, bool xf16, int64_t M, int64_t K, bool blocks, uint8_t* xq, float* xs,
                             hipStream_t st);
@@ -245,7 +248,10 @@ struct FfParams {
   uint16_t* dpre;          // [M][2 I]: their gradients
   uint16_t* dx;            // [M][H] or NULL
   uint16_t* dw;            // [2 I][H] or NULL
+  float* part;             // scratch of gated_ff_part_bytes or gated_ff_backward_part_bytes
 };
+size_t gated_ff_part_bytes(int64_t M, int64_t H, int64_t I);
+size_t gated_ff_backward_part_bytes(int64_t M, int64_t H, int64_t I);
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st);
 hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st);
 

@@ -1,8 +1,11 @@
 // tile.h -- what the dense tile kernels (gated_ff.hip, fp8.hip) share: buffer loads, the
 // order of tiles over the compute units, and the way of a tile's results through LDS.
 #pragma once
+#include <algorithm>
+
 #include "common.h"
 #include "dense.h"
+#include "launch.h"
 
 namespace cubic {
 
@@ -112,6 +115,110 @@ __device__ __forceinline__ void tile_write(unsigned char* smem, void* y, int ydt
     }
   }
   __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// Tiles and slices. A product with few tiles splits its contraction into slices, whose fp32
+// sums pass through the workspace ([slice][M][width]) and are added up in their order.
+struct TilePlan {
+  int shape, slices;       // of kTileShapes
+};
+constexpr int kTileShapes[][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 128}, {64, 64}};
+constexpr int kMaxSlices = 32;
+
+// The plan of least time for M rows, `width` columns of operand B and `stages` steps of the
+// contraction of 64 `unit` bytes, by a simple model in cycles: rounds of workgroups over the
+// compute units, each its stages (the larger of MFMA and LDS-fill cycles, and a barrier) and
+// its start and end; slices cost the join's launch and their bytes. No slice is empty.
+inline TilePlan plan_tiles(int64_t M, int64_t width, int64_t stages, int64_t unit) {
+  const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256;
+  TilePlan best{0, 1};
+  int64_t cost = INT64_MAX;
+  for (int k = 0; k < 5; ++k) {
+    const int64_t tm = kTileShapes[k][0], tn = kTileShapes[k][1];
+    const int64_t tiles = ((M + tm - 1) / tm) * ((width + tn - 1) / tn);
+    const int64_t per = std::max(tm * tn / 64, tm + tn) * unit + 64;
+    for (int s = 1; s <= kMaxSlices; ++s) {
+      if (s > 1 && (stages * unit < 4 * s || tiles * s > 2 * cu)) break;
+      const int64_t len = (stages + s - 1) / s;
+      if (len * (s - 1) >= stages) continue;
+      const int64_t rounds = (tiles * s + cu - 1) / cu;
+      int64_t c = rounds * (len * per + 3000);
+      if (s > 1) c += 5000 + M * width * 8 * s / 1700;
+      if (c < cost) {
+        cost = c;
+        best = {k, s};
+      }
+    }
+  }
+  return best;
+}
+inline size_t plan_bytes(const TilePlan& t, int64_t M, int64_t width) {
+  return t.slices > 1 ? (static_cast<size_t>(t.slices) * M * width * 4 + 255) / 256 * 256 : 0;
+}
+
+// What follows the slices: y = their sum (+ bias) in its type, or gated y = act(gate) * up of
+// the sum's halves, which pre receives where it is given.
+struct JoinParams {
+  const float* part;       // [slices][M][width]
+  int slices;
+  int64_t M, N, width;     // width N, gated 2 N
+  const float* bias;
+  void* y;
+  int ydt, gelu;
+  float* pre;
+};
+template <bool GATED, int V>                   // V neighbouring columns a thread
+__global__ __launch_bounds__(256) void k_tile_join(JoinParams p) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256, per = p.N / V, all = p.M * per, slice = p.M * p.width;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < all; at += step) {
+    const int64_t m = at / per, n = V * (at - m * per);
+    auto sum = [&](int64_t col, float* v) {
+      const float* q = p.part + m * p.width + col;
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = 0.0f;
+      for (int s = 0; s < p.slices; ++s, q += slice) {
+        if constexpr (V == 4) {
+          const f32x4 t = *reinterpret_cast<const f32x4*>(q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += t[e];
+        } else {
+          v[0] += *q;
+        }
+      }
+    };
+    float v[V];
+    sum(n, v);
+    if constexpr (GATED) {
+      float u[V];
+      sum(p.N + n, u);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (p.pre) {
+          p.pre[m * p.width + n + e] = v[e];
+          p.pre[m * p.width + p.N + n + e] = u[e];
+        }
+        v[e] = act_of(v[e], p.gelu).value * u[e];
+      }
+    } else if (p.bias) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] += p.bias[n + e];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) store_as(p.y, p.ydt, m * p.N + n + e, v[e]);
+  }
+}
+template <bool GATED>
+hipError_t launch_tile_join(const JoinParams& p, hipStream_t st) {
+  const bool quads = p.N % 4 == 0;
+  const int64_t items = p.M * (quads ? p.N / 4 : p.N);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, 4096));
+  if (quads) {
+    hipLaunchKernelGGL((k_tile_join<GATED, 4>), dim3(grid), dim3(256), 0, st, p);
+  } else {
+    hipLaunchKernelGGL((k_tile_join<GATED, 1>), dim3(grid), dim3(256), 0, st, p);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace cubic
