@@ -103,7 +103,7 @@ __device__ __forceinline__ f32x4 fp8_dot(const i32x8& a, const i32x8& b) {
           e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(a[2 * s]), static_cast<uint32_t>(a[2 * s + 1])}),
           e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(b[2 * s]), static_cast<uint32_t>(b[2 * s + 1])}), part, 0, 0, 0);
   } else {
-    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part, 0, 0, 0, 127, 0, 127);   // scales 2^0
+    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part, 0, 0, 0, 0, 0, 0);   // the form without scales
   }
   return part;
 }

@@ -38,14 +38,15 @@ template <int MB_, int NB_, int WM_, int WN_>
 struct Tile16 {
   static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN;
   static constexpr int TM = 32 * MB * WM, TN = 32 * NB * WN;
-  static constexpr int kStage = 64 * (TM + TN);                  // 32 k of every row
-  // 1024-byte pieces of a stage per wave (the last ones may be past the tile)
-  static constexpr int LA = (TM / 16 + W - 1) / W, LB = (TN / 16 + W - 1) / W, NL = LA + LB;
+  static constexpr int kStage = 128 * (TM + TN);                 // 64 k of every row
+  // 1024-byte pieces of a stage per wave
+  static constexpr int LA = TM / 8 / W, LB = TN / 8 / W, NL = LA + LB;
+  static_assert(LA * 8 * W == TM && LB * 8 * W == TN, "whole pieces");
   static constexpr int kLds = W == 8 ? 148 * 1024 : (2 * kStage > 64 * 1024 ? 2 * kStage : 64 * 1024);
   static_assert(2 * kStage <= kLds && kLds <= 160 * 1024, "one compute unit's LDS");
 };
 
-// One operand's stages: rows of 64 bytes (32 k), or with T 32 rows (one k each) of 2 ROWS bytes.
+// One operand's stages: rows of 128 bytes (64 k), or with T 64 rows (one k each) of 2 ROWS bytes.
 template <bool T, int ROWS, int W>
 struct Operand {
   static constexpr int kPieces = ROWS / 8;     // T: 16-byte pieces of a k row
@@ -54,14 +55,13 @@ struct Operand {
   int64_t ld;
   uint32_t bytes;                              // that the resource covers
   uint32_t lane_off, step, lane_k, slot;
-  int K, wave;
+  int K;
   bool on_col;
 
-  __device__ __forceinline__ void init(const uint16_t* base, int64_t ld_, int64_t row0, int64_t rows, int64_t K_, int wave_) {
+  __device__ __forceinline__ void init(const uint16_t* base, int64_t ld_, int64_t row0, int64_t rows, int64_t K_, int wave) {
     const int lane = threadIdx.x & 63;
     ld = ld_;
     K = static_cast<int>(K_);
-    wave = wave_;
     if constexpr (T) {
       p = base + row0;
       const int kk = kPer * wave + lane / kPieces, piece = lane % kPieces;
@@ -69,16 +69,17 @@ struct Operand {
       lane_off = static_cast<uint32_t>(kk) * static_cast<uint32_t>(2 * ld) + 16u * piece;
       step = static_cast<uint32_t>(kPer * W) * static_cast<uint32_t>(2 * ld);
       on_col = 8 * piece < rows - row0;        // rows a multiple of 8
-      bytes = 32u * static_cast<uint32_t>(2 * ld);
+      bytes = 64u * static_cast<uint32_t>(2 * ld);
       slot = static_cast<uint32_t>(kk) * (2 * ROWS) + (((piece >> 2) ^ swizzle(kk)) << 6) + 16 * (piece & 3);
     } else {
       p = base + row0 * ld;
-      lane_k = 16u * (lane & 3);
-      lane_off = static_cast<uint32_t>(16 * wave + (lane >> 2)) * static_cast<uint32_t>(2 * ld) + lane_k;
-      step = 16u * W * static_cast<uint32_t>(2 * ld);
+      lane_k = 16u * (lane & 7);
+      lane_off = static_cast<uint32_t>(8 * wave + (lane >> 3)) * static_cast<uint32_t>(2 * ld) + lane_k;
+      step = 8u * W * static_cast<uint32_t>(2 * ld);
       on_col = true;
       bytes = static_cast<uint32_t>(min(static_cast<int64_t>(ROWS), rows - row0)) * static_cast<uint32_t>(2 * ld);
-      slot = 1024u * wave + 64u * (lane >> 2) + 16u * ((lane & 3) ^ ((lane >> 4) & 3));
+      // piece ^ (row / 2 % 8): any 16 rows read at one piece hit all banks
+      slot = 1024u * wave + 128u * (lane >> 3) + 16u * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
     }
   }
   // T: the 64-byte segment of a k row is XORed with this, so that four k rows read at one
@@ -87,19 +88,18 @@ struct Operand {
     constexpr int nseg = ROWS / 32;            // segments of a row
     return nseg >= 4 ? (kk & 3) : nseg == 2 ? ((kk >> 1) & 1) : 0;
   }
-  static constexpr bool inside(int g, int wave) { return 16 * (W * g + wave) < ROWS; }
   // piece g of stage s; past K and past the tile zeros
   __device__ __forceinline__ u32x4 load(int s, int g) const {
     if constexpr (T) {
-      const bool on = on_col && inside(g, wave) && 32 * s + static_cast<int>(lane_k) + kPer * W * g < K;
-      return tile_load(tile_rsrc(p + static_cast<int64_t>(s) * 32 * ld, bytes), on ? lane_off + step * g : kPast);
+      const bool on = on_col && 64 * s + static_cast<int>(lane_k) + kPer * W * g < K;
+      return tile_load(tile_rsrc(p + static_cast<int64_t>(s) * 64 * ld, bytes), on ? lane_off + step * g : kPast);
     } else {
-      const bool on = inside(g, wave) && 64u * static_cast<uint32_t>(s) + lane_k < 2u * static_cast<uint32_t>(K);
-      return tile_load(tile_rsrc(p, bytes), on ? lane_off + 64u * s + step * g : kPast);
+      const bool on = 128u * static_cast<uint32_t>(s) + lane_k < 2u * static_cast<uint32_t>(K);
+      return tile_load(tile_rsrc(p, bytes), on ? lane_off + 128u * s + step * g : kPast);
     }
   }
   __device__ __forceinline__ void store(unsigned char* st, int g, const u32x4& v) const {
-    if (inside(g, wave)) *reinterpret_cast<u32x4*>(st + slot + 1024 * W * g) = v;
+    *reinterpret_cast<u32x4*>(st + slot + 1024 * W * g) = v;
   }
 };
 
@@ -119,7 +119,7 @@ __device__ __forceinline__ s16x8 fragment(const unsigned char* st, int blk, int 
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
     const int c = lane & 31, h = lane >> 5;
-    return *reinterpret_cast<const s16x8*>(st + (32 * blk + c) * 64 + (((2 * ks + h) ^ ((c >> 2) & 3)) << 4));
+    return *reinterpret_cast<const s16x8*>(st + (32 * blk + c) * 128 + (((2 * ks + h) ^ ((c >> 1) & 7)) << 4));
   }
 }
 
@@ -137,8 +137,7 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
   constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL;
-  constexpr int kLoads1 = (NL + 1) / 2;        // pieces of a stage that move in the half step after the barrier
-  constexpr int kStage = Shape::kStage, kBOff = TM * 64;
+  constexpr int kStage = Shape::kStage, kBOff = TM * 128;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   int im, in;
   const int tm = static_cast<int>((p.M + TM - 1) / TM), tn = static_cast<int>((p.N + TC - 1) / TC);
@@ -158,33 +157,30 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
     const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(TC), p.N - n0)) * static_cast<uint32_t>(2 * p.ldb);
 #pragma unroll
     for (int g = 0; g < LB; ++g) {
-      const int piece = W * g + wave, blk = piece >> 1;
+      const int row = 8 * (W * g + wave), blk = row >> 5;
       gated_rs[g] = tile_rsrc(p.b + ((blk & 1) * p.N + n0) * p.ldb, bytes);
-      gated_off[g] = static_cast<uint32_t>(32 * (blk >> 1) + 16 * (piece & 1) + (lane >> 2)) * static_cast<uint32_t>(2 * p.ldb) + B.lane_k;
+      gated_off[g] = static_cast<uint32_t>(32 * (blk >> 1) + (row & 31) + (lane >> 3)) * static_cast<uint32_t>(2 * p.ldb) + B.lane_k;
     }
   }
-  const int all = static_cast<int>((p.K + 31) >> 5), len = (all + p.slices - 1) / p.slices;
+  const int all = static_cast<int>((p.K + 63) >> 6), len = (all + p.slices - 1) / p.slices;
   const int s0 = slice * len, S = min(all - s0, len);   // stages s0 .. s0 + S - 1
-  u32x4 gr[2][NL];                             // pieces on their way: stages of either parity
-  auto load = [&](auto set_c, int s, int i) {
-    constexpr int set = decltype(set_c)::value;
+  u32x4 gr[NL];                                // a stage's pieces on their way
+  auto load = [&](int s, int i) {
     if (i < LA) {
-      gr[set][i] = A.load(s0 + s, i);
+      gr[i] = A.load(s0 + s, i);
     } else if constexpr (GATED) {
-      const uint32_t k = 64u * static_cast<uint32_t>(s0 + s);
-      const bool on = B.inside(i - LA, wave) && k + B.lane_k < 2u * static_cast<uint32_t>(B.K);
-      gr[set][i] = tile_load(gated_rs[i - LA], on ? gated_off[i - LA] + k : kPast);
+      const uint32_t k = 128u * static_cast<uint32_t>(s0 + s);
+      gr[i] = tile_load(gated_rs[i - LA], k + B.lane_k < 2u * static_cast<uint32_t>(B.K) ? gated_off[i - LA] + k : kPast);
     } else {
-      gr[set][i] = B.load(s0 + s, i - LA);
+      gr[i] = B.load(s0 + s, i - LA);
     }
   };
-  auto store = [&](auto set_c, int s, int i) {
-    constexpr int set = decltype(set_c)::value;
+  auto store = [&](int s, int i) {
     unsigned char* st = smem + (s & 1) * kStage;
     if (i < LA) {
-      A.store(st, i, gr[set][i]);
+      A.store(st, i, gr[i]);
     } else {
-      B.store(st + kBOff, i - LA, gr[set][i]);
+      B.store(st + kBOff, i - LA, gr[i]);
     }
   };
   const int wm = wave / WN, wn = wave % WN;
@@ -192,73 +188,53 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   auto read_b = [&](int s, int ks, int j) { return fragment<BT, TN>(smem + (s & 1) * kStage + kBOff, wn * NB + j, ks); };
 
   f32x16 acc[MB][NB] = {};
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using IL = std::integral_constant<int, kLoads1>;
-  using IN = std::integral_constant<int, NL>;
 #pragma unroll
-  for (int i = 0; i < NL; ++i) load(I0{}, 0, i);
-#pragma unroll
-  for (int i = 0; i < NL; ++i) load(I1{}, 1, i);
+  for (int i = 0; i < NL; ++i) load(0, i);
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    store(I0{}, 0, i);
-    load(I0{}, 2, i);
+    store(0, i);
+    load(1, i);
   }
   tile_barrier();
-#pragma unroll
-  for (int i = 0; i < kLoads1; ++i) {
-    store(I1{}, 1, i);
-    load(I1{}, 3, i);
-  }
   s16x8 fa[2][MB], fb[2][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
 #pragma unroll
   for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
 
-  // One half step: the MFMAs of fragments f (B times A, so that a lane's results are
-  // neighbouring columns of one row). Spread between them: the reads of the other half's
-  // fragments, and for pieces l0 .. l1 - 1 of stage s_st the write to LDS and the load of
-  // the piece two stages later into its registers.
-  auto half = [&](auto f_c, int s_read, int ks, auto set_c, int s_st, auto l0_c, auto l1_c) {
-    constexpr int f = decltype(f_c)::value, l0 = decltype(l0_c)::value, l1 = decltype(l1_c)::value;
-    constexpr int Q = MB * NB;
+  // A stage is four steps of 16 k: the MFMAs of one step's fragments (B times A, so that a
+  // lane's results are neighbouring columns of one row), spread between them the reads of
+  // the next step's. In the first three steps the next stage goes from its registers into
+  // LDS, each piece followed by the load of the piece one stage on; then every wave has
+  // read this stage and written the next, and after the barrier the next one is read.
+  constexpr int Q = MB * NB, kOver = 3 * Q;
+  for (int s = 0; s < S; ++s) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
-      acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
+    for (int ks = 0; ks < 4; ++ks) {
+      const int f = ks & 1;
+      if (ks == 3) tile_barrier();
 #pragma unroll
-      for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
-        if (r < MB) {
-          fa[1 - f][r] = read_a(s_read, ks, r);
-        } else {
-          fb[1 - f][r - MB] = read_b(s_read, ks, r - MB);
+      for (int q = 0; q < Q; ++q) {
+        const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB, t = ks * Q + q;
+        acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
+#pragma unroll
+        for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
+          const int sr = ks == 3 ? s + 1 : s, kr = (ks + 1) & 3;
+          if (r < MB) {
+            fa[1 - f][r] = read_a(sr, kr, r);
+          } else {
+            fb[1 - f][r - MB] = read_b(sr, kr, r - MB);
+          }
         }
-      }
 #pragma unroll
-      for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) {
-        store(set_c, s_st, r);
-        load(set_c, s_st + 2, r);
+        for (int r = t * NL / kOver; r < (t + 1) * NL / kOver && r < NL; ++r) {
+          store(s + 1, r);
+          load(s + 2, r);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-  };
-  // Stage s: its second half's fragments are read beside the first half's MFMAs; then
-  // stage s + 1 is whole in LDS (its last pieces were written there) and every wave is
-  // done with stage s, so that after the barrier stage s + 1 is read and stage s + 2
-  // takes the place of s.
-  auto stage = [&](int s, auto next_c, auto after_c) {
-    half(I0{}, s, 1, next_c, s + 1, IL{}, IN{});
-    tile_barrier();
-    half(I1{}, s + 1, 0, after_c, s + 2, I0{}, IL{});
-  };
-  int s = 0;
-  for (; s + 1 < S; s += 2) {
-    stage(s, I1{}, I0{});
-    stage(s + 1, I0{}, I1{});
   }
-  if (s < S) stage(s, I1{}, I0{});
 
   auto quad = [&](int i, int j, int g) { return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]}; };
   if constexpr (GATED) {
@@ -294,7 +270,7 @@ hipError_t launch_shape(const TileParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-TilePlan plan16(int64_t M, int64_t width, int64_t K) { return plan_tiles(M, width, (K + 31) / 32, 1); }
+TilePlan plan16(int64_t M, int64_t width, int64_t K) { return plan_tiles(M, width, (K + 63) / 64, 2); }
 
 // part: scratch of plan_bytes (several slices)
 template <bool AT, bool BT, bool GATED>
