@@ -47,6 +47,8 @@ struct Tile16 {
 };
 
 // One operand's stages: rows of 128 bytes (64 k), or with T 64 rows (one k each) of 2 ROWS bytes.
+// A piece of 1024 bytes is a wave's load: eight rows of 128 bytes, or with T some k rows; in
+// LDS its 16-byte parts lie in the lanes' order, and lanes load the part that belongs there.
 template <bool T, int ROWS, int W>
 struct Operand {
   static constexpr int kPieces = ROWS / 8;     // T: 16-byte pieces of a k row
@@ -54,7 +56,7 @@ struct Operand {
   const uint16_t* p;                           // first row, or with T first column
   int64_t ld;
   uint32_t bytes;                              // that the resource covers
-  uint32_t lane_off, step, lane_k, slot;
+  uint32_t lane_off, step, lane_k, place;
   int K;
   bool on_col;
 
@@ -64,23 +66,23 @@ struct Operand {
     K = static_cast<int>(K_);
     if constexpr (T) {
       p = base + row0;
-      const int kk = kPer * wave + lane / kPieces, piece = lane % kPieces;
+      const int kk = kPer * wave + lane / kPieces, at = lane % kPieces;
+      const int piece = ((at >> 2) ^ swizzle(kk)) * 4 + (at & 3);
       lane_k = static_cast<uint32_t>(kk);
       lane_off = static_cast<uint32_t>(kk) * static_cast<uint32_t>(2 * ld) + 16u * piece;
       step = static_cast<uint32_t>(kPer * W) * static_cast<uint32_t>(2 * ld);
       on_col = 8 * piece < rows - row0;        // rows a multiple of 8
       bytes = 64u * static_cast<uint32_t>(2 * ld);
-      slot = static_cast<uint32_t>(kk) * (2 * ROWS) + (((piece >> 2) ^ swizzle(kk)) << 6) + 16 * (piece & 3);
     } else {
       p = base + row0 * ld;
-      lane_k = 16u * (lane & 7);
+      // piece ^ (row / 2 % 8): any 16 rows read at one piece hit all banks
+      lane_k = 16u * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
       lane_off = static_cast<uint32_t>(8 * wave + (lane >> 3)) * static_cast<uint32_t>(2 * ld) + lane_k;
       step = 8u * W * static_cast<uint32_t>(2 * ld);
       on_col = true;
       bytes = static_cast<uint32_t>(min(static_cast<int64_t>(ROWS), rows - row0)) * static_cast<uint32_t>(2 * ld);
-      // piece ^ (row / 2 % 8): any 16 rows read at one piece hit all banks
-      slot = 1024u * wave + 128u * (lane >> 3) + 16u * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
     }
+    place = 1024u * wave;
   }
   // T: the 64-byte segment of a k row is XORed with this, so that four k rows read at one
   // segment hit all banks
@@ -88,18 +90,16 @@ struct Operand {
     constexpr int nseg = ROWS / 32;            // segments of a row
     return nseg >= 4 ? (kk & 3) : nseg == 2 ? ((kk >> 1) & 1) : 0;
   }
-  // piece g of stage s; past K and past the tile zeros
-  __device__ __forceinline__ u32x4 load(int s, int g) const {
+  // where piece g of stage s begins; past K and past the tile there is nothing to load
+  __device__ __forceinline__ uint32_t offset(int s, int g) const {
     if constexpr (T) {
-      const bool on = on_col && 64 * s + static_cast<int>(lane_k) + kPer * W * g < K;
-      return tile_load(tile_rsrc(p + static_cast<int64_t>(s) * 64 * ld, bytes), on ? lane_off + step * g : kPast);
+      return on_col && 64 * s + static_cast<int>(lane_k) + kPer * W * g < K ? lane_off + step * g : kPast;
     } else {
-      const bool on = 128u * static_cast<uint32_t>(s) + lane_k < 2u * static_cast<uint32_t>(K);
-      return tile_load(tile_rsrc(p, bytes), on ? lane_off + 128u * s + step * g : kPast);
+      return 128u * static_cast<uint32_t>(s) + lane_k < 2u * static_cast<uint32_t>(K) ? lane_off + 128u * s + step * g : kPast;
     }
   }
-  __device__ __forceinline__ void store(unsigned char* st, int g, const u32x4& v) const {
-    *reinterpret_cast<u32x4*>(st + slot + 1024 * W * g) = v;
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(int s) const {
+    return T ? tile_rsrc(p + static_cast<int64_t>(s) * 64 * ld, bytes) : tile_rsrc(p, bytes);
   }
 };
 
@@ -164,24 +164,37 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   }
   const int all = static_cast<int>((p.K + 63) >> 6), len = (all + p.slices - 1) / p.slices;
   const int s0 = slice * len, S = min(all - s0, len);   // stages s0 .. s0 + S - 1
-  u32x4 gr[NL];                                // a stage's pieces on their way
-  auto load = [&](int s, int i) {
+  // Pieces go straight into LDS where both operands' rows run along k. Transposed reads of
+  // LDS make the compiler wait for every such load first (229 us became 314), so there they
+  // pass through registers.
+  constexpr bool kDirect = !AT && !BT;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  u32x4 gr[kDirect ? 1 : NL];
+  auto place = [&](int s, int i) {
+    return smem + (s & 1) * kStage + (i < LA ? A.place + 1024 * W * i : kBOff + B.place + 1024 * W * (i - LA));
+  };
+  auto load = [&](int s, int i) {              // piece i of stage s
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t off;
     if (i < LA) {
-      gr[i] = A.load(s0 + s, i);
+      rs = A.resource(s0 + s);
+      off = A.offset(s0 + s, i);
     } else if constexpr (GATED) {
       const uint32_t k = 128u * static_cast<uint32_t>(s0 + s);
-      gr[i] = tile_load(gated_rs[i - LA], k + B.lane_k < 2u * static_cast<uint32_t>(B.K) ? gated_off[i - LA] + k : kPast);
+      rs = gated_rs[i - LA];
+      off = k + B.lane_k < 2u * static_cast<uint32_t>(B.K) ? gated_off[i - LA] + k : kPast;
     } else {
-      gr[i] = B.load(s0 + s, i - LA);
+      rs = B.resource(s0 + s);
+      off = B.offset(s0 + s, i - LA);
+    }
+    if constexpr (kDirect) {
+      tile_load_lds(rs, place(s, i), off);
+    } else {
+      gr[i] = tile_load(rs, off);
     }
   };
   auto store = [&](int s, int i) {
-    unsigned char* st = smem + (s & 1) * kStage;
-    if (i < LA) {
-      A.store(st, i, gr[i]);
-    } else {
-      B.store(st + kBOff, i - LA, gr[i]);
-    }
+    if constexpr (!kDirect) *reinterpret_cast<u32x4*>(place(s, i) + 16 * lane) = gr[i];
   };
   const int wm = wave / WN, wn = wave % WN;
   auto read_a = [&](int s, int ks, int i) { return fragment<AT, TM>(smem + (s & 1) * kStage, wm * MB + i, ks); };
@@ -195,6 +208,7 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
     store(0, i);
     load(1, i);
   }
+  if constexpr (kDirect) tile_wait<NL>();
   tile_barrier();
   s16x8 fa[2][MB], fb[2][NB];
 #pragma unroll
@@ -204,18 +218,23 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
 
   // A stage is four steps of 16 k: the MFMAs of one step's fragments (B times A, so that a
   // lane's results are neighbouring columns of one row), spread between them the reads of
-  // the next step's. In the first three steps the next stage goes from its registers into
-  // LDS, each piece followed by the load of the piece one stage on; then every wave has
-  // read this stage and written the next, and after the barrier the next one is read.
-  constexpr int Q = MB * NB, kOver = 3 * Q;
+  // the next step's. Before the last step every wave has read this stage and the next one is
+  // in LDS: after the barrier that one is read, and the stage behind it may take this one's
+  // place. Loads straight into LDS are issued then, a stage ahead; others earlier: in the
+  // first three steps the next stage goes from its registers into LDS, each piece followed
+  // by the load of the piece one stage on.
+  constexpr int Q = MB * NB, kFrom = kDirect ? 3 * Q : 0, kOver = kDirect ? Q : 3 * Q;
   for (int s = 0; s < S; ++s) {
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       const int f = ks & 1;
-      if (ks == 3) tile_barrier();
+      if (ks == 3) {
+        if constexpr (kDirect) tile_wait<0>();
+        tile_barrier();
+      }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB, t = ks * Q + q;
+        const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB, t = ks * Q + q - kFrom;
         acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
 #pragma unroll
         for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
@@ -226,15 +245,18 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
             fb[1 - f][r - MB] = read_b(sr, kr, r - MB);
           }
         }
+        if (t >= 0) {
 #pragma unroll
-        for (int r = t * NL / kOver; r < (t + 1) * NL / kOver && r < NL; ++r) {
-          store(s + 1, r);
-          load(s + 2, r);
+          for (int r = t * NL / kOver; r < (t + 1) * NL / kOver && r < NL; ++r) {
+            store(s + 1, r);
+            load(s + 2, r);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
+  if constexpr (kDirect) tile_wait<0>();       // loads behind the last stage
 
   auto quad = [&](int i, int j, int g) { return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]}; };
   if constexpr (GATED) {

@@ -21,6 +21,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* p, uint3
 __device__ __forceinline__ u32x4 tile_load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0));
 }
+// 16 bytes a lane straight into LDS, lane l's at lds + 16 l (lds the same in the whole wave).
+__device__ __forceinline__ void tile_load_lds(__amdgpu_buffer_rsrc_t r, unsigned char* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, static_cast<int>(off), 0, 0, 0);
+}
+// Waits until at most N of this wave's global loads are on their way.
+template <int N>
+__device__ __forceinline__ void tile_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 // A barrier that leaves global loads in flight.
 __device__ __forceinline__ void tile_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
