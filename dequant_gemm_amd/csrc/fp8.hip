@@ -76,17 +76,19 @@ __global__ __launch_bounds__(256) void k_quant_fp8_blocks(const uint16_t* __rest
 }
 
 // ---------------------------------------------------------------------------
-// A tile's shape: WM x WN waves with MB x NB blocks of 16 x 16 each.
-template <int MB_, int NB_, int WM_, int WN_>
+// A tile's shape: WM x WN waves with MB x NB blocks of 16 x 16 each, RING stages in LDS.
+template <int MB_, int NB_, int WM_, int WN_, int RING_>
 struct Tile8 {
   static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN;
   static constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN;
-  static constexpr int kStage = 128 * (TM + TN) + 4 * TM;        // 128 codes of every row, the rows' scales
+  // 128 codes of every row, the scales of the rows of A, those of B's blocks (a wave's load)
+  static constexpr int kStage = 128 * (TM + TN) + 4 * TM + 256;
   // 1024-byte pieces of a stage per wave (eight rows each)
   static constexpr int LA = TM / 8 / W, LB = TN / 8 / W, NL = LA + LB;
-  static_assert(LA * 8 * W == TM && LB * 8 * W == TN && TM <= 64 * W && 16 * NB <= 128 && 128 % (16 * NB) == 0, "whole pieces; a wave's rows in one block");
-  static constexpr int kLds = W == 8 ? 148 * 1024 : (2 * kStage > 64 * 1024 ? 2 * kStage : 64 * 1024);
-  static_assert(2 * kStage <= kLds && kLds <= 160 * 1024, "one compute unit's LDS");
+  static_assert(LA * 8 * W == TM && LB * 8 * W == TN && TM < 64 * W && TM % 64 == 0 && 128 % (16 * NB) == 0, "whole pieces; a wave's rows in one block");
+  static constexpr int kRing = RING_;
+  static constexpr int kLds = kRing * kStage;
+  static_assert(kRing >= 2 && kLds <= 160 * 1024, "one compute unit's LDS");
 };
 
 // One 16 x 16 block of results over the 128 codes of a stage. EXACT: on the bf16 MFMA, whose
@@ -127,50 +129,49 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
   const int len = (static_cast<int>(kb) + p.slices - 1) / p.slices;
   const int s0 = slice * len, S = min(static_cast<int>(kb) - s0, len);   // stages s0 .. s0 + S - 1
 
-  // ---- stage loads: wave w takes rows 8 (W i + w) .. + 7 of A, then of B; lane l loads the
-  // 16-byte piece l % 8 of row l / 8 into registers and writes it to slot piece ^ (row / 2 %
-  // 8) of the row (any 16 rows read at one piece hit all banks) ----
-  const uint32_t lane_k = 16u * (lane & 7);
+  // ---- stage loads, straight into LDS: wave w takes rows 8 (W i + w) .. + 7 of A, then of B;
+  // slot l % 8 of row l / 8 is lane l's and holds the row's piece l % 8 ^ (row / 2 % 8) (any
+  // 16 rows read at one piece hit all banks) ----
+  const uint32_t lane_k = 16u * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
   const uint32_t base = static_cast<uint32_t>(8 * wave + (lane >> 3)) * K + lane_k;
-  const uint32_t slot = 1024u * wave + 128u * (lane >> 3) + 16u * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
-  const __amdgpu_buffer_rsrc_t ars = tile_rsrc(p.xq + m0 * p.K, static_cast<uint32_t>(min(static_cast<int64_t>(TM), p.M - m0)) * K);
-  __amdgpu_buffer_rsrc_t brs[LB];
+  const uint32_t arows = static_cast<uint32_t>(min(static_cast<int64_t>(TM), p.M - m0));
+  const uint32_t brows = static_cast<uint32_t>(min(static_cast<int64_t>(TC), N - n0));
+  const uint8_t* bp[LB];
   uint32_t boff[LB];
 #pragma unroll
   for (int g = 0; g < LB; ++g) {
-    const uint32_t rows = static_cast<uint32_t>(min(static_cast<int64_t>(TC), N - n0));
     if constexpr (GATED) {                     // blocks of 16 rows are gate and up in turn
       const int row = 8 * (W * g + wave), blk = row >> 4;
-      brs[g] = tile_rsrc(p.w + ((blk & 1) * N + n0) * p.K, rows * K);
+      bp[g] = p.w + ((blk & 1) * N + n0) * p.K;
       boff[g] = static_cast<uint32_t>(16 * (blk >> 1) + (row & 15) + (lane >> 3)) * K + lane_k;
     } else {
-      brs[g] = tile_rsrc(p.w + n0 * p.K, rows * K);
+      bp[g] = p.w + n0 * p.K;
       boff[g] = base + 8u * W * g * K;
     }
   }
-  const float* xs = p.xs + m0 * kb;
-  const __amdgpu_buffer_rsrc_t srs = tile_rsrc(xs, static_cast<uint32_t>(min(static_cast<int64_t>(TM), p.M - m0) * kb * 4));
-  u32x4 gr[NL];
-  float sr = 0.0f;
+  // scales: the first waves take the rows' of A, the next one those of B's two blocks (gated:
+  // the block of the gate rows, of the up rows)
+  const uint32_t kb4 = static_cast<uint32_t>(4 * kb);
+  const bool of_a = wave < TM / 64;
+  const int64_t b0 = n0 >> 7, b1 = GATED ? (N + n0) >> 7 : min(b0 + 1, (N - 1) >> 7);
+  const void* sp = of_a ? static_cast<const void*>(p.xs + m0 * kb) : p.ws + b0 * kb;
+  const uint32_t sbytes = of_a ? arows * kb4 : static_cast<uint32_t>((b1 - b0 + 1) * kb4);
+  const uint32_t soff = of_a ? static_cast<uint32_t>(tid) * kb4 : lane == 0 ? 0u : lane == 1 ? sbytes - kb4 : kPast;
+  constexpr int kRing = Shape::kRing;
+  auto stage_at = [&](int s) { return smem + ((kRing & (kRing - 1)) ? s % kRing : s & (kRing - 1)) * kStage; };
   auto load = [&](int s, int i) {              // piece i of stage s; past K and past the rows zeros
+    unsigned char* st = stage_at(s) + 1024 * wave;
     const uint32_t k = 128u * static_cast<uint32_t>(s0 + s);
     const bool on = k + lane_k < K;
     if (i < LA) {
-      gr[i] = tile_load(ars, on ? base + k + 8u * W * i * K : kPast);
+      tile_load_lds(p.xq + m0 * p.K, arows * K, st + 1024 * W * i, on ? base + k + 8u * W * i * K : kPast);
     } else {
-      gr[i] = tile_load(brs[i - LA], on ? boff[i - LA] + k : kPast);
+      tile_load_lds(bp[i - LA], brows * K, st + kBOff + 1024 * W * (i - LA), on ? boff[i - LA] + k : kPast);
     }
   };
   auto load_scale = [&](int s) {
-    const bool on = tid < TM && s < S;
-    sr = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(srs, on ? static_cast<int>(4u * (static_cast<uint32_t>(tid) * static_cast<uint32_t>(kb) + static_cast<uint32_t>(s0 + s))) : -1, 0, 0));
-  };
-  auto store = [&](int s, int i) {
-    unsigned char* st = smem + (s & 1) * kStage;
-    *reinterpret_cast<u32x4*>(st + (i < LA ? 1024 * W * i : kBOff + 1024 * W * (i - LA)) + slot) = gr[i];
-  };
-  auto store_scale = [&](int s) {
-    if (tid < TM) *reinterpret_cast<float*>(smem + (s & 1) * kStage + kSOff + 4 * tid) = sr;
+    if (wave <= TM / 64)
+      tile_load_lds4(sp, sbytes, stage_at(s) + kSOff + 256 * wave, s < S ? soff + 4u * static_cast<uint32_t>(s0 + s) : kPast);
   };
 
   const int wm = wave / WN, wn = wave % WN;
@@ -180,45 +181,46 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(at + f0), hi = *reinterpret_cast<const i32x4*>(at + f1);
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
-  auto read_a = [&](int s, int i) { return frag(smem + (s & 1) * kStage + (wm * MB + i) * 2048); };
-  auto read_b = [&](int s, int j) { return frag(smem + (s & 1) * kStage + kBOff + (wn * NB + j) * 2048); };
-  auto read_scale = [&](int s, int i) { return *reinterpret_cast<const float*>(smem + (s & 1) * kStage + kSOff + 4 * ((wm * MB + i) * 16 + c)); };
+  auto read_a = [&](int s, int i) { return frag(stage_at(s) + (wm * MB + i) * 2048); };
+  auto read_b = [&](int s, int j) { return frag(stage_at(s) + kBOff + (wn * NB + j) * 2048); };
+  auto read_scale = [&](int s, int i) { return *reinterpret_cast<const float*>(stage_at(s) + kSOff + 4 * ((wm * MB + i) * 16 + c)); };
   // the wave's weight rows lie in one block of scales (gated: gate and up in one each)
-  const int64_t nb = GATED ? n0 + 8 * NB * wn : n0 + 16 * NB * wn;
-  const float* ws0 = p.ws + (min(nb, N - 1) >> 7) * kb + s0;
-  const float* ws1 = GATED ? p.ws + ((N + min(nb, N - 1)) >> 7) * kb + s0 : ws0;
+  const int wb = GATED ? 0 : static_cast<int>(((n0 + 16 * NB * wn) >> 7) - b0);
+  auto read_wscale = [&](int s, int b) { return *reinterpret_cast<const float*>(stage_at(s) + kSOff + 4 * (TM + b)); };
 
   f32x4 acc[MB][NB] = {};
+  constexpr int Q = MB * NB, kLag = 3;         // results are added this many MFMAs later
+  static_assert(NB % 2 == 0, "fb[0] holds a stage's first block again");
+  // a stage's loads are issued beside a last and a first part of the MFMAs
+  constexpr int kLast = MB, kFirst = MB * (NB / 2), kN1 = NL * kLast / (kLast + kFirst);
 #pragma unroll
-  for (int i = 0; i < NL; ++i) load(0, i);
-  load_scale(0);
+  for (int r = 0; r + 1 < kRing; ++r) {
+    load_scale(r);
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    store(0, i);
-    load(1, i);
+    for (int i = 0; i < NL; ++i) load(r, i);
   }
-  store_scale(0);
-  load_scale(1);
+#pragma unroll
+  for (int i = 0; i < kN1; ++i) load(kRing - 1, i);
+  // (the scales' loads, which not every wave has, are not counted: the waits are a little long)
+  tile_wait<(kRing - 2) * NL + kN1>();
   tile_barrier();
   i32x8 fa[MB], fb[2];
-  float sx[MB], sc0[MB], sc1[GATED ? MB : 1];
+  float sx[MB], w0, w1 = 0.0f;
   fb[0] = read_b(0, 0);
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     fa[i] = read_a(0, i);
     sx[i] = read_scale(0, i);
   }
-  float w0 = ws0[0], w1 = ws1[0];
-  constexpr int Q = MB * NB, kLag = 2;         // results are added this many MFMAs later
-  static_assert(NB % 2 == 0, "fb[0] holds a stage's first block again");
+  w0 = read_wscale(0, wb);
+  if constexpr (GATED) w1 = read_wscale(0, 1);
   for (int s = 0; s < S; ++s) {
+    float sc0[MB], sc1[GATED ? MB : 1];
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       sc0[i] = sx[i] * w0;
       if constexpr (GATED) sc1[i] = sx[i] * w1;
     }
-    w0 = ws0[min(s + 1, S - 1)];
-    if constexpr (GATED) w1 = ws1[min(s + 1, S - 1)];
     f32x4 part[kLag + 1];
     auto add = [&](int t) {
       const int i = t % MB, j = t / MB;
@@ -229,9 +231,11 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
 #pragma unroll
     for (int t = 0; t < Q; ++t) {
       const int i = t % MB, j = t / MB;
-      if (i == 0 && j == NB - 1) {
-        // every wave has this stage's last fragments in registers and the next stage in
-        // LDS: the next stage is read from here on
+      if (t == Q - kLast) {
+        // every wave has this stage's last fragments in registers, and its loads of the
+        // next stage are in LDS: that one is read from here on, and the stage after it
+        // kRing behind it takes this one's place
+        tile_wait<(kRing - 2) * NL>();
         tile_barrier();
         fb[(j + 1) & 1] = read_b(s + 1, 0);
       } else if (i == 0) {
@@ -241,25 +245,28 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
       if (j == NB - 1) {
         fa[i] = read_a(s + 1, i);
         sx[i] = read_scale(s + 1, i);
+        if (i == 0) {
+          w0 = read_wscale(s + 1, wb);
+          if constexpr (GATED) w1 = read_wscale(s + 1, 1);
+        }
       }
       if (t >= kLag) add(t - kLag);
-      // the next stage into LDS and the one after it into its registers, in the first
-      // NB - 1 of NB parts
-      constexpr int kOver = MB * (NB - 1);
+      if (t >= Q - kLast) {
+        constexpr int l1 = kN1;
+        const int u = t - (Q - kLast);
 #pragma unroll
-      for (int r = t * NL / kOver; r < (t + 1) * NL / kOver && r < NL; ++r) {
-        store(s + 1, r);
-        load(s + 2, r);
-      }
-      if (t == 0) {
-        store_scale(s + 1);
-        load_scale(s + 2);
+        for (int r = u * l1 / kLast; r < (u + 1) * l1 / kLast; ++r) load(s + kRing, r);
+      } else if (t < kFirst) {
+#pragma unroll
+        for (int r = kN1 + t * (NL - kN1) / kFirst; r < kN1 + (t + 1) * (NL - kN1) / kFirst; ++r) load(s - 1 + kRing, r);
+        if (t == 0) load_scale(s - 1 + kRing);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int t = Q - kLag; t < Q; ++t) add(t);
   }
+  tile_wait<0>();                              // loads behind the last stage
 
   if constexpr (GATED) {
     if (p.slices > 1) {
@@ -320,17 +327,17 @@ hipError_t launch_fp8_tiles(Fp8Params p, hipStream_t st) {
   if (!GATED && p.ydt == 0) {
     // fp32 results: smaller tiles for the largest shapes, since the converted operands take registers
     switch (plan.shape) {
-      case 0: case 1: case 2: e = launch_tile8<Tile8<4, 4, 2, 2>, true, false>(p, st); break;
-      case 3: e = launch_tile8<Tile8<2, 4, 2, 2>, true, false>(p, st); break;
-      default: e = launch_tile8<Tile8<2, 2, 2, 2>, true, false>(p, st); break;
+      case 0: case 1: case 2: e = launch_tile8<Tile8<4, 4, 2, 2, 2>, true, false>(p, st); break;
+      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4>, true, false>(p, st); break;
+      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4>, true, false>(p, st); break;
     }
   } else {
     switch (plan.shape) {
-      case 0: e = launch_tile8<Tile8<4, 8, 4, 2>, false, GATED>(p, st); break;
-      case 1: e = launch_tile8<Tile8<4, 4, 4, 2>, false, GATED>(p, st); break;
-      case 2: e = launch_tile8<Tile8<4, 4, 2, 2>, false, GATED>(p, st); break;
-      case 3: e = launch_tile8<Tile8<2, 4, 2, 2>, false, GATED>(p, st); break;
-      default: e = launch_tile8<Tile8<2, 2, 2, 2>, false, GATED>(p, st); break;
+      case 0: e = launch_tile8<Tile8<4, 8, 4, 2, 2>, false, GATED>(p, st); break;
+      case 1: e = launch_tile8<Tile8<4, 4, 4, 2, 3>, false, GATED>(p, st); break;
+      case 2: e = launch_tile8<Tile8<4, 4, 2, 2, 4>, false, GATED>(p, st); break;
+      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4>, false, GATED>(p, st); break;
+      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4>, false, GATED>(p, st); break;
     }
   }
   if (e != hipSuccess || plan.slices == 1) return e;

@@ -33,26 +33,29 @@ struct TileParams {
   float* part;
 };
 
-// A tile's shape: WM x WN waves with MB x NB blocks of 32 x 32 each.
-template <int MB_, int NB_, int WM_, int WN_>
+// A tile's shape: WM x WN waves with MB x NB blocks of 32 x 32 each; stages of KS steps of 16 k,
+// RING of them in LDS (one is read, the others are on their way), the loads of a stage issued
+// over SPREAD steps.
+template <int MB_, int NB_, int WM_, int WN_, int KS_, int RING_, int SPREAD_>
 struct Tile16 {
-  static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN;
+  static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN, KS = KS_, kRing = RING_, kSpread = SPREAD_;
   static constexpr int TM = 32 * MB * WM, TN = 32 * NB * WN;
-  static constexpr int kStage = 128 * (TM + TN);                 // 64 k of every row
+  static constexpr int kRow = 32 * KS;                           // bytes of a stage's row
+  static constexpr int kStage = kRow * (TM + TN);
   // 1024-byte pieces of a stage per wave
-  static constexpr int LA = TM / 8 / W, LB = TN / 8 / W, NL = LA + LB;
-  static_assert(LA * 8 * W == TM && LB * 8 * W == TN, "whole pieces");
-  static constexpr int kLds = W == 8 ? 148 * 1024 : (2 * kStage > 64 * 1024 ? 2 * kStage : 64 * 1024);
-  static_assert(2 * kStage <= kLds && kLds <= 160 * 1024, "one compute unit's LDS");
+  static constexpr int LA = TM * kRow / 1024 / W, LB = TN * kRow / 1024 / W, NL = LA + LB;
+  static_assert(LA * 1024 * W == TM * kRow && LB * 1024 * W == TN * kRow && kSpread <= KS, "whole pieces");
+  static constexpr int kLds = W * MB * NB > 16 ? 148 * 1024 : (kRing * kStage > 36 * 1024 ? kRing * kStage : 36 * 1024);
+  static_assert(kRing >= 2 && kRing * kStage <= kLds && kLds <= 160 * 1024, "one compute unit's LDS");
 };
 
-// One operand's stages: rows of 128 bytes (64 k), or with T 64 rows (one k each) of 2 ROWS bytes.
-// A piece of 1024 bytes is a wave's load: eight rows of 128 bytes, or with T some k rows; in
-// LDS its 16-byte parts lie in the lanes' order, and lanes load the part that belongs there.
-template <bool T, int ROWS, int W>
+// One operand's stages: rows of 32 KS bytes, or with T 16 KS rows (one k each) of 2 ROWS bytes.
+// A piece of 1024 bytes is a wave's load: some rows; in LDS its 16-byte parts lie in the
+// lanes' order, and lanes load the part that belongs there.
+template <bool T, int ROWS, int W, int KS>
 struct Operand {
-  static constexpr int kPieces = ROWS / 8;     // T: 16-byte pieces of a k row
-  static constexpr int kPer = 64 / kPieces;    // T: k rows of a wave's load
+  static constexpr int kParts = T ? ROWS / 8 : 2 * KS;           // 16-byte parts of a row
+  static constexpr int kPer = 64 / kParts;                       // rows of a wave's load
   const uint16_t* p;                           // first row, or with T first column
   int64_t ld;
   uint32_t bytes;                              // that the resource covers
@@ -64,48 +67,48 @@ struct Operand {
     const int lane = threadIdx.x & 63;
     ld = ld_;
     K = static_cast<int>(K_);
+    const int row = kPer * wave + lane / kParts, at = lane % kParts;
     if constexpr (T) {
       p = base + row0;
-      const int kk = kPer * wave + lane / kPieces, at = lane % kPieces;
-      const int piece = ((at >> 2) ^ swizzle(kk)) * 4 + (at & 3);
-      lane_k = static_cast<uint32_t>(kk);
-      lane_off = static_cast<uint32_t>(kk) * static_cast<uint32_t>(2 * ld) + 16u * piece;
-      step = static_cast<uint32_t>(kPer * W) * static_cast<uint32_t>(2 * ld);
-      on_col = 8 * piece < rows - row0;        // rows a multiple of 8
-      bytes = 64u * static_cast<uint32_t>(2 * ld);
+      const int part = ((at >> 2) ^ swizzle(row)) * 4 + (at & 3);
+      lane_k = static_cast<uint32_t>(row);
+      lane_off = static_cast<uint32_t>(row) * static_cast<uint32_t>(2 * ld) + 16u * part;
+      on_col = 8 * part < rows - row0;         // rows a multiple of 8
+      bytes = 16u * KS * static_cast<uint32_t>(2 * ld);
     } else {
       p = base + row0 * ld;
-      // piece ^ (row / 2 % 8): any 16 rows read at one piece hit all banks
-      lane_k = 16u * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
-      lane_off = static_cast<uint32_t>(8 * wave + (lane >> 3)) * static_cast<uint32_t>(2 * ld) + lane_k;
-      step = 8u * W * static_cast<uint32_t>(2 * ld);
+      lane_k = 16u * (at ^ swizzle(row));
+      lane_off = static_cast<uint32_t>(row) * static_cast<uint32_t>(2 * ld) + lane_k;
       on_col = true;
       bytes = static_cast<uint32_t>(min(static_cast<int64_t>(ROWS), rows - row0)) * static_cast<uint32_t>(2 * ld);
     }
+    step = static_cast<uint32_t>(kPer * W) * static_cast<uint32_t>(2 * ld);
     place = 1024u * wave;
   }
-  // T: the 64-byte segment of a k row is XORed with this, so that four k rows read at one
-  // segment hit all banks
-  static __device__ __forceinline__ int swizzle(int kk) {
-    constexpr int nseg = ROWS / 32;            // segments of a row
-    return nseg >= 4 ? (kk & 3) : nseg == 2 ? ((kk >> 1) & 1) : 0;
+  // The order of a row's parts: any 16 rows read at one part hit all banks. T: the order of
+  // its 64-byte segments: four k rows read at one segment hit all banks.
+  static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (T) {
+      constexpr int nseg = ROWS / 32;          // segments of a row
+      return nseg >= 4 ? (row & 3) : nseg == 2 ? ((row >> 1) & 1) : 0;
+    } else {
+      return KS == 4 ? (row >> 1) & 7 : (row >> 2) & 3;
+    }
   }
   // where piece g of stage s begins; past K and past the tile there is nothing to load
   __device__ __forceinline__ uint32_t offset(int s, int g) const {
     if constexpr (T) {
-      return on_col && 64 * s + static_cast<int>(lane_k) + kPer * W * g < K ? lane_off + step * g : kPast;
+      return on_col && 16 * KS * s + static_cast<int>(lane_k) + kPer * W * g < K ? lane_off + step * g : kPast;
     } else {
-      return 128u * static_cast<uint32_t>(s) + lane_k < 2u * static_cast<uint32_t>(K) ? lane_off + 128u * s + step * g : kPast;
+      return 32u * KS * s + lane_k < 2u * static_cast<uint32_t>(K) ? lane_off + 32u * KS * s + step * g : kPast;
     }
   }
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(int s) const {
-    return T ? tile_rsrc(p + static_cast<int64_t>(s) * 64 * ld, bytes) : tile_rsrc(p, bytes);
-  }
+  __device__ __forceinline__ const uint16_t* first(int s) const { return T ? p + static_cast<int64_t>(s) * (16 * KS) * ld : p; }
 };
 
 // Fragments of block `blk` (32 rows) for k 16 ks .. + 15 of a stage: lane l has row l % 32 and
 // eight k from 8 (l / 32) on.
-template <bool T, int ROWS>
+template <bool T, int ROWS, int KS>
 __device__ __forceinline__ s16x8 fragment(const unsigned char* st, int blk, int ks) {
   const int lane = threadIdx.x & 63;
   if constexpr (T) {
@@ -113,13 +116,13 @@ __device__ __forceinline__ s16x8 fragment(const unsigned char* st, int blk, int 
     typedef __attribute__((address_space(3))) s16x4* LdsPtr;
     const int grp = lane >> 4, kr = (lane & 15) >> 2;
     const int kk = 16 * ks + 8 * (grp >> 1) + kr;
-    const unsigned char* at = st + kk * (2 * ROWS) + ((blk ^ Operand<true, ROWS, 1>::swizzle(kr)) << 6) + 32 * (grp & 1) + 8 * (lane & 3);
+    const unsigned char* at = st + kk * (2 * ROWS) + ((blk ^ Operand<true, ROWS, 1, KS>::swizzle(kr)) << 6) + 32 * (grp & 1) + 8 * (lane & 3);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + 4 * (2 * ROWS)));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
     const int c = lane & 31, h = lane >> 5;
-    return *reinterpret_cast<const s16x8*>(st + (32 * blk + c) * 128 + (((2 * ks + h) ^ ((c >> 1) & 7)) << 4));
+    return *reinterpret_cast<const s16x8*>(st + (32 * blk + c) * (32 * KS) + (((2 * ks + h) ^ Operand<false, ROWS, 1, KS>::swizzle(c)) << 4));
   }
 }
 
@@ -136,8 +139,8 @@ template <class Shape, bool F16, bool AT, bool BT, bool GATED>
 __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
-  constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL;
-  constexpr int kStage = Shape::kStage, kBOff = TM * 128;
+  constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL, KS = Shape::KS;
+  constexpr int kStage = Shape::kStage, kBOff = TM * Shape::kRow;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   int im, in;
   const int tm = static_cast<int>((p.M + TM - 1) / TM), tn = static_cast<int>((p.N + TC - 1) / TC);
@@ -145,70 +148,51 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   tile_place(static_cast<int>(blockIdx.x) - slice * tm * tn, tm, tn, &im, &in);
   const int64_t m0 = static_cast<int64_t>(im) * TM, n0 = static_cast<int64_t>(in) * TC;
 
-  Operand<AT, TM, W> A;
+  Operand<AT, TM, W, KS> A;
   A.init(p.a, p.lda, m0, p.M, p.K, wave);
-  Operand<BT, TN, W> B;
+  Operand<BT, TN, W, KS> B;
   // gated: blocks of 32 rows are gate and up in turn, so that a wave holds both of a column
   uint32_t gated_off[GATED ? LB : 1];
-  __amdgpu_buffer_rsrc_t gated_rs[GATED ? LB : 1];
+  const uint16_t* gated_p[GATED ? LB : 1];
+  uint32_t gated_bytes = 0;
   B.init(p.b, p.ldb, n0, p.N, p.K, wave);
   if constexpr (GATED) {
     const int lane = threadIdx.x & 63;
-    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(TC), p.N - n0)) * static_cast<uint32_t>(2 * p.ldb);
+    gated_bytes = static_cast<uint32_t>(min(static_cast<int64_t>(TC), p.N - n0)) * static_cast<uint32_t>(2 * p.ldb);
 #pragma unroll
     for (int g = 0; g < LB; ++g) {
-      const int row = 8 * (W * g + wave), blk = row >> 5;
-      gated_rs[g] = tile_rsrc(p.b + ((blk & 1) * p.N + n0) * p.ldb, bytes);
-      gated_off[g] = static_cast<uint32_t>(32 * (blk >> 1) + (row & 31) + (lane >> 3)) * static_cast<uint32_t>(2 * p.ldb) + B.lane_k;
+      const int row = B.kPer * (W * g + wave), blk = row >> 5;
+      gated_p[g] = p.b + ((blk & 1) * p.N + n0) * p.ldb;
+      gated_off[g] = static_cast<uint32_t>(32 * (blk >> 1) + (row & 31) + lane / B.kParts) * static_cast<uint32_t>(2 * p.ldb) + B.lane_k;
     }
   }
-  const int all = static_cast<int>((p.K + 63) >> 6), len = (all + p.slices - 1) / p.slices;
+  const int all = static_cast<int>((p.K + 16 * KS - 1) / (16 * KS)), len = (all + p.slices - 1) / p.slices;
   const int s0 = slice * len, S = min(all - s0, len);   // stages s0 .. s0 + S - 1
-  // Pieces go straight into LDS where both operands' rows run along k. Transposed reads of
-  // LDS make the compiler wait for every such load first (229 us became 314), so there they
-  // pass through registers.
-  constexpr bool kDirect = !AT && !BT;
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  u32x4 gr[kDirect ? 1 : NL];
-  auto place = [&](int s, int i) {
-    return smem + (s & 1) * kStage + (i < LA ? A.place + 1024 * W * i : kBOff + B.place + 1024 * W * (i - LA));
-  };
-  auto load = [&](int s, int i) {              // piece i of stage s
-    __amdgpu_buffer_rsrc_t rs;
-    uint32_t off;
+  constexpr int kRing = Shape::kRing;
+  auto stage_at = [&](int s) { return smem + ((kRing & (kRing - 1)) ? s % kRing : s & (kRing - 1)) * kStage; };
+  auto load = [&](int s, int i) {              // piece i of stage s, straight into LDS
+    unsigned char* st = stage_at(s);
     if (i < LA) {
-      rs = A.resource(s0 + s);
-      off = A.offset(s0 + s, i);
+      tile_load_lds(A.first(s0 + s), A.bytes, st + A.place + 1024 * W * i, A.offset(s0 + s, i));
     } else if constexpr (GATED) {
-      const uint32_t k = 128u * static_cast<uint32_t>(s0 + s);
-      rs = gated_rs[i - LA];
-      off = k + B.lane_k < 2u * static_cast<uint32_t>(B.K) ? gated_off[i - LA] + k : kPast;
+      const uint32_t k = 32u * KS * static_cast<uint32_t>(s0 + s);
+      tile_load_lds(gated_p[i - LA], gated_bytes, st + kBOff + B.place + 1024 * W * (i - LA),
+                    k + B.lane_k < 2u * static_cast<uint32_t>(B.K) ? gated_off[i - LA] + k : kPast);
     } else {
-      rs = B.resource(s0 + s);
-      off = B.offset(s0 + s, i - LA);
+      tile_load_lds(B.first(s0 + s), B.bytes, st + kBOff + B.place + 1024 * W * (i - LA), B.offset(s0 + s, i - LA));
     }
-    if constexpr (kDirect) {
-      tile_load_lds(rs, place(s, i), off);
-    } else {
-      gr[i] = tile_load(rs, off);
-    }
-  };
-  auto store = [&](int s, int i) {
-    if constexpr (!kDirect) *reinterpret_cast<u32x4*>(place(s, i) + 16 * lane) = gr[i];
   };
   const int wm = wave / WN, wn = wave % WN;
-  auto read_a = [&](int s, int ks, int i) { return fragment<AT, TM>(smem + (s & 1) * kStage, wm * MB + i, ks); };
-  auto read_b = [&](int s, int ks, int j) { return fragment<BT, TN>(smem + (s & 1) * kStage + kBOff, wn * NB + j, ks); };
+  auto read_a = [&](int s, int ks, int i) { return fragment<AT, TM, KS>(stage_at(s), wm * MB + i, ks); };
+  auto read_b = [&](int s, int ks, int j) { return fragment<BT, TN, KS>(stage_at(s) + kBOff, wn * NB + j, ks); };
 
   f32x16 acc[MB][NB] = {};
+  constexpr int SP = Shape::kSpread;           // steps over which a stage's loads are issued
 #pragma unroll
-  for (int i = 0; i < NL; ++i) load(0, i);
+  for (int r = 0; r < kRing; ++r)
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    store(0, i);
-    load(1, i);
-  }
-  if constexpr (kDirect) tile_wait<NL>();
+    for (int i = 0; i < (r + 1 < kRing ? NL : NL / SP); ++i) load(r, i);
+  tile_wait<(kRing - 2) * NL + NL / SP>();
   tile_barrier();
   s16x8 fa[2][MB], fb[2][NB];
 #pragma unroll
@@ -216,47 +200,44 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
 #pragma unroll
   for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
 
-  // A stage is four steps of 16 k: the MFMAs of one step's fragments (B times A, so that a
-  // lane's results are neighbouring columns of one row), spread between them the reads of
-  // the next step's. Before the last step every wave has read this stage and the next one is
-  // in LDS: after the barrier that one is read, and the stage behind it may take this one's
-  // place. Loads straight into LDS are issued then, a stage ahead; others earlier: in the
-  // first three steps the next stage goes from its registers into LDS, each piece followed
-  // by the load of the piece one stage on.
-  constexpr int Q = MB * NB, kFrom = kDirect ? 3 * Q : 0, kOver = kDirect ? Q : 3 * Q;
+  // A step of 16 k: the MFMAs of its fragments (B times A, so that a lane's results are
+  // neighbouring columns of one row), spread between them the reads of the next step's.
+  // Before a stage's last step every wave has read that stage and its loads of the next one
+  // are in LDS: after the barrier that one is read, and the loads of the stage kRing behind
+  // this one take its place, from the last step on over SP steps.
+  constexpr int Q = MB * NB;
   for (int s = 0; s < S; ++s) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
+    for (int ks = 0; ks < KS; ++ks) {
       const int f = ks & 1;
-      if (ks == 3) {
-        if constexpr (kDirect) tile_wait<0>();
+      const int part = ks == KS - 1 ? 0 : ks + 1, to = (ks == KS - 1 ? s : s - 1) + kRing;
+      if (ks == KS - 1) {
+        tile_wait<(kRing - 2) * NL>();
         tile_barrier();
       }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB, t = ks * Q + q - kFrom;
+        const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
         acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
 #pragma unroll
         for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
-          const int sr = ks == 3 ? s + 1 : s, kr = (ks + 1) & 3;
+          const int sr = ks == KS - 1 ? s + 1 : s, kr = (ks + 1) % KS;
           if (r < MB) {
             fa[1 - f][r] = read_a(sr, kr, r);
           } else {
             fb[1 - f][r - MB] = read_b(sr, kr, r - MB);
           }
         }
-        if (t >= 0) {
+        if (part < SP) {
+          const int l0 = part * NL / SP, l1 = (part + 1) * NL / SP;
 #pragma unroll
-          for (int r = t * NL / kOver; r < (t + 1) * NL / kOver && r < NL; ++r) {
-            store(s + 1, r);
-            load(s + 2, r);
-          }
+          for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) load(to, r);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
-  if constexpr (kDirect) tile_wait<0>();       // loads behind the last stage
+  tile_wait<0>();                              // loads behind the last stage
 
   auto quad = [&](int i, int j, int g) { return f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]}; };
   if constexpr (GATED) {
@@ -292,7 +273,8 @@ hipError_t launch_shape(const TileParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-TilePlan plan16(int64_t M, int64_t width, int64_t K) { return plan_tiles(M, width, (K + 63) / 64, 2); }
+constexpr int kKS = 4;                         // of every shape: a stage's steps
+TilePlan plan16(int64_t M, int64_t width, int64_t K) { return plan_tiles(M, width, (K + 16 * kKS - 1) / (16 * kKS), kKS / 2); }
 
 // part: scratch of plan_bytes (several slices)
 template <bool AT, bool BT, bool GATED>
@@ -307,11 +289,11 @@ hipError_t launch_tile16(TileParams p, bool f16, float* part, hipStream_t st) {
   };
   hipError_t e;
   switch (plan.shape) {
-    case 0: e = go(Tile16<2, 4, 4, 2>{}); break;
-    case 1: e = go(Tile16<2, 2, 4, 2>{}); break;
-    case 2: e = go(Tile16<2, 2, 2, 2>{}); break;
-    case 3: e = go(Tile16<1, 2, 2, 2>{}); break;
-    default: e = go(Tile16<1, 2, 2, 1>{}); break;
+    case 0: e = go(Tile16<2, 4, 4, 2, kKS, 2, 2>{}); break;
+    case 1: e = go(Tile16<2, 2, 4, 2, kKS, 3, 1>{}); break;
+    case 2: e = go(Tile16<2, 2, 2, 2, kKS, 4, 1>{}); break;
+    case 3: e = go(Tile16<1, 2, 2, 2, kKS, 3, 1>{}); break;
+    default: e = go(Tile16<1, 2, 2, 1, kKS, 4, 1>{}); break;
   }
   if (e != hipSuccess || plan.slices == 1) return e;
   return launch_tile_join<GATED>({part, plan.slices, p.M, p.N, width, nullptr, p.y, p.ydt, p.gelu, p.pre}, st);

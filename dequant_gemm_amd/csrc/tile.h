@@ -22,8 +22,26 @@ __device__ __forceinline__ u32x4 tile_load(__amdgpu_buffer_rsrc_t r, uint32_t of
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0));
 }
 // 16 bytes a lane straight into LDS, lane l's at lds + 16 l (lds the same in the whole wave).
-__device__ __forceinline__ void tile_load_lds(__amdgpu_buffer_rsrc_t r, unsigned char* lds, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, static_cast<int>(off), 0, 0, 0);
+// In assembly, since the compiler lets every transposed read of LDS wait for all such loads
+// that it knows of (a product of 229 us took 314): the caller waits, by tile_wait and a barrier
+// before what is loaded is read.
+__device__ __forceinline__ u32x4 tile_lds_rsrc(const void* p, uint32_t bytes) {
+  const uint64_t base = reinterpret_cast<uint64_t>(p);
+  return u32x4{static_cast<uint32_t>(base), static_cast<uint32_t>(base >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+__device__ __forceinline__ uint32_t tile_lds_at(unsigned char* lds) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(lds)));
+}
+__device__ __forceinline__ void tile_load_lds(const void* p, uint32_t bytes, unsigned char* lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(tile_lds_at(lds)), "v"(off),
+               "s"(tile_lds_rsrc(p, bytes))
+               : "m0", "memory");
+}
+// The same with four bytes a lane, at lds + 4 l.
+__device__ __forceinline__ void tile_load_lds4(const void* p, uint32_t bytes, unsigned char* lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(tile_lds_at(lds)), "v"(off),
+               "s"(tile_lds_rsrc(p, bytes))
+               : "m0", "memory");
 }
 // Waits until at most N of this wave's global loads are on their way.
 template <int N>
