@@ -35,18 +35,21 @@ struct TileParams {
 
 // A tile's shape: WM x WN waves with MB x NB blocks of 32 x 32 each; stages of KS steps of 16 k,
 // RING of them in LDS (one is read, the others are on their way), the loads of a stage issued
-// over SPREAD steps.
-template <int MB_, int NB_, int WM_, int WN_, int KS_, int RING_, int SPREAD_>
+// over SPREAD steps. AHEAD: a wave holds the fragments of a whole stage and reads the next
+// one's meanwhile, for tiles whose steps are shorter than a read of LDS takes.
+template <int MB_, int NB_, int WM_, int WN_, int KS_, int RING_, int SPREAD_, bool AHEAD_>
 struct Tile16 {
   static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN, KS = KS_, kRing = RING_, kSpread = SPREAD_;
+  static constexpr bool kAhead = AHEAD_;
   static constexpr int TM = 32 * MB * WM, TN = 32 * NB * WN;
   static constexpr int kRow = 32 * KS;                           // bytes of a stage's row
   static constexpr int kStage = kRow * (TM + TN);
   // 1024-byte pieces of a stage per wave
   static constexpr int LA = TM * kRow / 1024 / W, LB = TN * kRow / 1024 / W, NL = LA + LB;
   static_assert(LA * 1024 * W == TM * kRow && LB * 1024 * W == TN * kRow && kSpread <= KS, "whole pieces");
-  static constexpr int kLds = W * MB * NB > 16 ? 148 * 1024 : (kRing * kStage > 36 * 1024 ? kRing * kStage : 36 * 1024);
-  static_assert(kRing >= 2 && kRing * kStage <= kLds && kLds <= 160 * 1024, "one compute unit's LDS");
+  // (results of the largest tile pass through LDS as a whole)
+  static constexpr int kLds = std::max(kRing * kStage, TM * TN > 32768 ? 148 * 1024 : 36 * 1024);
+  static_assert(kRing >= 2 && kLds <= 160 * 1024 && (kRing - 2) * NL + NL <= 63, "one compute unit's LDS, a wave's loads on their way");
 };
 
 // One operand's stages: rows of 32 KS bytes, or with T 16 KS rows (one k each) of 2 ROWS bytes.
@@ -187,53 +190,105 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   auto read_b = [&](int s, int ks, int j) { return fragment<BT, TN, KS>(stage_at(s) + kBOff, wn * NB + j, ks); };
 
   f32x16 acc[MB][NB] = {};
-  constexpr int SP = Shape::kSpread;           // steps over which a stage's loads are issued
-#pragma unroll
-  for (int r = 0; r < kRing; ++r)
-#pragma unroll
-    for (int i = 0; i < (r + 1 < kRing ? NL : NL / SP); ++i) load(r, i);
-  tile_wait<(kRing - 2) * NL + NL / SP>();
-  tile_barrier();
-  s16x8 fa[2][MB], fb[2][NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
-#pragma unroll
-  for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
-
-  // A step of 16 k: the MFMAs of its fragments (B times A, so that a lane's results are
-  // neighbouring columns of one row), spread between them the reads of the next step's.
-  // Before a stage's last step every wave has read that stage and its loads of the next one
-  // are in LDS: after the barrier that one is read, and the loads of the stage kRing behind
-  // this one take its place, from the last step on over SP steps.
   constexpr int Q = MB * NB;
-  for (int s = 0; s < S; ++s) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int f = ks & 1;
-      const int part = ks == KS - 1 ? 0 : ks + 1, to = (ks == KS - 1 ? s : s - 1) + kRing;
-      if (ks == KS - 1) {
-        tile_wait<(kRing - 2) * NL>();
-        tile_barrier();
+  if constexpr (Shape::kAhead) {
+    // Stage s: its MFMAs (B times A, so that a lane's results are neighbouring columns of one
+    // row) from fragments read before, spread between them the reads of the next stage's.
+    // At its start the loads of the next stage are in LDS, and every wave has read this one:
+    // the loads of the stage kRing behind it take its place.
+    s16x8 fa[2][KS][MB], fb[2][KS][NB];
+    constexpr int kReads = KS * (MB + NB), kTotal = KS * Q;
+    auto read = [&](auto to_c, int s, int r) {
+      constexpr int to = decltype(to_c)::value;
+      const int ks = r / (MB + NB), i = r % (MB + NB);
+      if (i < MB) {
+        fa[to][ks][i] = read_a(s, ks, i);
+      } else {
+        fb[to][ks][i - MB] = read_b(s, ks, i - MB);
       }
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
+    for (int r = 0; r < kRing; ++r)
+#pragma unroll
+      for (int i = 0; i < NL; ++i) load(r, i);
+    tile_wait<(kRing - 1) * NL>();
+    tile_barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(I0{}, 0, r);
+    auto stage = [&](int s, auto at_c, auto to_c) {
+      constexpr int at = decltype(at_c)::value;
+      tile_wait<(kRing - 2) * NL>();
+      tile_barrier();
+#pragma unroll
+      for (int t = 0; t < kTotal; ++t) {
+        const int ks = t / Q, q = t % Q;
         const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
-        acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
+        acc[i][j] = mma<F16>(fb[at][ks][j], fa[at][ks][i], acc[i][j]);
+        // in the first three quarters, so that they have arrived at the barrier
+        constexpr int kOver = kTotal * 3 / 4;
 #pragma unroll
-        for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
-          const int sr = ks == KS - 1 ? s + 1 : s, kr = (ks + 1) % KS;
-          if (r < MB) {
-            fa[1 - f][r] = read_a(sr, kr, r);
-          } else {
-            fb[1 - f][r - MB] = read_b(sr, kr, r - MB);
-          }
-        }
-        if (part < SP) {
-          const int l0 = part * NL / SP, l1 = (part + 1) * NL / SP;
+        for (int r = t * kReads / kOver; r < (t + 1) * kReads / kOver && r < kReads; ++r) read(to_c, s + 1, r);
 #pragma unroll
-          for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) load(to, r);
-        }
+        for (int r = t * NL / kTotal; r < (t + 1) * NL / kTotal; ++r) load(s + kRing, r);
         __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int s = 0;
+    for (; s + 1 < S; s += 2) {
+      stage(s, I0{}, I1{});
+      stage(s + 1, I1{}, I0{});
+    }
+    if (s < S) stage(s, I0{}, I1{});
+  } else {
+    constexpr int SP = Shape::kSpread;           // steps over which a stage's loads are issued
+#pragma unroll
+    for (int r = 0; r < kRing; ++r)
+#pragma unroll
+      for (int i = 0; i < (r + 1 < kRing ? NL : NL / SP); ++i) load(r, i);
+    tile_wait<(kRing - 2) * NL + NL / SP>();
+    tile_barrier();
+    s16x8 fa[2][MB], fb[2][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
+
+    // A step of 16 k: the MFMAs of its fragments (B times A, so that a lane's results are
+    // neighbouring columns of one row), spread between them the reads of the next step's.
+    // Before a stage's last step every wave has read that stage and its loads of the next one
+    // are in LDS: after the barrier that one is read, and the loads of the stage kRing behind
+    // this one take its place, from the last step on over SP steps.
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int f = ks & 1;
+        const int part = ks == KS - 1 ? 0 : ks + 1, to = (ks == KS - 1 ? s : s - 1) + kRing;
+        if (ks == KS - 1) {
+          tile_wait<(kRing - 2) * NL>();
+          tile_barrier();
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
+          acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
+#pragma unroll
+          for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
+            const int sr = ks == KS - 1 ? s + 1 : s, kr = (ks + 1) % KS;
+            if (r < MB) {
+              fa[1 - f][r] = read_a(sr, kr, r);
+            } else {
+              fb[1 - f][r - MB] = read_b(sr, kr, r - MB);
+            }
+          }
+          if (part < SP) {
+            const int l0 = part * NL / SP, l1 = (part + 1) * NL / SP;
+#pragma unroll
+            for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) load(to, r);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   }
@@ -289,11 +344,11 @@ hipError_t launch_tile16(TileParams p, bool f16, float* part, hipStream_t st) {
   };
   hipError_t e;
   switch (plan.shape) {
-    case 0: e = go(Tile16<2, 4, 4, 2, kKS, 2, 2>{}); break;
-    case 1: e = go(Tile16<2, 2, 4, 2, kKS, 3, 1>{}); break;
-    case 2: e = go(Tile16<2, 2, 2, 2, kKS, 4, 1>{}); break;
-    case 3: e = go(Tile16<1, 2, 2, 2, kKS, 3, 1>{}); break;
-    default: e = go(Tile16<1, 2, 2, 1, kKS, 4, 1>{}); break;
+    case 0: e = go(Tile16<2, 4, 4, 2, kKS, 2, 2, false>{}); break;
+    case 1: e = go(Tile16<2, 2, 4, 2, kKS, 3, 1, false>{}); break;
+    case 2: e = go(Tile16<1, 2, 4, 2, kKS, 4, 1, true>{}); break;
+    case 3: e = go(Tile16<1, 2, 2, 2, kKS, 3, 1, true>{}); break;
+    default: e = go(Tile16<1, 2, 2, 1, kKS, 4, 1, true>{}); break;
   }
   if (e != hipSuccess || plan.slices == 1) return e;
   return launch_tile_join<GATED>({part, plan.slices, p.M, p.N, width, nullptr, p.y, p.ydt, p.gelu, p.pre}, st);
