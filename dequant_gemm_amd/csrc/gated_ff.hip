@@ -138,17 +138,17 @@ __device__ __forceinline__ f32x16 mma(const s16x8& a, const s16x8& b, const f32x
   }
 }
 
+// One workgroup's share: tile and slice `block`.
 template <class Shape, bool F16, bool AT, bool BT, bool GATED>
-__global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
+__device__ __forceinline__ void tile16(const TileParams& p, int block, unsigned char* smem) {
   constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
   constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL, KS = Shape::KS;
   constexpr int kStage = Shape::kStage, kBOff = TM * Shape::kRow;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   int im, in;
   const int tm = static_cast<int>((p.M + TM - 1) / TM), tn = static_cast<int>((p.N + TC - 1) / TC);
-  const int slice = static_cast<int>(blockIdx.x) / (tm * tn);
-  tile_place(static_cast<int>(blockIdx.x) - slice * tm * tn, tm, tn, &im, &in);
+  const int slice = block / (tm * tn);
+  tile_place(block - slice * tm * tn, tm, tn, &im, &in);
   const int64_t m0 = static_cast<int64_t>(im) * TM, n0 = static_cast<int64_t>(in) * TC;
 
   Operand<AT, TM, W, KS> A;
@@ -316,42 +316,78 @@ __global__ __launch_bounds__(64 * Shape::W) void k_tile16(TileParams p) {
   }
 }
 
-template <class Shape, bool F16, bool AT, bool BT, bool GATED>
-hipError_t launch_shape(const TileParams& p, hipStream_t st) {
-  auto kern = k_tile16<Shape, F16, AT, BT, GATED>;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
-  if (e != hipSuccess) return e;
-  constexpr int TC = GATED ? Shape::TN / 2 : Shape::TN;
-  const int64_t tiles = ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + TC - 1) / TC) * p.slices;
-  if (tiles * 64 * Shape::W >= int64_t{1} << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tiles)), dim3(64 * Shape::W), Shape::kLds, st, p);
-  return hipGetLastError();
+template <class Shape, bool F16>
+__global__ __launch_bounds__(64 * Shape::W) void k_ff_forward(TileParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  tile16<Shape, F16, false, false, true>(p, static_cast<int>(blockIdx.x), smem);
 }
 
-constexpr int kKS = 4;                         // of every shape: a stage's steps
-TilePlan plan16(int64_t M, int64_t width, int64_t K) { return plan_tiles(M, width, (K + 16 * kKS - 1) / (16 * kKS), kKS / 2); }
-
-// part: scratch of plan_bytes (several slices)
-template <bool AT, bool BT, bool GATED>
-hipError_t launch_tile16(TileParams p, bool f16, float* part, hipStream_t st) {
-  const int64_t width = GATED ? 2 * p.N : p.N;
-  const TilePlan plan = plan16(p.M, width, p.K);
-  p.slices = plan.slices;
-  p.part = part;
-  auto go = [&](auto shape) {
-    using Shape = decltype(shape);
-    return f16 ? launch_shape<Shape, true, AT, BT, GATED>(p, st) : launch_shape<Shape, false, AT, BT, GATED>(p, st);
-  };
-  hipError_t e;
-  switch (plan.shape) {
-    case 0: e = go(Tile16<2, 4, 4, 2, kKS, 2, 2, false>{}); break;
-    case 1: e = go(Tile16<2, 2, 4, 2, kKS, 3, 1, false>{}); break;
-    case 2: e = go(Tile16<1, 2, 4, 2, kKS, 4, 1, true>{}); break;
-    case 3: e = go(Tile16<1, 2, 2, 2, kKS, 3, 1, true>{}); break;
-    default: e = go(Tile16<1, 2, 2, 1, kKS, 4, 1, true>{}); break;
+// The backward pass's two products in one launch, so that the compute units that the first one
+// leaves idle take up the second: dx = dpre w (its first workgroups), dw = dpre^T x.
+template <class Shape, bool F16>
+__global__ __launch_bounds__(64 * Shape::W) void k_ff_backward(TileParams dx, TileParams dw, int first) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < first) {
+    tile16<Shape, F16, false, true, false>(dx, block, smem);
+  } else {
+    tile16<Shape, F16, true, true, false>(dw, block - first, smem);
   }
-  if (e != hipSuccess || plan.slices == 1) return e;
-  return launch_tile_join<GATED>({part, plan.slices, p.M, p.N, width, nullptr, p.y, p.ydt, p.gelu, p.pre}, st);
+}
+
+constexpr int kKS = 4;                         // a stage's steps, in every shape
+// f(shape) with shape k of kTileShapes
+template <class F>
+hipError_t with_shape(int k, F f) {
+  switch (k) {
+    case 0: return f(Tile16<2, 4, 4, 2, kKS, 2, 2, false>{});
+    case 1: return f(Tile16<2, 2, 4, 2, kKS, 3, 1, false>{});
+    case 2: return f(Tile16<1, 2, 4, 2, kKS, 4, 1, true>{});
+    case 3: return f(Tile16<1, 2, 2, 2, kKS, 3, 1, true>{});
+    default: return f(Tile16<1, 2, 2, 1, kKS, 4, 1, true>{});
+  }
+}
+
+int64_t stages16(int64_t K) { return (K + 16 * kKS - 1) / (16 * kKS); }
+TilePlan plan_forward(int64_t M, int64_t H, int64_t I) { return plan_tiles(M, 2 * I, stages16(H), kKS / 2); }
+
+// Both products in one launch, where they share a shape and fill each other's rounds, or each
+// in its own. Does not depend on which of them is asked for, and so neither do the results.
+struct BackwardPlan {
+  TilePlan dx, dw;
+  bool together;
+};
+BackwardPlan plan_backward(int64_t M, int64_t H, int64_t I) {
+  const int64_t cu = plan_cus(), sx = stages16(2 * I), sw = stages16(M), unit = kKS / 2;
+  BackwardPlan one{}, two{};
+  int64_t cost1 = INT64_MAX, costx = INT64_MAX, costw = INT64_MAX;
+  for (int k = 0; k < kTileShapeCount; ++k) {
+    int64_t cx, cw;
+    const TilePlan x = plan_shape(k, M, H, sx, unit, &cx), w = plan_shape(k, 2 * I, H, sw, unit, &cw);
+    if (cx < costx) {
+      costx = cx;
+      two.dx = x;
+    }
+    if (cw < costw) {
+      costw = cw;
+      two.dw = w;
+    }
+    const int64_t nx = plan_tile_count(k, M, H) * x.slices, nw = plan_tile_count(k, 2 * I, H) * w.slices;
+    const int64_t tx = plan_workgroup(k, (sx + x.slices - 1) / x.slices, unit), tw = plan_workgroup(k, (sw + w.slices - 1) / w.slices, unit);
+    // workgroups follow each other without waiting for a round; the last ones run half alone
+    const int64_t longest = std::max(tx, tw);
+    const int64_t c = std::max(longest, (nx * tx + nw * tw) / cu + longest / 2) + plan_join(x.slices, M, H) + plan_join(w.slices, 2 * I, H);
+    if (c < cost1) {
+      cost1 = c;
+      one = {x, w, true};
+    }
+  }
+  return cost1 <= costx + costw + 4000 ? one : two;    // 4000: a launch
+}
+
+template <class Shape>
+int64_t tile_count(const TileParams& p, int64_t columns) {
+  return ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + columns - 1) / columns) * p.slices;
 }
 
 // [dg | du] from pre and dh, in the operands' type: the products that follow take 16-bit
@@ -386,12 +422,12 @@ unsigned quad_grid(int64_t M, int64_t I) {
 }  // namespace
 
 size_t gated_ff_part_bytes(int64_t M, int64_t H, int64_t I) {
-  return M <= kFewMaxM ? 0 : plan_bytes(plan16(M, 2 * I, H), M, 2 * I);
+  return M <= kFewMaxM ? 0 : plan_bytes(plan_forward(M, H, I), M, 2 * I);
 }
 
-// dx and dw run one after the other and share the scratch
 size_t gated_ff_backward_part_bytes(int64_t M, int64_t H, int64_t I) {
-  return std::max(plan_bytes(plan16(M, H, 2 * I), M, H), plan_bytes(plan16(2 * I, H, M), 2 * I, H));
+  const BackwardPlan plan = plan_backward(M, H, I);
+  return plan_bytes(plan.dx, M, H) + plan_bytes(plan.dw, 2 * I, H);
 }
 
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
@@ -410,24 +446,60 @@ hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
     const bool whole = p.M <= kFewWholeM && 2 * p.H <= kFewWholeBytes;
     return p.f16 ? launch_few<kFewF16, true>(f, whole, false, st) : launch_few<kFewBf16, true>(f, whole, false, st);
   }
-  return launch_tile16<false, false, true>({p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, dt, p.pre, p.gelu, 1, nullptr}, p.f16, p.part, st);
+  const TilePlan plan = plan_forward(p.M, p.H, p.I);
+  const TileParams t{p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, dt, p.pre, p.gelu, plan.slices, p.part};
+  const hipError_t e = with_shape(plan.shape, [&](auto shape) {
+    using Shape = decltype(shape);
+    auto kern = p.f16 ? k_ff_forward<Shape, true> : k_ff_forward<Shape, false>;
+    const int64_t grid = tile_count<Shape>(t, Shape::TN / 2);
+    if (grid * 64 * Shape::W >= int64_t{1} << 32) return hipErrorInvalidValue;
+    const hipError_t l = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
+    if (l != hipSuccess) return l;
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * Shape::W), Shape::kLds, st, t);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || plan.slices == 1) return e;
+  return launch_tile_join<true>({p.part, plan.slices, p.M, p.I, 2 * p.I, nullptr, p.h, dt, p.gelu, p.pre}, st);
 }
 
 hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
-  const unsigned grid = quad_grid(p.M, p.I);
+  const unsigned quads = quad_grid(p.M, p.I);
   if (p.f16) {
-    hipLaunchKernelGGL(k_ff_dpre<true>, dim3(grid), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
+    hipLaunchKernelGGL(k_ff_dpre<true>, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
   } else {
-    hipLaunchKernelGGL(k_ff_dpre<false>, dim3(grid), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
+    hipLaunchKernelGGL(k_ff_dpre<false>, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int dt = p.f16 ? 2 : 1;
-  if (p.dx) {
-    e = launch_tile16<false, true, false>({p.dpre, p.w, 2 * p.I, p.H, p.M, p.H, 2 * p.I, p.dx, dt, nullptr, 0, 1, nullptr}, p.f16, p.part, st);
-    if (e != hipSuccess) return e;
+  const BackwardPlan plan = plan_backward(p.M, p.H, p.I);
+  float* part = p.part;
+  float* part_w = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + plan_bytes(plan.dx, p.M, p.H));
+  const TileParams x{p.dpre, p.w, 2 * p.I, p.H, p.M, p.H, 2 * p.I, p.dx, dt, nullptr, 0, plan.dx.slices, part};
+  const TileParams w{p.dpre, p.x, 2 * p.I, p.H, 2 * p.I, p.H, p.M, p.dw, dt, nullptr, 0, plan.dw.slices, part_w};
+  auto launch = [&](int shape_index, bool with_x, bool with_w) {
+    if (!with_x && !with_w) return hipSuccess;
+    return with_shape(shape_index, [&](auto shape) {
+      using Shape = decltype(shape);
+      auto kern = p.f16 ? k_ff_backward<Shape, true> : k_ff_backward<Shape, false>;
+      const int64_t first = with_x ? tile_count<Shape>(x, Shape::TN) : 0, grid = first + (with_w ? tile_count<Shape>(w, Shape::TN) : 0);
+      if (grid * 64 * Shape::W >= int64_t{1} << 32) return hipErrorInvalidValue;
+      const hipError_t l = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
+      if (l != hipSuccess) return l;
+      hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * Shape::W), Shape::kLds, st, x, w, static_cast<int>(first));
+      return hipGetLastError();
+    });
+  };
+  if (plan.together) {
+    e = launch(plan.dx.shape, p.dx != nullptr, p.dw != nullptr);
+  } else {
+    e = launch(plan.dx.shape, p.dx != nullptr, false);
+    if (e == hipSuccess) e = launch(plan.dw.shape, false, p.dw != nullptr);
   }
-  if (p.dw) e = launch_tile16<true, true, false>({p.dpre, p.x, 2 * p.I, p.H, 2 * p.I, p.H, p.M, p.dw, dt, nullptr, 0, 1, nullptr}, p.f16, p.part, st);
+  if (e == hipSuccess && p.dx && plan.dx.slices > 1)
+    e = launch_tile_join<false>({part, plan.dx.slices, p.M, p.H, p.H, nullptr, p.dx, dt, 0, nullptr}, st);
+  if (e == hipSuccess && p.dw && plan.dw.slices > 1)
+    e = launch_tile_join<false>({part_w, plan.dw.slices, 2 * p.I, p.H, p.H, nullptr, p.dw, dt, 0, nullptr}, st);
   return e;
 }
 

@@ -151,31 +151,50 @@ struct TilePlan {
   int shape, slices;       // of kTileShapes
 };
 constexpr int kTileShapes[][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 128}, {64, 64}};
-constexpr int kMaxSlices = 32;
+constexpr int kTileShapeCount = 5, kMaxSlices = 32;
 
-// The plan of least time for M rows, `width` columns of operand B and `stages` steps of the
-// contraction of 64 `unit` bytes, by a simple model in cycles: rounds of workgroups over the
-// compute units, each its stages (the larger of MFMA and LDS-fill cycles, and a barrier) and
-// its start and end; slices cost the join's launch and their bytes. No slice is empty.
+// What the plans go by, in cycles: a workgroup's time in shape k over `len` steps of 64 `unit`
+// bytes of the contraction, the larger of its MFMA and its LDS and load cycles as measured
+// (1.55 and 2.2 times the peaks': 256 x 256 tiles 3200 a step of 128 bytes, 128 x 128 1200, 64 x
+// 128 650 to 900), and its start and end (17000 and 8000 measured for the first two).
+inline int64_t plan_workgroup(int k, int64_t len, int64_t unit) {
+  const int64_t tm = kTileShapes[k][0], tn = kTileShapes[k][1];
+  return len * (std::max(tm * tn * 99 / 4096, (tm + tn) * 11 / 5) * unit + 64) + 5000 + tm * tn / 6;
+}
+inline int64_t plan_tile_count(int k, int64_t M, int64_t width) {
+  return ((M + kTileShapes[k][0] - 1) / kTileShapes[k][0]) * ((width + kTileShapes[k][1] - 1) / kTileShapes[k][1]);
+}
+inline int64_t plan_cus() { return device_cu_count() > 0 ? device_cu_count() : 256; }
+// The join's launch and the slices' bytes.
+inline int64_t plan_join(int slices, int64_t M, int64_t width) { return slices > 1 ? 5000 + M * width * 8 * slices / 1700 : 0; }
+
+// The slices of least time for shape k, M rows, `width` columns of operand B and `stages` steps:
+// rounds of workgroups over the compute units, and the join. No slice is empty.
+inline TilePlan plan_shape(int k, int64_t M, int64_t width, int64_t stages, int64_t unit, int64_t* cost) {
+  const int64_t cu = plan_cus(), tiles = plan_tile_count(k, M, width);
+  TilePlan best{k, 1};
+  *cost = INT64_MAX;
+  for (int s = 1; s <= kMaxSlices; ++s) {
+    if (s > 1 && (stages * unit < 4 * s || tiles * s > 2 * cu)) break;
+    const int64_t len = (stages + s - 1) / s;
+    if (len * (s - 1) >= stages) continue;
+    const int64_t c = (tiles * s + cu - 1) / cu * plan_workgroup(k, len, unit) + plan_join(s, M, width);
+    if (c < *cost) {
+      *cost = c;
+      best.slices = s;
+    }
+  }
+  return best;
+}
 inline TilePlan plan_tiles(int64_t M, int64_t width, int64_t stages, int64_t unit) {
-  const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256;
-  TilePlan best{0, 1};
+  TilePlan best{};
   int64_t cost = INT64_MAX;
-  for (int k = 0; k < 5; ++k) {
-    const int64_t tm = kTileShapes[k][0], tn = kTileShapes[k][1];
-    const int64_t tiles = ((M + tm - 1) / tm) * ((width + tn - 1) / tn);
-    const int64_t per = std::max(tm * tn / 64, tm + tn) * unit + 64;
-    for (int s = 1; s <= kMaxSlices; ++s) {
-      if (s > 1 && (stages * unit < 4 * s || tiles * s > 2 * cu)) break;
-      const int64_t len = (stages + s - 1) / s;
-      if (len * (s - 1) >= stages) continue;
-      const int64_t rounds = (tiles * s + cu - 1) / cu;
-      int64_t c = rounds * (len * per + 3000);
-      if (s > 1) c += 5000 + M * width * 8 * s / 1700;
-      if (c < cost) {
-        cost = c;
-        best = {k, s};
-      }
+  for (int k = 0; k < kTileShapeCount; ++k) {
+    int64_t c;
+    const TilePlan t = plan_shape(k, M, width, stages, unit, &c);
+    if (c < cost) {
+      cost = c;
+      best = t;
     }
   }
   return best;
