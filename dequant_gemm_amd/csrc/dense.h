@@ -17,17 +17,45 @@ __device__ __forceinline__ uint32_t fp8_pack2(float a, float b, uint32_t old) {
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, static_cast<int>(old), HI));
 }
 
+// A block's scale with its reciprocal, correctly rounded (one Newton step from the hardware's,
+// except where the scale's significand is all ones).
+struct Fp8Scale {
+  float s, r;
+  bool fast;
+};
+__device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
+  Fp8Scale v;
+  v.s = fp8_scale(amax);
+  const float r = __builtin_amdgcn_rcpf(v.s);
+  v.r = fmaf(fmaf(-v.s, r, 1.0f), r, r);
+  v.fast = v.s >= 0x1p-80f && v.s <= 0x1p100f && (__float_as_uint(v.s) & 0x7fffffu) != 0x7fffffu;
+  return v;
+}
+
 // The codes of eight 16-bit values: e4m3(fp32(x / s)), at most 448 in magnitude; s = 0 gives
-// zeros, a NaN stays one (the comparisons below pass it on).
+// zeros, a NaN stays one (the comparisons below pass it on). The quotient without a division:
+// q = fl(x r) is within an ulp, its residual x - q s is exact in one fma, and fl(q + residual r)
+// is the correctly rounded quotient (Markstein; equal to the division for every pair of
+// significands of a scale and a 16-bit value). Scales outside [2^-80, 2^100], where the residual
+// might not be exact, take the division. Rounding 448 (1 + 2^-24) to e4m3 gives 448 by itself.
+// 4096 x 7168 rows: 28.7 us with divisions, 19 us so.
 template <bool XF16>
-__device__ __forceinline__ uint2 fp8_quant8(const u32x4& v, float s) {
+__device__ __forceinline__ uint2 fp8_quant8(const u32x4& v, const Fp8Scale& scale) {
   float f[8];
   unpack8<XF16>(v, f);
+  if (scale.fast) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float t = s != 0.0f ? __fdiv_rn(f[i], s) : 0.0f;
-    t = t > kE4m3Max ? kE4m3Max : t;
-    f[i] = t < -kE4m3Max ? -kE4m3Max : t;
+    for (int i = 0; i < 8; ++i) {
+      const float q = f[i] * scale.r;
+      f[i] = fmaf(fmaf(-q, scale.s, f[i]), scale.r, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float t = scale.s != 0.0f ? __fdiv_rn(f[i], scale.s) : 0.0f;
+      t = t > kE4m3Max ? kE4m3Max : t;
+      f[i] = t < -kE4m3Max ? -kE4m3Max : t;
+    }
   }
   return make_uint2(fp8_pack2<true>(f[2], f[3], fp8_pack2<false>(f[0], f[1], 0u)),
                     fp8_pack2<true>(f[6], f[7], fp8_pack2<false>(f[4], f[5], 0u)));

@@ -182,11 +182,11 @@ __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
           float a = absmax8<XF16, true>(v[m], 0.0f);
 #pragma unroll
           for (int d = 8; d >= 1; d >>= 1) a = larger<true>(a, __shfl_xor(a, d, 64));
-          const float s = fp8_scale(a);
+          const Fp8Scale s = fp8_scale_of(a);
           // eight codes: half a piece; past K up to the last step's end zeros
           if (vec < nsteps * 8)
             *reinterpret_cast<uint2*>(smem + place(vec >> 3, m, (vec >> 1) & 3) + 8 * (vec & 1)) = fp8_quant8<XF16>(v[m], s);
-          if ((tid & 15) == 0 && (vec >> 4) < kb) const_cast<float*>(whole_scales)[4 * (vec >> 4) + m] = s;
+          if ((tid & 15) == 0 && (vec >> 4) < kb) const_cast<float*>(whole_scales)[4 * (vec >> 4) + m] = s.s;
         }
       }
     }
@@ -352,7 +352,12 @@ hipError_t launch_few(FewParams p, bool whole, bool xf16, hipStream_t st) {
   auto go = [&](auto mt_c, auto whole_c, auto xf16_c) {
     constexpr int MT = decltype(mt_c)::value;
     constexpr bool WHOLE = decltype(whole_c)::value, XF16 = decltype(xf16_c)::value;
-    return nt == 1 ? launch_few_k<KIND, MT, 1, WHOLE, GATED, XF16>(p, st) : launch_few_k<KIND, MT, 2, WHOLE, GATED, XF16>(p, st);
+    // (e4m3 operands of two tiles by more rows than this go to the tile kernel: registers)
+    constexpr bool kTwo = !F8 || MT == 1 || (MT == 2 && KIND == kFewFp8);
+    if constexpr (kTwo) {
+      if (nt == 2) return launch_few_k<KIND, MT, 2, WHOLE, GATED, XF16>(p, st);
+    }
+    return nt == 1 ? launch_few_k<KIND, MT, 1, WHOLE, GATED, XF16>(p, st) : hipErrorInvalidValue;
   };
   using One = std::integral_constant<int, 1>;
   if (whole) {

@@ -38,9 +38,9 @@ __global__ __launch_bounds__(256) void k_quant_fp8_rows(const uint16_t* __restri
     const int64_t k = b * 128 + 8 * (threadIdx.x & 15);
     const bool on = k < K;
     const u32x4 v = on ? *reinterpret_cast<const u32x4*>(x + m * K + k) : u32x4{0u, 0u, 0u, 0u};
-    const float s = fp8_scale(larger16(absmax8<XF16, true>(v, 0.0f)));
+    const Fp8Scale s = fp8_scale_of(larger16(absmax8<XF16, true>(v, 0.0f)));
     if (on) *reinterpret_cast<uint2*>(xq + m * K + k) = fp8_quant8<XF16>(v, s);
-    if ((threadIdx.x & 15) == 0) xs[g] = s;
+    if ((threadIdx.x & 15) == 0) xs[g] = s.s;
   }
 }
 
@@ -64,14 +64,14 @@ __global__ __launch_bounds__(256) void k_quant_fp8_blocks(const uint16_t* __rest
     a = wave_larger<true>(a);
     if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = a;
     __syncthreads();
-    const float s = fp8_scale(larger<true>(larger<true>(s_max[0], s_max[1]), larger<true>(s_max[2], s_max[3])));
+    const Fp8Scale s = fp8_scale_of(larger<true>(larger<true>(s_max[0], s_max[1]), larger<true>(s_max[2], s_max[3])));
     __syncthreads();                           // read before the next block's are written
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t m = mb * 128 + 16 * i + (threadIdx.x >> 4);
       if (m < M && k < K) *reinterpret_cast<uint2*>(xq + m * K + k) = fp8_quant8<XF16>(v[i], s);
     }
-    if (threadIdx.x == 0) xs[at] = s;
+    if (threadIdx.x == 0) xs[at] = s.s;
   }
 }
 
@@ -379,19 +379,32 @@ FewParams few_params(const Fp8Params& p, bool gated) {
 }
 }  // namespace
 
-size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewMaxM ? 0 : plan_bytes(plan8(M, N, K), M, N); }
+// Rows that the streaming kernel takes. Measured against the tiles (N x K, 16-bit results, us): 16
+// rows 6144 x 7168 12.2 against 14.1, 32 rows 15.1 against 14.1, 7168 x 2048 7.8 against 8.8; 64
+// rows 4096 x 4096 11.2 against 11.1, 1003 x 1936 7.6 against 9.8, 1024 x 8192 15.3 against 11.9,
+// 6144 x 7168 27.5 against 15.0. fp32 results, 32 rows, 6144 x 7168: 19.1 against 16.7. wide: a
+// workgroup would have two tiles of weight rows.
+constexpr int64_t kFewAlways = 16;
+static bool fp8_few(const Fp8Params& p, bool gated) {
+  const bool wide = p.N > 16 * plan_cus();
+  if (p.M <= kFewAlways) return true;
+  if (p.M <= 32) return !(wide && p.ydt == 0 && !gated);
+  return p.M <= kFewMaxM && !wide && p.K <= 4096;
+}
+
+size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewAlways ? 0 : plan_bytes(plan8(M, N, K), M, N); }
 
 bool fp8_quantises(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
 
 hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st) {
-  if (p.M > kFewMaxM) return launch_fp8_tiles<false>(p, st);
+  if (!fp8_few(p, false)) return launch_fp8_tiles<false>(p, st);
   const FewParams f = few_params(p, false);
   return p.ydt == 0 ? launch_few<kFewFp8Exact, false>(f, p.x != nullptr, xf16, st)
                     : launch_few<kFewFp8, false>(f, p.x != nullptr, xf16, st);
 }
 
 hipError_t launch_fp8_gated(const Fp8Params& p, bool xf16, hipStream_t st) {
-  if (p.M > kFewMaxM) return launch_fp8_tiles<true>(p, st);
+  if (!fp8_few(p, true)) return launch_fp8_tiles<true>(p, st);
   return launch_few<kFewFp8, true>(few_params(p, true), p.x != nullptr, xf16, st);
 }
 
