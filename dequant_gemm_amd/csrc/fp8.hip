@@ -164,14 +164,14 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
     const uint32_t k = 128u * static_cast<uint32_t>(s0 + s);
     const bool on = k + lane_k < K;
     if (i < LA) {
-      tile_load_lds(p.xq + m0 * p.K, arows * K, st + 1024 * W * i, on ? base + k + 8u * W * i * K : kPast);
+      tile_load_lds<0>(tile_lds_rsrc(p.xq + m0 * p.K, arows * K), tile_lds_at(st + 1024 * W * i), on ? base + k + 8u * W * i * K : kPast, 0);
     } else {
-      tile_load_lds(bp[i - LA], brows * K, st + kBOff + 1024 * W * (i - LA), on ? boff[i - LA] + k : kPast);
+      tile_load_lds<0>(tile_lds_rsrc(bp[i - LA], brows * K), tile_lds_at(st + kBOff + 1024 * W * (i - LA)), on ? boff[i - LA] + k : kPast, 0);
     }
   };
   auto load_scale = [&](int s) {
     if (wave <= TM / 64)
-      tile_load_lds4(sp, sbytes, stage_at(s) + kSOff + 256 * wave, s < S ? soff + 4u * static_cast<uint32_t>(s0 + s) : kPast);
+      tile_load_lds4<0>(tile_lds_rsrc(sp, sbytes), tile_lds_at(stage_at(s) + kSOff + 256 * wave), s < S ? soff + 4u * static_cast<uint32_t>(s0 + s) : kPast, 0);
   };
 
   const int wm = wave / WN, wn = wave % WN;

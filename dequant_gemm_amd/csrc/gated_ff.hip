@@ -59,34 +59,47 @@ template <bool T, int ROWS, int W, int KS>
 struct Operand {
   static constexpr int kParts = T ? ROWS / 8 : 2 * KS;           // 16-byte parts of a row
   static constexpr int kPer = 64 / kParts;                       // rows of a wave's load
-  const uint16_t* p;                           // first row, or with T first column
-  int64_t ld;
-  uint32_t bytes;                              // that the resource covers
-  uint32_t lane_off, step, lane_k, place;
+  static constexpr int L = ROWS * 32 * KS / 1024 / W;            // pieces of a wave and stage
+  u32x4 rsrc[L];                               // one, but for gate and up rows
+  uint32_t voff[L], soff, inc;                 // a lane's offsets, the stage's on top
+  uint32_t lane_k;
   int K;
-  bool on_col;
 
-  __device__ __forceinline__ void init(const uint16_t* base, int64_t ld_, int64_t row0, int64_t rows, int64_t K_, int wave) {
+  // from stage s0 on
+  __device__ __forceinline__ void init(const uint16_t* base, int64_t ld, int64_t row0, int64_t rows, int64_t K_, int wave, int s0) {
     const int lane = threadIdx.x & 63;
-    ld = ld_;
     K = static_cast<int>(K_);
     const int row = kPer * wave + lane / kParts, at = lane % kParts;
-    if constexpr (T) {
-      p = base + row0;
-      const int part = ((at >> 2) ^ swizzle(row)) * 4 + (at & 3);
-      lane_k = static_cast<uint32_t>(row);
-      lane_off = static_cast<uint32_t>(row) * static_cast<uint32_t>(2 * ld) + 16u * part;
-      on_col = 8 * part < rows - row0;         // rows a multiple of 8
-      bytes = 16u * KS * static_cast<uint32_t>(2 * ld);
-    } else {
-      p = base + row0 * ld;
-      lane_k = 16u * (at ^ swizzle(row));
-      lane_off = static_cast<uint32_t>(row) * static_cast<uint32_t>(2 * ld) + lane_k;
-      on_col = true;
-      bytes = static_cast<uint32_t>(min(static_cast<int64_t>(ROWS), rows - row0)) * static_cast<uint32_t>(2 * ld);
+    const uint32_t ld2 = static_cast<uint32_t>(2 * ld);
+#pragma unroll
+    for (int g = 0; g < L; ++g) {
+      if constexpr (T) {
+        const int part = ((at >> 2) ^ swizzle(row)) * 4 + (at & 3);
+        lane_k = static_cast<uint32_t>(row);
+        voff[g] = 8 * part < rows - row0 ? static_cast<uint32_t>(row + kPer * W * g) * ld2 + 16u * part : kPast;   // rows a multiple of 8
+        rsrc[g] = tile_lds_rsrc(base + row0 + static_cast<int64_t>(s0) * (16 * KS) * ld, 16u * KS * ld2);
+      } else {
+        lane_k = 16u * (at ^ swizzle(row));
+        voff[g] = static_cast<uint32_t>(row + kPer * W * g) * ld2 + lane_k;
+        rsrc[g] = tile_lds_rsrc(base + row0 * ld, static_cast<uint32_t>(min(static_cast<int64_t>(ROWS), rows - row0)) * ld2);
+      }
     }
-    step = static_cast<uint32_t>(kPer * W) * static_cast<uint32_t>(2 * ld);
-    place = 1024u * wave;
+    soff = T ? 0u : 32u * KS * static_cast<uint32_t>(s0);
+    inc = T ? 16u * KS * ld2 : 32u * KS;
+  }
+  // Blocks of 32 rows are gate rows and up rows (`rows` further on) in turn, so that a wave
+  // holds both of a column; row0 and rows count columns.
+  __device__ __forceinline__ void init_gated(const uint16_t* base, int64_t ld, int64_t row0, int64_t rows, int64_t K_, int wave, int s0) {
+    static_assert(!T);
+    init(base, ld, row0, rows, K_, wave, s0);
+    const int lane = threadIdx.x & 63;
+    const uint32_t ld2 = static_cast<uint32_t>(2 * ld);
+#pragma unroll
+    for (int g = 0; g < L; ++g) {
+      const int row = kPer * (W * g + wave), blk = row >> 5;
+      rsrc[g] = tile_lds_rsrc(base + ((blk & 1) * rows + row0) * ld, static_cast<uint32_t>(min(static_cast<int64_t>(ROWS / 2), rows - row0)) * ld2);
+      voff[g] = static_cast<uint32_t>(32 * (blk >> 1) + (row & 31) + lane / kParts) * ld2 + lane_k;
+    }
   }
   // The order of a row's parts: any 16 rows read at one part hit all banks. T: the order of
   // its 64-byte segments: four k rows read at one segment hit all banks.
@@ -98,36 +111,70 @@ struct Operand {
       return KS == 4 ? (row >> 1) & 7 : (row >> 2) & 3;
     }
   }
-  // where piece g of stage s begins; past K and past the tile there is nothing to load
-  __device__ __forceinline__ uint32_t offset(int s, int g) const {
-    if constexpr (T) {
-      return on_col && 16 * KS * s + static_cast<int>(lane_k) + kPer * W * g < K ? lane_off + step * g : kPast;
-    } else {
-      return 32u * KS * s + lane_k < 2u * static_cast<uint32_t>(K) ? lane_off + 32u * KS * s + step * g : kPast;
+  // Before the loads of stage s, which is not whole or behind the last one: what lies past K is
+  // not read (and nothing of the stages that follow, in which it lies past K too).
+  __device__ __forceinline__ void cut(int s) {
+#pragma unroll
+    for (int g = 0; g < L; ++g) {
+      const bool past = T ? 16 * KS * s + static_cast<int>(lane_k) + kPer * W * g >= K : 32u * KS * s + lane_k >= 2u * static_cast<uint32_t>(K);
+      voff[g] = past ? kPast : voff[g];
     }
   }
-  __device__ __forceinline__ const uint16_t* first(int s) const { return T ? p + static_cast<int64_t>(s) * (16 * KS) * ld : p; }
+  // after a stage's loads
+  __device__ __forceinline__ void next() {
+    if constexpr (T) {
+#pragma unroll
+      for (int g = 0; g < L; ++g) {
+        const uint64_t at = (static_cast<uint64_t>(rsrc[g][1]) << 32 | rsrc[g][0]) + inc;
+        rsrc[g][0] = static_cast<uint32_t>(at);
+        rsrc[g][1] = static_cast<uint32_t>(at >> 32);
+      }
+    } else {
+      soff += inc;
+    }
+  }
 };
 
-// Fragments of block `blk` (32 rows) for k 16 ks .. + 15 of a stage: lane l has row l % 32 and
-// eight k from 8 (l / 32) on.
-template <bool T, int ROWS, int KS>
-__device__ __forceinline__ s16x8 fragment(const unsigned char* st, int blk, int ks) {
-  const int lane = threadIdx.x & 63;
-  if constexpr (T) {
-    // four k rows of 16 columns at a time come transposed out of LDS
-    typedef __attribute__((address_space(3))) s16x4* LdsPtr;
-    const int grp = lane >> 4, kr = (lane & 15) >> 2;
-    const int kk = 16 * ks + 8 * (grp >> 1) + kr;
-    const unsigned char* at = st + kk * (2 * ROWS) + ((blk ^ Operand<true, ROWS, 1, KS>::swizzle(kr)) << 6) + 32 * (grp & 1) + 8 * (lane & 3);
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + 4 * (2 * ROWS)));
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  } else {
-    const int c = lane & 31, h = lane >> 5;
-    return *reinterpret_cast<const s16x8*>(st + (32 * blk + c) * (32 * KS) + (((2 * ks + h) ^ Operand<false, ROWS, 1, KS>::swizzle(c)) << 4));
+// Fragments of a wave's blocks of 32 rows, for k 16 ks .. + 15 of a stage: lane l has row l % 32
+// and eight k from 8 (l / 32) on. Their addresses in LDS are made once for every slot of the
+// ring: one for each step, or with T for each block.
+template <bool T, int ROWS, int KS, int BLOCKS, int SLOTS>
+struct Fragments {
+  static constexpr int kAddr = T ? BLOCKS : KS;
+  uint32_t at[SLOTS][kAddr];
+
+  __device__ __forceinline__ void init(uint32_t lds, int stage, int first) {   // the wave's first block
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+      for (int n = 0; n < kAddr; ++n) {
+        uint32_t v = lds + static_cast<uint32_t>(s * stage);
+        if constexpr (T) {
+          // four k rows of 16 columns at a time come transposed out of LDS
+          const int grp = lane >> 4, kr = (lane & 15) >> 2;
+          v += (8 * (grp >> 1) + kr) * (2 * ROWS) + (((first + n) ^ Operand<true, ROWS, 1, KS>::swizzle(kr)) << 6) + 32 * (grp & 1) + 8 * (lane & 3);
+        } else {
+          const int c = lane & 31, h = lane >> 5;
+          v += (32 * first + c) * (32 * KS) + (((2 * n + h) ^ Operand<false, ROWS, 1, KS>::swizzle(c)) << 4);
+        }
+        asm("" : "+v"(v));                     // kept, instead of an addition beside every read
+        at[s][n] = v;
+      }
   }
-}
+  __device__ __forceinline__ s16x8 read(int slot, int ks, int i) const {
+    if constexpr (T) {
+      typedef __attribute__((address_space(3))) s16x4* LdsPtr;
+      const uint32_t a = at[slot][i] + 16 * ks * (2 * ROWS);
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(a));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(a + 4 * (2 * ROWS)));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      typedef __attribute__((address_space(3))) s16x8* LdsPtr;
+      return *(LdsPtr)(at[slot][ks] + 32 * i * (32 * KS));
+    }
+  }
+};
 
 template <bool F16>
 __device__ __forceinline__ f32x16 mma(const s16x8& a, const s16x8& b, const f32x16& c) {
@@ -151,46 +198,62 @@ __device__ __forceinline__ void tile16(const TileParams& p, int block, unsigned 
   tile_place(block - slice * tm * tn, tm, tn, &im, &in);
   const int64_t m0 = static_cast<int64_t>(im) * TM, n0 = static_cast<int64_t>(in) * TC;
 
-  Operand<AT, TM, W, KS> A;
-  A.init(p.a, p.lda, m0, p.M, p.K, wave);
-  Operand<BT, TN, W, KS> B;
-  // gated: blocks of 32 rows are gate and up in turn, so that a wave holds both of a column
-  uint32_t gated_off[GATED ? LB : 1];
-  const uint16_t* gated_p[GATED ? LB : 1];
-  uint32_t gated_bytes = 0;
-  B.init(p.b, p.ldb, n0, p.N, p.K, wave);
-  if constexpr (GATED) {
-    const int lane = threadIdx.x & 63;
-    gated_bytes = static_cast<uint32_t>(min(static_cast<int64_t>(TC), p.N - n0)) * static_cast<uint32_t>(2 * p.ldb);
-#pragma unroll
-    for (int g = 0; g < LB; ++g) {
-      const int row = B.kPer * (W * g + wave), blk = row >> 5;
-      gated_p[g] = p.b + ((blk & 1) * p.N + n0) * p.ldb;
-      gated_off[g] = static_cast<uint32_t>(32 * (blk >> 1) + (row & 31) + lane / B.kParts) * static_cast<uint32_t>(2 * p.ldb) + B.lane_k;
-    }
-  }
   const int all = static_cast<int>((p.K + 16 * KS - 1) / (16 * KS)), len = (all + p.slices - 1) / p.slices;
   const int s0 = slice * len, S = min(all - s0, len);   // stages s0 .. s0 + S - 1
+  const int whole = static_cast<int>(p.K / (16 * KS)) - s0;   // of this slice's, those that are whole
+  Operand<AT, TM, W, KS> A;
+  A.init(p.a, p.lda, m0, p.M, p.K, wave, s0);
+  Operand<BT, TN, W, KS> B;
+  if constexpr (GATED) {
+    B.init_gated(p.b, p.ldb, n0, p.N, p.K, wave, s0);
+  } else {
+    B.init(p.b, p.ldb, n0, p.N, p.K, wave, s0);
+  }
   constexpr int kRing = Shape::kRing;
-  auto stage_at = [&](int s) { return smem + ((kRing & (kRing - 1)) ? s % kRing : s & (kRing - 1)) * kStage; };
-  auto load = [&](int s, int i) {              // piece i of stage s, straight into LDS
-    unsigned char* st = stage_at(s);
-    if (i < LA) {
-      tile_load_lds(A.first(s0 + s), A.bytes, st + A.place + 1024 * W * i, A.offset(s0 + s, i));
-    } else if constexpr (GATED) {
-      const uint32_t k = 32u * KS * static_cast<uint32_t>(s0 + s);
-      tile_load_lds(gated_p[i - LA], gated_bytes, st + kBOff + B.place + 1024 * W * (i - LA),
-                    k + B.lane_k < 2u * static_cast<uint32_t>(B.K) ? gated_off[i - LA] + k : kPast);
+  const uint32_t lds = tile_lds_at(smem) + 1024u * wave;
+  // Piece i of stage s, straight into LDS at slot SLOT of the ring. Stages and pieces come in
+  // their order.
+  auto load = [&]<int SLOT>(std::integral_constant<int, SLOT>, int s, auto i_c) {
+    constexpr int i = decltype(i_c)::value;
+    if (i == 0 && s >= whole) {
+      asm volatile("" ::: "memory");           // a branch, rarely taken, and no selects in every stage
+      A.cut(s0 + s);
+      B.cut(s0 + s);
+    }
+    if constexpr (i < LA) {
+      tile_load_lds<SLOT * kStage + 1024 * W * i>(A.rsrc[0], lds, A.voff[i], A.soff);
     } else {
-      tile_load_lds(B.first(s0 + s), B.bytes, st + kBOff + B.place + 1024 * W * (i - LA), B.offset(s0 + s, i - LA));
+      tile_load_lds<SLOT * kStage + kBOff + 1024 * W * (i - LA)>(B.rsrc[GATED ? i - LA : 0], lds, B.voff[i - LA], B.soff);
+    }
+    if constexpr (i == NL - 1) {
+      A.next();
+      B.next();
     }
   };
+  // pieces L0 .. L1 - 1
+  auto loads = [&]<int SLOT, int L0, int L1>(std::integral_constant<int, SLOT> slot, int s, std::integral_constant<int, L0>, std::integral_constant<int, L1>) {
+    [&]<int... I>(std::integer_sequence<int, I...>) {
+      (load(slot, s, std::integral_constant<int, L0 + I>{}), ...);
+    }(std::make_integer_sequence<int, L1 - L0>{});
+  };
   const int wm = wave / WN, wn = wave % WN;
-  auto read_a = [&](int s, int ks, int i) { return fragment<AT, TM, KS>(stage_at(s), wm * MB + i, ks); };
-  auto read_b = [&](int s, int ks, int j) { return fragment<BT, TN, KS>(stage_at(s) + kBOff, wn * NB + j, ks); };
+  Fragments<AT, TM, KS, MB, kRing> FA;
+  Fragments<BT, TN, KS, NB, kRing> FB;
+  FA.init(tile_lds_at(smem), kStage, wm * MB);
+  FB.init(tile_lds_at(smem) + kBOff, kStage, wn * NB);
+  auto read_a = [&](int slot, int ks, int i) { return FA.read(slot, ks, i); };
+  auto read_b = [&](int slot, int ks, int j) { return FB.read(slot, ks, j); };
 
   f32x16 acc[MB][NB] = {};
   constexpr int Q = MB * NB;
+  // f(t) for t = 0 .. N - 1, known to the compiler
+  auto times = [&]<int N>(std::integral_constant<int, N>, auto f) {
+    [&]<int... T>(std::integer_sequence<int, T...>) {
+      (f(std::integral_constant<int, T>{}), ...);
+    }(std::make_integer_sequence<int, N>{});
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using INL = std::integral_constant<int, NL>;
   if constexpr (Shape::kAhead) {
     // Stage s: its MFMAs (B times A, so that a lane's results are neighbouring columns of one
     // row) from fragments read before, spread between them the reads of the next stage's.
@@ -198,55 +261,40 @@ __device__ __forceinline__ void tile16(const TileParams& p, int block, unsigned 
     // the loads of the stage kRing behind it take its place.
     s16x8 fa[2][KS][MB], fb[2][KS][NB];
     constexpr int kReads = KS * (MB + NB), kTotal = KS * Q;
-    auto read = [&](auto to_c, int s, int r) {
+    auto read = [&](auto to_c, int slot, int r) {
       constexpr int to = decltype(to_c)::value;
       const int ks = r / (MB + NB), i = r % (MB + NB);
       if (i < MB) {
-        fa[to][ks][i] = read_a(s, ks, i);
+        fa[to][ks][i] = read_a(slot, ks, i);
       } else {
-        fb[to][ks][i - MB] = read_b(s, ks, i - MB);
+        fb[to][ks][i - MB] = read_b(slot, ks, i - MB);
       }
     };
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-#pragma unroll
-    for (int r = 0; r < kRing; ++r)
-#pragma unroll
-      for (int i = 0; i < NL; ++i) load(r, i);
+    times(std::integral_constant<int, kRing>{}, [&](auto r) { loads(r, r, I0{}, INL{}); });
     tile_wait<(kRing - 1) * NL>();
     tile_barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(I0{}, 0, r);
-    auto stage = [&](int s, auto at_c, auto to_c) {
-      constexpr int at = decltype(at_c)::value;
+    tile_stages<kRing % 2 ? 2 * kRing : kRing>(S, [&](int s, auto u_c) {
+      constexpr int u = decltype(u_c)::value, at = u % 2, slot = u % kRing, to_slot = (u + 1) % kRing;
       tile_wait<(kRing - 2) * NL>();
       tile_barrier();
-#pragma unroll
-      for (int t = 0; t < kTotal; ++t) {
-        const int ks = t / Q, q = t % Q;
-        const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
+      times(std::integral_constant<int, kTotal>{}, [&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        constexpr int ks = t / Q, q = t % Q, i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
         acc[i][j] = mma<F16>(fb[at][ks][j], fa[at][ks][i], acc[i][j]);
         // in the first three quarters, so that they have arrived at the barrier
         constexpr int kOver = kTotal * 3 / 4;
 #pragma unroll
-        for (int r = t * kReads / kOver; r < (t + 1) * kReads / kOver && r < kReads; ++r) read(to_c, s + 1, r);
-#pragma unroll
-        for (int r = t * NL / kTotal; r < (t + 1) * NL / kTotal; ++r) load(s + kRing, r);
+        for (int r = t * kReads / kOver; r < (t + 1) * kReads / kOver && r < kReads; ++r) read(std::integral_constant<int, 1 - at>{}, to_slot, r);
+        loads(std::integral_constant<int, slot>{}, s + kRing, std::integral_constant<int, t * NL / kTotal>{}, std::integral_constant<int, (t + 1) * NL / kTotal>{});
         __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    int s = 0;
-    for (; s + 1 < S; s += 2) {
-      stage(s, I0{}, I1{});
-      stage(s + 1, I1{}, I0{});
-    }
-    if (s < S) stage(s, I0{}, I1{});
+      });
+    });
   } else {
-    constexpr int SP = Shape::kSpread;           // steps over which a stage's loads are issued
-#pragma unroll
-    for (int r = 0; r < kRing; ++r)
-#pragma unroll
-      for (int i = 0; i < (r + 1 < kRing ? NL : NL / SP); ++i) load(r, i);
+    constexpr int SP = Shape::kSpread;         // steps over which a stage's loads are issued
+    times(std::integral_constant<int, kRing - 1>{}, [&](auto r) { loads(r, r, I0{}, INL{}); });
+    loads(std::integral_constant<int, kRing - 1>{}, kRing - 1, I0{}, std::integral_constant<int, NL / SP>{});
     tile_wait<(kRing - 2) * NL + NL / SP>();
     tile_barrier();
     s16x8 fa[2][MB], fb[2][NB];
@@ -255,42 +303,40 @@ __device__ __forceinline__ void tile16(const TileParams& p, int block, unsigned 
 #pragma unroll
     for (int j = 0; j < NB; ++j) fb[0][j] = read_b(0, 0, j);
 
-    // A step of 16 k: the MFMAs of its fragments (B times A, so that a lane's results are
-    // neighbouring columns of one row), spread between them the reads of the next step's.
-    // Before a stage's last step every wave has read that stage and its loads of the next one
-    // are in LDS: after the barrier that one is read, and the loads of the stage kRing behind
-    // this one take its place, from the last step on over SP steps.
-    for (int s = 0; s < S; ++s) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int f = ks & 1;
-        const int part = ks == KS - 1 ? 0 : ks + 1, to = (ks == KS - 1 ? s : s - 1) + kRing;
-        if (ks == KS - 1) {
+    // A step of 16 k: the MFMAs of its fragments, spread between them the reads of the next
+    // step's. Before a stage's last step every wave has read that stage and its loads of the
+    // next one are in LDS: after the barrier that one is read, and the loads of the stage
+    // kRing behind this one take its place, from the last step on over SP steps. While an MFMA
+    // runs its wave issues nothing else, so what counts beside them is the number of other
+    // instructions: addresses are made once, slots of the ring known to the compiler.
+    tile_stages<kRing>(S, [&](int s, auto u_c) {
+      constexpr int slot = decltype(u_c)::value, next_slot = (slot + 1) % kRing, last_slot = (slot + kRing - 1) % kRing;
+      times(std::integral_constant<int, KS * Q>{}, [&](auto t_c) {
+        constexpr int t = decltype(t_c)::value, ks = t / Q, q = t % Q, f = ks & 1;
+        constexpr int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
+        if constexpr (ks == KS - 1 && q == 0) {
           tile_wait<(kRing - 2) * NL>();
           tile_barrier();
         }
+        acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          const int i = q / NB, j = (i & 1) ? NB - 1 - q % NB : q % NB;
-          acc[i][j] = mma<F16>(fb[f][j], fa[f][i], acc[i][j]);
-#pragma unroll
-          for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
-            const int sr = ks == KS - 1 ? s + 1 : s, kr = (ks + 1) % KS;
-            if (r < MB) {
-              fa[1 - f][r] = read_a(sr, kr, r);
-            } else {
-              fb[1 - f][r - MB] = read_b(sr, kr, r - MB);
-            }
+        for (int r = q * (MB + NB) / Q; r < (q + 1) * (MB + NB) / Q; ++r) {
+          const int from = ks == KS - 1 ? next_slot : slot, kr = (ks + 1) % KS;
+          if (r < MB) {
+            fa[1 - f][r] = read_a(from, kr, r);
+          } else {
+            fb[1 - f][r - MB] = read_b(from, kr, r - MB);
           }
-          if (part < SP) {
-            const int l0 = part * NL / SP, l1 = (part + 1) * NL / SP;
-#pragma unroll
-            for (int r = l0 + q * (l1 - l0) / Q; r < l0 + (q + 1) * (l1 - l0) / Q; ++r) load(to, r);
-          }
-          __builtin_amdgcn_sched_barrier(0);
         }
-      }
-    }
+        constexpr int part = ks == KS - 1 ? 0 : ks + 1;
+        if constexpr (part < SP) {
+          constexpr int l0 = part * NL / SP, l1 = (part + 1) * NL / SP;
+          loads(std::integral_constant<int, ks == KS - 1 ? slot : last_slot>{}, (ks == KS - 1 ? s : s - 1) + kRing,
+                std::integral_constant<int, l0 + q * (l1 - l0) / Q>{}, std::integral_constant<int, l0 + (q + 1) * (l1 - l0) / Q>{});
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
   }
   tile_wait<0>();                              // loads behind the last stage
 

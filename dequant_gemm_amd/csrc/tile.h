@@ -2,6 +2,8 @@
 // order of tiles over the compute units, and the way of a tile's results through LDS.
 #pragma once
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "common.h"
 #include "dense.h"
@@ -32,16 +34,31 @@ __device__ __forceinline__ u32x4 tile_lds_rsrc(const void* p, uint32_t bytes) {
 __device__ __forceinline__ uint32_t tile_lds_at(unsigned char* lds) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(lds)));
 }
-__device__ __forceinline__ void tile_load_lds(const void* p, uint32_t bytes, unsigned char* lds, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(tile_lds_at(lds)), "v"(off),
-               "s"(tile_lds_rsrc(p, bytes))
-               : "m0", "memory");
+// AT: added to lds; voff the lane's offset, checked against the resource's size, and soff the
+// wave's on top of it.
+template <int AT>
+__device__ __forceinline__ void tile_load_lds(const u32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds" ::"s"(lds), "n"(AT), "v"(voff),
+               "s"(rsrc), "s"(soff)
+               : "m0", "scc", "memory");
 }
-// The same with four bytes a lane, at lds + 4 l.
-__device__ __forceinline__ void tile_load_lds4(const void* p, uint32_t bytes, unsigned char* lds, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(tile_lds_at(lds)), "v"(off),
-               "s"(tile_lds_rsrc(p, bytes))
-               : "m0", "memory");
+// The same with four bytes a lane, at lds + AT + 4 l.
+template <int AT>
+__device__ __forceinline__ void tile_load_lds4(const u32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dword %2, %3, %4 offen lds" ::"s"(lds), "n"(AT), "v"(voff),
+               "s"(rsrc), "s"(soff)
+               : "m0", "scc", "memory");
+}
+// stage(s, I) for s = 0 .. S - 1 with I = s % U known to the compiler.
+template <int U, class Stage>
+__device__ __forceinline__ void tile_stages(int S, Stage stage) {
+  int s = 0;
+  auto all = [&]<int... I>(std::integer_sequence<int, I...>) {
+    for (; s + U <= S; s += U) (stage(s + I, std::integral_constant<int, I>{}), ...);
+    const int left = S - s;
+    ((I < left ? stage(s + I, std::integral_constant<int, I>{}) : void()), ...);
+  };
+  all(std::make_integer_sequence<int, U>{});
 }
 // Waits until at most N of this wave's global loads are on their way.
 template <int N>
