@@ -724,6 +724,11 @@ def _act(act) -> int:
     return _ACTS[act]
 
 
+def _dense_out(out, like: torch.Tensor, shape, dtype, index: int, name="out"):
+    """out, checked, or a new tensor (new_empty takes less host time than torch.empty)."""
+    return like.new_empty(shape, dtype=dtype) if out is None else _result(out, shape, dtype, index, name)
+
+
 def _scratch(workspace, need: int, index: int):
     """(tensor to keep, address, bytes) of the caller's workspace or a new one."""
     if workspace is None:
@@ -751,7 +756,7 @@ def _fp8_args(x: torch.Tensor, w: Fp8Weight, bias, out, out_dtype, index: int, n
         ba = _arg(bias, torch.float32, index, "bias")
         if bias.numel() != cw.N:
             raise ValueError(f"bias: expected {cw.N} values, got {bias.numel()}")
-    return cw, ba, yd, _result(out, (x.shape[0], cw.N), out_dtype, index)
+    return cw, ba, yd, _dense_out(out, x, (x.shape[0], cw.N), out_dtype, index)
 
 
 def cubic_quant_fp8(x: torch.Tensor, block_rows: int = 1, xq: torch.Tensor | None = None,
@@ -764,8 +769,8 @@ def cubic_quant_fp8(x: torch.Tensor, block_rows: int = 1, xq: torch.Tensor | Non
     index = _first(x, "x")
     xa = _arg(x, x.dtype, index, "x")
     M, K = x.shape
-    xq = _result(xq, (M, K), torch.float8_e4m3fn, index, "xq")
-    scales = _result(scales, (-(-M // block_rows), -(-K // 128)), torch.float32, index, "scales")
+    xq = _dense_out(xq, x, (M, K), torch.float8_e4m3fn, index, "xq")
+    scales = _dense_out(scales, x, (-(-M // block_rows), -(-K // 128)), torch.float32, index, "scales")
     _check(_call(index, load_library().cubic_quant_fp8, xa, xd, M, K, block_rows, xq.data_ptr(), scales.data_ptr()),
            "cubic_quant_fp8")
     return xq, scales
@@ -829,9 +834,9 @@ def cubic_gated_ff(x: torch.Tensor, w: torch.Tensor, act="silu", save_pre: bool 
     index = _first(x, "x")
     xa, wa, xd, M, H, I = _ff_args(x, w, index)
     kind = _act(act)
-    out = _result(out, (M, I), x.dtype, index)
+    out = _dense_out(out, x, (M, I), x.dtype, index)
     if save_pre or pre is not None:
-        pre = _result(pre, (M, 2 * I), torch.float32, index, "pre")
+        pre = _dense_out(pre, x, (M, 2 * I), torch.float32, index, "pre")
     lib = load_library()
     workspace, sa, n = _scratch(workspace, lib.cubic_gated_ff_workspace_bytes(M, H, I), index)
     _check(_call(index, lib.cubic_gated_ff, xa, wa, xd, M, H, I, kind, out.data_ptr(), None if pre is None else pre.data_ptr(),
@@ -853,8 +858,8 @@ def cubic_gated_ff_backward(dh: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
     da, pa = _arg(dh, x.dtype, index, "dh"), _arg(pre, torch.float32, index, "pre")
     if tuple(dh.shape) != (M, I) or tuple(pre.shape) != (M, 2 * I):
         raise ValueError(f"expected dh [{M}][{I}] and pre [{M}][{2 * I}], got {tuple(dh.shape)} and {tuple(pre.shape)}")
-    dx = _result(dx, (M, H), x.dtype, index, "dx") if need_dx else None
-    dw = _result(dw, (2 * I, H), x.dtype, index, "dw") if need_dw else None
+    dx = _dense_out(dx, x, (M, H), x.dtype, index, "dx") if need_dx else None
+    dw = _dense_out(dw, x, (2 * I, H), x.dtype, index, "dw") if need_dw else None
     lib = load_library()
     workspace, sa, n = _scratch(workspace, lib.cubic_gated_ff_backward_workspace_bytes(M, H, I), index)
     _check(_call(index, lib.cubic_gated_ff_backward, da, xa, wa, pa, xd, M, H, I, kind, None if dx is None else dx.data_ptr(),
@@ -878,7 +883,7 @@ def cubic_gated_ff_fp8(x: torch.Tensor, w: Fp8Weight, act="silu", out: torch.Ten
         raise ValueError(f"expected x [M][H] and a weight [2 I][H], got {tuple(x.shape)} and [{cw.N}][{cw.K}]")
     kind = _act(act)
     M, I = x.shape[0], cw.N // 2
-    out = _result(out, (M, I), out_dtype, index)
+    out = _dense_out(out, x, (M, I), out_dtype, index)
     lib = load_library()
     workspace, sa, n = _scratch(workspace, lib.cubic_gated_ff_fp8_workspace_bytes(M, cw.K, I), index)
     _check(_call(index, lib.cubic_gated_ff_fp8, xa, xd, M, ctypes.byref(cw), kind, out.data_ptr(), hd, sa, n),

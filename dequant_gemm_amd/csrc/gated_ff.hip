@@ -409,7 +409,7 @@ BackwardPlan plan_backward(int64_t M, int64_t H, int64_t I) {
   int64_t cost1 = INT64_MAX, costx = INT64_MAX, costw = INT64_MAX;
   for (int k = 0; k < kTileShapeCount; ++k) {
     int64_t cx, cw;
-    const TilePlan x = plan_shape(k, M, H, sx, unit, &cx), w = plan_shape(k, 2 * I, H, sw, unit, &cw);
+    const TilePlan x = plan_shape(k, cu, M, H, sx, unit, &cx), w = plan_shape(k, cu, 2 * I, H, sw, unit, &cw);
     if (cx < costx) {
       costx = cx;
       two.dx = x;

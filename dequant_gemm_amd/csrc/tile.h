@@ -187,8 +187,8 @@ inline int64_t plan_join(int slices, int64_t M, int64_t width) { return slices >
 
 // The slices of least time for shape k, M rows, `width` columns of operand B and `stages` steps:
 // rounds of workgroups over the compute units, and the join. No slice is empty.
-inline TilePlan plan_shape(int k, int64_t M, int64_t width, int64_t stages, int64_t unit, int64_t* cost) {
-  const int64_t cu = plan_cus(), tiles = plan_tile_count(k, M, width);
+inline TilePlan plan_shape(int k, int64_t cu, int64_t M, int64_t width, int64_t stages, int64_t unit, int64_t* cost) {
+  const int64_t tiles = plan_tile_count(k, M, width);
   TilePlan best{k, 1};
   *cost = INT64_MAX;
   for (int s = 1; s <= kMaxSlices; ++s) {
@@ -204,11 +204,12 @@ inline TilePlan plan_shape(int k, int64_t M, int64_t width, int64_t stages, int6
   return best;
 }
 inline TilePlan plan_tiles(int64_t M, int64_t width, int64_t stages, int64_t unit) {
+  const int64_t cu = plan_cus();
   TilePlan best{};
   int64_t cost = INT64_MAX;
   for (int k = 0; k < kTileShapeCount; ++k) {
     int64_t c;
-    const TilePlan t = plan_shape(k, M, width, stages, unit, &c);
+    const TilePlan t = plan_shape(k, cu, M, width, stages, unit, &c);
     if (c < cost) {
       cost = c;
       best = t;
