@@ -469,18 +469,25 @@ typedef struct cubic_weight_fp8 {
 
 /* y[m][n] = sum over blocks kb of x_scale[m][kb] * w->scales[n / 128][kb] * (sum of xq[m][k] *
  * w->codes[n][k] in the block) (+ bias[n]), for xq e4m3 [M][K] and x_scale fp32
- * [M][ceil(K / 128)] of cubic_quant_fp8. A block's products are exact and its sum and the sum
- * over blocks are fp32; the product of the two scales is rounded to fp32 first. y [M][N] in
- * CUBIC_DTYPE_F32, _BF16 or _F16, rounded once; bias fp32 [N] or NULL. The result does not
- * depend on timing. Codes of NaN and non-finite scales make what they enter non-finite. K a
- * positive multiple of 16 up to 2^20, M and N below 2^24; M == 0 or N == 0 is a no-op.
- * `workspace` may be NULL where the size query gives 0; calls that overlap need one each. */
+ * [M][ceil(K / 128)] of cubic_quant_fp8. y [M][N] in CUBIC_DTYPE_F32, _BF16 or _F16, rounded
+ * once; bias fp32 [N] or NULL. fp32 results: a block's products are exact, its sum and the sum
+ * over blocks fp32, the product of the two scales rounded to fp32 first. 16-bit results: the same,
+ * but a block's sum runs on the 8-bit MFMA, which drops what lies below about 2^-14 of the largest
+ * of the products that it adds (the 2-norm of the results is off by 1.3e-5 to 2.2e-5, a hundredth
+ * of a bf16 result's own rounding and a tenth of an fp16 one's). The result does not depend on
+ * timing, but its last bits may differ with the number of rows. Codes of NaN and non-finite
+ * scales make what they enter non-finite. K a positive multiple of 16 up to 2^20, M and N below
+ * 2^24; M == 0 or N == 0 is a no-op. `workspace` may be NULL where the size query gives 0; calls
+ * that overlap need one each. */
 size_t cubic_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, const cubic_weight_fp8* w,
                    const float* bias, void* y, int y_dtype, void* workspace, size_t ws_bytes,
                    cubic_stream_t stream);
 /* The same product of bf16 or fp16 activations x [M][K], quantised on the way by the rule of
- * cubic_quant_fp8 with block_rows 1: the result of that call followed by cubic_gemm_fp8. */
+ * cubic_quant_fp8 with block_rows 1: the result of that call followed by cubic_gemm_fp8. Up to
+ * four rows of K <= 32768 are quantised inside the product's kernel and need no workspace;
+ * others pass through the workspace (codes, then scales, each rounded up to 256 bytes, then the
+ * product's own). */
 size_t cubic_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int cubic_linear_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* w, const float* bias,
                      void* y, int y_dtype, void* workspace, size_t ws_bytes, cubic_stream_t stream);
@@ -491,7 +498,8 @@ int cubic_linear_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_f
  *   h       = act(g) * u
  * act: CUBIC_ACT_SILU, g / (1 + exp(-g)), or CUBIC_ACT_GELU_TANH, 0.5 g (1 + tanh(sqrt(2/pi)
  * (g + 0.044715 g^3))). x [M][H], w and h [M][I] in one dtype, CUBIC_DTYPE_BF16 or _F16; sums,
- * activation and product in fp32, h rounded once. pre fp32 [M][2I] receives g and u for the
+ * activation (exp2 and reciprocal of the hardware, within 2^-18 |g|) and product in fp32, h rounded
+ * once. pre fp32 [M][2I] receives g and u for the
  * backward pass, or is NULL (fp32, since g and u rounded to 16 bits would add as much error to
  * the gradients as the gradients' own rounding). H and I multiples of 8 up to 2^20, M below
  * 2^24 (CUBIC_ERR_SHAPE); CUBIC_ERR_OPTION for another act. M == 0 is a no-op. `workspace` may
