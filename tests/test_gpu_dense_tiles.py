@@ -1,0 +1,62 @@
+"""GPU parity of the dense products at sizes where each tile shape is the quickest, whole and cut into slices,
+against the oracle, within the tolerances of the operators' own tests."""
+import pytest
+import torch
+
+import dequant_gemm_amd as cq
+from tests import test_gpu_fp8 as fp8
+from tests import test_gpu_gated_ff as ff
+from tests._gpu import DEV, say
+
+pytestmark = pytest.mark.gpu
+ACT = {torch.bfloat16: "silu", torch.float16: "gelu_tanh"}
+
+
+# the largest tile of the forward product first, its sliced ones last
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,H,I", [(2051, 1032, 2056), (2051, 72, 2056), (4101, 72, 2056), (1300, 1032, 1032), (700, 4104, 264), (300, 1544, 520)])
+def test_forward_tiles(M, H, I, dtype):
+    say(f"gated_ff tiles M={M} H={H} I={I} {dtype}")
+    x, w, _ = ff._data(M + H, M, H, I, dtype)
+    h, guard = ff._guarded((M, I), dtype)
+    pre, guard_p = ff._guarded((M, 2 * I), torch.float32)
+    cq.cubic_gated_ff(x, w, act=ACT[dtype], out=h, pre=pre)
+    assert bool(torch.isnan(guard).all()) and bool(torch.isnan(guard_p).all())
+    ff._check_h(h, pre, x, w, ACT[dtype], dtype)
+
+
+# both gradients in one launch where that is quickest (256 x 256 down to 64 x 64), then each in its own
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,H,I", [(2500, 8200, 1544), (2051, 4104, 1032), (515, 4104, 520), (3000, 136, 136), (2051, 136, 136), (300, 136, 136), (4101, 72, 2056),
+                                   (2051, 4104, 136), (2051, 2056, 136), (3000, 1032, 136), (515, 1032, 2056), (1030, 136, 2056),
+                                   (300, 2056, 2056), (300, 1032, 2056), (1300, 1032, 1032), (3000, 1032, 264), (5000, 40, 4104)])
+def test_backward_tiles(M, H, I, dtype):
+    say(f"gated_ff_backward tiles M={M} H={H} I={I} {dtype}")
+    x, w, dh = ff._data(M + I, M, H, I, dtype)
+    pre = torch.randn((M, 2 * I), generator=torch.Generator(device=DEV).manual_seed(I), device=DEV)
+    dx, guard = ff._guarded((M, H), dtype)
+    dw, guard_w = ff._guarded((2 * I, H), dtype)
+    cq.cubic_gated_ff_backward(dh, x, w, pre, act=ACT[dtype], dx=dx, dw=dw)
+    assert bool(torch.isnan(guard).all()) and bool(torch.isnan(guard_w).all())
+    ff._check_grads(dx, dw, dh, x, w, pre, ACT[dtype], dtype)
+    one, _ = cq.cubic_gated_ff_backward(dh, x, w, pre, act=ACT[dtype], need_dw=False)
+    _, two = cq.cubic_gated_ff_backward(dh, x, w, pre, act=ACT[dtype], need_dx=False)
+    ff._check_grads(one, two, dh, x, w, pre, ACT[dtype], dtype)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(2051, 4113, 1168), (4101, 4113, 656), (2051, 4113, 144), (3000, 3001, 144), (4101, 4113, 144), (2051, 2050, 144), (1030, 2050, 144), (515, 2050, 528),
+                                   (130, 520, 144), (130, 1003, 2064)])
+def test_fp8_tiles(M, N, K, out):
+    say(f"gemm_fp8 tiles M={M} N={N} K={K} {out}")
+    xq, xs, w, b = fp8._data(M + N, M, N, K, bias=bool(N & 1))
+    y, guard = fp8._guarded((M, N), out)
+    cq.cubic_gemm_fp8(xq, xs, w, bias=b, out=y, out_dtype=out)
+    assert bool(torch.isnan(guard).all())
+    fp8._check(y, xq, xs, w, b, out)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,H,I", [(2051, 1168, 2048), (2051, 144, 2048), (4101, 144, 2048), (2051, 144, 1024), (1030, 144, 1024), (515, 528, 1024)])
+def test_fp8_block_tiles(M, H, I, out):
+    ff.test_fp8_block(M, H, I, ACT[out], out)
