@@ -865,8 +865,8 @@ int check_weight_fp8(const cubic_weight_fp8* w, int64_t M) {
 
 size_t fp8_codes_bytes(int64_t M, int64_t K) { return align256(static_cast<size_t>(M) * K); }
 // The activations' codes and scales, where the product does not quantise them itself.
-size_t fp8_staging_bytes(int64_t M, int64_t K) {
-  if (fp8_quantises(M, K)) return 0;
+size_t fp8_staging_bytes(int64_t M, int64_t N, int64_t K) {
+  if (fp8_quantises(M, N, K)) return 0;
   return fp8_codes_bytes(M, K) + align256(static_cast<size_t>(M) * blocks128(K) * 4);
 }
 
@@ -885,11 +885,11 @@ Fp8Params fp8_params(const cubic_weight_fp8* w, int64_t M, const float* bias, vo
 
 // x quantised into the workspace's first part, or for the product to quantise.
 hipError_t fp8_stage(Fp8Params* p, const void* x, int x_dtype, char* ws, hipStream_t s) {
-  if (fp8_quantises(p->M, p->K)) {
+  if (fp8_quantises(p->M, p->N, p->K)) {
     p->x = static_cast<const uint16_t*>(x);
     return hipSuccess;
   }
-  p->part = reinterpret_cast<float*>(ws + fp8_staging_bytes(p->M, p->K));
+  p->part = reinterpret_cast<float*>(ws + fp8_staging_bytes(p->M, p->N, p->K));
   uint8_t* xq = reinterpret_cast<uint8_t*>(ws);
   float* xs = reinterpret_cast<float*>(ws + fp8_codes_bytes(p->M, p->K));
   p->xq = xq;
@@ -933,7 +933,7 @@ CUBIC_API int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M,
 
 CUBIC_API size_t cubic_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return fp8_staging_bytes(M, K) + cubic_gemm_fp8_workspace_bytes(M, N, K);
+  return fp8_staging_bytes(M, N, K) + cubic_gemm_fp8_workspace_bytes(M, N, K);
 }
 
 CUBIC_API int cubic_linear_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* w, const float* bias, void* y,
@@ -1027,7 +1027,7 @@ CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void*
 
 CUBIC_API size_t cubic_gated_ff_fp8_workspace_bytes(int64_t M, int64_t H, int64_t I) {
   if (M <= 0 || H <= 0 || I <= 0) return 0;
-  return fp8_staging_bytes(M, H) + cubic_gemm_fp8_workspace_bytes(M, 2 * I, H);
+  return fp8_staging_bytes(M, 2 * I, H) + cubic_gemm_fp8_workspace_bytes(M, 2 * I, H);
 }
 
 CUBIC_API int cubic_gated_ff_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* gate_up, int act, void* h, int h_dtype,

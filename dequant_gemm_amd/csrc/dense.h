@@ -1,6 +1,8 @@
 // dense.h -- device helpers of the dense products (fp8.hip, gated_ff.hip): e4m3 values, the
 // gate's activations and outputs in three types.
 #pragma once
+#include <type_traits>
+
 #include "act_quant.h"
 #include "common.h"
 
@@ -8,8 +10,37 @@ namespace cubic {
 
 constexpr float kE4m3Max = 448.0f;
 
-// A block's scale: fp32(amax / 448), one rounding.
-__device__ __forceinline__ float fp8_scale(float amax) { return __fdiv_rn(amax, kE4m3Max); }
+// The largest magnitudes of 16-bit values by their bits, two at a time: NaN is the largest.
+__device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t mag8(const u32x4& v, uint32_t a) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a = mag_max(a, v[e] & 0x7fff7fffu);
+  return a;
+}
+// Of LANES neighbouring lanes, in each of them.
+template <int LANES>
+__device__ __forceinline__ uint32_t mag_lanes(uint32_t v) {
+  auto step = [&](auto ctrl_c) {
+    v = mag_max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), decltype(ctrl_c)::value, 0xf, 0xf, false)));
+  };
+  step(std::integral_constant<int, 0xb1>{});     // quad_perm [1, 0, 3, 2]
+  step(std::integral_constant<int, 0x4e>{});     // quad_perm [2, 3, 0, 1]
+  step(std::integral_constant<int, 0x141>{});    // row_half_mirror
+  if constexpr (LANES >= 16) step(std::integral_constant<int, 0x140>{});   // row_mirror
+  if constexpr (LANES == 64) {
+    v = mag_max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16, 64)));
+    v = mag_max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 32, 64)));
+  }
+  return v;
+}
+template <bool F16>
+__device__ __forceinline__ float mag_value(uint32_t v) {
+  const uint32_t m = max(v & 0xffffu, v >> 16);
+  return F16 ? static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(m))) : __uint_as_float(m << 16);
+}
 
 // Two fp32 values as e4m3 codes in the low or high half of a word, to nearest, ties to even.
 template <bool HI>
@@ -17,18 +48,23 @@ __device__ __forceinline__ uint32_t fp8_pack2(float a, float b, uint32_t old) {
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, static_cast<int>(old), HI));
 }
 
-// A block's scale with its reciprocal, correctly rounded (one Newton step from the hardware's,
-// except where the scale's significand is all ones).
+// A block's scale, fp32(amax / 448), and its reciprocal, both correctly rounded: the quotient as
+// below (equal to the division for every 16-bit amax in the range), the reciprocal by one Newton step from
+// the hardware's, except where the scale's significand is all ones. A block of zeros has 0 for both.
 struct Fp8Scale {
   float s, r;
   bool fast;
 };
 __device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
   Fp8Scale v;
-  v.s = fp8_scale(amax);
+  const float q = amax * (1.0f / kE4m3Max);
+  v.s = fmaf(fmaf(-q, kE4m3Max, amax), 1.0f / kE4m3Max, q);
   const float r = __builtin_amdgcn_rcpf(v.s);
-  v.r = fmaf(fmaf(-v.s, r, 1.0f), r, r);
-  v.fast = v.s >= 0x1p-80f && v.s <= 0x1p100f && (__float_as_uint(v.s) & 0x7fffffu) != 0x7fffffu;
+  const bool zeros = amax == 0.0f;
+  v.r = zeros ? 0.0f : fmaf(fmaf(-v.s, r, 1.0f), r, r);
+  const bool in_range = v.s >= 0x1p-80f && v.s <= 0x1p100f;
+  v.fast = zeros || (in_range && (__float_as_uint(v.s) & 0x7fffffu) != 0x7fffffu);
+  if (!zeros && !in_range) v.s = __fdiv_rn(amax, kE4m3Max);
   return v;
 }
 

@@ -6,9 +6,9 @@
 // from HBM to registers: a lane quad loads 64 contiguous bytes of a row, and the lanes
 // exchange the pieces through the LDS crossbar into the MFMA's operand order when they are
 // used. The activations pass through LDS in chunks of 64 KB, two buffers, one barrier a chunk
-// that leaves the weight loads in flight; up to four rows that fit are staged whole, in fp8
-// quantised by every workgroup itself beside its first weight loads. The waves' sums meet in
-// LDS and are added up in their order.
+// that leaves the weight loads in flight; up to four rows that fit are staged whole. In fp8
+// every workgroup can quantise the rows itself on their way into LDS: whole rows beside its first
+// weight loads, or a chunk at a time. The waves' sums meet in LDS and are added up in their order.
 //
 // Measured: 44 MB of e4m3 weights (6144 x 7168) in 9.9 us of the kernel with one row, 12.2 us with 16;
 // 58.7 MB of bf16 gate and up weights in 10.9 us (5.4 TB/s), 17 us of I 1024, H 8192 with 48 rows. From
@@ -67,7 +67,8 @@ __device__ __forceinline__ f32x4 few_dot(const i32x4& a, const i32x4& b, f32x4 c
 
 // MT: tiles of 16 activation rows; SPC = 4 / MT steps per wave and chunk; NT: tiles of 16
 // weight rows. Gated with NT 1: gate rows in the tile's first half, up rows in its second.
-template <int KIND, int MT, int NT, bool WHOLE, bool GATED, bool XF16>
+// QUANT: fp8, x in 16 bits, which every workgroup quantises a chunk at a time.
+template <int KIND, int MT, int NT, bool WHOLE, bool GATED, bool XF16, bool QUANT>
 __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr bool F8 = KIND == kFewFp8 || KIND == kFewFp8Exact;
@@ -134,9 +135,10 @@ __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
   // piece XORed with two row bits so that 16 rows read at one piece hit all banks ----
   auto place = [&](int st, int m, int j) { return ((st * RM + m) * 4 + (j ^ ((m >> 2) & 3))) * 16; };
   constexpr int XR = 4;                        // pieces per thread and chunk
-  u32x4 xv[XR];
+  constexpr int kIn = QUANT ? 2 : 1;           // of them, of x
+  u32x4 xv[XR * kIn];
   float xsv = 0.0f;
-  const __amdgpu_buffer_rsrc_t xrs = tile_rsrc(p.x, static_cast<uint32_t>(M) * KB);
+  const __amdgpu_buffer_rsrc_t xrs = tile_rsrc(p.x, kIn * static_cast<uint32_t>(M) * KB);
   constexpr int kPieces = 64 * SPC;            // pieces of a row in a chunk
   auto load_x = [&](int c) {
 #pragma unroll
@@ -144,22 +146,35 @@ __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
       const int idx = tid + 1024 * r;
       const int m = idx / kPieces;
       const uint32_t k = static_cast<uint32_t>(c) * (SPC * 1024) + 16u * (idx % kPieces);
-      xv[r] = tile_load(xrs, m < M && k < KB ? static_cast<uint32_t>(m) * KB + k : kPast);
+#pragma unroll
+      for (int h = 0; h < kIn; ++h)
+        xv[kIn * r + h] = tile_load(xrs, m < M && k < KB ? kIn * (static_cast<uint32_t>(m) * KB + k) + 16u * h : kPast);
     }
-    if constexpr (F8) {                        // 8 SPC blocks of each row: thread to (block, row)
+    if constexpr (F8 && !QUANT) {                    // 8 SPC blocks of each row: thread to (block, row)
       const int m = tid % RM, b = c * (8 * SPC) + tid / RM;
       xsv = tid < 512 && m < M && b < kb ? p.xs[static_cast<int64_t>(m) * kb + b] : 0.0f;
     }
   };
-  auto store_x = [&](int c) {
+  auto store_x = [&](int c) __attribute__((always_inline)) {   // (out of line its captures go to memory)
     unsigned char* buf = smem + (c & 1) * (kChunk + kScales);
-#pragma unroll
-    for (int r = 0; r < XR; ++r) {
+    auto piece = [&](auto r_c) {
+      constexpr int r = decltype(r_c)::value;
       const int idx = tid + 1024 * r;
       const int m = idx / kPieces, pk = idx % kPieces;
-      if (m < M) *reinterpret_cast<u32x4*>(buf + place(pk >> 2, m, pk & 3)) = xv[r];
-    }
-    if constexpr (F8) {
+      if (m >= M) return;                      // (a wave's pieces are of one row)
+      u32x4 codes = xv[kIn * r];
+      if constexpr (QUANT) {                   // 16 values; eight neighbouring lanes hold a block
+        const Fp8Scale s = fp8_scale_of(mag_value<XF16>(mag_lanes<8>(mag8(xv[kIn * r + 1], mag8(xv[kIn * r], 0u)))));
+        const uint2 lo = fp8_quant8<XF16>(xv[kIn * r], s), hi = fp8_quant8<XF16>(xv[kIn * r + 1], s);
+        codes = u32x4{lo.x, lo.y, hi.x, hi.y};
+        if ((tid & 7) == 0) *reinterpret_cast<float*>(buf + kChunk + 4 * ((pk >> 3) * RM + m)) = s.s;
+      }
+      *reinterpret_cast<u32x4*>(buf + place(pk >> 2, m, pk & 3)) = codes;
+    };
+    [&]<int... R>(std::integer_sequence<int, R...>) {
+      (piece(std::integral_constant<int, R>{}), ...);
+    }(std::make_integer_sequence<int, XR>{});
+    if constexpr (F8 && !QUANT) {
       if (tid < 512) *reinterpret_cast<float*>(buf + kChunk + 4 * tid) = xsv;
     }
   };
@@ -183,10 +198,7 @@ __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         if (m < M) {
-          float a = absmax8<XF16, true>(v[m], 0.0f);
-#pragma unroll
-          for (int d = 8; d >= 1; d >>= 1) a = larger<true>(a, __shfl_xor(a, d, 64));
-          const Fp8Scale s = fp8_scale_of(a);
+          const Fp8Scale s = fp8_scale_of(mag_value<XF16>(mag_lanes<16>(mag8(v[m], 0u))));
           // eight codes: half a piece; past K up to the last step's end zeros
           if (vec < nsteps * 8)
             *reinterpret_cast<uint2*>(smem + place(vec >> 3, m, (vec >> 1) & 3) + 8 * (vec & 1)) = fp8_quant8<XF16>(v[m], s);
@@ -318,9 +330,9 @@ __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
   }
 }
 
-template <int KIND, int MT, int NT, bool WHOLE, bool GATED, bool XF16>
+template <int KIND, int MT, int NT, bool WHOLE, bool GATED, bool XF16, bool QUANT>
 hipError_t launch_few_k(const FewParams& p, hipStream_t st) {
-  auto kern = k_few_rows<KIND, MT, NT, WHOLE, GATED, XF16>;
+  auto kern = k_few_rows<KIND, MT, NT, WHOLE, GATED, XF16, QUANT>;
   constexpr bool F8 = KIND == kFewFp8 || KIND == kFewFp8Exact;
   const int nsteps = static_cast<int>((p.K * (F8 ? 1 : 2) + 63) / 64);
   const int red = kFewWaves * NT * 16 * MT * 16 * 4;
@@ -334,9 +346,10 @@ hipError_t launch_few_k(const FewParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// whole: p.x holds up to kFewWholeM rows to stage whole (fp8: 16-bit rows to quantise).
+// whole: p.x holds up to kFewWholeM rows to stage whole (fp8: 16-bit rows to quantise). quant: fp8,
+// p.x holds 16-bit rows to quantise a chunk at a time.
 template <int KIND, bool GATED>
-hipError_t launch_few(FewParams p, bool whole, bool xf16, hipStream_t st) {
+hipError_t launch_few(FewParams p, bool whole, bool quant, bool xf16, hipStream_t st) {
   constexpr bool F8 = KIND == kFewFp8 || KIND == kFewFp8Exact;
   const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256;
   // equal shares of the columns, at most two tiles of 16 rows a workgroup
@@ -353,26 +366,32 @@ hipError_t launch_few(FewParams p, bool whole, bool xf16, hipStream_t st) {
     p.rt = static_cast<int>((c + nt - 1) / nt);
     p.cols = p.rt * nt;
   }
-  auto go = [&](auto mt_c, auto whole_c, auto xf16_c) {
+  auto go = [&](auto mt_c, auto whole_c, auto xf16_c, auto quant_c) {
     constexpr int MT = decltype(mt_c)::value;
-    constexpr bool WHOLE = decltype(whole_c)::value, XF16 = decltype(xf16_c)::value;
+    constexpr bool WHOLE = decltype(whole_c)::value, XF16 = decltype(xf16_c)::value, QUANT = decltype(quant_c)::value;
     // (e4m3 operands of two tiles by more rows than this go to the tile kernel: registers)
-    constexpr bool kTwo = !F8 || MT == 1 || (MT == 2 && KIND == kFewFp8);
+    constexpr bool kTwo = !F8 || MT == 1 || (MT == 2 && KIND == kFewFp8 && !QUANT);
     if constexpr (kTwo) {
-      if (nt == 2) return launch_few_k<KIND, MT, 2, WHOLE, GATED, XF16>(p, st);
+      if (nt == 2) return launch_few_k<KIND, MT, 2, WHOLE, GATED, XF16, QUANT>(p, st);
     }
-    return nt == 1 ? launch_few_k<KIND, MT, 1, WHOLE, GATED, XF16>(p, st) : hipErrorInvalidValue;
+    return nt == 1 ? launch_few_k<KIND, MT, 1, WHOLE, GATED, XF16, QUANT>(p, st) : hipErrorInvalidValue;
   };
   using One = std::integral_constant<int, 1>;
   if (whole) {
     if constexpr (F8) {
-      if (xf16) return go(One{}, std::true_type{}, std::true_type{});
+      if (xf16) return go(One{}, std::true_type{}, std::true_type{}, std::false_type{});
     }
-    return go(One{}, std::true_type{}, std::false_type{});
+    return go(One{}, std::true_type{}, std::false_type{}, std::false_type{});
   }
-  if (p.M <= 16) return go(One{}, std::false_type{}, std::false_type{});
-  if (p.M <= 32) return go(std::integral_constant<int, 2>{}, std::false_type{}, std::false_type{});
-  return go(std::integral_constant<int, 4>{}, std::false_type{}, std::false_type{});
+  auto rows = [&](auto xf16_c, auto quant_c) {
+    if (p.M <= 16) return go(One{}, std::false_type{}, xf16_c, quant_c);
+    if (p.M <= 32) return go(std::integral_constant<int, 2>{}, std::false_type{}, xf16_c, quant_c);
+    return go(std::integral_constant<int, 4>{}, std::false_type{}, xf16_c, quant_c);
+  };
+  if constexpr (F8) {
+    if (quant) return xf16 ? rows(std::true_type{}, std::true_type{}) : rows(std::false_type{}, std::true_type{});
+  }
+  return rows(std::false_type{}, std::false_type{});
 }
 
 }  // namespace cubic

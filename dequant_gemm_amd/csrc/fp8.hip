@@ -25,7 +25,6 @@
 // in the smaller tiles), results added 1 to 5 MFMAs later, the stage's loads issued at once.
 #include <algorithm>
 
-#include "act_quant.h"
 #include "common.h"
 #include "dense.h"
 #include "few_rows.h"
@@ -34,13 +33,6 @@
 
 namespace cubic {
 namespace {
-
-// The larger of the magnitudes of 16 neighbouring lanes, NaN as the largest.
-__device__ __forceinline__ float larger16(float v) {
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) v = larger<true>(v, __shfl_xor(v, o, 64));
-  return v;
-}
 
 // A launch takes fewer than 2^32 threads; what is more goes round again.
 constexpr int64_t kMaxGrid = (1 << 24) - 1;
@@ -56,7 +48,7 @@ __global__ __launch_bounds__(256) void k_quant_fp8_rows(const uint16_t* __restri
     const int64_t k = b * 128 + 8 * (threadIdx.x & 15);
     const bool on = k < K;
     const u32x4 v = on ? *reinterpret_cast<const u32x4*>(x + m * K + k) : u32x4{0u, 0u, 0u, 0u};
-    const Fp8Scale s = fp8_scale_of(larger16(absmax8<XF16, true>(v, 0.0f)));
+    const Fp8Scale s = fp8_scale_of(mag_value<XF16>(mag_lanes<16>(mag8(v, 0u))));
     if (on) *reinterpret_cast<uint2*>(xq + m * K + k) = fp8_quant8<XF16>(v, s);
     if ((threadIdx.x & 15) == 0) xs[g] = s.s;
   }
@@ -66,23 +58,23 @@ __global__ __launch_bounds__(256) void k_quant_fp8_rows(const uint16_t* __restri
 template <bool XF16>
 __global__ __launch_bounds__(256) void k_quant_fp8_blocks(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t kb,
                                                           uint8_t* __restrict__ xq, float* __restrict__ xs) {
-  __shared__ float s_max[4];
+  __shared__ uint32_t s_max[4];
   const int64_t blocks = (M + 127) / 128 * kb;
   for (int64_t at = blockIdx.x; at < blocks; at += gridDim.x) {
     const int64_t mb = at / kb, b = at - mb * kb;
     const int64_t k = b * 128 + 8 * (threadIdx.x & 15);
     u32x4 v[8];
-    float a = 0.0f;
+    uint32_t a = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t m = mb * 128 + 16 * i + (threadIdx.x >> 4);
       v[i] = m < M && k < K ? *reinterpret_cast<const u32x4*>(x + m * K + k) : u32x4{0u, 0u, 0u, 0u};
-      a = absmax8<XF16, true>(v[i], a);
+      a = mag8(v[i], a);
     }
-    a = wave_larger<true>(a);
+    a = mag_lanes<64>(a);
     if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = a;
     __syncthreads();
-    const Fp8Scale s = fp8_scale_of(larger<true>(larger<true>(s_max[0], s_max[1]), larger<true>(s_max[2], s_max[3])));
+    const Fp8Scale s = fp8_scale_of(mag_value<XF16>(mag_max(mag_max(s_max[0], s_max[1]), mag_max(s_max[2], s_max[3]))));
     __syncthreads();                           // read before the next block's are written
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -403,27 +395,38 @@ FewParams few_params(const Fp8Params& p, bool gated) {
 // 6144 x 7168 27.5 against 15.0. fp32 results, 32 rows, 6144 x 7168: 19.1 against 16.7. wide: a
 // workgroup would have two tiles of weight rows.
 constexpr int64_t kFewAlways = 16;
-static bool fp8_few(const Fp8Params& p, bool gated) {
-  const bool wide = p.N > 16 * plan_cus();
-  if (p.M <= kFewAlways) return true;
-  if (p.M <= 32) return !(wide && p.ydt == 0 && !gated);
-  return p.M <= kFewMaxM && !wide && p.K <= 4096;
+
+static bool fp8_wide(int64_t N) { return N > 16 * plan_cus(); }
+static bool fp8_few(int64_t M, int64_t N, int64_t K, bool exact) {
+  if (M <= kFewAlways) return true;
+  if (M <= 32) return !(fp8_wide(N) && exact);
+  return M <= kFewMaxM && !fp8_wide(N) && K <= 4096;
 }
 
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewAlways ? 0 : plan_bytes(plan8(M, N, K), M, N); }
 
-bool fp8_quantises(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
+static bool fp8_whole(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
+// Every workgroup quantises the rows itself, instead of a launch before the product's, up to about
+// as many values as cost the graph replays of a call what its launch costs a caller. Measured, in us (N x K;
+// replays, then calls; in the product against a launch of its own): 16 x 1936 values, N 1003, 8.4 and 8.6
+// against 7.3 and 15.0; 37 x 1936 10.7 and 10.3 against 9.3 and 15.3; 48 x 2048, N 4096, 12.0 and 11.5
+// against 9.3 and 15.1; 16 x 7168 13.6 and 13.0 against 10.4 and 15.3. Wide: 16 x 2048, N 7168, 10.2
+// and 9.7 against 9.2 and 14.7; 8 x 7168, N 6144, 15.3 and 14.8 against 14.1 and 15.0.
+bool fp8_quantises(int64_t M, int64_t N, int64_t K) {
+  return fp8_whole(M, K) || (fp8_few(M, N, K, true) && M * K <= (fp8_wide(N) ? 40 : 96) * 1024);
+}
 
 hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st) {
-  if (!fp8_few(p, false)) return launch_fp8_tiles<false>(p, st);
+  if (!fp8_few(p.M, p.N, p.K, p.ydt == 0)) return launch_fp8_tiles<false>(p, st);
   const FewParams f = few_params(p, false);
-  return p.ydt == 0 ? launch_few<kFewFp8Exact, false>(f, p.x != nullptr, xf16, st)
-                    : launch_few<kFewFp8, false>(f, p.x != nullptr, xf16, st);
+  const bool whole = p.x && fp8_whole(p.M, p.K);
+  return p.ydt == 0 ? launch_few<kFewFp8Exact, false>(f, whole, p.x != nullptr, xf16, st)
+                    : launch_few<kFewFp8, false>(f, whole, p.x != nullptr, xf16, st);
 }
 
 hipError_t launch_fp8_gated(const Fp8Params& p, bool xf16, hipStream_t st) {
-  if (!fp8_few(p, true)) return launch_fp8_tiles<true>(p, st);
-  return launch_few<kFewFp8, true>(few_params(p, true), p.x != nullptr, xf16, st);
+  if (!fp8_few(p.M, p.N, p.K, false)) return launch_fp8_tiles<true>(p, st);
+  return launch_few<kFewFp8, true>(few_params(p, true), p.x && fp8_whole(p.M, p.K), p.x != nullptr, xf16, st);
 }
 
 }  // namespace cubic

@@ -510,7 +510,7 @@ hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
     f.gelu = p.gelu;
     f.pre = p.pre;
     const bool whole = p.M <= kFewWholeM && 2 * p.H <= kFewWholeBytes;
-    return p.f16 ? launch_few<kFewF16, true>(f, whole, false, st) : launch_few<kFewBf16, true>(f, whole, false, st);
+    return p.f16 ? launch_few<kFewF16, true>(f, whole, false, false, st) : launch_few<kFewBf16, true>(f, whole, false, false, st);
   }
   const TilePlan plan = plan_forward(p.M, p.H, p.I);
   const TileParams t{p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, dt, p.pre, p.gelu, plan.slices, p.part};

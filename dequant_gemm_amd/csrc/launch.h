@@ -231,7 +231,7 @@ size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K);
 // One scale per 128 channels of a row, or (blocks) per 128 x 128 values.
 hipError_t launch_quant_fp8(const uint16_t* x, bool xf16, int64_t M, int64_t K, bool blocks, uint8_t* xq, float* xs,
                             hipStream_t st);
-bool fp8_quantises(int64_t M, int64_t K);   // the product takes x itself
+bool fp8_quantises(int64_t M, int64_t N, int64_t K);   // the product takes x itself
 hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st);
 // N = 2 I rows of w, gate rows first (I a multiple of 128): y [M][I] = act(gate) * up in bf16 or fp16
 hipError_t launch_fp8_gated(const Fp8Params& p, bool xf16, hipStream_t st);

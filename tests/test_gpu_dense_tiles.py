@@ -1,5 +1,6 @@
 """GPU parity of the dense products at sizes where each tile shape is the quickest, whole and cut into slices,
-against the oracle, within the tolerances of the operators' own tests."""
+against the oracle, within the tolerances of the operators' own tests; and the e4m3 linear call with few rows,
+which it quantises in one way or another."""
 import pytest
 import torch
 
@@ -59,4 +60,36 @@ def test_fp8_tiles(M, N, K, out):
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("M,H,I", [(2051, 1168, 2048), (2051, 144, 2048), (4101, 144, 2048), (2051, 144, 1024), (1030, 144, 1024), (515, 528, 1024)])
 def test_fp8_block_tiles(M, H, I, out):
+    ff.test_fp8_block(M, H, I, ACT[out], out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K", [(2, 64, 40960), (5, 40, 16400), (6, 129, 8208), (8, 7000, 4112), (16, 1003, 2048), (16, 6144, 2560), (17, 300, 5776),
+                                   (31, 2050, 1040), (33, 1003, 1936), (48, 4096, 2048), (64, 2050, 1536), (64, 37, 16)])
+def test_linear_of_few_rows_is_quantiser_and_product(M, N, K, dtype):
+    """Bit for bit, with blocks of zeros, of the type's smallest values and of non-finite ones."""
+    say(f"linear_fp8 few rows M={M} N={N} K={K} {dtype}")
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    x = fp8._acts(g, M, K, dtype)
+    x[0, :min(K, 256)] = 0
+    x[0, 0] = -0.0
+    x[1, :min(K, 128)] = -2.0 ** -133 if dtype == torch.bfloat16 else -2.0 ** -24
+    if M > 4:
+        x[3], x[4, 7], x[2, K - 1] = 0, float("nan"), -float("inf")
+    _, _, w, b = fp8._data(N, 8, N, K, bias=True)
+    xq, xs = cq.cubic_quant_fp8(x)
+    for out in (torch.float32, torch.bfloat16, torch.float16):
+        want = cq.cubic_gemm_fp8(xq, xs, w, bias=b, out_dtype=out)
+        y, guard = fp8._guarded((M, N), out)
+        assert cq.cubic_linear_fp8_workspace_bytes(M, N, K) >= cq.cubic_gemm_fp8_workspace_bytes(M, N, K)
+        cq.cubic_linear_fp8(x, w, bias=b, out=y, out_dtype=out)
+        assert bool(torch.isnan(guard).all())
+        bits = torch.int32 if out == torch.float32 else torch.int16
+        assert torch.equal(torch.isnan(y), torch.isnan(want)) and bool(torch.isfinite(y[:2]).all())
+        assert torch.equal(torch.where(torch.isnan(y), 0, y).view(bits), torch.where(torch.isnan(want), 0, want).view(bits))
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,H,I", [(5, 528, 384), (8, 4112, 2176), (16, 1040, 1152), (17, 528, 256), (31, 1040, 1024), (37, 528, 1024), (64, 1040, 128)])
+def test_fp8_block_of_few_rows(M, H, I, out):
     ff.test_fp8_block(M, H, I, ACT[out], out)
