@@ -22,7 +22,8 @@
 // (library 124). On zeros 87-90 us (library 60): the clock falls with the power of real operands.
 // Without the fmas 98 us. Not faster: operands through registers (110-116 us), 256 x 192 tiles in
 // whole rounds (186 us against 187), B's blocks read three ahead (spills 66 registers; 1 to 3 %
-// in the smaller tiles), results added 1 to 5 MFMAs later, the stage's loads issued at once.
+// in the smaller tiles), results added 1 to 5 MFMAs later, the stage's loads issued at once, 256 x
+// 128 tiles by four waves of 128 x 64 (2048 x 4096 x 7168: 87 us against 71).
 #include <algorithm>
 
 #include "common.h"
