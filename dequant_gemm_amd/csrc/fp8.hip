@@ -20,6 +20,9 @@
 // Measured: 4096 x 4096 x 7168 in 105-112 us (2.1-2.3 PFLOP/s; the library's product without
 // block scales 80 us), MFMA busy 51 % of the cycles at 2.0 GHz; 4096 x 6144 x 7168 187-203 us
 // (library 124). On zeros 87-90 us (library 60): the clock falls with the power of real operands.
+// Smaller tiles hold a stage's fragments ahead, with the ring's slots known to the compiler:
+// 100 x 6144 x 7168 22.2 -> 18.0 us, 256 rows 28 -> 24, 512 rows (128 x 128 tiles, also eight waves
+// instead of four) 42 -> 33, gated 256 x 7168 x 2048 26 -> 21.6.
 // Without the fmas 98 us. Not faster: operands through registers (110-116 us), 256 x 192 tiles in
 // whole rounds (186 us against 187), B's blocks read three ahead (spills 66 registers; 1 to 3 %
 // in the smaller tiles), results added 1 to 5 MFMAs later, the stage's loads issued at once, 256 x
@@ -87,9 +90,12 @@ __global__ __launch_bounds__(256) void k_quant_fp8_blocks(const uint16_t* __rest
 }
 
 // ---------------------------------------------------------------------------
-// A tile's shape: WM x WN waves with MB x NB blocks of 16 x 16 each, RING stages in LDS.
-template <int MB_, int NB_, int WM_, int WN_, int RING_>
+// A tile's shape: WM x WN waves with MB x NB blocks of 16 x 16 each, RING stages in LDS. AHEAD: a
+// wave holds the fragments of a whole stage and reads the next one's meanwhile, for tiles whose
+// MFMAs between a read and its use take less than the read.
+template <int MB_, int NB_, int WM_, int WN_, int RING_, bool AHEAD_>
 struct Tile8 {
+  static constexpr bool kAhead = AHEAD_;
   static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, W = WM * WN;
   static constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN;
   // 128 codes of every row, the scales of the rows of A, those of B's blocks (a wave's load)
@@ -121,8 +127,10 @@ __device__ __forceinline__ f32x4 fp8_dot(const i32x8& a, const i32x8& b) {
   return part;
 }
 
+// (AHEAD: two waves a SIMD, without which the compiler takes 330 registers, one workgroup to a
+// compute unit, and up to 10 % more time)
 template <class Shape, bool EXACT, bool GATED>
-__global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
+__global__ __launch_bounds__(64 * Shape::W, Shape::kAhead ? 2 : 1) void k_fp8_tile(Fp8Params p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
   constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL;
@@ -202,80 +210,169 @@ __global__ __launch_bounds__(64 * Shape::W) void k_fp8_tile(Fp8Params p) {
   f32x4 acc[MB][NB] = {};
   constexpr int Q = MB * NB, kLag = 3;         // results are added this many MFMAs later
   static_assert(NB % 2 == 0, "fb[0] holds a stage's first block again");
-  // a stage's loads are issued beside a last and a first part of the MFMAs
-  constexpr int kLast = MB, kFirst = MB * (NB / 2), kN1 = NL * kLast / (kLast + kFirst);
+  if constexpr (Shape::kAhead) {
+    // Stage s: at its start the loads of the next stage are in LDS, and every wave has read this
+    // one: the loads of the stage kRing behind it take its place.
+    // Slots of the ring are known to the compiler and offsets made once: what counts beside the
+    // MFMAs of such a tile is the number of other instructions.
+    static_assert(kRing % 2 == 0);
+    const u32x4 ra = tile_lds_rsrc(p.xq + m0 * p.K, arows * K);
+    u32x4 rb[LB];
+    uint32_t va[LA];
 #pragma unroll
-  for (int r = 0; r + 1 < kRing; ++r) {
-    load_scale(r);
+    for (int i = 0; i < LA; ++i) va[i] = base + 8u * W * i * K;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) load(r, i);
-  }
+    for (int i = 0; i < LB; ++i) rb[i] = tile_lds_rsrc(bp[i], brows * K);
+    const uint32_t lds = tile_lds_at(smem) + 1024u * wave;
+    const int whole = static_cast<int>(K >> 7) - s0;           // of this slice's stages, those that are whole
+    // Piece i of stage s into slot SLOT; stages and pieces come in their order.
+    auto put = [&]<int SLOT, int I>(std::integral_constant<int, SLOT>, int s, std::integral_constant<int, I>) {
+      const uint32_t k = 128u * static_cast<uint32_t>(s0 + s);
+      if (I == 0 && s >= whole) {              // past K nothing is read, nor of the stages that follow
+        asm volatile("" ::: "memory");
+        const bool past = k + lane_k >= K;
 #pragma unroll
-  for (int i = 0; i < kN1; ++i) load(kRing - 1, i);
-  // (the scales' loads, which not every wave has, are not counted: the waits are a little long)
-  tile_wait<(kRing - 2) * NL + kN1>();
-  tile_barrier();
-  i32x8 fa[MB], fb[2];
-  float sx[MB], w0, w1 = 0.0f;
-  fb[0] = read_b(0, 0);
+        for (int i = 0; i < LA; ++i) va[i] = past ? kPast : va[i];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    fa[i] = read_a(0, i);
-    sx[i] = read_scale(0, i);
-  }
-  w0 = read_wscale(0, wb);
-  if constexpr (GATED) w1 = read_wscale(0, 1);
-  for (int s = 0; s < S; ++s) {
-    float sc0[MB], sc1[GATED ? MB : 1];
+        for (int i = 0; i < LB; ++i) boff[i] = past ? kPast : boff[i];
+      }
+      if constexpr (I < LA) {
+        tile_load_lds<SLOT * kStage + 1024 * W * I>(ra, lds, va[I], k);
+      } else {
+        tile_load_lds<SLOT * kStage + kBOff + 1024 * W * (I - LA)>(rb[I - LA], lds, boff[I - LA], k);
+      }
+    };
+    auto times = [&]<int N0, int N1>(std::integral_constant<int, N0>, std::integral_constant<int, N1>, auto f) {
+      [&]<int... T>(std::integer_sequence<int, T...>) {
+        (f(std::integral_constant<int, N0 + T>{}), ...);
+      }(std::make_integer_sequence<int, N1 - N0>{});
+    };
+    using I0 = std::integral_constant<int, 0>;
+    i32x8 fa[2][MB], fb[2][NB];
+    float sx[2][MB], w[2][2];
+    constexpr int kReads = 1 + 2 * MB + NB, kOver = std::max(1, Q * 3 / 4);
+    auto read = [&]<int TO, int SLOT>(std::integral_constant<int, TO>, std::integral_constant<int, SLOT>, int r) {
+      if (r == 0) {
+        w[TO][0] = read_wscale(SLOT, wb);
+        w[TO][1] = GATED ? read_wscale(SLOT, 1) : 0.0f;
+      } else if (r <= MB) {
+        sx[TO][r - 1] = read_scale(SLOT, r - 1);
+      } else if (r <= 2 * MB) {
+        fa[TO][r - 1 - MB] = read_a(SLOT, r - 1 - MB);
+      } else {
+        fb[TO][r - 1 - 2 * MB] = read_b(SLOT, r - 1 - 2 * MB);
+      }
+    };
+    times(I0{}, std::integral_constant<int, kRing>{}, [&](auto slot) {
+      load_scale(slot);
+      times(I0{}, std::integral_constant<int, NL>{}, [&](auto i) { put(slot, slot, i); });
+    });
+    tile_wait<(kRing - 1) * NL>();
+    tile_barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(I0{}, I0{}, r);
+    tile_stages<kRing>(S, [&](int s, auto slot) {
+      constexpr int kSlot = decltype(slot)::value, u = kSlot % 2;
+      tile_wait<(kRing - 2) * NL>();
+      tile_barrier();
+      f32x4 part[kLag + 1];
+      auto add = [&](int t) {
+        const int i = t % MB, j = t / MB;
+        const float f = sx[u][i] * w[u][GATED ? j & 1 : 0];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(part[t % (kLag + 1)][e], f, acc[i][j][e]);
+      };
+      times(I0{}, std::integral_constant<int, Q>{}, [&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        part[t % (kLag + 1)] = fp8_dot<EXACT>(fb[u][t / MB], fa[u][t % MB]);
+        // in the first three quarters, so that they have arrived at the barrier
+#pragma unroll
+        for (int r = t * kReads / kOver; r < (t + 1) * kReads / kOver && r < kReads; ++r)
+          read(std::integral_constant<int, 1 - u>{}, std::integral_constant<int, (kSlot + 1) % kRing>{}, r);
+        if (t == 0) load_scale(s + kRing);
+        times(std::integral_constant<int, t * NL / Q>{}, std::integral_constant<int, (t + 1) * NL / Q>{}, [&](auto i) { put(slot, s + kRing, i); });
+        if (t >= kLag) add(t - kLag);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+#pragma unroll
+      for (int t = Q - kLag; t < Q; ++t) add(t);
+    });
+  } else {
+    // a stage's loads are issued beside a last and a first part of the MFMAs
+    constexpr int kLast = MB, kFirst = MB * (NB / 2), kN1 = NL * kLast / (kLast + kFirst);
+#pragma unroll
+    for (int r = 0; r + 1 < kRing; ++r) {
+      load_scale(r);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) load(r, i);
+    }
+#pragma unroll
+    for (int i = 0; i < kN1; ++i) load(kRing - 1, i);
+    // (the scales' loads, which not every wave has, are not counted: the waits are a little long)
+    tile_wait<(kRing - 2) * NL + kN1>();
+    tile_barrier();
+    i32x8 fa[MB], fb[2];
+    float sx[MB], w0, w1 = 0.0f;
+    fb[0] = read_b(0, 0);
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      sc0[i] = sx[i] * w0;
-      if constexpr (GATED) sc1[i] = sx[i] * w1;
+      fa[i] = read_a(0, i);
+      sx[i] = read_scale(0, i);
     }
-    f32x4 part[kLag + 1];
-    auto add = [&](int t) {
-      const int i = t % MB, j = t / MB;
-      const float f = GATED && (j & 1) ? sc1[GATED ? i : 0] : sc0[i];
+    w0 = read_wscale(0, wb);
+    if constexpr (GATED) w1 = read_wscale(0, 1);
+    for (int s = 0; s < S; ++s) {
+      float sc0[MB], sc1[GATED ? MB : 1];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(part[t % (kLag + 1)][e], f, acc[i][j][e]);
-    };
-#pragma unroll
-    for (int t = 0; t < Q; ++t) {
-      const int i = t % MB, j = t / MB;
-      if (t == Q - kLast) {
-        // every wave has this stage's last fragments in registers, and its loads of the
-        // next stage are in LDS: that one is read from here on, and the stage after it
-        // kRing behind it takes this one's place
-        tile_wait<(kRing - 2) * NL>();
-        tile_barrier();
-        fb[(j + 1) & 1] = read_b(s + 1, 0);
-      } else if (i == 0) {
-        fb[(j + 1) & 1] = read_b(s, j + 1);
+      for (int i = 0; i < MB; ++i) {
+        sc0[i] = sx[i] * w0;
+        if constexpr (GATED) sc1[i] = sx[i] * w1;
       }
-      part[t % (kLag + 1)] = fp8_dot<EXACT>(fb[j & 1], fa[i]);
-      if (j == NB - 1) {
-        fa[i] = read_a(s + 1, i);
-        sx[i] = read_scale(s + 1, i);
-        if (i == 0) {
-          w0 = read_wscale(s + 1, wb);
-          if constexpr (GATED) w1 = read_wscale(s + 1, 1);
+      f32x4 part[kLag + 1];
+      auto add = [&](int t) {
+        const int i = t % MB, j = t / MB;
+        const float f = GATED && (j & 1) ? sc1[GATED ? i : 0] : sc0[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(part[t % (kLag + 1)][e], f, acc[i][j][e]);
+      };
+#pragma unroll
+      for (int t = 0; t < Q; ++t) {
+        const int i = t % MB, j = t / MB;
+        if (t == Q - kLast) {
+          // every wave has this stage's last fragments in registers, and its loads of the
+          // next stage are in LDS: that one is read from here on, and the stage after it
+          // kRing behind it takes this one's place
+          tile_wait<(kRing - 2) * NL>();
+          tile_barrier();
+          fb[(j + 1) & 1] = read_b(s + 1, 0);
+        } else if (i == 0) {
+          fb[(j + 1) & 1] = read_b(s, j + 1);
         }
-      }
-      if (t >= kLag) add(t - kLag);
-      if (t >= Q - kLast) {
-        constexpr int l1 = kN1;
-        const int u = t - (Q - kLast);
+        part[t % (kLag + 1)] = fp8_dot<EXACT>(fb[j & 1], fa[i]);
+        if (j == NB - 1) {
+          fa[i] = read_a(s + 1, i);
+          sx[i] = read_scale(s + 1, i);
+          if (i == 0) {
+            w0 = read_wscale(s + 1, wb);
+            if constexpr (GATED) w1 = read_wscale(s + 1, 1);
+          }
+        }
+        if (t >= kLag) add(t - kLag);
+        if (t >= Q - kLast) {
+          constexpr int l1 = kN1;
+          const int u = t - (Q - kLast);
 #pragma unroll
-        for (int r = u * l1 / kLast; r < (u + 1) * l1 / kLast; ++r) load(s + kRing, r);
-      } else if (t < kFirst) {
+          for (int r = u * l1 / kLast; r < (u + 1) * l1 / kLast; ++r) load(s + kRing, r);
+        } else if (t < kFirst) {
 #pragma unroll
-        for (int r = kN1 + t * (NL - kN1) / kFirst; r < kN1 + (t + 1) * (NL - kN1) / kFirst; ++r) load(s - 1 + kRing, r);
-        if (t == 0) load_scale(s - 1 + kRing);
+          for (int r = kN1 + t * (NL - kN1) / kFirst; r < kN1 + (t + 1) * (NL - kN1) / kFirst; ++r) load(s - 1 + kRing, r);
+          if (t == 0) load_scale(s - 1 + kRing);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = Q - kLag; t < Q; ++t) add(t);
     }
-#pragma unroll
-    for (int t = Q - kLag; t < Q; ++t) add(t);
   }
   tile_wait<0>();                              // loads behind the last stage
 
@@ -338,17 +435,17 @@ hipError_t launch_fp8_tiles(Fp8Params p, hipStream_t st) {
   if (!GATED && p.ydt == 0) {
     // fp32 results: smaller tiles for the largest shapes, since the converted operands take registers
     switch (plan.shape) {
-      case 0: case 1: case 2: e = launch_tile8<Tile8<4, 4, 2, 2, 2>, true, false>(p, st); break;
-      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4>, true, false>(p, st); break;
-      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4>, true, false>(p, st); break;
+      case 0: case 1: case 2: e = launch_tile8<Tile8<4, 4, 2, 2, 2, false>, true, false>(p, st); break;
+      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4, true>, true, false>(p, st); break;
+      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4, true>, true, false>(p, st); break;
     }
   } else {
     switch (plan.shape) {
-      case 0: e = launch_tile8<Tile8<4, 8, 4, 2, 2>, false, GATED>(p, st); break;
-      case 1: e = launch_tile8<Tile8<4, 4, 4, 2, 3>, false, GATED>(p, st); break;
-      case 2: e = launch_tile8<Tile8<4, 4, 2, 2, 4>, false, GATED>(p, st); break;
-      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4>, false, GATED>(p, st); break;
-      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4>, false, GATED>(p, st); break;
+      case 0: e = launch_tile8<Tile8<4, 8, 4, 2, 2, false>, false, GATED>(p, st); break;
+      case 1: e = launch_tile8<Tile8<4, 4, 4, 2, 3, false>, false, GATED>(p, st); break;
+      case 2: e = launch_tile8<Tile8<2, 4, 4, 2, 4, true>, false, GATED>(p, st); break;
+      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4, true>, false, GATED>(p, st); break;
+      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4, true>, false, GATED>(p, st); break;
     }
   }
   if (e != hipSuccess || plan.slices == 1) return e;
