@@ -51,8 +51,10 @@ __device__ __forceinline__ uint32_t fp8_pack2(float a, float b, uint32_t old) {
 // A block's scale, fp32(amax / 448), and its reciprocal, both correctly rounded: the quotient as
 // below (equal to the division for every 16-bit amax in the range), the reciprocal by one Newton step from
 // the hardware's, except where the scale's significand is all ones. A block of zeros has 0 for both.
+// sign: the bit that codes take over from their values, none in a block of zeros.
 struct Fp8Scale {
   float s, r;
+  uint32_t sign;
   bool fast;
 };
 __device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
@@ -65,6 +67,7 @@ __device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
   const bool in_range = v.s >= 0x1p-80f && v.s <= 0x1p100f;
   v.fast = zeros || (in_range && (__float_as_uint(v.s) & 0x7fffffu) != 0x7fffffu);
   if (!zeros && !in_range) v.s = __fdiv_rn(amax, kE4m3Max);
+  v.sign = zeros ? 0u : 0x80000000u;
   return v;
 }
 
@@ -72,7 +75,8 @@ __device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
 // zeros, a NaN stays one (the comparisons below pass it on). The quotient without a division:
 // q = fl(x r) is within an ulp, its residual x - q s is exact in one fma, and fl(q + residual r)
 // is the correctly rounded quotient (Markstein; equal to the division for every pair of
-// significands of a scale and a 16-bit value). Scales outside [2^-80, 2^100], where the residual
+// significands of a scale and a 16-bit value), but for x = -0, whose residual is +0 and whose q that
+// makes +0: the sign comes from x. Scales outside [2^-80, 2^100], where the residual
 // might not be exact, take the division. Rounding 448 (1 + 2^-24) to e4m3 gives 448 by itself.
 // 4096 x 7168 rows: 28.7 us with divisions, 19 us so.
 template <bool XF16>
@@ -83,7 +87,8 @@ __device__ __forceinline__ uint2 fp8_quant8(const u32x4& v, const Fp8Scale& scal
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float q = f[i] * scale.r;
-      f[i] = fmaf(fmaf(-q, scale.s, f[i]), scale.r, q);
+      const float c = fmaf(fmaf(-q, scale.s, f[i]), scale.r, q);
+      f[i] = __uint_as_float((__float_as_uint(c) & ~scale.sign) | (__float_as_uint(f[i]) & scale.sign));
     }
   } else {
 #pragma unroll

@@ -452,8 +452,8 @@ int cubic_linear_w8a8(const void* x, int x_dtype, int64_t M, const cubic_weight_
  * cubic_quant_fp8: x bf16 or fp16 [M][K] -> xq e4m3 [M][K] and scales fp32
  * [ceil(M / block_rows)][ceil(K / 128)], block_rows 1 (activations) or 128 (weights);
  * blocks at the edges are cut. amax = max |x| of the block, scale = fp32(amax / 448) (IEEE
- * division), xq = e4m3(fp32(x / scale)) to nearest, ties to even, at most 448 in magnitude.
- * A scale of zero gives codes of zero; a non-finite value makes its block's scale non-finite
+ * division), xq = e4m3(fp32(x / scale)) to nearest, ties to even, at most 448 in magnitude, with
+ * x's sign, zeros too. A scale of zero gives codes of +0; a non-finite value makes its block's scale non-finite
  * and some of its codes NaN. Bit-exact. K a positive multiple of 16 up to 2^20, M below 2^24
  * (CUBIC_ERR_SHAPE); CUBIC_ERR_OPTION for another block_rows. M == 0 is a no-op. */
 int cubic_quant_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int block_rows,
