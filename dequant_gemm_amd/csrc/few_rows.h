@@ -23,10 +23,10 @@
 
 namespace cubic {
 
-enum FewKind { kFewBf16, kFewF16, kFewFp8, kFewFp8Exact };   // Exact: fp8 on the bf16 MFMA
+enum FewKind { kFewBf16, kFewF16, kFewFp8 };
 
 struct FewParams {
-  const void* x;           // 16 bits [M][K]; fp8: codes, or with WHOLE 16-bit values to quantise
+  const void* x;           // 16 bits [M][K]; fp8: codes, or with WHOLE or QUANT 16-bit values to quantise
   const float* xs;         // fp8: [M][kb]
   const void* w;           // [N][K], gated: N gate rows and N up rows
   const float* ws;         // fp8: [ceil(rows / 128)][kb]
@@ -55,11 +55,7 @@ __device__ __forceinline__ f32x4 few_dot(const i32x4& a, const i32x4& b, f32x4 c
     for (int s = 0; s < 2; ++s) {
       const u32x2 u{static_cast<uint32_t>(a[2 * s]), static_cast<uint32_t>(a[2 * s + 1])};
       const u32x2 v{static_cast<uint32_t>(b[2 * s]), static_cast<uint32_t>(b[2 * s + 1])};
-      if constexpr (KIND == kFewFp8Exact) {
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(u), e4m3x8_to_bf16(v), c, 0, 0, 0);
-      } else {
-        c = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(__builtin_bit_cast(long, u), __builtin_bit_cast(long, v), c, 0, 0, 0);
-      }
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(u), e4m3x8_to_bf16(v), c, 0, 0, 0);   // exact products
     }
     return c;
   }
@@ -71,7 +67,7 @@ __device__ __forceinline__ f32x4 few_dot(const i32x4& a, const i32x4& b, f32x4 c
 template <int KIND, int MT, int NT, bool WHOLE, bool GATED, bool XF16, bool QUANT>
 __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr bool F8 = KIND == kFewFp8 || KIND == kFewFp8Exact;
+  constexpr bool F8 = KIND == kFewFp8;
   constexpr int SPC = 4 / MT, PM = 4, kCode = F8 ? 1 : 2;
   constexpr int RM = WHOLE ? 4 : 16 * MT;      // activation rows held in LDS
   constexpr int kChunk = 65536, kScales = F8 && !WHOLE ? 2048 : 0;   // of a chunk: bytes, and of their scales
@@ -333,7 +329,7 @@ __global__ __launch_bounds__(1024) void k_few_rows(FewParams p) {
 template <int KIND, int MT, int NT, bool WHOLE, bool GATED, bool XF16, bool QUANT>
 hipError_t launch_few_k(const FewParams& p, hipStream_t st) {
   auto kern = k_few_rows<KIND, MT, NT, WHOLE, GATED, XF16, QUANT>;
-  constexpr bool F8 = KIND == kFewFp8 || KIND == kFewFp8Exact;
+  constexpr bool F8 = KIND == kFewFp8;
   const int nsteps = static_cast<int>((p.K * (F8 ? 1 : 2) + 63) / 64);
   const int red = kFewWaves * NT * 16 * MT * 16 * 4;
   const int x = WHOLE ? nsteps * 256 + (F8 ? static_cast<int>((p.K + 127) / 128) * 16 : 0) : 2 * (65536 + (F8 ? 2048 : 0));
@@ -350,7 +346,7 @@ hipError_t launch_few_k(const FewParams& p, hipStream_t st) {
 // p.x holds 16-bit rows to quantise a chunk at a time.
 template <int KIND, bool GATED>
 hipError_t launch_few(FewParams p, bool whole, bool quant, bool xf16, hipStream_t st) {
-  constexpr bool F8 = KIND == kFewFp8 || KIND == kFewFp8Exact;
+  constexpr bool F8 = KIND == kFewFp8;
   const int64_t cu = device_cu_count() > 0 ? device_cu_count() : 256;
   // equal shares of the columns, at most two tiles of 16 rows a workgroup
   const int64_t most = GATED ? 16 : 32;
@@ -370,7 +366,7 @@ hipError_t launch_few(FewParams p, bool whole, bool quant, bool xf16, hipStream_
     constexpr int MT = decltype(mt_c)::value;
     constexpr bool WHOLE = decltype(whole_c)::value, XF16 = decltype(xf16_c)::value, QUANT = decltype(quant_c)::value;
     // (e4m3 operands of two tiles by more rows than this go to the tile kernel: registers)
-    constexpr bool kTwo = !F8 || MT == 1 || (MT == 2 && KIND == kFewFp8 && !QUANT);
+    constexpr bool kTwo = !F8 || MT == 1;
     if constexpr (kTwo) {
       if (nt == 2) return launch_few_k<KIND, MT, 2, WHOLE, GATED, XF16, QUANT>(p, st);
     }

@@ -5,28 +5,24 @@
 //
 // (Block-scaled 8-bit weights of the dense parts beside the routed experts.) An e4m3 value is
 // exact in bf16 (three fraction bits, exponents -9 to 8), so a block's dot product on the bf16
-// MFMA has exact products and fp32 sums: that serves fp32 results. 16-bit results take the 8-bit
-// MFMA, twice as fast and off by 1.3e-5 to 2.2e-5 in the 2-norm.
+// MFMA has exact products and fp32 sums. The 8-bit MFMA, twice as fast, drops what lies below
+// about 2^-14 of the largest of the products that it adds: its sums are off by 1.3e-5 to 2.2e-5
+// in the 2-norm, and where large products cancel what is left may be lost whole.
 //
 // k_quant_fp8_rows, k_quant_fp8_blocks: bound by HBM. 4096 x 7168 rows: 19 us cold, 12 us beside a
 // product (88 MB; 17 us at the 5.1 TB/s of a large copy).
 //
-// Few rows (few_rows.h): 1 x 6144 x 7168 from bf16 10.5 us a call (44 MB: 8.6 us), 16 rows 12.2 us.
+// Few rows (few_rows.h): 1 x 6144 x 7168 from bf16 10.7 us a call (44 MB: 8.6 us), 16 rows 12.6 us.
 //
 // k_fp8_tile (more rows; bound by the MFMA and the power it takes): 256 x 256 tiles of eight
 // waves, 64 x 128 each, both operands straight into two LDS stages of 128 codes, one block of
-// scales; A's fragments stay in registers through a stage, B's come one by one, and each
-// 16 x 16 x 128 result goes into the sums by four fmas with the row's scale times the block's.
-// Measured: 4096 x 4096 x 7168 in 105-112 us (2.1-2.3 PFLOP/s; the library's product without
-// block scales 80 us), MFMA busy 51 % of the cycles at 2.0 GHz; 4096 x 6144 x 7168 187-203 us
-// (library 124). On zeros 87-90 us (library 60): the clock falls with the power of real operands.
-// Smaller tiles hold a stage's fragments ahead, with the ring's slots known to the compiler:
-// 100 x 6144 x 7168 22.2 -> 18.0 us, 256 rows 28 -> 24, 512 rows (128 x 128 tiles, also eight waves
-// instead of four) 42 -> 33, gated 256 x 7168 x 2048 26 -> 21.6.
-// Without the fmas 98 us. Not faster: operands through registers (110-116 us), 256 x 192 tiles in
-// whole rounds (186 us against 187), B's blocks read three ahead (spills 66 registers; 1 to 3 %
-// in the smaller tiles), results added 1 to 5 MFMAs later, the stage's loads issued at once, 256 x
-// 128 tiles by four waves of 128 x 64 (2048 x 4096 x 7168: 87 us against 71).
+// scales; A's fragments stay in registers through a stage, B's come one by one, both are
+// converted there, and each 16 x 16 x 128 result goes into the sums by four fmas with the row's
+// scale times the block's. Measured: 4096 x 4096 x 7168 in 171-179 us (1.34-1.4 PFLOP/s; the library's
+// product in bf16 160 us). Smaller tiles: 256 x 128 in two rounds 202-215 us, 128 x 128 226, 64 x 64
+// 275; the smaller ones hold a stage's fragments ahead, with the ring's slots known to the
+// compiler. Not faster: 128 x 128 by four waves (215 us, but 512 x 6144 x 7168 66 us against 52), 256 x 128
+// by waves of 128 x 32 (278 us, spills), 256 x 128 with a ring of two or as 128 x 256 (202).
 #include <algorithm>
 
 #include "common.h"
@@ -108,28 +104,21 @@ struct Tile8 {
   static_assert(kRing >= 2 && kLds <= 160 * 1024, "one compute unit's LDS");
 };
 
-// One 16 x 16 block of results over the 128 codes of a stage. EXACT: on the bf16 MFMA, whose
-// products and sums of such codes are those of fp32; else on the 8-bit one, twice as fast,
-// which drops what lies below about 2^-14 of the largest of the products that it adds
-// (2-norm of the sums off by 1.3e-5 to 2.2e-5: far below a 16-bit result's own rounding).
-template <bool EXACT>
+// One 16 x 16 block of results over the 128 codes of a stage. Codes that several blocks share are
+// converted once, as far as registers allow.
 __device__ __forceinline__ f32x4 fp8_dot(const i32x8& a, const i32x8& b) {
   f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (EXACT) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(a[2 * s]), static_cast<uint32_t>(a[2 * s + 1])}),
-          e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(b[2 * s]), static_cast<uint32_t>(b[2 * s + 1])}), part, 0, 0, 0);
-  } else {
-    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part, 0, 0, 0, 0, 0, 0);   // the form without scales
-  }
+  for (int s = 0; s < 4; ++s)
+    part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(a[2 * s]), static_cast<uint32_t>(a[2 * s + 1])}),
+        e4m3x8_to_bf16(u32x2{static_cast<uint32_t>(b[2 * s]), static_cast<uint32_t>(b[2 * s + 1])}), part, 0, 0, 0);
   return part;
 }
 
 // (AHEAD: two waves a SIMD, without which the compiler takes 330 registers, one workgroup to a
 // compute unit, and up to 10 % more time)
-template <class Shape, bool EXACT, bool GATED>
+template <class Shape, bool GATED>
 __global__ __launch_bounds__(64 * Shape::W, Shape::kAhead ? 2 : 1) void k_fp8_tile(Fp8Params p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
@@ -208,7 +197,9 @@ __global__ __launch_bounds__(64 * Shape::W, Shape::kAhead ? 2 : 1) void k_fp8_ti
   auto read_wscale = [&](int s, int b) { return *reinterpret_cast<const float*>(stage_at(s) + kSOff + 4 * (TM + b)); };
 
   f32x4 acc[MB][NB] = {};
-  constexpr int Q = MB * NB, kLag = 3;         // results are added this many MFMAs later
+  // results are added this many blocks later (gated 256 x 256 with three spills 8 registers: 208 us of
+  // 4096 x 7168 x 2048 against 194)
+  constexpr int Q = MB * NB, kLag = GATED ? 2 : 3;
   static_assert(NB % 2 == 0, "fb[0] holds a stage's first block again");
   if constexpr (Shape::kAhead) {
     // Stage s: at its start the loads of the next stage are in LDS, and every wave has read this
@@ -284,7 +275,7 @@ __global__ __launch_bounds__(64 * Shape::W, Shape::kAhead ? 2 : 1) void k_fp8_ti
       };
       times(I0{}, std::integral_constant<int, Q>{}, [&](auto t_c) {
         constexpr int t = decltype(t_c)::value;
-        part[t % (kLag + 1)] = fp8_dot<EXACT>(fb[u][t / MB], fa[u][t % MB]);
+        part[t % (kLag + 1)] = fp8_dot(fb[u][t / MB], fa[u][t % MB]);
         // in the first three quarters, so that they have arrived at the barrier
 #pragma unroll
         for (int r = t * kReads / kOver; r < (t + 1) * kReads / kOver && r < kReads; ++r)
@@ -348,7 +339,7 @@ __global__ __launch_bounds__(64 * Shape::W, Shape::kAhead ? 2 : 1) void k_fp8_ti
         } else if (i == 0) {
           fb[(j + 1) & 1] = read_b(s, j + 1);
         }
-        part[t % (kLag + 1)] = fp8_dot<EXACT>(fb[j & 1], fa[i]);
+        part[t % (kLag + 1)] = fp8_dot(fb[j & 1], fa[i]);
         if (j == NB - 1) {
           fa[i] = read_a(s + 1, i);
           sx[i] = read_scale(s + 1, i);
@@ -404,7 +395,7 @@ __global__ __launch_bounds__(64 * Shape::W, Shape::kAhead ? 2 : 1) void k_fp8_ti
       }
       return v;
     };
-    if constexpr (EXACT) {
+    if (p.ydt == 0) {
       tile_write<16, MB, NB, WM, WN, 4, Shape::kLds>(smem, p.y, 0, N, m0, p.M, n0, N, value);
     } else {
       tile_write<16, MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, N, m0, p.M, n0, N, value);
@@ -412,9 +403,9 @@ __global__ __launch_bounds__(64 * Shape::W, Shape::kAhead ? 2 : 1) void k_fp8_ti
   }
 }
 
-template <class Shape, bool EXACT, bool GATED>
+template <class Shape, bool GATED>
 hipError_t launch_tile8(const Fp8Params& p, hipStream_t st) {
-  auto kern = k_fp8_tile<Shape, EXACT, GATED>;
+  auto kern = k_fp8_tile<Shape, GATED>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), Shape::kLds);
   if (e != hipSuccess) return e;
   const int64_t N = GATED ? p.N / 2 : p.N, TC = GATED ? Shape::TN / 2 : Shape::TN;
@@ -432,21 +423,12 @@ hipError_t launch_fp8_tiles(Fp8Params p, hipStream_t st) {
   const TilePlan plan = plan8(p.M, p.N, p.K);
   p.slices = plan.slices;
   hipError_t e;
-  if (!GATED && p.ydt == 0) {
-    // fp32 results: smaller tiles for the largest shapes, since the converted operands take registers
-    switch (plan.shape) {
-      case 0: case 1: case 2: e = launch_tile8<Tile8<4, 4, 2, 2, 2, false>, true, false>(p, st); break;
-      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4, true>, true, false>(p, st); break;
-      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4, true>, true, false>(p, st); break;
-    }
-  } else {
-    switch (plan.shape) {
-      case 0: e = launch_tile8<Tile8<4, 8, 4, 2, 2, false>, false, GATED>(p, st); break;
-      case 1: e = launch_tile8<Tile8<4, 4, 4, 2, 3, false>, false, GATED>(p, st); break;
-      case 2: e = launch_tile8<Tile8<2, 4, 4, 2, 4, true>, false, GATED>(p, st); break;
-      case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4, true>, false, GATED>(p, st); break;
-      default: e = launch_tile8<Tile8<2, 2, 2, 2, 4, true>, false, GATED>(p, st); break;
-    }
+  switch (plan.shape) {
+    case 0: e = launch_tile8<Tile8<4, 8, 4, 2, 2, false>, GATED>(p, st); break;
+    case 1: e = launch_tile8<Tile8<4, 4, 4, 2, 3, false>, GATED>(p, st); break;
+    case 2: e = launch_tile8<Tile8<2, 4, 4, 2, 4, true>, GATED>(p, st); break;
+    case 3: e = launch_tile8<Tile8<2, 4, 2, 2, 4, true>, GATED>(p, st); break;
+    default: e = launch_tile8<Tile8<2, 2, 2, 2, 4, true>, GATED>(p, st); break;
   }
   if (e != hipSuccess || plan.slices == 1) return e;
   return launch_tile_join<GATED>({p.part, plan.slices, p.M, GATED ? p.N / 2 : p.N, p.N, p.bias, p.y, p.ydt, p.gelu, nullptr}, st);
@@ -487,18 +469,15 @@ FewParams few_params(const Fp8Params& p, bool gated) {
 }
 }  // namespace
 
-// Rows that the streaming kernel takes. Measured against the tiles (N x K, 16-bit results, us): 16
-// rows 6144 x 7168 12.2 against 14.1, 32 rows 15.1 against 14.1, 7168 x 2048 7.8 against 8.8; 64
-// rows 4096 x 4096 11.2 against 11.1, 1003 x 1936 7.6 against 9.8, 1024 x 8192 15.3 against 11.9,
-// 6144 x 7168 27.5 against 15.0. fp32 results, 32 rows, 6144 x 7168: 19.1 against 16.7. wide: a
-// workgroup would have two tiles of weight rows.
+// Rows that the streaming kernel takes. Measured against the tiles (N x K, us): 16 rows 6144 x 7168
+// 12.2 against 14.1, 32 rows 19.1 against 16.7, 7168 x 2048 7.8 against 8.8; 64 rows 4096 x 4096 11.2
+// against 11.1, 1003 x 1936 7.6 against 9.8, 1024 x 8192 15.3 against 11.9. wide: a workgroup would have two
+// tiles of weight rows.
 constexpr int64_t kFewAlways = 16;
 
 static bool fp8_wide(int64_t N) { return N > 16 * plan_cus(); }
-static bool fp8_few(int64_t M, int64_t N, int64_t K, bool exact) {
-  if (M <= kFewAlways) return true;
-  if (M <= 32) return !(fp8_wide(N) && exact);
-  return M <= kFewMaxM && !fp8_wide(N) && K <= 4096;
+static bool fp8_few(int64_t M, int64_t N, int64_t K) {
+  return M <= kFewAlways || (!fp8_wide(N) && (M <= 32 || (M <= kFewMaxM && K <= 4096)));
 }
 
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewAlways ? 0 : plan_bytes(plan8(M, N, K), M, N); }
@@ -511,19 +490,16 @@ static bool fp8_whole(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFe
 // 12.0 and 11.5 against 9.3; 16 x 7168 13.6 and 13.0 against 10.4 and 11.4. Wide: 16 x 2048, N 7168,
 // 10.2 and 9.7 against 9.2; 8 x 7168, N 6144, 15.3 and 14.8 against 14.1 and 13.6.
 bool fp8_quantises(int64_t M, int64_t N, int64_t K) {
-  return fp8_whole(M, K) || (fp8_few(M, N, K, true) && M * K <= (fp8_wide(N) ? 40 : 80) * 1024);
+  return fp8_whole(M, K) || (fp8_few(M, N, K) && M * K <= (fp8_wide(N) ? 40 : 80) * 1024);
 }
 
 hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st) {
-  if (!fp8_few(p.M, p.N, p.K, p.ydt == 0)) return launch_fp8_tiles<false>(p, st);
-  const FewParams f = few_params(p, false);
-  const bool whole = p.x && fp8_whole(p.M, p.K);
-  return p.ydt == 0 ? launch_few<kFewFp8Exact, false>(f, whole, p.x != nullptr, xf16, st)
-                    : launch_few<kFewFp8, false>(f, whole, p.x != nullptr, xf16, st);
+  if (!fp8_few(p.M, p.N, p.K)) return launch_fp8_tiles<false>(p, st);
+  return launch_few<kFewFp8, false>(few_params(p, false), p.x && fp8_whole(p.M, p.K), p.x != nullptr, xf16, st);
 }
 
 hipError_t launch_fp8_gated(const Fp8Params& p, bool xf16, hipStream_t st) {
-  if (!fp8_few(p.M, p.N, p.K, false)) return launch_fp8_tiles<true>(p, st);
+  if (!fp8_few(p.M, p.N, p.K)) return launch_fp8_tiles<true>(p, st);
   return launch_few<kFewFp8, true>(few_params(p, true), p.x && fp8_whole(p.M, p.K), p.x != nullptr, xf16, st);
 }
 

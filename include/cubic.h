@@ -470,11 +470,8 @@ typedef struct cubic_weight_fp8 {
 /* y[m][n] = sum over blocks kb of x_scale[m][kb] * w->scales[n / 128][kb] * (sum of xq[m][k] *
  * w->codes[n][k] in the block) (+ bias[n]), for xq e4m3 [M][K] and x_scale fp32
  * [M][ceil(K / 128)] of cubic_quant_fp8. y [M][N] in CUBIC_DTYPE_F32, _BF16 or _F16, rounded
- * once; bias fp32 [N] or NULL. fp32 results: a block's products are exact, its sum and the sum
- * over blocks fp32, the product of the two scales rounded to fp32 first. 16-bit results: the same,
- * but a block's sum runs on the 8-bit MFMA, which drops what lies below about 2^-14 of the largest
- * of the products that it adds (the 2-norm of the results is off by 1.3e-5 to 2.2e-5, a hundredth
- * of a bf16 result's own rounding and a tenth of an fp16 one's). The result does not depend on
+ * once; bias fp32 [N] or NULL. A block's products are exact, its sum and the sum over blocks fp32,
+ * the product of the two scales rounded to fp32 first. The result does not depend on
  * timing, but its last bits may differ with the number of rows. Codes of NaN and non-finite
  * scales make what they enter non-finite. K a positive multiple of 16 up to 2^20, M and N below
  * 2^24; M == 0 or N == 0 is a no-op. `workspace` may be NULL where the size query gives 0; calls
