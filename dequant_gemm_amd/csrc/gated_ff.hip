@@ -402,6 +402,7 @@ __global__ __launch_bounds__(64 * Shape::W) void k_ff_backward(TileParams dx, Ti
 }
 
 constexpr int kKS = 4;                         // a stage's steps, in every shape
+constexpr TileCosts kCosts16 = {{3232, 1752, 1190, 908, 626}, 626};   // for the plans
 // f(shape) with shape k of kTileShapes
 template <class F>
 hipError_t with_shape(int k, F f) {
@@ -415,7 +416,7 @@ hipError_t with_shape(int k, F f) {
 }
 
 int64_t stages16(int64_t K) { return (K + 16 * kKS - 1) / (16 * kKS); }
-TilePlan plan_forward(int64_t M, int64_t H, int64_t I) { return plan_tiles(M, 2 * I, stages16(H), kKS / 2); }
+TilePlan plan_forward(int64_t M, int64_t H, int64_t I) { return plan_tiles(M, 2 * I, stages16(H), kCosts16); }
 
 // Both products in one launch, where they share a shape and fill each other's rounds, or each
 // in its own. Does not depend on which of them is asked for, and so neither do the results.
@@ -424,12 +425,12 @@ struct BackwardPlan {
   bool together;
 };
 BackwardPlan plan_backward(int64_t M, int64_t H, int64_t I) {
-  const int64_t cu = plan_cus(), sx = stages16(2 * I), sw = stages16(M), unit = kKS / 2;
+  const int64_t cu = plan_cus(), sx = stages16(2 * I), sw = stages16(M);
   BackwardPlan one{}, two{};
   int64_t cost1 = INT64_MAX, costx = INT64_MAX, costw = INT64_MAX;
   for (int k = 0; k < kTileShapeCount; ++k) {
     int64_t cx, cw;
-    const TilePlan x = plan_shape(k, cu, M, H, sx, unit, &cx), w = plan_shape(k, cu, 2 * I, H, sw, unit, &cw);
+    const TilePlan x = plan_shape(k, cu, M, H, sx, kCosts16, &cx), w = plan_shape(k, cu, 2 * I, H, sw, kCosts16, &cw);
     if (cx < costx) {
       costx = cx;
       two.dx = x;
@@ -439,7 +440,7 @@ BackwardPlan plan_backward(int64_t M, int64_t H, int64_t I) {
       two.dw = w;
     }
     const int64_t nx = plan_tile_count(k, M, H) * x.slices, nw = plan_tile_count(k, 2 * I, H) * w.slices;
-    const int64_t tx = plan_workgroup(k, (sx + x.slices - 1) / x.slices, unit), tw = plan_workgroup(k, (sw + w.slices - 1) / w.slices, unit);
+    const int64_t tx = plan_workgroup(k, (sx + x.slices - 1) / x.slices, kCosts16, false), tw = plan_workgroup(k, (sw + w.slices - 1) / w.slices, kCosts16, false);
     // workgroups follow each other without waiting for a round; the last ones run half alone
     const int64_t longest = std::max(tx, tw);
     const int64_t c = std::max(longest, (nx * tx + nw * tw) / cu + longest / 2) + plan_join(x.slices, M, H) + plan_join(w.slices, 2 * I, H);

@@ -170,13 +170,15 @@ struct TilePlan {
 constexpr int kTileShapes[][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 128}, {64, 64}};
 constexpr int kTileShapeCount = 5, kMaxSlices = 32;
 
-// What the plans go by, in cycles: a workgroup's time in shape k over `len` steps of 64 `unit`
-// bytes of the contraction, the larger of its MFMA and its LDS and load cycles as measured
-// (1.55 and 2.2 times the peaks': 256 x 256 tiles 3200 a step of 128 bytes, 128 x 128 1200, 64 x
-// 128 650 to 900), and its start and end (17000 and 8000 measured for the first two).
-inline int64_t plan_workgroup(int k, int64_t len, int64_t unit) {
-  const int64_t tm = kTileShapes[k][0], tn = kTileShapes[k][1];
-  return len * (std::max(tm * tn * 99 / 4096, (tm + tn) * 11 / 5) * unit + 64) + 5000 + tm * tn / 6;
+// What the plans go by: cycles of a workgroup in each shape over a step of 128 bytes of the rows
+// (64 values of 16 bits or 128 codes), as measured with every compute unit at work, and those of the
+// last shape, two of which share a compute unit, where it has one to itself; a workgroup's start
+// and end (17000 and 8000 measured for the first two shapes) come on top.
+struct TileCosts {
+  int64_t step[kTileShapeCount], last_alone;
+};
+inline int64_t plan_workgroup(int k, int64_t len, const TileCosts& c, bool alone) {
+  return len * (alone && k == kTileShapeCount - 1 ? c.last_alone : c.step[k]) + 5000 + kTileShapes[k][0] * kTileShapes[k][1] / 6;
 }
 inline int64_t plan_tile_count(int k, int64_t M, int64_t width) {
   return ((M + kTileShapes[k][0] - 1) / kTileShapes[k][0]) * ((width + kTileShapes[k][1] - 1) / kTileShapes[k][1]);
@@ -187,15 +189,15 @@ inline int64_t plan_join(int slices, int64_t M, int64_t width) { return slices >
 
 // The slices of least time for shape k, M rows, `width` columns of operand B and `stages` steps:
 // rounds of workgroups over the compute units, and the join. No slice is empty.
-inline TilePlan plan_shape(int k, int64_t cu, int64_t M, int64_t width, int64_t stages, int64_t unit, int64_t* cost) {
+inline TilePlan plan_shape(int k, int64_t cu, int64_t M, int64_t width, int64_t stages, const TileCosts& costs, int64_t* cost) {
   const int64_t tiles = plan_tile_count(k, M, width);
   TilePlan best{k, 1};
   *cost = INT64_MAX;
   for (int s = 1; s <= kMaxSlices; ++s) {
-    if (s > 1 && (stages * unit < 4 * s || tiles * s > 2 * cu)) break;
+    if (s > 1 && (stages < 2 * s || tiles * s > 2 * cu)) break;
     const int64_t len = (stages + s - 1) / s;
     if (len * (s - 1) >= stages) continue;
-    const int64_t c = (tiles * s + cu - 1) / cu * plan_workgroup(k, len, unit) + plan_join(s, M, width);
+    const int64_t c = (tiles * s + cu - 1) / cu * plan_workgroup(k, len, costs, tiles * s <= cu) + plan_join(s, M, width);
     if (c < *cost) {
       *cost = c;
       best.slices = s;
@@ -203,13 +205,13 @@ inline TilePlan plan_shape(int k, int64_t cu, int64_t M, int64_t width, int64_t 
   }
   return best;
 }
-inline TilePlan plan_tiles(int64_t M, int64_t width, int64_t stages, int64_t unit) {
+inline TilePlan plan_tiles(int64_t M, int64_t width, int64_t stages, const TileCosts& costs) {
   const int64_t cu = plan_cus();
   TilePlan best{};
   int64_t cost = INT64_MAX;
   for (int k = 0; k < kTileShapeCount; ++k) {
     int64_t c;
-    const TilePlan t = plan_shape(k, cu, M, width, stages, unit, &c);
+    const TilePlan t = plan_shape(k, cu, M, width, stages, costs, &c);
     if (c < cost) {
       cost = c;
       best = t;
