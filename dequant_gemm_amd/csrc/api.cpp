@@ -960,6 +960,10 @@ int check_ff(int64_t M, int64_t H, int64_t I, int dtype, int act) {
   if (act != CUBIC_ACT_SILU && act != CUBIC_ACT_GELU_TANH) return CUBIC_ERR_OPTION;
   return CUBIC_OK;
 }
+// The backward pass's workspace (its size does not ask for the type): dg and du in 16 bits, in fp16 twice, and the largest
+// magnitudes of their rows and columns.
+size_t ff_dpre_bytes(int64_t M, int64_t I) { return align256(static_cast<size_t>(M) * I * 4); }
+size_t ff_range_bytes(int64_t M, int64_t I) { return align256((static_cast<size_t>(M) + 2 * I) * 4); }
 }  // namespace
 
 CUBIC_API size_t cubic_gated_ff_workspace_bytes(int64_t M, int64_t H, int64_t I) {
@@ -991,7 +995,7 @@ CUBIC_API int cubic_gated_ff(const void* x, const void* w, int dtype, int64_t M,
 
 CUBIC_API size_t cubic_gated_ff_backward_workspace_bytes(int64_t M, int64_t H, int64_t I) {
   if (M <= 0 || H <= 0 || I <= 0) return 0;
-  return align256(static_cast<size_t>(M) * I * 4) + gated_ff_backward_part_bytes(M, H, I);
+  return 2 * ff_dpre_bytes(M, I) + ff_range_bytes(M, I) + gated_ff_backward_part_bytes(M, H, I);
 }
 
 CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void* w, const float* pre, int dtype, int64_t M, int64_t H,
@@ -1018,8 +1022,11 @@ CUBIC_API int cubic_gated_ff_backward(const void* dh, const void* x, const void*
   p.gelu = act == CUBIC_ACT_GELU_TANH ? 1 : 0;
   p.pre = const_cast<float*>(pre);
   p.dh = static_cast<const uint16_t*>(dh);
-  p.dpre = static_cast<uint16_t*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(static_cast<size_t>(M) * I * 4));
+  char* ws = static_cast<char*>(workspace);
+  p.dpre = reinterpret_cast<uint16_t*>(ws);
+  p.dpre_w = reinterpret_cast<uint16_t*>(ws + ff_dpre_bytes(M, I));
+  p.range = reinterpret_cast<uint32_t*>(ws + 2 * ff_dpre_bytes(M, I));
+  p.part = reinterpret_cast<float*>(ws + 2 * ff_dpre_bytes(M, I) + ff_range_bytes(M, I));
   p.dx = static_cast<uint16_t*>(dx);
   p.dw = static_cast<uint16_t*>(dw);
   return hip_status(launch_gated_ff_backward(p, s));

@@ -5,8 +5,11 @@
 //
 // (The gated block of the dense parts beside the routed experts, whose own form cubic_moe_mlp
 // computes.) All three products take 16-bit operands and keep fp32 sums. dg and du are rounded to
-// 16 bits on the way to the last two, as large an error as the results' own rounding; the
-// pre-activations between the passes are fp32, since theirs would come on top.
+// 16 bits on the way to the last two, as large an error as the results' own rounding (two 16-bit halves of
+// them would take the backward products of 4096 x 7168 x 2048 from 420 to 750 us); the
+// pre-activations between the passes are fp32, since theirs would come on top. In fp16 dg and du are scaled by powers of two,
+// each row's for dx and each column's for dw, which the results get back: they may lie outside the
+// type's range where dx and dw do not. That takes two more launches: 4096 x 2048 in 23 us.
 //
 // Up to 64 rows (few_rows.h): 1 x 7168 x 2048 (58.7 MB of weights) 10.6-11 us, 5.4 TB/s.
 //
@@ -17,7 +20,7 @@
 // for dw) lie in LDS as they are and come out through the transposing reads, so nothing is
 // transposed in memory. Measured, 4096 x 7168 x 2048 in bf16: forward 177-190 us (1.27-1.36
 // PFLOP/s; the library's product of that size alone 153-160 us), both products of the backward
-// pass 410-430 us (library 192 + 222), dpre 20 us (117 MB). MFMA busy 65 % of the cycles at 1.8 GHz;
+// pass 410-430 us (library 192 + 222), dpre 20 us (117 MB; fp16, two of them, 27). MFMA busy 65 % of the cycles at 1.8 GHz;
 // on zeros 128 us (library 110). Not faster: operands through registers (189 us; with a barrier
 // every 16 MFMAs 207), four waves of 128 x 128 (180), two workgroups of four waves to a compute unit
 // (245), rings of four stages of 32 k (213), the barrier later in the step, reads earlier, wave
@@ -33,6 +36,10 @@
 
 namespace cubic {
 namespace {
+
+// The power of two that brings magnitudes up to the one with these bits (0: none) below 2^15: what is
+// scaled by it keeps fp16's eleven bits down to 2^-29 of the largest one, and 2^-40 of it below.
+__device__ __forceinline__ int range_exp(uint32_t bits) { return bits == 0u ? 0 : static_cast<int>(bits >> 23) - 141; }
 
 // ---------------------------------------------------------------------------
 // C[m][n] = sum_k A(m, k) B(n, k) in 16-bit operands and fp32 sums. A(m, k) is a[m * lda + k],
@@ -51,6 +58,7 @@ struct TileParams {
   // [slices][M][N], gated [slices][M][2 N]
   int slices;
   float* part;
+  const uint32_t* range;   // SCALED: [M] bits of the largest magnitudes by which A's rows are scaled (range_exp)
 };
 
 // A tile's shape: WM x WN waves with MB x NB blocks of 32 x 32 each; stages of KS steps of 16 k,
@@ -206,7 +214,7 @@ __device__ __forceinline__ f32x16 mma(const s16x8& a, const s16x8& b, const f32x
 }
 
 // One workgroup's share: tile and slice `block`.
-template <class Shape, bool F16, bool AT, bool BT, bool GATED>
+template <class Shape, bool F16, bool AT, bool BT, bool GATED, bool SCALED>
 __device__ __forceinline__ void tile16(const TileParams& p, int block, unsigned char* smem) {
   constexpr int MB = Shape::MB, NB = Shape::NB, WM = Shape::WM, WN = Shape::WN, W = Shape::W;
   constexpr int TM = Shape::TM, TN = Shape::TN, TC = GATED ? TN / 2 : TN, LA = Shape::LA, LB = Shape::LB, NL = Shape::NL, KS = Shape::KS;
@@ -375,17 +383,29 @@ __device__ __forceinline__ void tile16(const TileParams& p, int block, unsigned 
       for (int e = 0; e < 4; ++e) v[e] = act_of(a[e], p.gelu).value * u[e];
       return v;
     });
-  } else if (p.slices > 1) {
-    tile_write<32, MB, NB, WM, WN, 4, Shape::kLds>(smem, p.part + static_cast<int64_t>(slice) * p.M * p.N, 0, p.N, m0, p.M, n0, p.N, quad);
   } else {
-    tile_write<32, MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.N, m0, p.M, n0, p.N, quad);
+    int back[MB];                              // A's rows as they were: powers of two, exact
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+      back[i] = SCALED ? range_exp(p.range[min(m0 + 32 * (wm * MB + i) + (static_cast<int>(threadIdx.x) & 31), p.M - 1)]) : 0;
+    auto value = [&](int i, int j, int g) {
+      f32x4 v = quad(i, j, g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = SCALED ? ldexpf(v[e], back[i]) : v[e];
+      return v;
+    };
+    if (p.slices > 1) {
+      tile_write<32, MB, NB, WM, WN, 4, Shape::kLds>(smem, p.part + static_cast<int64_t>(slice) * p.M * p.N, 0, p.N, m0, p.M, n0, p.N, value);
+    } else {
+      tile_write<32, MB, NB, WM, WN, 2, Shape::kLds>(smem, p.y, p.ydt, p.N, m0, p.M, n0, p.N, value);
+    }
   }
 }
 
 template <class Shape, bool F16>
 __global__ __launch_bounds__(64 * Shape::W) void k_ff_forward(TileParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  tile16<Shape, F16, false, false, true>(p, static_cast<int>(blockIdx.x), smem);
+  tile16<Shape, F16, false, false, true, false>(p, static_cast<int>(blockIdx.x), smem);
 }
 
 // The backward pass's two products in one launch, so that the compute units that the first one
@@ -395,9 +415,9 @@ __global__ __launch_bounds__(64 * Shape::W) void k_ff_backward(TileParams dx, Ti
   extern __shared__ __align__(16) unsigned char smem[];
   const int block = static_cast<int>(blockIdx.x);
   if (block < first) {
-    tile16<Shape, F16, false, true, false>(dx, block, smem);
+    tile16<Shape, F16, false, true, false, F16>(dx, block, smem);
   } else {
-    tile16<Shape, F16, true, true, false>(dw, block - first, smem);
+    tile16<Shape, F16, true, true, false, F16>(dw, block - first, smem);
   }
 }
 
@@ -457,27 +477,126 @@ int64_t tile_count(const TileParams& p, int64_t columns) {
   return ((p.M + Shape::TM - 1) / Shape::TM) * ((p.N + columns - 1) / columns) * p.slices;
 }
 
-// [dg | du] from pre and dh, in the operands' type: the products that follow take 16-bit
-// operands, and their results are 16-bit values of the same type.
+// dg and du of four neighbouring columns i of row m, in fp32.
+struct Dpre {
+  f32x4 dg, du;
+};
 template <bool F16>
-__global__ __launch_bounds__(256) void k_ff_dpre(const float* __restrict__ pre, const uint16_t* __restrict__ dh, int64_t M,
-                                                 int64_t I, int gelu, uint16_t* __restrict__ dpre) {
+__device__ __forceinline__ Dpre dpre_of(const float* __restrict__ pre, const uint16_t* __restrict__ dh, int64_t m, int64_t i, int64_t I, int gelu) {
+  const f32x4 g = *reinterpret_cast<const f32x4*>(pre + m * 2 * I + i), u = *reinterpret_cast<const f32x4*>(pre + m * 2 * I + I + i);
+  const uint2 d = *reinterpret_cast<const uint2*>(dh + m * I + i);
+  Dpre r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t bits = (e < 2 ? d.x : d.y) >> (16 * (e & 1)) & 0xffffu;
+    const float t = F16 ? static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits))) : __uint_as_float(bits << 16);
+    const Act a = act_of(g[e], gelu);
+    r.dg[e] = t * u[e] * a.slope;
+    r.du[e] = t * a.value;
+  }
+  return r;
+}
+
+// The largest finite magnitudes of every row and every column of [dg | du], as bits, into `rows`
+// [M] and `cols` [2 I], which hold zeros (the atomic maxima do not depend on their order). A lane has
+// four columns, a workgroup a run of `run` rows, a multiple of 16, its waves four of them at a time;
+// what the waves found in a column meets in LDS, since atomics are what takes time: 4096 x 2048 in
+// runs of 4, 16 and 64 rows: 89, 34 and 19 us (84 MB).
+__global__ __launch_bounds__(256) void k_ff_range(const float* __restrict__ pre, const uint16_t* __restrict__ dh, int64_t M, int64_t I,
+                                                  int gelu, int run, uint32_t* __restrict__ rows, uint32_t* __restrict__ cols) {
+  __shared__ uint32_t s_cols[2][256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t qs = I >> 2, qb = (qs + 63) / 64, jobs = (M + run - 1) / run * qb;
+  for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+    const int64_t mb = job / qb, q0 = (job - mb * qb) * 64;
+    const int64_t i = 4 * min(q0 + lane, qs - 1), end = min((mb + 1) * run, M);   // (lanes behind the last column take it too)
+    uint32_t cg[4] = {}, cu[4] = {};
+    for (int64_t m0 = mb * run + 4 * wave; m0 < end; m0 += 16) {
+      uint32_t top[4] = {};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const Dpre d = dpre_of<true>(pre, dh, min(m0 + r, M - 1), i, I, gelu);    // (the last row again)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          auto take = [&](float v, uint32_t& c) {
+            const uint32_t b = __float_as_uint(v) & 0x7fffffffu, f = b < 0x7f800000u ? b : 0u;
+            c = max(c, f);
+            top[r] = max(top[r], f);
+          };
+          take(d.dg[e], cg[e]);
+          take(d.du[e], cu[e]);
+        }
+      }
+#pragma unroll
+      for (int l = 32; l > 0; l >>= 1)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top[r] = max(top[r], static_cast<uint32_t>(__shfl_xor(static_cast<int>(top[r]), l, 64)));
+      if (lane < 4 && m0 + lane < M) {
+        const uint32_t t = lane == 0 ? top[0] : lane == 1 ? top[1] : lane == 2 ? top[2] : top[3];
+        if (t != 0u) atomicMax(rows + m0 + lane, t);
+      }
+    }
+    s_cols[0][threadIdx.x] = 0u;
+    s_cols[1][threadIdx.x] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      atomicMax(&s_cols[0][4 * lane + e], cg[e]);
+      atomicMax(&s_cols[1][4 * lane + e], cu[e]);
+    }
+    __syncthreads();
+    const int64_t col = 4 * q0 + threadIdx.x;
+    if (col < I) {
+      if (s_cols[0][threadIdx.x] != 0u) atomicMax(cols + col, s_cols[0][threadIdx.x]);
+      if (s_cols[1][threadIdx.x] != 0u) atomicMax(cols + I + col, s_cols[1][threadIdx.x]);
+    }
+    __syncthreads();                           // read before the next job's are written
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ void store_dpre(const f32x4& v, uint16_t* at) {
+  *reinterpret_cast<uint2*>(at) = make_uint2(bits16<F16>(v[0]) | bits16<F16>(v[1]) << 16, bits16<F16>(v[2]) | bits16<F16>(v[3]) << 16);
+}
+
+// [dg | du] from pre and dh, in the operands' type: the products that follow take 16-bit
+// operands, and their results are 16-bit values of the same type. In fp16 dg and du need not lie in the type's range
+// where dx and dw do, so there are two of them: with rows scaled by powers of two for dx, with
+// columns scaled for dw; either may be NULL.
+__global__ __launch_bounds__(256) void k_ff_dpre_bf16(const float* __restrict__ pre, const uint16_t* __restrict__ dh, int64_t M, int64_t I, int gelu,
+                                                      uint16_t* __restrict__ dpre) {
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256, quads = M * (I >> 2);
   for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < quads; v += step) {
     const int64_t m = v / (I >> 2), i = 4 * (v - m * (I >> 2));
-    const f32x4 g = *reinterpret_cast<const f32x4*>(pre + m * 2 * I + i), u = *reinterpret_cast<const f32x4*>(pre + m * 2 * I + I + i);
-    const uint2 d = *reinterpret_cast<const uint2*>(dh + m * I + i);
-    uint32_t dg[4], du[4];
+    const Dpre d = dpre_of<false>(pre, dh, m, i, I, gelu);
+    store_dpre<false>(d.dg, dpre + m * 2 * I + i);
+    store_dpre<false>(d.du, dpre + m * 2 * I + I + i);
+  }
+}
+__global__ __launch_bounds__(256) void k_ff_dpre_f16(const float* __restrict__ pre, const uint16_t* __restrict__ dh, int64_t M, int64_t I, int gelu,
+                                                     const uint32_t* __restrict__ rows, const uint32_t* __restrict__ cols, uint16_t* __restrict__ for_x,
+                                                     uint16_t* __restrict__ for_w) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256, quads = M * (I >> 2);
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < quads; v += step) {
+    const int64_t m = v / (I >> 2), i = 4 * (v - m * (I >> 2));
+    const Dpre d = dpre_of<true>(pre, dh, m, i, I, gelu);
+    auto store = [&](const f32x4& t, int64_t col) {
+      f32x4 s;
+      if (for_x) {
+        const int e0 = range_exp(rows[m]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t bits = (e < 2 ? d.x : d.y) >> (16 * (e & 1)) & 0xffffu;
-      const float t = F16 ? static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits))) : __uint_as_float(bits << 16);
-      const Act a = act_of(g[e], gelu);
-      dg[e] = bits16<F16>(t * u[e] * a.slope);
-      du[e] = bits16<F16>(t * a.value);
-    }
-    *reinterpret_cast<uint2*>(dpre + m * 2 * I + i) = make_uint2(dg[0] | dg[1] << 16, dg[2] | dg[3] << 16);
-    *reinterpret_cast<uint2*>(dpre + m * 2 * I + I + i) = make_uint2(du[0] | du[1] << 16, du[2] | du[3] << 16);
+        for (int e = 0; e < 4; ++e) s[e] = ldexpf(t[e], -e0);
+        store_dpre<true>(s, for_x + m * 2 * I + col);
+      }
+      if (for_w) {
+        const u32x4 c = *reinterpret_cast<const u32x4*>(cols + col);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = ldexpf(t[e], -range_exp(c[e]));
+        store_dpre<true>(s, for_w + m * 2 * I + col);
+      }
+    };
+    store(d.dg, i);
+    store(d.du, I + i);
   }
 }
 
@@ -514,7 +633,7 @@ hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
     return p.f16 ? launch_few<kFewF16, true>(f, whole, false, false, st) : launch_few<kFewBf16, true>(f, whole, false, false, st);
   }
   const TilePlan plan = plan_forward(p.M, p.H, p.I);
-  const TileParams t{p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, dt, p.pre, p.gelu, plan.slices, p.part};
+  const TileParams t{p.x, p.w, p.H, p.H, p.M, p.I, p.H, p.h, dt, p.pre, p.gelu, plan.slices, p.part, nullptr};
   const hipError_t e = with_shape(plan.shape, [&](auto shape) {
     using Shape = decltype(shape);
     auto kern = p.f16 ? k_ff_forward<Shape, true> : k_ff_forward<Shape, false>;
@@ -531,19 +650,14 @@ hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
 
 hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
   const unsigned quads = quad_grid(p.M, p.I);
-  if (p.f16) {
-    hipLaunchKernelGGL(k_ff_dpre<true>, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
-  } else {
-    hipLaunchKernelGGL(k_ff_dpre<false>, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const int dt = p.f16 ? 2 : 1;
   const BackwardPlan plan = plan_backward(p.M, p.H, p.I);
   float* part = p.part;
   float* part_w = reinterpret_cast<float*>(reinterpret_cast<char*>(part) + plan_bytes(plan.dx, p.M, p.H));
-  const TileParams x{p.dpre, p.w, 2 * p.I, p.H, p.M, p.H, 2 * p.I, p.dx, dt, nullptr, 0, plan.dx.slices, part};
-  const TileParams w{p.dpre, p.x, 2 * p.I, p.H, 2 * p.I, p.H, p.M, p.dw, dt, nullptr, 0, plan.dw.slices, part_w};
+  // the largest magnitudes of the columns, on 16 bytes, then of the rows
+  uint32_t *cols = p.range, *rows = p.range + 2 * p.I;
+  const TileParams x{p.dpre, p.w, 2 * p.I, p.H, p.M, p.H, 2 * p.I, p.dx, dt, nullptr, 0, plan.dx.slices, part, rows};
+  const TileParams w{p.f16 ? p.dpre_w : p.dpre, p.x, 2 * p.I, p.H, 2 * p.I, p.H, p.M, p.dw, dt, nullptr, 0, plan.dw.slices, part_w, cols};
   auto launch = [&](int shape_index, bool with_x, bool with_w) {
     if (!with_x && !with_w) return hipSuccess;
     return with_shape(shape_index, [&](auto shape) {
@@ -557,6 +671,24 @@ hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
       return hipGetLastError();
     });
   };
+  hipError_t e;
+  if (p.f16) {
+    e = launch_fill_zero(reinterpret_cast<float*>(p.range), p.M + 2 * p.I, false, st);
+    if (e != hipSuccess) return e;
+    // runs that give each compute unit two workgroups, of 16 rows at least
+    const int64_t wide = (p.I / 4 + 63) / 64, run = std::clamp<int64_t>(p.M * wide / (2 * plan_cus()) / 16 * 16, 16, 128);
+    const int64_t jobs = (p.M + run - 1) / run * wide;
+    hipLaunchKernelGGL(k_ff_range, dim3(static_cast<unsigned>(std::min<int64_t>(jobs, 65536))), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu,
+                       static_cast<int>(run), rows, cols);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_ff_dpre_f16, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, rows, cols, p.dx ? p.dpre : nullptr,
+                       p.dw ? p.dpre_w : nullptr);
+  } else {
+    hipLaunchKernelGGL(k_ff_dpre_bf16, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
+  }
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (plan.together) {
     e = launch(plan.dx.shape, p.dx != nullptr, p.dw != nullptr);
   } else {

@@ -505,11 +505,14 @@ size_t cubic_gated_ff_workspace_bytes(int64_t M, int64_t H, int64_t I);
 int cubic_gated_ff(const void* x, const void* w, int dtype, int64_t M, int64_t H, int64_t I, int act,
                    void* h, float* pre, void* workspace, size_t ws_bytes, cubic_stream_t stream);
 /* Its backward pass: from dh [M][I], x, w and the forward's pre,
- *   dg = dh * u * act'(g),  du = dh * act(g)     fp32, rounded to dtype
+ *   dg = dh * u * act'(g),  du = dh * act(g)     fp32, rounded to 16 bits
  *   dx = dg Wg + du Wu      [M][H]
  *   dw = [dg | du]^T x      [2I][H]
  * with fp32 sums, dx and dw rounded to dtype once. The products take 16-bit operands, which is
- * why dg and du are rounded: one rounding of each term, of the size of the results' own. dx or
+ * why dg and du are rounded: one rounding of each term, of the size of the results' own. In fp16
+ * they are scaled before it by powers of two, one for each row (for dx) and column (for dw), which the
+ * results get back: dg and du may leave the range of fp16, 2^-29 of a row's or column's largest one keeps
+ * all its bits, and less is off by 2^-40 of that. dx or
  * dw may be NULL and is then not computed (w is read for dx alone, x for dw alone, and may be
  * NULL too). M == 0 writes zeros to dw. dw is overwritten, not added to. */
 size_t cubic_gated_ff_backward_workspace_bytes(int64_t M, int64_t H, int64_t I);
