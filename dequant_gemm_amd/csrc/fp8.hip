@@ -482,7 +482,7 @@ static bool fp8_few(int64_t M, int64_t N, int64_t K) {
   return M <= kFewAlways || (!fp8_wide(N) && (M <= 32 || (M <= kFewMaxM && K <= 4096)));
 }
 
-size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewAlways ? 0 : plan_bytes(plan8(M, N, K), M, N); }
+size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return fp8_few(M, N, K) ? 0 : plan_bytes(plan8(M, N, K), M, N); }
 
 static bool fp8_whole(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
 // Every workgroup quantises the rows itself, instead of a launch before the product's, up to about
