@@ -41,7 +41,7 @@ struct FewParams {
 };
 
 constexpr int kFewWaves = 16;
-constexpr int64_t kFewMaxM = 64, kFewWholeM = 4;
+constexpr int64_t kFewMaxM = 64, kFewWholeM = 4, kFewQuantM = 8;
 constexpr int64_t kFewWholeBytes = 32768;      // of a row held whole in LDS (four rows: 128 KB)
 
 template <int KIND>
@@ -343,7 +343,7 @@ hipError_t launch_few_k(const FewParams& p, hipStream_t st) {
 }
 
 // whole: p.x holds up to kFewWholeM rows to stage whole (fp8: 16-bit rows to quantise). quant: fp8,
-// p.x holds 16-bit rows to quantise a chunk at a time.
+// p.x holds up to kFewQuantM 16-bit rows to quantise a chunk at a time, beside one tile of weight rows.
 template <int KIND, bool GATED>
 hipError_t launch_few(FewParams p, bool whole, bool quant, bool xf16, hipStream_t st) {
   constexpr bool F8 = KIND == kFewFp8;
@@ -366,7 +366,7 @@ hipError_t launch_few(FewParams p, bool whole, bool quant, bool xf16, hipStream_
     constexpr int MT = decltype(mt_c)::value;
     constexpr bool WHOLE = decltype(whole_c)::value, XF16 = decltype(xf16_c)::value, QUANT = decltype(quant_c)::value;
     // (e4m3 operands of two tiles by more rows than this go to the tile kernel: registers)
-    constexpr bool kTwo = !F8 || MT == 1;
+    constexpr bool kTwo = !QUANT && (!F8 || MT == 1);
     if constexpr (kTwo) {
       if (nt == 2) return launch_few_k<KIND, MT, 2, WHOLE, GATED, XF16, QUANT>(p, st);
     }
@@ -379,15 +379,13 @@ hipError_t launch_few(FewParams p, bool whole, bool quant, bool xf16, hipStream_
     }
     return go(One{}, std::true_type{}, std::false_type{}, std::false_type{});
   }
-  auto rows = [&](auto xf16_c, auto quant_c) {
-    if (p.M <= 16) return go(One{}, std::false_type{}, xf16_c, quant_c);
-    if (p.M <= 32) return go(std::integral_constant<int, 2>{}, std::false_type{}, xf16_c, quant_c);
-    return go(std::integral_constant<int, 4>{}, std::false_type{}, xf16_c, quant_c);
-  };
+  const std::false_type no;
   if constexpr (F8) {
-    if (quant) return xf16 ? rows(std::true_type{}, std::true_type{}) : rows(std::false_type{}, std::true_type{});
+    if (quant) return xf16 ? go(One{}, no, std::true_type{}, std::true_type{}) : go(One{}, no, no, std::true_type{});
   }
-  return rows(std::false_type{}, std::false_type{});
+  if (p.M <= 16) return go(One{}, no, no, no);
+  if (p.M <= 32) return go(std::integral_constant<int, 2>{}, no, no, no);
+  return go(std::integral_constant<int, 4>{}, no, no, no);
 }
 
 }  // namespace cubic

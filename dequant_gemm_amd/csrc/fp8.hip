@@ -485,14 +485,14 @@ static bool fp8_few(int64_t M, int64_t N, int64_t K) {
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return fp8_few(M, N, K) ? 0 : plan_bytes(plan8(M, N, K), M, N); }
 
 static bool fp8_whole(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
-// Every workgroup quantises the rows itself, instead of a launch before the product's, up to about
-// as many values as add to a graph replay what the launch costs a caller. Measured, in us (values, N;
-// replays, then calls; in the product against a launch of its own, with which a call takes 11.4 to 12.6):
-// 16 x 1936, N 1003, 8.4 and 8.6 against 7.3; 37 x 1936 10.7 and 10.3 against 9.3; 48 x 2048, N 4096,
-// 12.0 and 11.5 against 9.3; 16 x 7168 13.6 and 13.0 against 10.4 and 11.4. Wide: 16 x 2048, N 7168,
-// 10.2 and 9.7 against 9.2; 8 x 7168, N 6144, 15.3 and 14.8 against 14.1 and 13.6.
+// Every workgroup quantises the rows itself, instead of a launch before the product's, where a graph replay does not
+// lose by it (every workgroup repeats the work). Measured from bf16, in us (rows x K, N; replays, then calls; in the
+// product against a launch of its own): 8 x 1024, N 1003, 7.0 and 8.8 against 7.0 and 11.9; 8 x 4096 7.7 and 8.5 against
+// 7.8 and 11.1; N 4096 7.6 and 8.6 against 8.1 and 11.3. More rows: 16 x 1024 8.9 and 8.6 against 7.0 and 11.5; 37 x 1936
+// 12.6 and 12.2 against 9.6 and 12.3. More values: 8 x 7168 10.7 and 10.4 against 9.3 and 11.3. Wide: 8 x 1936, N 7168, 9.9
+// and 9.5 against 9.0 and 11.1; 8 x 7168 19.2 and 18.7 against 15.6 and 15.1.
 bool fp8_quantises(int64_t M, int64_t N, int64_t K) {
-  return fp8_whole(M, K) || (fp8_few(M, N, K) && M * K <= (fp8_wide(N) ? 40 : 80) * 1024);
+  return fp8_whole(M, K) || (M <= kFewQuantM && !fp8_wide(N) && M * K <= 32 * 1024);
 }
 
 hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st) {

@@ -482,7 +482,8 @@ int cubic_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, const cub
                    cubic_stream_t stream);
 /* The same product of bf16 or fp16 activations x [M][K], quantised on the way by the rule of
  * cubic_quant_fp8 with block_rows 1: the result of that call followed by cubic_gemm_fp8. Few
- * activations are quantised inside the product's kernel and need no workspace; others pass through
+ * activations (up to four rows, or up to eight of a few thousand channels beside a narrow weight)
+ * are quantised inside the product's kernel and need no workspace; others pass through
  * the workspace (codes, then scales, each rounded up to 256 bytes, then the product's own). */
 size_t cubic_linear_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int cubic_linear_fp8(const void* x, int x_dtype, int64_t M, const cubic_weight_fp8* w, const float* bias,
