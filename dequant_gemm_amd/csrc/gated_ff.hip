@@ -607,8 +607,18 @@ unsigned quad_grid(int64_t M, int64_t I) {
 
 }  // namespace
 
+// Rows that the streaming kernel takes: every workgroup stages all of them, in each of its passes of 16 columns a
+// compute unit. Measured against the tiles (H / I, us of a replay): 4 rows 4096 / 8192 22.6 against 25.6, 4096 / 14336 35.0
+// against 35.1; 16 rows 7168 / 2048 13.3 against 19.3, 4096 / 6144 22.4 against 21.7, 4096 / 14336 44 against 35; 32 rows
+// 7168 / 2048 15.8 against 20.0, 2048 / 4352 16.6 against 14.8; 64 rows 2048 / 1024 10.1 against 13.0, 4096 / 4096 19.7
+// against 18.4, 7168 / 2048 21.6 against 18.7.
+static bool ff_few(int64_t M, int64_t H, int64_t I) {
+  const int64_t pass = 16 * plan_cus();
+  return M <= 4 || (M <= 16 && 2 * I <= 3 * pass) || (I <= pass && (M <= 32 || (M <= kFewMaxM && H <= 4096)));
+}
+
 size_t gated_ff_part_bytes(int64_t M, int64_t H, int64_t I) {
-  return M <= kFewMaxM ? 0 : plan_bytes(plan_forward(M, H, I), M, 2 * I);
+  return ff_few(M, H, I) ? 0 : plan_bytes(plan_forward(M, H, I), M, 2 * I);
 }
 
 size_t gated_ff_backward_part_bytes(int64_t M, int64_t H, int64_t I) {
@@ -618,7 +628,7 @@ size_t gated_ff_backward_part_bytes(int64_t M, int64_t H, int64_t I) {
 
 hipError_t launch_gated_ff(const FfParams& p, hipStream_t st) {
   const int dt = p.f16 ? 2 : 1;
-  if (p.M <= kFewMaxM) {
+  if (ff_few(p.M, p.H, p.I)) {
     FewParams f{};
     f.x = p.x;
     f.w = p.w;
