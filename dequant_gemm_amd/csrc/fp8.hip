@@ -471,19 +471,20 @@ FewParams few_params(const Fp8Params& p, bool gated) {
 }
 }  // namespace
 
-// Rows that the streaming kernel takes. Measured against the tiles (N x K, us): 16 rows 6144 x 7168
-// 12.2 against 14.1, 32 rows 19.1 against 16.7, 7168 x 2048 7.8 against 8.8; 64 rows 4096 x 4096 11.2
-// against 11.1, 1003 x 1936 7.6 against 9.8, 1024 x 8192 15.3 against 11.9. wide: a workgroup would have two
-// tiles of weight rows.
-constexpr int64_t kFewAlways = 16;
-
+// Rows that the streaming kernel takes: up to 32 weight rows a compute unit, one pass of its workgroups. Measured against
+// the tiles (N x K, us of a replay): one row 8192 x 4096 7.9 against 12.5, 10240 x 4096 15.7 against 14.0, 28672 x 4096 31
+// against 25; 16 rows 6144 x 7168 13.2 against 15.6, 8192 x 7168 14.8 against 16.6, 10240 x 7168 22.9 against 18.8. Beyond 16 rows
+// (wide: two tiles of weight rows a workgroup, not for them): 32 rows 2048 x 7168 11.3 against 11.8, 4096 x 7168 11.6
+// against 13.9; 64 rows 1003 x 1936 8.9 against 10.5, 4096 x 4096 12.1 against 12.0, 2048 x 7168 16.3 against 12.5.
 static bool fp8_wide(int64_t N) { return N > 16 * plan_cus(); }
 static bool fp8_few(int64_t M, int64_t N, int64_t K) {
-  return M <= kFewAlways || (!fp8_wide(N) && (M <= 32 || (M <= kFewMaxM && K <= 4096)));
+  if (N > 32 * plan_cus()) return false;
+  return M <= 16 || (!fp8_wide(N) && (M <= 32 || (M <= kFewMaxM && K <= 4096)));
 }
 
 size_t fp8_part_bytes(int64_t M, int64_t N, int64_t K) { return fp8_few(M, N, K) ? 0 : plan_bytes(plan8(M, N, K), M, N); }
 
+// Of those, the ones that are staged whole.
 static bool fp8_whole(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFewWholeBytes; }
 // Every workgroup quantises the rows itself, instead of a launch before the product's, where a graph replay does not
 // lose by it (every workgroup repeats the work). Measured from bf16, in us (rows x K, N; replays, then calls; in the
@@ -492,7 +493,7 @@ static bool fp8_whole(int64_t M, int64_t K) { return M <= kFewWholeM && K <= kFe
 // 12.6 and 12.2 against 9.6 and 12.3. More values: 8 x 7168 10.7 and 10.4 against 9.3 and 11.3. Wide: 8 x 1936, N 7168, 9.9
 // and 9.5 against 9.0 and 11.1; 8 x 7168 19.2 and 18.7 against 15.6 and 15.1.
 bool fp8_quantises(int64_t M, int64_t N, int64_t K) {
-  return fp8_whole(M, K) || (M <= kFewQuantM && !fp8_wide(N) && M * K <= 32 * 1024);
+  return fp8_few(M, N, K) && (fp8_whole(M, K) || (M <= kFewQuantM && !fp8_wide(N) && M * K <= 32 * 1024));
 }
 
 hipError_t launch_fp8(const Fp8Params& p, bool xf16, hipStream_t st) {

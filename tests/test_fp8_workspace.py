@@ -8,9 +8,9 @@ import torch
 import dequant_gemm_amd as cq
 
 DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-# rows that the streaming kernel takes, whatever the result's type: up to 16 always, to 32 beside up to 4096 weight rows, to 64 beside
-# those and up to 4096 channels
-FEW = [(1, 6144, 7168), (16, 20000, 7168), (17, 1003, 1936), (32, 4096, 7168), (33, 1003, 1936), (37, 1003, 1936), (64, 4096, 4096)]
+# rows that the streaming kernel takes, whatever the result's type: up to 16 beside up to 8192 weight rows, to 32 beside up to
+# 4096, to 64 beside those and up to 4096 channels
+FEW = [(1, 6144, 7168), (16, 8192, 7168), (17, 1003, 1936), (32, 4096, 7168), (33, 1003, 1936), (37, 1003, 1936), (64, 4096, 4096)]
 align = lambda n: -(-n // 256) * 256  # noqa: E731
 
 

@@ -10,7 +10,8 @@ from tests._gpu import DEV, say
 pytestmark = pytest.mark.gpu
 # (rows, weight rows, channels, quantised inside): rows staged whole, rows in chunks, too many rows, values or weight rows
 CASES = [(4, 300, 4112, True), (4, 5000, 32768, True), (4, 300, 32784, False), (5, 300, 4112, True), (8, 4096, 4096, True), (8, 1003, 1936, True), (8, 4096, 4112, False),
-         (5, 4352, 528, False), (9, 300, 528, False), (16, 1003, 1936, False), (37, 1003, 1936, False), (5, 300, 16, True)]
+         (5, 4352, 528, False), (9, 300, 528, False), (16, 1003, 1936, False), (37, 1003, 1936, False), (5, 300, 16, True),
+         (1, 8192, 528, True), (1, 8193, 528, False), (4, 8448, 272, False), (16, 9000, 144, False)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
