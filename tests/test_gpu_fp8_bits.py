@@ -36,3 +36,27 @@ def test_codes_byte_for_byte(M, K, rows, dtype, size):
     got = q.view(torch.uint8).cpu().numpy()
     assert np.array_equal(got, qr), np.argwhere(got != qr)[:4]
     assert (qr == 0x80).any() or K == 48          # the case has what it is about
+
+
+@pytest.mark.parametrize("dtype,steps", [(torch.bfloat16, 128), (torch.float16, 1024)])
+def test_every_pair_of_significands(dtype, steps):
+    """Quotients of every significand of a block's largest magnitude and every significand of a value, down to
+    codes of zero, against IEEE division on the CPU: scales and codes equal."""
+    say(f"quant_fp8 every pair of significands {dtype}")
+    sig = 1 + torch.arange(steps, dtype=torch.float32) / steps
+    per = -(-steps // 127)                            # blocks of 127 values and the largest magnitude
+    for k in range(20):
+        v = torch.zeros(per * 127)
+        v[:steps] = sig * 2.0 ** -k
+        x = torch.empty((steps, per, 128))
+        x[:, :, 0] = 1024 * sig[:, None]
+        x[:, :, 1:] = 1024 * v.view(per, 127) * torch.where(torch.arange(127) % 2 == 0, 1.0, -1.0)
+        if k == 0:                                    # no value above its block's largest magnitude
+            x[:, :, 1:] = torch.where(x[:, :, 1:].abs() > x[:, :, :1], 0.0, x[:, :, 1:])
+        x = x.view(steps, -1).to(dtype)
+        q, s = cq.cubic_quant_fp8(x.to(DEV))
+        want_s = (x[:, ::128].float() / 448.0)
+        quotient = (x.float().view(steps, per, 128) / want_s[:, :, None]).clamp(-448, 448)
+        want = quotient.to(torch.float8_e4m3fn).view(torch.uint8).view(steps, -1)
+        assert torch.equal(s.cpu(), want_s), k
+        assert torch.equal(q.cpu().view(torch.uint8), want), k
