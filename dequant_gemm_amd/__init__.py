@@ -830,7 +830,13 @@ def cubic_gated_ff_workspace_bytes(M: int, H: int, I: int) -> int:
 def cubic_gated_ff(x: torch.Tensor, w: torch.Tensor, act="silu", save_pre: bool = False, out: torch.Tensor | None = None,
                    pre: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """h [M][I] = act(x Wg^T) * (x Wu^T) for x [M][H] and w [2 I][H] (gate rows, then up rows), bf16 or fp16.
-    With save_pre or a tensor for it, (h, pre): pre fp32 [M][2 I] is what the backward pass takes."""
+    With save_pre or a tensor for it, (h, pre): pre fp32 [M][2 I] is what the backward pass takes.
+    No graph is recorded, so inputs that require a gradient are refused while one would be (as in
+    torch's out= forms): the forward and backward methods of a torch.autograd.Function call this and
+    cubic_gated_ff_backward."""
+    if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        raise RuntimeError("cubic_gated_ff records no graph, but an input requires a gradient: call it under torch.no_grad(), "
+                           "or in a torch.autograd.Function with cubic_gated_ff_backward")
     index = _first(x, "x")
     xa, wa, xd, M, H, I = _ff_args(x, w, index)
     kind = _act(act)
