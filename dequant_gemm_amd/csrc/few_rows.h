@@ -10,9 +10,9 @@
 // every workgroup can quantise the rows itself on their way into LDS: whole rows beside its first
 // weight loads, or a chunk at a time. The waves' sums meet in LDS and are added up in their order.
 //
-// Measured: 44 MB of e4m3 weights (6144 x 7168) in 9.9 us of the kernel with one row, 12.2 us with 16;
-// 58.7 MB of bf16 gate and up weights in 10.9 us (5.4 TB/s), 17 us of I 1024, H 8192 with 48 rows. From
-// 17 rows on the staging of the activations and the join of sixteen sums count.
+// Measured: 44 MB of e4m3 weights (6144 x 7168) in 10.4 us of the kernel with one row, 13.2 us with 16;
+// 58.7 MB of bf16 gate and up weights in 10.9 us (5.4 TB/s, partly from the last cache), 17 us of I 1024, H 8192
+// with 48 rows. From 17 rows on the staging of the activations and the join of sixteen sums count.
 #pragma once
 #include <algorithm>
 #include <type_traits>

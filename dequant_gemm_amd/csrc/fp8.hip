@@ -12,14 +12,16 @@
 // k_quant_fp8_rows, k_quant_fp8_blocks: bound by HBM. 4096 x 7168 rows: 19 us cold, 12 us beside a
 // product (88 MB; 17 us at the 5.1 TB/s of a large copy).
 //
-// Few rows (few_rows.h): 1 x 6144 x 7168 from bf16 10.7 us a call (44 MB: 8.6 us), 16 rows 12.6 us.
+// k_quant_fp8_blocks: 6144 x 7168 in 23.4 us (132 MB). Few rows (few_rows.h): 1 x 6144 x 7168 from
+// bf16 10.5-11.2 us a call (44 MB: 8.6 us), 16 rows 13.2 us.
 //
 // k_fp8_tile (more rows; bound by the MFMA and the power it takes): 256 x 256 tiles of eight
 // waves, 64 x 128 each, both operands straight into two LDS stages of 128 codes, one block of
 // scales; A's fragments stay in registers through a stage, B's come one by one, both are
 // converted there, and each 16 x 16 x 128 result goes into the sums by four fmas with the row's
-// scale times the block's. Measured: 4096 x 4096 x 7168 in 171-179 us (1.34-1.4 PFLOP/s; the library's
-// product in bf16 160 us). Smaller tiles: 256 x 128 in two rounds 202-215 us, 128 x 128 226, 64 x 64
+// scale times the block's. Measured: 4096 x 4096 x 7168 in 171-180 us (1.34-1.4 PFLOP/s; the library's
+// product in bf16 160 us), MFMA busy 57 % of the cycles, vector instructions (conversions) 56 %.
+// 4096 x 6144 x 7168, a round and a half of these, takes 256 x 128 tiles: 305-316 us. Smaller tiles: 256 x 128 in two rounds 202-215 us, 128 x 128 226, 64 x 64
 // 275; the smaller ones hold a stage's fragments ahead, with the ring's slots known to the
 // compiler. Not faster: 128 x 128 by four waves (215 us, but 512 x 6144 x 7168 66 us against 52), 256 x 128
 // by waves of 128 x 32 (278 us, spills), 256 x 128 with a ring of two or as 128 x 256 (202).
