@@ -19,12 +19,13 @@
 // waves, 64 x 128 each, both operands straight into two LDS stages of 128 codes, one block of
 // scales; A's fragments stay in registers through a stage, B's come one by one, both are
 // converted there, and each 16 x 16 x 128 result goes into the sums by four fmas with the row's
-// scale times the block's. Measured: 4096 x 4096 x 7168 in 171-180 us (1.34-1.4 PFLOP/s; the library's
-// product in bf16 160 us), MFMA busy 57 % of the cycles, vector instructions (conversions) 56 %.
-// 4096 x 6144 x 7168, a round and a half of these, takes 256 x 128 tiles: 305-316 us. Smaller tiles: 256 x 128 in two rounds 202-215 us, 128 x 128 226, 64 x 64
-// 275; the smaller ones hold a stage's fragments ahead, with the ring's slots known to the
-// compiler. Not faster: 128 x 128 by four waves (215 us, but 512 x 6144 x 7168 66 us against 52), 256 x 128
-// by waves of 128 x 32 (278 us, spills), 256 x 128 with a ring of two or as 128 x 256 (202).
+// scale times the block's. Measured: 4096 x 4096 x 7168 in 171-180 us (1.34-1.4 PFLOP/s; the
+// library's product in bf16 160 us), MFMA busy 57 % of the cycles, vector instructions
+// (conversions) 56 %. 4096 x 6144 x 7168, a round and a half of these, takes 256 x 128 tiles:
+// 305-316 us. Smaller tiles of 4096 x 4096 x 7168: 256 x 128 202-215 us, 128 x 128 226, 64 x 128
+// 283, 64 x 64 275; those of 128 x 128 and less hold a stage's fragments ahead, with the ring's slots
+// known to the compiler. Not faster: 128 x 128 by four waves (215 us, but 512 x 6144 x 7168 66
+// against 52), 256 x 128 by waves of 128 x 32 (278, spills), with a ring of two or as 128 x 256 (202).
 #include <algorithm>
 
 #include "common.h"
