@@ -5,11 +5,12 @@
 //
 // (The gated block of the dense parts beside the routed experts, whose own form cubic_moe_mlp
 // computes.) All three products take 16-bit operands and keep fp32 sums. dg and du are rounded to
-// 16 bits on the way to the last two, as large an error as the results' own rounding (two 16-bit halves of
-// them would take the backward products of 4096 x 7168 x 2048 from 420 to 750 us); the
-// pre-activations between the passes are fp32, since theirs would come on top. In fp16 dg and du are scaled by powers of two,
-// each row's for dx and each column's for dw, which the results get back: they may lie outside the
-// type's range where dx and dw do not. That takes two more launches: 4096 x 2048 in 23 us.
+// 16 bits on the way to the last two, as large an error as the results' own rounding (two 16-bit
+// halves of them would take the backward products of 4096 x 7168 x 2048 from 420 to 750 us); the
+// pre-activations between the passes are fp32, since theirs would come on top. In fp16 dg and du
+// are scaled by powers of two, each row's for dx and each column's for dw, which the results get
+// back: they may lie outside the type's range where dx and dw do not. That takes two more
+// launches (4096 x 2048 in 22 us) and dg and du twice.
 //
 // Up to 64 rows (few_rows.h): 1 x 7168 x 2048 (58.7 MB of weights) 10.6-11 us, 5.4 TB/s.
 //
@@ -20,7 +21,7 @@
 // for dw) lie in LDS as they are and come out through the transposing reads, so nothing is
 // transposed in memory. Measured, 4096 x 7168 x 2048 in bf16: forward 177-190 us (1.27-1.36
 // PFLOP/s; the library's product of that size alone 153-160 us), both products of the backward
-// pass 410-430 us (library 192 + 222), dpre 20 us (117 MB; fp16, two of them, 27). MFMA busy 65 % of the cycles at 1.8 GHz;
+// pass 410-430 us (library 192 + 222), dpre 20 us (117 MB). MFMA busy 65 % of the cycles at 1.8 GHz;
 // on zeros 128 us (library 110). Not faster: operands through registers (189 us; with a barrier
 // every 16 MFMAs 207), four waves of 128 x 128 (180), two workgroups of four waves to a compute unit
 // (245), rings of four stages of 32 k (213), the barrier later in the step, reads earlier, wave
@@ -683,6 +684,11 @@ hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
       return hipGetLastError();
     });
   };
+  auto products = [&](bool with_x, bool with_w) {
+    if (plan.together) return launch(plan.dx.shape, with_x, with_w);
+    const hipError_t l = launch(plan.dx.shape, with_x, false);
+    return l != hipSuccess ? l : launch(plan.dw.shape, false, with_w);
+  };
   hipError_t e;
   if (p.f16) {
     e = launch_fill_zero(reinterpret_cast<float*>(p.range), p.M + 2 * p.I, false, st);
@@ -694,18 +700,24 @@ hipError_t launch_gated_ff_backward(const FfParams& p, hipStream_t st) {
                        static_cast<int>(run), rows, cols);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_ff_dpre_f16, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, rows, cols, p.dx ? p.dpre : nullptr,
-                       p.dw ? p.dpre_w : nullptr);
+    auto dpre = [&](bool for_x, bool for_w) {
+      hipLaunchKernelGGL(k_ff_dpre_f16, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, rows, cols, for_x ? p.dpre : nullptr,
+                         for_w ? p.dpre_w : nullptr);
+      return hipGetLastError();
+    };
+    if (p.dpre_w != p.dpre || !p.dx || !p.dw) {
+      e = dpre(p.dx != nullptr, p.dw != nullptr);
+      if (e == hipSuccess) e = products(p.dx != nullptr, p.dw != nullptr);
+    } else {                                   // one after the other in one place
+      e = dpre(true, false);
+      if (e == hipSuccess) e = products(true, false);
+      if (e == hipSuccess) e = dpre(false, true);
+      if (e == hipSuccess) e = products(false, true);
+    }
   } else {
     hipLaunchKernelGGL(k_ff_dpre_bf16, dim3(quads), dim3(256), 0, st, p.pre, p.dh, p.M, p.I, p.gelu, p.dpre);
-  }
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (plan.together) {
-    e = launch(plan.dx.shape, p.dx != nullptr, p.dw != nullptr);
-  } else {
-    e = launch(plan.dx.shape, p.dx != nullptr, false);
-    if (e == hipSuccess) e = launch(plan.dw.shape, false, p.dw != nullptr);
+    e = hipGetLastError();
+    if (e == hipSuccess) e = products(p.dx != nullptr, p.dw != nullptr);
   }
   if (e == hipSuccess && p.dx && plan.dx.slices > 1)
     e = launch_tile_join<false>({part, plan.dx.slices, p.M, p.H, p.H, nullptr, p.dx, dt, 0, nullptr}, st);

@@ -246,7 +246,7 @@ struct FfParams {
   float* pre;              // [M][2 I]: gate, up before the activation
   const uint16_t* dh;      // [M][I]
   uint16_t* dpre;          // [M][2 I]: their gradients
-  uint16_t* dpre_w;        // fp16: the same for dw, with other scales
+  uint16_t* dpre_w;        // fp16: the same for dw, with other scales (may be dpre)
   uint32_t* range;         // fp16: [2 I + M] largest magnitudes of their columns and rows
   uint16_t* dx;            // [M][H] or NULL
   uint16_t* dw;            // [2 I][H] or NULL
